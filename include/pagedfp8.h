@@ -453,6 +453,139 @@ pkv_status pkv_paged_prefill(const void *q, const int32_t *cu_q, int total_q, in
                              int32_t *device_error, cudaStream_t stream);
 
 /*
+ * The 4-bit cache -- a second cache format, for contexts whose FP8 pages do
+ * not fit: 4.5 bits a value instead of 8.  A row of 128 values is 8 blocks of
+ * 16; a block holds E2M1 codes e (0, 0.5, 1, 1.5, 2, 3, 4, 6 and a sign) and
+ * one E4M3 scale s, and with the kv head's fp32 scale k a value is
+ *     e * s * k.
+ * k is the head's FP8 scale (pkv_kv_calibrate's, absmax / 448, serves both
+ * formats); any k in [2^-100, 2^100] works.
+ *
+ *   k_cache, v_cache : uint8 [num_pages][num_kv_heads][page_size / 16][1152],
+ *                      PKV_FP4_ROW_BYTES (72) bytes a row.  16 consecutive
+ *                      tokens of a kv head are one tile of 1152 bytes: first
+ *                      64 bytes of codes for each token (dim 2i in the low
+ *                      nibble of byte i, dim 2i + 1 in the high one), then 8
+ *                      scales for each token.
+ * Slots, block tables, per-sequence page sizes, ownership and device errors
+ * are those of the FP8 cache.
+ *
+ * Window and sinks.  The two attention calls take a window of W tokens and a
+ * number S of sinks: a query at position p then sees the tokens t <= p with
+ * t > p - W (itself and the W - 1 before it) or t < S.  W = 0 means no window
+ * (S has no effect).  The rows of pages in which no query of the call sees a
+ * token are not read and their table entries not looked at, so such pages may
+ * have been given away.
+ */
+#define PKV_FP4_ROW_BYTES 72
+
+/*
+ * kv_append_fp4 -- quantise new K and V tokens to 4 bits and write them into
+ * their pages.  For every token t with slot = slot_mapping[t] >= 0, every kv
+ * head h and every block of 16 dims, with k = k_scale[h]:
+ *     s    = E4M3(amax / (6 k))       amax: the block's largest |x|
+ *     code = E2M1(x / (s k))          (all codes 0 where s = 0)
+ * and the same for V.  6 k, s k and both quotients are rounded to fp32 (IEEE);
+ * E4M3 and E2M1 round to nearest, ties to even, and saturate (+-448, +-6), so
+ * +-Inf reads back as +-6 s k.  A block holding a NaN gets the NaN scale 0x7F
+ * and codes 0: all of it reads back as NaN.
+ *
+ * Arguments as pkv_kv_append_fp8, with pools of the 4-bit layout; two tokens
+ * with the same slot race.
+ */
+pkv_status pkv_kv_append_fp4(const void *k_new, const void *v_new, int in_dtype,
+                             int64_t num_tokens, int num_kv_heads, int head_dim,
+                             const int64_t *slot_mapping,
+                             const float *k_scale, const float *v_scale,
+                             uint8_t *k_cache, uint8_t *v_cache,
+                             int64_t num_pages, int page_size,
+                             int32_t *device_error, cudaStream_t stream);
+
+/*
+ * kv_read_fp4 -- read rows back: for every token t with slot =
+ * slot_mapping[t] >= 0,
+ *     k_out[t][h][d] = e * s * k_scale[h]       (one rounding to fp32)
+ * of the row at that slot, rounded to bf16 where out_dtype is PKV_BF16, and
+ * the same for V.  Rows of negative slots are left as they were; a slot
+ * outside the pool sets PKV_DEVERR_SLOT and reads as zeros.  A slot may occur
+ * more than once.
+ *
+ *   k_out, v_out   device, [num_tokens][num_kv_heads][head_dim], out_dtype
+ *                  PKV_F32 or PKV_BF16, 16-byte aligned.
+ * num_tokens == 0 is a no-op.
+ */
+pkv_status pkv_kv_read_fp4(const int64_t *slot_mapping, int64_t num_tokens,
+                           int num_kv_heads, int head_dim,
+                           const float *k_scale, const float *v_scale,
+                           const uint8_t *k_cache, const uint8_t *v_cache,
+                           int64_t num_pages, int page_size,
+                           void *k_out, void *v_out, int out_dtype,
+                           int32_t *device_error, cudaStream_t stream);
+
+/*
+ * paged_gqa_decode_fp4 -- pkv_paged_gqa_decode over the 4-bit cache, with a
+ * window and sinks: the query of sequence b sits at position seq_lens[b] - 1
+ * and sees the tokens named above; values are e * s times the head's scale.
+ * Arguments, errors, clamping, zero rows for empty sequences and determinism
+ * as pkv_paged_gqa_decode; q may have any finite bf16 values.  A bf16 output
+ * rounds the softmax weights once to f16 before they meet V (the sum that
+ * normalises them is of the rounded weights); an fp32 output keeps them as
+ * two f16 parts.
+ *
+ *   window, sinks  >= 0.
+ *   workspace      device, >= pkv_decode_fp4_workspace_size(...) bytes for the
+ *                  same sizes, 256-byte aligned; needs no initialisation, not
+ *                  to be shared by calls that overlap on the GPU.
+ * num_pages * num_kv_heads * page_size / 16 must be below 2^31.
+ */
+size_t pkv_decode_fp4_workspace_size(int batch, int num_q_heads, int num_kv_heads,
+                                     int head_dim, int max_seq_len, int page_size, int max_ctas);
+
+pkv_status pkv_paged_gqa_decode_fp4(const void *q,
+                                    const uint8_t *k_cache, const uint8_t *v_cache,
+                                    const float *k_scale, const float *v_scale,
+                                    const int32_t *block_table, int max_pages_per_seq,
+                                    const int32_t *seq_lens, int max_seq_len,
+                                    const int32_t *seq_page_sizes,
+                                    int batch, int num_q_heads, int num_kv_heads, int head_dim,
+                                    int page_size, int64_t num_pages, float sm_scale,
+                                    int window, int sinks,
+                                    void *out, int out_dtype,
+                                    void *workspace, size_t workspace_bytes,
+                                    int32_t *device_error, int max_ctas, cudaStream_t stream);
+
+/*
+ * paged_prefill_fp4 -- pkv_paged_prefill over the 4-bit cache, with a window
+ * and sinks (a query at position p = seq_lens[b] - n_b + c sees the tokens
+ * named above).  Call it after pkv_kv_append_fp4 has written the chunk's own
+ * K/V.  Arguments, errors, untouched rows and determinism as
+ * pkv_paged_prefill; the softmax weights are rounded as in
+ * pkv_paged_gqa_decode_fp4.
+ *
+ *   window, sinks  >= 0.
+ *   workspace      device, >= pkv_prefill_fp4_workspace_size(batch,
+ *                  num_kv_heads, max_q_len, max_kv_len, max_total_kv, window,
+ *                  sinks) bytes, 256-byte aligned.  Under a window only the
+ *                  keys that some query of the chunk sees are widened, so
+ *                  long contexts need room for the window and the chunk only.
+ */
+size_t pkv_prefill_fp4_workspace_size(int batch, int num_kv_heads, int max_q_len, int max_kv_len,
+                                      int64_t max_total_kv, int window, int sinks);
+
+pkv_status pkv_paged_prefill_fp4(const void *q, const int32_t *cu_q, int total_q, int max_q_len,
+                                 const uint8_t *k_cache, const uint8_t *v_cache,
+                                 const float *k_scale, const float *v_scale,
+                                 const int32_t *block_table, int max_pages_per_seq,
+                                 const int32_t *seq_lens, const int32_t *seq_page_sizes,
+                                 int batch, int max_kv_len, int64_t max_total_kv,
+                                 int num_q_heads, int num_kv_heads, int head_dim,
+                                 int page_size, int64_t num_pages, float sm_scale,
+                                 int window, int sinks,
+                                 void *out, int out_dtype,
+                                 void *workspace, size_t workspace_bytes,
+                                 int32_t *device_error, cudaStream_t stream);
+
+/*
  * read_device_error -- read (and optionally clear) a device error word after
  * the work already enqueued on `stream`.
  *

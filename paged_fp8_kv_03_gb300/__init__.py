@@ -11,6 +11,9 @@ stream.  The entry points mirror the C ABI in ``include/pagedfp8.h``:
 * ``pkv_decode_calibrate_split``, ``pkv_decode_set_split_weights``,
   ``pkv_decode_get_split_weights`` -- per-CTA weights of the decode split
 * ``pkv_decode_workspace_size``, ``pkv_status_string``, ``pkv_version``
+* ``pkv_kv_append_fp4``, ``pkv_kv_read_fp4``, ``pkv_paged_gqa_decode_fp4``,
+  ``pkv_paged_prefill_fp4`` -- the 4-bit cache: writing it, reading it back,
+  and decode and prefill attention over it with an optional sliding window
 
 ``kv_append_fp8`` / ``paged_gqa_decode`` are the same calls with the output
 and workspace allocated by torch when not given.  There is no CPU fallback:
@@ -33,6 +36,7 @@ DEVERR_SLOT, DEVERR_PAGE, DEVERR_SEQLEN, DEVERR_TIMEOUT, DEVERR_PAGESIZE, DEVERR
 HEAD_DIM = 128
 MAX_GROUP = 8
 MAX_BATCH = 8192
+FP4_ROW_BYTES = 72
 
 _lib = None
 _lock = threading.Lock()
@@ -86,6 +90,20 @@ def load() -> ctypes.CDLL:
         lib.pkv_paged_prefill.restype = i32
         lib.pkv_paged_prefill.argtypes = [vp, vp, i32, i32, vp, vp, vp, vp, vp, i32, vp, vp, i32, i32, i64, i32, i32,
                                           i32, i32, i64, ctypes.c_float, vp, i32, vp, sz, vp, vp]
+        lib.pkv_kv_append_fp4.restype = i32
+        lib.pkv_kv_append_fp4.argtypes = lib.pkv_kv_append_fp8.argtypes
+        lib.pkv_kv_read_fp4.restype = i32
+        lib.pkv_kv_read_fp4.argtypes = [vp, i64, i32, i32, vp, vp, vp, vp, i64, i32, vp, vp, i32, vp, vp]
+        lib.pkv_decode_fp4_workspace_size.restype = sz
+        lib.pkv_decode_fp4_workspace_size.argtypes = [i32, i32, i32, i32, i32, i32, i32]
+        lib.pkv_paged_gqa_decode_fp4.restype = i32
+        lib.pkv_paged_gqa_decode_fp4.argtypes = [vp, vp, vp, vp, vp, vp, i32, vp, i32, vp, i32, i32, i32, i32, i32,
+                                                 i64, f32, i32, i32, vp, i32, vp, sz, vp, i32, vp]
+        lib.pkv_prefill_fp4_workspace_size.restype = sz
+        lib.pkv_prefill_fp4_workspace_size.argtypes = [i32, i32, i32, i32, i64, i32, i32]
+        lib.pkv_paged_prefill_fp4.restype = i32
+        lib.pkv_paged_prefill_fp4.argtypes = [vp, vp, i32, i32, vp, vp, vp, vp, vp, i32, vp, vp, i32, i32, i64, i32,
+                                              i32, i32, i32, i64, f32, i32, i32, vp, i32, vp, sz, vp, vp]
         lib.pkv_read_device_error.restype = i32
         lib.pkv_read_device_error.argtypes = [vp, i32, ctypes.POINTER(ctypes.c_int32), vp]
         lib.pkv_decode_set_split_weights.restype = i32
@@ -587,6 +605,240 @@ def paged_prefill(q, cu_q, k_cache, v_cache, k_scale, v_scale, block_table, seq_
     return out
 
 
+# ---------------------------------------------------------------------------
+# the 4-bit cache
+# ---------------------------------------------------------------------------
+def _check_fp4_pools(k_cache, v_cache):
+    _need(k_cache, "k_cache", torch.uint8, 4)
+    _need(v_cache, "v_cache", torch.uint8, 4)
+    if v_cache.shape != k_cache.shape or k_cache.shape[3] != FP4_ROW_BYTES:
+        raise ValueError(f"4-bit caches must be uint8 [num_pages, Hkv, P, {FP4_ROW_BYTES}], both alike")
+
+
+def _check_window(window, sinks):
+    if int(window) < 0 or int(sinks) < 0:
+        raise ValueError("window and sinks must not be negative")
+
+
+def fp4_cache(num_pages, num_kv_heads, page_size, device=None) -> torch.Tensor:
+    """One zeroed 4-bit pool (K or V): uint8 [num_pages, Hkv, P, 72]."""
+    device = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
+    return torch.zeros((num_pages, num_kv_heads, page_size, FP4_ROW_BYTES), dtype=torch.uint8, device=device)
+
+
+def pkv_kv_append_fp4(k_new, v_new, slot_mapping, k_scale, v_scale, k_cache, v_cache,
+                      device_error=None, stream=None) -> None:
+    """k_new/v_new [T, Hkv, 128] fp32|bf16; slot_mapping int64 [T] (negative:
+    not written); scales fp32 [Hkv]; caches uint8 [num_pages, Hkv, P, 72]
+    (written in place)."""
+    _need(k_new, "k_new", dim=3)
+    _need(v_new, "v_new", dtype=k_new.dtype, dim=3)
+    _need(slot_mapping, "slot_mapping", torch.int64, 1)
+    _need(k_scale, "k_scale", torch.float32, 1)
+    _need(v_scale, "v_scale", torch.float32, 1)
+    _check_fp4_pools(k_cache, v_cache)
+    if device_error is not None:
+        _need(device_error, "device_error", torch.int32)
+    T, H, D = k_new.shape
+    NP, H2, P, _ = k_cache.shape
+    if v_new.shape != k_new.shape or H2 != H:
+        raise ValueError("k/v shapes disagree")
+    if slot_mapping.shape[0] != T or k_scale.shape[0] != H or v_scale.shape[0] != H:
+        raise ValueError("slot_mapping / scale shapes disagree")
+    _same_device(k_new, v_new, slot_mapping, k_scale, v_scale, k_cache, v_cache, device_error)
+    with _device_of(k_new):
+        st = load().pkv_kv_append_fp4(_ptr(k_new), _ptr(v_new), _act_code(k_new), T, H, D, _ptr(slot_mapping),
+                                      _ptr(k_scale), _ptr(v_scale), _ptr(k_cache), _ptr(v_cache), NP, P,
+                                      _ptr(device_error), _stream(stream))
+    if st != 0:
+        raise PkvError(st, "pkv_kv_append_fp4")
+
+
+def pkv_kv_read_fp4(slot_mapping, k_scale, v_scale, k_cache, v_cache, k_out, v_out, device_error=None,
+                    stream=None) -> None:
+    """The rows at slot_mapping (int64 [T]) as values, into k_out/v_out
+    [T, Hkv, 128] fp32|bf16; rows of negative slots are left as they were."""
+    _need(slot_mapping, "slot_mapping", torch.int64, 1)
+    _need(k_scale, "k_scale", torch.float32, 1)
+    _need(v_scale, "v_scale", torch.float32, 1)
+    _check_fp4_pools(k_cache, v_cache)
+    _need(k_out, "k_out", dim=3)
+    _need(v_out, "v_out", dtype=k_out.dtype, dim=3)
+    if device_error is not None:
+        _need(device_error, "device_error", torch.int32)
+    T, H, D = k_out.shape
+    NP, H2, P, _ = k_cache.shape
+    if v_out.shape != k_out.shape or H2 != H:
+        raise ValueError("k/v shapes disagree")
+    if slot_mapping.shape[0] != T or k_scale.shape[0] != H or v_scale.shape[0] != H:
+        raise ValueError("slot_mapping / scale shapes disagree")
+    _same_device(slot_mapping, k_scale, v_scale, k_cache, v_cache, k_out, v_out, device_error)
+    with _device_of(slot_mapping):
+        st = load().pkv_kv_read_fp4(_ptr(slot_mapping), T, H, D, _ptr(k_scale), _ptr(v_scale), _ptr(k_cache),
+                                    _ptr(v_cache), NP, P, _ptr(k_out), _ptr(v_out), _act_code(k_out),
+                                    _ptr(device_error), _stream(stream))
+    if st != 0:
+        raise PkvError(st, "pkv_kv_read_fp4")
+
+
+def kv_append_fp4(k_new, v_new, slot_mapping, k_scale, v_scale, k_cache, v_cache, device_error=None,
+                  stream=None) -> None:
+    pkv_kv_append_fp4(k_new, v_new, slot_mapping, k_scale, v_scale, k_cache, v_cache, device_error, stream)
+
+
+def kv_read_fp4(slot_mapping, k_scale, v_scale, k_cache, v_cache, k_out=None, v_out=None,
+                out_dtype=torch.bfloat16, device_error=None, stream=None) -> tuple:
+    """Allocating form of pkv_kv_read_fp4: (K, V) [T, Hkv, 128]; without
+    outputs given, rows of negative slots are zeros."""
+    if (k_out is None) != (v_out is None):
+        raise ValueError("give both outputs or neither")
+    if k_out is None:
+        shape = (slot_mapping.shape[0], k_cache.shape[1], HEAD_DIM)
+        k_out = torch.zeros(shape, dtype=out_dtype, device=slot_mapping.device)
+        v_out = torch.zeros_like(k_out)
+    pkv_kv_read_fp4(slot_mapping, k_scale, v_scale, k_cache, v_cache, k_out, v_out, device_error, stream)
+    return k_out, v_out
+
+
+def pkv_decode_fp4_workspace_size(batch, num_q_heads, num_kv_heads, head_dim=HEAD_DIM, max_seq_len=0, page_size=16,
+                                  max_ctas=0) -> int:
+    """Workspace bytes of a 4-bit decode call of these sizes."""
+    return int(load().pkv_decode_fp4_workspace_size(int(batch), int(num_q_heads), int(num_kv_heads), int(head_dim),
+                                                    int(max_seq_len), int(page_size), int(max_ctas)))
+
+
+def pkv_paged_gqa_decode_fp4(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, out, workspace,
+                             sm_scale=None, device_error=None, max_ctas=0, stream=None, max_seq_len=0,
+                             seq_page_sizes=None, window=0, sinks=0) -> None:
+    """pkv_paged_gqa_decode over 4-bit caches uint8 [num_pages, Hkv, P, 72];
+    window > 0: only the last `window` tokens and the first `sinks` are
+    attended.  workspace uint8 (pkv_decode_fp4_workspace_size bytes)."""
+    _need(q, "q", torch.bfloat16, 3)
+    _check_fp4_pools(k_cache, v_cache)
+    _need(k_scale, "k_scale", torch.float32, 1)
+    _need(v_scale, "v_scale", torch.float32, 1)
+    _need(block_table, "block_table", torch.int32, 2)
+    _need(seq_lens, "seq_lens", torch.int32, 1)
+    _need(out, "out", dim=3)
+    _need(workspace, "workspace", torch.uint8)
+    if device_error is not None:
+        _need(device_error, "device_error", torch.int32)
+    B, Hq, D = q.shape
+    NP, Hkv, P, _ = k_cache.shape
+    if out.shape != q.shape:
+        raise ValueError("q / out shapes disagree")
+    if block_table.shape[0] != B or seq_lens.shape[0] != B:
+        raise ValueError("block_table / seq_lens shapes disagree with q")
+    if k_scale.shape[0] != Hkv or v_scale.shape[0] != Hkv:
+        raise ValueError("scales must have one entry per kv head")
+    _check_page_sizes(seq_page_sizes, B)
+    _check_window(window, sinks)
+    _same_device(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, out, workspace, device_error,
+                 seq_page_sizes)
+    if sm_scale is None:
+        sm_scale = 1.0 / math.sqrt(D)
+    with _device_of(q):
+        st = load().pkv_paged_gqa_decode_fp4(_ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale),
+                                             _ptr(block_table), block_table.shape[1], _ptr(seq_lens),
+                                             int(max_seq_len), _ptr(seq_page_sizes), B, Hq, Hkv, D, P, NP,
+                                             float(sm_scale), int(window), int(sinks), _ptr(out), _act_code(out),
+                                             _ptr(workspace), workspace.numel(), _ptr(device_error), int(max_ctas),
+                                             _stream(stream))
+    if st != 0:
+        raise PkvError(st, "pkv_paged_gqa_decode_fp4")
+
+
+def paged_gqa_decode_fp4(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, out=None,
+                         out_dtype=torch.bfloat16, workspace=None, sm_scale=None, device_error=None, max_ctas=0,
+                         stream=None, max_seq_len=0, seq_page_sizes=None, window=0, sinks=0) -> torch.Tensor:
+    """Allocating form of pkv_paged_gqa_decode_fp4."""
+    if out is None:
+        out = torch.empty(q.shape, dtype=out_dtype, device=q.device)
+    max_seq_len = _default_max_len(block_table, k_cache, max_seq_len, seq_page_sizes)
+    if workspace is None:
+        with _device_of(q):
+            n = pkv_decode_fp4_workspace_size(q.shape[0], q.shape[1], k_cache.shape[1], q.shape[2], max_seq_len,
+                                              k_cache.shape[2], max_ctas)
+        if n == 0:
+            raise PkvError(4, "pkv_decode_fp4_workspace_size")
+        workspace = torch.empty(n, dtype=torch.uint8, device=q.device)
+    pkv_paged_gqa_decode_fp4(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, out, workspace, sm_scale,
+                             device_error, max_ctas, stream, max_seq_len, seq_page_sizes, window, sinks)
+    return out
+
+
+def pkv_prefill_fp4_workspace_size(batch, num_kv_heads, max_q_len, max_kv_len, max_total_kv=0, window=0,
+                                   sinks=0) -> int:
+    return int(load().pkv_prefill_fp4_workspace_size(int(batch), int(num_kv_heads), int(max_q_len), int(max_kv_len),
+                                                     int(max_total_kv), int(window), int(sinks)))
+
+
+def pkv_paged_prefill_fp4(q, cu_q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, out, max_q_len,
+                          max_kv_len, workspace, sm_scale=None, device_error=None, stream=None, max_total_kv=0,
+                          seq_page_sizes=None, window=0, sinks=0) -> None:
+    """pkv_paged_prefill over 4-bit caches uint8 [num_pages, Hkv, P, 72];
+    window > 0: a query sees itself, the window - 1 tokens before it and the
+    first `sinks` tokens.  workspace uint8 (pkv_prefill_fp4_workspace_size
+    bytes for the same bounds)."""
+    _need(q, "q", torch.bfloat16, 3)
+    _need(cu_q, "cu_q", torch.int32, 1)
+    _check_fp4_pools(k_cache, v_cache)
+    _need(k_scale, "k_scale", torch.float32, 1)
+    _need(v_scale, "v_scale", torch.float32, 1)
+    _need(block_table, "block_table", torch.int32, 2)
+    _need(seq_lens, "seq_lens", torch.int32, 1)
+    _need(out, "out", dim=3)
+    _need(workspace, "workspace", torch.uint8)
+    if device_error is not None:
+        _need(device_error, "device_error", torch.int32)
+    T, Hq, D = q.shape
+    NP, Hkv, P, _ = k_cache.shape
+    B = seq_lens.shape[0]
+    if out.shape != q.shape:
+        raise ValueError("q / out shapes disagree")
+    if block_table.shape[0] != B or cu_q.shape[0] != B + 1:
+        raise ValueError("block_table / cu_q shapes disagree with seq_lens")
+    if k_scale.shape[0] != Hkv or v_scale.shape[0] != Hkv:
+        raise ValueError("scales must have one entry per kv head")
+    _check_page_sizes(seq_page_sizes, B)
+    _check_window(window, sinks)
+    _same_device(q, cu_q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, out, workspace, device_error,
+                 seq_page_sizes)
+    if sm_scale is None:
+        sm_scale = 1.0 / math.sqrt(D)
+    with _device_of(q):
+        st = load().pkv_paged_prefill_fp4(_ptr(q), _ptr(cu_q), T, int(max_q_len), _ptr(k_cache), _ptr(v_cache),
+                                          _ptr(k_scale), _ptr(v_scale), _ptr(block_table), block_table.shape[1],
+                                          _ptr(seq_lens), _ptr(seq_page_sizes), B, int(max_kv_len),
+                                          int(max_total_kv), Hq, Hkv, D, P, NP, float(sm_scale), int(window),
+                                          int(sinks), _ptr(out), _act_code(out), _ptr(workspace), workspace.numel(),
+                                          _ptr(device_error), _stream(stream))
+    if st != 0:
+        raise PkvError(st, "pkv_paged_prefill_fp4")
+
+
+def paged_prefill_fp4(q, cu_q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, max_q_len, out=None,
+                      out_dtype=torch.bfloat16, max_kv_len=None, workspace=None, sm_scale=None, device_error=None,
+                      stream=None, max_total_kv=0, seq_page_sizes=None, window=0, sinks=0) -> torch.Tensor:
+    """Allocating form of pkv_paged_prefill_fp4: max_kv_len defaults to the
+    block table's capacity, as in paged_prefill."""
+    if out is None:
+        out = torch.empty(q.shape, dtype=out_dtype, device=q.device)
+    if max_kv_len is None:
+        if seq_page_sizes is not None:
+            raise ValueError("give max_kv_len when seq_page_sizes is given")
+        max_kv_len = block_table.shape[1] * k_cache.shape[2]
+    if workspace is None:
+        _check_window(window, sinks)
+        n = pkv_prefill_fp4_workspace_size(seq_lens.shape[0], k_cache.shape[1], max_q_len, max_kv_len, max_total_kv,
+                                           window, sinks)
+        workspace = torch.empty(n, dtype=torch.uint8, device=q.device)
+    pkv_paged_prefill_fp4(q, cu_q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, out, max_q_len,
+                          max_kv_len, workspace, sm_scale, device_error, stream, max_total_kv, seq_page_sizes,
+                          window, sinks)
+    return out
+
+
 __all__ = ["load", "lib_path", "pkv_kv_append_fp8", "pkv_paged_gqa_decode", "pkv_decode_workspace_size",
            "pkv_paged_gqa_decode_noalloc", "pkv_decode_noalloc_scratch_bytes", "pkv_append_decode_fp8",
            "append_decode_fp8", "pkv_kv_calibrate", "pkv_paged_prefill", "paged_prefill", "pkv_prefill_workspace_size",
@@ -594,4 +846,7 @@ __all__ = ["load", "lib_path", "pkv_kv_append_fp8", "pkv_paged_gqa_decode", "pkv
            "paged_gqa_decode", "decode_workspace", "pkv_decode_set_split_weights", "pkv_decode_get_split_weights",
            "pkv_decode_calibrate_split",
            "PkvError", "PKV_F32", "PKV_BF16", "DEVERR_SLOT", "DEVERR_PAGE", "DEVERR_SEQLEN",
-           "DEVERR_TIMEOUT", "DEVERR_PAGESIZE", "DEVERR_INTERNAL", "pkv_last_cuda_error"]
+           "DEVERR_TIMEOUT", "DEVERR_PAGESIZE", "DEVERR_INTERNAL", "pkv_last_cuda_error",
+           "FP4_ROW_BYTES", "fp4_cache", "pkv_kv_append_fp4", "pkv_kv_read_fp4", "kv_append_fp4", "kv_read_fp4",
+           "pkv_decode_fp4_workspace_size", "pkv_paged_gqa_decode_fp4", "paged_gqa_decode_fp4",
+           "pkv_prefill_fp4_workspace_size", "pkv_paged_prefill_fp4", "paged_prefill_fp4"]

@@ -9,8 +9,8 @@
 #include <tuple>
 #include <vector>
 
+#include "api.h"
 #include "context.h"
-#include "internal.h"
 
 namespace pkv {
 
@@ -56,13 +56,6 @@ thread_local int t_last_cuda = 0;                           // error behind this
 thread_local const char *t_last_site = "";                  // the call that failed
 thread_local char t_last_text[160];
 
-pkv_status cuda_failed(cudaError_t e, const char *site = "")
-{
-    t_last_cuda = e == cudaSuccess ? static_cast<int>(cudaErrorUnknown) : static_cast<int>(e);
-    t_last_site = site;
-    return PKV_ERR_CUDA;
-}
-
 typedef CUresult (*EncodeTiledFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
                                   const cuuint64_t *, const cuuint32_t *, const cuuint32_t *,
                                   CUtensorMapInterleave, CUtensorMapSwizzle, CUtensorMapL2promotion,
@@ -99,6 +92,15 @@ bool make_page_map(CUtensorMap *tm, const uint8_t *pool, int64_t num_pages, int 
     return fn(tm, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<uint8_t *>(pool), dims, strides, box, estr,
               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+}  // namespace
+
+pkv_status cuda_failed(cudaError_t e, const char *site)
+{
+    t_last_cuda = e == cudaSuccess ? static_cast<int>(cudaErrorUnknown) : static_cast<int>(e);
+    t_last_site = site;
+    return PKV_ERR_CUDA;
 }
 
 // Queries [total_q][hq][128] bf16 as a 3-D tensor (128 dims, hq heads, total_q
@@ -138,10 +140,7 @@ bool make_kv16_map(CUtensorMap *tm, const void *base, long long rows, CUtensorMa
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-bool aligned(const void *p, uintptr_t a)
-{
-    return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0;
-}
+namespace {
 
 int current_device()
 {
@@ -220,24 +219,6 @@ int decode_num_ctas(int page_size, int batch, int max_ctas)
     return c;
 }
 
-// Workspace: header and segment records, then one partial slot per worker
-// plus one per segment (a piece is a worker's range within one segment; its
-// slot is worker + the segment's rank in list order, distinct for every piece).  Independent of the
-// sequence lengths.
-size_t decode_workspace_bytes(int batch, int hq, int hkv, long long /*max_len*/, int num_ctas)
-{
-    const long long workers = static_cast<long long>(num_ctas) * kWarps;
-    const size_t slots = static_cast<size_t>(workers) + static_cast<size_t>(batch) * hkv;
-    const size_t bytes = slots * static_cast<size_t>(hq / hkv) * kPartialStride * sizeof(float);
-    return decode_segment_bytes(batch, hkv) + ((bytes + 255) & ~size_t(255));
-}
-
-}  // namespace pkv
-
-using namespace pkv;
-
-namespace {
-
 pkv_status check_decode_shape(int batch, int hq, int hkv, int head_dim, int page_size, int max_pages,
                               int64_t num_pages)
 {
@@ -258,12 +239,23 @@ pkv_status check_decode_shape(int batch, int hq, int hkv, int head_dim, int page
     return PKV_OK;
 }
 
-// Effective bound of seq_lens: max_seq_len, or the table's capacity at the
-// pool page size when max_seq_len is 0.
-long long effective_max_len(int max_seq_len, int max_pages, int page_size)
+// Workspace: header and segment records, then one partial slot per worker
+// plus one per segment (a piece is a worker's range within one segment; its
+// slot is worker + the segment's rank in list order, distinct for every piece).  Independent of the
+// sequence lengths.
+size_t decode_workspace_bytes(int batch, int hq, int hkv, long long /*max_len*/, int num_ctas)
 {
-    return max_seq_len > 0 ? max_seq_len : static_cast<long long>(max_pages) * page_size;
+    const long long workers = static_cast<long long>(num_ctas) * kWarps;
+    const size_t slots = static_cast<size_t>(workers) + static_cast<size_t>(batch) * hkv;
+    const size_t bytes = slots * static_cast<size_t>(hq / hkv) * kPartialStride * sizeof(float);
+    return decode_segment_bytes(batch, hkv) + ((bytes + 255) & ~size_t(255));
 }
+
+}  // namespace pkv
+
+using namespace pkv;
+
+namespace {
 
 pkv_status decode_impl(const void *k_new, const void *v_new, int in_dtype, int n_new, const void *q, uint8_t *k_cache,
                        uint8_t *v_cache, const float *k_scale, const float *v_scale, const int32_t *block_table,

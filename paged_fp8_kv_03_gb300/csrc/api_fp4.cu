@@ -1,0 +1,242 @@
+// C entry points of the 4-bit cache: argument checks on the host and launches.
+#include <math.h>
+
+#include "api.h"
+#include "fp4.h"
+
+using namespace pkv;
+
+namespace {
+
+pkv_status check_rows(int64_t num_tokens, int hkv, int head_dim, int64_t num_pages, int page_size, int dtype)
+{
+    if (num_tokens < 0 || hkv <= 0 || num_pages <= 0)
+        return PKV_ERR_SHAPE;
+    if (dtype != PKV_F32 && dtype != PKV_BF16)
+        return PKV_ERR_DTYPE;
+    if (head_dim != kHeadDim || !page_size_ok(page_size))
+        return PKV_ERR_UNSUPPORTED;
+    return PKV_OK;
+}
+
+pkv_status rows_args(Fp4RowArgs &a, const void *k, const void *v, int dtype, int64_t num_tokens, int hkv,
+                     const int64_t *slots, const float *k_scale, const float *v_scale, const uint8_t *k_cache,
+                     const uint8_t *v_cache, int64_t num_pages, int page_size, int32_t *device_error)
+{
+    if (!k || !v || !slots || !k_scale || !v_scale || !k_cache || !v_cache)
+        return PKV_ERR_NULL;
+    if (!aligned(k, 16) || !aligned(v, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(slots, 8) ||
+        !aligned(k_scale, 4) || !aligned(v_scale, 4) || !aligned(device_error, 4))
+        return PKV_ERR_ALIGN;
+    a = Fp4RowArgs();
+    a.bf16 = dtype == PKV_BF16;
+    a.num_tokens = num_tokens;
+    a.hkv = hkv;
+    a.slots = slots;
+    a.k_scale = k_scale;
+    a.v_scale = v_scale;
+    a.k_cache = const_cast<uint8_t *>(k_cache);
+    a.v_cache = const_cast<uint8_t *>(v_cache);
+    a.num_slots = num_pages * page_size;
+    a.page_size = page_size;
+    a.err = device_error;
+    return PKV_OK;
+}
+
+// Checks that decode and prefill share.
+pkv_status check_attn(int batch, int hq, int hkv, int head_dim, int page_size, int max_pages, int64_t num_pages,
+                      const int32_t *seq_page_sizes, int window, int sinks, int out_dtype)
+{
+    const pkv_status st = check_decode_shape(batch, hq, hkv, head_dim, page_size, max_pages, num_pages);
+    if (st != PKV_OK)
+        return st;
+    if (window < 0 || sinks < 0)
+        return PKV_ERR_SHAPE;
+    if (num_pages * hkv * (page_size / 16) >= (int64_t(1) << 31))
+        return PKV_ERR_UNSUPPORTED;
+    if (seq_page_sizes && static_cast<int64_t>(max_pages) * 256 >= (int64_t(1) << 31))
+        return PKV_ERR_UNSUPPORTED;
+    if (out_dtype != PKV_F32 && out_dtype != PKV_BF16)
+        return PKV_ERR_DTYPE;
+    return PKV_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+pkv_status pkv_kv_append_fp4(const void *k_new, const void *v_new, int in_dtype, int64_t num_tokens,
+                             int num_kv_heads, int head_dim, const int64_t *slot_mapping, const float *k_scale,
+                             const float *v_scale, uint8_t *k_cache, uint8_t *v_cache, int64_t num_pages,
+                             int page_size, int32_t *device_error, cudaStream_t stream)
+{
+    pkv_status st = check_rows(num_tokens, num_kv_heads, head_dim, num_pages, page_size, in_dtype);
+    if (st != PKV_OK || num_tokens == 0)
+        return st;
+    Fp4RowArgs a;
+    st = rows_args(a, k_new, v_new, in_dtype, num_tokens, num_kv_heads, slot_mapping, k_scale, v_scale, k_cache,
+                   v_cache, num_pages, page_size, device_error);
+    if (st != PKV_OK)
+        return st;
+    a.k_in = k_new;
+    a.v_in = v_new;
+    const cudaError_t e = launch_kv_append_fp4(a, stream);
+    return e == cudaSuccess ? PKV_OK : cuda_failed(e, "4-bit append kernel launch");
+}
+
+pkv_status pkv_kv_read_fp4(const int64_t *slot_mapping, int64_t num_tokens, int num_kv_heads, int head_dim,
+                           const float *k_scale, const float *v_scale, const uint8_t *k_cache,
+                           const uint8_t *v_cache, int64_t num_pages, int page_size, void *k_out, void *v_out,
+                           int out_dtype, int32_t *device_error, cudaStream_t stream)
+{
+    pkv_status st = check_rows(num_tokens, num_kv_heads, head_dim, num_pages, page_size, out_dtype);
+    if (st != PKV_OK || num_tokens == 0)
+        return st;
+    Fp4RowArgs a;
+    st = rows_args(a, k_out, v_out, out_dtype, num_tokens, num_kv_heads, slot_mapping, k_scale, v_scale, k_cache,
+                   v_cache, num_pages, page_size, device_error);
+    if (st != PKV_OK)
+        return st;
+    a.k_out = k_out;
+    a.v_out = v_out;
+    const cudaError_t e = launch_kv_read_fp4(a, stream);
+    return e == cudaSuccess ? PKV_OK : cuda_failed(e, "4-bit read-back kernel launch");
+}
+
+size_t pkv_decode_fp4_workspace_size(int batch, int num_q_heads, int num_kv_heads, int head_dim, int max_seq_len,
+                                     int page_size, int max_ctas)
+{
+    if (check_decode_shape(batch, num_q_heads, num_kv_heads, head_dim, page_size, 1, 1) != PKV_OK ||
+        max_seq_len < 0 || max_ctas < 0)
+        return 0;
+    return 256;
+}
+
+pkv_status pkv_paged_gqa_decode_fp4(const void *q, const uint8_t *k_cache, const uint8_t *v_cache,
+                                    const float *k_scale, const float *v_scale, const int32_t *block_table,
+                                    int max_pages_per_seq, const int32_t *seq_lens, int max_seq_len,
+                                    const int32_t *seq_page_sizes, int batch, int num_q_heads, int num_kv_heads,
+                                    int head_dim, int page_size, int64_t num_pages, float sm_scale, int window,
+                                    int sinks, void *out, int out_dtype, void *workspace, size_t workspace_bytes,
+                                    int32_t *device_error, int max_ctas, cudaStream_t stream)
+{
+    const pkv_status st = check_attn(batch, num_q_heads, num_kv_heads, head_dim, page_size, max_pages_per_seq,
+                                     num_pages, seq_page_sizes, window, sinks, out_dtype);
+    if (st != PKV_OK)
+        return st;
+    if (max_seq_len < 0 || !(sm_scale == sm_scale) || isinf(sm_scale))
+        return PKV_ERR_SHAPE;
+    if (batch == 0)
+        return PKV_OK;
+    if (!q || !k_cache || !v_cache || !k_scale || !v_scale || !block_table || !seq_lens || !out)
+        return PKV_ERR_NULL;
+    if (!aligned(q, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(out, 16) ||
+        !aligned(block_table, 4) || !aligned(seq_lens, 4) || !aligned(k_scale, 4) || !aligned(v_scale, 4) ||
+        !aligned(device_error, 4) || !aligned(seq_page_sizes, 4))
+        return PKV_ERR_ALIGN;
+    if (!workspace || !aligned(workspace, 256) || workspace_bytes < 256)
+        return PKV_ERR_WORKSPACE;
+    const long long max_len = effective_max_len(max_seq_len, max_pages_per_seq, page_size);
+    if (max_len >= (int64_t(1) << 31))
+        return PKV_ERR_UNSUPPORTED;
+    Fp4AttnArgs a = {};
+    a.q = static_cast<const __nv_bfloat16 *>(q);
+    a.k_scale = k_scale;
+    a.v_scale = v_scale;
+    a.block_table = block_table;
+    a.max_pages = max_pages_per_seq;
+    a.seq_lens = seq_lens;
+    a.max_len = static_cast<int>(max_len);
+    a.page_sizes = seq_page_sizes;
+    a.batch = batch;
+    a.hq = num_q_heads;
+    a.hkv = num_kv_heads;
+    a.group = num_q_heads / num_kv_heads;
+    a.page_size = page_size;
+    a.pool_log2 = 31 - __builtin_clz(static_cast<unsigned>(page_size));
+    a.num_pages = num_pages;
+    a.k_cache = k_cache;
+    a.v_cache = v_cache;
+    a.sm_scale_log2 = sm_scale * 1.4426950408889634f;
+    a.win.window = window;
+    a.win.sinks = sinks;
+    a.out = out;
+    a.out_f32 = out_dtype == PKV_F32;
+    a.err = device_error;
+    (void)max_ctas;
+    const cudaError_t e = launch_attend_fp4(a, stream);
+    return e == cudaSuccess ? PKV_OK : cuda_failed(e, "4-bit decode kernel launch");
+}
+
+size_t pkv_prefill_fp4_workspace_size(int batch, int num_kv_heads, int max_q_len, int max_kv_len,
+                                      int64_t max_total_kv, int window, int sinks)
+{
+    if (batch < 0 || num_kv_heads <= 0 || max_q_len < 0 || max_kv_len < 0 || max_total_kv < 0 || window < 0 ||
+        sinks < 0)
+        return 0;
+    return 256;
+}
+
+pkv_status pkv_paged_prefill_fp4(const void *q, const int32_t *cu_q, int total_q, int max_q_len,
+                                 const uint8_t *k_cache, const uint8_t *v_cache, const float *k_scale,
+                                 const float *v_scale, const int32_t *block_table, int max_pages_per_seq,
+                                 const int32_t *seq_lens, const int32_t *seq_page_sizes, int batch, int max_kv_len,
+                                 int64_t max_total_kv, int num_q_heads, int num_kv_heads, int head_dim,
+                                 int page_size, int64_t num_pages, float sm_scale, int window, int sinks, void *out,
+                                 int out_dtype, void *workspace, size_t workspace_bytes, int32_t *device_error,
+                                 cudaStream_t stream)
+{
+    const pkv_status st = check_attn(batch, num_q_heads, num_kv_heads, head_dim, page_size, max_pages_per_seq,
+                                     num_pages, seq_page_sizes, window, sinks, out_dtype);
+    if (st != PKV_OK)
+        return st;
+    if (total_q < 0 || max_q_len < 0 || max_kv_len < 0 || max_total_kv < 0)
+        return PKV_ERR_SHAPE;
+    if (!(sm_scale > 0.f) || isinf(sm_scale))
+        return PKV_ERR_SHAPE;
+    if (batch == 0 || total_q == 0 || max_q_len == 0)
+        return PKV_OK;
+    if (!q || !cu_q || !k_cache || !v_cache || !k_scale || !v_scale || !block_table || !seq_lens || !out)
+        return PKV_ERR_NULL;
+    if (!aligned(q, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(out, 16) ||
+        !aligned(cu_q, 4) || !aligned(block_table, 4) || !aligned(seq_lens, 4) || !aligned(k_scale, 4) ||
+        !aligned(v_scale, 4) || !aligned(device_error, 4) || !aligned(seq_page_sizes, 4))
+        return PKV_ERR_ALIGN;
+    if (static_cast<int64_t>(total_q) * num_kv_heads >= (int64_t(1) << 31))
+        return PKV_ERR_UNSUPPORTED;
+    if (max_kv_len == 0)
+        return PKV_OK;                                   // no sequence can hold a query
+    if (!workspace || !aligned(workspace, 256) || workspace_bytes < 256)
+        return PKV_ERR_WORKSPACE;
+    Fp4AttnArgs a = {};
+    a.q = static_cast<const __nv_bfloat16 *>(q);
+    a.cu_q = cu_q;
+    a.total_q = total_q;
+    a.max_q_len = max_q_len;
+    a.k_scale = k_scale;
+    a.v_scale = v_scale;
+    a.block_table = block_table;
+    a.max_pages = max_pages_per_seq;
+    a.seq_lens = seq_lens;
+    a.max_len = max_kv_len;
+    a.page_sizes = seq_page_sizes;
+    a.batch = batch;
+    a.hq = num_q_heads;
+    a.hkv = num_kv_heads;
+    a.group = num_q_heads / num_kv_heads;
+    a.page_size = page_size;
+    a.pool_log2 = 31 - __builtin_clz(static_cast<unsigned>(page_size));
+    a.num_pages = num_pages;
+    a.k_cache = k_cache;
+    a.v_cache = v_cache;
+    a.sm_scale_log2 = sm_scale * 1.4426950408889634f;
+    a.win.window = window;
+    a.win.sinks = sinks;
+    a.out = out;
+    a.out_f32 = out_dtype == PKV_F32;
+    a.err = device_error;
+    const cudaError_t e = launch_attend_fp4(a, stream);
+    return e == cudaSuccess ? PKV_OK : cuda_failed(e, "4-bit prefill kernel launch");
+}
+
+}  // extern "C"

@@ -1,0 +1,61 @@
+// Declarations of the 4-bit cache's translation units (not installed): the
+// tile layout, the arguments of the kernels and their launchers.
+#pragma once
+
+#include "internal.h"
+
+namespace pkv {
+
+// 16 tokens of one kv head are one tile: 64 bytes of codes a token (dim 2i in
+// the low nibble of byte i, dim 2i + 1 in the high one), then 8 scales a token.
+constexpr int kFp4Tile = 16 * PKV_FP4_ROW_BYTES;           // 1152 bytes
+constexpr int kFp4Codes = 16 * (kHeadDim / 2);             // 1024: where the scales start
+
+struct Fp4RowArgs {                                        // append and read back
+    const void *k_in, *v_in;                               // append: rows to quantise
+    void *k_out, *v_out;                                   // read back: rows to write
+    int bf16;                                              // rows are bf16 (else fp32)
+    int64_t num_tokens;
+    int hkv;
+    const int64_t *slots;
+    const float *k_scale, *v_scale;
+    uint8_t *k_cache, *v_cache;
+    int64_t num_slots;
+    int page_size;
+    int32_t *err;
+};
+
+// Tokens a query at position p sees: t <= p with t > p - window or t < sinks
+// (window == 0: all t <= p).
+struct Fp4Window {
+    int window, sinks;
+};
+
+// One query row against the cache: the fields that the shared page walk
+// (seq_page_log2, seq_token_page) reads have the same names as in DecodeArgs.
+struct Fp4AttnArgs {
+    const __nv_bfloat16 *q;
+    const int32_t *cu_q;                                   // [batch + 1], or nullptr: one row per sequence (decode)
+    int total_q, max_q_len;
+    const float *k_scale, *v_scale;
+    const int32_t *block_table;
+    int max_pages;
+    const int32_t *seq_lens;
+    int max_len;
+    const int32_t *page_sizes;
+    int batch, hq, hkv, group;
+    int page_size, pool_log2;
+    int64_t num_pages;
+    const uint8_t *k_cache, *v_cache;
+    float sm_scale_log2;
+    Fp4Window win;
+    void *out;
+    int out_f32;
+    int32_t *err;
+};
+
+cudaError_t launch_kv_append_fp4(const Fp4RowArgs &a, cudaStream_t stream);
+cudaError_t launch_kv_read_fp4(const Fp4RowArgs &a, cudaStream_t stream);
+cudaError_t launch_attend_fp4(const Fp4AttnArgs &a, cudaStream_t stream);
+
+}  // namespace pkv
