@@ -168,8 +168,7 @@ int device_sm_count()
     return n;
 }
 
-// Persistent grid: every resident CTA slot on the device (capped by max_ctas).
-int decode_num_ctas(int page_size, int batch, int max_ctas)
+int resident_ctas(const void *kern, int threads, size_t smem, int max_ctas)
 {
     const int dev = current_device();
     const int sms = device_sm_count();
@@ -177,8 +176,6 @@ int decode_num_ctas(int page_size, int batch, int max_ctas)
         cuda_failed(cudaGetLastError(), "device query");
         return 0;
     }
-    const size_t smem = decode_smem_bytes(page_size, batch);
-    const void *kern = decode_kernel_for(page_size);
     int per_sm = 0;
     {
         unsigned long long ctx = 0;
@@ -201,7 +198,7 @@ int decode_num_ctas(int page_size, int batch, int max_ctas)
         if (it != g_occupancy.end()) {
             per_sm = it->second;
         } else {
-            const cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, kThreads, smem);
+            const cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, threads, smem);
             if (e != cudaSuccess) {
                 cuda_failed(e, "cudaOccupancyMaxActiveBlocksPerMultiprocessor (decode)");
                 return 0;
@@ -217,6 +214,17 @@ int decode_num_ctas(int page_size, int batch, int max_ctas)
     if (max_ctas > 0 && max_ctas < c)
         c = max_ctas;
     return c;
+}
+
+// Persistent grid: every resident CTA slot on the device (capped by max_ctas).
+int decode_num_ctas(int page_size, int batch, int max_ctas)
+{
+    return resident_ctas(decode_kernel_for(page_size), kThreads, decode_smem_bytes(page_size, batch), max_ctas);
+}
+
+int withheld_load()
+{
+    return g_withhold.load(std::memory_order_relaxed);
 }
 
 pkv_status check_decode_shape(int batch, int hq, int hkv, int head_dim, int page_size, int max_pages,

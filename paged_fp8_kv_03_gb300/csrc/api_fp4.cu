@@ -61,6 +61,26 @@ pkv_status check_attn(int batch, int hq, int hkv, int head_dim, int page_size, i
     return PKV_OK;
 }
 
+// CTAs of the decode grid (the kernel with two parts a weight needs no fewer
+// registers, so its count holds for both).
+int decode_ctas(int batch, int max_ctas)
+{
+    const size_t smem = decode_fp4_smem(batch);
+    const int one = resident_ctas(decode_fp4_kernel(false), 32 * kFp4DecodeWarps, smem, max_ctas);
+    const int two = one <= 0 ? 0 : resident_ctas(decode_fp4_kernel(true), 32 * kFp4DecodeWarps, smem, max_ctas);
+    return two < one ? two : one;
+}
+
+// Workspace: the segments' first and last workers, then one state a worker
+// and one a segment (a piece's slot is worker + rank of its segment, distinct
+// because both grow along the list).
+size_t decode_workspace(int batch, int hq, int hkv, int ctas)
+{
+    const size_t slots = static_cast<size_t>(ctas) * kFp4DecodeWarps + static_cast<size_t>(batch) * hkv;
+    const size_t bytes = slots * static_cast<size_t>(hq / hkv) * kPartialStride * sizeof(float);
+    return decode_fp4_join_bytes(batch, hkv) + ((bytes + 255) & ~size_t(255));
+}
+
 }  // namespace
 
 extern "C" {
@@ -109,7 +129,8 @@ size_t pkv_decode_fp4_workspace_size(int batch, int num_q_heads, int num_kv_head
     if (check_decode_shape(batch, num_q_heads, num_kv_heads, head_dim, page_size, 1, 1) != PKV_OK ||
         max_seq_len < 0 || max_ctas < 0)
         return 0;
-    return 256;
+    const int ctas = decode_ctas(batch, max_ctas);
+    return ctas <= 0 ? 0 : decode_workspace(batch, num_q_heads, num_kv_heads, ctas);
 }
 
 pkv_status pkv_paged_gqa_decode_fp4(const void *q, const uint8_t *k_cache, const uint8_t *v_cache,
@@ -134,7 +155,7 @@ pkv_status pkv_paged_gqa_decode_fp4(const void *q, const uint8_t *k_cache, const
         !aligned(block_table, 4) || !aligned(seq_lens, 4) || !aligned(k_scale, 4) || !aligned(v_scale, 4) ||
         !aligned(device_error, 4) || !aligned(seq_page_sizes, 4))
         return PKV_ERR_ALIGN;
-    if (!workspace || !aligned(workspace, 256) || workspace_bytes < 256)
+    if (!workspace || !aligned(workspace, 256))
         return PKV_ERR_WORKSPACE;
     const long long max_len = effective_max_len(max_seq_len, max_pages_per_seq, page_size);
     if (max_len >= (int64_t(1) << 31))
@@ -163,9 +184,33 @@ pkv_status pkv_paged_gqa_decode_fp4(const void *q, const uint8_t *k_cache, const
     a.out = out;
     a.out_f32 = out_dtype == PKV_F32;
     a.err = device_error;
-    (void)max_ctas;
-    const cudaError_t e = launch_attend_fp4(a, stream);
-    return e == cudaSuccess ? PKV_OK : cuda_failed(e, "4-bit decode kernel launch");
+    // Units of 32 tokens that the longest sequence can show; a list with fewer
+    // units than the device has workers needs no more CTAs than it has units.
+    long long tiles = (max_len + 15) / 16;
+    if (window > 0) {
+        const long long seen = (static_cast<long long>(sinks) + 15) / 16 + (static_cast<long long>(window) + 15) / 16 + 1;
+        tiles = seen < tiles ? seen : tiles;
+    }
+    const long long units = (tiles + 1) / 2 * batch * num_kv_heads;
+    if (units >= (int64_t(1) << 31))
+        return PKV_ERR_UNSUPPORTED;
+    int ctas = decode_ctas(batch, max_ctas);
+    if (ctas <= 0)
+        return PKV_ERR_CUDA;                             // resident_ctas recorded the failing call
+    if (workspace_bytes < decode_workspace(batch, num_q_heads, num_kv_heads, ctas))
+        return PKV_ERR_WORKSPACE;
+    if (units < ctas)
+        ctas = static_cast<int>(units > 0 ? units : 1);
+    Fp4DecodeArgs da;
+    da.a = a;
+    da.joins = static_cast<int2 *>(workspace);
+    const size_t joins = decode_fp4_join_bytes(batch, num_kv_heads);
+    da.partials = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + joins);
+    da.num_slots = static_cast<long long>((workspace_bytes - joins) / (sizeof(float) * a.group * kPartialStride));
+    da.withhold = withheld_load();
+    const char *site = "";
+    const cudaError_t e = launch_paged_decode_fp4(da, ctas, stream, &site);
+    return e == cudaSuccess ? PKV_OK : cuda_failed(e, site);
 }
 
 size_t pkv_prefill_fp4_workspace_size(int batch, int num_kv_heads, int max_q_len, int max_kv_len,

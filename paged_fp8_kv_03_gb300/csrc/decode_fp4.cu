@@ -1,0 +1,776 @@
+// paged_gqa_decode_fp4: grouped-query decode attention over the 4-bit cache,
+// with an optional window and sinks.
+//   s_t = sm_scale k_scale q . (e s)_t,  w = softmax(s),  o = v_scale sum_t w_t (e s)_t
+//
+// What bounds it: every visible row is read once, 72 bytes of K and 72 of V,
+// so the floor is the HBM's.  At that rate an SM gets a 16-token tile (2304
+// bytes) about every 100 cycles, and widening its 4096 codes costs an SMSP's
+// issue slots and its conversion pipe (2 cycles a pair of codes and scale:
+// measured 2.5 with the multiply) more than the two matrix products do
+// (mma.sync m16n8k16: 8 cycles), so the design keeps everything else few.
+//
+// Work split.  The visible tokens of a (sequence, kv head) segment are cut in
+// units of two 16-token tiles (a window leaves the tiles of the sinks and
+// those of the window).  The segments lie end to end in one list, kv head by
+// kv head; every warp of the grid takes an equal contiguous range of it,
+// whatever the lengths.  A range cuts segments into pieces: a whole segment
+// is written out, other pieces leave a (max, sum, accumulator) state in
+// workspace slot worker + rank of the segment, and a second kernel (a
+// programmatic dependent launch) joins them in worker order.  Worker w is
+// warp w / CTAs of CTA w % CTAs, so that short lists spread over the SMs.
+//
+// A warp brings its units in by bulk copies (a tile of K and one of V are
+// 1152 contiguous bytes each) into its own ring, each stage with its own
+// mbarrier.  The codes go from shared memory straight into mma.sync
+// fragments, because the order of the contracted index is free as long as
+// both operands agree on it:
+//   S^T[t][g] = K[t][:] . Q[g][:]    A = K: lane (r, c) takes the 32 dims 32c .. 32c+31 of row r,
+//                                    16 bytes of codes and two scales
+//   O^T[d][g] += V^T[d][t] P^T[t][g]  A = V^T: lane (r, c) takes the 16 dims of block r of 4 tokens;
+//                                    two tokens' nibbles are interleaved before they are widened,
+//                                    so that a conversion gives a pair of tokens
+// Codes times their block scale are exact in f16 (6 significant bits).  The
+// weights leave the S^T fragment as B operand through two 8x8 transposes.
+// Heads are columns of both results, so the running maximum and sum of a head
+// sit in the lanes that hold its accumulator and a rescale needs no exchange;
+// the maximum is moved only when a score exceeds it by more than 2^8.
+//
+// Every wait on an mbarrier is bounded (2 s): on expiry the kernel raises
+// PKV_DEVERR_TIMEOUT, stops issuing copies, drains those in flight, returns.
+#include <math.h>
+
+#include "fp4.cuh"
+
+namespace pkv {
+
+namespace {
+
+constexpr int kWarpsD = kFp4DecodeWarps;
+constexpr int kThreadsD = 32 * kWarpsD;
+constexpr int kStagesD = 3;
+constexpr int kUnitBytes = 4 * kFp4Tile;                   // K tile 0, K tile 1, V tile 0, V tile 1
+constexpr float kMoveMax = 8.f;                            // log2 units
+// Units after which a piece's accumulator is added into an fp32 copy: the
+// tensor cores add with truncation, whose error grows with the chain.
+constexpr int kFoldUnits = 64;
+constexpr uint64_t kLimitNs = 2000000000ull;
+
+struct SmemD {                                             // the ring, [warps][stages][kUnitBytes], comes first
+    static constexpr int kFold = kWarpsD * kStagesD * kUnitBytes;           // [warps][32 values][32 lanes]
+    static constexpr int kBar = kFold + kWarpsD * 32 * 32 * 4;
+    static constexpr int kFlag = kBar + kWarpsD * kStagesD * 8;
+    static constexpr int kSums = kFlag + 16;
+    static constexpr int kStart = kSums + 16 * ((kWarpsD * 4 + 15) / 16);   // int [batch + 1]
+    static size_t bytes(int batch) { return static_cast<size_t>(kStart) + 4u * (batch + 1); }
+};
+
+// What one sequence shows its query: tokens [0, sinks) and [from, len), as
+// tiles 0 .. first - 1 and then first + skip .. (tiles in all).
+struct Sight {
+    int len, sinks, from, first, skip, tiles;
+};
+
+__device__ __forceinline__ Sight sight_of(const Fp4AttnArgs &a, int b)
+{
+    Sight s;
+    const int lp = seq_page_log2(a, b);
+    const long long cap = lp < 0 ? 0 : static_cast<long long>(a.max_pages) << lp;
+    const int most = cap < a.max_len ? static_cast<int>(cap) : a.max_len;
+    const int L = __ldg(a.seq_lens + b);
+    s.len = L < 0 ? 0 : min(L, most);
+    s.from = a.win.window == 0 ? 0 : max(0, s.len - a.win.window);
+    s.sinks = min(a.win.sinks, s.from);
+    s.first = (s.sinks + 15) >> 4;
+    s.skip = max(s.from >> 4, s.first) - s.first;
+    s.tiles = ((s.len + 15) >> 4) - s.skip;
+    return s;
+}
+
+// Tile of the sequence that is tile i of its visible ones.
+__device__ __forceinline__ int tile_at(const Sight &s, int i)
+{
+    return i < s.first ? i : i + s.skip;
+}
+
+struct Place {
+    int b, h, unit;
+};
+
+__device__ __forceinline__ Place place_of(const int *start, int batch, int x)
+{
+    const int per_head = start[batch];
+    Place p;
+    p.h = x / per_head;
+    const int rem = x - p.h * per_head;
+    int lo = 0, hi = batch - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (start[mid] <= rem)
+            lo = mid;
+        else
+            hi = mid - 1;
+    }
+    p.b = lo;
+    p.unit = rem - start[lo];
+    return p;
+}
+
+__device__ __forceinline__ bool wait_stage(uint32_t bar, uint32_t parity, volatile int *stop, int32_t *err, int lane)
+{
+    uint64_t t0 = 0;
+    for (uint32_t it = 0;; ++it) {
+        if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity)))
+            return true;
+        if ((it & 15u) == 15u) {
+            int quit = 0;
+            if (lane == 0) {
+                if (t0 == 0)
+                    t0 = global_timer_ns();
+                if (*stop) {
+                    quit = 1;
+                } else if (global_timer_ns() - t0 > kLimitNs) {
+                    *stop = 1;
+                    if (err)
+                        atomicOr(err, PKV_DEVERR_TIMEOUT);
+                    quit = 1;
+                }
+            }
+            if (__shfl_sync(0xffffffffu, quit, 0))
+                return false;
+        }
+    }
+}
+
+__device__ __forceinline__ void lds128(uint32_t at, uint32_t (&r)[4])
+{
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(at));
+}
+__device__ __forceinline__ void lds64(uint32_t at, uint32_t (&r)[2])
+{
+    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(r[0]), "=r"(r[1]) : "r"(at));
+}
+__device__ __forceinline__ uint32_t lds16(uint32_t at)
+{
+    uint16_t v;
+    asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(at));
+    return v;
+}
+__device__ __forceinline__ uint32_t lds8(uint32_t at)
+{
+    uint32_t v;
+    asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(at));
+    return v;
+}
+
+__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b)
+{
+    uint32_t d;
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+}
+
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t a)
+{
+    uint32_t d;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
+    return d;
+}
+
+// Two E4M3 bytes (low 16 bits) -> f16 pair.
+__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t s)
+{
+    uint32_t d;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(d) : "h"(static_cast<uint16_t>(s)));
+    return d;
+}
+
+// Row n of a fragment is token order(n) of its tile (8 + order(n - 8) for the
+// upper half): adjacent lanes' K rows then differ in parity (conflict-free
+// 16-byte reads) and a quad's V rows pair up even and odd (2-way).
+__device__ __forceinline__ int order(int n)
+{
+    return n ^ ((n >> 1) & 1);
+}
+
+// One tile's raw bytes of a lane.
+struct Raw {
+    uint32_t k[2][4];     // codes of K rows order(r), order(r) + 8: dims 32c ..
+    uint32_t ks[2];       // their two block scales
+    uint32_t v[4][2];     // codes of block r of V rows order(2c), order(2c + 1), and both + 8
+    uint32_t vs[2];       // scale bytes of the first pair, of the second pair
+};
+
+__device__ __forceinline__ void load_raw(uint32_t kt, uint32_t vt, int r, int c, Raw &x)
+{
+    const int k0 = order(r), v0 = order(2 * c), v1 = order(2 * c + 1);
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+        lds128(kt + (k0 + 8 * j) * 64 + 16 * c, x.k[j]);
+        x.ks[j] = lds16(kt + kFp4Codes + (k0 + 8 * j) * 8 + 2 * c);
+        lds64(vt + (v0 + 8 * j) * 64 + 8 * r, x.v[2 * j]);
+        lds64(vt + (v1 + 8 * j) * 64 + 8 * r, x.v[2 * j + 1]);
+        x.vs[j] = lds8(vt + kFp4Codes + (v0 + 8 * j) * 8 + r) | (lds8(vt + kFp4Codes + (v1 + 8 * j) * 8 + r) << 8);
+    }
+}
+
+// Scores of a tile: lane (r, c) gets tokens order(r) (y[0], y[1]) and
+// order(r) + 8 (y[2], y[3]) of heads 2c, 2c + 1, times f0, f1.
+__device__ __forceinline__ void scores(const Raw &x, const uint32_t (&q)[8][2], float f0, float f1, float (&y)[4])
+{
+    uint32_t s[2][2];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+        const uint32_t p = e4m3x2_to_f16x2(x.ks[j]);
+        s[j][0] = __byte_perm(p, p, 0x1010);
+        s[j][1] = __byte_perm(p, p, 0x3232);
+    }
+    float d[2][4] = {};
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+        uint32_t a[2][4];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            e2m1x8_to_f16x8(x.k[j][w], a[j]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                a[j][i] = mul_f16x2(a[j][i], s[j][w >> 1]);
+        }
+        mma_16816(d[0], a[0][0], a[1][0], a[0][1], a[1][1], q[2 * w][0], q[2 * w][1]);
+        mma_16816(d[1], a[0][2], a[1][2], a[0][3], a[1][3], q[2 * w + 1][0], q[2 * w + 1][1]);
+    }
+    y[0] = (d[0][0] + d[1][0]) * f0;
+    y[1] = (d[0][1] + d[1][1]) * f1;
+    y[2] = (d[0][2] + d[1][2]) * f0;
+    y[3] = (d[0][3] + d[1][3]) * f1;
+}
+
+// acc += V^T P^T for a tile; b: the weights of its 16 tokens (B fragment) in
+// kParts f16 parts.
+template <int kParts>
+__device__ __forceinline__ void accumulate(const Raw &x, const uint32_t (&b)[kParts][2], float (&acc)[8][4])
+{
+    const uint32_t s0 = e4m3x2_to_f16x2(x.vs[0]), s1 = e4m3x2_to_f16x2(x.vs[1]);
+    constexpr uint32_t kLow = 0x0F0F0F0Fu;
+#pragma unroll
+    for (int w = 0; w < 2; ++w) {
+        uint32_t e[2][4], o[2][4];                         // even, odd dims of the block; pair 0, pair 1
+#pragma unroll
+        for (int p = 0; p < 2; ++p) {
+            const uint32_t t0 = x.v[2 * p][w], t1 = x.v[2 * p + 1][w];
+            e2m1x8_to_f16x8((t0 & kLow) | ((t1 << 4) & ~kLow), e[p]);
+            e2m1x8_to_f16x8(((t0 >> 4) & kLow) | (t1 & ~kLow), o[p]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                e[p][i] = mul_f16x2(e[p][i], p ? s1 : s0);
+                o[p][i] = mul_f16x2(o[p][i], p ? s1 : s0);
+            }
+        }
+#pragma unroll
+        for (int part = 0; part < kParts; ++part)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                mma_16816(acc[4 * w + i], e[0][i], o[0][i], e[1][i], o[1][i], b[part][0], b[part][1]);
+    }
+}
+
+// 16 consecutive dims of one output row.
+__device__ __forceinline__ void store16(const Fp4AttnArgs &a, int64_t row, int d, const float (&v)[16])
+{
+    if (a.out_f32) {
+        float4 *p = reinterpret_cast<float4 *>(static_cast<float *>(a.out) + row * kHeadDim + d);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            p[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+    } else {
+        uint4 *p = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.out) + row * kHeadDim + d);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            uint32_t w[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const __nv_bfloat162 b = __floats2bfloat162_rn(v[8 * i + 2 * j], v[8 * i + 2 * j + 1]);
+                w[j] = *reinterpret_cast<const uint32_t *>(&b);
+            }
+            p[i] = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+    }
+}
+
+// kParts: f16 parts of a softmax weight.  One (rounded to f16, 2^-11, and the
+// normalising sum is of the rounded ones) is enough under a bf16 output's
+// 2^-8; two keep an fp32 output to 2^-21.
+template <int kParts>
+__global__ void __launch_bounds__(kThreadsD, kFp4DecodeCtas) paged_gqa_decode_fp4_kernel(const Fp4DecodeArgs da)
+{
+    const Fp4AttnArgs &a = da.a;
+    extern __shared__ __align__(128) uint8_t smem[];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    int *start = reinterpret_cast<int *>(smem + SmemD::kStart);
+    volatile int *stop = reinterpret_cast<volatile int *>(smem + SmemD::kFlag);
+    int *sums = reinterpret_cast<int *>(smem + SmemD::kSums);
+
+    // ---- first unit of every sequence (of one kv head): a prefix sum over the batch
+    {
+        const int per = (a.batch + kThreadsD - 1) / kThreadsD;
+        const int b0 = min(a.batch, tid * per), b1 = min(a.batch, b0 + per);
+        int mine = 0;
+        for (int b = b0; b < b1; ++b)
+            mine += (sight_of(a, b).tiles + 1) >> 1;
+        int incl = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int v = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o)
+                incl += v;
+        }
+        if (lane == 31)
+            sums[warp] = incl;
+        if (tid == 0) {
+            *stop = 0;
+            for (int s = 0; s < kWarpsD * kStagesD; ++s)
+                mbar_init(smem_addr(smem + SmemD::kBar) + 8 * s, 1);
+            fence_barrier_init();
+        }
+        __syncthreads();
+        int run = incl - mine;
+        for (int w = 0; w < warp; ++w)
+            run += sums[w];
+        for (int b = b0; b < b1; ++b) {
+            const Sight s = sight_of(a, b);
+            start[b] = run;
+            run += (s.tiles + 1) >> 1;
+            if (blockIdx.x == 0 && a.err) {
+                if (seq_page_log2(a, b) < 0)
+                    atomicOr(a.err, PKV_DEVERR_PAGESIZE);
+                else if (__ldg(a.seq_lens + b) != s.len)
+                    atomicOr(a.err, PKV_DEVERR_SEQLEN);
+            }
+        }
+        if (tid == kThreadsD - 1)
+            start[a.batch] = run;
+        __syncthreads();
+    }
+
+    // ---- sequences with no tokens: zero rows, and nothing to join
+    for (int sg = blockIdx.x; sg < a.batch * a.hkv; sg += gridDim.x) {
+        const int b = sg / a.hkv;
+        if (start[b + 1] == start[b]) {
+            const int64_t row0 = static_cast<int64_t>(b) * a.hq + static_cast<int64_t>(sg % a.hkv) * a.group;
+            for (int e = tid; e < a.group * kHeadDim; e += kThreadsD) {
+                if (a.out_f32)
+                    static_cast<float *>(a.out)[row0 * kHeadDim + e] = 0.f;
+                else
+                    static_cast<__nv_bfloat16 *>(a.out)[row0 * kHeadDim + e] = __float2bfloat16_rn(0.f);
+            }
+            if (tid == 0)
+                da.joins[sg] = make_int2(-1, -1);
+        }
+    }
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+
+    const int total = start[a.batch] * a.hkv;
+    const int worker = warp * gridDim.x + blockIdx.x;
+    const int active = min(static_cast<int>(gridDim.x) * kWarpsD, total);
+    if (worker >= active)
+        return;                                            // no CTA barrier follows
+    const int lo = static_cast<int>(static_cast<int64_t>(total) * worker / active);
+    const int n = static_cast<int>(static_cast<int64_t>(total) * (worker + 1) / active) - lo;
+
+    const uint32_t ring = smem_addr(smem) + warp * kStagesD * kUnitBytes;
+    const uint32_t bars = smem_addr(smem + SmemD::kBar) + warp * kStagesD * 8;
+    float *fold = reinterpret_cast<float *>(smem + SmemD::kFold) + warp * 1024 + lane;
+
+    // ---- tile addresses, 16 units ahead: lane 2i + j has tile j of unit i.
+    // -1: a page outside the pool; -2: no such tile.
+    auto look_up = [&](int u0) -> int {
+        const int u = u0 + (lane >> 1);
+        if (u >= n)
+            return -2;
+        const Place p = place_of(start, a.batch, lo + u);
+        const Sight s = sight_of(a, p.b);
+        const int i = 2 * p.unit + (lane & 1);
+        if (i >= s.tiles)
+            return -2;
+        int phys, row;
+        if (!seq_token_page(a, p.b, seq_page_log2(a, p.b), 16 * tile_at(s, i), phys, row)) {
+            if (a.err)
+                atomicOr(a.err, PKV_DEVERR_PAGE);
+            return -1;
+        }
+        return (phys * a.hkv + p.h) * (a.page_size >> 4) + (row >> 4);
+    };
+    int now = look_up(0), next = look_up(16), base = 0;
+    uint32_t bad = 0, pending = 0, pend_par = 0;           // per stage: missing tiles (2 bits), copies in flight
+    auto issue = [&](int u) {
+        if (u >= base + 16) {
+            base += 16;
+            now = next;
+            next = look_up(base + 16);
+        }
+        const int s = u % kStagesD;
+        const int t = __shfl_sync(0xffffffffu, now, 2 * (u - base) + (lane & 1));
+        const uint32_t have = __ballot_sync(0xffffffffu, t >= 0) & 3u;
+        bad = (bad & ~(3u << (2 * s))) | ((~have & 3u) << (2 * s));
+        const bool go = __shfl_sync(0xffffffffu, !*stop && !(worker == da.withhold && u == 0), 0);
+        if (go) {
+            if (lane == 0)
+                mbar_arrive_expect_tx(bars + 8 * s, 2 * kFp4Tile * __popc(have));
+            __syncwarp();
+            if (lane < 4 && t >= 0)                        // lanes 0, 1: K tiles; 2, 3: V tiles
+                bulk_load(ring + s * kUnitBytes + lane * kFp4Tile,
+                          (lane < 2 ? a.k_cache : a.v_cache) + static_cast<int64_t>(t) * kFp4Tile, kFp4Tile,
+                          bars + 8 * s);
+            pending |= 1u << s;
+            pend_par = (pend_par & ~(1u << s)) | ((static_cast<uint32_t>(u / kStagesD) & 1u) << s);
+        }
+    };
+    for (int u = 0; u < kStagesD && u < n; ++u)
+        issue(u);
+
+    const int r = lane >> 2, c = lane & 3;
+    const int tok = order(r);
+    int stage = 0;
+    uint32_t parity = 0;
+    int u = 0;
+    while (u < n) {
+        const Place p = place_of(start, a.batch, lo + u);
+        const Sight sg = sight_of(a, p.b);
+        const int units = start[p.b + 1] - start[p.b];
+        const int take = min(units - p.unit, n - u);
+        const bool whole = p.unit == 0 && take == units;
+        const int64_t row0 = static_cast<int64_t>(p.b) * a.hq + static_cast<int64_t>(p.h) * a.group;
+        if (lane == 0) {                                   // who holds the segment's first and last unit
+            int2 *j = da.joins + p.b * a.hkv + p.h;
+            if (p.unit == 0)
+                j->x = whole ? -1 : worker;
+            if (p.unit + take == units)
+                j->y = worker;
+        }
+        // Q as B fragment: head r, dims 32c + 4 kk + {0, 1} and {2, 3}; brought
+        // to [1, 2) by a power of two, so that f16 holds all its bits.
+        uint32_t q[8][2];
+        float f0, f1;
+        {
+            uint4 v[4];
+            const uint4 *src = reinterpret_cast<const uint4 *>(a.q + (row0 + (r < a.group ? r : 0)) * kHeadDim + 32 * c);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                v[i] = __ldg(src + i);
+            const uint32_t *w = reinterpret_cast<const uint32_t *>(v);
+            uint32_t top = 0;                              // largest |q|, as its bits
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+                top = max(top, max((w[i] << 16) & 0x7FFFFFFFu, w[i] & 0x7FFF0000u));
+            top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+            top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+            const int ex = min(max(static_cast<int>(top >> 23), 1), 253);
+            const float down = __uint_as_float(static_cast<uint32_t>(254 - ex) << 23);
+            const float up = __uint_as_float(static_cast<uint32_t>(ex) << 23) * (__ldg(a.k_scale + p.h) * a.sm_scale_log2);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                const bool on = r < a.group;
+                q[i >> 1][i & 1] = f32x2_to_f16x2(on ? __uint_as_float(w[i] << 16) * down : 0.f,
+                                                  on ? __uint_as_float(w[i] & 0xFFFF0000u) * down : 0.f);
+            }
+            f0 = __shfl_sync(0xffffffffu, up, 8 * c);
+            f1 = __shfl_sync(0xffffffffu, up, 8 * c + 4);
+        }
+        float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f, mf0 = -INFINITY, mf1 = -INFINITY;
+        float acc[8][4];
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                acc[i][k] = 0.f;
+
+        for (int i = 0; i < take; ++i, ++u) {
+            const uint32_t st = ring + stage * kUnitBytes;
+            const bool ready = wait_stage(bars + 8 * stage, parity, stop, a.err, lane);
+            if (ready)
+                pending &= ~(1u << stage);
+            Raw x[2];
+            if (ready) {
+                load_raw(st, st + 2 * kFp4Tile, r, c, x[0]);
+                load_raw(st + kFp4Tile, st + 3 * kFp4Tile, r, c, x[1]);
+            }
+            const uint32_t missing = (bad >> (2 * stage)) & 3u;
+            if (++stage == kStagesD) {
+                stage = 0;
+                parity ^= 1u;
+            }
+            if (u + kStagesD < n) {
+                fence_proxy_async_smem();
+                __syncwarp();
+                issue(u + kStagesD);
+            }
+            if (!ready)
+                continue;
+            // which of the unit's 32 tokens are visible
+            const int ti = 2 * (p.unit + i) + (lane >> 4);
+            const int t = 16 * tile_at(sg, ti) + (lane & 15);
+            const uint32_t seen =
+                __ballot_sync(0xffffffffu, ti < sg.tiles && t < sg.len && (t < sg.sinks || t >= sg.from));
+            if (seen != 0xffffffffu || missing) {
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    // a missing page reads as zeros; values of unseen tokens may be anything
+                    if (missing & (1u << j))
+                        x[j].ks[0] = x[j].ks[1] = x[j].vs[0] = x[j].vs[1] = 0u;
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        const uint32_t s = seen >> (16 * j + 8 * k);
+                        x[j].vs[k] &= ((s >> order(2 * c)) & 1u ? 0x00FFu : 0u) |
+                                      ((s >> order(2 * c + 1)) & 1u ? 0xFF00u : 0u);
+                    }
+                }
+            }
+            float y[2][4];
+            scores(x[0], q, f0, f1, y[0]);
+            scores(x[1], q, f0, f1, y[1]);
+            if (seen != 0xffffffffu) {
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        if (!((seen >> (16 * j + 8 * (k >> 1) + tok)) & 1u))
+                            y[j][k] = -INFINITY;
+            }
+            const float t0 = fmaxf(fmaxf(y[0][0], y[0][2]), fmaxf(y[1][0], y[1][2]));
+            const float t1 = fmaxf(fmaxf(y[0][1], y[0][3]), fmaxf(y[1][1], y[1][3]));
+            if (__any_sync(0xffffffffu, t0 > m0 + kMoveMax || t1 > m1 + kMoveMax)) {
+                float n0 = t0, n1 = t1;
+#pragma unroll
+                for (int o = 4; o < 32; o <<= 1) {
+                    n0 = fmaxf(n0, __shfl_xor_sync(0xffffffffu, n0, o));
+                    n1 = fmaxf(n1, __shfl_xor_sync(0xffffffffu, n1, o));
+                }
+                n0 = fmaxf(n0, m0);
+                n1 = fmaxf(n1, m1);
+                const float g0 = ex2_approx(m0 - n0), g1 = ex2_approx(m1 - n1);
+                m0 = n0;
+                m1 = n1;
+                l0 *= g0;
+                l1 *= g1;
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    acc[k][0] *= g0;
+                    acc[k][1] *= g1;
+                    acc[k][2] *= g0;
+                    acc[k][3] *= g1;
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const float p0 = ex2_approx(y[j][0] - m0), p1 = ex2_approx(y[j][1] - m1);
+                const float p2 = ex2_approx(y[j][2] - m0), p3 = ex2_approx(y[j][3] - m1);
+                const uint32_t ha = f32x2_to_f16x2(p0, p1), hb = f32x2_to_f16x2(p2, p3);
+                const float2 va = f16x2_to_f32x2(ha), vb = f16x2_to_f32x2(hb);
+                uint32_t b[kParts][2];
+                b[0][0] = transpose8x8(ha);
+                b[0][1] = transpose8x8(hb);
+                if constexpr (kParts == 2) {
+                    l0 += p0 + p2;
+                    l1 += p1 + p3;
+                    b[1][0] = transpose8x8(f32x2_to_f16x2(p0 - va.x, p1 - va.y));
+                    b[1][1] = transpose8x8(f32x2_to_f16x2(p2 - vb.x, p3 - vb.y));
+                } else {
+                    l0 += va.x + vb.x;
+                    l1 += va.y + vb.y;
+                }
+                accumulate<kParts>(x[j], b, acc);
+            }
+            if ((i + 1) % kFoldUnits == 0 || (i + 1 == take && take > kFoldUnits)) {
+                const float g0 = ex2_approx(mf0 - m0), g1 = ex2_approx(mf1 - m1);
+                const bool old = i + 1 > kFoldUnits, last = i + 1 == take;
+#pragma unroll
+                for (int k = 0; k < 32; ++k) {
+                    const float v = acc[k >> 2][k & 3] + (old ? fold[32 * k] * ((k & 1) ? g1 : g0) : 0.f);
+                    if (!last)
+                        fold[32 * k] = v;
+                    acc[k >> 2][k & 3] = last ? v : 0.f;
+                }
+                mf0 = m0;
+                mf1 = m1;
+            }
+        }
+
+        // ---- end of piece: heads 2c, 2c + 1; dims 16 r ..
+#pragma unroll
+        for (int o = 4; o < 32; o <<= 1) {
+            l0 += __shfl_xor_sync(0xffffffffu, l0, o);
+            l1 += __shfl_xor_sync(0xffffffffu, l1, o);
+        }
+        const int64_t slot = static_cast<int64_t>(worker) + p.h * a.batch + p.b;
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const int g = 2 * c + j;
+            if (g >= a.group)
+                continue;
+            float v[16];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                v[2 * k] = acc[k][j];
+                v[2 * k + 1] = acc[k][j + 2];
+            }
+            if (whole) {
+                const float f = __ldg(a.v_scale + p.h) / (j ? l1 : l0);
+#pragma unroll
+                for (int k = 0; k < 16; ++k)
+                    v[k] *= f;
+                store16(a, row0 + g, 16 * r, v);
+            } else if (slot < da.num_slots) {
+                float *s = da.partials + (slot * a.group + g) * kPartialStride;
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    reinterpret_cast<float4 *>(s + 16 * r)[k] = make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
+                if (r == 0)
+                    *reinterpret_cast<float2 *>(s + kHeadDim) = make_float2(j ? m1 : m0, j ? l1 : l0);
+            } else if (a.err && r == 0) {
+                atomicOr(a.err, PKV_DEVERR_INTERNAL);
+            }
+        }
+    }
+
+    // After an abort: no copy may land in this ring once the warp has left.
+    for (int s = 0; s < kStagesD; ++s)
+        if (pending & (1u << s)) {
+            const uint64_t t0 = global_timer_ns();
+            while (!mbar_try_wait(bars + 8 * s, (pend_par >> s) & 1u) && global_timer_ns() - t0 < kLimitNs) {
+            }
+        }
+}
+
+// Joins the states of a segment's pieces for one query head, in worker order:
+// out = v_scale sum_i 2^(m_i - M) A_i / sum_i 2^(m_i - M) l_i.  A CTA per
+// (segment, head); its warps take the pieces in turns of kJoin, all of a
+// turn's loads in flight together, and are joined in warp order.
+constexpr int kJoin = 8;
+constexpr int kJoinWarps = 8;
+
+__global__ void __launch_bounds__(32 * kJoinWarps) join_fp4_kernel(const Fp4DecodeArgs da)
+{
+    __shared__ __align__(16) float ra[kJoinWarps][kHeadDim];
+    __shared__ float2 rm[kJoinWarps];
+    const Fp4AttnArgs &a = da.a;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
+    const int sg = blockIdx.x / a.group, g = blockIdx.x % a.group;
+    const int b = sg / a.hkv, h = sg % a.hkv;
+    const float vs = __ldg(a.v_scale + h);
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int2 j = da.joins[sg];
+    if (j.x < 0)
+        return;
+    const int pieces = j.y - j.x + 1;
+    const int64_t slot0 = static_cast<int64_t>(j.x) + h * a.batch + b;
+    if (j.y < j.x || slot0 + pieces > da.num_slots)
+        return;                                            // an aborted call, or flagged by the decode kernel
+    const float *base = da.partials + (slot0 * a.group + g) * kPartialStride;
+    const int64_t stride = static_cast<int64_t>(a.group) * kPartialStride;
+    float M = -INFINITY, L = 0.f;
+    float4 A = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int i0 = warp * kJoin; i0 < pieces; i0 += warps * kJoin) {
+        float4 v[kJoin];
+        float2 ml[kJoin];
+#pragma unroll
+        for (int i = 0; i < kJoin; ++i) {
+            const bool on = i0 + i < pieces;
+            const float *s = base + (on ? i0 + i : 0) * stride;
+            ml[i] = on ? *reinterpret_cast<const float2 *>(s + kHeadDim) : make_float2(-INFINITY, 0.f);
+            v[i] = on ? *reinterpret_cast<const float4 *>(s + 4 * lane) : make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+        float mn = M;
+#pragma unroll
+        for (int i = 0; i < kJoin; ++i)
+            mn = fmaxf(mn, ml[i].x);
+        const float f = ex2_approx(M - mn);
+        M = mn;
+        L *= f;
+        A = make_float4(A.x * f, A.y * f, A.z * f, A.w * f);
+#pragma unroll
+        for (int i = 0; i < kJoin; ++i) {
+            const float e = i0 + i < pieces ? ex2_approx(ml[i].x - mn) : 0.f;
+            L += e * ml[i].y;
+            A.x += e * v[i].x;
+            A.y += e * v[i].y;
+            A.z += e * v[i].z;
+            A.w += e * v[i].w;
+        }
+    }
+    if (warps > 1) {
+        *reinterpret_cast<float4 *>(&ra[warp][4 * lane]) = A;
+        if (lane == 0)
+            rm[warp] = make_float2(M, L);
+        __syncthreads();
+        if (warp != 0)
+            return;
+        float mn = M;
+        for (int w = 1; w < warps; ++w)
+            mn = fmaxf(mn, rm[w].x);
+        L = 0.f;
+        A = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int w = 0; w < warps; ++w) {
+            if (w * kJoin >= pieces)
+                break;                                     // a warp with no pieces
+            const float e = ex2_approx(rm[w].x - mn);
+            const float4 v = *reinterpret_cast<const float4 *>(&ra[w][4 * lane]);
+            L += e * rm[w].y;
+            A.x += e * v.x;
+            A.y += e * v.y;
+            A.z += e * v.z;
+            A.w += e * v.w;
+        }
+    }
+    const float f = vs / L;
+    const int64_t at = (static_cast<int64_t>(b) * a.hq + static_cast<int64_t>(h) * a.group + g) * kHeadDim + 4 * lane;
+    if (a.out_f32) {
+        *reinterpret_cast<float4 *>(static_cast<float *>(a.out) + at) = make_float4(A.x * f, A.y * f, A.z * f, A.w * f);
+    } else {
+        const __nv_bfloat162 x = __floats2bfloat162_rn(A.x * f, A.y * f), y = __floats2bfloat162_rn(A.z * f, A.w * f);
+        *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(a.out) + at) =
+            make_uint2(*reinterpret_cast<const uint32_t *>(&x), *reinterpret_cast<const uint32_t *>(&y));
+    }
+}
+
+}  // namespace
+
+size_t decode_fp4_smem(int batch)
+{
+    return SmemD::bytes(batch);
+}
+
+const void *decode_fp4_kernel(bool two_parts)
+{
+    return two_parts ? reinterpret_cast<const void *>(&paged_gqa_decode_fp4_kernel<2>)
+                     : reinterpret_cast<const void *>(&paged_gqa_decode_fp4_kernel<1>);
+}
+
+cudaError_t launch_paged_decode_fp4(const Fp4DecodeArgs &da, int ctas, cudaStream_t stream, const char **site)
+{
+    const size_t smem = SmemD::bytes(da.a.batch);
+    *site = "4-bit decode kernel launch";
+    if (da.a.out_f32)
+        paged_gqa_decode_fp4_kernel<2><<<ctas, kThreadsD, smem, stream>>>(da);
+    else
+        paged_gqa_decode_fp4_kernel<1><<<ctas, kThreadsD, smem, stream>>>(da);
+    cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess)
+        return e;
+    *site = "4-bit join kernel launch";
+    const long long segs = static_cast<long long>(da.a.batch) * da.a.hkv;
+    const long long pieces = (static_cast<long long>(ctas) * kWarpsD + segs - 1) / segs + 1;   // a segment's, on average
+    int warps = 1;
+    while (warps < kJoinWarps && warps * kJoin < pieces)
+        warps *= 2;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(segs * da.a.group));
+    cfg.blockDim = dim3(static_cast<unsigned>(32 * warps));
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, join_fp4_kernel, da);
+}
+
+}  // namespace pkv

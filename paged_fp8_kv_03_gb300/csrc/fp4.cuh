@@ -14,6 +14,17 @@ __device__ __forceinline__ int64_t fp4_tile_offset(int64_t page, int h, int row,
     return ((page * hkv + h) * (page_size >> 4) + (row >> 4)) * kFp4Tile;
 }
 
+// Bulk copy of contiguous bytes (a multiple of 16, both ends 16-byte aligned)
+// into shared memory, completing on an mbarrier; read once, so first to leave L2.
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_t bytes, uint32_t bar)
+{
+    asm volatile(
+        "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1], %2, [%3], %4;" ::"r"(
+            dst),
+        "l"(src), "r"(bytes), "r"(bar), "l"(l2_policy_evict_first())
+        : "memory");
+}
+
 __device__ __forceinline__ float e4m3_value(uint8_t c)
 {
     const __half_raw h = __nv_cvt_fp8_to_halfraw(c, __NV_E4M3);

@@ -54,6 +54,28 @@ struct Fp4AttnArgs {
     int32_t *err;
 };
 
+// Decode: warps of a CTA (each a worker of the split) and CTAs resident on an
+// SM.
+constexpr int kFp4DecodeWarps = 4;
+constexpr int kFp4DecodeCtas = 3;
+
+struct Fp4DecodeArgs {
+    Fp4AttnArgs a;
+    int2 *joins;                                           // [batch * hkv]: workers of the segment's first and last
+                                                           // piece; x = -1: nothing to join
+    float *partials;                                       // [num_slots][group][kPartialStride]
+    long long num_slots;
+    int withhold;                                          // failure-detection test hook (-1 = off)
+};
+
+inline size_t decode_fp4_join_bytes(int batch, int hkv)
+{
+    return (static_cast<size_t>(batch) * hkv * sizeof(int2) + 255) & ~size_t(255);
+}
+
+size_t decode_fp4_smem(int batch);
+const void *decode_fp4_kernel(bool two_parts);
+cudaError_t launch_paged_decode_fp4(const Fp4DecodeArgs &da, int ctas, cudaStream_t stream, const char **site);
 cudaError_t launch_kv_append_fp4(const Fp4RowArgs &a, cudaStream_t stream);
 cudaError_t launch_kv_read_fp4(const Fp4RowArgs &a, cudaStream_t stream);
 cudaError_t launch_attend_fp4(const Fp4AttnArgs &a, cudaStream_t stream);
