@@ -61,6 +61,16 @@ pkv_status check_attn(int batch, int hq, int hkv, int head_dim, int page_size, i
     return PKV_OK;
 }
 
+// A window no sequence outgrows is none; sinks past the longest sequence say
+// nothing more (so the kernels' sums of positions stay within 32 bits).
+Fp4Window clamp_window(int window, int sinks, long long max_len)
+{
+    Fp4Window w;
+    w.window = window >= max_len ? 0 : window;
+    w.sinks = w.window == 0 ? 0 : static_cast<int>(sinks < max_len ? sinks : max_len);
+    return w;
+}
+
 // CTAs of the decode grid (the kernel with two parts a weight needs no fewer
 // registers, so its count holds for both).
 int decode_ctas(int batch, int max_ctas)
@@ -179,8 +189,7 @@ pkv_status pkv_paged_gqa_decode_fp4(const void *q, const uint8_t *k_cache, const
     a.k_cache = k_cache;
     a.v_cache = v_cache;
     a.sm_scale_log2 = sm_scale * 1.4426950408889634f;
-    a.win.window = window;
-    a.win.sinks = sinks;
+    a.win = clamp_window(window, sinks, max_len);
     a.out = out;
     a.out_f32 = out_dtype == PKV_F32;
     a.err = device_error;
@@ -219,7 +228,8 @@ size_t pkv_prefill_fp4_workspace_size(int batch, int num_kv_heads, int max_q_len
     if (batch < 0 || num_kv_heads <= 0 || max_q_len < 0 || max_kv_len < 0 || max_total_kv < 0 || window < 0 ||
         sinks < 0)
         return 0;
-    return 256;
+    return prefill_fp4_bytes(batch, prefill_fp4_rows(batch, num_kv_heads, max_q_len, max_kv_len, max_total_kv, window,
+                                                     sinks));
 }
 
 pkv_status pkv_paged_prefill_fp4(const void *q, const int32_t *cu_q, int total_q, int max_q_len,
@@ -247,40 +257,59 @@ pkv_status pkv_paged_prefill_fp4(const void *q, const int32_t *cu_q, int total_q
         !aligned(cu_q, 4) || !aligned(block_table, 4) || !aligned(seq_lens, 4) || !aligned(k_scale, 4) ||
         !aligned(v_scale, 4) || !aligned(device_error, 4) || !aligned(seq_page_sizes, 4))
         return PKV_ERR_ALIGN;
-    if (static_cast<int64_t>(total_q) * num_kv_heads >= (int64_t(1) << 31))
+    const int group = num_q_heads / num_kv_heads;
+    const int tpt = 128 / group;
+    const int64_t max_tiles = (static_cast<int64_t>(max_q_len) + tpt - 1) / tpt;
+    if (static_cast<int64_t>(batch) * num_kv_heads * max_tiles >= (int64_t(1) << 31))
         return PKV_ERR_UNSUPPORTED;
     if (max_kv_len == 0)
         return PKV_OK;                                   // no sequence can hold a query
-    if (!workspace || !aligned(workspace, 256) || workspace_bytes < 256)
+    const long long rows = prefill_fp4_rows(batch, num_kv_heads, max_q_len, max_kv_len, max_total_kv, window, sinks);
+    if (rows >= (int64_t(1) << 31))
+        return PKV_ERR_UNSUPPORTED;
+    if (!workspace || !aligned(workspace, 256) || workspace_bytes < prefill_fp4_bytes(batch, rows))
         return PKV_ERR_WORKSPACE;
-    Fp4AttnArgs a = {};
-    a.q = static_cast<const __nv_bfloat16 *>(q);
+    __half *k16 = reinterpret_cast<__half *>(static_cast<uint8_t *>(workspace) + prefill_header_bytes(batch));
+    __half *v16 = k16 + static_cast<size_t>(rows) * kHeadDim;
+    alignas(64) CUtensorMap tm_q;
+    alignas(64) CUtensorMap tm_k;
+    alignas(64) CUtensorMap tm_v;
+    if (!make_q_map(&tm_q, q, total_q, num_q_heads, group, tpt) ||
+        !make_kv16_map(&tm_k, k16, rows, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16) ||
+        !make_kv16_map(&tm_v, v16, rows, CU_TENSOR_MAP_DATA_TYPE_FLOAT16))
+        return cuda_failed(cudaErrorInvalidValue, "cuTensorMapEncodeTiled (4-bit prefill)");
+    PrefillArgs a = {};
     a.cu_q = cu_q;
     a.total_q = total_q;
     a.max_q_len = max_q_len;
+    a.tokens_per_tile = tpt;
+    a.max_tiles = static_cast<int>(max_tiles);
     a.k_scale = k_scale;
     a.v_scale = v_scale;
     a.block_table = block_table;
     a.max_pages = max_pages_per_seq;
     a.seq_lens = seq_lens;
-    a.max_len = max_kv_len;
-    a.page_sizes = seq_page_sizes;
     a.batch = batch;
     a.hq = num_q_heads;
     a.hkv = num_kv_heads;
-    a.group = num_q_heads / num_kv_heads;
+    a.group = group;
     a.page_size = page_size;
-    a.pool_log2 = 31 - __builtin_clz(static_cast<unsigned>(page_size));
     a.num_pages = num_pages;
     a.k_cache = k_cache;
     a.v_cache = v_cache;
+    a.page_sizes = seq_page_sizes;
+    a.pool_log2 = 31 - __builtin_clz(static_cast<unsigned>(page_size));
+    a.max_kv_len = max_kv_len;
+    a.tile_off = static_cast<int *>(workspace);
+    a.rows_cap = rows;
+    a.k16 = k16;
+    a.v16 = v16;
+    a.withhold_block = withheld_load();
     a.sm_scale_log2 = sm_scale * 1.4426950408889634f;
-    a.win.window = window;
-    a.win.sinks = sinks;
     a.out = out;
     a.out_f32 = out_dtype == PKV_F32;
     a.err = device_error;
-    const cudaError_t e = launch_attend_fp4(a, stream);
+    const cudaError_t e = launch_paged_prefill_fp4(a, clamp_window(window, sinks, max_kv_len), tm_q, tm_k, tm_v, stream);
     return e == cudaSuccess ? PKV_OK : cuda_failed(e, "4-bit prefill kernel launch");
 }
 

@@ -31,12 +31,10 @@ struct Fp4Window {
     int window, sinks;
 };
 
-// One query row against the cache: the fields that the shared page walk
-// (seq_page_log2, seq_token_page) reads have the same names as in DecodeArgs.
+// Decode's arguments: the fields that the shared page walk (seq_page_log2,
+// seq_token_page) reads have the same names as in DecodeArgs.
 struct Fp4AttnArgs {
     const __nv_bfloat16 *q;
-    const int32_t *cu_q;                                   // [batch + 1], or nullptr: one row per sequence (decode)
-    int total_q, max_q_len;
     const float *k_scale, *v_scale;
     const int32_t *block_table;
     int max_pages;
@@ -73,11 +71,38 @@ inline size_t decode_fp4_join_bytes(int batch, int hkv)
     return (static_cast<size_t>(batch) * hkv * sizeof(int2) + 255) & ~size_t(255);
 }
 
+// Prefill: 128-key tiles that a sequence's 16-bit copy can need, and the rows
+// and bytes of the workspace (laid out as pkv_paged_prefill's).  Under a
+// window a chunk of n queries sees the sinks and the n + window - 1 keys
+// before its end, which touch at most (n + window - 2) / 128 + 2 tiles.
+inline long long prefill_fp4_rows(int batch, int hkv, int max_q_len, int max_kv_len, long long max_total_kv,
+                                  int window, int sinks)
+{
+    long long per = (static_cast<long long>(max_kv_len) + 127) / 128;
+    if (window > 0) {
+        const long long seen = (static_cast<long long>(sinks) + 127) / 128 +
+                               (static_cast<long long>(max_q_len) + window) / 128 + 2;
+        per = seen < per ? seen : per;
+    }
+    long long tiles = per * batch;
+    if (max_total_kv > 0) {
+        const long long t2 = (max_total_kv + 127) / 128 + batch;   // sum of ceil(L_b / 128) <= sum L_b / 128 + batch
+        tiles = t2 < tiles ? t2 : tiles;
+    }
+    return tiles * 128 * hkv;
+}
+
+inline size_t prefill_fp4_bytes(int batch, long long rows)
+{
+    return prefill_header_bytes(batch) + 2 * static_cast<size_t>(rows) * kHeadDim * sizeof(__half);
+}
+
 size_t decode_fp4_smem(int batch);
 const void *decode_fp4_kernel(bool two_parts);
 cudaError_t launch_paged_decode_fp4(const Fp4DecodeArgs &da, int ctas, cudaStream_t stream, const char **site);
 cudaError_t launch_kv_append_fp4(const Fp4RowArgs &a, cudaStream_t stream);
 cudaError_t launch_kv_read_fp4(const Fp4RowArgs &a, cudaStream_t stream);
-cudaError_t launch_attend_fp4(const Fp4AttnArgs &a, cudaStream_t stream);
+cudaError_t launch_paged_prefill_fp4(const PrefillArgs &a, const Fp4Window &win, const CUtensorMap &tm_q,
+                                     const CUtensorMap &tm_k16, const CUtensorMap &tm_v16, cudaStream_t stream);
 
 }  // namespace pkv

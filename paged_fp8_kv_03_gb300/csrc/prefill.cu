@@ -55,7 +55,7 @@
 #include <mutex>
 
 #include "context.h"
-#include "internal.h"
+#include "fp4.cuh"
 #include "tcgen05.cuh"
 
 namespace pkv {
@@ -268,15 +268,37 @@ __device__ __forceinline__ bool sequence_ok(const PrefillArgs &a, int b, int q0,
     return ok;
 }
 
+// Key tiles of a sequence that some query of its chunk sees, under a window of
+// the 4-bit cache's calls: tiles 0 .. first - 1 (sinks) and then first + skip ..
+// (keys from `from` on).  Without a window: all of them (first = skip = 0).
+struct KeyTiles {
+    int from, sinks;                                     // keys t >= from or t < sinks are seen by someone
+    int first, skip;
+};
+
+template <bool kWin>
+__device__ __forceinline__ KeyTiles key_tiles(const Fp4Window &w, int first_pos)
+{
+    KeyTiles k = {0, 0, 0, 0};
+    if (kWin && w.window > 0) {
+        k.from = max(0, first_pos - w.window + 1);
+        k.sinks = min(w.sinks, k.from);
+        k.first = (k.sinks + kKeys - 1) / kKeys;
+        k.skip = max(k.from / kKeys, k.first) - k.first;
+    }
+    return k;
+}
+
 // 128-row tiles of sequence b's widened region (all its kv heads): zero for a
 // sequence with an empty or inconsistent chunk.
-__device__ __forceinline__ long long region_tiles(const PrefillArgs &a, int b)
+template <bool kWin>
+__device__ __forceinline__ long long region_tiles(const PrefillArgs &a, const Fp4Window &w, int b)
 {
     const int q0 = __ldg(a.cu_q + b), q1 = __ldg(a.cu_q + b + 1);
     const int L = __ldg(a.seq_lens + b);
     if (q1 - q0 <= 0 || !sequence_ok(a, b, q0, q1, L, false))
         return 0;
-    return static_cast<long long>(a.hkv) * ((L + kKeys - 1) / kKeys);
+    return static_cast<long long>(a.hkv) * ((L + kKeys - 1) / kKeys - key_tiles<kWin>(w, L - (q1 - q0)).skip);
 }
 
 // ---------------------------------------------------------------------- widening
@@ -288,7 +310,11 @@ __device__ __forceinline__ long long region_tiles(const PrefillArgs &a, int b)
 // row of one kv head) of K and of V reads them through the block table and
 // writes 32 bytes of 16-bit values to the region.  Rows from L up to the next
 // multiple of 128 are zeros.
-__global__ void __launch_bounds__(256) kv_widen_kernel(const PrefillArgs a)
+// (kFp4: the 4-bit cache, one thread per block of 16 codes and its scale; e s
+// has 6 significant bits, exact in bf16 and f16.  Keys no query sees under the
+// window get no rows, or zero rows within a tile that others are seen of.)
+template <bool kFp4>
+__global__ void __launch_bounds__(256) kv_widen_kernel(const PrefillArgs a, const Fp4Window win)
 {
     extern __shared__ int off[];                         // [batch + 1], then 8 warp sums
     int *warp_sum = off + a.batch + 1;
@@ -299,7 +325,7 @@ __global__ void __launch_bounds__(256) kv_widen_kernel(const PrefillArgs a)
         const int b0 = min(a.batch, tid * chunk), b1 = min(a.batch, b0 + chunk);
         long long local = 0;
         for (int b = b0; b < b1; ++b)
-            local += region_tiles(a, b);
+            local += region_tiles<kFp4>(a, win, b);
         // saturate: nothing past cap_tiles + 1 matters
         int loc = static_cast<int>(local < cap_tiles + 1 ? local : cap_tiles + 1);
         int incl = loc;
@@ -318,7 +344,7 @@ __global__ void __launch_bounds__(256) kv_widen_kernel(const PrefillArgs a)
         int run = min(base + incl - loc, static_cast<int>(cap_tiles + 1));
         for (int b = b0; b < b1; ++b) {
             off[b] = run;
-            run = static_cast<int>(min(run + region_tiles(a, b), cap_tiles + 1));
+            run = static_cast<int>(min(run + region_tiles<kFp4>(a, win, b), cap_tiles + 1));
         }
         if (tid == 255)
             off[a.batch] = min(base + incl, static_cast<int>(cap_tiles + 1));
@@ -350,22 +376,56 @@ __global__ void __launch_bounds__(256) kv_widen_kernel(const PrefillArgs a)
         if (off[b + 1] > cap_tiles)
             continue;                                           // region past the workspace: flagged above
         const int L = __ldg(a.seq_lens + b);
-        const int pad = ((L + kKeys - 1) / kKeys) * kKeys;
+        KeyTiles kt = {0, 0, 0, 0};
+        if (kFp4)
+            kt = key_tiles<kFp4>(win, L - (__ldg(a.cu_q + b + 1) - __ldg(a.cu_q + b)));
+        const int pad = ((L + kKeys - 1) / kKeys - kt.skip) * kKeys;
         const int local = static_cast<int>(R - static_cast<int64_t>(off[b]) * 128);
-        const int h = local / pad, r = local - h * pad;
-        uint4 k = make_uint4(0, 0, 0, 0), v = make_uint4(0, 0, 0, 0);
-        if (r < L) {
-            int pg, row;
-            if (seq_token_page(a, b, seq_page_log2(a, b), r, pg, row)) {
-                const int64_t src = ((static_cast<int64_t>(pg) * a.hkv + h) * a.page_size + row) * kHeadDim + 16 * e;
-                k = __ldg(reinterpret_cast<const uint4 *>(a.k_cache + src));
-                v = __ldg(reinterpret_cast<const uint4 *>(a.v_cache + src));
-            } else if (e == 0 && a.err) {
-                atomicOr(a.err, PKV_DEVERR_PAGE);
-            }
-        }
+        const int h = local / pad, vr = local - h * pad;
+        const int r = vr < kt.first * kKeys ? vr : vr + kt.skip * kKeys;   // the key
         const int64_t dst = R * kHeadDim + 16 * e;              // in 16-bit elements
+        int pg = 0, row = 0;
+        bool have = false;
+        if (r < L && (!kFp4 || r < kt.sinks || r >= kt.from)) {
+            have = seq_token_page(a, b, seq_page_log2(a, b), r, pg, row);
+            if (!have && e == 0 && a.err)
+                atomicOr(a.err, PKV_DEVERR_PAGE);
+        }
         uint4 lo4, hi4;
+        if constexpr (kFp4) {
+            uint32_t k[2][4] = {}, v[2][4] = {};
+            if (have) {
+                const int64_t tile = fp4_tile_offset(pg, h, row, a.hkv, a.page_size);
+                const int64_t codes = tile + (row & 15) * 64 + 8 * e, scale = tile + kFp4Codes + (row & 15) * 8 + e;
+                const uint2 kc = __ldg(reinterpret_cast<const uint2 *>(a.k_cache + codes));
+                const uint2 vc = __ldg(reinterpret_cast<const uint2 *>(a.v_cache + codes));
+                const __half2 ks = __float2half2_rn(e4m3_value(__ldg(a.k_cache + scale)));
+                const __half2 vs = __float2half2_rn(e4m3_value(__ldg(a.v_cache + scale)));
+                e2m1x8_to_f16x8(kc.x, k[0]);
+                e2m1x8_to_f16x8(kc.y, k[1]);
+                e2m1x8_to_f16x8(vc.x, v[0]);
+                e2m1x8_to_f16x8(vc.y, v[1]);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const __half2 kp = __hmul2(*reinterpret_cast<const __half2 *>(&k[i >> 2][i & 3]), ks);
+                    const __half2 vp = __hmul2(*reinterpret_cast<const __half2 *>(&v[i >> 2][i & 3]), vs);
+                    k[i >> 2][i & 3] = f16x2_to_bf16x2(*reinterpret_cast<const uint32_t *>(&kp));
+                    v[i >> 2][i & 3] = *reinterpret_cast<const uint32_t *>(&vp);
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                reinterpret_cast<uint4 *>(a.k16 + dst)[i] = make_uint4(k[i][0], k[i][1], k[i][2], k[i][3]);
+                reinterpret_cast<uint4 *>(a.v16 + dst)[i] = make_uint4(v[i][0], v[i][1], v[i][2], v[i][3]);
+            }
+            continue;
+        }
+        uint4 k = make_uint4(0, 0, 0, 0), v = make_uint4(0, 0, 0, 0);
+        if (have) {
+            const int64_t src = ((static_cast<int64_t>(pg) * a.hkv + h) * a.page_size + row) * kHeadDim + 16 * e;
+            k = __ldg(reinterpret_cast<const uint4 *>(a.k_cache + src));
+            v = __ldg(reinterpret_cast<const uint4 *>(a.v_cache + src));
+        }
         e4m3x4_to_f16x4(k.x, lo4.x, lo4.y);
         e4m3x4_to_f16x4(k.y, lo4.z, lo4.w);
         e4m3x4_to_f16x4(k.z, hi4.x, hi4.y);
@@ -384,9 +444,16 @@ __global__ void __launch_bounds__(256) kv_widen_kernel(const PrefillArgs a)
 }
 
 // ---------------------------------------------------------------------- attention
+// kParts: f16 parts of P.  Two for the FP8 cache and for fp32 outputs; one, and
+// half the PV products, for bf16 outputs over the 4-bit cache: P loses its low
+// 13 mantissa bits, and so does the sum that normalises it, which leaves at
+// most 2^-11 of the largest |v - o| against a bf16 output's 2^-8.
+// kWin: the calls with a window; a row may then see nothing of a tile, or of
+// all tiles so far (its running maximum is -inf until it does).
+template <int kParts, bool kWin>
 __global__ void __launch_bounds__(kPThreads, 1)
     paged_prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
-                         const __grid_constant__ CUtensorMap tm_v, const PrefillArgs a)
+                         const __grid_constant__ CUtensorMap tm_v, const PrefillArgs a, const Fp4Window win)
 {
     // ---------------------------------------------------------------- the tile
     // (sequence, kv head)-major order, heaviest query tiles (largest positions)
@@ -406,7 +473,8 @@ __global__ void __launch_bounds__(kPThreads, 1)
     // this sequence's widened region (laid out by the widening kernel); a
     // region past the workspace was flagged there and is not attended
     const int off0 = __ldg(a.tile_off + b), off1 = __ldg(a.tile_off + b + 1);
-    if (off1 > a.rows_cap / 128 || off1 - off0 != a.hkv * ((L + kKeys - 1) / kKeys))
+    const KeyTiles seq_kt = key_tiles<kWin>(win, L - n);
+    if (off1 > a.rows_cap / 128 || off1 - off0 != a.hkv * ((L + kKeys - 1) / kKeys - seq_kt.skip))
         return;
     const int row0 = off0 * 128 + h * (off1 - off0) / a.hkv * 128;   // first row of this kv head's copy
     const int t0 = qt * tpt;                             // first token of the tile in the chunk
@@ -415,7 +483,14 @@ __global__ void __launch_bounds__(kPThreads, 1)
     const int nv = min(tpt, n - t0);                     // tokens of the tile
     const int pos0 = L - n + t0;                         // position of its first token
     const int last = pos0 + nv - 1;                      // largest position in the tile
-    const int nt = last / kKeys + 1;                     // key tiles to visit
+    const KeyTiles kt = key_tiles<kWin>(win, pos0);      // what some row of this tile sees
+    const int nt = last / kKeys + 1 - kt.skip;           // key tiles to visit
+    // the i-th one, and where it lies in the sequence's copy
+    auto key_tile = [&](int i) { return !kWin || i < kt.first ? i : i + kt.skip; };
+    auto copy_tile = [&](int i) {
+        const int t = key_tile(i);
+        return !kWin || t < seq_kt.first ? t : t - seq_kt.skip;
+    };
 
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -483,9 +558,9 @@ __global__ void __launch_bounds__(kPThreads, 1)
                 if (t > 0 || static_cast<int>(blockIdx.x) != a.withhold_block) {
                     mbar_arrive_expect_tx(bar(PS::K_FULL + ks), PS::kTile);
                     karmed[ks] = static_cast<uint32_t>(t / kKStages) + 1;
-                    tma_load_3d_plain(sb + PS::kK16 + ks * PS::kTile, &tm_k, 0, row0 + t * kKeys, z,
+                    tma_load_3d_plain(sb + PS::kK16 + ks * PS::kTile, &tm_k, 0, row0 + copy_tile(t) * kKeys, z,
                                       bar(PS::K_FULL + ks));
-                    tma_load_3d_plain(sb + PS::kK16 + ks * PS::kTile + 16384, &tm_k, 64, row0 + t * kKeys, z,
+                    tma_load_3d_plain(sb + PS::kK16 + ks * PS::kTile + 16384, &tm_k, 64, row0 + copy_tile(t) * kKeys, z,
                                       bar(PS::K_FULL + ks));
                 }
                 if (t >= kVStages &&
@@ -495,9 +570,9 @@ __global__ void __launch_bounds__(kPThreads, 1)
                 }
                 mbar_arrive_expect_tx(bar(PS::V_FULL + vs), PS::kTile);
                 varmed[vs] = static_cast<uint32_t>(t / kVStages) + 1;
-                tma_load_3d_plain(sb + PS::kV16 + vs * PS::kTile, &tm_v, 0, row0 + t * kKeys, z,
+                tma_load_3d_plain(sb + PS::kV16 + vs * PS::kTile, &tm_v, 0, row0 + copy_tile(t) * kKeys, z,
                                   bar(PS::V_FULL + vs));
-                tma_load_3d_plain(sb + PS::kV16 + vs * PS::kTile + 16384, &tm_v, 64, row0 + t * kKeys, z,
+                tma_load_3d_plain(sb + PS::kV16 + vs * PS::kTile + 16384, &tm_v, 64, row0 + copy_tile(t) * kKeys, z,
                                   bar(PS::V_FULL + vs));
             }
             // No copy may still be landing when the CTA leaves.
@@ -564,7 +639,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
                         tc::mma_ts(o_tm, p_tm + 32 * (s >> 1) + 8 * (s & 1), vmn_step(vd, s), id_pv,
                                    s > 0 ? 1u : acc0);
 #pragma unroll
-                    for (int s = 0; s < 8; ++s)
+                    for (int s = 0; s < (kParts == 2 ? 8 : 0); ++s)
                         tc::mma_ts(o_tm, p_tm + 32 * (s >> 1) + 8 * (s & 1) + 16, vmn_step(vd, s), id_pv, 1u);
                     tc::commit(bar_ptr + PS::PV_DONE);
                     tc::commit(bar_ptr + PS::V_EMPTY + vs);
@@ -625,7 +700,8 @@ __global__ void __launch_bounds__(kPThreads, 1)
             // pass 1 on the raw scores (sl2 > 0): the maximum of the visible scaled
             // logits of this half is sl2 x the maximum raw score.  Hidden keys
             // become -inf, so pass 2 needs no mask.
-            const int vis = p_row - j * kKeys - 64 * half;
+            const int key0 = key_tile(j) * kKeys + 64 * half;
+            const int vis = p_row - key0;
             float mx[8];
 #pragma unroll
             for (int k = 0; k < 8; ++k)
@@ -637,6 +713,18 @@ __global__ void __launch_bounds__(kPThreads, 1)
                     for (int k = 0; k < 32; ++k)
                         if (32 * c + k > vis)
                             x[c][k] = __float_as_uint(-INFINITY);
+            }
+            if (kWin && win.window > 0) {
+                // keys before the window and behind the sinks
+                const int out = vis - win.window, snk = win.sinks - key0;
+                if (out >= 0 && snk < 64) {
+#pragma unroll
+                    for (int c = 0; c < 2; ++c)
+#pragma unroll
+                        for (int k = 0; k < 32; ++k)
+                            if (32 * c + k <= out && 32 * c + k >= snk)
+                                x[c][k] = __float_as_uint(-INFINITY);
+                }
             }
 #pragma unroll
             for (int c = 0; c < 2; ++c)
@@ -651,6 +739,8 @@ __global__ void __launch_bounds__(kPThreads, 1)
             // Pairs of elements go through the paired fp32 add / fma (fewer
             // instructions on the softmax warps' issue slots; same roundings).
             auto emit = [&](float mm) -> float {
+                if (kWin && mm == -INFINITY)
+                    mm = 0.f;                              // nothing seen yet: every P is 2^-inf
                 uint64_t ls[4];                            // ls[i] = sums of elements 2i, 2i+1 (mod 8)
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
@@ -665,16 +755,22 @@ __global__ void __launch_bounds__(kPThreads, 1)
                             f2_fma(f2_pack(__uint_as_float(x[c][2 * q]), __uint_as_float(x[c][2 * q + 1])), sl2x2, nmm));
                         const float p0 = ex2_approx(y.x), p1 = ex2_approx(y.y);
                         const uint64_t pp = f2_pack(p0, p1);
-                        ls[q & 3] = f2_add(ls[q & 3], pp);
+                        if (kParts == 2)
+                            ls[q & 3] = f2_add(ls[q & 3], pp);
                         // hi = P with its low 13 mantissa bits cleared, lo = the rest (split_pair)
                         const float h0 = __uint_as_float(__float_as_uint(p0) & 0xFFFFE000u);
                         const float h1 = __uint_as_float(__float_as_uint(p1) & 0xFFFFE000u);
                         ph[q] = f32x2_to_f16x2(h0, h1);
-                        const float2 r = f2_unpack(f2_sub(pp, f2_pack(h0, h1)));
-                        pl[q] = f32x2_to_f16x2(r.x, r.y);
+                        if (kParts == 2) {
+                            const float2 r = f2_unpack(f2_sub(pp, f2_pack(h0, h1)));
+                            pl[q] = f32x2_to_f16x2(r.x, r.y);
+                        } else {
+                            ls[q & 3] = f2_add(ls[q & 3], f2_pack(h0, h1));
+                        }
                     }
                     tc::st16(s_tm + 32 * c, ph);
-                    tc::st16(s_tm + 32 * c + 16, pl);
+                    if (kParts == 2)
+                        tc::st16(s_tm + 32 * c + 16, pl);
                 }
                 const float2 s0 = f2_unpack(ls[0]), s1 = f2_unpack(ls[1]), s2 = f2_unpack(ls[2]), s3 = f2_unpack(ls[3]);
                 return ((s0.x + s0.y) + (s1.x + s1.y)) + ((s2.x + s2.y) + (s3.x + s3.y));
@@ -696,7 +792,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
             const float mloc = fmaxf(mh, red_max[(fb * 2 + (half ^ 1)) * kRows + row]);
             bool redo = !spec;
             if (j == 0) {
-                m = mloc;                                  // key 0 is visible to every row
+                m = mloc;                                  // key 0 is visible to every row (unless kWin)
             } else {
                 // Every kFold tiles the segment accumulator (O_seg, TMEM columns
                 // kColO..) is added into O (kColM..) in fp32 and PV_j starts a new
@@ -715,7 +811,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
                     }
                     tc::fence_after();
                     const float mn = need ? mloc : m;
-                    const float f = rescale ? ex2_approx(m - mn) : 1.f;
+                    const float f = rescale && (!kWin || need) ? ex2_approx(m - mn) : 1.f;
 #pragma unroll 1
                     for (int c = 0; c < 4; ++c) {
                         const uint32_t cs = lanes + kColO + 64 * half + 16 * c;
@@ -815,7 +911,60 @@ __global__ void __launch_bounds__(kPThreads, 1)
 }
 
 std::mutex g_prefill_mu;
-unsigned long long g_prefill_attr_ctx[64] = {0};   // per device: the context the kernel's limit was raised in
+unsigned long long g_prefill_attr_ctx[64][5] = {};   // per device and kernel: the context its limit was raised in
+
+typedef void (*PrefillKernel)(const CUtensorMap, const CUtensorMap, const CUtensorMap, const PrefillArgs,
+                              const Fp4Window);
+
+cudaError_t raise_limit(PrefillKernel kernel, int which)
+{
+    int dev = -1;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess)
+        return e;
+    if (dev < 0 || dev >= 64)
+        return cudaErrorInvalidDevice;
+    unsigned long long ctx = 0;
+    const bool known = current_context_id(&ctx);
+    std::lock_guard<std::mutex> lk(g_prefill_mu);
+    if (!known || g_prefill_attr_ctx[dev][which] != ctx) {
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(PS::bytes()));
+        if (e != cudaSuccess)
+            return e;
+        g_prefill_attr_ctx[dev][which] = known ? ctx : 0;
+    }
+    return cudaSuccess;
+}
+
+template <bool kFp4>
+cudaError_t launch_prefill(PrefillKernel kernel, int which, const PrefillArgs &a, const Fp4Window &win,
+                           const CUtensorMap &tm_q, const CUtensorMap &tm_k16, const CUtensorMap &tm_v16,
+                           cudaStream_t stream)
+{
+    const int64_t grid = static_cast<int64_t>(a.batch) * a.hkv * a.max_tiles;
+    if (grid <= 0)
+        return cudaSuccess;
+    cudaError_t e = raise_limit(kernel, which);
+    if (e != cudaSuccess)
+        return e;
+    const int64_t pieces = a.rows_cap * 8;
+    int64_t wblocks = (pieces + 255) / 256;
+    const int64_t cap = static_cast<int64_t>(device_sm_count()) * 16;
+    if (wblocks > cap)
+        wblocks = cap;
+    if (wblocks < 1)
+        wblocks = 1;                                     // CTA 0 always lays out the regions
+    const size_t wsmem = (static_cast<size_t>(a.batch) + 1 + 8) * sizeof(int);
+    if (wsmem > 48 * 1024) {
+        e = cudaFuncSetAttribute(kv_widen_kernel<kFp4>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 static_cast<int>(wsmem));
+        if (e != cudaSuccess)
+            return e;
+    }
+    kv_widen_kernel<kFp4><<<static_cast<unsigned>(wblocks), 256, wsmem, stream>>>(a, win);
+    kernel<<<static_cast<unsigned>(grid), kPThreads, PS::bytes(), stream>>>(tm_q, tm_k16, tm_v16, a, win);
+    return cudaGetLastError();
+}
 
 }  // namespace
 
@@ -827,44 +976,17 @@ size_t prefill_smem_bytes()
 cudaError_t launch_paged_prefill(const PrefillArgs &a, const CUtensorMap &tm_q, const CUtensorMap &tm_k16,
                                  const CUtensorMap &tm_v16, cudaStream_t stream)
 {
-    const int64_t grid = static_cast<int64_t>(a.batch) * a.hkv * a.max_tiles;
-    if (grid <= 0)
-        return cudaSuccess;
-    int dev = -1;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess)
-        return e;
-    if (dev < 0 || dev >= 64)
-        return cudaErrorInvalidDevice;
-    {
-        unsigned long long ctx = 0;
-        const bool known = current_context_id(&ctx);
-        std::lock_guard<std::mutex> lk(g_prefill_mu);
-        if (!known || g_prefill_attr_ctx[dev] != ctx) {
-            e = cudaFuncSetAttribute(paged_prefill_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                     static_cast<int>(PS::bytes()));
-            if (e != cudaSuccess)
-                return e;
-            g_prefill_attr_ctx[dev] = known ? ctx : 0;
-        }
-    }
-    const int64_t pieces = a.rows_cap * 8;
-    int64_t wblocks = (pieces + 255) / 256;
-    const int64_t cap = static_cast<int64_t>(device_sm_count()) * 16;
-    if (wblocks > cap)
-        wblocks = cap;
-    if (wblocks < 1)
-        wblocks = 1;                                     // CTA 0 always lays out the regions
-    const size_t wsmem = (static_cast<size_t>(a.batch) + 1 + 8) * sizeof(int);
-    if (wsmem > 48 * 1024) {
-        e = cudaFuncSetAttribute(kv_widen_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 static_cast<int>(wsmem));
-        if (e != cudaSuccess)
-            return e;
-    }
-    kv_widen_kernel<<<static_cast<unsigned>(wblocks), 256, wsmem, stream>>>(a);
-    paged_prefill_kernel<<<static_cast<unsigned>(grid), kPThreads, PS::bytes(), stream>>>(tm_q, tm_k16, tm_v16, a);
-    return cudaGetLastError();
+    return launch_prefill<false>(paged_prefill_kernel<2, false>, 0, a, Fp4Window{0, 0}, tm_q, tm_k16, tm_v16, stream);
+}
+
+cudaError_t launch_paged_prefill_fp4(const PrefillArgs &a, const Fp4Window &win, const CUtensorMap &tm_q,
+                                     const CUtensorMap &tm_k16, const CUtensorMap &tm_v16, cudaStream_t stream)
+{
+    if (win.window > 0)
+        return a.out_f32 ? launch_prefill<true>(paged_prefill_kernel<2, true>, 1, a, win, tm_q, tm_k16, tm_v16, stream)
+                         : launch_prefill<true>(paged_prefill_kernel<1, true>, 2, a, win, tm_q, tm_k16, tm_v16, stream);
+    return a.out_f32 ? launch_prefill<true>(paged_prefill_kernel<2, false>, 3, a, win, tm_q, tm_k16, tm_v16, stream)
+                     : launch_prefill<true>(paged_prefill_kernel<1, false>, 4, a, win, tm_q, tm_k16, tm_v16, stream);
 }
 
 }  // namespace pkv
