@@ -52,12 +52,12 @@ constexpr int kUnitBytes = 4 * kFp4Tile;                   // K tile 0, K tile 1
 constexpr float kMoveMax = 8.f;                            // log2 units
 // Units after which a piece's accumulator is added into an fp32 copy: the
 // tensor cores add with truncation, whose error grows with the chain.
-constexpr int kFoldUnits = 64;
+template <int kParts>
+constexpr int kFoldUnits = 128 / kParts;
 constexpr uint64_t kLimitNs = 2000000000ull;
 
 struct SmemD {                                             // the ring, [warps][stages][kUnitBytes], comes first
-    static constexpr int kFold = kWarpsD * kStagesD * kUnitBytes;           // [warps][32 values][32 lanes]
-    static constexpr int kBar = kFold + kWarpsD * 32 * 32 * 4;
+    static constexpr int kBar = kWarpsD * kStagesD * kUnitBytes;
     static constexpr int kFlag = kBar + kWarpsD * kStagesD * 8;
     static constexpr int kSums = kFlag + 16;
     static constexpr int kStart = kSums + 16 * ((kWarpsD * 4 + 15) / 16);   // int [batch + 1]
@@ -192,35 +192,91 @@ __device__ __forceinline__ int order(int n)
     return n ^ ((n >> 1) & 1);
 }
 
-// One tile's raw bytes of a lane.
-struct Raw {
-    uint32_t k[2][4];     // codes of K rows order(r), order(r) + 8: dims 32c ..
-    uint32_t ks[2];       // their two block scales
-    uint32_t v[4][2];     // codes of block r of V rows order(2c), order(2c + 1), and both + 8
-    uint32_t vs[2];       // scale bytes of the first pair, of the second pair
+// Two fp32 values in one 64-bit register pair; each half rounds like the
+// scalar operation.
+__device__ __forceinline__ uint64_t pack2(float a, float b)
+{
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ float2 unpack2(uint64_t r)
+{
+    float2 v;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(v.x), "=f"(v.y) : "l"(r));
+    return v;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b)
+{
+    uint64_t d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c)
+{
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+__device__ __forceinline__ float max3(float a, float b, float c)
+{
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+
+// Where a lane (r, c) reads within a tile.
+struct LaneOffsets {
+    uint32_t k, ks;          // K row order(r): its 16 bytes, its two scales (row + 8: 512, 64 further)
+    uint32_t v0, v1, s0, s1; // V rows order(2c), order(2c + 1): block r's 8 bytes, its scale
 };
 
-__device__ __forceinline__ void load_raw(uint32_t kt, uint32_t vt, int r, int c, Raw &x)
+__device__ __forceinline__ LaneOffsets lane_offsets(int r, int c)
 {
-    const int k0 = order(r), v0 = order(2 * c), v1 = order(2 * c + 1);
+    LaneOffsets o;
+    o.k = order(r) * 64 + 16 * c;
+    o.ks = kFp4Codes + order(r) * 8 + 2 * c;
+    o.v0 = order(2 * c) * 64 + 8 * r;
+    o.v1 = order(2 * c + 1) * 64 + 8 * r;
+    o.s0 = kFp4Codes + order(2 * c) * 8 + r;
+    o.s1 = kFp4Codes + order(2 * c + 1) * 8 + r;
+    return o;
+}
+
+struct RawK {
+    uint32_t k[2][4], s[2];   // rows order(r), order(r) + 8
+};
+struct RawV {
+    uint32_t v[4][2], s[2];   // rows order(2c), order(2c + 1), and both + 8; scale bytes of each pair
+};
+
+__device__ __forceinline__ void load_k(uint32_t kt, const LaneOffsets &o, RawK &x)
+{
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
-        lds128(kt + (k0 + 8 * j) * 64 + 16 * c, x.k[j]);
-        x.ks[j] = lds16(kt + kFp4Codes + (k0 + 8 * j) * 8 + 2 * c);
-        lds64(vt + (v0 + 8 * j) * 64 + 8 * r, x.v[2 * j]);
-        lds64(vt + (v1 + 8 * j) * 64 + 8 * r, x.v[2 * j + 1]);
-        x.vs[j] = lds8(vt + kFp4Codes + (v0 + 8 * j) * 8 + r) | (lds8(vt + kFp4Codes + (v1 + 8 * j) * 8 + r) << 8);
+        lds128(kt + o.k + 512 * j, x.k[j]);
+        x.s[j] = lds16(kt + o.ks + 64 * j);
     }
 }
 
-// Scores of a tile: lane (r, c) gets tokens order(r) (y[0], y[1]) and
-// order(r) + 8 (y[2], y[3]) of heads 2c, 2c + 1, times f0, f1.
-__device__ __forceinline__ void scores(const Raw &x, const uint32_t (&q)[8][2], float f0, float f1, float (&y)[4])
+__device__ __forceinline__ void load_v(uint32_t vt, const LaneOffsets &o, RawV &x)
+{
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+        lds64(vt + o.v0 + 512 * j, x.v[2 * j]);
+        lds64(vt + o.v1 + 512 * j, x.v[2 * j + 1]);
+        x.s[j] = lds8(vt + o.s0 + 64 * j) | (lds8(vt + o.s1 + 64 * j) << 8);
+    }
+}
+
+// Unscaled scores of a tile: lane (r, c) gets tokens order(r) (y[0]) and
+// order(r) + 8 (y[1]), each for heads 2c, 2c + 1.
+__device__ __forceinline__ void scores(const RawK &x, const uint32_t (&q)[8][2], uint64_t (&y)[2])
 {
     uint32_t s[2][2];
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
-        const uint32_t p = e4m3x2_to_f16x2(x.ks[j]);
+        const uint32_t p = e4m3x2_to_f16x2(x.s[j]);
         s[j][0] = __byte_perm(p, p, 0x1010);
         s[j][1] = __byte_perm(p, p, 0x3232);
     }
@@ -238,19 +294,21 @@ __device__ __forceinline__ void scores(const Raw &x, const uint32_t (&q)[8][2], 
         mma_16816(d[0], a[0][0], a[1][0], a[0][1], a[1][1], q[2 * w][0], q[2 * w][1]);
         mma_16816(d[1], a[0][2], a[1][2], a[0][3], a[1][3], q[2 * w + 1][0], q[2 * w + 1][1]);
     }
-    y[0] = (d[0][0] + d[1][0]) * f0;
-    y[1] = (d[0][1] + d[1][1]) * f1;
-    y[2] = (d[0][2] + d[1][2]) * f0;
-    y[3] = (d[0][3] + d[1][3]) * f1;
+    y[0] = add2(pack2(d[0][0], d[0][1]), pack2(d[1][0], d[1][1]));
+    y[1] = add2(pack2(d[0][2], d[0][3]), pack2(d[1][2], d[1][3]));
 }
 
-// acc += V^T P^T for a tile; b: the weights of its 16 tokens (B fragment) in
-// kParts f16 parts.
+// acc += V^T P^T and sum += 1^T P^T for a tile; b: the weights of its 16 tokens
+// (B fragment) in kParts f16 parts.
 template <int kParts>
-__device__ __forceinline__ void accumulate(const Raw &x, const uint32_t (&b)[kParts][2], float (&acc)[8][4])
+__device__ __forceinline__ void accumulate(const RawV &x, const uint32_t (&b)[kParts][2], float (&acc)[8][4],
+                                           float (&sum)[4])
 {
-    const uint32_t s0 = e4m3x2_to_f16x2(x.vs[0]), s1 = e4m3x2_to_f16x2(x.vs[1]);
-    constexpr uint32_t kLow = 0x0F0F0F0Fu;
+    const uint32_t s0 = e4m3x2_to_f16x2(x.s[0]), s1 = e4m3x2_to_f16x2(x.s[1]);
+    constexpr uint32_t kLow = 0x0F0F0F0Fu, kOnes = 0x3C003C00u;
+#pragma unroll
+    for (int part = 0; part < kParts; ++part)
+        mma_16816(sum, kOnes, kOnes, kOnes, kOnes, b[part][0], b[part][1]);
 #pragma unroll
     for (int w = 0; w < 2; ++w) {
         uint32_t e[2][4], o[2][4];                         // even, odd dims of the block; pair 0, pair 1
@@ -378,7 +436,6 @@ __global__ void __launch_bounds__(kThreadsD, kFp4DecodeCtas) paged_gqa_decode_fp
 
     const uint32_t ring = smem_addr(smem) + warp * kStagesD * kUnitBytes;
     const uint32_t bars = smem_addr(smem + SmemD::kBar) + warp * kStagesD * 8;
-    float *fold = reinterpret_cast<float *>(smem + SmemD::kFold) + warp * 1024 + lane;
 
     // ---- tile addresses, 16 units ahead: lane 2i + j has tile j of unit i.
     // -1: a page outside the pool; -2: no such tile.
@@ -400,19 +457,17 @@ __global__ void __launch_bounds__(kThreadsD, kFp4DecodeCtas) paged_gqa_decode_fp
         return (phys * a.hkv + p.h) * (a.page_size >> 4) + (row >> 4);
     };
     int now = look_up(0), next = look_up(16), base = 0;
-    uint32_t bad = 0, pending = 0, pend_par = 0;           // per stage: missing tiles (2 bits), copies in flight
-    auto issue = [&](int u) {
+    uint32_t bad = 0;                                      // missing tiles, 2 bits a stage
+    auto issue = [&](int u, int s) {                       // unit u into stage s = u % kStagesD
         if (u >= base + 16) {
             base += 16;
             now = next;
             next = look_up(base + 16);
         }
-        const int s = u % kStagesD;
         const int t = __shfl_sync(0xffffffffu, now, 2 * (u - base) + (lane & 1));
         const uint32_t have = __ballot_sync(0xffffffffu, t >= 0) & 3u;
         bad = (bad & ~(3u << (2 * s))) | ((~have & 3u) << (2 * s));
-        const bool go = __shfl_sync(0xffffffffu, !*stop && !(worker == da.withhold && u == 0), 0);
-        if (go) {
+        if (worker != da.withhold || u != 0) {
             if (lane == 0)
                 mbar_arrive_expect_tx(bars + 8 * s, 2 * kFp4Tile * __popc(have));
             __syncwarp();
@@ -420,17 +475,16 @@ __global__ void __launch_bounds__(kThreadsD, kFp4DecodeCtas) paged_gqa_decode_fp
                 bulk_load(ring + s * kUnitBytes + lane * kFp4Tile,
                           (lane < 2 ? a.k_cache : a.v_cache) + static_cast<int64_t>(t) * kFp4Tile, kFp4Tile,
                           bars + 8 * s);
-            pending |= 1u << s;
-            pend_par = (pend_par & ~(1u << s)) | ((static_cast<uint32_t>(u / kStagesD) & 1u) << s);
         }
     };
-    for (int u = 0; u < kStagesD && u < n; ++u)
-        issue(u);
+    for (int v = 0; v < kStagesD && v < n; ++v)
+        issue(v, v);
 
     const int r = lane >> 2, c = lane & 3;
-    const int tok = order(r);
+    const LaneOffsets lo_off = lane_offsets(r, c);
     int stage = 0;
     uint32_t parity = 0;
+    bool dead = false;                                     // a wait ran out
     int u = 0;
     while (u < n) {
         const Place p = place_of(start, a.batch, lo + u);
@@ -475,82 +529,88 @@ __global__ void __launch_bounds__(kThreadsD, kFp4DecodeCtas) paged_gqa_decode_fp
             f0 = __shfl_sync(0xffffffffu, up, 8 * c);
             f1 = __shfl_sync(0xffffffffu, up, 8 * c + 4);
         }
-        float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f, mf0 = -INFINITY, mf1 = -INFINITY;
-        float acc[8][4];
+        const uint64_t f = pack2(f0, f1);
+        const int64_t slot = static_cast<int64_t>(worker) + p.h * a.batch + p.b;
+        // units of which every token is visible: past the sinks and the window's
+        // first tile, before the last tokens
+        const int full_lo = (sg.from > 0 ? sg.first + 2 : 1) >> 1;
+        const int full_hi = ((sg.len >> 4) - sg.skip) >> 1;
+        float m0 = -INFINITY, m1 = -INFINITY, mf0 = -INFINITY, mf1 = -INFINITY;
+        float l0 = 0.f, l1 = 0.f;                          // sums of the units folded so far
+        float acc[8][4], sum[4];
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
+        for (int k = 0; k < 4; ++k) {
+            sum[k] = 0.f;
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
+            for (int i = 0; i < 8; ++i)
                 acc[i][k] = 0.f;
+        }
 
         for (int i = 0; i < take; ++i, ++u) {
             const uint32_t st = ring + stage * kUnitBytes;
-            const bool ready = wait_stage(bars + 8 * stage, parity, stop, a.err, lane);
-            if (ready)
-                pending &= ~(1u << stage);
-            Raw x[2];
-            if (ready) {
-                load_raw(st, st + 2 * kFp4Tile, r, c, x[0]);
-                load_raw(st + kFp4Tile, st + 3 * kFp4Tile, r, c, x[1]);
+            if (!wait_stage(bars + 8 * stage, parity, stop, a.err, lane)) {
+                dead = true;
+                break;
             }
             const uint32_t missing = (bad >> (2 * stage)) & 3u;
-            if (++stage == kStagesD) {
-                stage = 0;
-                parity ^= 1u;
-            }
-            if (u + kStagesD < n) {
-                fence_proxy_async_smem();
-                __syncwarp();
-                issue(u + kStagesD);
-            }
-            if (!ready)
-                continue;
-            // which of the unit's 32 tokens are visible
-            const int ti = 2 * (p.unit + i) + (lane >> 4);
-            const int t = 16 * tile_at(sg, ti) + (lane & 15);
-            const uint32_t seen =
-                __ballot_sync(0xffffffffu, ti < sg.tiles && t < sg.len && (t < sg.sinks || t >= sg.from));
-            if (seen != 0xffffffffu || missing) {
+            uint64_t y[2][2];
+            {
+                RawK x[2];
+                load_k(st, lo_off, x[0]);
+                load_k(st + kFp4Tile, lo_off, x[1]);
+                if (missing) {                             // a missing page reads as zeros
 #pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    // a missing page reads as zeros; values of unseen tokens may be anything
-                    if (missing & (1u << j))
-                        x[j].ks[0] = x[j].ks[1] = x[j].vs[0] = x[j].vs[1] = 0u;
-#pragma unroll
-                    for (int k = 0; k < 2; ++k) {
-                        const uint32_t s = seen >> (16 * j + 8 * k);
-                        x[j].vs[k] &= ((s >> order(2 * c)) & 1u ? 0x00FFu : 0u) |
-                                      ((s >> order(2 * c + 1)) & 1u ? 0xFF00u : 0u);
-                    }
+                    for (int j = 0; j < 2; ++j)
+                        if (missing & (1u << j))
+                            x[j].s[0] = x[j].s[1] = 0u;
                 }
+                scores(x[0], q, y[0]);
+                scores(x[1], q, y[1]);
             }
-            float y[2][4];
-            scores(x[0], q, f0, f1, y[0]);
-            scores(x[1], q, f0, f1, y[1]);
-            if (seen != 0xffffffffu) {
+            const int unit = p.unit + i;
+            uint32_t seen = 0xffffffffu;                   // the visible ones of the unit's 32 tokens
+            float2 z[2][2];
+            const uint64_t nm = pack2(-m0, -m1);
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+#pragma unroll
+                for (int k = 0; k < 2; ++k)
+                    z[j][k] = unpack2(fma2(y[j][k], f, nm));
+            const bool edge = unit < full_lo || unit >= full_hi;
+            const float top = fmaxf(max3(fmaxf(z[0][0].x, z[0][0].y), z[0][1].x, z[0][1].y),
+                                    max3(fmaxf(z[1][0].x, z[1][0].y), z[1][1].x, z[1][1].y));
+            if (edge || __any_sync(0xffffffffu, !(top <= kMoveMax))) {
+                // an edge of the sequence or of its window, or the maximum moves
+                if (edge) {
+                    const int ti = 2 * unit + (lane >> 4);
+                    const int t = 16 * tile_at(sg, ti) + (lane & 15);
+                    seen = __ballot_sync(0xffffffffu,
+                                         ti < sg.tiles && t < sg.len && (t < sg.sinks || t >= sg.from));
+                }
+                float t0 = -INFINITY, t1 = -INFINITY;
+                float2 w[2][2];
 #pragma unroll
                 for (int j = 0; j < 2; ++j)
 #pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        if (!((seen >> (16 * j + 8 * (k >> 1) + tok)) & 1u))
-                            y[j][k] = -INFINITY;
-            }
-            const float t0 = fmaxf(fmaxf(y[0][0], y[0][2]), fmaxf(y[1][0], y[1][2]));
-            const float t1 = fmaxf(fmaxf(y[0][1], y[0][3]), fmaxf(y[1][1], y[1][3]));
-            if (__any_sync(0xffffffffu, t0 > m0 + kMoveMax || t1 > m1 + kMoveMax)) {
-                float n0 = t0, n1 = t1;
+                    for (int k = 0; k < 2; ++k) {
+                        w[j][k] = unpack2(y[j][k]);
+                        const bool on = (seen >> (16 * j + 8 * k + order(r))) & 1u;
+                        w[j][k].x = on ? w[j][k].x * f0 : -INFINITY;
+                        w[j][k].y = on ? w[j][k].y * f1 : -INFINITY;
+                        t0 = fmaxf(t0, w[j][k].x);
+                        t1 = fmaxf(t1, w[j][k].y);
+                    }
 #pragma unroll
                 for (int o = 4; o < 32; o <<= 1) {
-                    n0 = fmaxf(n0, __shfl_xor_sync(0xffffffffu, n0, o));
-                    n1 = fmaxf(n1, __shfl_xor_sync(0xffffffffu, n1, o));
+                    t0 = fmaxf(t0, __shfl_xor_sync(0xffffffffu, t0, o));
+                    t1 = fmaxf(t1, __shfl_xor_sync(0xffffffffu, t1, o));
                 }
-                n0 = fmaxf(n0, m0);
-                n1 = fmaxf(n1, m1);
-                const float g0 = ex2_approx(m0 - n0), g1 = ex2_approx(m1 - n1);
+                const float n0 = t0 > m0 + kMoveMax ? t0 : m0, n1 = t1 > m1 + kMoveMax ? t1 : m1;
+                const float g0 = n0 == m0 ? 1.f : ex2_approx(m0 - n0), g1 = n1 == m1 ? 1.f : ex2_approx(m1 - n1);
                 m0 = n0;
                 m1 = n1;
-                l0 *= g0;
-                l1 *= g1;
+                sum[0] *= g0;
+                sum[1] *= g1;
 #pragma unroll
                 for (int k = 0; k < 8; ++k) {
                     acc[k][0] *= g0;
@@ -558,49 +618,86 @@ __global__ void __launch_bounds__(kThreadsD, kFp4DecodeCtas) paged_gqa_decode_fp
                     acc[k][2] *= g0;
                     acc[k][3] *= g1;
                 }
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+#pragma unroll
+                    for (int k = 0; k < 2; ++k)
+                        z[j][k] = make_float2(w[j][k].x - m0, w[j][k].y - m1);
             }
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-                const float p0 = ex2_approx(y[j][0] - m0), p1 = ex2_approx(y[j][1] - m1);
-                const float p2 = ex2_approx(y[j][2] - m0), p3 = ex2_approx(y[j][3] - m1);
+                RawV x;
+                load_v(st + (2 + j) * kFp4Tile, lo_off, x);
+                if (seen != 0xffffffffu || missing) {      // values of unseen tokens may be anything
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        const uint32_t s = missing & (1u << j) ? 0u : seen >> (16 * j + 8 * k);
+                        x.s[k] &= ((s >> order(2 * c)) & 1u ? 0x00FFu : 0u) |
+                                  ((s >> order(2 * c + 1)) & 1u ? 0xFF00u : 0u);
+                    }
+                }
+                const float p0 = ex2_approx(z[j][0].x), p1 = ex2_approx(z[j][0].y);
+                const float p2 = ex2_approx(z[j][1].x), p3 = ex2_approx(z[j][1].y);
                 const uint32_t ha = f32x2_to_f16x2(p0, p1), hb = f32x2_to_f16x2(p2, p3);
-                const float2 va = f16x2_to_f32x2(ha), vb = f16x2_to_f32x2(hb);
                 uint32_t b[kParts][2];
                 b[0][0] = transpose8x8(ha);
                 b[0][1] = transpose8x8(hb);
                 if constexpr (kParts == 2) {
-                    l0 += p0 + p2;
-                    l1 += p1 + p3;
+                    const float2 va = f16x2_to_f32x2(ha), vb = f16x2_to_f32x2(hb);
                     b[1][0] = transpose8x8(f32x2_to_f16x2(p0 - va.x, p1 - va.y));
                     b[1][1] = transpose8x8(f32x2_to_f16x2(p2 - vb.x, p3 - vb.y));
-                } else {
-                    l0 += va.x + vb.x;
-                    l1 += va.y + vb.y;
                 }
-                accumulate<kParts>(x[j], b, acc);
+                accumulate<kParts>(x, b, acc, sum);
             }
-            if ((i + 1) % kFoldUnits == 0 || (i + 1 == take && take > kFoldUnits)) {
-                const float g0 = ex2_approx(mf0 - m0), g1 = ex2_approx(mf1 - m1);
-                const bool old = i + 1 > kFoldUnits, last = i + 1 == take;
+            if (u + kStagesD < n) {                        // the stage just read takes the unit after the ring's
+                fence_proxy_async_smem();
+                __syncwarp();
+                issue(u + kStagesD, stage);
+            }
+            if (++stage == kStagesD) {
+                stage = 0;
+                parity ^= 1u;
+            }
+            if ((i + 1) % kFoldUnits<kParts> == 0 || (i + 1 == take && take > kFoldUnits<kParts>)) {
+                // the piece's own slot of the workspace holds the copy (each lane its own elements)
+                const float g0 = i + 1 > kFoldUnits<kParts> ? ex2_approx(mf0 - m0) : 0.f;
+                const float g1 = i + 1 > kFoldUnits<kParts> ? ex2_approx(mf1 - m1) : 0.f;
+                const bool old = i + 1 > kFoldUnits<kParts>, last = i + 1 == take;
+                if (slot >= da.num_slots) {
+                    if (a.err && lane == 0)
+                        atomicOr(a.err, PKV_DEVERR_INTERNAL);
+                } else {
+                    float *s = da.partials + slot * a.group * kPartialStride;
 #pragma unroll
-                for (int k = 0; k < 32; ++k) {
-                    const float v = acc[k >> 2][k & 3] + (old ? fold[32 * k] * ((k & 1) ? g1 : g0) : 0.f);
-                    if (!last)
-                        fold[32 * k] = v;
-                    acc[k >> 2][k & 3] = last ? v : 0.f;
+                    for (int j = 0; j < 2; ++j) {
+                        if (2 * c + j >= a.group)
+                            continue;
+                        float *at = s + (2 * c + j) * kPartialStride + 16 * r;
+#pragma unroll
+                        for (int k = 0; k < 16; ++k) {
+                            float &v = acc[k >> 1][2 * (k & 1) + j];
+                            v += old ? at[k] * (j ? g1 : g0) : 0.f;
+                            if (!last) {
+                                at[k] = v;
+                                v = 0.f;
+                            }
+                        }
+                    }
                 }
+                l0 = l0 * g0 + sum[0];
+                l1 = l1 * g1 + sum[1];
+                sum[0] = last ? l0 : 0.f;
+                sum[1] = last ? l1 : 0.f;
                 mf0 = m0;
                 mf1 = m1;
             }
         }
+        if (dead)
+            break;
 
         // ---- end of piece: heads 2c, 2c + 1; dims 16 r ..
-#pragma unroll
-        for (int o = 4; o < 32; o <<= 1) {
-            l0 += __shfl_xor_sync(0xffffffffu, l0, o);
-            l1 += __shfl_xor_sync(0xffffffffu, l1, o);
-        }
-        const int64_t slot = static_cast<int64_t>(worker) + p.h * a.batch + p.b;
+        l0 = sum[0];
+        l1 = sum[1];
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
             const int g = 2 * c + j;
@@ -632,10 +729,11 @@ __global__ void __launch_bounds__(kThreadsD, kFp4DecodeCtas) paged_gqa_decode_fp
     }
 
     // After an abort: no copy may land in this ring once the warp has left.
-    for (int s = 0; s < kStagesD; ++s)
-        if (pending & (1u << s)) {
+    if (dead)
+        for (int v = u; v < n && v < u + kStagesD; ++v) {
             const uint64_t t0 = global_timer_ns();
-            while (!mbar_try_wait(bars + 8 * s, (pend_par >> s) & 1u) && global_timer_ns() - t0 < kLimitNs) {
+            while (!mbar_try_wait(bars + 8 * (v % kStagesD), (v / kStagesD) & 1u) &&
+                   global_timer_ns() - t0 < kLimitNs) {
             }
         }
 }
