@@ -115,7 +115,8 @@ __device__ __forceinline__ Place place_of(const int *start, int batch, int x)
     return p;
 }
 
-__device__ __forceinline__ bool wait_stage(uint32_t bar, uint32_t parity, volatile int *stop, int32_t *err, int lane)
+// Bounded wait by a whole warp.
+__device__ __noinline__ bool wait_slow(uint32_t bar, uint32_t parity, volatile int *stop, int32_t *err, int lane)
 {
     uint64_t t0 = 0;
     for (uint32_t it = 0;; ++it) {
@@ -139,6 +140,11 @@ __device__ __forceinline__ bool wait_stage(uint32_t bar, uint32_t parity, volati
                 return false;
         }
     }
+}
+
+__device__ __forceinline__ bool wait_stage(uint32_t bar, uint32_t parity, volatile int *stop, int32_t *err, int lane)
+{
+    return __all_sync(0xffffffffu, mbar_try_wait(bar, parity)) || wait_slow(bar, parity, stop, err, lane);
 }
 
 __device__ __forceinline__ void lds128(uint32_t at, uint32_t (&r)[4])
@@ -265,7 +271,7 @@ __device__ __forceinline__ void load_v(uint32_t vt, const LaneOffsets &o, RawV &
     for (int j = 0; j < 2; ++j) {
         lds64(vt + o.v0 + 512 * j, x.v[2 * j]);
         lds64(vt + o.v1 + 512 * j, x.v[2 * j + 1]);
-        x.s[j] = lds8(vt + o.s0 + 64 * j) | (lds8(vt + o.s1 + 64 * j) << 8);
+        x.s[j] = lds8(vt + o.s1 + 64 * j) * 256u + lds8(vt + o.s0 + 64 * j);
     }
 }
 
@@ -273,14 +279,14 @@ __device__ __forceinline__ void load_v(uint32_t vt, const LaneOffsets &o, RawV &
 // order(r) + 8 (y[1]), each for heads 2c, 2c + 1.
 __device__ __forceinline__ void scores(const RawK &x, const uint32_t (&q)[8][2], uint64_t (&y)[2])
 {
-    uint32_t s[2][2];
+    __half2 s[2][2];
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
         const uint32_t p = e4m3x2_to_f16x2(x.s[j]);
-        s[j][0] = __byte_perm(p, p, 0x1010);
-        s[j][1] = __byte_perm(p, p, 0x3232);
+        s[j][0] = __low2half2(*reinterpret_cast<const __half2 *>(&p));
+        s[j][1] = __high2half2(*reinterpret_cast<const __half2 *>(&p));
     }
-    float d[2][4] = {};
+    float d[4] = {};
 #pragma unroll
     for (int w = 0; w < 4; ++w) {
         uint32_t a[2][4];
@@ -288,14 +294,16 @@ __device__ __forceinline__ void scores(const RawK &x, const uint32_t (&q)[8][2],
         for (int j = 0; j < 2; ++j) {
             e2m1x8_to_f16x8(x.k[j][w], a[j]);
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                a[j][i] = mul_f16x2(a[j][i], s[j][w >> 1]);
+            for (int i = 0; i < 4; ++i) {
+                const __half2 v = __hmul2(*reinterpret_cast<const __half2 *>(&a[j][i]), s[j][w >> 1]);
+                a[j][i] = *reinterpret_cast<const uint32_t *>(&v);
+            }
         }
-        mma_16816(d[0], a[0][0], a[1][0], a[0][1], a[1][1], q[2 * w][0], q[2 * w][1]);
-        mma_16816(d[1], a[0][2], a[1][2], a[0][3], a[1][3], q[2 * w + 1][0], q[2 * w + 1][1]);
+        mma_16816(d, a[0][0], a[1][0], a[0][1], a[1][1], q[2 * w][0], q[2 * w][1]);
+        mma_16816(d, a[0][2], a[1][2], a[0][3], a[1][3], q[2 * w + 1][0], q[2 * w + 1][1]);
     }
-    y[0] = add2(pack2(d[0][0], d[0][1]), pack2(d[1][0], d[1][1]));
-    y[1] = add2(pack2(d[0][2], d[0][3]), pack2(d[1][2], d[1][3]));
+    y[0] = pack2(d[0], d[1]);
+    y[1] = pack2(d[2], d[3]);
 }
 
 // acc += V^T P^T and sum += 1^T P^T for a tile; b: the weights of its 16 tokens
@@ -437,6 +445,8 @@ __global__ void __launch_bounds__(kThreadsD, kFp4DecodeCtas) paged_gqa_decode_fp
     const uint32_t ring = smem_addr(smem) + warp * kStagesD * kUnitBytes;
     const uint32_t bars = smem_addr(smem + SmemD::kBar) + warp * kStagesD * 8;
 
+    const uint64_t policy = l2_policy_evict_first();
+
     // ---- tile addresses, 16 units ahead: lane 2i + j has tile j of unit i.
     // -1: a page outside the pool; -2: no such tile.
     auto look_up = [&](int u0) -> int {
@@ -457,24 +467,28 @@ __global__ void __launch_bounds__(kThreadsD, kFp4DecodeCtas) paged_gqa_decode_fp
         return (phys * a.hkv + p.h) * (a.page_size >> 4) + (row >> 4);
     };
     int now = look_up(0), next = look_up(16), base = 0;
+    uint32_t have = __ballot_sync(0xffffffffu, now >= 0);
     uint32_t bad = 0;                                      // missing tiles, 2 bits a stage
+    const uint32_t my_dst = ring + (lane & 3) * kFp4Tile;  // lanes 0, 1 bring K tiles; 2, 3: V tiles
+    const uint8_t *my_src = lane < 2 ? a.k_cache : a.v_cache;
     auto issue = [&](int u, int s) {                       // unit u into stage s = u % kStagesD
         if (u >= base + 16) {
             base += 16;
             now = next;
+            have = __ballot_sync(0xffffffffu, now >= 0);
             next = look_up(base + 16);
         }
-        const int t = __shfl_sync(0xffffffffu, now, 2 * (u - base) + (lane & 1));
-        const uint32_t have = __ballot_sync(0xffffffffu, t >= 0) & 3u;
-        bad = (bad & ~(3u << (2 * s))) | ((~have & 3u) << (2 * s));
-        if (worker != da.withhold || u != 0) {
+        const int i = 2 * (u - base);
+        const int t = __shfl_sync(0xffffffffu, now, i + (lane & 1));
+        const uint32_t both = (have >> i) & 3u;
+        bad = (bad & ~(3u << (2 * s))) | ((both ^ 3u) << (2 * s));
+        if (lane < 4 && (worker != da.withhold || u != 0)) {
+            const uint32_t bar = bars + 8 * s;
+            // (bytes that land before they are announced are only counted early)
             if (lane == 0)
-                mbar_arrive_expect_tx(bars + 8 * s, 2 * kFp4Tile * __popc(have));
-            __syncwarp();
-            if (lane < 4 && t >= 0)                        // lanes 0, 1: K tiles; 2, 3: V tiles
-                bulk_load(ring + s * kUnitBytes + lane * kFp4Tile,
-                          (lane < 2 ? a.k_cache : a.v_cache) + static_cast<int64_t>(t) * kFp4Tile, kFp4Tile,
-                          bars + 8 * s);
+                mbar_arrive_expect_tx(bar, both == 3u ? 4 * kFp4Tile : both ? 2 * kFp4Tile : 0);
+            if (t >= 0)
+                bulk_load(my_dst + s * kUnitBytes, my_src + static_cast<int64_t>(t) * kFp4Tile, kFp4Tile, bar, policy);
         }
     };
     for (int v = 0; v < kStagesD && v < n; ++v)

@@ -15,13 +15,14 @@ __device__ __forceinline__ int64_t fp4_tile_offset(int64_t page, int h, int row,
 }
 
 // Bulk copy of contiguous bytes (a multiple of 16, both ends 16-byte aligned)
-// into shared memory, completing on an mbarrier; read once, so first to leave L2.
-__device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_t bytes, uint32_t bar)
+// into shared memory, completing on an mbarrier.
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_t bytes, uint32_t bar,
+                                          uint64_t policy)
 {
     asm volatile(
         "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1], %2, [%3], %4;" ::"r"(
             dst),
-        "l"(src), "r"(bytes), "r"(bar), "l"(l2_policy_evict_first())
+        "l"(src), "r"(bytes), "r"(bar), "l"(policy)
         : "memory");
 }
 
