@@ -608,15 +608,102 @@ def paged_prefill(q, cu_q, k_cache, v_cache, k_scale, v_scale, block_table, seq_
 # ---------------------------------------------------------------------------
 # the 4-bit cache
 # ---------------------------------------------------------------------------
-def _check_fp4_pools(k_cache, v_cache):
-    _need(k_cache, "k_cache", torch.uint8, 4)
-    _need(v_cache, "v_cache", torch.uint8, 4)
-    if v_cache.shape != k_cache.shape or k_cache.shape[3] != FP4_ROW_BYTES:
+# A decode step makes these calls once a layer and the smallest of them run for
+# a few microseconds, so the checks are made in one pass over each tensor.
+def _addr(t, name, dtype, dim, dev):
+    """The address of a contiguous tensor of this type and number of
+    dimensions on CUDA device index dev."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.get_device() != dev:
+        if not t.is_cuda:
+            raise ValueError(f"{name} must be on a CUDA device")
+        raise ValueError(f"all tensors must be on cuda:{dev}, got {name} on {t.device}")
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if dim is not None and t.dim() != dim:
+        raise ValueError(f"{name} must have {dim} dims, got {tuple(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def _cuda_index(t, name):
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    dev = t.get_device()
+    if dev < 0 or not t.is_cuda:
+        raise ValueError(f"{name} must be on a CUDA device")
+    return dev
+
+
+def _act(t, name):
+    if t.dtype is torch.bfloat16:
+        return PKV_BF16
+    if t.dtype is torch.float32:
+        return PKV_F32
+    raise TypeError(f"{name} must be float32 or bfloat16, got {t.dtype}")
+
+
+def _call(name, dev, stream, fn, *args):
+    """fn(*args, stream) with device dev current; stream None: its current one."""
+    if dev != torch.cuda.current_device():
+        with torch.cuda.device(dev):
+            return _call(name, dev, stream, fn, *args)
+    if stream is None:
+        raw = torch._C._cuda_getCurrentRawStream(dev)
+    elif isinstance(stream, torch.cuda.Stream):
+        raw = stream.cuda_stream
+    else:
+        raw = int(stream)
+    st = fn(*args, raw)
+    if st != 0:
+        raise PkvError(st, name)
+
+
+def _fp4_pools(k_cache, v_cache, dev):
+    """Addresses, pages, kv heads and page size of a K and a V pool."""
+    k, v = _addr(k_cache, "k_cache", torch.uint8, 4, dev), _addr(v_cache, "v_cache", torch.uint8, 4, dev)
+    shape = k_cache.shape
+    if v_cache.shape != shape or shape[3] != FP4_ROW_BYTES:
         raise ValueError(f"4-bit caches must be uint8 [num_pages, Hkv, P, {FP4_ROW_BYTES}], both alike")
+    return k, v, shape[0], shape[1], shape[2]
+
+
+def _fp4_rows(slot_mapping, k_scale, v_scale, k, v, H, dev):
+    """What append and read back share: addresses of slots, scales and rows."""
+    shape = k.shape
+    slots = _addr(slot_mapping, "slot_mapping", torch.int64, 1, dev)
+    ks, vs = _addr(k_scale, "k_scale", torch.float32, 1, dev), _addr(v_scale, "v_scale", torch.float32, 1, dev)
+    if v.shape != shape or shape[1] != H:
+        raise ValueError("k/v shapes disagree")
+    if slot_mapping.shape[0] != shape[0] or k_scale.shape[0] != H or v_scale.shape[0] != H:
+        raise ValueError("slot_mapping / scale shapes disagree")
+    return slots, ks, vs, shape[0], shape[2]
+
+
+def _error_word(device_error, dev):
+    return None if device_error is None else _addr(device_error, "device_error", torch.int32, None, dev)
+
+
+def _fp4_attention(q, out, k_scale, v_scale, block_table, seq_lens, seq_page_sizes, workspace, Hkv, dev):
+    """What decode and prefill share: the tensors' addresses."""
+    if out.shape != q.shape:
+        raise ValueError("q / out shapes disagree")
+    B = seq_lens.shape[0]
+    if k_scale.shape[0] != Hkv or v_scale.shape[0] != Hkv:
+        raise ValueError("scales must have one entry per kv head")
+    if block_table.shape[0] != B or (seq_page_sizes is not None and seq_page_sizes.shape[0] != B):
+        raise ValueError("block_table, seq_lens and seq_page_sizes must have one entry per sequence")
+    return (_addr(q, "q", torch.bfloat16, 3, dev), _addr(out, "out", out.dtype, 3, dev), _act(out, "out"),
+            _addr(k_scale, "k_scale", torch.float32, 1, dev), _addr(v_scale, "v_scale", torch.float32, 1, dev),
+            _addr(block_table, "block_table", torch.int32, 2, dev), _addr(seq_lens, "seq_lens", torch.int32, 1, dev),
+            None if seq_page_sizes is None else _addr(seq_page_sizes, "seq_page_sizes", torch.int32, 1, dev),
+            _addr(workspace, "workspace", torch.uint8, None, dev))
 
 
 def _check_window(window, sinks):
-    if int(window) < 0 or int(sinks) < 0:
+    if window < 0 or sinks < 0:
         raise ValueError("window and sinks must not be negative")
 
 
@@ -631,54 +718,24 @@ def pkv_kv_append_fp4(k_new, v_new, slot_mapping, k_scale, v_scale, k_cache, v_c
     """k_new/v_new [T, Hkv, 128] fp32|bf16; slot_mapping int64 [T] (negative:
     not written); scales fp32 [Hkv]; caches uint8 [num_pages, Hkv, P, 72]
     (written in place)."""
-    _need(k_new, "k_new", dim=3)
-    _need(v_new, "v_new", dtype=k_new.dtype, dim=3)
-    _need(slot_mapping, "slot_mapping", torch.int64, 1)
-    _need(k_scale, "k_scale", torch.float32, 1)
-    _need(v_scale, "v_scale", torch.float32, 1)
-    _check_fp4_pools(k_cache, v_cache)
-    if device_error is not None:
-        _need(device_error, "device_error", torch.int32)
-    T, H, D = k_new.shape
-    NP, H2, P, _ = k_cache.shape
-    if v_new.shape != k_new.shape or H2 != H:
-        raise ValueError("k/v shapes disagree")
-    if slot_mapping.shape[0] != T or k_scale.shape[0] != H or v_scale.shape[0] != H:
-        raise ValueError("slot_mapping / scale shapes disagree")
-    _same_device(k_new, v_new, slot_mapping, k_scale, v_scale, k_cache, v_cache, device_error)
-    with _device_of(k_new):
-        st = load().pkv_kv_append_fp4(_ptr(k_new), _ptr(v_new), _act_code(k_new), T, H, D, _ptr(slot_mapping),
-                                      _ptr(k_scale), _ptr(v_scale), _ptr(k_cache), _ptr(v_cache), NP, P,
-                                      _ptr(device_error), _stream(stream))
-    if st != 0:
-        raise PkvError(st, "pkv_kv_append_fp4")
+    dev = _cuda_index(k_new, "k_new")
+    k, v = _addr(k_new, "k_new", k_new.dtype, 3, dev), _addr(v_new, "v_new", k_new.dtype, 3, dev)
+    kc, vc, NP, H, P = _fp4_pools(k_cache, v_cache, dev)
+    slots, ks, vs, T, D = _fp4_rows(slot_mapping, k_scale, v_scale, k_new, v_new, H, dev)
+    _call("pkv_kv_append_fp4", dev, stream, (_lib or load()).pkv_kv_append_fp4, k, v, _act(k_new, "k_new"), T, H, D,
+          slots, ks, vs, kc, vc, NP, P, _error_word(device_error, dev))
 
 
 def pkv_kv_read_fp4(slot_mapping, k_scale, v_scale, k_cache, v_cache, k_out, v_out, device_error=None,
                     stream=None) -> None:
     """The rows at slot_mapping (int64 [T]) as values, into k_out/v_out
     [T, Hkv, 128] fp32|bf16; rows of negative slots are left as they were."""
-    _need(slot_mapping, "slot_mapping", torch.int64, 1)
-    _need(k_scale, "k_scale", torch.float32, 1)
-    _need(v_scale, "v_scale", torch.float32, 1)
-    _check_fp4_pools(k_cache, v_cache)
-    _need(k_out, "k_out", dim=3)
-    _need(v_out, "v_out", dtype=k_out.dtype, dim=3)
-    if device_error is not None:
-        _need(device_error, "device_error", torch.int32)
-    T, H, D = k_out.shape
-    NP, H2, P, _ = k_cache.shape
-    if v_out.shape != k_out.shape or H2 != H:
-        raise ValueError("k/v shapes disagree")
-    if slot_mapping.shape[0] != T or k_scale.shape[0] != H or v_scale.shape[0] != H:
-        raise ValueError("slot_mapping / scale shapes disagree")
-    _same_device(slot_mapping, k_scale, v_scale, k_cache, v_cache, k_out, v_out, device_error)
-    with _device_of(slot_mapping):
-        st = load().pkv_kv_read_fp4(_ptr(slot_mapping), T, H, D, _ptr(k_scale), _ptr(v_scale), _ptr(k_cache),
-                                    _ptr(v_cache), NP, P, _ptr(k_out), _ptr(v_out), _act_code(k_out),
-                                    _ptr(device_error), _stream(stream))
-    if st != 0:
-        raise PkvError(st, "pkv_kv_read_fp4")
+    dev = _cuda_index(k_out, "k_out")
+    k, v = _addr(k_out, "k_out", k_out.dtype, 3, dev), _addr(v_out, "v_out", k_out.dtype, 3, dev)
+    kc, vc, NP, H, P = _fp4_pools(k_cache, v_cache, dev)
+    slots, ks, vs, T, D = _fp4_rows(slot_mapping, k_scale, v_scale, k_out, v_out, H, dev)
+    _call("pkv_kv_read_fp4", dev, stream, (_lib or load()).pkv_kv_read_fp4, slots, T, H, D, ks, vs, kc, vc, NP, P, k,
+          v, _act(k_out, "k_out"), _error_word(device_error, dev))
 
 
 def kv_append_fp4(k_new, v_new, slot_mapping, k_scale, v_scale, k_cache, v_cache, device_error=None,
@@ -713,39 +770,18 @@ def pkv_paged_gqa_decode_fp4(q, k_cache, v_cache, k_scale, v_scale, block_table,
     """pkv_paged_gqa_decode over 4-bit caches uint8 [num_pages, Hkv, P, 72];
     window > 0: only the last `window` tokens and the first `sinks` are
     attended.  workspace uint8 (pkv_decode_fp4_workspace_size bytes)."""
-    _need(q, "q", torch.bfloat16, 3)
-    _check_fp4_pools(k_cache, v_cache)
-    _need(k_scale, "k_scale", torch.float32, 1)
-    _need(v_scale, "v_scale", torch.float32, 1)
-    _need(block_table, "block_table", torch.int32, 2)
-    _need(seq_lens, "seq_lens", torch.int32, 1)
-    _need(out, "out", dim=3)
-    _need(workspace, "workspace", torch.uint8)
-    if device_error is not None:
-        _need(device_error, "device_error", torch.int32)
+    dev = _cuda_index(q, "q")
+    kc, vc, NP, Hkv, P = _fp4_pools(k_cache, v_cache, dev)
+    qa, oa, odt, ks, vs, bt, lens, psz, ws = _fp4_attention(q, out, k_scale, v_scale, block_table, seq_lens,
+                                                           seq_page_sizes, workspace, Hkv, dev)
     B, Hq, D = q.shape
-    NP, Hkv, P, _ = k_cache.shape
-    if out.shape != q.shape:
-        raise ValueError("q / out shapes disagree")
-    if block_table.shape[0] != B or seq_lens.shape[0] != B:
-        raise ValueError("block_table / seq_lens shapes disagree with q")
-    if k_scale.shape[0] != Hkv or v_scale.shape[0] != Hkv:
-        raise ValueError("scales must have one entry per kv head")
-    _check_page_sizes(seq_page_sizes, B)
+    if seq_lens.shape[0] != B:
+        raise ValueError("seq_lens must have one entry per row of q")
     _check_window(window, sinks)
-    _same_device(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, out, workspace, device_error,
-                 seq_page_sizes)
-    if sm_scale is None:
-        sm_scale = 1.0 / math.sqrt(D)
-    with _device_of(q):
-        st = load().pkv_paged_gqa_decode_fp4(_ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale),
-                                             _ptr(block_table), block_table.shape[1], _ptr(seq_lens),
-                                             int(max_seq_len), _ptr(seq_page_sizes), B, Hq, Hkv, D, P, NP,
-                                             float(sm_scale), int(window), int(sinks), _ptr(out), _act_code(out),
-                                             _ptr(workspace), workspace.numel(), _ptr(device_error), int(max_ctas),
-                                             _stream(stream))
-    if st != 0:
-        raise PkvError(st, "pkv_paged_gqa_decode_fp4")
+    _call("pkv_paged_gqa_decode_fp4", dev, stream, (_lib or load()).pkv_paged_gqa_decode_fp4, qa, kc, vc, ks, vs, bt,
+          block_table.shape[1], lens, int(max_seq_len), psz, B, Hq, Hkv, D, P, NP,
+          1.0 / math.sqrt(D) if sm_scale is None else float(sm_scale), int(window), int(sinks), oa, odt, ws, workspace.numel(),
+          _error_word(device_error, dev), int(max_ctas))
 
 
 def paged_gqa_decode_fp4(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, out=None,
@@ -756,6 +792,7 @@ def paged_gqa_decode_fp4(q, k_cache, v_cache, k_scale, v_scale, block_table, seq
         out = torch.empty(q.shape, dtype=out_dtype, device=q.device)
     max_seq_len = _default_max_len(block_table, k_cache, max_seq_len, seq_page_sizes)
     if workspace is None:
+        _cuda_index(q, "q")
         with _device_of(q):
             n = pkv_decode_fp4_workspace_size(q.shape[0], q.shape[1], k_cache.shape[1], q.shape[2], max_seq_len,
                                               k_cache.shape[2], max_ctas)
@@ -780,41 +817,20 @@ def pkv_paged_prefill_fp4(q, cu_q, k_cache, v_cache, k_scale, v_scale, block_tab
     window > 0: a query sees itself, the window - 1 tokens before it and the
     first `sinks` tokens.  workspace uint8 (pkv_prefill_fp4_workspace_size
     bytes for the same bounds)."""
-    _need(q, "q", torch.bfloat16, 3)
-    _need(cu_q, "cu_q", torch.int32, 1)
-    _check_fp4_pools(k_cache, v_cache)
-    _need(k_scale, "k_scale", torch.float32, 1)
-    _need(v_scale, "v_scale", torch.float32, 1)
-    _need(block_table, "block_table", torch.int32, 2)
-    _need(seq_lens, "seq_lens", torch.int32, 1)
-    _need(out, "out", dim=3)
-    _need(workspace, "workspace", torch.uint8)
-    if device_error is not None:
-        _need(device_error, "device_error", torch.int32)
+    dev = _cuda_index(q, "q")
+    kc, vc, NP, Hkv, P = _fp4_pools(k_cache, v_cache, dev)
+    qa, oa, odt, ks, vs, bt, lens, psz, ws = _fp4_attention(q, out, k_scale, v_scale, block_table, seq_lens,
+                                                           seq_page_sizes, workspace, Hkv, dev)
+    cu = _addr(cu_q, "cu_q", torch.int32, 1, dev)
     T, Hq, D = q.shape
-    NP, Hkv, P, _ = k_cache.shape
     B = seq_lens.shape[0]
-    if out.shape != q.shape:
-        raise ValueError("q / out shapes disagree")
-    if block_table.shape[0] != B or cu_q.shape[0] != B + 1:
-        raise ValueError("block_table / cu_q shapes disagree with seq_lens")
-    if k_scale.shape[0] != Hkv or v_scale.shape[0] != Hkv:
-        raise ValueError("scales must have one entry per kv head")
-    _check_page_sizes(seq_page_sizes, B)
+    if cu_q.shape[0] != B + 1:
+        raise ValueError("cu_q must have one entry more than seq_lens")
     _check_window(window, sinks)
-    _same_device(q, cu_q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, out, workspace, device_error,
-                 seq_page_sizes)
-    if sm_scale is None:
-        sm_scale = 1.0 / math.sqrt(D)
-    with _device_of(q):
-        st = load().pkv_paged_prefill_fp4(_ptr(q), _ptr(cu_q), T, int(max_q_len), _ptr(k_cache), _ptr(v_cache),
-                                          _ptr(k_scale), _ptr(v_scale), _ptr(block_table), block_table.shape[1],
-                                          _ptr(seq_lens), _ptr(seq_page_sizes), B, int(max_kv_len),
-                                          int(max_total_kv), Hq, Hkv, D, P, NP, float(sm_scale), int(window),
-                                          int(sinks), _ptr(out), _act_code(out), _ptr(workspace), workspace.numel(),
-                                          _ptr(device_error), _stream(stream))
-    if st != 0:
-        raise PkvError(st, "pkv_paged_prefill_fp4")
+    _call("pkv_paged_prefill_fp4", dev, stream, (_lib or load()).pkv_paged_prefill_fp4, qa, cu, T, int(max_q_len), kc,
+          vc, ks, vs, bt, block_table.shape[1], lens, psz, B, int(max_kv_len), int(max_total_kv), Hq, Hkv, D, P, NP,
+          1.0 / math.sqrt(D) if sm_scale is None else float(sm_scale), int(window), int(sinks), oa, odt, ws, workspace.numel(),
+          _error_word(device_error, dev))
 
 
 def paged_prefill_fp4(q, cu_q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, max_q_len, out=None,

@@ -52,8 +52,10 @@ constexpr int kUnitBytes = 4 * kFp4Tile;                   // K tile 0, K tile 1
 constexpr float kMoveMax = 8.f;                            // log2 units
 // Units after which a piece's accumulator is added into an fp32 copy: the
 // tensor cores add with truncation, whose error grows with the chain.
+// 2048 additions (512 units of one part) may leave 2^-12 under a bf16
+// output's 2^-8, 256 (64 units of two parts) 2^-15 under an fp32 one.
 template <int kParts>
-constexpr int kFoldUnits = 128 / kParts;
+constexpr int kFoldUnits = kParts == 1 ? 512 : 64;
 constexpr uint64_t kLimitNs = 2000000000ull;
 
 struct SmemD {                                             // the ring, [warps][stages][kUnitBytes], comes first
@@ -581,6 +583,18 @@ __global__ void __launch_bounds__(kThreadsD, kFp4DecodeCtas) paged_gqa_decode_fp
                 scores(x[0], q, y[0]);
                 scores(x[1], q, y[1]);
             }
+            RawV xv[2];
+            load_v(st + 2 * kFp4Tile, lo_off, xv[0]);
+            load_v(st + 3 * kFp4Tile, lo_off, xv[1]);
+            if (u + kStagesD < n) {                        // the stage just read takes the unit after the ring's
+                fence_proxy_async_smem();
+                __syncwarp();
+                issue(u + kStagesD, stage);
+            }
+            if (++stage == kStagesD) {
+                stage = 0;
+                parity ^= 1u;
+            }
             const int unit = p.unit + i;
             uint32_t seen = 0xffffffffu;                   // the visible ones of the unit's 32 tokens
             float2 z[2][2];
@@ -640,8 +654,7 @@ __global__ void __launch_bounds__(kThreadsD, kFp4DecodeCtas) paged_gqa_decode_fp
             }
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-                RawV x;
-                load_v(st + (2 + j) * kFp4Tile, lo_off, x);
+                RawV &x = xv[j];
                 if (seen != 0xffffffffu || missing) {      // values of unseen tokens may be anything
 #pragma unroll
                     for (int k = 0; k < 2; ++k) {
@@ -662,15 +675,6 @@ __global__ void __launch_bounds__(kThreadsD, kFp4DecodeCtas) paged_gqa_decode_fp
                     b[1][1] = transpose8x8(f32x2_to_f16x2(p2 - vb.x, p3 - vb.y));
                 }
                 accumulate<kParts>(x, b, acc, sum);
-            }
-            if (u + kStagesD < n) {                        // the stage just read takes the unit after the ring's
-                fence_proxy_async_smem();
-                __syncwarp();
-                issue(u + kStagesD, stage);
-            }
-            if (++stage == kStagesD) {
-                stage = 0;
-                parity ^= 1u;
             }
             if ((i + 1) % kFoldUnits<kParts> == 0 || (i + 1 == take && take > kFoldUnits<kParts>)) {
                 // the piece's own slot of the workspace holds the copy (each lane its own elements)

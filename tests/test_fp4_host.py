@@ -98,22 +98,58 @@ def test_more_refusals(lib):
         assert pkv.pkv_prefill_fp4_workspace_size(*bad) == 0, bad
 
 
+class _OnDevice(torch.Tensor):
+    """A host tensor that says it is on cuda:0: the checks never read it."""
+    is_cuda = True
+
+    def get_device(self):
+        return 0
+
+
+def _fake(*shape, dtype=torch.float32):
+    return torch.zeros(shape, dtype=dtype).as_subclass(_OnDevice)
+
+
 def test_binding_refuses():
-    with pytest.raises(ValueError, match="72"):
-        pkv._check_fp4_pools(*[_fake((2, 1, 16, 128))] * 2)
-    with pytest.raises(ValueError):
+    f32, u8, i64 = torch.float32, torch.uint8, torch.int64
+    z, s, slots = _fake(3, 2, 128), _fake(2), _fake(3, dtype=i64)
+    pool = _fake(4, 2, 16, 72, dtype=u8)
+    good = dict(k_new=z, v_new=z, slot_mapping=slots, k_scale=s, v_scale=s, k_cache=pool, v_cache=pool)
+    for name, bad, error in (("k_new", torch.zeros(3, 2, 128), ValueError), ("k_new", 3, TypeError),
+                             ("v_new", z.to(torch.bfloat16), TypeError), ("k_new", _fake(3, 128), ValueError),
+                             ("v_new", _fake(2, 2, 128), ValueError), ("slot_mapping", _fake(3), TypeError),
+                             ("slot_mapping", _fake(4, dtype=i64), ValueError), ("k_scale", _fake(3), ValueError),
+                             ("v_scale", _fake(2, dtype=torch.float64), TypeError),
+                             ("k_cache", _fake(4, 2, 16, 128, dtype=u8), ValueError),
+                             ("v_cache", _fake(4, 2, 32, 72, dtype=u8), ValueError),
+                             ("k_new", _fake(3, 128, 2).transpose(1, 2), ValueError),
+                             ("k_cache", torch.zeros(4, 2, 16, 72, dtype=u8), ValueError)):
+        with pytest.raises(error):
+            pkv.kv_append_fp4(**{**good, name: bad})
+    with pytest.raises(TypeError, match="float32 or bfloat16"):
+        pkv.kv_append_fp4(**{**good, "k_new": z.half(), "v_new": z.half()})
+    with pytest.raises(ValueError, match="both outputs"):
+        pkv.kv_read_fp4(slots, s, s, pool, pool, k_out=z)
+    with pytest.raises(ValueError, match="negative"):
         pkv._check_window(-1, 0)
-    with pytest.raises(ValueError):
-        pkv.kv_read_fp4(torch.zeros(1), None, None, None, None, k_out=torch.zeros(1))
-    with pytest.raises(ValueError, match="CUDA"):
-        z = torch.zeros(1, 1, 128)
-        pkv.kv_append_fp4(z, z, torch.zeros(1, dtype=torch.int64), z, z, z, z)
 
-
-def _fake(shape):
-    class T(torch.Tensor):
-        is_cuda = True
-    return torch.zeros(shape, dtype=torch.uint8).as_subclass(T)
+    q = _fake(3, 4, 128).to(torch.bfloat16)
+    bt, lens = _fake(3, 5, dtype=torch.int32), _fake(3, dtype=torch.int32)
+    ws = _fake(1024, dtype=u8)
+    good = dict(q=q, k_cache=pool, v_cache=pool, k_scale=s, v_scale=s, block_table=bt, seq_lens=lens, out=q,
+                workspace=ws)
+    for name, bad, error in (("q", z, ValueError), ("q", _fake(3, 4, 128), TypeError), ("out", _fake(3, 4, 64), ValueError),
+                             ("out", q.half(), TypeError), ("block_table", _fake(2, 5, dtype=torch.int32), ValueError),
+                             ("seq_lens", _fake(2, dtype=torch.int32), ValueError), ("k_scale", _fake(3), ValueError),
+                             ("seq_lens", _fake(3), TypeError), ("workspace", s, TypeError), ("window", -1, ValueError),
+                             ("seq_page_sizes", _fake(2, dtype=torch.int32), ValueError), ("sinks", -2, ValueError)):
+        with pytest.raises(error):
+            pkv.pkv_paged_gqa_decode_fp4(**{**good, name: bad})
+    pre = dict(good, cu_q=_fake(4, dtype=torch.int32), max_q_len=2, max_kv_len=80)
+    for name, bad, error in (("cu_q", lens, ValueError), ("cu_q", _fake(4), TypeError), ("out", z, ValueError),
+                             ("window", -1, ValueError), ("k_cache", _fake(4, 1, 16, 72, dtype=u8), ValueError)):
+        with pytest.raises(error):
+            pkv.pkv_paged_prefill_fp4(**{**pre, name: bad})
 
 
 # ---------------------------------------------------------------- the plain form
