@@ -39,6 +39,7 @@ pkv_status rows_args(Fp4RowArgs &a, const void *k, const void *v, int dtype, int
     a.v_cache = const_cast<uint8_t *>(v_cache);
     a.num_slots = num_pages * page_size;
     a.page_size = page_size;
+    a.page_log2 = 31 - __builtin_clz(static_cast<unsigned>(page_size));
     a.err = device_error;
     return PKV_OK;
 }

@@ -21,7 +21,8 @@ struct Fp4RowArgs {                                        // append and read ba
     const float *k_scale, *v_scale;
     uint8_t *k_cache, *v_cache;
     int64_t num_slots;
-    int page_size;
+    int page_size, page_log2;
+    int64_t slab;                                          // tokens of one grid row (launcher)
     int32_t *err;
 };
 

@@ -10,190 +10,260 @@
 // conversions to nearest, ties to even.  e s has 6 significant bits, so f16,
 // bf16 and fp32 all hold it exactly.
 //
-// One thread owns one block of one (token, kv head) row, of K and of V.
+// What bounds them: the bytes, 256 or 512 of the row and 72 of the cache each
+// way.  A thread owns 16 bytes of a row (8 bf16 or 4 fp32 values; a block is 2
+// or 4 neighbouring lanes), of K and of V, so a warp reads or writes 512
+// contiguous bytes of the rows an instruction; a thread with 16-value blocks
+// left half of every 32-byte sector to a second instruction and reached 3.8
+// (append and read back) and 5.0 TB/s (read back).  In calls large enough a
+// thread takes the same place in several consecutive tokens, their loads in
+// flight together.
 #include "fp4.cuh"
 
 namespace pkv {
 
 namespace {
 
-constexpr int kBlocks = kHeadDim / 16;
+constexpr int kRowThreads = 256;
 
+// The 16 bytes of a row that a thread owns, as fp32 values.
 template <bool kBf16>
-__device__ __forceinline__ void load_block(const void *base, int64_t elem, float (&x)[16])
+struct Part {
+    static constexpr int kVals = kBf16 ? 8 : 4;
+    static constexpr int kPerRow = kHeadDim / kVals;       // threads a row
+    static constexpr int kLanes = 16 / kVals;              // lanes a block
+};
+
+// Where a thread works: its token group (kTokens tokens), kv head and part.
+struct RowPlace {
+    int64_t token;
+    int h, part;
+    bool in;
+};
+
+template <bool kBf16, int kTokens>
+__device__ __forceinline__ RowPlace row_place(const Fp4RowArgs &a)
 {
-    if (kBf16) {
-        const uint4 *p = reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(base) + elem);
-        const uint4 u[2] = {__ldg(p), __ldg(p + 1)};
-        const uint32_t *w = reinterpret_cast<const uint32_t *>(u);
+    using P = Part<kBf16>;
+    RowPlace p;
+    const uint32_t i = blockIdx.x * kRowThreads + threadIdx.x;     // (a slab of tokens keeps it within 32 bits)
+    p.part = i % P::kPerRow;
+    const uint32_t row = i / P::kPerRow, g = row / static_cast<uint32_t>(a.hkv);
+    p.h = static_cast<int>(row - g * a.hkv);
+    p.token = static_cast<int64_t>(blockIdx.y) * a.slab + static_cast<int64_t>(g) * kTokens;
+    p.in = g * kTokens < a.slab && p.token < a.num_tokens;
+    return p;
+}
+
+// Byte offset of the row at `slot` in a pool: its tile, and its row in it.
+__device__ __forceinline__ int64_t slot_tile(const Fp4RowArgs &a, int64_t slot, int h, int &r)
+{
+    const int64_t page = slot >> a.page_log2;
+    r = static_cast<int>(slot & (a.page_size - 1));
+    const int64_t tile = fp4_tile_offset(page, h, r, a.hkv, a.page_size);
+    r &= 15;
+    return tile;
+}
+
+// x / d for a thread's values, correctly rounded, as E2M1 codes (4 bits each,
+// first value lowest).  With y = RN(1 / d) one Newton step on x y is a faithful
+// quotient, and a second one then is the correctly rounded one (Markstein,
+// "Computation of elementary functions on the IBM RISC System/6000", 1990), as
+// long as nothing under- or overflows: |d| in [2^-100, 2^100] and no x beyond
+// what the block's scale can hold.  What fails that is divided plainly.
+template <int kVals>
+__device__ __forceinline__ uint32_t codes_of(const float (&x)[kVals], float d, bool plain)
+{
+    float q[8];
+    if (plain) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            x[2 * i] = __uint_as_float(w[i] << 16);
-            x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-        }
+        for (int i = 0; i < kVals; ++i)
+            q[i] = __fdiv_rn(x[i], d);
     } else {
-        const float4 *p = reinterpret_cast<const float4 *>(static_cast<const float *>(base) + elem);
+        const float y = __frcp_rn(d);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float4 v = __ldg(p + i);
-            x[4 * i] = v.x;
-            x[4 * i + 1] = v.y;
-            x[4 * i + 2] = v.z;
-            x[4 * i + 3] = v.w;
+        for (int i = 0; i < kVals; ++i) {
+            const float q0 = __fmul_rn(x[i], y);
+            const float q1 = __fmaf_rn(__fmaf_rn(-q0, d, x[i]), y, q0);
+            // (the sign anew: the steps turn -0 into +0)
+            q[i] = copysignf(__fmaf_rn(__fmaf_rn(-q1, d, x[i]), y, q1), x[i]);
         }
     }
+#pragma unroll
+    for (int i = kVals; i < 8; ++i)
+        q[i] = 0.f;
+    return f32x8_to_e2m1x8(q);
 }
 
-// 16 values -> 8 bytes of codes and the scale byte.
-__device__ __forceinline__ uint2 quantise_block(const float (&x)[16], float k, uint8_t &scale)
-{
-    float amax = 0.f;
-    bool nan = false;
-#pragma unroll
-    for (int i = 0; i < 16; ++i) {
-        amax = fmaxf(amax, fabsf(x[i]));
-        nan |= x[i] != x[i];
-    }
-    scale = static_cast<uint8_t>(
-        nan ? 0x7F : __nv_cvt_float_to_fp8(__fdiv_rn(amax, 6.f * k), __NV_SATFINITE, __NV_E4M3));
-    if ((scale & 0x7F) == 0 || nan)
-        return make_uint2(0u, 0u);
-    const float step = __fmul_rn(e4m3_value(scale), k);
-    float q[2][8];
-#pragma unroll
-    for (int i = 0; i < 16; ++i)
-        q[i >> 3][i & 7] = __fdiv_rn(x[i], step);
-    return make_uint2(f32x8_to_e2m1x8(q[0]), f32x8_to_e2m1x8(q[1]));
-}
-
+// Quantises a thread's part of a row (16 bytes, with the other lanes of its
+// block) and stores codes and scale.
 template <bool kBf16>
-__global__ void __launch_bounds__(256) kv_append_fp4_kernel(const Fp4RowArgs a)
+__device__ __forceinline__ void quantise_part(uint4 u, float k, uint8_t *tile, int r, int part, bool store)
 {
-    const int64_t total = a.num_tokens * a.hkv * kBlocks;
-    for (int64_t c = blockIdx.x * static_cast<int64_t>(blockDim.x) + threadIdx.x; c < total;
-         c += static_cast<int64_t>(gridDim.x) * blockDim.x) {
-        const int part = static_cast<int>(c % kBlocks);
-        const int64_t row = c / kBlocks;
-        const int h = static_cast<int>(row % a.hkv);
-        const int64_t slot = __ldg(a.slots + row / a.hkv);
-        if (slot < 0)
-            continue;
-        if (slot >= a.num_slots) {
-            if (a.err && part == 0)
-                atomicOr(a.err, PKV_DEVERR_SLOT);
-            continue;
-        }
-        const int64_t page = slot / a.page_size;
-        const int r = static_cast<int>(slot - page * a.page_size);
-        const int64_t tile = fp4_tile_offset(page, h, r, a.hkv, a.page_size);
-        const int64_t codes = tile + (r & 15) * 64 + part * 8, scales = tile + kFp4Codes + (r & 15) * 8 + part;
-        float x[16];
-        load_block<kBf16>(a.k_in, row * kHeadDim + part * 16, x);
-        *reinterpret_cast<uint2 *>(a.k_cache + codes) = quantise_block(x, __ldg(a.k_scale + h), a.k_cache[scales]);
-        load_block<kBf16>(a.v_in, row * kHeadDim + part * 16, x);
-        *reinterpret_cast<uint2 *>(a.v_cache + codes) = quantise_block(x, __ldg(a.v_scale + h), a.v_cache[scales]);
+    using P = Part<kBf16>;
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+    float x[P::kVals];
+    uint32_t top = 0;                                      // largest |x| as its bits; a NaN's exceed all others'
+#pragma unroll
+    for (int i = 0; i < P::kVals; ++i) {
+        x[i] = __uint_as_float(kBf16 ? ((i & 1) ? w[i >> 1] & 0xFFFF0000u : w[i >> 1] << 16) : w[i & 3]);
+        top = max(top, __float_as_uint(x[i]) & 0x7FFFFFFFu);
+    }
+#pragma unroll
+    for (int o = 1; o < P::kLanes; o <<= 1)
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+    uint8_t scale = 0x7F;
+    uint32_t c = 0;
+    if (top <= 0x7F800000u) {
+        scale = static_cast<uint8_t>(
+            __nv_cvt_float_to_fp8(__fdiv_rn(__uint_as_float(top), 6.f * k), __NV_SATFINITE, __NV_E4M3));
+        const float step = __fmul_rn(e4m3_value(scale), k);
+        if (scale != 0)
+            c = codes_of<P::kVals>(x, step, scale == 0x7E || !(step >= 0x1p-100f && step <= 0x1p100f));
+    }
+    if (store) {
+        if (kBf16)
+            *reinterpret_cast<uint32_t *>(tile + r * 64 + part * 4) = c;
+        else
+            *reinterpret_cast<uint16_t *>(tile + r * 64 + part * 2) = static_cast<uint16_t>(c);
+        if (part % P::kLanes == 0)
+            tile[kFp4Codes + r * 8 + part / P::kLanes] = scale;
     }
 }
 
-// One block of a row: its 16 values times k to the output.
-template <bool kBf16>
-__device__ __forceinline__ void store_block(void *out, int64_t elem, uint2 codes, uint8_t scale, float k)
+template <bool kBf16, int kTokens>
+__global__ void __launch_bounds__(kRowThreads) kv_append_fp4_kernel(const Fp4RowArgs a)
 {
-    const float s = e4m3_value(scale);
-    float v[16];
+    using P = Part<kBf16>;
+    const RowPlace p = row_place<kBf16, kTokens>(a);
+    const float ks = __ldg(a.k_scale + p.h), vs = __ldg(a.v_scale + p.h);
+    int64_t slot[kTokens];
+    uint4 k[kTokens], v[kTokens];
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        uint32_t p[4];
-        e2m1x8_to_f16x8(i ? codes.y : codes.x, p);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const float2 f = f16x2_to_f32x2(p[j]);
-            v[8 * i + 2 * j] = f.x * s * k;                 // e s is exact: one rounding
-            v[8 * i + 2 * j + 1] = f.y * s * k;
-        }
+    for (int i = 0; i < kTokens; ++i) {
+        const int64_t t = p.token + i;
+        const bool in = p.in && t < a.num_tokens;
+        slot[i] = in ? __ldg(a.slots + t) : -1;
+        const int64_t at = (t * a.hkv + p.h) * P::kPerRow + p.part;
+        k[i] = in ? __ldg(static_cast<const uint4 *>(a.k_in) + at) : make_uint4(0, 0, 0, 0);
+        v[i] = in ? __ldg(static_cast<const uint4 *>(a.v_in) + at) : make_uint4(0, 0, 0, 0);
     }
-    if (kBf16) {
-        uint4 *p = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(out) + elem);
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            uint32_t w[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const __nv_bfloat162 b = __floats2bfloat162_rn(v[8 * i + 2 * j], v[8 * i + 2 * j + 1]);
-                w[j] = *reinterpret_cast<const uint32_t *>(&b);
-            }
-            p[i] = make_uint4(w[0], w[1], w[2], w[3]);
-        }
-    } else {
-        float4 *p = reinterpret_cast<float4 *>(static_cast<float *>(out) + elem);
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            p[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
-    }
-}
-
-template <bool kBf16>
-__global__ void __launch_bounds__(256) kv_read_fp4_kernel(const Fp4RowArgs a)
-{
-    const int64_t total = a.num_tokens * a.hkv * kBlocks;
-    for (int64_t c = blockIdx.x * static_cast<int64_t>(blockDim.x) + threadIdx.x; c < total;
-         c += static_cast<int64_t>(gridDim.x) * blockDim.x) {
-        const int part = static_cast<int>(c % kBlocks);
-        const int64_t row = c / kBlocks;
-        const int h = static_cast<int>(row % a.hkv);
-        const int64_t slot = __ldg(a.slots + row / a.hkv);
-        if (slot < 0)
-            continue;
-        const bool in = slot < a.num_slots;
-        if (!in && a.err && part == 0)
+    for (int i = 0; i < kTokens; ++i) {                    // (lanes of a block share their token, so its slot)
+        const bool store = slot[i] >= 0 && slot[i] < a.num_slots;
+        if (slot[i] >= a.num_slots && a.err && p.part == 0)
             atomicOr(a.err, PKV_DEVERR_SLOT);
-        uint2 kc = make_uint2(0u, 0u), vc = make_uint2(0u, 0u);
-        uint8_t ks = 0, vs = 0;
-        if (in) {
-            const int64_t page = slot / a.page_size;
-            const int r = static_cast<int>(slot - page * a.page_size);
-            const int64_t tile = fp4_tile_offset(page, h, r, a.hkv, a.page_size);
-            const int64_t codes = tile + (r & 15) * 64 + part * 8, scales = tile + kFp4Codes + (r & 15) * 8 + part;
-            kc = *reinterpret_cast<const uint2 *>(a.k_cache + codes);
-            vc = *reinterpret_cast<const uint2 *>(a.v_cache + codes);
-            ks = a.k_cache[scales];
-            vs = a.v_cache[scales];
-        }
-        store_block<kBf16>(a.k_out, row * kHeadDim + part * 16, kc, ks, __ldg(a.k_scale + h));
-        store_block<kBf16>(a.v_out, row * kHeadDim + part * 16, vc, vs, __ldg(a.v_scale + h));
+        int r = 0;
+        const int64_t tile = store ? slot_tile(a, slot[i], p.h, r) : 0;
+        quantise_part<kBf16>(k[i], ks, a.k_cache + tile, r, p.part, store);
+        quantise_part<kBf16>(v[i], vs, a.v_cache + tile, r, p.part, store);
     }
 }
 
-unsigned row_blocks(const Fp4RowArgs &a)
+// A thread's codes (8 or 4, lowest first) and its block's scale as 16 bytes of
+// a row.
+template <bool kBf16>
+__device__ __forceinline__ uint4 values_part(uint32_t codes, uint8_t scale, float k)
 {
-    const int64_t total = a.num_tokens * a.hkv * kBlocks;
-    int64_t blocks = (total + 255) / 256;
-    const int64_t cap = static_cast<int64_t>(device_sm_count()) * 16;
-    return static_cast<unsigned>(blocks > cap ? cap : blocks);
+    using P = Part<kBf16>;
+    const float s = e4m3_value(scale);
+    uint32_t p[4];
+    e2m1x8_to_f16x8(codes, p);
+    uint32_t w[4];
+#pragma unroll
+    for (int j = 0; j < P::kVals / 2; ++j) {
+        const float2 f = f16x2_to_f32x2(p[j]);
+        const float lo = f.x * s * k, hi = f.y * s * k;     // e s is exact: one rounding
+        if (kBf16) {
+            const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
+            w[j] = *reinterpret_cast<const uint32_t *>(&b);
+        } else {
+            w[2 * (j & 1)] = __float_as_uint(lo);
+            w[2 * (j & 1) + 1] = __float_as_uint(hi);
+        }
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+template <bool kBf16, int kTokens>
+__global__ void __launch_bounds__(kRowThreads) kv_read_fp4_kernel(const Fp4RowArgs a)
+{
+    using P = Part<kBf16>;
+    const RowPlace p = row_place<kBf16, kTokens>(a);
+    if (!p.in)
+        return;
+    const float ks = __ldg(a.k_scale + p.h), vs = __ldg(a.v_scale + p.h);
+    int64_t slot[kTokens];
+    uint32_t kc[kTokens], vc[kTokens];
+    uint8_t kb[kTokens], vb[kTokens];
+#pragma unroll
+    for (int i = 0; i < kTokens; ++i)
+        slot[i] = p.token + i < a.num_tokens ? __ldg(a.slots + p.token + i) : -1;
+#pragma unroll
+    for (int i = 0; i < kTokens; ++i) {
+        kc[i] = vc[i] = 0;
+        kb[i] = vb[i] = 0;
+        if (slot[i] >= 0 && slot[i] < a.num_slots) {
+            int r;
+            const int64_t tile = slot_tile(a, slot[i], p.h, r);
+            const int64_t at = tile + r * 64 + p.part * (P::kVals / 2), sc = tile + kFp4Codes + r * 8 + p.part / P::kLanes;
+            kc[i] = kBf16 ? *reinterpret_cast<const uint32_t *>(a.k_cache + at)
+                          : *reinterpret_cast<const uint16_t *>(a.k_cache + at);
+            vc[i] = kBf16 ? *reinterpret_cast<const uint32_t *>(a.v_cache + at)
+                          : *reinterpret_cast<const uint16_t *>(a.v_cache + at);
+            kb[i] = a.k_cache[sc];
+            vb[i] = a.v_cache[sc];
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < kTokens; ++i) {
+        if (slot[i] < 0)
+            continue;
+        if (slot[i] >= a.num_slots && a.err && p.part == 0)
+            atomicOr(a.err, PKV_DEVERR_SLOT);
+        const int64_t at = ((p.token + i) * a.hkv + p.h) * P::kPerRow + p.part;
+        static_cast<uint4 *>(a.k_out)[at] = values_part<kBf16>(kc[i], kb[i], ks);
+        static_cast<uint4 *>(a.v_out)[at] = values_part<kBf16>(vc[i], vb[i], vs);
+    }
+}
+
+typedef void (*RowKernel)(const Fp4RowArgs);
+
+// A thread takes four tokens where that still fills the GPU with threads.
+cudaError_t launch_rows(RowKernel one, RowKernel four, const Fp4RowArgs &args, cudaStream_t stream)
+{
+    if (args.num_tokens == 0)
+        return cudaSuccess;
+    Fp4RowArgs a = args;
+    const int per_row = a.bf16 ? Part<true>::kPerRow : Part<false>::kPerRow;
+    const int64_t threads = a.num_tokens * a.hkv * per_row;
+    const int tokens = threads >= static_cast<int64_t>(device_sm_count()) * 2048 * 4 ? 4 : 1;
+    // tokens a slab: its threads count in 32 bits, and whole groups
+    int64_t slab = ((int64_t(1) << 30) / (static_cast<int64_t>(a.hkv) * per_row) + tokens) / tokens * tokens;
+    if (slab > a.num_tokens)
+        slab = (a.num_tokens + tokens - 1) / tokens * tokens;
+    const int64_t slabs = (a.num_tokens + slab - 1) / slab;
+    if (slabs > 65535)
+        return cudaErrorInvalidValue;
+    a.slab = slab;
+    const int64_t blocks = (slab / tokens * a.hkv * per_row + kRowThreads - 1) / kRowThreads;
+    (tokens == 4 ? four : one)<<<dim3(static_cast<unsigned>(blocks), static_cast<unsigned>(slabs)), kRowThreads, 0,
+                                 stream>>>(a);
+    return cudaGetLastError();
 }
 
 }  // namespace
 
 cudaError_t launch_kv_append_fp4(const Fp4RowArgs &a, cudaStream_t stream)
 {
-    if (a.num_tokens == 0)
-        return cudaSuccess;
-    if (a.bf16)
-        kv_append_fp4_kernel<true><<<row_blocks(a), 256, 0, stream>>>(a);
-    else
-        kv_append_fp4_kernel<false><<<row_blocks(a), 256, 0, stream>>>(a);
-    return cudaGetLastError();
+    return a.bf16 ? launch_rows(kv_append_fp4_kernel<true, 1>, kv_append_fp4_kernel<true, 4>, a, stream)
+                  : launch_rows(kv_append_fp4_kernel<false, 1>, kv_append_fp4_kernel<false, 4>, a, stream);
 }
 
 cudaError_t launch_kv_read_fp4(const Fp4RowArgs &a, cudaStream_t stream)
 {
-    if (a.num_tokens == 0)
-        return cudaSuccess;
-    if (a.bf16)
-        kv_read_fp4_kernel<true><<<row_blocks(a), 256, 0, stream>>>(a);
-    else
-        kv_read_fp4_kernel<false><<<row_blocks(a), 256, 0, stream>>>(a);
-    return cudaGetLastError();
+    return a.bf16 ? launch_rows(kv_read_fp4_kernel<true, 1>, kv_read_fp4_kernel<true, 4>, a, stream)
+                  : launch_rows(kv_read_fp4_kernel<false, 1>, kv_read_fp4_kernel<false, 4>, a, stream);
 }
 
 }  // namespace pkv
