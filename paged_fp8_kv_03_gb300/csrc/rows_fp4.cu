@@ -11,13 +11,14 @@
 // bf16 and fp32 all hold it exactly.
 //
 // What bounds them: the bytes, 256 or 512 of the row and 72 of the cache each
-// way.  A thread owns 16 bytes of a row (8 bf16 or 4 fp32 values; a block is 2
-// or 4 neighbouring lanes), of K and of V, so a warp reads or writes 512
-// contiguous bytes of the rows an instruction; a thread with 16-value blocks
-// left half of every 32-byte sector to a second instruction and reached 3.8
-// (append and read back) and 5.0 TB/s (read back).  In calls large enough a
-// thread takes the same place in several consecutive tokens, their loads in
-// flight together.
+// way.  Reading back, a thread owns 16 bytes of a row (8 bf16 or 4 fp32
+// values), of K and of V, so a warp writes 512 contiguous bytes an instruction
+// (with 32 a thread, half of every sector waits for a second instruction: 5.0
+// instead of 6.2 TB/s).  Appending, it owns 32 bytes (16 or 8 values; a block is
+// one or two lanes), because what a block's scale costs is paid once a thread
+// and instructions, not bytes, are the limit.  In calls large enough a thread
+// takes the same place in several consecutive tokens, their loads in flight
+// together.
 #include "fp4.cuh"
 
 namespace pkv {
@@ -26,10 +27,10 @@ namespace {
 
 constexpr int kRowThreads = 256;
 
-// The 16 bytes of a row that a thread owns, as fp32 values.
-template <bool kBf16>
+// The bytes of a row that a thread owns.
+template <bool kBf16, int kBytes>
 struct Part {
-    static constexpr int kVals = kBf16 ? 8 : 4;
+    static constexpr int kVals = kBytes / (kBf16 ? 2 : 4);
     static constexpr int kPerRow = kHeadDim / kVals;       // threads a row
     static constexpr int kLanes = 16 / kVals;              // lanes a block
 };
@@ -41,10 +42,9 @@ struct RowPlace {
     bool in;
 };
 
-template <bool kBf16, int kTokens>
+template <typename P, int kTokens>
 __device__ __forceinline__ RowPlace row_place(const Fp4RowArgs &a)
 {
-    using P = Part<kBf16>;
     RowPlace p;
     const uint32_t i = blockIdx.x * kRowThreads + threadIdx.x;     // (a slab of tokens keeps it within 32 bits)
     p.part = i % P::kPerRow;
@@ -65,67 +65,103 @@ __device__ __forceinline__ int64_t slot_tile(const Fp4RowArgs &a, int64_t slot, 
     return tile;
 }
 
-// x / d for a thread's values, correctly rounded, as E2M1 codes (4 bits each,
-// first value lowest).  With y = RN(1 / d) one Newton step on x y is a faithful
-// quotient, and a second one then is the correctly rounded one (Markstein,
-// "Computation of elementary functions on the IBM RISC System/6000", 1990), as
-// long as nothing under- or overflows: |d| in [2^-100, 2^100] and no x beyond
-// what the block's scale can hold.  What fails that is divided plainly.
-template <int kVals>
-__device__ __forceinline__ uint32_t codes_of(const float (&x)[kVals], float d, bool plain)
+// x / d correctly rounded, from y = RN(1 / d): one Newton step on x y gives a
+// faithful quotient, and a second one then the correctly rounded one
+// (Markstein, "Computation of elementary functions on the IBM RISC System/6000",
+// 1990), as long as nothing under- or overflows.  (Remainders with the sign
+// turned: that way -0 stays -0.)
+__device__ __forceinline__ float divide(float x, float d, float y)
 {
-    float q[8];
-    if (plain) {
-#pragma unroll
-        for (int i = 0; i < kVals; ++i)
-            q[i] = __fdiv_rn(x[i], d);
-    } else {
-        const float y = __frcp_rn(d);
-#pragma unroll
-        for (int i = 0; i < kVals; ++i) {
-            const float q0 = __fmul_rn(x[i], y);
-            const float q1 = __fmaf_rn(__fmaf_rn(-q0, d, x[i]), y, q0);
-            // (the sign anew: the steps turn -0 into +0)
-            q[i] = copysignf(__fmaf_rn(__fmaf_rn(-q1, d, x[i]), y, q1), x[i]);
-        }
-    }
-#pragma unroll
-    for (int i = kVals; i < 8; ++i)
-        q[i] = 0.f;
-    return f32x8_to_e2m1x8(q);
+    const float q0 = __fmul_rn(x, y);
+    const float q1 = __fmaf_rn(-__fmaf_rn(q0, d, -x), y, q0);
+    return __fmaf_rn(-__fmaf_rn(q1, d, -x), y, q1);
 }
 
-// Quantises a thread's part of a row (16 bytes, with the other lanes of its
-// block) and stores codes and scale.
-template <bool kBf16>
-__device__ __forceinline__ void quantise_part(uint4 u, float k, uint8_t *tile, int r, int part, bool store)
+// A kv head's scale k and what quantising divides by: 6 k.
+struct HeadScale {
+    float k, k6, inv_k6;
+    bool plain;                                            // out of the range in which divide() is safe
+};
+
+__device__ __forceinline__ HeadScale head_scale(float k)
 {
-    using P = Part<kBf16>;
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-    float x[P::kVals];
-    uint32_t top = 0;                                      // largest |x| as its bits; a NaN's exceed all others'
+    HeadScale h;
+    h.k = k;
+    h.k6 = __fmul_rn(6.f, k);
+    h.inv_k6 = __frcp_rn(h.k6);
+    h.plain = !(k >= 0x1p-60f && k <= 0x1p60f);
+    return h;
+}
+
+__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b)
+{
+    uint32_t d;
+    asm("max.u16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+}
+
+// Quantises a thread's part of a row (32 bytes; fp32: with the neighbouring
+// lane that has the block's other half) and stores codes and scale.
+template <bool kBf16>
+__device__ __forceinline__ void quantise_part(const uint4 (&u)[2], const HeadScale &hs, uint8_t *tile, int r, int part,
+                                              bool store)
+{
+    using P = Part<kBf16, 32>;
+    const uint32_t w[8] = {u[0].x, u[0].y, u[0].z, u[0].w, u[1].x, u[1].y, u[1].z, u[1].w};
+    uint32_t m[8], top;                                    // largest |x| as its bits; a NaN's exceed all others'
 #pragma unroll
-    for (int i = 0; i < P::kVals; ++i) {
-        x[i] = __uint_as_float(kBf16 ? ((i & 1) ? w[i >> 1] & 0xFFFF0000u : w[i >> 1] << 16) : w[i & 3]);
-        top = max(top, __float_as_uint(x[i]) & 0x7FFFFFFFu);
-    }
+    for (int i = 0; i < 8; ++i)
+        m[i] = w[i] & (kBf16 ? 0x7FFF7FFFu : 0x7FFFFFFFu);
 #pragma unroll
-    for (int o = 1; o < P::kLanes; o <<= 1)
-        top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+    for (int n = 4; n > 0; n >>= 1)
+#pragma unroll
+        for (int i = 0; i < n; ++i)
+            m[i] = kBf16 ? max_u16x2(m[i], m[i + n]) : max(m[i], m[i + n]);
+    if (kBf16)
+        top = max_u16x2(m[0], m[0] << 16) & 0xFFFF0000u;
+    else
+        top = max(m[0], __shfl_xor_sync(0xffffffffu, m[0], 1));
+    const float amax = __uint_as_float(top);
     uint8_t scale = 0x7F;
-    uint32_t c = 0;
+    uint32_t c[2] = {0u, 0u};
     if (top <= 0x7F800000u) {
-        scale = static_cast<uint8_t>(
-            __nv_cvt_float_to_fp8(__fdiv_rn(__uint_as_float(top), 6.f * k), __NV_SATFINITE, __NV_E4M3));
-        const float step = __fmul_rn(e4m3_value(scale), k);
-        if (scale != 0)
-            c = codes_of<P::kVals>(x, step, scale == 0x7E || !(step >= 0x1p-100f && step <= 0x1p100f));
+        // (amax = Inf, or a quotient past the largest fp32, is beyond divide(); a
+        // subnormal amax gives scale 0 either way)
+        const bool huge = hs.plain || !(amax < 0x1p60f);
+        float ratio;
+        if (huge)
+            ratio = __fdiv_rn(amax, hs.k6);
+        else
+            ratio = divide(amax, hs.k6, hs.inv_k6);
+        scale = static_cast<uint8_t>(__nv_cvt_float_to_fp8(ratio, __NV_SATFINITE, __NV_E4M3));
+        const float step = __fmul_rn(e4m3_value(scale), hs.k);
+        float q[2][8];
+        auto value = [&](int i) {
+            return __uint_as_float(kBf16 ? ((i & 1) ? w[i >> 1] & 0xFFFF0000u : w[i >> 1] << 16) : w[i & 7]);
+        };
+        if (huge || scale == 0x7E) {                       // a saturated scale: x / step may be anything
+#pragma unroll 1
+            for (int i = 0; i < P::kVals; i += 8) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    q[0][j] = __fdiv_rn(i ? value(j + P::kVals - 8) : value(j), step);
+                c[i >> 3] = f32x8_to_e2m1x8(q[0]);
+            }
+        } else if (scale != 0) {
+            const float y = __frcp_rn(step);
+#pragma unroll
+            for (int i = 0; i < P::kVals; ++i)
+                q[i >> 3][i & 7] = divide(value(i), step, y);
+#pragma unroll
+            for (int i = 0; i < P::kVals / 8; ++i)
+                c[i] = f32x8_to_e2m1x8(q[i]);
+        }
     }
     if (store) {
         if (kBf16)
-            *reinterpret_cast<uint32_t *>(tile + r * 64 + part * 4) = c;
+            *reinterpret_cast<uint2 *>(tile + r * 64 + part * 8) = make_uint2(c[0], c[1]);
         else
-            *reinterpret_cast<uint16_t *>(tile + r * 64 + part * 2) = static_cast<uint16_t>(c);
+            *reinterpret_cast<uint32_t *>(tile + r * 64 + part * 4) = c[0];
         if (part % P::kLanes == 0)
             tile[kFp4Codes + r * 8 + part / P::kLanes] = scale;
     }
@@ -134,19 +170,22 @@ __device__ __forceinline__ void quantise_part(uint4 u, float k, uint8_t *tile, i
 template <bool kBf16, int kTokens>
 __global__ void __launch_bounds__(kRowThreads) kv_append_fp4_kernel(const Fp4RowArgs a)
 {
-    using P = Part<kBf16>;
-    const RowPlace p = row_place<kBf16, kTokens>(a);
-    const float ks = __ldg(a.k_scale + p.h), vs = __ldg(a.v_scale + p.h);
+    using P = Part<kBf16, 32>;
+    const RowPlace p = row_place<P, kTokens>(a);
+    const HeadScale ks = head_scale(__ldg(a.k_scale + p.h)), vs = head_scale(__ldg(a.v_scale + p.h));
     int64_t slot[kTokens];
-    uint4 k[kTokens], v[kTokens];
+    uint4 k[kTokens][2], v[kTokens][2];
 #pragma unroll
     for (int i = 0; i < kTokens; ++i) {
         const int64_t t = p.token + i;
         const bool in = p.in && t < a.num_tokens;
         slot[i] = in ? __ldg(a.slots + t) : -1;
-        const int64_t at = (t * a.hkv + p.h) * P::kPerRow + p.part;
-        k[i] = in ? __ldg(static_cast<const uint4 *>(a.k_in) + at) : make_uint4(0, 0, 0, 0);
-        v[i] = in ? __ldg(static_cast<const uint4 *>(a.v_in) + at) : make_uint4(0, 0, 0, 0);
+        const int64_t at = ((t * a.hkv + p.h) * P::kPerRow + p.part) * 2;
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            k[i][j] = in ? __ldg(static_cast<const uint4 *>(a.k_in) + at + j) : make_uint4(0, 0, 0, 0);
+            v[i][j] = in ? __ldg(static_cast<const uint4 *>(a.v_in) + at + j) : make_uint4(0, 0, 0, 0);
+        }
     }
 #pragma unroll
     for (int i = 0; i < kTokens; ++i) {                    // (lanes of a block share their token, so its slot)
@@ -165,7 +204,7 @@ __global__ void __launch_bounds__(kRowThreads) kv_append_fp4_kernel(const Fp4Row
 template <bool kBf16>
 __device__ __forceinline__ uint4 values_part(uint32_t codes, uint8_t scale, float k)
 {
-    using P = Part<kBf16>;
+    using P = Part<kBf16, 16>;
     const float s = e4m3_value(scale);
     uint32_t p[4];
     e2m1x8_to_f16x8(codes, p);
@@ -188,8 +227,8 @@ __device__ __forceinline__ uint4 values_part(uint32_t codes, uint8_t scale, floa
 template <bool kBf16, int kTokens>
 __global__ void __launch_bounds__(kRowThreads) kv_read_fp4_kernel(const Fp4RowArgs a)
 {
-    using P = Part<kBf16>;
-    const RowPlace p = row_place<kBf16, kTokens>(a);
+    using P = Part<kBf16, 16>;
+    const RowPlace p = row_place<P, kTokens>(a);
     if (!p.in)
         return;
     const float ks = __ldg(a.k_scale + p.h), vs = __ldg(a.v_scale + p.h);
@@ -229,15 +268,15 @@ __global__ void __launch_bounds__(kRowThreads) kv_read_fp4_kernel(const Fp4RowAr
 
 typedef void (*RowKernel)(const Fp4RowArgs);
 
-// A thread takes four tokens where that still fills the GPU with threads.
-cudaError_t launch_rows(RowKernel one, RowKernel four, const Fp4RowArgs &args, cudaStream_t stream)
+// A thread takes `most` tokens where that still fills the GPU with threads.
+cudaError_t launch_rows(RowKernel one, RowKernel many, int most, int per_row, const Fp4RowArgs &args,
+                        cudaStream_t stream)
 {
     if (args.num_tokens == 0)
         return cudaSuccess;
     Fp4RowArgs a = args;
-    const int per_row = a.bf16 ? Part<true>::kPerRow : Part<false>::kPerRow;
     const int64_t threads = a.num_tokens * a.hkv * per_row;
-    const int tokens = threads >= static_cast<int64_t>(device_sm_count()) * 2048 * 4 ? 4 : 1;
+    const int tokens = threads >= static_cast<int64_t>(device_sm_count()) * 2048 * most ? most : 1;
     // tokens a slab: its threads count in 32 bits, and whole groups
     int64_t slab = ((int64_t(1) << 30) / (static_cast<int64_t>(a.hkv) * per_row) + tokens) / tokens * tokens;
     if (slab > a.num_tokens)
@@ -247,8 +286,8 @@ cudaError_t launch_rows(RowKernel one, RowKernel four, const Fp4RowArgs &args, c
         return cudaErrorInvalidValue;
     a.slab = slab;
     const int64_t blocks = (slab / tokens * a.hkv * per_row + kRowThreads - 1) / kRowThreads;
-    (tokens == 4 ? four : one)<<<dim3(static_cast<unsigned>(blocks), static_cast<unsigned>(slabs)), kRowThreads, 0,
-                                 stream>>>(a);
+    (tokens > 1 ? many : one)<<<dim3(static_cast<unsigned>(blocks), static_cast<unsigned>(slabs)), kRowThreads, 0,
+                                stream>>>(a);
     return cudaGetLastError();
 }
 
@@ -256,14 +295,18 @@ cudaError_t launch_rows(RowKernel one, RowKernel four, const Fp4RowArgs &args, c
 
 cudaError_t launch_kv_append_fp4(const Fp4RowArgs &a, cudaStream_t stream)
 {
-    return a.bf16 ? launch_rows(kv_append_fp4_kernel<true, 1>, kv_append_fp4_kernel<true, 4>, a, stream)
-                  : launch_rows(kv_append_fp4_kernel<false, 1>, kv_append_fp4_kernel<false, 4>, a, stream);
+    return a.bf16 ? launch_rows(kv_append_fp4_kernel<true, 1>, kv_append_fp4_kernel<true, 2>, 2,
+                                Part<true, 32>::kPerRow, a, stream)
+                  : launch_rows(kv_append_fp4_kernel<false, 1>, kv_append_fp4_kernel<false, 2>, 2,
+                                Part<false, 32>::kPerRow, a, stream);
 }
 
 cudaError_t launch_kv_read_fp4(const Fp4RowArgs &a, cudaStream_t stream)
 {
-    return a.bf16 ? launch_rows(kv_read_fp4_kernel<true, 1>, kv_read_fp4_kernel<true, 4>, a, stream)
-                  : launch_rows(kv_read_fp4_kernel<false, 1>, kv_read_fp4_kernel<false, 4>, a, stream);
+    return a.bf16 ? launch_rows(kv_read_fp4_kernel<true, 1>, kv_read_fp4_kernel<true, 4>, 4,
+                                Part<true, 16>::kPerRow, a, stream)
+                  : launch_rows(kv_read_fp4_kernel<false, 1>, kv_read_fp4_kernel<false, 4>, 4,
+                                Part<false, 16>::kPerRow, a, stream);
 }
 
 }  // namespace pkv
