@@ -19,7 +19,7 @@ LIB_DIR = os.path.join(PKG, "lib")
 LIB = os.path.join(LIB_DIR, "libpagedfp8.so")
 
 SOURCES = ["append.cu", "decode.cu", "api.cu", "noalloc.cu", "calibrate.cu", "prefill.cu",
-           "rows_fp4.cu", "decode_fp4.cu", "api_fp4.cu"]
+           "rows_fp4.cu", "prefill_fp4.cu", "decode_fp4.cu", "api_fp4.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",
          "--expt-relaxed-constexpr"]

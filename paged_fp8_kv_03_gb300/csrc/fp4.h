@@ -101,6 +101,8 @@ inline size_t prefill_fp4_bytes(int batch, long long rows)
 size_t decode_fp4_smem(int batch);
 const void *decode_fp4_kernel(bool two_parts);
 cudaError_t launch_paged_decode_fp4(const Fp4DecodeArgs &da, int ctas, cudaStream_t stream, const char **site);
+cudaError_t launch_prefill_pair(const PrefillArgs &a, const Fp4Window &win, const CUtensorMap &tm_q,
+                                const CUtensorMap &tm_k16, const CUtensorMap &tm_v16, cudaStream_t stream);
 cudaError_t launch_kv_append_fp4(const Fp4RowArgs &a, cudaStream_t stream);
 cudaError_t launch_kv_read_fp4(const Fp4RowArgs &a, cudaStream_t stream);
 cudaError_t launch_paged_prefill_fp4(const PrefillArgs &a, const Fp4Window &win, const CUtensorMap &tm_q,

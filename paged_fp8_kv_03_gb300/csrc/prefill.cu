@@ -55,23 +55,18 @@
 #include <mutex>
 
 #include "context.h"
-#include "fp4.cuh"
-#include "tcgen05.cuh"
+#include "prefill.cuh"
 
 namespace pkv {
 
 namespace {
 
-constexpr int kRows = 128;                       // M: rows of a query tile
-constexpr int kKeys = 128;                       // keys per tile
 constexpr int kKStages = 2, kVStages = 3;        // operand rings: K bf16, V f16
 constexpr int kFold = 32;                        // key tiles per tensor-core accumulation segment of O
 constexpr int kSmWarp0 = 2;                      // first softmax warp
 constexpr int kSmWarps = 8;
 constexpr int kPThreads = 32 * (kSmWarp0 + kSmWarps);
 constexpr uint32_t kColO = 256, kColM = 384;     // TMEM columns: S/P 0-255, O of the segment 256-383, O 384-511
-constexpr uint64_t kWaitNs = 2000000000ull;
-constexpr unsigned kAll = 0xffffffffu;
 static_assert(kSmWarps == 8, "two softmax warps per TMEM lane quarter");
 
 // Shared memory, offsets from a 1024-byte aligned base.  Operand tiles are
@@ -99,206 +94,12 @@ struct PS {
 };
 static_assert(PS::bytes() <= 232448, "prefill tile buffers exceed the shared memory of one CTA");
 
-// Bounded wait, one thread.  honour_abort = false for drains.
-__device__ __forceinline__ bool pwait(uint32_t bar, uint32_t parity, volatile int *abort_flag, int32_t *err,
-                                      bool honour_abort = true)
-{
-    if (mbar_try_wait(bar, parity))
-        return true;
-    const uint64_t t0 = global_timer_ns();
-    for (uint32_t it = 1;; ++it) {
-        if (mbar_try_wait(bar, parity))
-            return true;
-        if ((it & 15u) == 0) {
-            if (honour_abort && *abort_flag)
-                return false;
-            if (global_timer_ns() - t0 > kWaitNs) {
-                *abort_flag = 1;
-                if (err)
-                    atomicOr(err, PKV_DEVERR_TIMEOUT);
-                return false;
-            }
-        }
-    }
-}
-
-// Bounded wait by a whole warp; the result is warp-uniform.
-__device__ __forceinline__ bool wwait(uint32_t bar, uint32_t parity, volatile int *abort_flag, int32_t *err,
-                                      int lane)
-{
-    uint64_t t0 = 0;
-    for (uint32_t it = 0;; ++it) {
-        if (__all_sync(kAll, mbar_try_wait(bar, parity)))
-            return true;
-        if ((it & 15u) == 15u) {
-            int stop = 0;
-            if (lane == 0) {
-                if (*abort_flag) {
-                    stop = 1;
-                } else if (t0 == 0) {
-                    t0 = global_timer_ns();
-                } else if (global_timer_ns() - t0 > kWaitNs) {
-                    *abort_flag = 1;
-                    if (err)
-                        atomicOr(err, PKV_DEVERR_TIMEOUT);
-                    stop = 1;
-                }
-            }
-            if (__shfl_sync(kAll, stop, 0))
-                return false;
-        }
-    }
-}
-
-// Descriptors are built once per ring stage; a K step then only advances the
-// start-address field (bytes / 16, the low bits of the descriptor), so the
-// issuing thread spends its time issuing, not rebuilding 64-bit descriptors.
-// K-major operand (128 rows x 128 dims, 128B swizzle; the query tile as A and
-// a K tile as B of S = Q K^T): K step s of 16 dims starts (s / 4) * 16 KB +
-// (s % 4) * 32 B into the tile.
-__device__ __forceinline__ uint64_t kmajor_base(uint32_t tile)
-{
-    return tc::smem_desc_sw128(tile, 16, 1024);
-}
-__device__ __forceinline__ uint64_t kmajor_step(uint64_t base, int s)
-{
-    return base + static_cast<uint64_t>(((s >> 2) * 16384 + (s & 3) * 32) >> 4);
-}
-
-// V as the B operand of O += P V: rows = keys (the K dimension), 128 dims (N)
-// contiguous in two 64-dim column blocks 16 KB apart; K step s = keys 16s..16s+15
-// starts s * 2 KB into the tile.
-__device__ __forceinline__ uint64_t vmn_base(uint32_t tile)
-{
-    return tc::smem_desc_sw128(tile, 16384, 1024);
-}
-__device__ __forceinline__ uint64_t vmn_step(uint64_t base, int s)
-{
-    return base + static_cast<uint64_t>((s * 2048) >> 4);
-}
-
 // f16 pair -> bf16 pair (exact for widened E4M3 values: 3 mantissa bits).
 __device__ __forceinline__ uint32_t f16x2_to_bf16x2(uint32_t h)
 {
     const float2 f = f16x2_to_f32x2(h);
     __nv_bfloat162 b = __floats2bfloat162_rn(f.x, f.y);
     return *reinterpret_cast<uint32_t *>(&b);
-}
-
-// P = 2^(x - m) as two f16 parts: hi = P with its low 13 mantissa bits cleared
-// (exact in f16 for P >= 2^-14), lo = the rest (exact in fp32, rounded to f16).
-// hi + lo equals P to about 2^-22 relative; below 2^-14 the parts keep an
-// absolute error under 2^-24.
-__device__ __forceinline__ void split_pair(float p0, float p1, uint32_t &hi, uint32_t &lo)
-{
-    const float h0 = __uint_as_float(__float_as_uint(p0) & 0xFFFFE000u);
-    const float h1 = __uint_as_float(__float_as_uint(p1) & 0xFFFFE000u);
-    hi = f32x2_to_f16x2(h0, h1);
-    lo = f32x2_to_f16x2(p0 - h0, p1 - h1);
-}
-
-// Packed pairs of fp32 (one 64-bit register pair): the paired add and fma
-// run two lanes of fp32 arithmetic per instruction, each rounded exactly as
-// the scalar operation, so results equal the scalar code bit for bit.
-__device__ __forceinline__ uint64_t f2_pack(float a, float b)
-{
-    uint64_t r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
-    return r;
-}
-
-__device__ __forceinline__ float2 f2_unpack(uint64_t r)
-{
-    float2 v;
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(v.x), "=f"(v.y) : "l"(r));
-    return v;
-}
-
-__device__ __forceinline__ uint64_t f2_add(uint64_t a, uint64_t b)
-{
-    uint64_t d;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-    return d;
-}
-
-__device__ __forceinline__ uint64_t f2_sub(uint64_t a, uint64_t b)
-{
-    uint64_t d;
-    asm("sub.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-    return d;
-}
-
-__device__ __forceinline__ uint64_t f2_fma(uint64_t a, uint64_t b, uint64_t c)
-{
-    uint64_t d;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
-    return d;
-}
-
-// max(a, b, c) in one instruction (exact, like two fmaxf).
-__device__ __forceinline__ float max3(float a, float b, float c)
-{
-    float d;
-    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
-    return d;
-}
-
-// True in exactly one lane of the (converged) warp.
-__device__ __forceinline__ bool elect_one()
-{
-    uint32_t p;
-    asm volatile(
-        "{\n\t.reg .pred e;\n\t"
-        "elect.sync _|e, 0xffffffff;\n\t"
-        "selp.u32 %0, 1, 0, e;\n\t}"
-        : "=r"(p));
-    return p != 0;
-}
-
-// Checks a sequence's sizes; false (and PKV_DEVERR_SEQLEN when `report`) when
-// the chunk or its length are inconsistent.
-__device__ __forceinline__ bool sequence_ok(const PrefillArgs &a, int b, int q0, int q1, int L, bool report)
-{
-    const int n = q1 - q0;
-    const int lp = seq_page_log2(a, b);
-    const bool ok = q0 >= 0 && n >= 0 && q1 <= a.total_q && n <= a.max_q_len && L >= n && L <= a.max_kv_len &&
-                    lp >= 0 && static_cast<int64_t>(L) <= (static_cast<int64_t>(a.max_pages) << lp);
-    if (!ok && report && a.err)
-        atomicOr(a.err, lp < 0 ? PKV_DEVERR_PAGESIZE : PKV_DEVERR_SEQLEN);
-    return ok;
-}
-
-// Key tiles of a sequence that some query of its chunk sees, under a window of
-// the 4-bit cache's calls: tiles 0 .. first - 1 (sinks) and then first + skip ..
-// (keys from `from` on).  Without a window: all of them (first = skip = 0).
-struct KeyTiles {
-    int from, sinks;                                     // keys t >= from or t < sinks are seen by someone
-    int first, skip;
-};
-
-template <bool kWin>
-__device__ __forceinline__ KeyTiles key_tiles(const Fp4Window &w, int first_pos)
-{
-    KeyTiles k = {0, 0, 0, 0};
-    if (kWin && w.window > 0) {
-        k.from = max(0, first_pos - w.window + 1);
-        k.sinks = min(w.sinks, k.from);
-        k.first = (k.sinks + kKeys - 1) / kKeys;
-        k.skip = max(k.from / kKeys, k.first) - k.first;
-    }
-    return k;
-}
-
-// 128-row tiles of sequence b's widened region (all its kv heads): zero for a
-// sequence with an empty or inconsistent chunk.
-template <bool kWin>
-__device__ __forceinline__ long long region_tiles(const PrefillArgs &a, const Fp4Window &w, int b)
-{
-    const int q0 = __ldg(a.cu_q + b), q1 = __ldg(a.cu_q + b + 1);
-    const int L = __ldg(a.seq_lens + b);
-    if (q1 - q0 <= 0 || !sequence_ok(a, b, q0, q1, L, false))
-        return 0;
-    return static_cast<long long>(a.hkv) * ((L + kKeys - 1) / kKeys - key_tiles<kWin>(w, L - (q1 - q0)).skip);
 }
 
 // ---------------------------------------------------------------------- widening
@@ -444,13 +245,10 @@ __global__ void __launch_bounds__(256) kv_widen_kernel(const PrefillArgs a, cons
 }
 
 // ---------------------------------------------------------------------- attention
-// kParts: f16 parts of P.  Two for the FP8 cache and for fp32 outputs; one, and
-// half the PV products, for bf16 outputs over the 4-bit cache: P loses its low
-// 13 mantissa bits, and so does the sum that normalises it, which leaves at
-// most 2^-11 of the largest |v - o| against a bf16 output's 2^-8.
-// kWin: the calls with a window; a row may then see nothing of a tile, or of
-// all tiles so far (its running maximum is -inf until it does).
-template <int kParts, bool kWin>
+// kWin: the 4-bit cache's calls with a window (and an fp32 output); a row may
+// then see nothing of a tile, or of all tiles so far (its running maximum is
+// -inf until it does).
+template <bool kWin>
 __global__ void __launch_bounds__(kPThreads, 1)
     paged_prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                          const __grid_constant__ CUtensorMap tm_v, const PrefillArgs a, const Fp4Window win)
@@ -639,7 +437,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
                         tc::mma_ts(o_tm, p_tm + 32 * (s >> 1) + 8 * (s & 1), vmn_step(vd, s), id_pv,
                                    s > 0 ? 1u : acc0);
 #pragma unroll
-                    for (int s = 0; s < (kParts == 2 ? 8 : 0); ++s)
+                    for (int s = 0; s < 8; ++s)
                         tc::mma_ts(o_tm, p_tm + 32 * (s >> 1) + 8 * (s & 1) + 16, vmn_step(vd, s), id_pv, 1u);
                     tc::commit(bar_ptr + PS::PV_DONE);
                     tc::commit(bar_ptr + PS::V_EMPTY + vs);
@@ -714,7 +512,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
                         if (32 * c + k > vis)
                             x[c][k] = __float_as_uint(-INFINITY);
             }
-            if (kWin && win.window > 0) {
+            if (kWin) {
                 // keys before the window and behind the sinks
                 const int out = vis - win.window, snk = win.sinks - key0;
                 if (out >= 0 && snk < 64) {
@@ -755,22 +553,18 @@ __global__ void __launch_bounds__(kPThreads, 1)
                             f2_fma(f2_pack(__uint_as_float(x[c][2 * q]), __uint_as_float(x[c][2 * q + 1])), sl2x2, nmm));
                         const float p0 = ex2_approx(y.x), p1 = ex2_approx(y.y);
                         const uint64_t pp = f2_pack(p0, p1);
-                        if (kParts == 2)
-                            ls[q & 3] = f2_add(ls[q & 3], pp);
-                        // hi = P with its low 13 mantissa bits cleared, lo = the rest (split_pair)
+                        ls[q & 3] = f2_add(ls[q & 3], pp);
+                        // hi = P with its low 13 mantissa bits cleared (exact in f16 for P >= 2^-14), lo = the
+                        // rest (exact in fp32, rounded to f16): hi + lo equals P to about 2^-22 relative; below
+                        // 2^-14 the parts keep an absolute error under 2^-24
                         const float h0 = __uint_as_float(__float_as_uint(p0) & 0xFFFFE000u);
                         const float h1 = __uint_as_float(__float_as_uint(p1) & 0xFFFFE000u);
                         ph[q] = f32x2_to_f16x2(h0, h1);
-                        if (kParts == 2) {
-                            const float2 r = f2_unpack(f2_sub(pp, f2_pack(h0, h1)));
-                            pl[q] = f32x2_to_f16x2(r.x, r.y);
-                        } else {
-                            ls[q & 3] = f2_add(ls[q & 3], f2_pack(h0, h1));
-                        }
+                        const float2 r = f2_unpack(f2_sub(pp, f2_pack(h0, h1)));
+                        pl[q] = f32x2_to_f16x2(r.x, r.y);
                     }
                     tc::st16(s_tm + 32 * c, ph);
-                    if (kParts == 2)
-                        tc::st16(s_tm + 32 * c + 16, pl);
+                    tc::st16(s_tm + 32 * c + 16, pl);
                 }
                 const float2 s0 = f2_unpack(ls[0]), s1 = f2_unpack(ls[1]), s2 = f2_unpack(ls[2]), s3 = f2_unpack(ls[3]);
                 return ((s0.x + s0.y) + (s1.x + s1.y)) + ((s2.x + s2.y) + (s3.x + s3.y));
@@ -911,7 +705,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
 }
 
 std::mutex g_prefill_mu;
-unsigned long long g_prefill_attr_ctx[64][5] = {};   // per device and kernel: the context its limit was raised in
+unsigned long long g_prefill_attr_ctx[64][2] = {};   // per device and kernel: the context its limit was raised in
 
 typedef void (*PrefillKernel)(const CUtensorMap, const CUtensorMap, const CUtensorMap, const PrefillArgs,
                               const Fp4Window);
@@ -936,17 +730,10 @@ cudaError_t raise_limit(PrefillKernel kernel, int which)
     return cudaSuccess;
 }
 
+// The widening launch.
 template <bool kFp4>
-cudaError_t launch_prefill(PrefillKernel kernel, int which, const PrefillArgs &a, const Fp4Window &win,
-                           const CUtensorMap &tm_q, const CUtensorMap &tm_k16, const CUtensorMap &tm_v16,
-                           cudaStream_t stream)
+cudaError_t launch_widen(const PrefillArgs &a, const Fp4Window &win, cudaStream_t stream)
 {
-    const int64_t grid = static_cast<int64_t>(a.batch) * a.hkv * a.max_tiles;
-    if (grid <= 0)
-        return cudaSuccess;
-    cudaError_t e = raise_limit(kernel, which);
-    if (e != cudaSuccess)
-        return e;
     const int64_t pieces = a.rows_cap * 8;
     int64_t wblocks = (pieces + 255) / 256;
     const int64_t cap = static_cast<int64_t>(device_sm_count()) * 16;
@@ -956,13 +743,22 @@ cudaError_t launch_prefill(PrefillKernel kernel, int which, const PrefillArgs &a
         wblocks = 1;                                     // CTA 0 always lays out the regions
     const size_t wsmem = (static_cast<size_t>(a.batch) + 1 + 8) * sizeof(int);
     if (wsmem > 48 * 1024) {
-        e = cudaFuncSetAttribute(kv_widen_kernel<kFp4>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 static_cast<int>(wsmem));
+        const cudaError_t e = cudaFuncSetAttribute(kv_widen_kernel<kFp4>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                   static_cast<int>(wsmem));
         if (e != cudaSuccess)
             return e;
     }
     kv_widen_kernel<kFp4><<<static_cast<unsigned>(wblocks), 256, wsmem, stream>>>(a, win);
-    kernel<<<static_cast<unsigned>(grid), kPThreads, PS::bytes(), stream>>>(tm_q, tm_k16, tm_v16, a, win);
+    return cudaGetLastError();
+}
+
+template <bool kWin>
+cudaError_t launch_attention(const PrefillArgs &a, const Fp4Window &win, const CUtensorMap &tm_q,
+                             const CUtensorMap &tm_k16, const CUtensorMap &tm_v16, cudaStream_t stream)
+{
+    const int64_t grid = static_cast<int64_t>(a.batch) * a.hkv * a.max_tiles;
+    paged_prefill_kernel<kWin><<<static_cast<unsigned>(grid), kPThreads, PS::bytes(), stream>>>(tm_q, tm_k16, tm_v16, a,
+                                                                                               win);
     return cudaGetLastError();
 }
 
@@ -976,17 +772,31 @@ size_t prefill_smem_bytes()
 cudaError_t launch_paged_prefill(const PrefillArgs &a, const CUtensorMap &tm_q, const CUtensorMap &tm_k16,
                                  const CUtensorMap &tm_v16, cudaStream_t stream)
 {
-    return launch_prefill<false>(paged_prefill_kernel<2, false>, 0, a, Fp4Window{0, 0}, tm_q, tm_k16, tm_v16, stream);
+    if (static_cast<int64_t>(a.batch) * a.hkv * a.max_tiles <= 0)
+        return cudaSuccess;
+    const Fp4Window none = {0, 0};
+    cudaError_t e = raise_limit(paged_prefill_kernel<false>, 0);
+    if (e == cudaSuccess)
+        e = launch_widen<false>(a, none, stream);
+    return e == cudaSuccess ? launch_attention<false>(a, none, tm_q, tm_k16, tm_v16, stream) : e;
 }
 
 cudaError_t launch_paged_prefill_fp4(const PrefillArgs &a, const Fp4Window &win, const CUtensorMap &tm_q,
                                      const CUtensorMap &tm_k16, const CUtensorMap &tm_v16, cudaStream_t stream)
 {
-    if (win.window > 0)
-        return a.out_f32 ? launch_prefill<true>(paged_prefill_kernel<2, true>, 1, a, win, tm_q, tm_k16, tm_v16, stream)
-                         : launch_prefill<true>(paged_prefill_kernel<1, true>, 2, a, win, tm_q, tm_k16, tm_v16, stream);
-    return a.out_f32 ? launch_prefill<true>(paged_prefill_kernel<2, false>, 3, a, win, tm_q, tm_k16, tm_v16, stream)
-                     : launch_prefill<true>(paged_prefill_kernel<1, false>, 4, a, win, tm_q, tm_k16, tm_v16, stream);
+    if (static_cast<int64_t>(a.batch) * a.hkv * a.max_tiles <= 0)
+        return cudaSuccess;
+    cudaError_t e = cudaSuccess;
+    if (a.out_f32)
+        e = win.window > 0 ? raise_limit(paged_prefill_kernel<true>, 1) : raise_limit(paged_prefill_kernel<false>, 0);
+    if (e == cudaSuccess)
+        e = launch_widen<true>(a, win, stream);
+    if (e != cudaSuccess)
+        return e;
+    if (!a.out_f32)
+        return launch_prefill_pair(a, win, tm_q, tm_k16, tm_v16, stream);
+    return win.window > 0 ? launch_attention<true>(a, win, tm_q, tm_k16, tm_v16, stream)
+                          : launch_attention<false>(a, win, tm_q, tm_k16, tm_v16, stream);
 }
 
 }  // namespace pkv

@@ -1,0 +1,442 @@
+// The attention of paged_prefill_fp4 with a bf16 output, on the
+// 5th-generation tensor cores, over the 16-bit copies that the widening kernel
+// made (K as bf16, V as f16: e s has 6 significant bits, exact in both).
+//
+// What bounds it.  A tile of 128 rows (tokens x query heads of the group) and
+// 128 keys costs the tensor cores 2 x 128^3 multiply-adds and the softmax 128^2
+// exponentials.  One f16 part of P is enough under a bf16 output's 2^-8 (the
+// weights are rounded once, 2^-11 each), so the products are two thirds of
+// those that a second part would need, and the softmax must keep up with
+// them: per score a half each of max, fma, add and conversion, and one
+// exponential at a quarter of an SMSP's issue rate or less.
+//
+// So one CTA takes two query tiles, A and B, of the same kv head.  Each has its
+// own softmax warpgroup (one row a thread: no exchange between warps), its own
+// scores in TMEM and its own accumulator, and while the tensor cores work for
+// one tile the other's softmax runs; each K and V tile brought on chip serves
+// both.  P overwrites the first half of its scores' columns in two steps, so
+// that the products with V start on the first 64 keys while the last 64 are
+// still being exponentiated.
+//   warp 0      TMA: two query tiles, then K and V tiles into 2-stage rings
+//   warp 1      tcgen05.mma, in the order  S_A(j+1) after O_A += P_A(j) V(j),
+//               S_B(j+1) after O_B += P_B(j) V(j)
+//   warps 2-5   softmax and output of tile A,  warps 6-9 of tile B
+// The accumulation is one chain of MMAs: the tensor cores add with truncation,
+// and a 128K context's 8192 additions of 16 keys leave at most 2^-11 in the
+// accumulator, on average half of that.
+// Every wait is bounded (2 s): on expiry the CTA sets PKV_DEVERR_TIMEOUT,
+// drains its own copies and MMAs, frees TMEM and exits.
+#include <mutex>
+
+#include "context.h"
+#include "prefill.cuh"
+
+namespace pkv {
+
+namespace {
+
+constexpr int kStages2 = 2;                      // K and V rings
+constexpr int kWarp0 = 2;                        // first softmax warp
+constexpr int kThreads2 = 32 * (kWarp0 + 8);
+constexpr uint32_t kScoreCol = 128, kOutCol = 256;   // tile x: scores at 128 x, accumulator at 256 + 128 x
+
+// Shared memory, offsets from a 1024-byte aligned base.  Operand tiles are
+// [2 column blocks][128 rows][128 bytes] with the 128-byte swizzle.
+struct P2 {
+    static constexpr int kTile = 32768;
+    static constexpr int kQ = 0;                           // query tiles A and B
+    static constexpr int kK = 2 * kTile;
+    static constexpr int kV = kK + kStages2 * kTile;
+    static constexpr int kBars = kV + kStages2 * kTile;
+    enum {
+        Q_FULL, Q_READY = Q_FULL + 2, K_FULL = Q_READY + 2, K_EMPTY = K_FULL + kStages2, V_FULL = K_EMPTY + kStages2,
+        V_EMPTY = V_FULL + kStages2, S_FULL = V_EMPTY + kStages2, P_FULL = S_FULL + 2, PV_DONE = P_FULL + 4,
+        DRAIN = PV_DONE + 2, kNumBars = DRAIN + 1
+    };
+    static constexpr int kTmem = kBars + kNumBars * 8;
+    static constexpr int kFlag = kTmem + 4;
+    static constexpr int kEnd = kFlag + 4;
+    static constexpr size_t bytes() { return static_cast<size_t>(kEnd) + 1024; }
+};
+static_assert(P2::bytes() <= 232448, "prefill tile buffers exceed the shared memory of one CTA");
+
+template <bool kWin>
+__global__ void __launch_bounds__(kThreads2, 1)
+    paged_prefill_pair_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                              const __grid_constant__ CUtensorMap tm_v, const PrefillArgs a, const Fp4Window win)
+{
+    // (sequence, kv head)-major, heaviest pairs of tiles first within each
+    const int pairs = (a.max_tiles + 1) >> 1;
+    const int bh = blockIdx.x / pairs;
+    const int qp = pairs - 1 - (blockIdx.x - bh * pairs);
+    const int b = bh / a.hkv;
+    const int h = bh - b * a.hkv;
+    const int G = a.group, tpt = a.tokens_per_tile;
+    const int q0 = __ldg(a.cu_q + b), q1 = __ldg(a.cu_q + b + 1);
+    const int n = q1 - q0;
+    const int L = __ldg(a.seq_lens + b);
+    if (!sequence_ok(a, b, q0, q1, L, qp == 0 && h == 0 && threadIdx.x == 0))
+        return;
+    const int off0 = __ldg(a.tile_off + b), off1 = __ldg(a.tile_off + b + 1);
+    const KeyTiles seq_kt = key_tiles<kWin>(win, L - n);
+    if (off1 > a.rows_cap / 128 || off1 - off0 != a.hkv * ((L + kKeys - 1) / kKeys - seq_kt.skip))
+        return;
+    const int row0 = off0 * 128 + h * (off1 - off0) / a.hkv * 128;   // first row of this kv head's copy
+    const int t0 = qp * 2 * tpt;                         // first token of the pair in the chunk
+    if (t0 >= n)
+        return;
+    const int nv0 = min(tpt, n - t0), nv1 = max(0, min(tpt, n - t0 - tpt));   // tokens of A and of B
+    const int pos0 = L - n + t0;                         // position of the first one
+    const KeyTiles kt = key_tiles<kWin>(win, pos0);      // what some row of the pair sees
+    const int nt0 = (pos0 + nv0 - 1) / kKeys + 1 - kt.skip;   // key tiles that A visits
+    const int nt1 = nv1 > 0 ? (pos0 + tpt + nv1 - 1) / kKeys + 1 - kt.skip : 0;
+    const int nt = max(nt0, nt1);
+    // the i-th one, and where it lies in the sequence's copy
+    auto key_tile = [&](int i) { return !kWin || i < kt.first ? i : i + kt.skip; };
+    auto copy_tile = [&](int i) {
+        const int t = key_tile(i);
+        return !kWin || t < seq_kt.first ? t : t - seq_kt.skip;
+    };
+
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const uint32_t sb = smem_addr(smem);
+    auto bar = [&](int i) { return sb + P2::kBars + 8u * i; };
+    uint64_t *bar_ptr = reinterpret_cast<uint64_t *>(smem + P2::kBars);
+    uint32_t *tslot = reinterpret_cast<uint32_t *>(smem + P2::kTmem);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + P2::kFlag);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < P2::kNumBars; ++i)
+            mbar_init(bar(i), i >= P2::Q_READY && i < P2::K_FULL ? 4 : (i >= P2::P_FULL && i < P2::PV_DONE ? 4 : 1));
+        *abort_flag = 0;
+        fence_barrier_init();
+    }
+    if (warp == 1) {
+        tc::tmem_alloc(tslot, 512);
+        tc::tmem_relinquish();
+    }
+    tc::fence_before();
+    __syncthreads();
+    tc::fence_after();
+    const uint32_t tm = *tslot;
+
+    if (warp == 0) {
+        // ------------------------------------------------------------ TMA
+        if (lane == 0) {
+            prefetch_tensormap(&tm_k);
+            prefetch_tensormap(&tm_v);
+            const uint64_t pol = l2_policy_evict_first();
+            const int nq = nv1 > 0 ? 2 : 1;
+            for (int x = 0; x < nq; ++x) {
+                mbar_arrive_expect_tx(bar(P2::Q_FULL + x), 2u * 128u * G * tpt);
+                tma_load_3d(sb + P2::kQ + x * P2::kTile, &tm_q, 0, h * G, q0 + t0 + x * tpt, bar(P2::Q_FULL + x), pol);
+                tma_load_3d(sb + P2::kQ + x * P2::kTile + 16384, &tm_q, 64, h * G, q0 + t0 + x * tpt,
+                            bar(P2::Q_FULL + x), pol);
+            }
+            uint32_t karmed[kStages2] = {}, varmed[kStages2] = {};
+            bool ok = true;
+            for (int t = 0; ok && t < nt; ++t) {
+                const int s = t % kStages2;
+                const int row = row0 + copy_tile(t) * kKeys;
+                if (t >= kStages2 && !pwait(bar(P2::K_EMPTY + s), ((t / kStages2) - 1) & 1, abort_flag, a.err)) {
+                    ok = false;
+                    break;
+                }
+                // (test facility: the withheld CTA never arms or loads its first K tile)
+                if (t > 0 || static_cast<int>(blockIdx.x) != a.withhold_block) {
+                    mbar_arrive_expect_tx(bar(P2::K_FULL + s), P2::kTile);
+                    karmed[s] = static_cast<uint32_t>(t / kStages2) + 1;
+                    tma_load_3d_plain(sb + P2::kK + s * P2::kTile, &tm_k, 0, row, 0, bar(P2::K_FULL + s));
+                    tma_load_3d_plain(sb + P2::kK + s * P2::kTile + 16384, &tm_k, 64, row, 0, bar(P2::K_FULL + s));
+                }
+                if (t >= kStages2 && !pwait(bar(P2::V_EMPTY + s), ((t / kStages2) - 1) & 1, abort_flag, a.err)) {
+                    ok = false;
+                    break;
+                }
+                mbar_arrive_expect_tx(bar(P2::V_FULL + s), P2::kTile);
+                varmed[s] = static_cast<uint32_t>(t / kStages2) + 1;
+                tma_load_3d_plain(sb + P2::kV + s * P2::kTile, &tm_v, 0, row, 0, bar(P2::V_FULL + s));
+                tma_load_3d_plain(sb + P2::kV + s * P2::kTile + 16384, &tm_v, 64, row, 0, bar(P2::V_FULL + s));
+            }
+            // No copy may still be landing when the CTA leaves.
+            for (int x = 0; x < nq; ++x)
+                pwait(bar(P2::Q_FULL + x), 0, abort_flag, a.err, false);
+            for (int s = 0; s < kStages2; ++s) {
+                if (karmed[s])
+                    pwait(bar(P2::K_FULL + s), (karmed[s] - 1) & 1, abort_flag, a.err, false);
+                if (varmed[s])
+                    pwait(bar(P2::V_FULL + s), (varmed[s] - 1) & 1, abort_flag, a.err, false);
+            }
+        }
+    } else if (warp == 1) {
+        // ------------------------------------------------------------ MMA issue
+        // The whole warp runs this converged; one elected lane issues.
+        const uint32_t id_qk = tc::idesc_bf16_f32(kRows, kKeys, false);
+        const uint32_t id_pv = tc::idesc_f16_f32(kRows, kHeadDim, true);
+        uint64_t qdesc[2], kdesc[kStages2], vdesc[kStages2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            qdesc[i] = kmajor_base(sb + P2::kQ + i * P2::kTile);
+#pragma unroll
+        for (int i = 0; i < kStages2; ++i) {
+            kdesc[i] = kmajor_base(sb + P2::kK + i * P2::kTile);
+            vdesc[i] = vmn_base(sb + P2::kV + i * P2::kTile);
+        }
+        const bool leader = elect_one();
+        bool ok = true;
+        // scores of tile x against key tile j
+        auto score = [&](int x, int j, bool last) {
+            const int s = j % kStages2;
+            if (!wwait(bar(P2::K_FULL + s), (j / kStages2) & 1, abort_flag, a.err, lane))
+                return false;
+            tc::fence_after();
+            if (leader) {
+#pragma unroll
+                for (int d = 0; d < 8; ++d)             // dims 16d..16d+15
+                    tc::mma_ss(tm + kScoreCol * x, kmajor_step(qdesc[x], d), kmajor_step(kdesc[s], d), id_qk, d > 0);
+                tc::commit(bar_ptr + P2::S_FULL + x);
+                if (last)
+                    tc::commit(bar_ptr + P2::K_EMPTY + s);
+            }
+            __syncwarp();
+            return true;
+        };
+        // O += P V of tile x, key tile j: keys 16d..16d+15 of P in columns 8d ..
+        auto output = [&](int x, int j, bool last) {
+            const int s = j % kStages2;
+            if (!wwait(bar(P2::V_FULL + s), (j / kStages2) & 1, abort_flag, a.err, lane))
+                return false;
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+                if (!wwait(bar(P2::P_FULL + 2 * x + half), j & 1, abort_flag, a.err, lane))
+                    return false;
+                tc::fence_after();
+                if (leader) {
+#pragma unroll
+                    for (int d = 4 * half; d < 4 * half + 4; ++d)
+                        tc::mma_ts(tm + kOutCol + kScoreCol * x, tm + kScoreCol * x + 8 * d, vmn_step(vdesc[s], d),
+                                   id_pv, j > 0 || d > 0 ? 1u : 0u);
+                    if (half == 1) {
+                        tc::commit(bar_ptr + P2::PV_DONE + x);
+                        if (last)
+                            tc::commit(bar_ptr + P2::V_EMPTY + s);
+                    }
+                }
+                __syncwarp();
+            }
+            return true;
+        };
+        ok = wwait(bar(P2::Q_READY), 0, abort_flag, a.err, lane) && score(0, 0, nt1 == 0);
+        if (ok && nt1 > 0)
+            ok = wwait(bar(P2::Q_READY + 1), 0, abort_flag, a.err, lane) && score(1, 0, true);
+        for (int j = 0; ok && j < nt; ++j) {
+            if (j < nt0)
+                ok = output(0, j, j >= nt1) && (j + 1 >= nt0 || score(0, j + 1, j + 1 >= nt1));
+            if (ok && j < nt1)
+                ok = output(1, j, true) && (j + 1 >= nt1 || score(1, j + 1, true));
+        }
+        // Every MMA issued has finished before TMEM is released.
+        if (leader) {
+            tc::commit(bar_ptr + P2::DRAIN);
+            pwait(bar(P2::DRAIN), 0, abort_flag, a.err, false);
+        }
+        __syncwarp();
+    } else {
+        // ------------------------------------------------------------ softmax + output
+        const int x = (warp - kWarp0) >> 2;              // the warpgroup's tile
+        const int qtr = warp & 3;                        // TMEM lane quarter of this warp
+        const int row = qtr * 32 + lane;
+        const int nvx = x ? nv1 : nv0, ntx = x ? nt1 : nt0;
+        const int tl = row / G;
+        const int g = row - tl * G;
+        const bool valid = row < G * tpt && tl < nvx;
+        const int p_row = pos0 + x * tpt + (valid ? tl : nvx - 1);   // padding rows mirror the last row
+        const float sl2 = __ldg(a.k_scale + h) * a.sm_scale_log2;
+        const uint32_t s_tm = tm + (static_cast<uint32_t>(qtr * 32) << 16) + kScoreCol * x;
+        const uint32_t o_tm = s_tm + kOutCol;
+        float m = -INFINITY, l = 0.f;
+        bool ok = ntx > 0 && wwait(bar(P2::Q_FULL + x), 0, abort_flag, a.err, lane);
+        if (ok) {
+            // rows past the G x tpt that the copy fills are zeroed
+            if (row >= G * tpt) {
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                    uint4 *qrow = reinterpret_cast<uint4 *>(smem + P2::kQ + x * P2::kTile + half * 16384 + row * 128);
+#pragma unroll
+                    for (int c = 0; c < 8; ++c)
+                        qrow[c] = make_uint4(0, 0, 0, 0);
+                }
+            }
+            fence_proxy_async_smem();     // generic-proxy writes -> visible to the tensor cores
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(bar(P2::Q_READY + x));
+        }
+        for (int j = 0; ok && j < ntx; ++j) {
+            if (!wwait(bar(P2::S_FULL + x), j & 1, abort_flag, a.err, lane)) {
+                ok = false;
+                break;
+            }
+            tc::fence_after();
+            uint32_t v[4][32];
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+                tc::ld32(s_tm + 32 * c, v[c]);
+            tc::wait_ld();
+            // hidden keys become -inf: after the row's position, or before its
+            // window and behind the sinks
+            const int key0 = key_tile(j) * kKeys;
+            const int vis = p_row - key0;
+            if (vis < kKeys - 1) {
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+#pragma unroll
+                    for (int k = 0; k < 32; ++k)
+                        if (32 * c + k > vis)
+                            v[c][k] = __float_as_uint(-INFINITY);
+            }
+            if (kWin) {
+                const int out = vis - win.window, snk = win.sinks - key0;
+                if (out >= 0 && snk < kKeys) {
+#pragma unroll
+                    for (int c = 0; c < 4; ++c)
+#pragma unroll
+                        for (int k = 0; k < 32; ++k)
+                            if (32 * c + k <= out && 32 * c + k >= snk)
+                                v[c][k] = __float_as_uint(-INFINITY);
+                }
+            }
+            float mx[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                mx[k] = max3(__uint_as_float(v[0][2 * k]), __uint_as_float(v[0][2 * k + 1]), -INFINITY);
+#pragma unroll
+            for (int k = 8; k < 64; ++k)
+                mx[k & 7] = max3(mx[k & 7], __uint_as_float(v[k >> 4][2 * (k & 15)]),
+                                 __uint_as_float(v[k >> 4][2 * (k & 15) + 1]));
+            const float top = fmaxf(max3(mx[0], mx[1], mx[2]), max3(max3(mx[3], mx[4], mx[5]), mx[6], mx[7])) * sl2;
+            // The maximum moves only when it is exceeded by more than 2^8.
+            const bool need = top > m + 8.f;
+            if (__any_sync(kAll, need)) {
+                const float mn = need ? top : m;
+                const float f = need ? ex2_approx(m - mn) : 1.f;
+                m = mn;
+                l *= f;
+                if (j > 0) {                               // the accumulator holds tiles 0 .. j-1
+                    if (!wwait(bar(P2::PV_DONE + x), (j - 1) & 1, abort_flag, a.err, lane)) {
+                        ok = false;
+                        break;
+                    }
+                    tc::fence_after();
+#pragma unroll 1
+                    for (int c = 0; c < 8; ++c) {
+                        uint32_t o[16];
+                        tc::ld16(o_tm + 16 * c, o);
+                        tc::wait_ld();
+#pragma unroll
+                        for (int k = 0; k < 16; ++k)
+                            o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
+                        tc::st16(o_tm + 16 * c, o);
+                    }
+                    tc::wait_st();
+                }
+            }
+            // P = 2^(s sl2 - m) as f16 pairs over the scores' first 64 columns
+            // (a row that has seen nothing yet: every P is 2^-inf)
+            const float ms = kWin && m == -INFINITY ? 0.f : m;
+            const uint64_t sl2x2 = f2_pack(sl2, sl2), nmm = f2_pack(-ms, -ms);
+            uint64_t ls[4] = {0ull, 0ull, 0ull, 0ull};
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+                uint32_t ph[32];
+#pragma unroll
+                for (int q = 0; q < 32; ++q) {
+                    const int c = 2 * half + (q >> 4), k = 2 * (q & 15);
+                    const float2 y = f2_unpack(
+                        f2_fma(f2_pack(__uint_as_float(v[c][k]), __uint_as_float(v[c][k + 1])), sl2x2, nmm));
+                    const float p0 = ex2_approx(y.x), p1 = ex2_approx(y.y);
+                    ls[q & 3] = f2_add(ls[q & 3], f2_pack(p0, p1));
+                    ph[q] = f32x2_to_f16x2(p0, p1);
+                }
+                tc::st32(s_tm + 32 * half, ph);
+                tc::wait_st();
+                tc::fence_before();
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(bar(P2::P_FULL + 2 * x + half));
+            }
+            const float2 s0 = f2_unpack(f2_add(ls[0], ls[1])), s1 = f2_unpack(f2_add(ls[2], ls[3]));
+            l += (s0.x + s0.y) + (s1.x + s1.y);
+        }
+        if (ok && wwait(bar(P2::PV_DONE + x), (ntx - 1) & 1, abort_flag, a.err, lane)) {
+            tc::fence_after();
+            const float inv = __ldg(a.v_scale + h) / l;
+            const int64_t orow = (static_cast<int64_t>(q0) + t0 + x * tpt + tl) * a.hq + h * G + g;
+            uint4 *dst = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.out) + orow * kHeadDim);
+#pragma unroll 1
+            for (int c = 0; c < 4; ++c) {
+                uint32_t o[32];
+                tc::ld32(o_tm + 32 * c, o);
+                tc::wait_ld();
+                if (!valid)
+                    continue;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    uint32_t w[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const __nv_bfloat162 b2 = __floats2bfloat162_rn(__uint_as_float(o[8 * k + 2 * e]) * inv,
+                                                                        __uint_as_float(o[8 * k + 2 * e + 1]) * inv);
+                        w[e] = *reinterpret_cast<const uint32_t *>(&b2);
+                    }
+                    dst[4 * c + k] = make_uint4(w[0], w[1], w[2], w[3]);
+                }
+            }
+        }
+    }
+
+    tc::fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        tc::fence_after();
+        tc::tmem_dealloc(tm, 512);
+    }
+}
+
+std::mutex g_pair_mu;
+unsigned long long g_pair_ctx[64][2] = {};   // per device and kernel: the context its limit was raised in
+
+}  // namespace
+
+// The attention launch alone: the widening kernel has been enqueued before.
+cudaError_t launch_prefill_pair(const PrefillArgs &a, const Fp4Window &win, const CUtensorMap &tm_q,
+                                const CUtensorMap &tm_k16, const CUtensorMap &tm_v16, cudaStream_t stream)
+{
+    const int which = win.window > 0 ? 1 : 0;
+    const auto kernel = which ? paged_prefill_pair_kernel<true> : paged_prefill_pair_kernel<false>;
+    int dev = -1;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess)
+        return e;
+    if (dev < 0 || dev >= 64)
+        return cudaErrorInvalidDevice;
+    {
+        unsigned long long ctx = 0;
+        const bool known = current_context_id(&ctx);
+        std::lock_guard<std::mutex> lk(g_pair_mu);
+        if (!known || g_pair_ctx[dev][which] != ctx) {
+            e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                     static_cast<int>(P2::bytes()));
+            if (e != cudaSuccess)
+                return e;
+            g_pair_ctx[dev][which] = known ? ctx : 0;
+        }
+    }
+    const int64_t grid = static_cast<int64_t>(a.batch) * a.hkv * ((a.max_tiles + 1) / 2);
+    kernel<<<static_cast<unsigned>(grid), kThreads2, P2::bytes(), stream>>>(tm_q, tm_k16, tm_v16, a, win);
+    return cudaGetLastError();
+}
+
+}  // namespace pkv
