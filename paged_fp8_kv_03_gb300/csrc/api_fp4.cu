@@ -72,13 +72,13 @@ Fp4Window clamp_window(int window, int sinks, long long max_len)
     return w;
 }
 
-// CTAs of the decode grid (the kernel with two parts a weight needs no fewer
-// registers, so its count holds for both).
+// CTAs of the decode grid (of the kernel with one part a weight and of that
+// with two, whichever has fewer resident).
 int decode_ctas(int batch, int max_ctas)
 {
     const size_t smem = decode_fp4_smem(batch);
-    const int one = resident_ctas(decode_fp4_kernel(false), 32 * kFp4DecodeWarps, smem, max_ctas);
-    const int two = one <= 0 ? 0 : resident_ctas(decode_fp4_kernel(true), 32 * kFp4DecodeWarps, smem, max_ctas);
+    const int one = resident_ctas(decode_fp4_kernel(false, false), 32 * kFp4DecodeWarps, smem, max_ctas);
+    const int two = one <= 0 ? 0 : resident_ctas(decode_fp4_kernel(true, false), 32 * kFp4DecodeWarps, smem, max_ctas);
     return two < one ? two : one;
 }
 
@@ -197,7 +197,7 @@ pkv_status pkv_paged_gqa_decode_fp4(const void *q, const uint8_t *k_cache, const
     // Units of 32 tokens that the longest sequence can show; a list with fewer
     // units than the device has workers needs no more CTAs than it has units.
     long long tiles = (max_len + 15) / 16;
-    if (window > 0) {
+    if (a.win.window > 0) {
         const long long seen = (static_cast<long long>(sinks) + 15) / 16 + (static_cast<long long>(window) + 15) / 16 + 1;
         tiles = seen < tiles ? seen : tiles;
     }
@@ -209,10 +209,17 @@ pkv_status pkv_paged_gqa_decode_fp4(const void *q, const uint8_t *k_cache, const
         return PKV_ERR_CUDA;                             // resident_ctas recorded the failing call
     if (workspace_bytes < decode_workspace(batch, num_q_heads, num_kv_heads, ctas))
         return PKV_ERR_WORKSPACE;
-    if (units < ctas)
-        ctas = static_cast<int>(units > 0 ? units : 1);
     Fp4DecodeArgs da;
     da.a = a;
+    da.cluster = 0;
+    if (max_ctas == 0) {
+        const int slots = resident_ctas(decode_fp4_kernel(a.out_f32, true), 32 * kFp4DecodeWarps, decode_fp4_smem(0), 0);
+        if (slots <= 0)
+            return PKV_ERR_CUDA;
+        da.cluster = decode_fp4_cluster((tiles + 1) / 2, static_cast<long long>(batch) * num_kv_heads, slots);
+    }
+    if (units < ctas)
+        ctas = static_cast<int>(units > 0 ? units : 1);
     da.joins = static_cast<int2 *>(workspace);
     const size_t joins = decode_fp4_join_bytes(batch, num_kv_heads);
     da.partials = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + joins);

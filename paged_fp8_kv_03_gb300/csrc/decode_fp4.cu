@@ -50,6 +50,9 @@ constexpr int kThreadsD = 32 * kWarpsD;
 constexpr int kStagesD = 3;
 constexpr int kUnitBytes = 4 * kFp4Tile;                   // K tile 0, K tile 1, V tile 0, V tile 1
 constexpr float kMoveMax = 8.f;                            // log2 units
+// Units a warp of a cluster takes at most: beyond it the list's even split and
+// a second launch for the join are faster.
+constexpr int kClusterUnits = 6;
 // Units after which a piece's accumulator is added into an fp32 copy: the
 // tensor cores add with truncation, whose error grows with the chain.
 // 2048 additions (512 units of one part) may leave 2^-12 under a bf16
@@ -214,12 +217,6 @@ __device__ __forceinline__ float2 unpack2(uint64_t r)
     asm("mov.b64 {%0, %1}, %2;" : "=f"(v.x), "=f"(v.y) : "l"(r));
     return v;
 }
-__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b)
-{
-    uint64_t d;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-    return d;
-}
 __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c)
 {
     uint64_t d;
@@ -364,10 +361,48 @@ __device__ __forceinline__ void store16(const Fp4AttnArgs &a, int64_t row, int d
     }
 }
 
+__device__ __forceinline__ void store4(const Fp4AttnArgs &a, int64_t row, int d, float4 v)
+{
+    if (a.out_f32) {
+        *reinterpret_cast<float4 *>(static_cast<float *>(a.out) + row * kHeadDim + d) = v;
+    } else {
+        const __nv_bfloat162 x = __floats2bfloat162_rn(v.x, v.y), y = __floats2bfloat162_rn(v.z, v.w);
+        *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(a.out) + row * kHeadDim + d) =
+            make_uint2(*reinterpret_cast<const uint32_t *>(&x), *reinterpret_cast<const uint32_t *>(&y));
+    }
+}
+
+// All threads of the cluster (one CTA: of the CTA).
+__device__ __forceinline__ void cluster_sync(int ctas)
+{
+    if (ctas > 1)
+        asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+    else
+        __syncthreads();
+}
+
+// The float at address `at` of this CTA's shared memory in CTA `cta` of the
+// cluster (own: in this one).
+__device__ __forceinline__ float cluster_load(uint32_t at, int cta, bool own)
+{
+    float v;
+    if (own) {
+        asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(at) : "memory");
+    } else {
+        uint32_t there;
+        asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(there) : "r"(at), "r"(cta));
+        asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(there) : "memory");
+    }
+    return v;
+}
+
 // kParts: f16 parts of a softmax weight.  One (rounded to f16, 2^-11, and the
 // normalising sum is of the rounded ones) is enough under a bf16 output's
 // 2^-8; two keep an fp32 output to 2^-21.
-template <int kParts>
+// kCluster: short work, one cluster of da.cluster CTAs a segment.  Its warps
+// share the segment's units evenly, leave their states in shared memory and
+// join them there: one launch and no partial states in memory.
+template <int kParts, bool kCluster>
 __global__ void __launch_bounds__(kThreadsD, kFp4DecodeCtas) paged_gqa_decode_fp4_kernel(const Fp4DecodeArgs da)
 {
     const Fp4AttnArgs &a = da.a;
@@ -377,6 +412,34 @@ __global__ void __launch_bounds__(kThreadsD, kFp4DecodeCtas) paged_gqa_decode_fp
     volatile int *stop = reinterpret_cast<volatile int *>(smem + SmemD::kFlag);
     int *sums = reinterpret_cast<int *>(smem + SmemD::kSums);
 
+    int worker, lo, n;                                     // this warp's units: n from list position lo
+    Place seg = {0, 0, 0};                                 // kCluster: the segment, and its units
+    int seg_units = 0, rank = 0;
+    if constexpr (kCluster) {
+        rank = static_cast<int>(blockIdx.x) % da.cluster;
+        const int sg = static_cast<int>(blockIdx.x) / da.cluster;
+        seg.b = sg / a.hkv;
+        seg.h = sg % a.hkv;
+        const Sight s = sight_of(a, seg.b);
+        seg_units = (s.tiles + 1) >> 1;
+        if (tid == 0) {
+            *stop = 0;
+            for (int i = 0; i < kWarpsD * kStagesD; ++i)
+                mbar_init(smem_addr(smem + SmemD::kBar) + 8 * i, 1);
+            fence_barrier_init();
+            if (a.err && rank == 0 && seg.h == 0) {
+                if (seq_page_log2(a, seg.b) < 0)
+                    atomicOr(a.err, PKV_DEVERR_PAGESIZE);
+                else if (__ldg(a.seq_lens + seg.b) != s.len)
+                    atomicOr(a.err, PKV_DEVERR_SEQLEN);
+            }
+        }
+        __syncthreads();
+        const int at = rank * kWarpsD + warp, workers = da.cluster * kWarpsD;
+        worker = static_cast<int>(blockIdx.x) * kWarpsD + warp;
+        lo = seg_units * at / workers;
+        n = seg_units * (at + 1) / workers - lo;
+    } else {
     // ---- first unit of every sequence (of one kv head): a prefix sum over the batch
     {
         const int per = (a.batch + kThreadsD - 1) / kThreadsD;
@@ -434,20 +497,43 @@ __global__ void __launch_bounds__(kThreadsD, kFp4DecodeCtas) paged_gqa_decode_fp
                 da.joins[sg] = make_int2(-1, -1);
         }
     }
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    launch_dependents();
 
     const int total = start[a.batch] * a.hkv;
-    const int worker = warp * gridDim.x + blockIdx.x;
+    worker = warp * gridDim.x + blockIdx.x;
     const int active = min(static_cast<int>(gridDim.x) * kWarpsD, total);
     if (worker >= active)
         return;                                            // no CTA barrier follows
-    const int lo = static_cast<int>(static_cast<int64_t>(total) * worker / active);
-    const int n = static_cast<int>(static_cast<int64_t>(total) * (worker + 1) / active) - lo;
+    lo = static_cast<int>(static_cast<int64_t>(total) * worker / active);
+    n = static_cast<int>(static_cast<int64_t>(total) * (worker + 1) / active) - lo;
+    }
+    auto place = [&](int x) -> Place {
+        if constexpr (kCluster)
+            return Place{seg.b, seg.h, x};
+        else
+            return place_of(start, a.batch, x);
+    };
 
     const uint32_t ring = smem_addr(smem) + warp * kStagesD * kUnitBytes;
     const uint32_t bars = smem_addr(smem + SmemD::kBar) + warp * kStagesD * 8;
 
+    // a piece's query rows (kCluster: on their way while the tiles are looked up)
+    const int r = lane >> 2, c = lane & 3;
+    uint4 qraw[4];
+    float kscale;
+    auto load_q = [&](const Place &p) {
+        const int64_t row = static_cast<int64_t>(p.b) * a.hq + static_cast<int64_t>(p.h) * a.group + (r < a.group ? r : 0);
+        const uint4 *src = reinterpret_cast<const uint4 *>(a.q + row * kHeadDim + 32 * c);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            qraw[i] = __ldg(src + i);
+        kscale = __ldg(a.k_scale + p.h);
+    };
+    if constexpr (kCluster)
+        load_q(seg);
+
     const uint64_t policy = l2_policy_evict_first();
+    float *state = reinterpret_cast<float *>(smem + warp * kStagesD * kUnitBytes);   // kCluster: over the ring, at the end
 
     // ---- tile addresses, 16 units ahead: lane 2i + j has tile j of unit i.
     // -1: a page outside the pool; -2: no such tile.
@@ -455,7 +541,7 @@ __global__ void __launch_bounds__(kThreadsD, kFp4DecodeCtas) paged_gqa_decode_fp
         const int u = u0 + (lane >> 1);
         if (u >= n)
             return -2;
-        const Place p = place_of(start, a.batch, lo + u);
+        const Place p = place(lo + u);
         const Sight s = sight_of(a, p.b);
         const int i = 2 * p.unit + (lane & 1);
         if (i >= s.tiles)
@@ -496,20 +582,19 @@ __global__ void __launch_bounds__(kThreadsD, kFp4DecodeCtas) paged_gqa_decode_fp
     for (int v = 0; v < kStagesD && v < n; ++v)
         issue(v, v);
 
-    const int r = lane >> 2, c = lane & 3;
     const LaneOffsets lo_off = lane_offsets(r, c);
     int stage = 0;
     uint32_t parity = 0;
     bool dead = false;                                     // a wait ran out
     int u = 0;
     while (u < n) {
-        const Place p = place_of(start, a.batch, lo + u);
+        const Place p = place(lo + u);
         const Sight sg = sight_of(a, p.b);
-        const int units = start[p.b + 1] - start[p.b];
+        const int units = kCluster ? seg_units : start[p.b + 1] - start[p.b];
         const int take = min(units - p.unit, n - u);
         const bool whole = p.unit == 0 && take == units;
         const int64_t row0 = static_cast<int64_t>(p.b) * a.hq + static_cast<int64_t>(p.h) * a.group;
-        if (lane == 0) {                                   // who holds the segment's first and last unit
+        if (!kCluster && lane == 0) {                      // who holds the segment's first and last unit
             int2 *j = da.joins + p.b * a.hkv + p.h;
             if (p.unit == 0)
                 j->x = whole ? -1 : worker;
@@ -521,12 +606,9 @@ __global__ void __launch_bounds__(kThreadsD, kFp4DecodeCtas) paged_gqa_decode_fp
         uint32_t q[8][2];
         float f0, f1;
         {
-            uint4 v[4];
-            const uint4 *src = reinterpret_cast<const uint4 *>(a.q + (row0 + (r < a.group ? r : 0)) * kHeadDim + 32 * c);
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                v[i] = __ldg(src + i);
-            const uint32_t *w = reinterpret_cast<const uint32_t *>(v);
+            if (!kCluster)
+                load_q(p);
+            const uint32_t *w = reinterpret_cast<const uint32_t *>(qraw);
             uint32_t top = 0;                              // largest |q|, as its bits
 #pragma unroll
             for (int i = 0; i < 16; ++i)
@@ -535,7 +617,7 @@ __global__ void __launch_bounds__(kThreadsD, kFp4DecodeCtas) paged_gqa_decode_fp
             top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
             const int ex = min(max(static_cast<int>(top >> 23), 1), 253);
             const float down = __uint_as_float(static_cast<uint32_t>(254 - ex) << 23);
-            const float up = __uint_as_float(static_cast<uint32_t>(ex) << 23) * (__ldg(a.k_scale + p.h) * a.sm_scale_log2);
+            const float up = __uint_as_float(static_cast<uint32_t>(ex) << 23) * (kscale * a.sm_scale_log2);
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
                 const bool on = r < a.group;
@@ -676,7 +758,8 @@ __global__ void __launch_bounds__(kThreadsD, kFp4DecodeCtas) paged_gqa_decode_fp
                 }
                 accumulate<kParts>(x, b, acc, sum);
             }
-            if ((i + 1) % kFoldUnits<kParts> == 0 || (i + 1 == take && take > kFoldUnits<kParts>)) {
+            // (a cluster's warps have fewer units than a fold)
+            if (!kCluster && ((i + 1) % kFoldUnits<kParts> == 0 || (i + 1 == take && take > kFoldUnits<kParts>))) {
                 // the piece's own slot of the workspace holds the copy (each lane its own elements)
                 const float g0 = i + 1 > kFoldUnits<kParts> ? ex2_approx(mf0 - m0) : 0.f;
                 const float g1 = i + 1 > kFoldUnits<kParts> ? ex2_approx(mf1 - m1) : 0.f;
@@ -714,6 +797,7 @@ __global__ void __launch_bounds__(kThreadsD, kFp4DecodeCtas) paged_gqa_decode_fp
             break;
 
         // ---- end of piece: heads 2c, 2c + 1; dims 16 r ..
+        __syncwarp();                                      // (kCluster: the state overwrites the ring)
         l0 = sum[0];
         l1 = sum[1];
 #pragma unroll
@@ -727,7 +811,14 @@ __global__ void __launch_bounds__(kThreadsD, kFp4DecodeCtas) paged_gqa_decode_fp
                 v[2 * k] = acc[k][j];
                 v[2 * k + 1] = acc[k][j + 2];
             }
-            if (whole) {
+            if constexpr (kCluster) {
+                float *s = state + g * kPartialStride;
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    reinterpret_cast<float4 *>(s + 16 * r)[k] = make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
+                if (r == 0)
+                    *reinterpret_cast<float2 *>(s + kHeadDim) = make_float2(j ? m1 : m0, j ? l1 : l0);
+            } else if (whole) {
                 const float f = __ldg(a.v_scale + p.h) / (j ? l1 : l0);
 #pragma unroll
                 for (int k = 0; k < 16; ++k)
@@ -754,6 +845,71 @@ __global__ void __launch_bounds__(kThreadsD, kFp4DecodeCtas) paged_gqa_decode_fp
                    global_timer_ns() - t0 < kLimitNs) {
             }
         }
+
+    if constexpr (kCluster) {
+        // ---- join the cluster's states (at most 32, one a lane), in worker
+        // order: CTA k takes the heads k, k + CTAs, ..; of several CTAs each warp
+        // 32 dims of all of them, of one CTA a warp every fourth head
+        if ((n == 0 || dead) && lane < a.group)
+            *reinterpret_cast<float2 *>(state + lane * kPartialStride + kHeadDim) = make_float2(-INFINITY, 0.f);
+        cluster_sync(da.cluster);
+        const bool one = da.cluster == 1;
+        const int workers = da.cluster * kWarpsD;
+        for (int g = one ? warp : rank; g < a.group; g += one ? kWarpsD : da.cluster) {
+            const uint32_t mine = smem_addr(smem) + g * kPartialStride * 4;    // warp 0's state of this head, this CTA
+            float m = -INFINITY, l = 0.f;
+            if (lane < workers) {
+                const uint32_t at = mine + (lane & 3) * kStagesD * kUnitBytes + kHeadDim * 4;
+                m = cluster_load(at, lane >> 2, one);
+                l = cluster_load(at + 4, lane >> 2, one);
+            }
+            float M = m;
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1)
+                M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+            const float e = m == -INFINITY ? 0.f : ex2_approx(m - M);
+            float sum = e * l;
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1)
+                sum += __shfl_xor_sync(0xffffffffu, sum, o);
+            const float f = seg_units == 0 ? 0.f : __ldg(a.v_scale + seg.h) / sum;
+            const int64_t row = static_cast<int64_t>(seg.b) * a.hq + static_cast<int64_t>(seg.h) * a.group + g;
+            // (what a warp without units left is read, but not used)
+            if (one) {
+                float4 A = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                for (int i = 0; i < kWarpsD; ++i) {
+                    const float ei = __shfl_sync(0xffffffffu, e, i);
+                    const float4 v = *reinterpret_cast<const float4 *>(smem + i * kStagesD * kUnitBytes +
+                                                                       (g * kPartialStride + 4 * lane) * 4);
+                    A.x += ei != 0.f ? ei * v.x : 0.f;
+                    A.y += ei != 0.f ? ei * v.y : 0.f;
+                    A.z += ei != 0.f ? ei * v.z : 0.f;
+                    A.w += ei != 0.f ? ei * v.w : 0.f;
+                }
+                store4(a, row, 4 * lane, make_float4(A.x * f, A.y * f, A.z * f, A.w * f));
+            } else {
+                const int d = 32 * warp + lane;
+                float A = 0.f;
+                for (int i0 = 0; i0 < workers; i0 += 8) {
+                    float v[8];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        v[i] = cluster_load(mine + (i & 3) * kStagesD * kUnitBytes + 4 * d, (i0 + i) >> 2, false);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const float ei = __shfl_sync(0xffffffffu, e, i0 + i);
+                        A += ei != 0.f ? ei * v[i] : 0.f;
+                    }
+                }
+                if (a.out_f32)
+                    static_cast<float *>(a.out)[row * kHeadDim + d] = A * f;
+                else
+                    static_cast<__nv_bfloat16 *>(a.out)[row * kHeadDim + d] = __float2bfloat16_rn(A * f);
+            }
+        }
+        cluster_sync(da.cluster);                          // no CTA leaves while its states are read
+    }
 }
 
 // Joins the states of a segment's pieces for one query head, in worker order:
@@ -772,7 +928,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_fp4_kernel(const Fp4Deco
     const int sg = blockIdx.x / a.group, g = blockIdx.x % a.group;
     const int b = sg / a.hkv, h = sg % a.hkv;
     const float vs = __ldg(a.v_scale + h);
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    grid_wait();
     const int2 j = da.joins[sg];
     if (j.x < 0)
         return;
@@ -837,14 +993,8 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_fp4_kernel(const Fp4Deco
         }
     }
     const float f = vs / L;
-    const int64_t at = (static_cast<int64_t>(b) * a.hq + static_cast<int64_t>(h) * a.group + g) * kHeadDim + 4 * lane;
-    if (a.out_f32) {
-        *reinterpret_cast<float4 *>(static_cast<float *>(a.out) + at) = make_float4(A.x * f, A.y * f, A.z * f, A.w * f);
-    } else {
-        const __nv_bfloat162 x = __floats2bfloat162_rn(A.x * f, A.y * f), y = __floats2bfloat162_rn(A.z * f, A.w * f);
-        *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(a.out) + at) =
-            make_uint2(*reinterpret_cast<const uint32_t *>(&x), *reinterpret_cast<const uint32_t *>(&y));
-    }
+    store4(a, static_cast<int64_t>(b) * a.hq + static_cast<int64_t>(h) * a.group + g, 4 * lane,
+           make_float4(A.x * f, A.y * f, A.z * f, A.w * f));
 }
 
 }  // namespace
@@ -854,21 +1004,38 @@ size_t decode_fp4_smem(int batch)
     return SmemD::bytes(batch);
 }
 
-const void *decode_fp4_kernel(bool two_parts)
+const void *decode_fp4_kernel(bool two_parts, bool cluster)
 {
-    return two_parts ? reinterpret_cast<const void *>(&paged_gqa_decode_fp4_kernel<2>)
-                     : reinterpret_cast<const void *>(&paged_gqa_decode_fp4_kernel<1>);
+    if (cluster)
+        return two_parts ? reinterpret_cast<const void *>(&paged_gqa_decode_fp4_kernel<2, true>)
+                         : reinterpret_cast<const void *>(&paged_gqa_decode_fp4_kernel<1, true>);
+    return two_parts ? reinterpret_cast<const void *>(&paged_gqa_decode_fp4_kernel<2, false>)
+                     : reinterpret_cast<const void *>(&paged_gqa_decode_fp4_kernel<1, false>);
+}
+
+// A cluster a segment, of the fewest CTAs (1, 2, 4, 8) that leave a warp at
+// most kClusterUnits units, if all of them are resident at once; 0: the list.
+// (`units`: of the longest sequence, `slots`: resident CTAs.)
+int decode_fp4_cluster(long long units, long long segments, int slots)
+{
+    for (int c = 1; c <= 8; c *= 2)
+        if (units <= static_cast<long long>(c) * kWarpsD * kClusterUnits)
+            return segments * c <= slots ? c : 0;
+    return 0;
 }
 
 cudaError_t launch_paged_decode_fp4(const Fp4DecodeArgs &da, int ctas, cudaStream_t stream, const char **site)
 {
-    const size_t smem = SmemD::bytes(da.a.batch);
     *site = "4-bit decode kernel launch";
-    if (da.a.out_f32)
-        paged_gqa_decode_fp4_kernel<2><<<ctas, kThreadsD, smem, stream>>>(da);
-    else
-        paged_gqa_decode_fp4_kernel<1><<<ctas, kThreadsD, smem, stream>>>(da);
-    cudaError_t e = cudaGetLastError();
+    const bool two = da.a.out_f32;
+    if (da.cluster > 0) {
+        const dim3 grid(static_cast<unsigned>(da.a.batch * da.a.hkv * da.cluster));
+        return launch_with(two ? paged_gqa_decode_fp4_kernel<2, true> : paged_gqa_decode_fp4_kernel<1, true>, grid,
+                           kThreadsD, SmemD::bytes(0), da.cluster, false, stream, da);
+    }
+    cudaError_t e = launch_with(two ? paged_gqa_decode_fp4_kernel<2, false> : paged_gqa_decode_fp4_kernel<1, false>,
+                                dim3(static_cast<unsigned>(ctas)), kThreadsD, SmemD::bytes(da.a.batch), 1, false, stream,
+                                da);
     if (e != cudaSuccess)
         return e;
     *site = "4-bit join kernel launch";
@@ -877,16 +1044,8 @@ cudaError_t launch_paged_decode_fp4(const Fp4DecodeArgs &da, int ctas, cudaStrea
     int warps = 1;
     while (warps < kJoinWarps && warps * kJoin < pieces)
         warps *= 2;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(segs * da.a.group));
-    cfg.blockDim = dim3(static_cast<unsigned>(32 * warps));
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, join_fp4_kernel, da);
+    return launch_with(join_fp4_kernel, dim3(static_cast<unsigned>(segs * da.a.group)), 32 * warps, 0, 1, true, stream,
+                       da);
 }
 
 }  // namespace pkv

@@ -8,6 +8,17 @@
 
 namespace pkv {
 
+// Waits until the kernels ahead in the stream have ended and their writes are
+// seen; lets the next kernel be brought onto the GPU (it waits in turn).
+__device__ __forceinline__ void grid_wait()
+{
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+__device__ __forceinline__ void launch_dependents()
+{
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
 // Byte offset in a pool of the tile holding row `row` of pool page `page`.
 __device__ __forceinline__ int64_t fp4_tile_offset(int64_t page, int h, int row, int hkv, int page_size)
 {

@@ -64,8 +64,39 @@ struct Fp4DecodeArgs {
                                                            // piece; x = -1: nothing to join
     float *partials;                                       // [num_slots][group][kPartialStride]
     long long num_slots;
+    int cluster;                                           // CTAs a segment; 0: one list for all segments
     int withhold;                                          // failure-detection test hook (-1 = off)
 };
+
+// Launches clusters of `cluster` CTAs (1: none), and, if `early`, with
+// programmatic stream serialization: the kernel may be brought onto the GPU
+// before the one ahead of it has ended, and waits for that with grid_wait().
+template <typename... Params, typename... Args>
+cudaError_t launch_with(void (*kernel)(Params...), dim3 grid, unsigned threads, size_t smem, int cluster, bool early,
+                        cudaStream_t stream, const Args &...args)
+{
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    unsigned n = 0;
+    if (early) {
+        attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[n++].val.programmaticStreamSerializationAllowed = 1;
+    }
+    if (cluster > 1) {
+        attr[n].id = cudaLaunchAttributeClusterDimension;
+        attr[n].val.clusterDim.x = static_cast<unsigned>(cluster);
+        attr[n].val.clusterDim.y = attr[n].val.clusterDim.z = 1;
+        ++n;
+    }
+    cfg.attrs = attr;
+    cfg.numAttrs = n;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 
 inline size_t decode_fp4_join_bytes(int batch, int hkv)
 {
@@ -99,7 +130,8 @@ inline size_t prefill_fp4_bytes(int batch, long long rows)
 }
 
 size_t decode_fp4_smem(int batch);
-const void *decode_fp4_kernel(bool two_parts);
+const void *decode_fp4_kernel(bool two_parts, bool cluster);
+int decode_fp4_cluster(long long units, long long segments, int slots);
 cudaError_t launch_paged_decode_fp4(const Fp4DecodeArgs &da, int ctas, cudaStream_t stream, const char **site);
 cudaError_t launch_prefill_pair(const PrefillArgs &a, const Fp4Window &win, const CUtensorMap &tm_q,
                                 const CUtensorMap &tm_k16, const CUtensorMap &tm_v16, cudaStream_t stream);
