@@ -529,8 +529,11 @@ __global__ void __launch_bounds__(kThreadsD, kFp4DecodeCtas) paged_gqa_decode_fp
             qraw[i] = __ldg(src + i);
         kscale = __ldg(a.k_scale + p.h);
     };
-    if constexpr (kCluster)
+    float vscale = 0.f;
+    if constexpr (kCluster) {
         load_q(seg);
+        vscale = __ldg(a.v_scale + seg.h);
+    }
 
     const uint64_t policy = l2_policy_evict_first();
     float *state = reinterpret_cast<float *>(smem + warp * kStagesD * kUnitBytes);   // kCluster: over the ring, at the end
@@ -872,7 +875,7 @@ __global__ void __launch_bounds__(kThreadsD, kFp4DecodeCtas) paged_gqa_decode_fp
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1)
                 sum += __shfl_xor_sync(0xffffffffu, sum, o);
-            const float f = seg_units == 0 ? 0.f : __ldg(a.v_scale + seg.h) / sum;
+            const float f = seg_units == 0 ? 0.f : vscale / sum;
             const int64_t row = static_cast<int64_t>(seg.b) * a.hq + static_cast<int64_t>(seg.h) * a.group + g;
             // (what a warp without units left is read, but not used)
             if (one) {
@@ -891,16 +894,14 @@ __global__ void __launch_bounds__(kThreadsD, kFp4DecodeCtas) paged_gqa_decode_fp
             } else {
                 const int d = 32 * warp + lane;
                 float A = 0.f;
-                for (int i0 = 0; i0 < workers; i0 += 8) {
-                    float v[8];
+                float v[32];                               // all on their way together: one round trip
 #pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        v[i] = cluster_load(mine + (i & 3) * kStagesD * kUnitBytes + 4 * d, (i0 + i) >> 2, false);
+                for (int i = 0; i < 32; ++i)
+                    v[i] = i < workers ? cluster_load(mine + (i & 3) * kStagesD * kUnitBytes + 4 * d, i >> 2, false) : 0.f;
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const float ei = __shfl_sync(0xffffffffu, e, i0 + i);
-                        A += ei != 0.f ? ei * v[i] : 0.f;
-                    }
+                for (int i = 0; i < 32; ++i) {
+                    const float ei = __shfl_sync(0xffffffffu, e, i);
+                    A += ei != 0.f ? ei * v[i] : 0.f;
                 }
                 if (a.out_f32)
                     static_cast<float *>(a.out)[row * kHeadDim + d] = A * f;
