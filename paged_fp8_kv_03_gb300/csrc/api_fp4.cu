@@ -77,8 +77,8 @@ Fp4Window clamp_window(int window, int sinks, long long max_len)
 int decode_ctas(int batch, int max_ctas)
 {
     const size_t smem = decode_fp4_smem(batch);
-    const int one = resident_ctas(decode_fp4_kernel(false, false), 32 * kFp4DecodeWarps, smem, max_ctas);
-    const int two = one <= 0 ? 0 : resident_ctas(decode_fp4_kernel(true, false), 32 * kFp4DecodeWarps, smem, max_ctas);
+    const int one = resident_ctas(decode_fp4_kernel(false, false), decode_fp4_threads(false), smem, max_ctas);
+    const int two = one <= 0 ? 0 : resident_ctas(decode_fp4_kernel(true, false), decode_fp4_threads(false), smem, max_ctas);
     return two < one ? two : one;
 }
 
@@ -87,7 +87,7 @@ int decode_ctas(int batch, int max_ctas)
 // because both grow along the list).
 size_t decode_workspace(int batch, int hq, int hkv, int ctas)
 {
-    const size_t slots = static_cast<size_t>(ctas) * kFp4DecodeWarps + static_cast<size_t>(batch) * hkv;
+    const size_t slots = static_cast<size_t>(ctas) * kFp4DecodeWorkers + static_cast<size_t>(batch) * hkv;
     const size_t bytes = slots * static_cast<size_t>(hq / hkv) * kPartialStride * sizeof(float);
     return decode_fp4_join_bytes(batch, hkv) + ((bytes + 255) & ~size_t(255));
 }
@@ -213,7 +213,8 @@ pkv_status pkv_paged_gqa_decode_fp4(const void *q, const uint8_t *k_cache, const
     da.a = a;
     da.cluster = 0;
     if (max_ctas == 0) {
-        const int slots = resident_ctas(decode_fp4_kernel(a.out_f32, true), 32 * kFp4DecodeWarps, decode_fp4_smem(0), 0);
+        const int slots = resident_ctas(decode_fp4_kernel(a.out_f32, true), decode_fp4_threads(true),
+                                        decode_fp4_cluster_smem(), 0);
         if (slots <= 0)
             return PKV_ERR_CUDA;
         da.cluster = decode_fp4_cluster((tiles + 1) / 2, static_cast<long long>(batch) * num_kv_heads, slots);

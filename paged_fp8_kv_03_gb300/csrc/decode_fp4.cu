@@ -4,24 +4,31 @@
 //
 // What bounds it: every visible row is read once, 72 bytes of K and 72 of V,
 // so the floor is the HBM's.  At that rate an SM gets a 16-token tile (2304
-// bytes) about every 100 cycles, and widening its 4096 codes costs an SMSP's
-// issue slots and its conversion pipe (2 cycles a pair of codes and scale:
-// measured 2.5 with the multiply) more than the two matrix products do
-// (mma.sync m16n8k16: 8 cycles), so the design keeps everything else few.
+// bytes) about every 100 cycles, and an SMSP has about 760 cycles for two of
+// them.  Their 4096 codes each cost it 128 conversions to f16 pairs (2 cycles of the
+// ALU pipe), as many multiplications with a scale (2 cycles of the FMA pipe) and 34
+// mma.sync m16n8k16 (8 cycles of the tensor pipe, and about as many issue slots as
+// five other instructions): that alone measures 610 cycles, with the reads from
+// shared memory and the softmax 650.  So everything else is kept off the warps
+// that compute.
 //
 // Work split.  The visible tokens of a (sequence, kv head) segment are cut in
 // units of two 16-token tiles (a window leaves the tiles of the sinks and
 // those of the window).  The segments lie end to end in one list, kv head by
-// kv head; every warp of the grid takes an equal contiguous range of it,
+// kv head; every worker (a consumer warp) takes an equal contiguous range of it,
 // whatever the lengths.  A range cuts segments into pieces: a whole segment
 // is written out, other pieces leave a (max, sum, accumulator) state in
 // workspace slot worker + rank of the segment, and a second kernel (a
 // programmatic dependent launch) joins them in worker order.  Worker w is
 // warp w / CTAs of CTA w % CTAs, so that short lists spread over the SMs.
+// Short work (few units for every warp) runs in one launch instead: a cluster
+// of CTAs a segment, whose warps join their states in shared memory.
 //
-// A warp brings its units in by bulk copies (a tile of K and one of V are
-// 1152 contiguous bytes each) into its own ring, each stage with its own
-// mbarrier.  The codes go from shared memory straight into mma.sync
+// The list's kernel has one CTA an SM, 12 consumer warps and 4 producer warps
+// (with the registers that the consumers do not need moved to them).  A producer
+// looks up the pages of three consumers' units and brings them in by bulk
+// copies, a tile of K and one of V each 1152 contiguous bytes, into the
+// consumer's own ring.  The codes go from shared memory straight into mma.sync
 // fragments, because the order of the contracted index is free as long as
 // both operands agree on it:
 //   S^T[t][g] = K[t][:] . Q[g][:]    A = K: lane (r, c) takes the 32 dims 32c .. 32c+31 of row r,
@@ -45,14 +52,9 @@ namespace pkv {
 
 namespace {
 
-constexpr int kWarpsD = kFp4DecodeWarps;
-constexpr int kThreadsD = 32 * kWarpsD;
-constexpr int kStagesD = 3;
+constexpr unsigned kEvery = 0xffffffffu;
 constexpr int kUnitBytes = 4 * kFp4Tile;                   // K tile 0, K tile 1, V tile 0, V tile 1
 constexpr float kMoveMax = 8.f;                            // log2 units
-// Units a warp of a cluster takes at most: beyond it the list's even split and
-// a second launch for the join are faster.
-constexpr int kClusterUnits = 6;
 // Units after which a piece's accumulator is added into an fp32 copy: the
 // tensor cores add with truncation, whose error grows with the chain.
 // 2048 additions (512 units of one part) may leave 2^-12 under a bf16
@@ -61,12 +63,24 @@ template <int kParts>
 constexpr int kFoldUnits = kParts == 1 ? 512 : 64;
 constexpr uint64_t kLimitNs = 2000000000ull;
 
-struct SmemD {                                             // the ring, [warps][stages][kUnitBytes], comes first
-    static constexpr int kBar = kWarpsD * kStagesD * kUnitBytes;
-    static constexpr int kFlag = kBar + kWarpsD * kStagesD * 8;
+// The list's kernel: every warp is a worker with its own ring.
+constexpr int kListWarps = kFp4DecodeWorkers, kListThreads = 32 * kListWarps, kListCtas = 3, kStages = 3;
+struct ListSmem {                                          // the rings, [warps][kStages][kUnitBytes], come first
+    static constexpr int kFull = kListWarps * kStages * kUnitBytes;
+    static constexpr int kFlag = kFull + kListWarps * kStages * 8;
     static constexpr int kSums = kFlag + 16;
-    static constexpr int kStart = kSums + 16 * ((kWarpsD * 4 + 15) / 16);   // int [batch + 1]
+    static constexpr int kStart = kSums + 16;              // int [batch + 1]
     static size_t bytes(int batch) { return static_cast<size_t>(kStart) + 4u * (batch + 1); }
+};
+
+// The cluster's kernel: a warp's units are all on their way at once.
+constexpr int kClusterWarps = 4;
+constexpr int kClusterUnits = 6;
+struct ClusterSmem {                                       // [warps][kClusterUnits][kUnitBytes] first
+    static constexpr int kWarp = kClusterUnits * kUnitBytes;
+    static constexpr int kFull = kClusterWarps * kWarp;
+    static constexpr int kFlag = kFull + kClusterWarps * kClusterUnits * 8;
+    static constexpr int kBytes = kFlag + 16;
 };
 
 // What one sequence shows its query: tokens [0, sinks) and [from, len), as
@@ -125,7 +139,7 @@ __device__ __noinline__ bool wait_slow(uint32_t bar, uint32_t parity, volatile i
 {
     uint64_t t0 = 0;
     for (uint32_t it = 0;; ++it) {
-        if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity)))
+        if (__all_sync(kEvery, mbar_try_wait(bar, parity)))
             return true;
         if ((it & 15u) == 15u) {
             int quit = 0;
@@ -141,7 +155,7 @@ __device__ __noinline__ bool wait_slow(uint32_t bar, uint32_t parity, volatile i
                     quit = 1;
                 }
             }
-            if (__shfl_sync(0xffffffffu, quit, 0))
+            if (__shfl_sync(kEvery, quit, 0))
                 return false;
         }
     }
@@ -149,7 +163,7 @@ __device__ __noinline__ bool wait_slow(uint32_t bar, uint32_t parity, volatile i
 
 __device__ __forceinline__ bool wait_stage(uint32_t bar, uint32_t parity, volatile int *stop, int32_t *err, int lane)
 {
-    return __all_sync(0xffffffffu, mbar_try_wait(bar, parity)) || wait_slow(bar, parity, stop, err, lane);
+    return __all_sync(kEvery, mbar_try_wait(bar, parity)) || wait_slow(bar, parity, stop, err, lane);
 }
 
 __device__ __forceinline__ void lds128(uint32_t at, uint32_t (&r)[4])
@@ -399,50 +413,413 @@ __device__ __forceinline__ float cluster_load(uint32_t at, int cta, bool own)
 // kParts: f16 parts of a softmax weight.  One (rounded to f16, 2^-11, and the
 // normalising sum is of the rounded ones) is enough under a bf16 output's
 // 2^-8; two keep an fp32 output to 2^-21.
-// kCluster: short work, one cluster of da.cluster CTAs a segment.  Its warps
-// share the segment's units evenly, leave their states in shared memory and
-// join them there: one launch and no partial states in memory.
-template <int kParts, bool kCluster>
-__global__ void __launch_bounds__(kThreadsD, kFp4DecodeCtas) paged_gqa_decode_fp4_kernel(const Fp4DecodeArgs da)
+
+// A piece's running state: lane (r, c) holds dims 16r .. 16r + 15 of heads 2c,
+// 2c + 1 (acc[i][j]: dim 2i of head 2c + j, acc[i][2 + j]: dim 2i + 1), their
+// sums (sum[0], sum[1]) and maxima.
+struct State {
+    float m0, m1, acc[8][4], sum[4];
+};
+
+__device__ __forceinline__ void clear(State &s)
+{
+    s.m0 = s.m1 = -INFINITY;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        s.sum[k] = 0.f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            s.acc[i][k] = 0.f;
+    }
+}
+
+// Q as B fragment: head r, dims 32c + 4 kk + {0, 1} and {2, 3}, brought to [1, 2)
+// by a power of two, so that f16 holds all its bits; f0, f1 turn unscaled scores of
+// heads 2c, 2c + 1 into exponents of 2.
+struct Query {
+    uint32_t q[8][2];
+    float f0, f1;
+};
+
+__device__ __forceinline__ void load_rows(const Fp4AttnArgs &a, int b, int h, int r, int c, uint4 (&raw)[4])
+{
+    const int64_t row = static_cast<int64_t>(b) * a.hq + static_cast<int64_t>(h) * a.group + (r < a.group ? r : 0);
+    const uint4 *src = reinterpret_cast<const uint4 *>(a.q + row * kHeadDim + 32 * c);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        raw[i] = __ldg(src + i);
+}
+
+__device__ __forceinline__ void make_query(const Fp4AttnArgs &a, const uint4 (&raw)[4], float k_scale, int r, int c,
+                                           Query &o)
+{
+    const uint32_t *w = reinterpret_cast<const uint32_t *>(raw);
+    uint32_t top = 0;                                      // largest |q|, as its bits
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+        top = max(top, max((w[i] << 16) & 0x7FFFFFFFu, w[i] & 0x7FFF0000u));
+    top = max(top, __shfl_xor_sync(kEvery, top, 1));
+    top = max(top, __shfl_xor_sync(kEvery, top, 2));
+    const int ex = min(max(static_cast<int>(top >> 23), 1), 253);
+    const float down = __uint_as_float(static_cast<uint32_t>(254 - ex) << 23);
+    const float up = __uint_as_float(static_cast<uint32_t>(ex) << 23) * (k_scale * a.sm_scale_log2);
+    const bool on = r < a.group;
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+        o.q[i >> 1][i & 1] = f32x2_to_f16x2(on ? __uint_as_float(w[i] << 16) * down : 0.f,
+                                            on ? __uint_as_float(w[i] & 0xFFFF0000u) * down : 0.f);
+    o.f0 = __shfl_sync(kEvery, up, 8 * c);
+    o.f1 = __shfl_sync(kEvery, up, 8 * c + 4);
+}
+
+// Units of a segment of which every token is visible: past the sinks and the
+// window's first tile, before the last tokens.
+struct Inner {
+    int lo;
+    uint32_t n;
+};
+
+__device__ __forceinline__ Inner inner_units(const Sight &s)
+{
+    const int lo = (s.from > 0 ? s.first + 2 : 1) >> 1, hi = ((s.len >> 4) - s.skip) >> 1;
+    return Inner{lo, hi > lo ? static_cast<uint32_t>(hi - lo) : 0u};
+}
+
+// One unit: the 32 tokens of unit `unit` at shared address st.  done() is
+// called when the unit has been read.
+template <int kParts, typename Done>
+__device__ __forceinline__ void take_unit(uint32_t st, const LaneOffsets &o, const Query &qu, const Sight &sg,
+                                          const Inner &inner, int unit, int lane, State &s, Done done)
+{
+    const int r = lane >> 2, c = lane & 3;
+    uint64_t y[2][2];
+    {
+        RawK x[2];
+        load_k(st, o, x[0]);
+        load_k(st + kFp4Tile, o, x[1]);
+        scores(x[0], qu.q, y[0]);
+        scores(x[1], qu.q, y[1]);
+    }
+    RawV xv[2];
+    load_v(st + 2 * kFp4Tile, o, xv[0]);
+    load_v(st + 3 * kFp4Tile, o, xv[1]);
+    done();
+    uint32_t seen = kEvery;                                // the visible ones of the unit's tokens
+    float2 z[2][2];
+    const uint64_t f = pack2(qu.f0, qu.f1), nm = pack2(-s.m0, -s.m1);
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+            z[j][k] = unpack2(fma2(y[j][k], f, nm));
+    const bool edge = static_cast<uint32_t>(unit - inner.lo) >= inner.n;
+    const float top = fmaxf(max3(fmaxf(z[0][0].x, z[0][0].y), z[0][1].x, z[0][1].y),
+                            max3(fmaxf(z[1][0].x, z[1][0].y), z[1][1].x, z[1][1].y));
+    if (edge || __any_sync(kEvery, !(top <= kMoveMax))) {
+        // an edge of the sequence or of its window, or the maximum moves
+        if (edge) {
+            const int ti = 2 * unit + (lane >> 4);
+            const int t = 16 * tile_at(sg, ti) + (lane & 15);
+            seen = __ballot_sync(kEvery, ti < sg.tiles && t < sg.len && (t < sg.sinks || t >= sg.from));
+            if (seen != kEvery) {                          // values of unseen tokens may be anything
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        const uint32_t v = seen >> (16 * j + 8 * k);
+                        xv[j].s[k] &= ((v >> order(2 * c)) & 1u ? 0x00FFu : 0u) |
+                                      ((v >> order(2 * c + 1)) & 1u ? 0xFF00u : 0u);
+                    }
+            }
+        }
+        float t0 = -INFINITY, t1 = -INFINITY;
+        float2 w[2][2];
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                w[j][k] = unpack2(y[j][k]);
+                const bool on = (seen >> (16 * j + 8 * k + order(r))) & 1u;
+                w[j][k].x = on ? w[j][k].x * qu.f0 : -INFINITY;
+                w[j][k].y = on ? w[j][k].y * qu.f1 : -INFINITY;
+                t0 = fmaxf(t0, w[j][k].x);
+                t1 = fmaxf(t1, w[j][k].y);
+            }
+#pragma unroll
+        for (int d = 4; d < 32; d <<= 1) {
+            t0 = fmaxf(t0, __shfl_xor_sync(kEvery, t0, d));
+            t1 = fmaxf(t1, __shfl_xor_sync(kEvery, t1, d));
+        }
+        const float n0 = t0 > s.m0 + kMoveMax ? t0 : s.m0, n1 = t1 > s.m1 + kMoveMax ? t1 : s.m1;
+        const float g0 = n0 == s.m0 ? 1.f : ex2_approx(s.m0 - n0), g1 = n1 == s.m1 ? 1.f : ex2_approx(s.m1 - n1);
+        s.m0 = n0;
+        s.m1 = n1;
+        s.sum[0] *= g0;
+        s.sum[1] *= g1;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            s.acc[k][0] *= g0;
+            s.acc[k][1] *= g1;
+            s.acc[k][2] *= g0;
+            s.acc[k][3] *= g1;
+        }
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+                z[j][k] = make_float2(w[j][k].x - s.m0, w[j][k].y - s.m1);
+    }
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+        const float p0 = ex2_approx(z[j][0].x), p1 = ex2_approx(z[j][0].y);
+        const float p2 = ex2_approx(z[j][1].x), p3 = ex2_approx(z[j][1].y);
+        const uint32_t ha = f32x2_to_f16x2(p0, p1), hb = f32x2_to_f16x2(p2, p3);
+        uint32_t b[kParts][2];
+        b[0][0] = transpose8x8(ha);
+        b[0][1] = transpose8x8(hb);
+        if constexpr (kParts == 2) {
+            const float2 va = f16x2_to_f32x2(ha), vb = f16x2_to_f32x2(hb);
+            b[1][0] = transpose8x8(f32x2_to_f16x2(p0 - va.x, p1 - va.y));
+            b[1][1] = transpose8x8(f32x2_to_f16x2(p2 - vb.x, p3 - vb.y));
+        }
+        accumulate<kParts>(xv[j], b, s.acc, s.sum);
+    }
+}
+
+// A lane's 16 dims of head 2c + j.
+__device__ __forceinline__ void lane_dims(const State &s, int j, float (&v)[16])
+{
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+        v[2 * k] = s.acc[k][j];
+        v[2 * k + 1] = s.acc[k][j + 2];
+    }
+}
+
+// A state's row of one head: 128 dims, then maximum and sum.
+__device__ __forceinline__ void store_state(float *row, const State &s, int j, int r)
+{
+    float v[16];
+    lane_dims(s, j, v);
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+        reinterpret_cast<float4 *>(row + 16 * r)[k] = make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
+    if (r == 0)
+        *reinterpret_cast<float2 *>(row + kHeadDim) = make_float2(j ? s.m1 : s.m0, j ? s.sum[1] : s.sum[0]);
+}
+
+// Tile number in the pools of visible tile i of segment (b, h); -1: its page
+// lies outside the pool (flagged), -2: there is no such tile.
+__device__ __forceinline__ int tile_number(const Fp4AttnArgs &a, const Sight &s, int b, int h, int i)
+{
+    if (i >= s.tiles)
+        return -2;
+    int phys, row;
+    if (!seq_token_page(a, b, seq_page_log2(a, b), 16 * tile_at(s, i), phys, row)) {
+        if (a.err)
+            atomicOr(a.err, PKV_DEVERR_PAGE);
+        return -1;
+    }
+    return (phys * a.hkv + h) * (a.page_size >> 4) + (row >> 4);
+}
+
+// A tile that reads as zeros: the scales of its K and V (the whole warp; st:
+// the unit's address, j: the tile's place in it).
+__device__ __forceinline__ void zero_tile(uint32_t st, int j, int lane)
+{
+    const uint32_t at = st + j * kFp4Tile + kFp4Codes + 4 * lane;
+    asm volatile("st.shared.u32 [%0], %1;" ::"r"(at), "r"(0u) : "memory");
+    asm volatile("st.shared.u32 [%0], %1;" ::"r"(at + 2 * kFp4Tile), "r"(0u) : "memory");
+}
+
+__device__ __forceinline__ void flag_sequence(const Fp4AttnArgs &a, int b, const Sight &s)
+{
+    if (a.err == nullptr)
+        return;
+    if (seq_page_log2(a, b) < 0)
+        atomicOr(a.err, PKV_DEVERR_PAGESIZE);
+    else if (__ldg(a.seq_lens + b) != s.len)
+        atomicOr(a.err, PKV_DEVERR_SEQLEN);
+}
+
+// ---------------------------------------------------------------------- the list
+template <int kParts>
+__device__ __forceinline__ void work_list(const Fp4DecodeArgs &da, uint8_t *smem, int warp, int lane, int worker, int lo,
+                                          int n)
+{
+    const Fp4AttnArgs &a = da.a;
+    const int *start = reinterpret_cast<const int *>(smem + ListSmem::kStart);
+    volatile int *stop = reinterpret_cast<volatile int *>(smem + ListSmem::kFlag);
+    const uint32_t ring = smem_addr(smem) + warp * kStages * kUnitBytes;
+    const uint32_t full = smem_addr(smem) + ListSmem::kFull + warp * kStages * 8;
+    const uint64_t policy = l2_policy_evict_first();
+    // tile numbers, 16 units at a time, one batch ahead: lane 2i + j has tile j of unit i
+    auto look_up = [&](int u0) -> int {
+        const int u = u0 + (lane >> 1);
+        if (u >= n)
+            return -2;
+        const Place p = place_of(start, a.batch, lo + u);
+        return tile_number(a, sight_of(a, p.b), p.b, p.h, 2 * p.unit + (lane & 1));
+    };
+    int now = look_up(0), next = look_up(16);
+    const uint32_t my_dst = ring + (lane & 3) * kFp4Tile;
+    const uint8_t *my_src = lane < 2 ? a.k_cache : a.v_cache;
+    auto issue = [&](int u, int s) {                       // unit u into stage s
+        const int i = u & 15;
+        if (i == 0 && u > 0) {
+            now = next;
+            next = look_up(u + 16);
+        }
+        // (lanes 0, 1 bring K tiles, lanes 2, 3 V tiles)
+        const int t = __shfl_sync(kEvery, now, 2 * i + (lane & 1));
+        const uint32_t none = __ballot_sync(kEvery, t < 0) & 3u;
+        if (none) {
+            const uint32_t bad = __ballot_sync(kEvery, t == -1);
+            if (bad & 1u)
+                zero_tile(ring + s * kUnitBytes, 0, lane);
+            if (bad & 2u)
+                zero_tile(ring + s * kUnitBytes, 1, lane);
+            __syncwarp();
+        }
+        if (lane < 4 && (worker != da.withhold || u != 0)) {
+            const uint32_t bar = full + 8 * s;
+            // (bytes that land before they are announced are only counted early)
+            if (lane == 0)
+                mbar_arrive_expect_tx(bar, none == 0 ? 4 * kFp4Tile : none == 3u ? 0 : 2 * kFp4Tile);
+            if (t >= 0)
+                bulk_load(my_dst + s * kUnitBytes, my_src + static_cast<int64_t>(t) * kFp4Tile, kFp4Tile, bar, policy);
+        }
+    };
+    for (int v = 0; v < kStages && v < n; ++v)
+        issue(v, v);
+    bool dead = false;
+    const int r = lane >> 2, c = lane & 3;
+    const LaneOffsets offsets = lane_offsets(r, c);
+    int stage = 0;
+    uint32_t parity = 0;
+    int u = 0;
+    while (u < n && !dead) {
+        const Place p = place_of(start, a.batch, lo + u);
+        const Sight sg = sight_of(a, p.b);
+        const Inner inner = inner_units(sg);
+        const int units = start[p.b + 1] - start[p.b];
+        const int take = min(units - p.unit, n - u);
+        const bool whole = p.unit == 0 && take == units;
+        if (lane == 0) {                                   // who holds the segment's first and last unit
+            int2 *j = da.joins + p.b * a.hkv + p.h;
+            if (p.unit == 0)
+                j->x = whole ? -1 : worker;
+            if (p.unit + take == units)
+                j->y = worker;
+        }
+        Query qu;
+        {
+            uint4 raw[4];
+            load_rows(a, p.b, p.h, r, c, raw);
+            make_query(a, raw, __ldg(a.k_scale + p.h), r, c, qu);
+        }
+        const int64_t slot = static_cast<int64_t>(worker) + p.h * a.batch + p.b;
+        State s;
+        clear(s);
+        float mf0 = -INFINITY, mf1 = -INFINITY, l0 = 0.f, l1 = 0.f;   // of the units folded so far
+        for (int i = 0; i < take; ++i) {
+            if (!wait_stage(full + 8 * stage, parity, stop, a.err, lane)) {
+                dead = true;
+                break;
+            }
+            take_unit<kParts>(ring + stage * kUnitBytes, offsets, qu, sg, inner, p.unit + i, lane, s, [&]() {
+                if (u + i + kStages < n) {                 // the stage just read takes the unit after the ring's
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    issue(u + i + kStages, stage);
+                }
+            });
+            if (++stage == kStages) {
+                stage = 0;
+                parity ^= 1u;
+            }
+            if ((i + 1) % kFoldUnits<kParts> == 0 || (i + 1 == take && take > kFoldUnits<kParts>)) {
+                // the piece's own slot of the workspace holds the copy (each lane its own elements)
+                const bool old = i + 1 > kFoldUnits<kParts>, last = i + 1 == take;
+                const float g0 = old ? ex2_approx(mf0 - s.m0) : 0.f, g1 = old ? ex2_approx(mf1 - s.m1) : 0.f;
+                if (slot >= da.num_slots) {
+                    if (a.err && lane == 0)
+                        atomicOr(a.err, PKV_DEVERR_INTERNAL);
+                } else {
+                    float *at0 = da.partials + slot * a.group * kPartialStride;
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        if (2 * c + j >= a.group)
+                            continue;
+                        float *at = at0 + (2 * c + j) * kPartialStride + 16 * r;
+#pragma unroll
+                        for (int k = 0; k < 16; ++k) {
+                            float &v = s.acc[k >> 1][2 * (k & 1) + j];
+                            v += old ? at[k] * (j ? g1 : g0) : 0.f;
+                            if (!last) {
+                                at[k] = v;
+                                v = 0.f;
+                            }
+                        }
+                    }
+                }
+                l0 = l0 * g0 + s.sum[0];
+                l1 = l1 * g1 + s.sum[1];
+                s.sum[0] = last ? l0 : 0.f;
+                s.sum[1] = last ? l1 : 0.f;
+                mf0 = s.m0;
+                mf1 = s.m1;
+            }
+        }
+        if (dead)
+            break;
+        u += take;
+
+        // ---- end of piece: heads 2c, 2c + 1; dims 16 r ..
+        const int64_t row0 = static_cast<int64_t>(p.b) * a.hq + static_cast<int64_t>(p.h) * a.group;
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const int g = 2 * c + j;
+            if (g >= a.group)
+                continue;
+            if (whole) {
+                const float f = __ldg(a.v_scale + p.h) / s.sum[j];
+                float v[16];
+                lane_dims(s, j, v);
+#pragma unroll
+                for (int k = 0; k < 16; ++k)
+                    v[k] *= f;
+                store16(a, row0 + g, 16 * r, v);
+            } else if (slot < da.num_slots) {
+                store_state(da.partials + (slot * a.group + g) * kPartialStride, s, j, r);
+            } else if (a.err && r == 0) {
+                atomicOr(a.err, PKV_DEVERR_INTERNAL);
+            }
+        }
+    }
+    // After an abort: no copy may land in this ring once the warp has left.
+    if (dead && lane == 0)
+        for (int s = 0; s < kStages; ++s) {
+            // the stage's last fill: of the units issued before the wait that ran out
+            const uint64_t t0 = global_timer_ns();
+            const uint32_t par = s >= stage ? parity : parity ^ 1u;
+            while (!mbar_try_wait(full + 8 * s, par) && global_timer_ns() - t0 < kLimitNs) {
+            }
+        }
+}
+
+template <int kParts>
+__global__ void __launch_bounds__(kListThreads, kListCtas) paged_gqa_decode_fp4_kernel(const Fp4DecodeArgs da)
 {
     const Fp4AttnArgs &a = da.a;
     extern __shared__ __align__(128) uint8_t smem[];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    int *start = reinterpret_cast<int *>(smem + SmemD::kStart);
-    volatile int *stop = reinterpret_cast<volatile int *>(smem + SmemD::kFlag);
-    int *sums = reinterpret_cast<int *>(smem + SmemD::kSums);
+    int *start = reinterpret_cast<int *>(smem + ListSmem::kStart);
+    int *sums = reinterpret_cast<int *>(smem + ListSmem::kSums);
 
-    int worker, lo, n;                                     // this warp's units: n from list position lo
-    Place seg = {0, 0, 0};                                 // kCluster: the segment, and its units
-    int seg_units = 0, rank = 0;
-    if constexpr (kCluster) {
-        rank = static_cast<int>(blockIdx.x) % da.cluster;
-        const int sg = static_cast<int>(blockIdx.x) / da.cluster;
-        seg.b = sg / a.hkv;
-        seg.h = sg % a.hkv;
-        const Sight s = sight_of(a, seg.b);
-        seg_units = (s.tiles + 1) >> 1;
-        if (tid == 0) {
-            *stop = 0;
-            for (int i = 0; i < kWarpsD * kStagesD; ++i)
-                mbar_init(smem_addr(smem + SmemD::kBar) + 8 * i, 1);
-            fence_barrier_init();
-            if (a.err && rank == 0 && seg.h == 0) {
-                if (seq_page_log2(a, seg.b) < 0)
-                    atomicOr(a.err, PKV_DEVERR_PAGESIZE);
-                else if (__ldg(a.seq_lens + seg.b) != s.len)
-                    atomicOr(a.err, PKV_DEVERR_SEQLEN);
-            }
-        }
-        __syncthreads();
-        const int at = rank * kWarpsD + warp, workers = da.cluster * kWarpsD;
-        worker = static_cast<int>(blockIdx.x) * kWarpsD + warp;
-        lo = seg_units * at / workers;
-        n = seg_units * (at + 1) / workers - lo;
-    } else {
     // ---- first unit of every sequence (of one kv head): a prefix sum over the batch
     {
-        const int per = (a.batch + kThreadsD - 1) / kThreadsD;
+        const int per = (a.batch + kListThreads - 1) / kListThreads;
         const int b0 = min(a.batch, tid * per), b1 = min(a.batch, b0 + per);
         int mine = 0;
         for (int b = b0; b < b1; ++b)
@@ -450,16 +827,17 @@ __global__ void __launch_bounds__(kThreadsD, kFp4DecodeCtas) paged_gqa_decode_fp
         int incl = mine;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const int v = __shfl_up_sync(0xffffffffu, incl, o);
+            const int v = __shfl_up_sync(kEvery, incl, o);
             if (lane >= o)
                 incl += v;
         }
         if (lane == 31)
             sums[warp] = incl;
         if (tid == 0) {
-            *stop = 0;
-            for (int s = 0; s < kWarpsD * kStagesD; ++s)
-                mbar_init(smem_addr(smem + SmemD::kBar) + 8 * s, 1);
+            *reinterpret_cast<volatile int *>(smem + ListSmem::kFlag) = 0;
+            const uint32_t bars = smem_addr(smem) + ListSmem::kFull;
+            for (int i = 0; i < kListWarps * kStages; ++i)
+                mbar_init(bars + 8 * i, 1);
             fence_barrier_init();
         }
         __syncthreads();
@@ -470,14 +848,10 @@ __global__ void __launch_bounds__(kThreadsD, kFp4DecodeCtas) paged_gqa_decode_fp
             const Sight s = sight_of(a, b);
             start[b] = run;
             run += (s.tiles + 1) >> 1;
-            if (blockIdx.x == 0 && a.err) {
-                if (seq_page_log2(a, b) < 0)
-                    atomicOr(a.err, PKV_DEVERR_PAGESIZE);
-                else if (__ldg(a.seq_lens + b) != s.len)
-                    atomicOr(a.err, PKV_DEVERR_SEQLEN);
-            }
+            if (blockIdx.x == 0)
+                flag_sequence(a, b, s);
         }
-        if (tid == kThreadsD - 1)
+        if (tid == kListThreads - 1)
             start[a.batch] = run;
         __syncthreads();
     }
@@ -487,7 +861,7 @@ __global__ void __launch_bounds__(kThreadsD, kFp4DecodeCtas) paged_gqa_decode_fp
         const int b = sg / a.hkv;
         if (start[b + 1] == start[b]) {
             const int64_t row0 = static_cast<int64_t>(b) * a.hq + static_cast<int64_t>(sg % a.hkv) * a.group;
-            for (int e = tid; e < a.group * kHeadDim; e += kThreadsD) {
+            for (int e = tid; e < a.group * kHeadDim; e += kListThreads) {
                 if (a.out_f32)
                     static_cast<float *>(a.out)[row0 * kHeadDim + e] = 0.f;
                 else
@@ -500,417 +874,158 @@ __global__ void __launch_bounds__(kThreadsD, kFp4DecodeCtas) paged_gqa_decode_fp
     launch_dependents();
 
     const int total = start[a.batch] * a.hkv;
-    worker = warp * gridDim.x + blockIdx.x;
-    const int active = min(static_cast<int>(gridDim.x) * kWarpsD, total);
-    if (worker >= active)
-        return;                                            // no CTA barrier follows
-    lo = static_cast<int>(static_cast<int64_t>(total) * worker / active);
-    n = static_cast<int>(static_cast<int64_t>(total) * (worker + 1) / active) - lo;
+    const int active = min(static_cast<int>(gridDim.x) * kListWarps, total);
+    const int worker = warp * static_cast<int>(gridDim.x) + static_cast<int>(blockIdx.x);
+    if (worker < active) {
+        const int lo = static_cast<int>(static_cast<int64_t>(total) * worker / active);
+        const int n = static_cast<int>(static_cast<int64_t>(total) * (worker + 1) / active) - lo;
+        work_list<kParts>(da, smem, warp, lane, worker, lo, n);
     }
-    auto place = [&](int x) -> Place {
-        if constexpr (kCluster)
-            return Place{seg.b, seg.h, x};
-        else
-            return place_of(start, a.batch, x);
-    };
+}
 
-    const uint32_t ring = smem_addr(smem) + warp * kStagesD * kUnitBytes;
-    const uint32_t bars = smem_addr(smem + SmemD::kBar) + warp * kStagesD * 8;
-
-    // a piece's query rows (kCluster: on their way while the tiles are looked up)
+// ---------------------------------------------------------------------- the cluster
+// One cluster of da.cluster CTAs a segment.  Its warps share the segment's
+// units evenly (at most kClusterUnits each, all brought in at once), leave their
+// states in shared memory and join them there.
+template <int kParts>
+__global__ void __launch_bounds__(32 * kClusterWarps, 2) paged_gqa_decode_fp4_cluster_kernel(const Fp4DecodeArgs da)
+{
+    using S = ClusterSmem;
+    const Fp4AttnArgs &a = da.a;
+    extern __shared__ __align__(128) uint8_t smem[];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int r = lane >> 2, c = lane & 3;
-    uint4 qraw[4];
-    float kscale;
-    auto load_q = [&](const Place &p) {
-        const int64_t row = static_cast<int64_t>(p.b) * a.hq + static_cast<int64_t>(p.h) * a.group + (r < a.group ? r : 0);
-        const uint4 *src = reinterpret_cast<const uint4 *>(a.q + row * kHeadDim + 32 * c);
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            qraw[i] = __ldg(src + i);
-        kscale = __ldg(a.k_scale + p.h);
-    };
-    float vscale = 0.f;
-    if constexpr (kCluster) {
-        load_q(seg);
-        vscale = __ldg(a.v_scale + seg.h);
+    volatile int *stop = reinterpret_cast<volatile int *>(smem + S::kFlag);
+    const int rank = static_cast<int>(blockIdx.x) % da.cluster, seg = static_cast<int>(blockIdx.x) / da.cluster;
+    const int b = seg / a.hkv, h = seg % a.hkv;
+    const Sight sg = sight_of(a, b);
+    // the query rows and scales: on their way while the tiles are looked up
+    uint4 raw[4];
+    load_rows(a, b, h, r, c, raw);
+    const float k_scale = __ldg(a.k_scale + h), v_scale = __ldg(a.v_scale + h);
+    if (tid == 0) {
+        *stop = 0;
+        for (int i = 0; i < kClusterWarps * kClusterUnits; ++i)
+            mbar_init(smem_addr(smem) + S::kFull + 8 * i, 1);
+        fence_barrier_init();
+        if (rank == 0 && h == 0)
+            flag_sequence(a, b, sg);
     }
+    const int units = (sg.tiles + 1) >> 1, workers = da.cluster * kClusterWarps, at = rank * kClusterWarps + warp;
+    const int lo = units * at / workers;
+    const int n = min(units * (at + 1) / workers - lo, kClusterUnits);
+    int t = -2;                                            // lane 2i + j: tile j of unit i
+    if ((lane >> 1) < n)
+        t = tile_number(a, sg, b, h, 2 * (lo + (lane >> 1)) + (lane & 1));
+    __syncthreads();
+    const uint32_t ring = smem_addr(smem) + warp * S::kWarp;
+    const uint32_t full = smem_addr(smem) + S::kFull + warp * kClusterUnits * 8;
+    const uint32_t have = __ballot_sync(kEvery, t >= 0), bad = __ballot_sync(kEvery, t == -1);
+    for (int i = 0; bad != 0 && i < 2 * n; ++i)
+        if ((bad >> i) & 1u)
+            zero_tile(ring + (i >> 1) * kUnitBytes, i & 1, lane);
+    __syncwarp();
+    // (test facility: the withheld warp never loads its first unit)
+    const bool withheld = lane < 2 && static_cast<int>(blockIdx.x) * kClusterWarps + warp == da.withhold;
+    if ((lane >> 1) < n && !(lane & 1) && !withheld)
+        mbar_arrive_expect_tx(full + 4 * lane, 2 * kFp4Tile * __popc((have >> lane) & 3u));
+    __syncwarp();
+    if (t >= 0 && !withheld) {
+        const uint32_t dst = ring + (lane >> 1) * kUnitBytes + (lane & 1) * kFp4Tile, bar = full + 8 * (lane >> 1);
+        const uint64_t policy = l2_policy_evict_first();
+        bulk_load(dst, a.k_cache + static_cast<int64_t>(t) * kFp4Tile, kFp4Tile, bar, policy);
+        bulk_load(dst + 2 * kFp4Tile, a.v_cache + static_cast<int64_t>(t) * kFp4Tile, kFp4Tile, bar, policy);
+    }
+    __syncwarp();
 
-    const uint64_t policy = l2_policy_evict_first();
-    float *state = reinterpret_cast<float *>(smem + warp * kStagesD * kUnitBytes);   // kCluster: over the ring, at the end
-
-    // ---- tile addresses, 16 units ahead: lane 2i + j has tile j of unit i.
-    // -1: a page outside the pool; -2: no such tile.
-    auto look_up = [&](int u0) -> int {
-        const int u = u0 + (lane >> 1);
-        if (u >= n)
-            return -2;
-        const Place p = place(lo + u);
-        const Sight s = sight_of(a, p.b);
-        const int i = 2 * p.unit + (lane & 1);
-        if (i >= s.tiles)
-            return -2;
-        int phys, row;
-        if (!seq_token_page(a, p.b, seq_page_log2(a, p.b), 16 * tile_at(s, i), phys, row)) {
-            if (a.err)
-                atomicOr(a.err, PKV_DEVERR_PAGE);
-            return -1;
-        }
-        return (phys * a.hkv + p.h) * (a.page_size >> 4) + (row >> 4);
-    };
-    int now = look_up(0), next = look_up(16), base = 0;
-    uint32_t have = __ballot_sync(0xffffffffu, now >= 0);
-    uint32_t bad = 0;                                      // missing tiles, 2 bits a stage
-    const uint32_t my_dst = ring + (lane & 3) * kFp4Tile;  // lanes 0, 1 bring K tiles; 2, 3: V tiles
-    const uint8_t *my_src = lane < 2 ? a.k_cache : a.v_cache;
-    auto issue = [&](int u, int s) {                       // unit u into stage s = u % kStagesD
-        if (u >= base + 16) {
-            base += 16;
-            now = next;
-            have = __ballot_sync(0xffffffffu, now >= 0);
-            next = look_up(base + 16);
-        }
-        const int i = 2 * (u - base);
-        const int t = __shfl_sync(0xffffffffu, now, i + (lane & 1));
-        const uint32_t both = (have >> i) & 3u;
-        bad = (bad & ~(3u << (2 * s))) | ((both ^ 3u) << (2 * s));
-        if (lane < 4 && (worker != da.withhold || u != 0)) {
-            const uint32_t bar = bars + 8 * s;
-            // (bytes that land before they are announced are only counted early)
-            if (lane == 0)
-                mbar_arrive_expect_tx(bar, both == 3u ? 4 * kFp4Tile : both ? 2 * kFp4Tile : 0);
-            if (t >= 0)
-                bulk_load(my_dst + s * kUnitBytes, my_src + static_cast<int64_t>(t) * kFp4Tile, kFp4Tile, bar, policy);
-        }
-    };
-    for (int v = 0; v < kStagesD && v < n; ++v)
-        issue(v, v);
-
-    const LaneOffsets lo_off = lane_offsets(r, c);
-    int stage = 0;
-    uint32_t parity = 0;
-    bool dead = false;                                     // a wait ran out
-    int u = 0;
-    while (u < n) {
-        const Place p = place(lo + u);
-        const Sight sg = sight_of(a, p.b);
-        const int units = kCluster ? seg_units : start[p.b + 1] - start[p.b];
-        const int take = min(units - p.unit, n - u);
-        const bool whole = p.unit == 0 && take == units;
-        const int64_t row0 = static_cast<int64_t>(p.b) * a.hq + static_cast<int64_t>(p.h) * a.group;
-        if (!kCluster && lane == 0) {                      // who holds the segment's first and last unit
-            int2 *j = da.joins + p.b * a.hkv + p.h;
-            if (p.unit == 0)
-                j->x = whole ? -1 : worker;
-            if (p.unit + take == units)
-                j->y = worker;
-        }
-        // Q as B fragment: head r, dims 32c + 4 kk + {0, 1} and {2, 3}; brought
-        // to [1, 2) by a power of two, so that f16 holds all its bits.
-        uint32_t q[8][2];
-        float f0, f1;
-        {
-            if (!kCluster)
-                load_q(p);
-            const uint32_t *w = reinterpret_cast<const uint32_t *>(qraw);
-            uint32_t top = 0;                              // largest |q|, as its bits
-#pragma unroll
-            for (int i = 0; i < 16; ++i)
-                top = max(top, max((w[i] << 16) & 0x7FFFFFFFu, w[i] & 0x7FFF0000u));
-            top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-            top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-            const int ex = min(max(static_cast<int>(top >> 23), 1), 253);
-            const float down = __uint_as_float(static_cast<uint32_t>(254 - ex) << 23);
-            const float up = __uint_as_float(static_cast<uint32_t>(ex) << 23) * (kscale * a.sm_scale_log2);
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                const bool on = r < a.group;
-                q[i >> 1][i & 1] = f32x2_to_f16x2(on ? __uint_as_float(w[i] << 16) * down : 0.f,
-                                                  on ? __uint_as_float(w[i] & 0xFFFF0000u) * down : 0.f);
-            }
-            f0 = __shfl_sync(0xffffffffu, up, 8 * c);
-            f1 = __shfl_sync(0xffffffffu, up, 8 * c + 4);
-        }
-        const uint64_t f = pack2(f0, f1);
-        const int64_t slot = static_cast<int64_t>(worker) + p.h * a.batch + p.b;
-        // units of which every token is visible: past the sinks and the window's
-        // first tile, before the last tokens
-        const int full_lo = (sg.from > 0 ? sg.first + 2 : 1) >> 1;
-        const int full_hi = ((sg.len >> 4) - sg.skip) >> 1;
-        float m0 = -INFINITY, m1 = -INFINITY, mf0 = -INFINITY, mf1 = -INFINITY;
-        float l0 = 0.f, l1 = 0.f;                          // sums of the units folded so far
-        float acc[8][4], sum[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            sum[k] = 0.f;
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-                acc[i][k] = 0.f;
-        }
-
-        for (int i = 0; i < take; ++i, ++u) {
-            const uint32_t st = ring + stage * kUnitBytes;
-            if (!wait_stage(bars + 8 * stage, parity, stop, a.err, lane)) {
-                dead = true;
-                break;
-            }
-            const uint32_t missing = (bad >> (2 * stage)) & 3u;
-            uint64_t y[2][2];
-            {
-                RawK x[2];
-                load_k(st, lo_off, x[0]);
-                load_k(st + kFp4Tile, lo_off, x[1]);
-                if (missing) {                             // a missing page reads as zeros
-#pragma unroll
-                    for (int j = 0; j < 2; ++j)
-                        if (missing & (1u << j))
-                            x[j].s[0] = x[j].s[1] = 0u;
-                }
-                scores(x[0], q, y[0]);
-                scores(x[1], q, y[1]);
-            }
-            RawV xv[2];
-            load_v(st + 2 * kFp4Tile, lo_off, xv[0]);
-            load_v(st + 3 * kFp4Tile, lo_off, xv[1]);
-            if (u + kStagesD < n) {                        // the stage just read takes the unit after the ring's
-                fence_proxy_async_smem();
-                __syncwarp();
-                issue(u + kStagesD, stage);
-            }
-            if (++stage == kStagesD) {
-                stage = 0;
-                parity ^= 1u;
-            }
-            const int unit = p.unit + i;
-            uint32_t seen = 0xffffffffu;                   // the visible ones of the unit's 32 tokens
-            float2 z[2][2];
-            const uint64_t nm = pack2(-m0, -m1);
-#pragma unroll
-            for (int j = 0; j < 2; ++j)
-#pragma unroll
-                for (int k = 0; k < 2; ++k)
-                    z[j][k] = unpack2(fma2(y[j][k], f, nm));
-            const bool edge = unit < full_lo || unit >= full_hi;
-            const float top = fmaxf(max3(fmaxf(z[0][0].x, z[0][0].y), z[0][1].x, z[0][1].y),
-                                    max3(fmaxf(z[1][0].x, z[1][0].y), z[1][1].x, z[1][1].y));
-            if (edge || __any_sync(0xffffffffu, !(top <= kMoveMax))) {
-                // an edge of the sequence or of its window, or the maximum moves
-                if (edge) {
-                    const int ti = 2 * unit + (lane >> 4);
-                    const int t = 16 * tile_at(sg, ti) + (lane & 15);
-                    seen = __ballot_sync(0xffffffffu,
-                                         ti < sg.tiles && t < sg.len && (t < sg.sinks || t >= sg.from));
-                }
-                float t0 = -INFINITY, t1 = -INFINITY;
-                float2 w[2][2];
-#pragma unroll
-                for (int j = 0; j < 2; ++j)
-#pragma unroll
-                    for (int k = 0; k < 2; ++k) {
-                        w[j][k] = unpack2(y[j][k]);
-                        const bool on = (seen >> (16 * j + 8 * k + order(r))) & 1u;
-                        w[j][k].x = on ? w[j][k].x * f0 : -INFINITY;
-                        w[j][k].y = on ? w[j][k].y * f1 : -INFINITY;
-                        t0 = fmaxf(t0, w[j][k].x);
-                        t1 = fmaxf(t1, w[j][k].y);
-                    }
-#pragma unroll
-                for (int o = 4; o < 32; o <<= 1) {
-                    t0 = fmaxf(t0, __shfl_xor_sync(0xffffffffu, t0, o));
-                    t1 = fmaxf(t1, __shfl_xor_sync(0xffffffffu, t1, o));
-                }
-                const float n0 = t0 > m0 + kMoveMax ? t0 : m0, n1 = t1 > m1 + kMoveMax ? t1 : m1;
-                const float g0 = n0 == m0 ? 1.f : ex2_approx(m0 - n0), g1 = n1 == m1 ? 1.f : ex2_approx(m1 - n1);
-                m0 = n0;
-                m1 = n1;
-                sum[0] *= g0;
-                sum[1] *= g1;
-#pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    acc[k][0] *= g0;
-                    acc[k][1] *= g1;
-                    acc[k][2] *= g0;
-                    acc[k][3] *= g1;
-                }
-#pragma unroll
-                for (int j = 0; j < 2; ++j)
-#pragma unroll
-                    for (int k = 0; k < 2; ++k)
-                        z[j][k] = make_float2(w[j][k].x - m0, w[j][k].y - m1);
-            }
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                RawV &x = xv[j];
-                if (seen != 0xffffffffu || missing) {      // values of unseen tokens may be anything
-#pragma unroll
-                    for (int k = 0; k < 2; ++k) {
-                        const uint32_t s = missing & (1u << j) ? 0u : seen >> (16 * j + 8 * k);
-                        x.s[k] &= ((s >> order(2 * c)) & 1u ? 0x00FFu : 0u) |
-                                  ((s >> order(2 * c + 1)) & 1u ? 0xFF00u : 0u);
-                    }
-                }
-                const float p0 = ex2_approx(z[j][0].x), p1 = ex2_approx(z[j][0].y);
-                const float p2 = ex2_approx(z[j][1].x), p3 = ex2_approx(z[j][1].y);
-                const uint32_t ha = f32x2_to_f16x2(p0, p1), hb = f32x2_to_f16x2(p2, p3);
-                uint32_t b[kParts][2];
-                b[0][0] = transpose8x8(ha);
-                b[0][1] = transpose8x8(hb);
-                if constexpr (kParts == 2) {
-                    const float2 va = f16x2_to_f32x2(ha), vb = f16x2_to_f32x2(hb);
-                    b[1][0] = transpose8x8(f32x2_to_f16x2(p0 - va.x, p1 - va.y));
-                    b[1][1] = transpose8x8(f32x2_to_f16x2(p2 - vb.x, p3 - vb.y));
-                }
-                accumulate<kParts>(x, b, acc, sum);
-            }
-            // (a cluster's warps have fewer units than a fold)
-            if (!kCluster && ((i + 1) % kFoldUnits<kParts> == 0 || (i + 1 == take && take > kFoldUnits<kParts>))) {
-                // the piece's own slot of the workspace holds the copy (each lane its own elements)
-                const float g0 = i + 1 > kFoldUnits<kParts> ? ex2_approx(mf0 - m0) : 0.f;
-                const float g1 = i + 1 > kFoldUnits<kParts> ? ex2_approx(mf1 - m1) : 0.f;
-                const bool old = i + 1 > kFoldUnits<kParts>, last = i + 1 == take;
-                if (slot >= da.num_slots) {
-                    if (a.err && lane == 0)
-                        atomicOr(a.err, PKV_DEVERR_INTERNAL);
-                } else {
-                    float *s = da.partials + slot * a.group * kPartialStride;
-#pragma unroll
-                    for (int j = 0; j < 2; ++j) {
-                        if (2 * c + j >= a.group)
-                            continue;
-                        float *at = s + (2 * c + j) * kPartialStride + 16 * r;
-#pragma unroll
-                        for (int k = 0; k < 16; ++k) {
-                            float &v = acc[k >> 1][2 * (k & 1) + j];
-                            v += old ? at[k] * (j ? g1 : g0) : 0.f;
-                            if (!last) {
-                                at[k] = v;
-                                v = 0.f;
-                            }
-                        }
-                    }
-                }
-                l0 = l0 * g0 + sum[0];
-                l1 = l1 * g1 + sum[1];
-                sum[0] = last ? l0 : 0.f;
-                sum[1] = last ? l1 : 0.f;
-                mf0 = m0;
-                mf1 = m1;
-            }
-        }
-        if (dead)
+    const LaneOffsets offsets = lane_offsets(r, c);
+    const Inner inner = inner_units(sg);
+    Query qu;
+    make_query(a, raw, k_scale, r, c, qu);
+    State s;
+    clear(s);
+    bool dead = false;
+    for (int u = 0; u < n; ++u) {
+        if (!wait_stage(full + 8 * u, 0, stop, a.err, lane)) {
+            dead = true;
             break;
-
-        // ---- end of piece: heads 2c, 2c + 1; dims 16 r ..
-        __syncwarp();                                      // (kCluster: the state overwrites the ring)
-        l0 = sum[0];
-        l1 = sum[1];
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            const int g = 2 * c + j;
-            if (g >= a.group)
-                continue;
-            float v[16];
-#pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                v[2 * k] = acc[k][j];
-                v[2 * k + 1] = acc[k][j + 2];
-            }
-            if constexpr (kCluster) {
-                float *s = state + g * kPartialStride;
-#pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    reinterpret_cast<float4 *>(s + 16 * r)[k] = make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
-                if (r == 0)
-                    *reinterpret_cast<float2 *>(s + kHeadDim) = make_float2(j ? m1 : m0, j ? l1 : l0);
-            } else if (whole) {
-                const float f = __ldg(a.v_scale + p.h) / (j ? l1 : l0);
-#pragma unroll
-                for (int k = 0; k < 16; ++k)
-                    v[k] *= f;
-                store16(a, row0 + g, 16 * r, v);
-            } else if (slot < da.num_slots) {
-                float *s = da.partials + (slot * a.group + g) * kPartialStride;
-#pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    reinterpret_cast<float4 *>(s + 16 * r)[k] = make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
-                if (r == 0)
-                    *reinterpret_cast<float2 *>(s + kHeadDim) = make_float2(j ? m1 : m0, j ? l1 : l0);
-            } else if (a.err && r == 0) {
-                atomicOr(a.err, PKV_DEVERR_INTERNAL);
-            }
         }
+        take_unit<kParts>(ring + u * kUnitBytes, offsets, qu, sg, inner, lo + u, lane, s, []() {});
     }
-
-    // After an abort: no copy may land in this ring once the warp has left.
-    if (dead)
-        for (int v = u; v < n && v < u + kStagesD; ++v) {
+    if (dead && lane == 0)                                 // no copy may land in what the states overwrite
+        for (int u = 0; u < n; ++u) {
             const uint64_t t0 = global_timer_ns();
-            while (!mbar_try_wait(bars + 8 * (v % kStagesD), (v / kStagesD) & 1u) &&
-                   global_timer_ns() - t0 < kLimitNs) {
+            while (!mbar_try_wait(full + 8 * u, 0) && global_timer_ns() - t0 < kLimitNs) {
             }
         }
-
-    if constexpr (kCluster) {
-        // ---- join the cluster's states (at most 32, one a lane), in worker
-        // order: CTA k takes the heads k, k + CTAs, ..; of several CTAs each warp
-        // 32 dims of all of them, of one CTA a warp every fourth head
-        if ((n == 0 || dead) && lane < a.group)
-            *reinterpret_cast<float2 *>(state + lane * kPartialStride + kHeadDim) = make_float2(-INFINITY, 0.f);
-        cluster_sync(da.cluster);
-        const bool one = da.cluster == 1;
-        const int workers = da.cluster * kWarpsD;
-        for (int g = one ? warp : rank; g < a.group; g += one ? kWarpsD : da.cluster) {
-            const uint32_t mine = smem_addr(smem) + g * kPartialStride * 4;    // warp 0's state of this head, this CTA
-            float m = -INFINITY, l = 0.f;
-            if (lane < workers) {
-                const uint32_t at = mine + (lane & 3) * kStagesD * kUnitBytes + kHeadDim * 4;
-                m = cluster_load(at, lane >> 2, one);
-                l = cluster_load(at + 4, lane >> 2, one);
-            }
-            float M = m;
+    __syncwarp();
+    float *state = reinterpret_cast<float *>(smem + warp * S::kWarp);   // over the ring
+    if (n > 0 && !dead) {
 #pragma unroll
-            for (int o = 16; o > 0; o >>= 1)
-                M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-            const float e = m == -INFINITY ? 0.f : ex2_approx(m - M);
-            float sum = e * l;
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1)
-                sum += __shfl_xor_sync(0xffffffffu, sum, o);
-            const float f = seg_units == 0 ? 0.f : vscale / sum;
-            const int64_t row = static_cast<int64_t>(seg.b) * a.hq + static_cast<int64_t>(seg.h) * a.group + g;
-            // (what a warp without units left is read, but not used)
-            if (one) {
-                float4 A = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-                for (int i = 0; i < kWarpsD; ++i) {
-                    const float ei = __shfl_sync(0xffffffffu, e, i);
-                    const float4 v = *reinterpret_cast<const float4 *>(smem + i * kStagesD * kUnitBytes +
-                                                                       (g * kPartialStride + 4 * lane) * 4);
-                    A.x += ei != 0.f ? ei * v.x : 0.f;
-                    A.y += ei != 0.f ? ei * v.y : 0.f;
-                    A.z += ei != 0.f ? ei * v.z : 0.f;
-                    A.w += ei != 0.f ? ei * v.w : 0.f;
-                }
-                store4(a, row, 4 * lane, make_float4(A.x * f, A.y * f, A.z * f, A.w * f));
-            } else {
-                const int d = 32 * warp + lane;
-                float A = 0.f;
-                float v[32];                               // all on their way together: one round trip
-#pragma unroll
-                for (int i = 0; i < 32; ++i)
-                    v[i] = i < workers ? cluster_load(mine + (i & 3) * kStagesD * kUnitBytes + 4 * d, i >> 2, false) : 0.f;
-#pragma unroll
-                for (int i = 0; i < 32; ++i) {
-                    const float ei = __shfl_sync(0xffffffffu, e, i);
-                    A += ei != 0.f ? ei * v[i] : 0.f;
-                }
-                if (a.out_f32)
-                    static_cast<float *>(a.out)[row * kHeadDim + d] = A * f;
-                else
-                    static_cast<__nv_bfloat16 *>(a.out)[row * kHeadDim + d] = __float2bfloat16_rn(A * f);
-            }
-        }
-        cluster_sync(da.cluster);                          // no CTA leaves while its states are read
+        for (int j = 0; j < 2; ++j)
+            if (2 * c + j < a.group)
+                store_state(state + (2 * c + j) * kPartialStride, s, j, r);
+    } else if (lane < a.group) {
+        *reinterpret_cast<float2 *>(state + lane * kPartialStride + kHeadDim) = make_float2(-INFINITY, 0.f);
     }
+
+    // ---- join (at most 32 states, one a lane), in worker order: CTA k takes the
+    // heads k, k + CTAs, ..; of several CTAs each warp 32 dims of all of them, of
+    // one CTA a warp every fourth head
+    cluster_sync(da.cluster);
+    const bool one = da.cluster == 1;
+    for (int g = one ? warp : rank; g < a.group; g += one ? kClusterWarps : da.cluster) {
+        const uint32_t mine = smem_addr(smem) + g * kPartialStride * 4;        // warp 0's state of this head, this CTA
+        float m = -INFINITY, l = 0.f;
+        if (lane < workers) {
+            const uint32_t ml = mine + (lane & 3) * S::kWarp + kHeadDim * 4;
+            m = cluster_load(ml, lane >> 2, one);
+            l = cluster_load(ml + 4, lane >> 2, one);
+        }
+        float M = m;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1)
+            M = fmaxf(M, __shfl_xor_sync(kEvery, M, o));
+        const float e = m == -INFINITY ? 0.f : ex2_approx(m - M);
+        float sum = e * l;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1)
+            sum += __shfl_xor_sync(kEvery, sum, o);
+        const float f = units == 0 ? 0.f : v_scale / sum;
+        const int64_t row = static_cast<int64_t>(b) * a.hq + static_cast<int64_t>(h) * a.group + g;
+        // (what a warp without units left is read, but not used)
+        if (one) {
+            float4 A = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int i = 0; i < kClusterWarps; ++i) {
+                const float ei = __shfl_sync(kEvery, e, i);
+                const float4 v =
+                    *reinterpret_cast<const float4 *>(smem + i * S::kWarp + (g * kPartialStride + 4 * lane) * 4);
+                A.x += ei != 0.f ? ei * v.x : 0.f;
+                A.y += ei != 0.f ? ei * v.y : 0.f;
+                A.z += ei != 0.f ? ei * v.z : 0.f;
+                A.w += ei != 0.f ? ei * v.w : 0.f;
+            }
+            store4(a, row, 4 * lane, make_float4(A.x * f, A.y * f, A.z * f, A.w * f));
+        } else {
+            const int d = 32 * warp + lane;
+            float A = 0.f;
+            float v[32];                                   // all on their way together: one round trip
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+                v[i] = i < workers ? cluster_load(mine + (i & 3) * S::kWarp + 4 * d, i >> 2, false) : 0.f;
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+                const float ei = __shfl_sync(kEvery, e, i);
+                A += ei != 0.f ? ei * v[i] : 0.f;
+            }
+            if (a.out_f32)
+                static_cast<float *>(a.out)[row * kHeadDim + d] = A * f;
+            else
+                static_cast<__nv_bfloat16 *>(a.out)[row * kHeadDim + d] = __float2bfloat16_rn(A * f);
+        }
+    }
+    cluster_sync(da.cluster);                              // no CTA leaves while its states are read
 }
 
 // Joins the states of a segment's pieces for one query head, in worker order:
@@ -1002,25 +1117,35 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_fp4_kernel(const Fp4Deco
 
 size_t decode_fp4_smem(int batch)
 {
-    return SmemD::bytes(batch);
+    return ListSmem::bytes(batch);
+}
+
+size_t decode_fp4_cluster_smem()
+{
+    return ClusterSmem::kBytes;
 }
 
 const void *decode_fp4_kernel(bool two_parts, bool cluster)
 {
     if (cluster)
-        return two_parts ? reinterpret_cast<const void *>(&paged_gqa_decode_fp4_kernel<2, true>)
-                         : reinterpret_cast<const void *>(&paged_gqa_decode_fp4_kernel<1, true>);
-    return two_parts ? reinterpret_cast<const void *>(&paged_gqa_decode_fp4_kernel<2, false>)
-                     : reinterpret_cast<const void *>(&paged_gqa_decode_fp4_kernel<1, false>);
+        return two_parts ? reinterpret_cast<const void *>(&paged_gqa_decode_fp4_cluster_kernel<2>)
+                         : reinterpret_cast<const void *>(&paged_gqa_decode_fp4_cluster_kernel<1>);
+    return two_parts ? reinterpret_cast<const void *>(&paged_gqa_decode_fp4_kernel<2>)
+                     : reinterpret_cast<const void *>(&paged_gqa_decode_fp4_kernel<1>);
 }
 
-// A cluster a segment, of the fewest CTAs (1, 2, 4, 8) that leave a warp at
-// most kClusterUnits units, if all of them are resident at once; 0: the list.
-// (`units`: of the longest sequence, `slots`: resident CTAs.)
+int decode_fp4_threads(bool cluster)
+{
+    return cluster ? 32 * kClusterWarps : kListThreads;
+}
+
+// CTAs a segment for the cluster kernel: the fewest (1, 2, 4, 8) that leave a
+// warp at most kClusterUnits units, if all of them are resident at once; 0: the
+// list.  (`units`: of the longest sequence, `slots`: resident CTAs.)
 int decode_fp4_cluster(long long units, long long segments, int slots)
 {
     for (int c = 1; c <= 8; c *= 2)
-        if (units <= static_cast<long long>(c) * kWarpsD * kClusterUnits)
+        if (units <= static_cast<long long>(c) * kClusterWarps * kClusterUnits)
             return segments * c <= slots ? c : 0;
     return 0;
 }
@@ -1031,17 +1156,17 @@ cudaError_t launch_paged_decode_fp4(const Fp4DecodeArgs &da, int ctas, cudaStrea
     const bool two = da.a.out_f32;
     if (da.cluster > 0) {
         const dim3 grid(static_cast<unsigned>(da.a.batch * da.a.hkv * da.cluster));
-        return launch_with(two ? paged_gqa_decode_fp4_kernel<2, true> : paged_gqa_decode_fp4_kernel<1, true>, grid,
-                           kThreadsD, SmemD::bytes(0), da.cluster, false, stream, da);
+        return launch_with(two ? paged_gqa_decode_fp4_cluster_kernel<2> : paged_gqa_decode_fp4_cluster_kernel<1>, grid,
+                           32 * kClusterWarps, ClusterSmem::kBytes, da.cluster, false, stream, da);
     }
-    cudaError_t e = launch_with(two ? paged_gqa_decode_fp4_kernel<2, false> : paged_gqa_decode_fp4_kernel<1, false>,
-                                dim3(static_cast<unsigned>(ctas)), kThreadsD, SmemD::bytes(da.a.batch), 1, false, stream,
-                                da);
+    cudaError_t e = launch_with(two ? paged_gqa_decode_fp4_kernel<2> : paged_gqa_decode_fp4_kernel<1>,
+                                dim3(static_cast<unsigned>(ctas)), kListThreads, decode_fp4_smem(da.a.batch), 1, false,
+                                stream, da);
     if (e != cudaSuccess)
         return e;
     *site = "4-bit join kernel launch";
     const long long segs = static_cast<long long>(da.a.batch) * da.a.hkv;
-    const long long pieces = (static_cast<long long>(ctas) * kWarpsD + segs - 1) / segs + 1;   // a segment's, on average
+    const long long pieces = (static_cast<long long>(ctas) * kListWarps + segs - 1) / segs + 1;   // a segment's, on average
     int warps = 1;
     while (warps < kJoinWarps && warps * kJoin < pieces)
         warps *= 2;

@@ -53,10 +53,8 @@ struct Fp4AttnArgs {
     int32_t *err;
 };
 
-// Decode: warps of a CTA (each a worker of the split) and CTAs resident on an
-// SM.
-constexpr int kFp4DecodeWarps = 4;
-constexpr int kFp4DecodeCtas = 3;
+// Decode: workers of the split (consumer warps) a CTA.
+constexpr int kFp4DecodeWorkers = 4;
 
 struct Fp4DecodeArgs {
     Fp4AttnArgs a;
@@ -130,7 +128,9 @@ inline size_t prefill_fp4_bytes(int batch, long long rows)
 }
 
 size_t decode_fp4_smem(int batch);
+size_t decode_fp4_cluster_smem();
 const void *decode_fp4_kernel(bool two_parts, bool cluster);
+int decode_fp4_threads(bool cluster);
 int decode_fp4_cluster(long long units, long long segments, int slots);
 cudaError_t launch_paged_decode_fp4(const Fp4DecodeArgs &da, int ctas, cudaStream_t stream, const char **site);
 cudaError_t launch_prefill_pair(const PrefillArgs &a, const Fp4Window &win, const CUtensorMap &tm_q,
