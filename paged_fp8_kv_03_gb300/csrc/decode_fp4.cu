@@ -231,6 +231,12 @@ __device__ __forceinline__ float2 unpack2(uint64_t r)
     asm("mov.b64 {%0, %1}, %2;" : "=f"(v.x), "=f"(v.y) : "l"(r));
     return v;
 }
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b)
+{
+    uint64_t d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
 __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c)
 {
     uint64_t d;
@@ -319,17 +325,13 @@ __device__ __forceinline__ void scores(const RawK &x, const uint32_t (&q)[8][2],
     y[1] = pack2(d[2], d[3]);
 }
 
-// acc += V^T P^T and sum += 1^T P^T for a tile; b: the weights of its 16 tokens
-// (B fragment) in kParts f16 parts.
+// acc += V^T P^T for a tile; b: the weights of its 16 tokens (B fragment) in
+// kParts f16 parts.
 template <int kParts>
-__device__ __forceinline__ void accumulate(const RawV &x, const uint32_t (&b)[kParts][2], float (&acc)[8][4],
-                                           float (&sum)[4])
+__device__ __forceinline__ void accumulate(const RawV &x, const uint32_t (&b)[kParts][2], float (&acc)[8][4])
 {
     const uint32_t s0 = e4m3x2_to_f16x2(x.s[0]), s1 = e4m3x2_to_f16x2(x.s[1]);
-    constexpr uint32_t kLow = 0x0F0F0F0Fu, kOnes = 0x3C003C00u;
-#pragma unroll
-    for (int part = 0; part < kParts; ++part)
-        mma_16816(sum, kOnes, kOnes, kOnes, kOnes, b[part][0], b[part][1]);
+    constexpr uint32_t kLow = 0x0F0F0F0Fu;
 #pragma unroll
     for (int w = 0; w < 2; ++w) {
         uint32_t e[2][4], o[2][4];                         // even, odd dims of the block; pair 0, pair 1
@@ -410,26 +412,39 @@ __device__ __forceinline__ float cluster_load(uint32_t at, int cta, bool own)
     return v;
 }
 
-// kParts: f16 parts of a softmax weight.  One (rounded to f16, 2^-11, and the
-// normalising sum is of the rounded ones) is enough under a bf16 output's
-// 2^-8; two keep an fp32 output to 2^-21.
+// kParts: f16 parts of a softmax weight.  One (rounded to f16, 2^-11) is enough
+// under a bf16 output's 2^-8; two keep an fp32 output to 2^-21.  The sum that
+// normalises them is of the fp32 weights.
 
 // A piece's running state: lane (r, c) holds dims 16r .. 16r + 15 of heads 2c,
 // 2c + 1 (acc[i][j]: dim 2i of head 2c + j, acc[i][2 + j]: dim 2i + 1), their
-// sums (sum[0], sum[1]) and maxima.
+// maxima, and their sums (both heads') over its own tokens.
 struct State {
-    float m0, m1, acc[8][4], sum[4];
+    float m0, m1, acc[8][4];
+    uint64_t sum;
 };
 
 __device__ __forceinline__ void clear(State &s)
 {
     s.m0 = s.m1 = -INFINITY;
+    s.sum = 0ull;
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-        s.sum[k] = 0.f;
+    for (int k = 0; k < 4; ++k)
 #pragma unroll
         for (int i = 0; i < 8; ++i)
             s.acc[i][k] = 0.f;
+}
+
+// The heads' sums over all tokens, in every lane.
+__device__ __forceinline__ void whole_sums(const State &s, float (&l)[2])
+{
+    const float2 v = unpack2(s.sum);
+    l[0] = v.x;
+    l[1] = v.y;
+#pragma unroll
+    for (int o = 4; o < 32; o <<= 1) {
+        l[0] += __shfl_xor_sync(kEvery, l[0], o);
+        l[1] += __shfl_xor_sync(kEvery, l[1], o);
     }
 }
 
@@ -554,8 +569,7 @@ __device__ __forceinline__ void take_unit(uint32_t st, const LaneOffsets &o, con
         const float g0 = n0 == s.m0 ? 1.f : ex2_approx(s.m0 - n0), g1 = n1 == s.m1 ? 1.f : ex2_approx(s.m1 - n1);
         s.m0 = n0;
         s.m1 = n1;
-        s.sum[0] *= g0;
-        s.sum[1] *= g1;
+        s.sum = fma2(s.sum, pack2(g0, g1), 0ull);
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
             s.acc[k][0] *= g0;
@@ -573,6 +587,7 @@ __device__ __forceinline__ void take_unit(uint32_t st, const LaneOffsets &o, con
     for (int j = 0; j < 2; ++j) {
         const float p0 = ex2_approx(z[j][0].x), p1 = ex2_approx(z[j][0].y);
         const float p2 = ex2_approx(z[j][1].x), p3 = ex2_approx(z[j][1].y);
+        s.sum = add2(s.sum, add2(pack2(p0, p1), pack2(p2, p3)));
         const uint32_t ha = f32x2_to_f16x2(p0, p1), hb = f32x2_to_f16x2(p2, p3);
         uint32_t b[kParts][2];
         b[0][0] = transpose8x8(ha);
@@ -582,7 +597,7 @@ __device__ __forceinline__ void take_unit(uint32_t st, const LaneOffsets &o, con
             b[1][0] = transpose8x8(f32x2_to_f16x2(p0 - va.x, p1 - va.y));
             b[1][1] = transpose8x8(f32x2_to_f16x2(p2 - vb.x, p3 - vb.y));
         }
-        accumulate<kParts>(xv[j], b, s.acc, s.sum);
+        accumulate<kParts>(xv[j], b, s.acc);
     }
 }
 
@@ -597,7 +612,7 @@ __device__ __forceinline__ void lane_dims(const State &s, int j, float (&v)[16])
 }
 
 // A state's row of one head: 128 dims, then maximum and sum.
-__device__ __forceinline__ void store_state(float *row, const State &s, int j, int r)
+__device__ __forceinline__ void store_state(float *row, const State &s, const float (&l)[2], int j, int r)
 {
     float v[16];
     lane_dims(s, j, v);
@@ -605,7 +620,7 @@ __device__ __forceinline__ void store_state(float *row, const State &s, int j, i
     for (int k = 0; k < 4; ++k)
         reinterpret_cast<float4 *>(row + 16 * r)[k] = make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
     if (r == 0)
-        *reinterpret_cast<float2 *>(row + kHeadDim) = make_float2(j ? s.m1 : s.m0, j ? s.sum[1] : s.sum[0]);
+        *reinterpret_cast<float2 *>(row + kHeadDim) = make_float2(j ? s.m1 : s.m0, l[j]);
 }
 
 // Tile number in the pools of visible tile i of segment (b, h); -1: its page
@@ -721,7 +736,7 @@ __device__ __forceinline__ void work_list(const Fp4DecodeArgs &da, uint8_t *smem
         const int64_t slot = static_cast<int64_t>(worker) + p.h * a.batch + p.b;
         State s;
         clear(s);
-        float mf0 = -INFINITY, mf1 = -INFINITY, l0 = 0.f, l1 = 0.f;   // of the units folded so far
+        float mf0 = -INFINITY, mf1 = -INFINITY;            // maxima of the units folded so far
         for (int i = 0; i < take; ++i) {
             if (!wait_stage(full + 8 * stage, parity, stop, a.err, lane)) {
                 dead = true;
@@ -763,10 +778,6 @@ __device__ __forceinline__ void work_list(const Fp4DecodeArgs &da, uint8_t *smem
                         }
                     }
                 }
-                l0 = l0 * g0 + s.sum[0];
-                l1 = l1 * g1 + s.sum[1];
-                s.sum[0] = last ? l0 : 0.f;
-                s.sum[1] = last ? l1 : 0.f;
                 mf0 = s.m0;
                 mf1 = s.m1;
             }
@@ -776,6 +787,8 @@ __device__ __forceinline__ void work_list(const Fp4DecodeArgs &da, uint8_t *smem
         u += take;
 
         // ---- end of piece: heads 2c, 2c + 1; dims 16 r ..
+        float l[2];
+        whole_sums(s, l);
         const int64_t row0 = static_cast<int64_t>(p.b) * a.hq + static_cast<int64_t>(p.h) * a.group;
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
@@ -783,7 +796,7 @@ __device__ __forceinline__ void work_list(const Fp4DecodeArgs &da, uint8_t *smem
             if (g >= a.group)
                 continue;
             if (whole) {
-                const float f = __ldg(a.v_scale + p.h) / s.sum[j];
+                const float f = __ldg(a.v_scale + p.h) / l[j];
                 float v[16];
                 lane_dims(s, j, v);
 #pragma unroll
@@ -791,7 +804,7 @@ __device__ __forceinline__ void work_list(const Fp4DecodeArgs &da, uint8_t *smem
                     v[k] *= f;
                 store16(a, row0 + g, 16 * r, v);
             } else if (slot < da.num_slots) {
-                store_state(da.partials + (slot * a.group + g) * kPartialStride, s, j, r);
+                store_state(da.partials + (slot * a.group + g) * kPartialStride, s, l, j, r);
             } else if (a.err && r == 0) {
                 atomicOr(a.err, PKV_DEVERR_INTERNAL);
             }
@@ -961,10 +974,12 @@ __global__ void __launch_bounds__(32 * kClusterWarps, 2) paged_gqa_decode_fp4_cl
     __syncwarp();
     float *state = reinterpret_cast<float *>(smem + warp * S::kWarp);   // over the ring
     if (n > 0 && !dead) {
+        float l[2];
+        whole_sums(s, l);
 #pragma unroll
         for (int j = 0; j < 2; ++j)
             if (2 * c + j < a.group)
-                store_state(state + (2 * c + j) * kPartialStride, s, j, r);
+                store_state(state + (2 * c + j) * kPartialStride, s, l, j, r);
     } else if (lane < a.group) {
         *reinterpret_cast<float2 *>(state + lane * kPartialStride + kHeadDim) = make_float2(-INFINITY, 0.f);
     }
