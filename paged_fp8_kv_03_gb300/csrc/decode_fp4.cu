@@ -63,8 +63,10 @@ template <int kParts>
 constexpr int kFoldUnits = kParts == 1 ? 512 : 64;
 constexpr uint64_t kLimitNs = 2000000000ull;
 
-// The list's kernel: every warp is a worker with its own ring.
-constexpr int kListWarps = kFp4DecodeWorkers, kListThreads = 32 * kListWarps, kListCtas = 3, kStages = 3;
+// The list's kernel: every warp is a worker with its own ring, whose stages are
+// filled and waited for in pairs (one by one, the copies' issue and the waits cost
+// 4% more of the whole).
+constexpr int kListWarps = kFp4DecodeWorkers, kListThreads = 32 * kListWarps, kListCtas = 3, kStages = 4;
 struct ListSmem {                                          // the rings, [warps][kStages][kUnitBytes], come first
     static constexpr int kFull = kListWarps * kStages * kUnitBytes;
     static constexpr int kFlag = kFull + kListWarps * kStages * 8;
@@ -677,35 +679,34 @@ __device__ __forceinline__ void work_list(const Fp4DecodeArgs &da, uint8_t *smem
         return tile_number(a, sight_of(a, p.b), p.b, p.h, 2 * p.unit + (lane & 1));
     };
     int now = look_up(0), next = look_up(16);
-    const uint32_t my_dst = ring + (lane & 3) * kFp4Tile;
-    const uint8_t *my_src = lane < 2 ? a.k_cache : a.v_cache;
-    auto issue = [&](int u, int s) {                       // unit u into stage s
+    const uint32_t my_dst = ring + ((lane & 3) >> 1) * kUnitBytes + ((lane & 1) + 2 * ((lane >> 2) & 1)) * kFp4Tile;
+    const uint8_t *my_src = lane < 4 ? a.k_cache : a.v_cache;
+    auto issue = [&](int u, int s) {                       // units u, u + 1 (even) into stages s, s + 1
         const int i = u & 15;
         if (i == 0 && u > 0) {
             now = next;
             next = look_up(u + 16);
         }
-        // (lanes 0, 1 bring K tiles, lanes 2, 3 V tiles)
-        const int t = __shfl_sync(kEvery, now, 2 * i + (lane & 1));
-        const uint32_t none = __ballot_sync(kEvery, t < 0) & 3u;
+        // (lanes 0 .. 3 bring K tiles, lanes 4 .. 7 V tiles, of two units)
+        const int t = __shfl_sync(kEvery, now, 2 * i + (lane & 3));
+        const uint32_t none = __ballot_sync(kEvery, t < 0) & 15u;
         if (none) {
             const uint32_t bad = __ballot_sync(kEvery, t == -1);
-            if (bad & 1u)
-                zero_tile(ring + s * kUnitBytes, 0, lane);
-            if (bad & 2u)
-                zero_tile(ring + s * kUnitBytes, 1, lane);
+            for (int k = 0; k < 4; ++k)
+                if ((bad >> k) & 1u)
+                    zero_tile(ring + (s + (k >> 1)) * kUnitBytes, k & 1, lane);
             __syncwarp();
         }
-        if (lane < 4 && (worker != da.withhold || u != 0)) {
-            const uint32_t bar = full + 8 * s;
+        if (lane < 8 && (worker != da.withhold || u != 0)) {
+            const uint32_t bar = full + 4 * s;
             // (bytes that land before they are announced are only counted early)
             if (lane == 0)
-                mbar_arrive_expect_tx(bar, none == 0 ? 4 * kFp4Tile : none == 3u ? 0 : 2 * kFp4Tile);
+                mbar_arrive_expect_tx(bar, 2 * kFp4Tile * (4 - __popc(none)));
             if (t >= 0)
                 bulk_load(my_dst + s * kUnitBytes, my_src + static_cast<int64_t>(t) * kFp4Tile, kFp4Tile, bar, policy);
         }
     };
-    for (int v = 0; v < kStages && v < n; ++v)
+    for (int v = 0; v < kStages && v < n; v += 2)
         issue(v, v);
     bool dead = false;
     const int r = lane >> 2, c = lane & 3;
@@ -738,15 +739,15 @@ __device__ __forceinline__ void work_list(const Fp4DecodeArgs &da, uint8_t *smem
         clear(s);
         float mf0 = -INFINITY, mf1 = -INFINITY;            // maxima of the units folded so far
         for (int i = 0; i < take; ++i) {
-            if (!wait_stage(full + 8 * stage, parity, stop, a.err, lane)) {
+            if (!(stage & 1) && !wait_stage(full + 4 * stage, parity, stop, a.err, lane)) {
                 dead = true;
                 break;
             }
             take_unit<kParts>(ring + stage * kUnitBytes, offsets, qu, sg, inner, p.unit + i, lane, s, [&]() {
-                if (u + i + kStages < n) {                 // the stage just read takes the unit after the ring's
+                if ((stage & 1) && u + i + kStages - 1 < n) {   // the two units just read make room
                     fence_proxy_async_smem();
                     __syncwarp();
-                    issue(u + i + kStages, stage);
+                    issue(u + i + kStages - 1, stage - 1);
                 }
             });
             if (++stage == kStages) {
@@ -812,11 +813,11 @@ __device__ __forceinline__ void work_list(const Fp4DecodeArgs &da, uint8_t *smem
     }
     // After an abort: no copy may land in this ring once the warp has left.
     if (dead && lane == 0)
-        for (int s = 0; s < kStages; ++s) {
-            // the stage's last fill: of the units issued before the wait that ran out
+        for (int s = 0; s < kStages; s += 2) {
+            // the stages' last fill: of the units issued before the wait that ran out
             const uint64_t t0 = global_timer_ns();
             const uint32_t par = s >= stage ? parity : parity ^ 1u;
-            while (!mbar_try_wait(full + 8 * s, par) && global_timer_ns() - t0 < kLimitNs) {
+            while (!mbar_try_wait(full + 4 * s, par) && global_timer_ns() - t0 < kLimitNs) {
             }
         }
 }
