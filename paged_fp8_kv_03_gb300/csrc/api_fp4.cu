@@ -202,7 +202,7 @@ pkv_status pkv_paged_gqa_decode_fp4(const void *q, const uint8_t *k_cache, const
         tiles = seen < tiles ? seen : tiles;
     }
     const long long units = (tiles + 1) / 2 * batch * num_kv_heads;
-    if (units >= (int64_t(1) << 31))
+    if (units + static_cast<int64_t>(batch) * num_kv_heads >= (int64_t(1) << 31))
         return PKV_ERR_UNSUPPORTED;
     int ctas = decode_ctas(batch, max_ctas);
     if (ctas <= 0)

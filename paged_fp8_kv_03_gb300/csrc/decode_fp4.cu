@@ -163,6 +163,26 @@ __device__ __noinline__ bool wait_slow(uint32_t bar, uint32_t parity, volatile i
     }
 }
 
+// The list's position of position x of the same list with one more, empty unit
+// after every segment: an empty one counts as the next segment's first.
+__device__ __forceinline__ int real_position(const int *start, int batch, int hkv, int x)
+{
+    const int per_head = start[batch], wide = per_head + batch;
+    const int h = x / wide;
+    if (h >= hkv)
+        return per_head * hkv;
+    const int rem = x - h * wide;
+    int lo = 0, hi = batch - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (start[mid] + mid <= rem)
+            lo = mid;
+        else
+            hi = mid - 1;
+    }
+    return h * per_head + min(rem - lo, start[lo + 1]);
+}
+
 __device__ __forceinline__ bool wait_stage(uint32_t bar, uint32_t parity, volatile int *stop, int32_t *err, int lane)
 {
     return __all_sync(kEvery, mbar_try_wait(bar, parity)) || wait_slow(bar, parity, stop, err, lane);
@@ -670,7 +690,7 @@ __device__ __forceinline__ void work_list(const Fp4DecodeArgs &da, uint8_t *smem
     const uint32_t ring = smem_addr(smem) + warp * kStages * kUnitBytes;
     const uint32_t full = smem_addr(smem) + ListSmem::kFull + warp * kStages * 8;
     const uint64_t policy = l2_policy_evict_first();
-    // tile numbers, 16 units at a time, one batch ahead: lane 2i + j has tile j of unit i
+    // tile numbers, 16 units at a time, half a batch ahead: lane 2i + j has tile j of unit i
     auto look_up = [&](int u0) -> int {
         const int u = u0 + (lane >> 1);
         if (u >= n)
@@ -678,15 +698,15 @@ __device__ __forceinline__ void work_list(const Fp4DecodeArgs &da, uint8_t *smem
         const Place p = place_of(start, a.batch, lo + u);
         return tile_number(a, sight_of(a, p.b), p.b, p.h, 2 * p.unit + (lane & 1));
     };
-    int now = look_up(0), next = look_up(16);
+    int now = look_up(0), next = -2;
     const uint32_t my_dst = ring + ((lane & 3) >> 1) * kUnitBytes + ((lane & 1) + 2 * ((lane >> 2) & 1)) * kFp4Tile;
     const uint8_t *my_src = lane < 4 ? a.k_cache : a.v_cache;
     auto issue = [&](int u, int s) {                       // units u, u + 1 (even) into stages s, s + 1
         const int i = u & 15;
-        if (i == 0 && u > 0) {
+        if (i == 0 && u > 0)
             now = next;
-            next = look_up(u + 16);
-        }
+        if (i == 8)
+            next = look_up(u + 8);
         // (lanes 0 .. 3 bring K tiles, lanes 4 .. 7 V tiles, of two units)
         const int t = __shfl_sync(kEvery, now, 2 * i + (lane & 3));
         const uint32_t none = __ballot_sync(kEvery, t < 0) & 15u;
@@ -706,8 +726,7 @@ __device__ __forceinline__ void work_list(const Fp4DecodeArgs &da, uint8_t *smem
                 bulk_load(my_dst + s * kUnitBytes, my_src + static_cast<int64_t>(t) * kFp4Tile, kFp4Tile, bar, policy);
         }
     };
-    for (int v = 0; v < kStages && v < n; v += 2)
-        issue(v, v);
+    issue(0, 0);                                           // (the rest of the ring once the query is there)
     bool dead = false;
     const int r = lane >> 2, c = lane & 3;
     const LaneOffsets offsets = lane_offsets(r, c);
@@ -733,6 +752,10 @@ __device__ __forceinline__ void work_list(const Fp4DecodeArgs &da, uint8_t *smem
             uint4 raw[4];
             load_rows(a, p.b, p.h, r, c, raw);
             make_query(a, raw, __ldg(a.k_scale + p.h), r, c, qu);
+        }
+        if (u == 0) {
+            for (int v = 2; v < kStages && v < n; v += 2)
+                issue(v, v);
         }
         const int64_t slot = static_cast<int64_t>(worker) + p.h * a.batch + p.b;
         State s;
@@ -831,6 +854,7 @@ __global__ void __launch_bounds__(kListThreads, kListCtas) paged_gqa_decode_fp4_
     int *start = reinterpret_cast<int *>(smem + ListSmem::kStart);
     int *sums = reinterpret_cast<int *>(smem + ListSmem::kSums);
 
+    bool no_empty;
     // ---- first unit of every sequence (of one kv head): a prefix sum over the batch
     {
         const int per = (a.batch + kListThreads - 1) / kListThreads;
@@ -867,7 +891,10 @@ __global__ void __launch_bounds__(kListThreads, kListCtas) paged_gqa_decode_fp4_
         }
         if (tid == kListThreads - 1)
             start[a.batch] = run;
-        __syncthreads();
+        bool some = true;                                  // this thread's sequences all have tokens
+        for (int b = b0; b < b1; ++b)
+            some = some && (b + 1 < b1 ? start[b + 1] : run) > start[b];
+        no_empty = __syncthreads_and(some) != 0;
     }
 
     // ---- sequences with no tokens: zero rows, and nothing to join
@@ -891,8 +918,18 @@ __global__ void __launch_bounds__(kListThreads, kListCtas) paged_gqa_decode_fp4_
     const int active = min(static_cast<int>(gridDim.x) * kListWarps, total);
     const int worker = warp * static_cast<int>(gridDim.x) + static_cast<int>(blockIdx.x);
     if (worker < active) {
-        const int lo = static_cast<int>(static_cast<int64_t>(total) * worker / active);
-        const int n = static_cast<int>(static_cast<int64_t>(total) * (worker + 1) / active) - lo;
+        // A range with a segment's end in it has one more piece to set up and to
+        // store, which costs about a unit's time: the ranges are equal in a list
+        // with an empty unit after every segment.  (Two units a range, and no
+        // empty sequence: then every range still holds a unit, as the join needs.)
+        const bool wide = no_empty && total >= 2 * active;
+        const int length = total + (wide ? a.batch * a.hkv : 0);
+        const int each = length / active, more = length - each * active;   // the first `more` ranges: one longer
+        const int w = worker + (lane & 1);                 // even lanes: where the range begins, odd ones: where it ends
+        int edge = w * each + min(w, more);
+        if (wide)
+            edge = real_position(start, a.batch, a.hkv, edge);
+        const int lo = __shfl_sync(kEvery, edge, 0), n = __shfl_sync(kEvery, edge, 1) - lo;
         work_list<kParts>(da, smem, warp, lane, worker, lo, n);
     }
 }
