@@ -133,6 +133,7 @@ const void *decode_fp4_kernel(bool two_parts, bool cluster);
 int decode_fp4_threads(bool cluster);
 int decode_fp4_cluster(long long units, long long segments, int slots);
 cudaError_t launch_paged_decode_fp4(const Fp4DecodeArgs &da, int ctas, cudaStream_t stream, const char **site);
+cudaError_t launch_widen_fp4(const PrefillArgs &a, const Fp4Window &win, cudaStream_t stream);
 cudaError_t launch_prefill_pair(const PrefillArgs &a, const Fp4Window &win, const CUtensorMap &tm_q,
                                 const CUtensorMap &tm_k16, const CUtensorMap &tm_v16, cudaStream_t stream);
 cudaError_t launch_kv_append_fp4(const Fp4RowArgs &a, cudaStream_t stream);

@@ -111,11 +111,7 @@ __device__ __forceinline__ uint32_t f16x2_to_bf16x2(uint32_t h)
 // row of one kv head) of K and of V reads them through the block table and
 // writes 32 bytes of 16-bit values to the region.  Rows from L up to the next
 // multiple of 128 are zeros.
-// (kFp4: the 4-bit cache, one thread per block of 16 codes and its scale; e s
-// has 6 significant bits, exact in bf16 and f16.  Keys no query sees under the
-// window get no rows, or zero rows within a tile that others are seen of.)
-template <bool kFp4>
-__global__ void __launch_bounds__(256) kv_widen_kernel(const PrefillArgs a, const Fp4Window win)
+__global__ void __launch_bounds__(256) kv_widen_kernel(const PrefillArgs a)
 {
     extern __shared__ int off[];                         // [batch + 1], then 8 warp sums
     int *warp_sum = off + a.batch + 1;
@@ -126,7 +122,7 @@ __global__ void __launch_bounds__(256) kv_widen_kernel(const PrefillArgs a, cons
         const int b0 = min(a.batch, tid * chunk), b1 = min(a.batch, b0 + chunk);
         long long local = 0;
         for (int b = b0; b < b1; ++b)
-            local += region_tiles<kFp4>(a, win, b);
+            local += region_tiles<false>(a, Fp4Window{0, 0}, b);
         // saturate: nothing past cap_tiles + 1 matters
         int loc = static_cast<int>(local < cap_tiles + 1 ? local : cap_tiles + 1);
         int incl = loc;
@@ -145,7 +141,7 @@ __global__ void __launch_bounds__(256) kv_widen_kernel(const PrefillArgs a, cons
         int run = min(base + incl - loc, static_cast<int>(cap_tiles + 1));
         for (int b = b0; b < b1; ++b) {
             off[b] = run;
-            run = static_cast<int>(min(run + region_tiles<kFp4>(a, win, b), cap_tiles + 1));
+            run = static_cast<int>(min(run + region_tiles<false>(a, Fp4Window{0, 0}, b), cap_tiles + 1));
         }
         if (tid == 255)
             off[a.batch] = min(base + incl, static_cast<int>(cap_tiles + 1));
@@ -177,56 +173,22 @@ __global__ void __launch_bounds__(256) kv_widen_kernel(const PrefillArgs a, cons
         if (off[b + 1] > cap_tiles)
             continue;                                           // region past the workspace: flagged above
         const int L = __ldg(a.seq_lens + b);
-        KeyTiles kt = {0, 0, 0, 0};
-        if (kFp4)
-            kt = key_tiles<kFp4>(win, L - (__ldg(a.cu_q + b + 1) - __ldg(a.cu_q + b)));
-        const int pad = ((L + kKeys - 1) / kKeys - kt.skip) * kKeys;
+        const int pad = ((L + kKeys - 1) / kKeys) * kKeys;
         const int local = static_cast<int>(R - static_cast<int64_t>(off[b]) * 128);
-        const int h = local / pad, vr = local - h * pad;
-        const int r = vr < kt.first * kKeys ? vr : vr + kt.skip * kKeys;   // the key
-        const int64_t dst = R * kHeadDim + 16 * e;              // in 16-bit elements
-        int pg = 0, row = 0;
-        bool have = false;
-        if (r < L && (!kFp4 || r < kt.sinks || r >= kt.from)) {
-            have = seq_token_page(a, b, seq_page_log2(a, b), r, pg, row);
-            if (!have && e == 0 && a.err)
-                atomicOr(a.err, PKV_DEVERR_PAGE);
-        }
-        uint4 lo4, hi4;
-        if constexpr (kFp4) {
-            uint32_t k[2][4] = {}, v[2][4] = {};
-            if (have) {
-                const int64_t tile = fp4_tile_offset(pg, h, row, a.hkv, a.page_size);
-                const int64_t codes = tile + (row & 15) * 64 + 8 * e, scale = tile + kFp4Codes + (row & 15) * 8 + e;
-                const uint2 kc = __ldg(reinterpret_cast<const uint2 *>(a.k_cache + codes));
-                const uint2 vc = __ldg(reinterpret_cast<const uint2 *>(a.v_cache + codes));
-                const __half2 ks = __float2half2_rn(e4m3_value(__ldg(a.k_cache + scale)));
-                const __half2 vs = __float2half2_rn(e4m3_value(__ldg(a.v_cache + scale)));
-                e2m1x8_to_f16x8(kc.x, k[0]);
-                e2m1x8_to_f16x8(kc.y, k[1]);
-                e2m1x8_to_f16x8(vc.x, v[0]);
-                e2m1x8_to_f16x8(vc.y, v[1]);
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const __half2 kp = __hmul2(*reinterpret_cast<const __half2 *>(&k[i >> 2][i & 3]), ks);
-                    const __half2 vp = __hmul2(*reinterpret_cast<const __half2 *>(&v[i >> 2][i & 3]), vs);
-                    k[i >> 2][i & 3] = f16x2_to_bf16x2(*reinterpret_cast<const uint32_t *>(&kp));
-                    v[i >> 2][i & 3] = *reinterpret_cast<const uint32_t *>(&vp);
-                }
-            }
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                reinterpret_cast<uint4 *>(a.k16 + dst)[i] = make_uint4(k[i][0], k[i][1], k[i][2], k[i][3]);
-                reinterpret_cast<uint4 *>(a.v16 + dst)[i] = make_uint4(v[i][0], v[i][1], v[i][2], v[i][3]);
-            }
-            continue;
-        }
+        const int h = local / pad, r = local - h * pad;
         uint4 k = make_uint4(0, 0, 0, 0), v = make_uint4(0, 0, 0, 0);
-        if (have) {
-            const int64_t src = ((static_cast<int64_t>(pg) * a.hkv + h) * a.page_size + row) * kHeadDim + 16 * e;
-            k = __ldg(reinterpret_cast<const uint4 *>(a.k_cache + src));
-            v = __ldg(reinterpret_cast<const uint4 *>(a.v_cache + src));
+        if (r < L) {
+            int pg, row;
+            if (seq_token_page(a, b, seq_page_log2(a, b), r, pg, row)) {
+                const int64_t src = ((static_cast<int64_t>(pg) * a.hkv + h) * a.page_size + row) * kHeadDim + 16 * e;
+                k = __ldg(reinterpret_cast<const uint4 *>(a.k_cache + src));
+                v = __ldg(reinterpret_cast<const uint4 *>(a.v_cache + src));
+            } else if (e == 0 && a.err) {
+                atomicOr(a.err, PKV_DEVERR_PAGE);
+            }
         }
+        const int64_t dst = R * kHeadDim + 16 * e;              // in 16-bit elements
+        uint4 lo4, hi4;
         e4m3x4_to_f16x4(k.x, lo4.x, lo4.y);
         e4m3x4_to_f16x4(k.y, lo4.z, lo4.w);
         e4m3x4_to_f16x4(k.z, hi4.x, hi4.y);
@@ -730,9 +692,8 @@ cudaError_t raise_limit(PrefillKernel kernel, int which)
     return cudaSuccess;
 }
 
-// The widening launch.
-template <bool kFp4>
-cudaError_t launch_widen(const PrefillArgs &a, const Fp4Window &win, cudaStream_t stream)
+// The widening launch of the FP8 call.
+cudaError_t launch_widen(const PrefillArgs &a, cudaStream_t stream)
 {
     const int64_t pieces = a.rows_cap * 8;
     int64_t wblocks = (pieces + 255) / 256;
@@ -743,12 +704,12 @@ cudaError_t launch_widen(const PrefillArgs &a, const Fp4Window &win, cudaStream_
         wblocks = 1;                                     // CTA 0 always lays out the regions
     const size_t wsmem = (static_cast<size_t>(a.batch) + 1 + 8) * sizeof(int);
     if (wsmem > 48 * 1024) {
-        const cudaError_t e = cudaFuncSetAttribute(kv_widen_kernel<kFp4>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        const cudaError_t e = cudaFuncSetAttribute(kv_widen_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                    static_cast<int>(wsmem));
         if (e != cudaSuccess)
             return e;
     }
-    kv_widen_kernel<kFp4><<<static_cast<unsigned>(wblocks), 256, wsmem, stream>>>(a, win);
+    kv_widen_kernel<<<static_cast<unsigned>(wblocks), 256, wsmem, stream>>>(a);
     return cudaGetLastError();
 }
 
@@ -777,7 +738,7 @@ cudaError_t launch_paged_prefill(const PrefillArgs &a, const CUtensorMap &tm_q, 
     const Fp4Window none = {0, 0};
     cudaError_t e = raise_limit(paged_prefill_kernel<false>, 0);
     if (e == cudaSuccess)
-        e = launch_widen<false>(a, none, stream);
+        e = launch_widen(a, stream);
     return e == cudaSuccess ? launch_attention<false>(a, none, tm_q, tm_k16, tm_v16, stream) : e;
 }
 
@@ -790,7 +751,7 @@ cudaError_t launch_paged_prefill_fp4(const PrefillArgs &a, const Fp4Window &win,
     if (a.out_f32)
         e = win.window > 0 ? raise_limit(paged_prefill_kernel<true>, 1) : raise_limit(paged_prefill_kernel<false>, 0);
     if (e == cudaSuccess)
-        e = launch_widen<true>(a, win, stream);
+        e = launch_widen_fp4(a, win, stream);
     if (e != cudaSuccess)
         return e;
     if (!a.out_f32)

@@ -1,8 +1,8 @@
-// The attention of paged_prefill_fp4 with a bf16 output, on the
-// 5th-generation tensor cores, over the 16-bit copies that the widening kernel
-// made (K as bf16, V as f16: e s has 6 significant bits, exact in both).
+// paged_prefill_fp4: the widening of the 4-bit cache to 16-bit copies (K as bf16,
+// V as f16: e s has 6 significant bits, exact in both), and the attention over
+// them with a bf16 output, on the 5th-generation tensor cores.
 //
-// What bounds it.  A tile of 128 rows (tokens x query heads of the group) and
+// What bounds the attention.  A tile of 128 rows (tokens x query heads of the group) and
 // 128 keys costs the tensor cores 2 x 128^3 multiply-adds and the softmax 128^2
 // exponentials.  One f16 part of P is enough under a bf16 output's 2^-8 (the
 // weights are rounded once, 2^-11 each), so the products are two thirds of
@@ -60,6 +60,124 @@ struct P2 {
 };
 static_assert(P2::bytes() <= 232448, "prefill tile buffers exceed the shared memory of one CTA");
 
+// ---------------------------------------------------------------------- widening
+// The 16-bit copies' regions are laid out as the FP8 widening kernel's: tile_off
+// is the prefix sum of the sequences' 128-row tiles (a region past the workspace
+// is flagged), K and V of a sequence's kv head in consecutive rows, zero rows up
+// to a whole tile.  Keys that no query sees under the window get no tile, or
+// zero rows in a tile others are seen of.
+//
+// Bytes bound it: 144 of the cache to 512 of the copies a row.  A CTA takes a
+// tile (or a quarter of one, where there are few), so what the tile belongs to is
+// found once; a thread takes 8 values of kRowsEach of its rows, of K and of V, 16
+// lanes write a row's 256 bytes.
+template <int kRowsEach>
+__global__ void __launch_bounds__(256) kv_widen_fp4_kernel(const PrefillArgs a, const Fp4Window win)
+{
+    constexpr int kPieces = 8 / kRowsEach;               // CTAs' steps a tile
+    extern __shared__ int off[];                         // [batch + 1], then 8 warp sums
+    int *warp_sum = off + a.batch + 1;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const long long cap_tiles = a.rows_cap / kKeys;
+    const int most = static_cast<int>(cap_tiles + 1);    // sums saturate just past the workspace
+    {
+        const int chunk = (a.batch + 255) / 256;
+        const int b0 = min(a.batch, tid * chunk), b1 = min(a.batch, b0 + chunk);
+        long long local = 0;
+        for (int b = b0; b < b1; ++b)
+            local += region_tiles<true>(a, win, b);
+        const int loc = static_cast<int>(local < most ? local : most);
+        int incl = loc;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int v = __shfl_up_sync(kAll, incl, o);
+            if (lane >= o)
+                incl = min(incl + v, most);
+        }
+        if (lane == 31)
+            warp_sum[warp] = incl;
+        __syncthreads();
+        int base = 0;
+        for (int w = 0; w < warp; ++w)
+            base = min(base + warp_sum[w], most);
+        int run = min(base + incl - loc, most);
+        for (int b = b0; b < b1; ++b) {
+            off[b] = run;
+            run = static_cast<int>(min(run + region_tiles<true>(a, win, b), static_cast<long long>(most)));
+        }
+        if (tid == 255)
+            off[a.batch] = min(base + incl, most);
+        __syncthreads();
+        if (blockIdx.x == 0)
+            for (int b = tid; b <= a.batch; b += 256) {
+                a.tile_off[b] = off[b];
+                if (b < a.batch && off[b + 1] > cap_tiles && off[b + 1] > off[b] && a.err)
+                    atomicOr(a.err, PKV_DEVERR_SEQLEN);  // its region does not fit the workspace
+            }
+    }
+    const int part = tid & 15;                           // dims 8 part .. 8 part + 7
+    const int tiles = static_cast<int>(min(static_cast<long long>(off[a.batch]), cap_tiles));
+    for (int piece = blockIdx.x; piece < tiles * kPieces; piece += gridDim.x) {
+        const int tile = piece / kPieces, first = (piece % kPieces) * 16 * kRowsEach + (tid >> 4);   // first row
+        int lo = 0, hi = a.batch - 1;                    // the sequence whose region holds the tile
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            if (off[mid] <= tile)
+                lo = mid;
+            else
+                hi = mid - 1;
+        }
+        const int b = lo;
+        if (off[b + 1] > cap_tiles)
+            continue;                                    // region past the workspace: flagged above
+        const int L = __ldg(a.seq_lens + b), lp = seq_page_log2(a, b);
+        const KeyTiles kt = key_tiles<true>(win, L - (__ldg(a.cu_q + b + 1) - __ldg(a.cu_q + b)));
+        const int per_head = (off[b + 1] - off[b]) / a.hkv;
+        const int h = (tile - off[b]) / per_head, vt = (tile - off[b]) - h * per_head;
+        const int key0 = (vt < kt.first ? vt : vt + kt.skip) * kKeys;
+        uint32_t kc[kRowsEach], vc[kRowsEach];
+        uint8_t ks[kRowsEach], vs[kRowsEach];
+#pragma unroll
+        for (int i = 0; i < kRowsEach; ++i) {
+            const int t = key0 + first + 16 * i;
+            kc[i] = vc[i] = 0;
+            ks[i] = vs[i] = 0;
+            if (t < L && (t < kt.sinks || t >= kt.from)) {
+                int pg, row;
+                if (seq_token_page(a, b, lp, t, pg, row)) {
+                    const int64_t at = fp4_tile_offset(pg, h, row, a.hkv, a.page_size);
+                    const int64_t codes = at + (row & 15) * 64 + 4 * part, scale = at + kFp4Codes + (row & 15) * 8 + (part >> 1);
+                    kc[i] = __ldg(reinterpret_cast<const uint32_t *>(a.k_cache + codes));
+                    vc[i] = __ldg(reinterpret_cast<const uint32_t *>(a.v_cache + codes));
+                    ks[i] = __ldg(a.k_cache + scale);
+                    vs[i] = __ldg(a.v_cache + scale);
+                } else if (part == 0 && a.err) {
+                    atomicOr(a.err, PKV_DEVERR_PAGE);
+                }
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < kRowsEach; ++i) {
+            const int64_t at = (static_cast<int64_t>(tile) * kKeys + first + 16 * i) * kHeadDim + 8 * part;
+            const __half2 sk = __float2half2_rn(e4m3_value(ks[i])), sv = __float2half2_rn(e4m3_value(vs[i]));
+            uint32_t k[4], v[4];
+            e2m1x8_to_f16x8(kc[i], k);
+            e2m1x8_to_f16x8(vc[i], v);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const float2 kf = __half22float2(__hmul2(*reinterpret_cast<const __half2 *>(&k[e]), sk));
+                const __nv_bfloat162 kb = __floats2bfloat162_rn(kf.x, kf.y);
+                const __half2 vh = __hmul2(*reinterpret_cast<const __half2 *>(&v[e]), sv);
+                k[e] = *reinterpret_cast<const uint32_t *>(&kb);
+                v[e] = *reinterpret_cast<const uint32_t *>(&vh);
+            }
+            *reinterpret_cast<uint4 *>(a.k16 + at) = make_uint4(k[0], k[1], k[2], k[3]);
+            *reinterpret_cast<uint4 *>(a.v16 + at) = make_uint4(v[0], v[1], v[2], v[3]);
+        }
+    }
+}
+
+// ---------------------------------------------------------------------- attention
 template <bool kWin>
 __global__ void __launch_bounds__(kThreads2, 1)
     paged_prefill_pair_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
@@ -292,20 +410,24 @@ __global__ void __launch_bounds__(kThreads2, 1)
             if (vis < kKeys - 1) {
 #pragma unroll
                 for (int c = 0; c < 4; ++c)
+                    if (vis < 32 * c + 31) {
 #pragma unroll
-                    for (int k = 0; k < 32; ++k)
-                        if (32 * c + k > vis)
-                            v[c][k] = __float_as_uint(-INFINITY);
+                        for (int k = 0; k < 32; ++k)
+                            if (32 * c + k > vis)
+                                v[c][k] = __float_as_uint(-INFINITY);
+                    }
             }
             if (kWin) {
                 const int out = vis - win.window, snk = win.sinks - key0;
                 if (out >= 0 && snk < kKeys) {
 #pragma unroll
                     for (int c = 0; c < 4; ++c)
+                        if (out >= 32 * c && snk < 32 * c + 32) {
 #pragma unroll
-                        for (int k = 0; k < 32; ++k)
-                            if (32 * c + k <= out && 32 * c + k >= snk)
-                                v[c][k] = __float_as_uint(-INFINITY);
+                            for (int k = 0; k < 32; ++k)
+                                if (32 * c + k <= out && 32 * c + k >= snk)
+                                    v[c][k] = __float_as_uint(-INFINITY);
+                        }
                 }
             }
             float mx[8];
@@ -409,6 +531,18 @@ std::mutex g_pair_mu;
 unsigned long long g_pair_ctx[64][2] = {};   // per device and kernel: the context its limit was raised in
 
 }  // namespace
+
+// The widening launch of the 4-bit calls.
+cudaError_t launch_widen_fp4(const PrefillArgs &a, const Fp4Window &win, cudaStream_t stream)
+{
+    const int64_t tiles = a.rows_cap / kKeys, most = static_cast<int64_t>(device_sm_count()) * 8;
+    const size_t smem = (static_cast<size_t>(a.batch) + 1 + 8) * sizeof(int);
+    if (tiles * 4 <= most)                               // (CTA 0 always lays out the regions)
+        kv_widen_fp4_kernel<2><<<static_cast<unsigned>(tiles < 1 ? 1 : tiles * 4), 256, smem, stream>>>(a, win);
+    else
+        kv_widen_fp4_kernel<8><<<static_cast<unsigned>(tiles < most ? tiles : most), 256, smem, stream>>>(a, win);
+    return cudaGetLastError();
+}
 
 // The attention launch alone: the widening kernel has been enqueued before.
 cudaError_t launch_prefill_pair(const PrefillArgs &a, const Fp4Window &win, const CUtensorMap &tm_q,
