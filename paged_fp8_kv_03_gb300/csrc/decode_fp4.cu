@@ -40,7 +40,7 @@
 // weights leave the S^T fragment as B operand through two 8x8 transposes.
 // Heads are columns of both results, so the running maximum and sum of a head
 // sit in the lanes that hold its accumulator and a rescale needs no exchange;
-// the maximum is moved only when a score exceeds it by more than 2^8.
+// the maximum is moved only when a score exceeds it by more than 2^14.
 //
 // Every wait on an mbarrier is bounded (2 s): on expiry the kernel raises
 // PKV_DEVERR_TIMEOUT, stops issuing copies, drains those in flight, returns.
@@ -54,7 +54,9 @@ namespace {
 
 constexpr unsigned kEvery = 0xffffffffu;
 constexpr int kUnitBytes = 4 * kFp4Tile;                   // K tile 0, K tile 1, V tile 0, V tile 1
-constexpr float kMoveMax = 8.f;                            // log2 units
+// The running maximum moves only when a score exceeds it by more than this
+// (log2 units): weights up to 2^14 are within f16.
+constexpr float kMoveMax = 14.f;
 // Units after which a piece's accumulator is added into an fp32 copy: the
 // tensor cores add with truncation, whose error grows with the chain.
 // 2048 additions (512 units of one part) may leave 2^-12 under a bf16

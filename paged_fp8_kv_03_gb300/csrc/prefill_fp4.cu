@@ -38,6 +38,9 @@ namespace {
 constexpr int kStages2 = 2;                      // K and V rings
 constexpr int kWarp0 = 2;                        // first softmax warp
 constexpr int kThreads2 = 32 * (kWarp0 + 8);
+// The running maximum moves only when it is exceeded by more than this (log2
+// units): P <= 2^14 is within f16, and moving it costs a pass over the accumulator.
+constexpr float kMoveMax = 14.f;
 constexpr uint32_t kScoreCol = 128, kOutCol = 256;   // tile x: scores at 128 x, accumulator at 256 + 128 x
 
 // Shared memory, offsets from a 1024-byte aligned base.  Operand tiles are
@@ -439,8 +442,7 @@ __global__ void __launch_bounds__(kThreads2, 1)
                 mx[k & 7] = max3(mx[k & 7], __uint_as_float(v[k >> 4][2 * (k & 15)]),
                                  __uint_as_float(v[k >> 4][2 * (k & 15) + 1]));
             const float top = fmaxf(max3(mx[0], mx[1], mx[2]), max3(max3(mx[3], mx[4], mx[5]), mx[6], mx[7])) * sl2;
-            // The maximum moves only when it is exceeded by more than 2^8.
-            const bool need = top > m + 8.f;
+            const bool need = top > m + kMoveMax;
             if (__any_sync(kAll, need)) {
                 const float mn = need ? top : m;
                 const float f = need ? ex2_approx(m - mn) : 1.f;
