@@ -528,15 +528,17 @@ pkv_status pkv_kv_read_fp4(const int64_t *slot_mapping, int64_t num_tokens,
  * and sees the tokens named above; values are e * s times the head's scale.
  * Arguments, errors, clamping, zero rows for empty sequences and determinism
  * as pkv_paged_gqa_decode; q may have any finite bf16 values.  A bf16 output
- * rounds the softmax weights once to f16 before they meet V (the sum that
- * normalises them is of the rounded weights); an fp32 output keeps them as
- * two f16 parts.
+ * rounds the softmax weights once to f16 before they meet V; an fp32 output
+ * keeps them as two f16 parts.  One launch where max_seq_len (or the window)
+ * bounds every sequence to short work and max_ctas is 0, else two.
  *
  *   window, sinks  >= 0.
  *   workspace      device, >= pkv_decode_fp4_workspace_size(...) bytes for the
  *                  same sizes, 256-byte aligned; needs no initialisation, not
  *                  to be shared by calls that overlap on the GPU.
- * num_pages * num_kv_heads * page_size / 16 must be below 2^31.
+ * num_pages * num_kv_heads * page_size / 16 must be below 2^31, and so must
+ * num_kv_heads times the sum over the batch of the 32-token units that
+ * max_seq_len, or the window and the sinks, allow a sequence (plus one each).
  */
 size_t pkv_decode_fp4_workspace_size(int batch, int num_q_heads, int num_kv_heads,
                                      int head_dim, int max_seq_len, int page_size, int max_ctas);

@@ -411,7 +411,7 @@ extern "C" {
 
 int pkv_version(void)
 {
-    return (1 << 16) | 0;
+    return (1 << 16) | 1;
 }
 
 void pkv_test_withhold_load(int index)
