@@ -9,13 +9,13 @@
 // ALU pipe), as many multiplications with a scale (2 cycles of the FMA pipe) and 34
 // mma.sync m16n8k16 (8 cycles of the tensor pipe, and about as many issue slots as
 // five other instructions): that alone measures 610 cycles, with the reads from
-// shared memory and the softmax 650.  So everything else is kept off the warps
-// that compute.
+// shared memory and the softmax 650.  So HBM and issue slots are both nearly
+// full, and everything beside those instructions has to be few.
 //
 // Work split.  The visible tokens of a (sequence, kv head) segment are cut in
 // units of two 16-token tiles (a window leaves the tiles of the sinks and
 // those of the window).  The segments lie end to end in one list, kv head by
-// kv head; every worker (a consumer warp) takes an equal contiguous range of it,
+// kv head; every worker (a warp) takes an equal contiguous range of it,
 // whatever the lengths.  A range cuts segments into pieces: a whole segment
 // is written out, other pieces leave a (max, sum, accumulator) state in
 // workspace slot worker + rank of the segment, and a second kernel (a
@@ -24,11 +24,13 @@
 // Short work (few units for every warp) runs in one launch instead: a cluster
 // of CTAs a segment, whose warps join their states in shared memory.
 //
-// The list's kernel has one CTA an SM, 12 consumer warps and 4 producer warps
-// (with the registers that the consumers do not need moved to them).  A producer
-// looks up the pages of three consumers' units and brings them in by bulk
-// copies, a tile of K and one of V each 1152 contiguous bytes, into the
-// consumer's own ring.  The codes go from shared memory straight into mma.sync
+// The list's kernel has three CTAs an SM of four warps, and each warp feeds itself: it
+// looks up its units' pages half a batch ahead and brings the tiles in by bulk
+// copies, a tile of K and one of V each 1152 contiguous bytes, into a
+// ring of its own, 18 KB deep, so that an SM has 221 KB on their way.  Four CTAs an
+// SM with shorter rings took 13% longer, and producer warps beside 12 that
+// compute 36%: they take issue slots from the same SMSPs.
+// The codes go from shared memory straight into mma.sync
 // fragments, because the order of the contracted index is free as long as
 // both operands agree on it:
 //   S^T[t][g] = K[t][:] . Q[g][:]    A = K: lane (r, c) takes the 32 dims 32c .. 32c+31 of row r,
@@ -58,11 +60,12 @@ constexpr int kUnitBytes = 4 * kFp4Tile;                   // K tile 0, K tile 1
 // (log2 units): weights up to 2^14 are within f16.
 constexpr float kMoveMax = 14.f;
 // Units after which a piece's accumulator is added into an fp32 copy: the
-// tensor cores add with truncation, whose error grows with the chain.
-// 2048 additions (512 units of one part) may leave 2^-12 under a bf16
-// output's 2^-8, 256 (64 units of two parts) 2^-15 under an fp32 one.
+// tensor cores add with truncation, whose error grows with the chain.  1024
+// additions (512 units of one part) may leave 2^-13 under a bf16 output's 2^-8.
+// Under an fp32 one 64 (16 units of two parts) are kept to 2^-18, and measure
+// 1e-6 over 8K to 60K tokens, what a plain fp32 computation has; 256 measured 3e-6.
 template <int kParts>
-constexpr int kFoldUnits = kParts == 1 ? 512 : 64;
+constexpr int kFoldUnits = kParts == 1 ? 512 : 16;
 constexpr uint64_t kLimitNs = 2000000000ull;
 
 // The list's kernel: every warp is a worker with its own ring, whose stages are

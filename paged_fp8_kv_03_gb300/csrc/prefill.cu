@@ -62,7 +62,7 @@ namespace pkv {
 namespace {
 
 constexpr int kKStages = 2, kVStages = 3;        // operand rings: K bf16, V f16
-constexpr int kFold = 32;                        // key tiles per tensor-core accumulation segment of O
+constexpr int kFold8 = 32, kFold4 = 4;           // key tiles per segment of O: FP8 cache; 4-bit cache, fp32 output
 constexpr int kSmWarp0 = 2;                      // first softmax warp
 constexpr int kSmWarps = 8;
 constexpr int kPThreads = 32 * (kSmWarp0 + kSmWarps);
@@ -210,7 +210,8 @@ __global__ void __launch_bounds__(256) kv_widen_kernel(const PrefillArgs a)
 // kWin: the 4-bit cache's calls with a window (and an fp32 output); a row may
 // then see nothing of a tile, or of all tiles so far (its running maximum is
 // -inf until it does).
-template <bool kWin>
+// kFold: key tiles per tensor-core accumulation segment of O.
+template <bool kWin, int kFold>
 __global__ void __launch_bounds__(kPThreads, 1)
     paged_prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                          const __grid_constant__ CUtensorMap tm_v, const PrefillArgs a, const Fp4Window win)
@@ -667,7 +668,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
 }
 
 std::mutex g_prefill_mu;
-unsigned long long g_prefill_attr_ctx[64][2] = {};   // per device and kernel: the context its limit was raised in
+unsigned long long g_prefill_attr_ctx[64][3] = {};   // per device and kernel: the context its limit was raised in
 
 typedef void (*PrefillKernel)(const CUtensorMap, const CUtensorMap, const CUtensorMap, const PrefillArgs,
                               const Fp4Window);
@@ -713,13 +714,13 @@ cudaError_t launch_widen(const PrefillArgs &a, cudaStream_t stream)
     return cudaGetLastError();
 }
 
-template <bool kWin>
+template <bool kWin, int kFold>
 cudaError_t launch_attention(const PrefillArgs &a, const Fp4Window &win, const CUtensorMap &tm_q,
                              const CUtensorMap &tm_k16, const CUtensorMap &tm_v16, cudaStream_t stream)
 {
     const int64_t grid = static_cast<int64_t>(a.batch) * a.hkv * a.max_tiles;
-    paged_prefill_kernel<kWin><<<static_cast<unsigned>(grid), kPThreads, PS::bytes(), stream>>>(tm_q, tm_k16, tm_v16, a,
-                                                                                               win);
+    paged_prefill_kernel<kWin, kFold><<<static_cast<unsigned>(grid), kPThreads, PS::bytes(), stream>>>(tm_q, tm_k16,
+                                                                                                      tm_v16, a, win);
     return cudaGetLastError();
 }
 
@@ -736,10 +737,10 @@ cudaError_t launch_paged_prefill(const PrefillArgs &a, const CUtensorMap &tm_q, 
     if (static_cast<int64_t>(a.batch) * a.hkv * a.max_tiles <= 0)
         return cudaSuccess;
     const Fp4Window none = {0, 0};
-    cudaError_t e = raise_limit(paged_prefill_kernel<false>, 0);
+    cudaError_t e = raise_limit(paged_prefill_kernel<false, kFold8>, 0);
     if (e == cudaSuccess)
         e = launch_widen(a, stream);
-    return e == cudaSuccess ? launch_attention<false>(a, none, tm_q, tm_k16, tm_v16, stream) : e;
+    return e == cudaSuccess ? launch_attention<false, kFold8>(a, none, tm_q, tm_k16, tm_v16, stream) : e;
 }
 
 cudaError_t launch_paged_prefill_fp4(const PrefillArgs &a, const Fp4Window &win, const CUtensorMap &tm_q,
@@ -749,15 +750,16 @@ cudaError_t launch_paged_prefill_fp4(const PrefillArgs &a, const Fp4Window &win,
         return cudaSuccess;
     cudaError_t e = cudaSuccess;
     if (a.out_f32)
-        e = win.window > 0 ? raise_limit(paged_prefill_kernel<true>, 1) : raise_limit(paged_prefill_kernel<false>, 0);
+        e = win.window > 0 ? raise_limit(paged_prefill_kernel<true, kFold4>, 1)
+                           : raise_limit(paged_prefill_kernel<false, kFold4>, 2);
     if (e == cudaSuccess)
         e = launch_widen_fp4(a, win, stream);
     if (e != cudaSuccess)
         return e;
     if (!a.out_f32)
         return launch_prefill_pair(a, win, tm_q, tm_k16, tm_v16, stream);
-    return win.window > 0 ? launch_attention<true>(a, win, tm_q, tm_k16, tm_v16, stream)
-                          : launch_attention<false>(a, win, tm_q, tm_k16, tm_v16, stream);
+    return win.window > 0 ? launch_attention<true, kFold4>(a, win, tm_q, tm_k16, tm_v16, stream)
+                          : launch_attention<false, kFold4>(a, win, tm_q, tm_k16, tm_v16, stream);
 }
 
 }  // namespace pkv
