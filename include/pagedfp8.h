@@ -475,7 +475,8 @@ pkv_status pkv_paged_prefill(const void *q, const int32_t *cu_q, int total_q, in
  * t > p - W (itself and the W - 1 before it) or t < S.  W = 0 means no window
  * (S has no effect).  The rows of pages in which no query of the call sees a
  * token are not read and their table entries not looked at, so such pages may
- * have been given away.
+ * have been given away.  A NaN reaches only those who see it: one in a block of
+ * K the whole output row, one in a block of V its 16 dims.
  */
 #define PKV_FP4_ROW_BYTES 72
 

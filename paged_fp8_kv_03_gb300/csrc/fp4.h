@@ -53,7 +53,7 @@ struct Fp4AttnArgs {
     int32_t *err;
 };
 
-// Decode: workers of the split (consumer warps) a CTA.
+// Decode: workers of the split (warps) a CTA.
 constexpr int kFp4DecodeWorkers = 4;
 
 struct Fp4DecodeArgs {
@@ -95,14 +95,15 @@ cudaError_t launch_with(void (*kernel)(Params...), dim3 grid, unsigned threads, 
     return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
-
 inline size_t decode_fp4_join_bytes(int batch, int hkv)
 {
     return (static_cast<size_t>(batch) * hkv * sizeof(int2) + 255) & ~size_t(255);
 }
 
 // Prefill: 128-key tiles that a sequence's 16-bit copy can need, and the rows
-// and bytes of the workspace (laid out as pkv_paged_prefill's).  Under a
+// and bytes of the workspace: laid out as pkv_paged_prefill's, then a word a
+// tile, each byte of it not zero where one of 32 V rows holds a NaN block, then a
+// byte a row, a bit a NaN block (written where the 32 rows' byte is not zero).  Under a
 // window a chunk of n queries sees the sinks and the n + window - 1 keys
 // before its end, which touch at most (n + window - 2) / 128 + 2 tiles.
 inline long long prefill_fp4_rows(int batch, int hkv, int max_q_len, int max_kv_len, long long max_total_kv,
@@ -124,7 +125,8 @@ inline long long prefill_fp4_rows(int batch, int hkv, int max_q_len, int max_kv_
 
 inline size_t prefill_fp4_bytes(int batch, long long rows)
 {
-    return prefill_header_bytes(batch) + 2 * static_cast<size_t>(rows) * kHeadDim * sizeof(__half);
+    return prefill_header_bytes(batch) + static_cast<size_t>(rows) * (2 * kHeadDim * sizeof(__half) + 1) +
+           static_cast<size_t>(rows / 128) * sizeof(uint32_t);
 }
 
 size_t decode_fp4_smem(int batch);

@@ -52,6 +52,7 @@
 //               (O + O_seg) / l x v_scale.
 // Every wait is bounded (2 s): on expiry the CTA sets PKV_DEVERR_TIMEOUT,
 // drains its own copies and MMAs, frees TMEM and exits.
+#include <math.h>
 #include <mutex>
 
 #include "context.h"
@@ -209,13 +210,13 @@ __global__ void __launch_bounds__(256) kv_widen_kernel(const PrefillArgs a)
 // ---------------------------------------------------------------------- attention
 // kWin: the 4-bit cache's calls with a window (and an fp32 output); a row may
 // then see nothing of a tile, or of all tiles so far (its running maximum is
-// -inf until it does).
-// kFold: key tiles per tensor-core accumulation segment of O.
-template <bool kWin, int kFold>
+// -inf until it does).  kFp4: the 4-bit cache's.
+template <bool kWin, bool kFp4>
 __global__ void __launch_bounds__(kPThreads, 1)
     paged_prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                          const __grid_constant__ CUtensorMap tm_v, const PrefillArgs a, const Fp4Window win)
 {
+    constexpr int kFold = kFp4 ? kFold4 : kFold8;
     // ---------------------------------------------------------------- the tile
     // (sequence, kv head)-major order, heaviest query tiles (largest positions)
     // first within each: the CTAs resident at one time mostly read the K/V of
@@ -622,6 +623,9 @@ __global__ void __launch_bounds__(kPThreads, 1)
         if (ok) {
             const float inv = __ldg(a.v_scale + h) / (l + red_l[(half ^ 1) * kRows + row]);
             const int64_t orow = (static_cast<int64_t>(q0) + t0 + tl) * a.hq + h * G + g;
+            uint32_t nans = 0;
+            if (kFp4)
+                nans = nan_blocks<kWin>(a, win, row0 / kKeys, nt, valid ? pos0 + tl : last, lane, key_tile, copy_tile);
             const bool have_o = nt > kFold;                // at least one segment was folded into O
 #pragma unroll 1
             for (int c = 0; c < 4; ++c) {
@@ -633,9 +637,10 @@ __global__ void __launch_bounds__(kPThreads, 1)
                 if (!valid)
                     continue;
                 float v[16];
+                const float f = kFp4 && ((nans >> (4 * half + c)) & 1u) ? NAN : inv;
 #pragma unroll
                 for (int k = 0; k < 16; ++k)
-                    v[k] = ((have_o ? __uint_as_float(t[k]) : 0.f) + __uint_as_float(o[k])) * inv;
+                    v[k] = ((have_o ? __uint_as_float(t[k]) : 0.f) + __uint_as_float(o[k])) * f;
                 const int d0 = 64 * half + 16 * c;
                 if (a.out_f32) {
                     float4 *dst = reinterpret_cast<float4 *>(static_cast<float *>(a.out) + orow * kHeadDim + d0);
@@ -714,13 +719,13 @@ cudaError_t launch_widen(const PrefillArgs &a, cudaStream_t stream)
     return cudaGetLastError();
 }
 
-template <bool kWin, int kFold>
+template <bool kWin, bool kFp4>
 cudaError_t launch_attention(const PrefillArgs &a, const Fp4Window &win, const CUtensorMap &tm_q,
                              const CUtensorMap &tm_k16, const CUtensorMap &tm_v16, cudaStream_t stream)
 {
     const int64_t grid = static_cast<int64_t>(a.batch) * a.hkv * a.max_tiles;
-    paged_prefill_kernel<kWin, kFold><<<static_cast<unsigned>(grid), kPThreads, PS::bytes(), stream>>>(tm_q, tm_k16,
-                                                                                                      tm_v16, a, win);
+    paged_prefill_kernel<kWin, kFp4><<<static_cast<unsigned>(grid), kPThreads, PS::bytes(), stream>>>(tm_q, tm_k16,
+                                                                                                     tm_v16, a, win);
     return cudaGetLastError();
 }
 
@@ -737,10 +742,10 @@ cudaError_t launch_paged_prefill(const PrefillArgs &a, const CUtensorMap &tm_q, 
     if (static_cast<int64_t>(a.batch) * a.hkv * a.max_tiles <= 0)
         return cudaSuccess;
     const Fp4Window none = {0, 0};
-    cudaError_t e = raise_limit(paged_prefill_kernel<false, kFold8>, 0);
+    cudaError_t e = raise_limit(paged_prefill_kernel<false, false>, 0);
     if (e == cudaSuccess)
         e = launch_widen(a, stream);
-    return e == cudaSuccess ? launch_attention<false, kFold8>(a, none, tm_q, tm_k16, tm_v16, stream) : e;
+    return e == cudaSuccess ? launch_attention<false, false>(a, none, tm_q, tm_k16, tm_v16, stream) : e;
 }
 
 cudaError_t launch_paged_prefill_fp4(const PrefillArgs &a, const Fp4Window &win, const CUtensorMap &tm_q,
@@ -750,16 +755,16 @@ cudaError_t launch_paged_prefill_fp4(const PrefillArgs &a, const Fp4Window &win,
         return cudaSuccess;
     cudaError_t e = cudaSuccess;
     if (a.out_f32)
-        e = win.window > 0 ? raise_limit(paged_prefill_kernel<true, kFold4>, 1)
-                           : raise_limit(paged_prefill_kernel<false, kFold4>, 2);
+        e = win.window > 0 ? raise_limit(paged_prefill_kernel<true, true>, 1)
+                           : raise_limit(paged_prefill_kernel<false, true>, 2);
     if (e == cudaSuccess)
         e = launch_widen_fp4(a, win, stream);
     if (e != cudaSuccess)
         return e;
     if (!a.out_f32)
         return launch_prefill_pair(a, win, tm_q, tm_k16, tm_v16, stream);
-    return win.window > 0 ? launch_attention<true, kFold4>(a, win, tm_q, tm_k16, tm_v16, stream)
-                          : launch_attention<false, kFold4>(a, win, tm_q, tm_k16, tm_v16, stream);
+    return win.window > 0 ? launch_attention<true, true>(a, win, tm_q, tm_k16, tm_v16, stream)
+                          : launch_attention<false, true>(a, win, tm_q, tm_k16, tm_v16, stream);
 }
 
 }  // namespace pkv

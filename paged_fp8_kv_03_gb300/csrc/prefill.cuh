@@ -182,6 +182,49 @@ __device__ __forceinline__ KeyTiles key_tiles(const Fp4Window &w, int first_pos)
     return k;
 }
 
+// NaN blocks of the 4-bit cache's V.  A weight of zero times a NaN is a NaN, so
+// the widening kernel writes zeros for them and records where they were; the
+// attention puts NaNs into the outputs of the rows that see them.
+__device__ __forceinline__ uint32_t *nan_tiles(const PrefillArgs &a)
+{
+    return reinterpret_cast<uint32_t *>(a.v16 + a.rows_cap * kHeadDim);
+}
+
+__device__ __forceinline__ uint8_t *nan_rows(const PrefillArgs &a)
+{
+    return reinterpret_cast<uint8_t *>(nan_tiles(a) + a.rows_cap / kKeys);
+}
+
+// Blocks of 16 dims (a bit each) in which a row at position p sees a NaN: nt
+// key tiles, the i-th one is key_tile(i) of the sequence and copy_tile(i) of the
+// copy, which starts at tile `tile0` (the whole warp).
+template <bool kWin, typename KeyTile, typename CopyTile>
+__device__ __forceinline__ uint32_t nan_blocks(const PrefillArgs &a, const Fp4Window &w, int tile0, int nt, int p, int lane,
+                                               KeyTile key_tile, CopyTile copy_tile)
+{
+    const uint32_t *tiles = nan_tiles(a);
+    bool some = false;
+    for (int i = lane; i < nt; i += 32)
+        some = some || __ldg(tiles + tile0 + copy_tile(i)) != 0;
+    uint32_t hit = 0;
+    if (__any_sync(kAll, some)) {
+#pragma unroll 1
+        for (int i = 0; i < nt; ++i) {
+            const int64_t tile = tile0 + copy_tile(i);
+            const uint32_t word = __ldg(tiles + tile);
+            if (word == 0)
+                continue;
+#pragma unroll 1
+            for (int k = 0; k < kKeys; ++k) {
+                const int t = key_tile(i) * kKeys + k;
+                if ((word >> (8 * (k >> 5)) & 0xFFu) != 0 && t <= p && (!kWin || t > p - w.window || t < w.sinks))
+                    hit |= __ldg(nan_rows(a) + tile * kKeys + k);
+            }
+        }
+    }
+    return hit;
+}
+
 // 128-row tiles of sequence b's widened region (all its kv heads): zero for a
 // sequence with an empty or inconsistent chunk.
 template <bool kWin>

@@ -26,6 +26,7 @@
 // accumulator, on average half of that.
 // Every wait is bounded (2 s): on expiry the CTA sets PKV_DEVERR_TIMEOUT,
 // drains its own copies and MMAs, frees TMEM and exits.
+#include <math.h>
 #include <mutex>
 
 #include "context.h"
@@ -68,7 +69,8 @@ static_assert(P2::bytes() <= 232448, "prefill tile buffers exceed the shared mem
 // is the prefix sum of the sequences' 128-row tiles (a region past the workspace
 // is flagged), K and V of a sequence's kv head in consecutive rows, zero rows up
 // to a whole tile.  Keys that no query sees under the window get no tile, or
-// zero rows in a tile others are seen of.
+// zero rows in a tile others are seen of.  A NaN block of V is widened to zeros
+// and recorded.
 //
 // Bytes bound it: 144 of the cache to 512 of the copies a row.  A CTA takes a
 // tile (or a quarter of one, where there are few), so what the tile belongs to is
@@ -78,6 +80,7 @@ template <int kRowsEach>
 __global__ void __launch_bounds__(256) kv_widen_fp4_kernel(const PrefillArgs a, const Fp4Window win)
 {
     constexpr int kPieces = 8 / kRowsEach;               // CTAs' steps a tile
+    static_assert(kPieces == 1 || kPieces == 4, "a tile's word has a byte a piece");
     extern __shared__ int off[];                         // [batch + 1], then 8 warp sums
     int *warp_sum = off + a.batch + 1;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -140,6 +143,7 @@ __global__ void __launch_bounds__(256) kv_widen_fp4_kernel(const PrefillArgs a, 
         const int key0 = (vt < kt.first ? vt : vt + kt.skip) * kKeys;
         uint32_t kc[kRowsEach], vc[kRowsEach];
         uint8_t ks[kRowsEach], vs[kRowsEach];
+        uint32_t nans = 0;                               // V's, a bit a row
 #pragma unroll
         for (int i = 0; i < kRowsEach; ++i) {
             const int t = key0 + first + 16 * i;
@@ -154,6 +158,10 @@ __global__ void __launch_bounds__(256) kv_widen_fp4_kernel(const PrefillArgs a, 
                     vc[i] = __ldg(reinterpret_cast<const uint32_t *>(a.v_cache + codes));
                     ks[i] = __ldg(a.k_cache + scale);
                     vs[i] = __ldg(a.v_cache + scale);
+                    if ((vs[i] & 0x7F) == 0x7F) {
+                        vs[i] = 0;
+                        nans |= 1u << i;
+                    }
                 } else if (part == 0 && a.err) {
                     atomicOr(a.err, PKV_DEVERR_PAGE);
                 }
@@ -176,6 +184,25 @@ __global__ void __launch_bounds__(256) kv_widen_fp4_kernel(const PrefillArgs a, 
             }
             *reinterpret_cast<uint4 *>(a.k16 + at) = make_uint4(k[0], k[1], k[2], k[3]);
             *reinterpret_cast<uint4 *>(a.v16 + at) = make_uint4(v[0], v[1], v[2], v[3]);
+        }
+        const bool any = __syncthreads_or(static_cast<int>(nans)) != 0;
+        if (tid == 0) {
+            if (kPieces == 1)
+                nan_tiles(a)[tile] = any ? 0x01010101u : 0u;
+            else
+                reinterpret_cast<uint8_t *>(nan_tiles(a) + tile)[piece % kPieces] = any;
+        }
+        if (any) {
+#pragma unroll
+            for (int i = 0; i < kRowsEach; ++i) {
+                // even lanes of a row's 16 stand for its blocks
+                uint32_t x = __ballot_sync(kAll, (nans >> i) & 1u) >> (lane & 16) & 0x5555u;
+                x = (x | x >> 1) & 0x3333u;
+                x = (x | x >> 2) & 0x0F0Fu;
+                x = (x | x >> 4) & 0xFFu;
+                if (part == 0)
+                    nan_rows(a)[static_cast<int64_t>(tile) * kKeys + first + 16 * i] = static_cast<uint8_t>(x);
+            }
         }
     }
 }
@@ -497,6 +524,7 @@ __global__ void __launch_bounds__(kThreads2, 1)
         if (ok && wwait(bar(P2::PV_DONE + x), (ntx - 1) & 1, abort_flag, a.err, lane)) {
             tc::fence_after();
             const float inv = __ldg(a.v_scale + h) / l;
+            const uint32_t nans = nan_blocks<kWin>(a, win, row0 / kKeys, ntx, p_row, lane, key_tile, copy_tile);
             const int64_t orow = (static_cast<int64_t>(q0) + t0 + x * tpt + tl) * a.hq + h * G + g;
             uint4 *dst = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.out) + orow * kHeadDim);
 #pragma unroll 1
@@ -509,10 +537,11 @@ __global__ void __launch_bounds__(kThreads2, 1)
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
                     uint32_t w[4];
+                    const float f = (nans >> (2 * c + (k >> 1))) & 1u ? NAN : inv;
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        const __nv_bfloat162 b2 = __floats2bfloat162_rn(__uint_as_float(o[8 * k + 2 * e]) * inv,
-                                                                        __uint_as_float(o[8 * k + 2 * e + 1]) * inv);
+                        const __nv_bfloat162 b2 = __floats2bfloat162_rn(__uint_as_float(o[8 * k + 2 * e]) * f,
+                                                                        __uint_as_float(o[8 * k + 2 * e + 1]) * f);
                         w[e] = *reinterpret_cast<const uint32_t *>(&b2);
                     }
                     dst[4 * c + k] = make_uint4(w[0], w[1], w[2], w[3]);

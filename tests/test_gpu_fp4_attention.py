@@ -322,6 +322,43 @@ def test_prefill_page_sizes_and_errors(pkv, cuda_device):
     _prefill(pkv, c, ns, 4, sample=10, err=pkv.DEVERR_PAGE)
 
 
+@pytest.mark.parametrize("out_dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("lens,ns", [([400, 3], [200, 3]), ([9000], [300])])
+def test_prefill_nan_rows(pkv, cuda_device, out_dtype, lens, ns):
+    """A NaN block of V is NaN in its 16 dims of the queries that see it, one
+    of K in their whole rows; the others' rows are as without it."""
+    c = Cache(26, lens, 2, 16, cuda_device)
+    cu = np.concatenate(([0], np.cumsum(ns))).astype(np.int32)
+    _, qd = c.queries(int(cu[-1]), 8)
+    n, L = ns[0], lens[0]
+
+    def run(window):
+        out = torch.full(qd.shape, 9.0, dtype=out_dtype, device=c.dev)
+        ws = torch.full((pkv.pkv_prefill_fp4_workspace_size(len(lens), 2, n, L, 0, window, 5),), 0xFF,
+                        dtype=torch.uint8, device=c.dev)
+        pkv.paged_prefill_fp4(qd, _dev(cu, c.dev), c.kc, c.vc, c.ksd, c.vsd, c.tabled, c.lensd, n, out=out,
+                              max_kv_len=L, window=window, sinks=5, workspace=ws)
+        return out.float().cpu().numpy()
+
+    clean = {w: run(w) for w in (0, 70)}
+    slots = fp4_ref.slots_of(c.table[0], L, 16)
+    v_at, k_at = L - n + 60, L - n + 150
+    for pool, h, t, block in ((c.vc, 1, v_at, 3), (c.vc, 1, 2, 6), (c.kc, 0, k_at, 0)):
+        pg, r = divmod(int(slots[t]), 16)
+        pool.view(c.pages, 2, 1, 1152)[pg, h, 0, 1024 + 8 * r + block] = 0x7F
+    p = L - n + np.arange(n)
+    for w in (0, 70):
+        exp = clean[w].copy()
+
+        def sees(t):
+            return np.flatnonzero((p >= t) & ((w == 0) | (t > p - w) | (t < 5)))
+
+        exp[sees(v_at), 4:, 48:64] = np.nan
+        exp[sees(2), 4:, 96:112] = np.nan
+        exp[sees(k_at), :4] = np.nan
+        assert np.array_equal(run(w), exp, equal_nan=True), w
+
+
 def test_prefill_one_query_is_a_decode_step(pkv, cuda_device):
     lens = [1, 130, 77, 600]
     c = Cache(24, lens, 2, 16, cuda_device)
@@ -398,3 +435,55 @@ def test_a_prompt_and_its_answer(pkv, cuda_device, window, sinks):
     got, _ = pkv.kv_read_fp4(sd, ks, vs, kc, vc, out_dtype=torch.float32)
     exp = (fp4_ref.block_values(pools[0], slots) * ksn.reshape(1, hkv, 1)).astype(np.float32)
     assert np.array_equal(got.cpu().numpy(), exp)
+
+
+@pytest.mark.parametrize("batch,max_ctas", [(8192, 0), (8192, 200), (5000, 1000)])
+def test_decode_large_batches(pkv, cuda_device, batch, max_ctas):
+    """Thousands of sequences, one of them long: the rows are those of the
+    same sequences in small batches."""
+    lens = [3, 0, 40, 17, 1, 90]
+    c = Cache(27, lens + [3000], 1, 16, cuda_device)
+    pick = np.arange(batch) % len(lens)
+    pick[batch // 2] = len(lens)
+    q, qd = c.queries(batch, 2)
+    at = _dev(pick, cuda_device)
+    table, lensd = c.tabled[at].contiguous(), c.lensd[at].contiguous()
+    err = torch.zeros(1, dtype=torch.int32, device=cuda_device)
+    out = pkv.paged_gqa_decode_fp4(qd, c.kc, c.vc, c.ksd, c.vsd, table, lensd, out_dtype=torch.float32,
+                                   max_seq_len=3000, max_ctas=max_ctas, device_error=err)
+    torch.cuda.synchronize()
+    assert int(err.item()) == 0
+    for b in (*range(12), batch // 2 - 1, batch // 2, batch // 2 + 1, batch - 2, batch - 1):
+        k, v, L = c.k[pick[b]], c.v[pick[b]], len(c.k[pick[b]])
+        ref = fp4_ref.attend(q[b].astype(np.float64), k, v, L - 1, 0, 0, fp4_ref.SM)
+        _check(out[b], ref, fp4_ref.attention_tolerance(q[b], k, v, ref, fp4_ref.SM, False), b)
+
+
+def test_calls_at_once_on_two_streams(pkv, cuda_device):
+    """Decode and prefill on two streams at the same time, with workspaces of
+    their own, give the bits of the calls one after the other."""
+    lens = [5000, 300, 2000]
+    c = Cache(28, lens, 2, 16, cuda_device)
+    _, qd = c.queries(3, 8)
+    _, qp = c.queries(600, 8)
+    cu = torch.tensor([0, 300, 400, 600], dtype=torch.int32, device=cuda_device)
+
+    def decode(stream=None):
+        return pkv.paged_gqa_decode_fp4(qd, c.kc, c.vc, c.ksd, c.vsd, c.tabled, c.lensd, max_seq_len=5000,
+                                        out_dtype=torch.float32, stream=stream)
+
+    def prefill(stream=None):
+        return pkv.paged_prefill_fp4(qp, cu, c.kc, c.vc, c.ksd, c.vsd, c.tabled, c.lensd, 300, max_kv_len=5000,
+                                     window=1000, sinks=4, stream=stream)
+
+    ref = decode(), prefill()
+    torch.cuda.synchronize()
+    streams = torch.cuda.Stream(), torch.cuda.Stream()
+    got = []
+    for _ in range(5):
+        for s in streams:
+            with torch.cuda.stream(s):
+                got.append((decode(), prefill()))
+    torch.cuda.synchronize()
+    for d, p in got:
+        assert torch.equal(d, ref[0]) and torch.equal(p, ref[1])
