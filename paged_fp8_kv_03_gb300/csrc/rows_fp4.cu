@@ -7,7 +7,8 @@
 //                            within 1/16 of it (it saturates there),
 //   code = E2M1(x / (s k)),
 // the products 6 k and s k and both quotients rounded to fp32 (IEEE), both
-// conversions to nearest, ties to even.  e s has 6 significant bits, so f16,
+// conversions to nearest, ties to even (a bound on either side of x / (s k)
+// mostly settles the code without the division).  e s has 6 significant bits, so f16,
 // bf16 and fp32 all hold it exactly.
 //
 // What bounds them: the bytes, 256 or 512 of the row and 72 of the cache each
@@ -16,7 +17,8 @@
 // (with 32 a thread, half of every sector waits for a second instruction: 5.0
 // instead of 6.2 TB/s).  Appending, it owns 32 bytes (16 or 8 values; a block is
 // one or two lanes), because what a block's scale costs is paid once a thread
-// and instructions, not bytes, are the limit.  In calls large enough a thread
+// and instructions are as much of a limit as bytes (128K bf16 tokens of 8 heads:
+// 122 us, 5.6 TB/s; fp32: 195 us, 6.3 TB/s).  In calls large enough a thread
 // takes the same place in several consecutive tokens, their loads in flight
 // together.
 #include "fp4.cuh"
@@ -81,6 +83,7 @@ __device__ __forceinline__ float divide(float x, float d, float y)
 struct HeadScale {
     float k, k6, inv_k6;
     bool plain;                                            // out of the range in which divide() is safe
+    bool few_bits;                                         // k is a bf16 value
 };
 
 __device__ __forceinline__ HeadScale head_scale(float k)
@@ -89,6 +92,7 @@ __device__ __forceinline__ HeadScale head_scale(float k)
     h.k = k;
     h.k6 = __fmul_rn(6.f, k);
     h.inv_k6 = __frcp_rn(h.k6);
+    h.few_bits = (__float_as_uint(k) & 0xFFFFu) == 0;
     h.plain = !(k >= 0x1p-60f && k <= 0x1p60f);
     return h;
 }
@@ -135,7 +139,7 @@ __device__ __forceinline__ void quantise_part(const uint4 (&u)[2], const HeadSca
             ratio = divide(amax, hs.k6, hs.inv_k6);
         scale = static_cast<uint8_t>(__nv_cvt_float_to_fp8(ratio, __NV_SATFINITE, __NV_E4M3));
         const float step = __fmul_rn(e4m3_value(scale), hs.k);
-        float q[2][8];
+        float q[8];
         auto value = [&](int i) {
             return __uint_as_float(kBf16 ? ((i & 1) ? w[i >> 1] & 0xFFFF0000u : w[i >> 1] << 16) : w[i & 7]);
         };
@@ -144,17 +148,41 @@ __device__ __forceinline__ void quantise_part(const uint4 (&u)[2], const HeadSca
             for (int i = 0; i < P::kVals; i += 8) {
 #pragma unroll
                 for (int j = 0; j < 8; ++j)
-                    q[0][j] = __fdiv_rn(i ? value(j + P::kVals - 8) : value(j), step);
-                c[i >> 3] = f32x8_to_e2m1x8(q[0]);
+                    q[j] = __fdiv_rn(i ? value(j + P::kVals - 8) : value(j), step);
+                c[i >> 3] = f32x8_to_e2m1x8(q);
             }
         } else if (scale != 0) {
+            // The quotient lies between x y (1 - 2^-20) and x y (1 + 2^-20) (their
+            // roundings and the quotient's are off by less than 2^-22), so where both
+            // have the same code, it has that too.  Where they differ, in one warp of 700,
+            // it is divided; and always where k has so few bits that a bf16 x is often
+            // exactly halfway between two codes (16K bf16 tokens of 8 heads: 19 us,
+            // dividing always 21, dividing after most comparisons 26).
             const float y = __frcp_rn(step);
+            uint32_t differ = hs.few_bits;
+            if (differ == 0) {
+                const float less = __fmul_rn(y, 1.f - 0x1p-20f), more = __fmul_rn(y, 1.f + 0x1p-20f);
 #pragma unroll
-            for (int i = 0; i < P::kVals; ++i)
-                q[i >> 3][i & 7] = divide(value(i), step, y);
+                for (int i = 0; i < P::kVals / 8; ++i) {
+                    float lo[8], hi[8];
 #pragma unroll
-            for (int i = 0; i < P::kVals / 8; ++i)
-                c[i] = f32x8_to_e2m1x8(q[i]);
+                    for (int j = 0; j < 8; ++j) {
+                        lo[j] = __fmul_rn(value(8 * i + j), less);
+                        hi[j] = __fmul_rn(value(8 * i + j), more);
+                    }
+                    c[i] = f32x8_to_e2m1x8(hi);
+                    differ |= c[i] ^ f32x8_to_e2m1x8(lo);
+                }
+            }
+            if (differ != 0) {
+#pragma unroll
+                for (int i = 0; i < P::kVals / 8; ++i) {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        q[j] = divide(value(8 * i + j), step, y);
+                    c[i] = f32x8_to_e2m1x8(q);
+                }
+            }
         }
     }
     if (store) {
@@ -168,7 +196,7 @@ __device__ __forceinline__ void quantise_part(const uint4 (&u)[2], const HeadSca
 }
 
 template <bool kBf16, int kTokens>
-__global__ void __launch_bounds__(kRowThreads) kv_append_fp4_kernel(const Fp4RowArgs a)
+__global__ void __launch_bounds__(kRowThreads, kBf16 ? 3 : 4) kv_append_fp4_kernel(const Fp4RowArgs a)
 {
     using P = Part<kBf16, 32>;
     const RowPlace p = row_place<P, kTokens>(a);
