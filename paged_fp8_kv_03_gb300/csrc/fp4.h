@@ -22,6 +22,7 @@ struct Fp4RowArgs {                                        // append and read ba
     uint8_t *k_cache, *v_cache;
     int64_t num_slots;
     int page_size, page_log2;
+    int tokens;                                            // tokens of a thread (launcher)
     int64_t slab;                                          // tokens of one grid row (launcher)
     int32_t *err;
 };

@@ -18,9 +18,9 @@
 // instead of 6.2 TB/s).  Appending, it owns 32 bytes (16 or 8 values; a block is
 // one or two lanes), because what a block's scale costs is paid once a thread
 // and instructions are as much of a limit as bytes (128K bf16 tokens of 8 heads:
-// 122 us, 5.6 TB/s; fp32: 195 us, 6.3 TB/s).  In calls large enough a thread
-// takes the same place in several consecutive tokens, their loads in flight
-// together.
+// 114 us, 6.0 TB/s; fp32: 186 us, 6.6 TB/s).  In calls large enough a thread
+// takes the same place in several consecutive tokens: reading back, their loads are
+// in flight together; appending, the next one's while one is quantised.
 #include "fp4.cuh"
 
 namespace pkv {
@@ -44,16 +44,16 @@ struct RowPlace {
     bool in;
 };
 
-template <typename P, int kTokens>
-__device__ __forceinline__ RowPlace row_place(const Fp4RowArgs &a)
+template <typename P>
+__device__ __forceinline__ RowPlace row_place(const Fp4RowArgs &a, int tokens)
 {
     RowPlace p;
     const uint32_t i = blockIdx.x * kRowThreads + threadIdx.x;     // (a slab of tokens keeps it within 32 bits)
     p.part = i % P::kPerRow;
     const uint32_t row = i / P::kPerRow, g = row / static_cast<uint32_t>(a.hkv);
     p.h = static_cast<int>(row - g * a.hkv);
-    p.token = static_cast<int64_t>(blockIdx.y) * a.slab + static_cast<int64_t>(g) * kTokens;
-    p.in = g * kTokens < a.slab && p.token < a.num_tokens;
+    p.token = static_cast<int64_t>(blockIdx.y) * a.slab + static_cast<int64_t>(g) * tokens;
+    p.in = static_cast<int64_t>(g) * tokens < a.slab && p.token < a.num_tokens;
     return p;
 }
 
@@ -104,6 +104,14 @@ __device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b)
     return d;
 }
 
+// The larger magnitude (with some sign) of each pair; a NaN wins.
+__device__ __forceinline__ uint32_t max_abs_bf16x2(uint32_t a, uint32_t b)
+{
+    uint32_t d;
+    asm("max.NaN.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+}
+
 // Quantises a thread's part of a row (32 bytes; fp32: with the neighbouring
 // lane that has the block's other half) and stores codes and scale.
 template <bool kBf16>
@@ -115,14 +123,14 @@ __device__ __forceinline__ void quantise_part(const uint4 (&u)[2], const HeadSca
     uint32_t m[8], top;                                    // largest |x| as its bits; a NaN's exceed all others'
 #pragma unroll
     for (int i = 0; i < 8; ++i)
-        m[i] = w[i] & (kBf16 ? 0x7FFF7FFFu : 0x7FFFFFFFu);
+        m[i] = kBf16 ? w[i] : w[i] & 0x7FFFFFFFu;
 #pragma unroll
     for (int n = 4; n > 0; n >>= 1)
 #pragma unroll
         for (int i = 0; i < n; ++i)
-            m[i] = kBf16 ? max_u16x2(m[i], m[i + n]) : max(m[i], m[i + n]);
+            m[i] = kBf16 ? max_abs_bf16x2(m[i], m[i + n]) : max(m[i], m[i + n]);
     if (kBf16)
-        top = max_u16x2(m[0], m[0] << 16) & 0xFFFF0000u;
+        top = max_u16x2(m[0] & 0x7FFF7FFFu, (m[0] << 16) & 0x7FFF0000u) & 0xFFFF0000u;
     else
         top = max(m[0], __shfl_xor_sync(0xffffffffu, m[0], 1));
     const float amax = __uint_as_float(top);
@@ -156,8 +164,8 @@ __device__ __forceinline__ void quantise_part(const uint4 (&u)[2], const HeadSca
             // roundings and the quotient's are off by less than 2^-22), so where both
             // have the same code, it has that too.  Where they differ, in one warp of 700,
             // it is divided; and always where k has so few bits that a bf16 x is often
-            // exactly halfway between two codes (16K bf16 tokens of 8 heads: 19 us,
-            // dividing always 21, dividing after most comparisons 26).
+            // exactly halfway between two codes (16K bf16 tokens of 8 heads: 18 us,
+            // dividing always 20; after most comparisons 5 us more).
             const float y = __frcp_rn(step);
             uint32_t differ = hs.few_bits;
             if (differ == 0) {
@@ -195,35 +203,44 @@ __device__ __forceinline__ void quantise_part(const uint4 (&u)[2], const HeadSca
     }
 }
 
-template <bool kBf16, int kTokens>
+template <bool kBf16, bool kMany>
 __global__ void __launch_bounds__(kRowThreads, kBf16 ? 3 : 4) kv_append_fp4_kernel(const Fp4RowArgs a)
 {
     using P = Part<kBf16, 32>;
-    const RowPlace p = row_place<P, kTokens>(a);
+    const int tokens = kMany ? a.tokens : 1;
+    const RowPlace p = row_place<P>(a, tokens);
     const HeadScale ks = head_scale(__ldg(a.k_scale + p.h)), vs = head_scale(__ldg(a.v_scale + p.h));
-    int64_t slot[kTokens];
-    uint4 k[kTokens][2], v[kTokens][2];
-#pragma unroll
-    for (int i = 0; i < kTokens; ++i) {
+    // the next token's loads are on their way while one is quantised
+    struct Token {
+        int64_t slot;
+        uint4 k[2], v[2];
+    };
+    auto load = [&](int i) {
+        Token x;
         const int64_t t = p.token + i;
         const bool in = p.in && t < a.num_tokens;
-        slot[i] = in ? __ldg(a.slots + t) : -1;
+        x.slot = in ? __ldg(a.slots + t) : -1;
         const int64_t at = ((t * a.hkv + p.h) * P::kPerRow + p.part) * 2;
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-            k[i][j] = in ? __ldg(static_cast<const uint4 *>(a.k_in) + at + j) : make_uint4(0, 0, 0, 0);
-            v[i][j] = in ? __ldg(static_cast<const uint4 *>(a.v_in) + at + j) : make_uint4(0, 0, 0, 0);
+            x.k[j] = in ? __ldg(static_cast<const uint4 *>(a.k_in) + at + j) : make_uint4(0, 0, 0, 0);
+            x.v[j] = in ? __ldg(static_cast<const uint4 *>(a.v_in) + at + j) : make_uint4(0, 0, 0, 0);
         }
-    }
-#pragma unroll
-    for (int i = 0; i < kTokens; ++i) {                    // (lanes of a block share their token, so its slot)
-        const bool store = slot[i] >= 0 && slot[i] < a.num_slots;
-        if (slot[i] >= a.num_slots && a.err && p.part == 0)
+        return x;
+    };
+    Token next = load(0);
+#pragma unroll 1
+    for (int i = 0; i < tokens; ++i) {                    // (lanes of a block share their token, so its slot)
+        const Token x = next;
+        if (i + 1 < tokens)
+            next = load(i + 1);
+        const bool store = x.slot >= 0 && x.slot < a.num_slots;
+        if (x.slot >= a.num_slots && a.err && p.part == 0)
             atomicOr(a.err, PKV_DEVERR_SLOT);
         int r = 0;
-        const int64_t tile = store ? slot_tile(a, slot[i], p.h, r) : 0;
-        quantise_part<kBf16>(k[i], ks, a.k_cache + tile, r, p.part, store);
-        quantise_part<kBf16>(v[i], vs, a.v_cache + tile, r, p.part, store);
+        const int64_t tile = store ? slot_tile(a, x.slot, p.h, r) : 0;
+        quantise_part<kBf16>(x.k, ks, a.k_cache + tile, r, p.part, store);
+        quantise_part<kBf16>(x.v, vs, a.v_cache + tile, r, p.part, store);
     }
 }
 
@@ -256,7 +273,7 @@ template <bool kBf16, int kTokens>
 __global__ void __launch_bounds__(kRowThreads) kv_read_fp4_kernel(const Fp4RowArgs a)
 {
     using P = Part<kBf16, 16>;
-    const RowPlace p = row_place<P, kTokens>(a);
+    const RowPlace p = row_place<P>(a, kTokens);
     if (!p.in)
         return;
     const float ks = __ldg(a.k_scale + p.h), vs = __ldg(a.v_scale + p.h);
@@ -296,15 +313,27 @@ __global__ void __launch_bounds__(kRowThreads) kv_read_fp4_kernel(const Fp4RowAr
 
 typedef void (*RowKernel)(const Fp4RowArgs);
 
-// A thread takes `most` tokens where that still fills the GPU with threads.
-cudaError_t launch_rows(RowKernel one, RowKernel many, int most, int per_row, const Fp4RowArgs &args,
+// A thread takes `tokens` tokens in `many` where that still fills the GPU with
+// threads, else one.  tokens = 0: as many as give `resident` threads an SM equal
+// shares, in rounds of at most 10 (append of bf16 rows of 8 heads: 16K tokens, 9 a thread
+// in one round, 18.0 us, one a thread 19.2; 128K, 9 a thread, 114 us, 72 in one round 118;
+// 4K, 3 a thread 6.7 us, one 5.4).
+cudaError_t launch_rows(RowKernel one, RowKernel many, int tokens, int resident, int per_row, const Fp4RowArgs &args,
                         cudaStream_t stream)
 {
     if (args.num_tokens == 0)
         return cudaSuccess;
     Fp4RowArgs a = args;
-    const int64_t threads = a.num_tokens * a.hkv * per_row;
-    const int tokens = threads >= static_cast<int64_t>(device_sm_count()) * 2048 * most ? most : 1;
+    const int64_t threads = a.num_tokens * a.hkv * per_row, sms = device_sm_count();
+    if (tokens == 0) {
+        const int64_t share = (threads + sms * resident - 1) / (sms * resident), rounds = (share + 9) / 10;
+        tokens = static_cast<int>((share + rounds - 1) / rounds);
+        if (tokens < 4)
+            tokens = 1;
+    } else if (threads < sms * 2048 * tokens) {
+        tokens = 1;
+    }
+    a.tokens = tokens;
     // tokens a slab: its threads count in 32 bits, and whole groups
     int64_t slab = ((int64_t(1) << 30) / (static_cast<int64_t>(a.hkv) * per_row) + tokens) / tokens * tokens;
     if (slab > a.num_tokens)
@@ -323,17 +352,17 @@ cudaError_t launch_rows(RowKernel one, RowKernel many, int most, int per_row, co
 
 cudaError_t launch_kv_append_fp4(const Fp4RowArgs &a, cudaStream_t stream)
 {
-    return a.bf16 ? launch_rows(kv_append_fp4_kernel<true, 1>, kv_append_fp4_kernel<true, 2>, 2,
+    return a.bf16 ? launch_rows(kv_append_fp4_kernel<true, false>, kv_append_fp4_kernel<true, true>, 0, 768,
                                 Part<true, 32>::kPerRow, a, stream)
-                  : launch_rows(kv_append_fp4_kernel<false, 1>, kv_append_fp4_kernel<false, 2>, 2,
+                  : launch_rows(kv_append_fp4_kernel<false, false>, kv_append_fp4_kernel<false, true>, 16, 0,
                                 Part<false, 32>::kPerRow, a, stream);
 }
 
 cudaError_t launch_kv_read_fp4(const Fp4RowArgs &a, cudaStream_t stream)
 {
-    return a.bf16 ? launch_rows(kv_read_fp4_kernel<true, 1>, kv_read_fp4_kernel<true, 4>, 4,
+    return a.bf16 ? launch_rows(kv_read_fp4_kernel<true, 1>, kv_read_fp4_kernel<true, 4>, 4, 0,
                                 Part<true, 16>::kPerRow, a, stream)
-                  : launch_rows(kv_read_fp4_kernel<false, 1>, kv_read_fp4_kernel<false, 4>, 4,
+                  : launch_rows(kv_read_fp4_kernel<false, 1>, kv_read_fp4_kernel<false, 4>, 4, 0,
                                 Part<false, 16>::kPerRow, a, stream);
 }
 

@@ -183,3 +183,37 @@ def test_on_another_stream_and_in_a_graph(pkv, cuda_device):
     ek, _ = _expect(y, y, s, s, slots, 4, 4, 16)
     exp = (fp4_ref.block_values(ek, slots) * s.reshape(1, 4, 1)).astype(np.float32)
     assert np.array_equal(ko.cpu().numpy(), exp)
+
+
+@pytest.mark.parametrize("T,H,dtype", [(9001, 8, torch.bfloat16), (70003, 5, torch.bfloat16),
+                                       (40013, 8, torch.float32)])
+def test_large_calls_are_small_ones(pkv, cuda_device, T, H, dtype):
+    """In large calls a thread takes several tokens: pages and rows are those
+    of the same tokens in small calls, with slots that are not written and
+    slots outside the pool between them."""
+    P, pages = 16, T // 16 + 2
+    g = torch.Generator(device="cuda").manual_seed(T)
+    k, v = (torch.randn(T, H, 128, generator=g, device=cuda_device).to(dtype) for _ in range(2))
+    ks, vs = (0.01 + 0.01 * torch.rand(H, generator=g, device=cuda_device) for _ in range(2))
+    slots = torch.randperm(pages * P, generator=g, device=cuda_device)[:T]
+    slots[5::7] = -1
+    slots[T // 2] = pages * P
+    slots[-1] = 1 << 40
+    step = 500
+    pools, outs = [], []
+    for cuts in ([(0, T)], [(i, min(i + step, T)) for i in range(0, T, step)]):
+        err = torch.zeros(1, dtype=torch.int32, device=cuda_device)
+        kc, vc = (torch.full((pages, H, P, 72), 0x55, dtype=torch.uint8, device=cuda_device) for _ in range(2))
+        for lo, hi in cuts:
+            pkv.kv_append_fp4(k[lo:hi], v[lo:hi], slots[lo:hi], ks, vs, kc, vc, err)
+        assert int(err.item()) == pkv.DEVERR_SLOT
+        pools.append((kc, vc))
+        err.zero_()
+        ko, vo = (torch.full((T, H, 128), 9.0, dtype=dtype, device=cuda_device) for _ in range(2))
+        for lo, hi in cuts:
+            pkv.pkv_kv_read_fp4(slots[lo:hi], ks, vs, *pools[0], ko[lo:hi], vo[lo:hi], err)
+        assert int(err.item()) == pkv.DEVERR_SLOT
+        outs.append((ko, vo))
+    for x, y in zip(pools[0] + outs[0], pools[1] + outs[1]):
+        assert torch.equal(x, y)
+    assert (outs[0][0][slots == -1] == 9).all() and (outs[0][0][slots >= pages * P] == 0).all()
