@@ -1089,9 +1089,14 @@ __global__ void __launch_bounds__(32 * kClusterWarps, 2) paged_gqa_decode_fp4_cl
 // Joins the states of a segment's pieces for one query head, in worker order:
 // out = v_scale sum_i 2^(m_i - M) A_i / sum_i 2^(m_i - M) l_i.  A CTA per
 // (segment, head); its warps take the pieces in turns of kJoin, all of a
-// turn's loads in flight together, and are joined in warp order.
-constexpr int kJoin = 8;
-constexpr int kJoinWarps = 8;
+// turn's loads in flight together, and are joined in warp order.  A turn is a round
+// trip to the L2, so turns are long and up to 16 warps share them (8 states and 8
+// warps: one 8K sequence 13.8 us instead of 12.5, a 128K one among 63 of 512 tokens 60
+// instead of 54).  Warps are as few as an average segment needs, because a CTA of one
+// or two is on its SM before the list's CTAs have left it (four at least: 64 x 2K
+// tokens 37 us instead of 34.5).
+constexpr int kJoin = 16;
+constexpr int kJoinWarps = 16;
 
 __global__ void __launch_bounds__(32 * kJoinWarps) join_fp4_kernel(const Fp4DecodeArgs da)
 {
