@@ -19,8 +19,8 @@
 // whatever the lengths.  A range cuts segments into pieces: a whole segment
 // is written out, other pieces leave a (max, sum, accumulator) state in
 // workspace slot worker + rank of the segment, and a second kernel (a
-// programmatic dependent launch) joins them in worker order.  Worker w is
-// warp w / CTAs of CTA w % CTAs, so that short lists spread over the SMs.
+// programmatic dependent launch) joins them in worker order.  A CTA whose four
+// ranges lie within one segment joins their states itself.
 // Short work (few units for every warp) runs in one launch instead: a cluster
 // of CTAs a segment, whose warps join their states in shared memory.
 //
@@ -76,7 +76,9 @@ struct ListSmem {                                          // the rings, [warps]
     static constexpr int kFull = kListWarps * kStages * kUnitBytes;
     static constexpr int kFlag = kFull + kListWarps * kStages * 8;
     static constexpr int kSums = kFlag + 16;
-    static constexpr int kStart = kSums + 16;              // int [batch + 1]
+    static constexpr int kHow = kSums + 16;                // int [warps]: slot of the CTA's one state, or one of
+    static constexpr int kStart = kHow + 16;               // these; int [batch + 1]
+    enum { SPREAD = -1, ADJACENT = -2 };
     static size_t bytes(int batch) { return static_cast<size_t>(kStart) + 4u * (batch + 1); }
 };
 
@@ -685,6 +687,43 @@ __device__ __forceinline__ void flag_sequence(const Fp4AttnArgs &a, int b, const
 }
 
 // ---------------------------------------------------------------------- the list
+__device__ __forceinline__ float *warp_state(uint8_t *smem, int warp)
+{
+    return reinterpret_cast<float *>(smem + warp * kStages * kUnitBytes);
+}
+
+// Joins the states of a CTA's warps, whose ranges all lie within one segment,
+// into one (out: [group][kPartialStride]).  Out of line, so that the loop above it
+// is compiled as without it (in line, the mixed batch takes 0.5% longer).
+__device__ __noinline__ void join_warps(float *out, int group, uint8_t *smem, int warp, int lane)
+{
+    for (int g = warp; g < group; g += kListWarps) {
+        float m[kListWarps], l[kListWarps], M = -INFINITY, L = 0.f;
+        float4 A = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int w = 0; w < kListWarps; ++w) {
+            const float2 ml = *reinterpret_cast<const float2 *>(warp_state(smem, w) + g * kPartialStride + kHeadDim);
+            m[w] = ml.x;
+            l[w] = ml.y;
+            M = fmaxf(M, ml.x);
+        }
+#pragma unroll
+        for (int w = 0; w < kListWarps; ++w) {
+            const float e = ex2_approx(m[w] - M);
+            const float4 v = *reinterpret_cast<const float4 *>(warp_state(smem, w) + g * kPartialStride + 4 * lane);
+            L += e * l[w];
+            A.x += e * v.x;
+            A.y += e * v.y;
+            A.z += e * v.z;
+            A.w += e * v.w;
+        }
+        float *row = out + g * kPartialStride;
+        *reinterpret_cast<float4 *>(row + 4 * lane) = A;
+        if (lane == 0)
+            *reinterpret_cast<float2 *>(row + kHeadDim) = make_float2(M, L);
+    }
+}
+
 template <int kParts>
 __device__ __forceinline__ void work_list(const Fp4DecodeArgs &da, uint8_t *smem, int warp, int lane, int worker, int lo,
                                           int n)
@@ -703,6 +742,8 @@ __device__ __forceinline__ void work_list(const Fp4DecodeArgs &da, uint8_t *smem
         const Place p = place_of(start, a.batch, lo + u);
         return tile_number(a, sight_of(a, p.b), p.b, p.h, 2 * p.unit + (lane & 1));
     };
+    // (read where it is needed: a register less in the loop)
+    auto how = [&]() { return *reinterpret_cast<volatile int *>(smem + ListSmem::kHow + 4 * warp); };
     int now = look_up(0), next = -2;
     const uint32_t my_dst = ring + ((lane & 3) >> 1) * kUnitBytes + ((lane & 1) + 2 * ((lane >> 2) & 1)) * kFp4Tile;
     const uint8_t *my_src = lane < 4 ? a.k_cache : a.v_cache;
@@ -750,7 +791,7 @@ __device__ __forceinline__ void work_list(const Fp4DecodeArgs &da, uint8_t *smem
             if (p.unit == 0)
                 j->x = whole ? -1 : worker;
             if (p.unit + take == units)
-                j->y = worker;
+                j->y = how() == ListSmem::SPREAD ? worker : ~worker;
         }
         Query qu;
         {
@@ -832,6 +873,8 @@ __device__ __forceinline__ void work_list(const Fp4DecodeArgs &da, uint8_t *smem
                 for (int k = 0; k < 16; ++k)
                     v[k] *= f;
                 store16(a, row0 + g, 16 * r, v);
+            } else if (how() >= 0) {                       // over the ring, which nothing more is brought into
+                store_state(warp_state(smem, warp) + g * kPartialStride, s, l, j, r);
             } else if (slot < da.num_slots) {
                 store_state(da.partials + (slot * a.group + g) * kPartialStride, s, l, j, r);
             } else if (a.err && r == 0) {
@@ -921,7 +964,13 @@ __global__ void __launch_bounds__(kListThreads, kListCtas) paged_gqa_decode_fp4_
 
     const int total = start[a.batch] * a.hkv;
     const int active = min(static_cast<int>(gridDim.x) * kListWarps, total);
-    const int worker = warp * static_cast<int>(gridDim.x) + static_cast<int>(blockIdx.x);
+    // A CTA's warps take adjacent ranges, so that those within a segment leave one
+    // state for the join (one 32K sequence 16.7 us instead of 18.5, a 128K one among
+    // 63 of 512 tokens 45 instead of 54, the mixed batch 260.8 instead of 259.8).  The
+    // ranges of a list shorter than the workers spread over the CTAs.
+    const bool adjacent = total >= static_cast<int>(gridDim.x) * kListWarps;
+    const int worker = adjacent ? static_cast<int>(blockIdx.x) * kListWarps + warp
+                                : warp * static_cast<int>(gridDim.x) + static_cast<int>(blockIdx.x);
     if (worker < active) {
         // A range with a segment's end in it has one more piece to set up and to
         // store, which costs about a unit's time: the ranges are equal in a list
@@ -930,12 +979,33 @@ __global__ void __launch_bounds__(kListThreads, kListCtas) paged_gqa_decode_fp4_
         const bool wide = no_empty && total >= 2 * active;
         const int length = total + (wide ? a.batch * a.hkv : 0);
         const int each = length / active, more = length - each * active;   // the first `more` ranges: one longer
-        const int w = worker + (lane & 1);                 // even lanes: where the range begins, odd ones: where it ends
+        // lanes 4i, 4i + 1: where the range begins and ends; 4i + 2, 4i + 3: the CTA's ranges
+        const int w = (lane & 2 ? worker - warp : worker) + (lane & 1) * (lane & 2 ? kListWarps : 1);
         int edge = w * each + min(w, more);
         if (wide)
             edge = real_position(start, a.batch, a.hkv, edge);
         const int lo = __shfl_sync(kEvery, edge, 0), n = __shfl_sync(kEvery, edge, 1) - lo;
+        volatile int *how = reinterpret_cast<volatile int *>(smem + ListSmem::kHow + 4 * warp);
+        {
+            const int first = __shfl_sync(kEvery, edge, 2), last = __shfl_sync(kEvery, edge, 3);
+            int h = ListSmem::SPREAD;
+            if (adjacent) {
+                const Place p = place_of(start, a.batch, first);
+                const bool within = p.unit > 0 && last - first < start[p.b + 1] - start[p.b] - p.unit;
+                h = within ? worker - warp + p.h * a.batch + p.b : static_cast<int>(ListSmem::ADJACENT);
+            }
+            if (lane == 0)
+                *how = h;
+            __syncwarp();
+        }
         work_list<kParts>(da, smem, warp, lane, worker, lo, n);
+        if (*how >= 0) {                                   // the segment begins before and ends behind the CTA's ranges
+            __syncthreads();
+            if (*how < da.num_slots)
+                join_warps(da.partials + static_cast<int64_t>(*how) * a.group * kPartialStride, a.group, smem, warp, lane);
+            else if (a.err && lane == 0)
+                atomicOr(a.err, PKV_DEVERR_INTERNAL);
+        }
     }
 }
 
@@ -1091,8 +1161,8 @@ __global__ void __launch_bounds__(32 * kClusterWarps, 2) paged_gqa_decode_fp4_cl
 // (segment, head); its warps take the pieces in turns of kJoin, all of a
 // turn's loads in flight together, and are joined in warp order.  A turn is a round
 // trip to the L2, so turns are long and up to 16 warps share them (8 states and 8
-// warps: one 8K sequence 13.8 us instead of 12.5, a 128K one among 63 of 512 tokens 60
-// instead of 54).  Warps are as few as an average segment needs, because a CTA of one
+// warps, before CTAs joined their own: one 8K sequence 13.8 us instead of 12.5, a 128K
+// one among 63 of 512 tokens 60 instead of 54).  Warps are as few as an average segment needs, because a CTA of one
 // or two is on its SM before the list's CTAs have left it (four at least: 64 x 2K
 // tokens 37 us instead of 34.5).
 constexpr int kJoin = 16;
@@ -1108,13 +1178,24 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_fp4_kernel(const Fp4Deco
     const int b = sg / a.hkv, h = sg % a.hkv;
     const float vs = __ldg(a.v_scale + h);
     grid_wait();
-    const int2 j = da.joins[sg];
+    int2 j = da.joins[sg];
     if (j.x < 0)
         return;
-    const int pieces = j.y - j.x + 1;
+    // Of the workers x .. y, the CTAs strictly between have left one state, in the first
+    // of their slots (y = ~the last worker; else every worker has its own).
+    int head = 0, full = 0;
+    if (j.y < 0) {
+        j.y = ~j.y;
+        head = kListWarps - j.x % kListWarps;
+        full = max(0, j.y / kListWarps - 1 - j.x / kListWarps);
+    }
     const int64_t slot0 = static_cast<int64_t>(j.x) + h * a.batch + b;
-    if (j.y < j.x || slot0 + pieces > da.num_slots)
+    if (j.y < j.x || slot0 + (j.y - j.x) >= da.num_slots)
         return;                                            // an aborted call, or flagged by the decode kernel
+    const int pieces = j.y - j.x + 1 - (kListWarps - 1) * full;
+    auto worker = [&](int i) {                             // beyond x
+        return i < head || full == 0 ? i : (i < head + full ? head + kListWarps * (i - head) : i + (kListWarps - 1) * full);
+    };
     const float *base = da.partials + (slot0 * a.group + g) * kPartialStride;
     const int64_t stride = static_cast<int64_t>(a.group) * kPartialStride;
     float M = -INFINITY, L = 0.f;
@@ -1125,7 +1206,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_fp4_kernel(const Fp4Deco
 #pragma unroll
         for (int i = 0; i < kJoin; ++i) {
             const bool on = i0 + i < pieces;
-            const float *s = base + (on ? i0 + i : 0) * stride;
+            const float *s = base + (on ? worker(i0 + i) : 0) * stride;
             ml[i] = on ? *reinterpret_cast<const float2 *>(s + kHeadDim) : make_float2(-INFINITY, 0.f);
             v[i] = on ? *reinterpret_cast<const float4 *>(s + 4 * lane) : make_float4(0.f, 0.f, 0.f, 0.f);
         }

@@ -117,6 +117,17 @@ def test_decode_long_chain(pkv, cuda_device):
     _decode(pkv, c, q, qd)
 
 
+@pytest.mark.parametrize("max_ctas", [0, 5, 23])
+@pytest.mark.parametrize("out_dtype", [torch.float32, torch.bfloat16])
+def test_decode_one_long_sequence(pkv, cuda_device, max_ctas, out_dtype):
+    """A segment over many CTAs' ranges, beside short and empty ones."""
+    c = Cache(29, [40, 6000, 0, 7], 2, 16, cuda_device)
+    q, qd = c.queries(4, 14)
+    a = _decode(pkv, c, q, qd, out_dtype=out_dtype, max_ctas=max_ctas)
+    assert torch.equal(_decode(pkv, c, q, qd, out_dtype=out_dtype, max_ctas=max_ctas), a)
+    _decode(pkv, c, q, qd, 5000, 100, out_dtype=out_dtype, max_ctas=max_ctas)
+
+
 @pytest.mark.parametrize("spread", [30.0, 1e-4, 1e4])
 def test_decode_large_and_small_scores(pkv, cuda_device, spread):
     """Scores from almost equal to one that takes all the weight, rising and
