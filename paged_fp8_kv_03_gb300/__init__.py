@@ -688,18 +688,32 @@ def _error_word(device_error, dev):
 
 def _fp4_attention(q, out, k_scale, v_scale, block_table, seq_lens, seq_page_sizes, workspace, Hkv, dev):
     """What decode and prefill share: the tensors' addresses."""
-    if out.shape != q.shape:
-        raise ValueError("q / out shapes disagree")
-    B = seq_lens.shape[0]
-    if k_scale.shape[0] != Hkv or v_scale.shape[0] != Hkv:
-        raise ValueError("scales must have one entry per kv head")
-    if block_table.shape[0] != B or (seq_page_sizes is not None and seq_page_sizes.shape[0] != B):
-        raise ValueError("block_table, seq_lens and seq_page_sizes must have one entry per sequence")
-    return (_addr(q, "q", torch.bfloat16, 3, dev), _addr(out, "out", out.dtype, 3, dev), _act(out, "out"),
-            _addr(k_scale, "k_scale", torch.float32, 1, dev), _addr(v_scale, "v_scale", torch.float32, 1, dev),
-            _addr(block_table, "block_table", torch.int32, 2, dev), _addr(seq_lens, "seq_lens", torch.int32, 1, dev),
+    try:
+        if out.shape != q.shape:
+            raise ValueError("q / out shapes disagree")
+        B = seq_lens.shape[0]
+        if k_scale.shape[0] != Hkv or v_scale.shape[0] != Hkv:
+            raise ValueError("scales must have one entry per kv head")
+        if block_table.shape[0] != B or (seq_page_sizes is not None and seq_page_sizes.shape[0] != B):
+            raise ValueError("block_table, seq_lens and seq_page_sizes must have one entry per sequence")
+    except (AttributeError, IndexError):                       # no tensor, or of no dimensions: refused below
+        pass
+    return (_addr(q, "q", torch.bfloat16, 3, dev), _addr(out, "out", getattr(out, "dtype", None), 3, dev),
+            _act(out, "out"), _addr(k_scale, "k_scale", torch.float32, 1, dev),
+            _addr(v_scale, "v_scale", torch.float32, 1, dev), _addr(block_table, "block_table", torch.int32, 2, dev),
+            _addr(seq_lens, "seq_lens", torch.int32, 1, dev),
             None if seq_page_sizes is None else _addr(seq_page_sizes, "seq_page_sizes", torch.int32, 1, dev),
             _addr(workspace, "workspace", torch.uint8, None, dev))
+
+
+def _on(stream, device):
+    """Where a call allocates: memory belongs to the stream that uses it (else
+    work still ahead on the current stream may write to it, or get it next)."""
+    if stream is None:
+        return contextlib.nullcontext()
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream), device) if int(stream) else torch.cuda.default_stream(device)
+    return torch.cuda.stream(stream)
 
 
 def _check_window(window, sinks):
@@ -751,8 +765,9 @@ def kv_read_fp4(slot_mapping, k_scale, v_scale, k_cache, v_cache, k_out=None, v_
         raise ValueError("give both outputs or neither")
     if k_out is None:
         shape = (slot_mapping.shape[0], k_cache.shape[1], HEAD_DIM)
-        k_out = torch.zeros(shape, dtype=out_dtype, device=slot_mapping.device)
-        v_out = torch.zeros_like(k_out)
+        with _on(stream, slot_mapping.device):
+            k_out = torch.zeros(shape, dtype=out_dtype, device=slot_mapping.device)
+            v_out = torch.zeros_like(k_out)
     pkv_kv_read_fp4(slot_mapping, k_scale, v_scale, k_cache, v_cache, k_out, v_out, device_error, stream)
     return k_out, v_out
 
@@ -787,9 +802,10 @@ def pkv_paged_gqa_decode_fp4(q, k_cache, v_cache, k_scale, v_scale, block_table,
 def paged_gqa_decode_fp4(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, out=None,
                          out_dtype=torch.bfloat16, workspace=None, sm_scale=None, device_error=None, max_ctas=0,
                          stream=None, max_seq_len=0, seq_page_sizes=None, window=0, sinks=0) -> torch.Tensor:
-    """Allocating form of pkv_paged_gqa_decode_fp4."""
+    """Allocating form of pkv_paged_gqa_decode_fp4 (on the stream it runs on)."""
     if out is None:
-        out = torch.empty(q.shape, dtype=out_dtype, device=q.device)
+        with _on(stream, q.device):
+            out = torch.empty(q.shape, dtype=out_dtype, device=q.device)
     max_seq_len = _default_max_len(block_table, k_cache, max_seq_len, seq_page_sizes)
     if workspace is None:
         _cuda_index(q, "q")
@@ -798,7 +814,8 @@ def paged_gqa_decode_fp4(q, k_cache, v_cache, k_scale, v_scale, block_table, seq
                                               k_cache.shape[2], max_ctas)
         if n == 0:
             raise PkvError(4, "pkv_decode_fp4_workspace_size")
-        workspace = torch.empty(n, dtype=torch.uint8, device=q.device)
+        with _on(stream, q.device):
+            workspace = torch.empty(n, dtype=torch.uint8, device=q.device)
     pkv_paged_gqa_decode_fp4(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, out, workspace, sm_scale,
                              device_error, max_ctas, stream, max_seq_len, seq_page_sizes, window, sinks)
     return out
@@ -836,10 +853,11 @@ def pkv_paged_prefill_fp4(q, cu_q, k_cache, v_cache, k_scale, v_scale, block_tab
 def paged_prefill_fp4(q, cu_q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, max_q_len, out=None,
                       out_dtype=torch.bfloat16, max_kv_len=None, workspace=None, sm_scale=None, device_error=None,
                       stream=None, max_total_kv=0, seq_page_sizes=None, window=0, sinks=0) -> torch.Tensor:
-    """Allocating form of pkv_paged_prefill_fp4: max_kv_len defaults to the
-    block table's capacity, as in paged_prefill."""
+    """Allocating form of pkv_paged_prefill_fp4 (on the stream it runs on):
+    max_kv_len defaults to the block table's capacity, as in paged_prefill."""
     if out is None:
-        out = torch.empty(q.shape, dtype=out_dtype, device=q.device)
+        with _on(stream, q.device):
+            out = torch.empty(q.shape, dtype=out_dtype, device=q.device)
     if max_kv_len is None:
         if seq_page_sizes is not None:
             raise ValueError("give max_kv_len when seq_page_sizes is given")
@@ -848,7 +866,8 @@ def paged_prefill_fp4(q, cu_q, k_cache, v_cache, k_scale, v_scale, block_table, 
         _check_window(window, sinks)
         n = pkv_prefill_fp4_workspace_size(seq_lens.shape[0], k_cache.shape[1], max_q_len, max_kv_len, max_total_kv,
                                            window, sinks)
-        workspace = torch.empty(n, dtype=torch.uint8, device=q.device)
+        with _on(stream, q.device):
+            workspace = torch.empty(n, dtype=torch.uint8, device=q.device)
     pkv_paged_prefill_fp4(q, cu_q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, out, max_q_len,
                           max_kv_len, workspace, sm_scale, device_error, stream, max_total_kv, seq_page_sizes,
                           window, sinks)

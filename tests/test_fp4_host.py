@@ -226,3 +226,21 @@ def test_plain_window_counts():
     assert list(fp4_ref.visible(9, 0, 5)) == list(range(10))
     assert list(fp4_ref.visible(0, 1, 0)) == [0]
     assert fp4_ref.visible(-1, 4, 4).size == 0
+
+
+def test_binding_refuses_what_is_no_tensor():
+    u8, i32 = torch.uint8, torch.int32
+    pool, s = _fake(4, 2, 16, 72, dtype=u8), _fake(2)
+    q = _fake(3, 4, 128).to(torch.bfloat16)
+    good = dict(q=q, k_cache=pool, v_cache=pool, k_scale=s, v_scale=s, block_table=_fake(3, 5, dtype=i32),
+                seq_lens=_fake(3, dtype=i32), out=q, workspace=_fake(64, dtype=u8))
+    for name in good:
+        with pytest.raises(TypeError, match=f"{name} must be a torch.Tensor"):
+            pkv.pkv_paged_gqa_decode_fp4(**{**good, name: [1, 2, 3]})
+    with pytest.raises(TypeError, match="cu_q must be a torch.Tensor"):
+        pkv.pkv_paged_prefill_fp4(**good, cu_q=[0, 1, 2, 3], max_q_len=2, max_kv_len=80)
+    rows = dict(slot_mapping=_fake(3, dtype=torch.int64), k_scale=s, v_scale=s, k_cache=pool, v_cache=pool,
+                k_out=_fake(3, 2, 128), v_out=_fake(3, 2, 128))
+    for name in rows:
+        with pytest.raises(TypeError, match=f"{name} must be a torch.Tensor"):
+            pkv.pkv_kv_read_fp4(**{**rows, name: 5})

@@ -498,3 +498,32 @@ def test_calls_at_once_on_two_streams(pkv, cuda_device):
     torch.cuda.synchronize()
     for d, p in got:
         assert torch.equal(d, ref[0]) and torch.equal(p, ref[1])
+
+
+@pytest.mark.parametrize("as_int", [False, True])
+def test_allocating_calls_on_another_stream(pkv, cuda_device, as_int):
+    """What a call allocates belongs to the stream it runs on: work still ahead
+    on the current stream does not write to it."""
+    lens = [900, 33]
+    c = Cache(30, lens, 2, 16, cuda_device)
+    _, qd = c.queries(2, 8)
+    _, qp = c.queries(60, 8)
+    cu = torch.tensor([0, 40, 60], dtype=torch.int32, device=cuda_device)
+    slots = _dev(fp4_ref.slots_of(c.table[0], 900, 16), cuda_device)
+    slots[7] = -1
+    calls = [lambda s: pkv.paged_gqa_decode_fp4(qd, c.kc, c.vc, c.ksd, c.vsd, c.tabled, c.lensd, stream=s,
+                                                max_seq_len=900, max_ctas=3),
+             lambda s: pkv.paged_prefill_fp4(qp, cu, c.kc, c.vc, c.ksd, c.vsd, c.tabled, c.lensd, 40, max_kv_len=900,
+                                             stream=s),
+             lambda s: pkv.kv_read_fp4(slots, c.ksd, c.vsd, c.kc, c.vc, stream=s)[0]]
+    side = torch.cuda.Stream()
+    for call in calls:
+        ref = call(None)
+        n = ref.numel() * ref.element_size()
+        torch.cuda.synchronize()
+        torch.cuda._sleep(20_000_000)                            # some 10 ms of the current stream
+        for size in (n, n, 1 << 20, 4 << 20, 16 << 20):
+            torch.empty(size, dtype=torch.uint8, device=cuda_device).fill_(0x7F)
+        got = call(side.cuda_stream if as_int else side)
+        torch.cuda.synchronize()
+        assert torch.equal(got, ref)
