@@ -529,8 +529,9 @@ pkv_status pkv_kv_read_fp4(const int64_t *slot_mapping, int64_t num_tokens,
  * and sees the tokens named above; values are e * s times the head's scale.
  * Arguments, errors, clamping, zero rows for empty sequences and determinism
  * as pkv_paged_gqa_decode; q may have any finite bf16 values.  A bf16 output
- * rounds the softmax weights once to f16 before they meet V; an fp32 output
- * keeps them as two f16 parts.  One launch where max_seq_len (or the window)
+ * rounds the softmax weights once to f16 before they meet V (those below
+ * 2^-16 of the largest one to multiples of 2^-26 of it); an fp32 output
+ * keeps them as two f16 parts (2^-21, to 2^-36).  One launch where max_seq_len (or the window)
  * bounds every sequence to short work and max_ctas is 0, else two.
  *
  *   window, sinks  >= 0.

@@ -217,6 +217,9 @@ __global__ void __launch_bounds__(kPThreads, 1)
                          const __grid_constant__ CUtensorMap tm_v, const PrefillArgs a, const Fp4Window win)
 {
     constexpr int kFold = kFp4 ? kFold4 : kFold8;
+    // (4-bit cache: the reference of P's exponents is set well below the maximum, so that
+    // P's parts lose 2^-37 of the largest weight a key, not 2^-25)
+    constexpr float kMove = kFp4 ? 15.9f : 8.f, kLift = kFp4 ? 12.f : 0.f;
     // ---------------------------------------------------------------- the tile
     // (sequence, kv head)-major order, heaviest query tiles (largest positions)
     // first within each: the CTAs resident at one time mostly read the K/V of
@@ -539,7 +542,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
             // than 2^8 in this tile (then both warps redo it with the new one).
             red_max[(fb * 2 + half) * kRows + row] = mh;
             mbar_arrive(bar(PS::MX + fb * 4 + qtr));
-            const bool spec = j > 0 && !__any_sync(kAll, mh > m + 8.f);
+            const bool spec = j > 0 && !__any_sync(kAll, mh > m + kMove);
             float psum = 0.f;
             if (spec)
                 psum = emit(m);
@@ -550,7 +553,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
             const float mloc = fmaxf(mh, red_max[(fb * 2 + (half ^ 1)) * kRows + row]);
             bool redo = !spec;
             if (j == 0) {
-                m = mloc;                                  // key 0 is visible to every row (unless kWin)
+                m = mloc - kLift;                          // key 0 is visible to every row (unless kWin)
             } else {
                 // Every kFold tiles the segment accumulator (O_seg, TMEM columns
                 // kColO..) is added into O (kColM..) in fp32 and PV_j starts a new
@@ -559,7 +562,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
                 // 16K of them) would bias O by ~1e-3 relative.
                 const bool fold = (j % kFold) == 0;
                 const bool have_o = j > kFold;             // O holds earlier segments
-                const bool need = mloc > m + 8.f;
+                const bool need = mloc > m + kMove;
                 const bool rescale = __any_sync(kAll, need);
                 if (fold || rescale) {
                     // O_seg holds the segment up to tile j-1: wait for that PV.
@@ -568,7 +571,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
                         break;
                     }
                     tc::fence_after();
-                    const float mn = need ? mloc : m;
+                    const float mn = need ? mloc - kLift : m;
                     const float f = rescale && (!kWin || need) ? ex2_approx(m - mn) : 1.f;
 #pragma unroll 1
                     for (int c = 0; c < 4; ++c) {

@@ -527,3 +527,32 @@ def test_allocating_calls_on_another_stream(pkv, cuda_device, as_int):
         got = call(side.cuda_stream if as_int else side)
         torch.cuda.synchronize()
         assert torch.equal(got, ref)
+
+
+@pytest.mark.parametrize("out_dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("e", [12.0, 20.0, 26.0, 27.5])
+def test_many_small_weights(pkv, cuda_device, e, out_dtype):
+    """One token takes almost all the weight; 128K others, 2^-e of it each,
+    still count."""
+    L, dev = 131072, cuda_device
+    k, v = torch.zeros(L, 1, 128, device=dev), torch.ones(L, 1, 128, device=dev)
+    k[0, :, 0] = 6
+    v[0] = 0
+    s = torch.full((1,), 2.0 ** -6, device=dev)
+    kc, vc = pkv.fp4_cache(L // 16, 1, 16), pkv.fp4_cache(L // 16, 1, 16)
+    slots = torch.arange(L, device=dev)
+    pkv.kv_append_fp4(k, v, slots, s, s, kc, vc)
+    kr, vr = (x.double().cpu().numpy() for x in pkv.kv_read_fp4(slots, s, s, kc, vc, out_dtype=torch.float32))
+    q = torch.zeros(2, 4, 128, device=dev, dtype=torch.bfloat16)
+    q[:, :, 0] = 1
+    sm = float(np.float32(e * np.log(2) / kr[0, 0, 0]))
+    bt = torch.arange(L // 16, device=dev, dtype=torch.int32)[None]
+    ln = torch.tensor([L], device=dev, dtype=torch.int32)
+    cu = torch.tensor([0, 2], device=dev, dtype=torch.int32)
+    x = q[0].double().cpu().numpy()
+    ref = fp4_ref.attend(x, kr, vr, L - 1, 0, 0, sm)
+    tol = fp4_ref.attention_tolerance(x, kr, vr, ref, sm, out_dtype == torch.bfloat16)
+    got = pkv.paged_gqa_decode_fp4(q[1:], kc, vc, s, s, bt, ln, out_dtype=out_dtype, sm_scale=sm, max_seq_len=L)
+    _check(got[0], ref, tol, "decode")
+    got = pkv.paged_prefill_fp4(q, cu, kc, vc, s, s, bt, ln, 2, out_dtype=out_dtype, sm_scale=sm, max_kv_len=L)
+    _check(got[1], ref, tol, "prefill")
