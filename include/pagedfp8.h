@@ -528,11 +528,13 @@ pkv_status pkv_kv_read_fp4(const int64_t *slot_mapping, int64_t num_tokens,
  * window and sinks: the query of sequence b sits at position seq_lens[b] - 1
  * and sees the tokens named above; values are e * s times the head's scale.
  * Arguments, errors, clamping, zero rows for empty sequences and determinism
- * as pkv_paged_gqa_decode; q may have any finite bf16 values.  A bf16 output
- * rounds the softmax weights once to f16 before they meet V (those below
- * 2^-16 of the largest one to multiples of 2^-26 of it); an fp32 output
- * keeps them as two f16 parts (2^-21, to 2^-36).  One launch where max_seq_len (or the window)
- * bounds every sequence to short work and max_ctas is 0, else two.
+ * as pkv_paged_gqa_decode; q may have any finite bf16 values (those below 2^-17
+ * of their row's largest are taken to 2^-25 of it).  A bf16 output rounds the
+ * softmax weights once to f16 before they meet V (those below 2^-16 of the
+ * largest one to multiples of 2^-26 of it); an fp32 output keeps them as two
+ * f16 parts (2^-21, or 2^-37 of the largest).  One launch where max_seq_len
+ * (or the window) bounds every sequence to short work and max_ctas is 0, else
+ * two.
  *
  *   window, sinks  >= 0.
  *   workspace      device, >= pkv_decode_fp4_workspace_size(...) bytes for the

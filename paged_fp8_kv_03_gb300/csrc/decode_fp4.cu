@@ -484,7 +484,8 @@ __device__ __forceinline__ void whole_sums(const State &s, float (&l)[2])
 }
 
 // Q as B fragment: head r, dims 32c + 4 kk + {0, 1} and {2, 3}, brought to [1, 2)
-// by a power of two, so that f16 holds all its bits; f0, f1 turn unscaled scores of
+// by a power of two, so that f16 holds all bits of what is at least 2^-17 of the
+// row's largest |q|, and the rest to 2^-25 of that; f0, f1 turn unscaled scores of
 // heads 2c, 2c + 1 into exponents of 2.
 struct Query {
     uint32_t q[8][2];
