@@ -82,14 +82,14 @@ int decode_ctas(int batch, int max_ctas)
     return two < one ? two : one;
 }
 
-// Workspace: the segments' first and last workers, then one state a worker
+// Workspace: the segments' first and last workers, the workers' cut segments, then one state a worker
 // and one a segment (a piece's slot is worker + rank of its segment, distinct
 // because both grow along the list).
 size_t decode_workspace(int batch, int hq, int hkv, int ctas)
 {
     const size_t slots = static_cast<size_t>(ctas) * kFp4DecodeWorkers + static_cast<size_t>(batch) * hkv;
     const size_t bytes = slots * static_cast<size_t>(hq / hkv) * kPartialStride * sizeof(float);
-    return decode_fp4_join_bytes(batch, hkv) + ((bytes + 255) & ~size_t(255));
+    return decode_fp4_join_bytes(batch, hkv, ctas) + ((bytes + 255) & ~size_t(255));
 }
 
 }  // namespace
@@ -222,7 +222,8 @@ pkv_status pkv_paged_gqa_decode_fp4(const void *q, const uint8_t *k_cache, const
     if (units < ctas)
         ctas = static_cast<int>(units > 0 ? units : 1);
     da.joins = static_cast<int2 *>(workspace);
-    const size_t joins = decode_fp4_join_bytes(batch, num_kv_heads);
+    const size_t joins = decode_fp4_join_bytes(batch, num_kv_heads, ctas);
+    da.firsts = reinterpret_cast<int *>(da.joins + static_cast<size_t>(batch) * num_kv_heads);
     da.partials = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + joins);
     da.num_slots = static_cast<long long>((workspace_bytes - joins) / (sizeof(float) * a.group * kPartialStride));
     da.withhold = withheld_load();

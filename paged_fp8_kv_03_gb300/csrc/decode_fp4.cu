@@ -798,6 +798,8 @@ __device__ __forceinline__ void work_list(const Fp4DecodeArgs &da, uint8_t *smem
             int2 *j = da.joins + p.b * a.hkv + p.h;
             if (p.unit == 0)
                 j->x = whole ? -1 : worker;
+            if (p.unit == 0 && !whole)
+                da.firsts[worker] = p.b * a.hkv + p.h;
             if (p.unit + take == units)
                 j->y = how() == ListSmem::SPREAD ? worker : ~worker;
         }
@@ -979,6 +981,8 @@ __global__ void __launch_bounds__(kListThreads, kListCtas) paged_gqa_decode_fp4_
     const bool adjacent = total >= static_cast<int>(gridDim.x) * kListWarps;
     const int worker = adjacent ? static_cast<int>(blockIdx.x) * kListWarps + warp
                                 : warp * static_cast<int>(gridDim.x) + static_cast<int>(blockIdx.x);
+    if (lane == 0)
+        da.firsts[worker] = -1;
     if (worker < active) {
         // A range with a segment's end in it has one more piece to set up and to
         // store, which costs about a unit's time: the ranges are equal in a list
@@ -1165,27 +1169,26 @@ __global__ void __launch_bounds__(32 * kClusterWarps, 2) paged_gqa_decode_fp4_cl
 }
 
 // Joins the states of a segment's pieces for one query head, in worker order:
-// out = v_scale sum_i 2^(m_i - M) A_i / sum_i 2^(m_i - M) l_i.  A CTA per
-// (segment, head); its warps take the pieces in turns of kJoin, all of a
-// turn's loads in flight together, and are joined in warp order.  A turn is a round
-// trip to the L2, so turns are long and up to 16 warps share them (8 states and 8
-// warps, before CTAs joined their own: one 8K sequence 13.8 us instead of 12.5, a 128K
-// one among 63 of 512 tokens 60 instead of 54).  Warps are as few as an average segment needs, because a CTA of one
+// out = v_scale sum_i 2^(m_i - M) A_i / sum_i 2^(m_i - M) l_i.  Warps take the
+// pieces in turns, all of a turn's loads in flight together, and are joined in warp
+// order.  A turn is a round trip to the L2, so turns are long and, with a CTA a
+// (segment, head), up to 16 warps share them (8 states and 8 warps, before CTAs joined
+// their own: one 8K sequence 13.8 us instead of 12.5, a 128K one among 63 of 512 tokens
+// 60 instead of 54).  Warps are as few as an average segment needs, because a CTA of one
 // or two is on its SM before the list's CTAs have left it (four at least: 64 x 2K
 // tokens 37 us instead of 34.5).
-constexpr int kJoin = 16;
-constexpr int kJoinWarps = 16;
+constexpr int kJoin = 16, kJoinWarps = 16;
+constexpr int kJoinCut = 8;
 
-__global__ void __launch_bounds__(32 * kJoinWarps) join_fp4_kernel(const Fp4DecodeArgs da)
+// Head g of segment sg, by `warps` warps of the CTA (ra, rm: theirs), kTurn pieces
+// a turn.
+template <int kTurn>
+__device__ __forceinline__ void join_head(const Fp4DecodeArgs &da, int sg, int g, int warp, int warps, int lane,
+                                          float (*ra)[kHeadDim], float2 *rm)
 {
-    __shared__ __align__(16) float ra[kJoinWarps][kHeadDim];
-    __shared__ float2 rm[kJoinWarps];
     const Fp4AttnArgs &a = da.a;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
-    const int sg = blockIdx.x / a.group, g = blockIdx.x % a.group;
     const int b = sg / a.hkv, h = sg % a.hkv;
     const float vs = __ldg(a.v_scale + h);
-    grid_wait();
     int2 j = da.joins[sg];
     if (j.x < 0)
         return;
@@ -1208,11 +1211,11 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_fp4_kernel(const Fp4Deco
     const int64_t stride = static_cast<int64_t>(a.group) * kPartialStride;
     float M = -INFINITY, L = 0.f;
     float4 A = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int i0 = warp * kJoin; i0 < pieces; i0 += warps * kJoin) {
-        float4 v[kJoin];
-        float2 ml[kJoin];
+    for (int i0 = warp * kTurn; i0 < pieces; i0 += warps * kTurn) {
+        float4 v[kTurn];
+        float2 ml[kTurn];
 #pragma unroll
-        for (int i = 0; i < kJoin; ++i) {
+        for (int i = 0; i < kTurn; ++i) {
             const bool on = i0 + i < pieces;
             const float *s = base + (on ? worker(i0 + i) : 0) * stride;
             ml[i] = on ? *reinterpret_cast<const float2 *>(s + kHeadDim) : make_float2(-INFINITY, 0.f);
@@ -1220,14 +1223,14 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_fp4_kernel(const Fp4Deco
         }
         float mn = M;
 #pragma unroll
-        for (int i = 0; i < kJoin; ++i)
+        for (int i = 0; i < kTurn; ++i)
             mn = fmaxf(mn, ml[i].x);
         const float f = ex2_approx(M - mn);
         M = mn;
         L *= f;
         A = make_float4(A.x * f, A.y * f, A.z * f, A.w * f);
 #pragma unroll
-        for (int i = 0; i < kJoin; ++i) {
+        for (int i = 0; i < kTurn; ++i) {
             const float e = i0 + i < pieces ? ex2_approx(ml[i].x - mn) : 0.f;
             L += e * ml[i].y;
             A.x += e * v[i].x;
@@ -1249,7 +1252,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_fp4_kernel(const Fp4Deco
         L = 0.f;
         A = make_float4(0.f, 0.f, 0.f, 0.f);
         for (int w = 0; w < warps; ++w) {
-            if (w * kJoin >= pieces)
+            if (w * kTurn >= pieces)
                 break;                                     // a warp with no pieces
             const float e = ex2_approx(rm[w].x - mn);
             const float4 v = *reinterpret_cast<const float4 *>(&ra[w][4 * lane]);
@@ -1263,6 +1266,29 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_fp4_kernel(const Fp4Deco
     const float f = vs / L;
     store4(a, static_cast<int64_t>(b) * a.hq + static_cast<int64_t>(h) * a.group + g, 4 * lane,
            make_float4(A.x * f, A.y * f, A.z * f, A.w * f));
+}
+
+__global__ void __launch_bounds__(32 * kJoinWarps) join_fp4_kernel(const Fp4DecodeArgs da)
+{
+    __shared__ __align__(16) float ra[kJoinWarps][kHeadDim];
+    __shared__ float2 rm[kJoinWarps];
+    grid_wait();
+    join_head<kJoin>(da, blockIdx.x / da.a.group, blockIdx.x % da.a.group, threadIdx.x >> 5, blockDim.x >> 5,
+                     threadIdx.x & 31, ra, rm);
+}
+
+// The same for lists of many segments, of which at most one a worker is cut: a CTA a
+// worker, for the segment that its range begins and does not end; a warp a head.  A
+// CTA a (segment, head) is what such lists spend their time on: 64 query heads, 512 x
+// 128 tokens 43 us, this way 31; 1024 x 128 84 and 55; 128 x 512 29.4 and 26.8; 64 x
+// 1024 25.2 and 24.6.  With few segments it is the slower one (32 query heads, 64 x 2048: 35.4,
+// 35.1; 16 x 4096: 22.7, 21.7), as long segments have more pieces than a warp's turn.
+__global__ void __launch_bounds__(32 * PKV_MAX_GROUP) join_cut_fp4_kernel(const Fp4DecodeArgs da)
+{
+    grid_wait();
+    const int sg = da.firsts[blockIdx.x];
+    if (sg >= 0)
+        join_head<kJoinCut>(da, sg, threadIdx.x >> 5, 0, 1, threadIdx.x & 31, nullptr, nullptr);
 }
 
 }  // namespace
@@ -1321,7 +1347,11 @@ cudaError_t launch_paged_decode_fp4(const Fp4DecodeArgs &da, int ctas, cudaStrea
         return e;
     *site = "4-bit join kernel launch";
     const long long segs = static_cast<long long>(da.a.batch) * da.a.hkv;
-    const long long pieces = (static_cast<long long>(ctas) * kListWarps + segs - 1) / segs + 1;   // a segment's, on average
+    const int workers = ctas * kListWarps;
+    if (segs * da.a.group >= 2ll * workers)
+        return launch_with(join_cut_fp4_kernel, dim3(static_cast<unsigned>(workers)), 32 * da.a.group, 0, 1, true, stream,
+                           da);
+    const long long pieces = (workers + segs - 1) / segs + 1;   // a segment's, on average
     int warps = 1;
     while (warps < kJoinWarps && warps * kJoin < pieces)
         warps *= 2;

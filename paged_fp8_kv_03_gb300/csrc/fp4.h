@@ -61,6 +61,8 @@ struct Fp4DecodeArgs {
     Fp4AttnArgs a;
     int2 *joins;                                           // [batch * hkv]: workers of the segment's first and last
                                                            // piece; x = -1: nothing to join
+    int *firsts;                                           // [workers]: the segment that a worker's range begins and
+                                                           // does not end; -1: none
     float *partials;                                       // [num_slots][group][kPartialStride]
     long long num_slots;
     int cluster;                                           // CTAs a segment; 0: one list for all segments
@@ -96,9 +98,10 @@ cudaError_t launch_with(void (*kernel)(Params...), dim3 grid, unsigned threads, 
     return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
-inline size_t decode_fp4_join_bytes(int batch, int hkv)
+inline size_t decode_fp4_join_bytes(int batch, int hkv, int ctas)
 {
-    return (static_cast<size_t>(batch) * hkv * sizeof(int2) + 255) & ~size_t(255);
+    return (static_cast<size_t>(batch) * hkv * sizeof(int2) +
+            static_cast<size_t>(ctas) * kFp4DecodeWorkers * sizeof(int) + 255) & ~size_t(255);
 }
 
 // Prefill: 128-key tiles that a sequence's 16-bit copy can need, and the rows

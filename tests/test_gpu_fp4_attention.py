@@ -128,6 +128,17 @@ def test_decode_one_long_sequence(pkv, cuda_device, max_ctas, out_dtype):
     _decode(pkv, c, q, qd, 5000, 100, out_dtype=out_dtype, max_ctas=max_ctas)
 
 
+@pytest.mark.parametrize("max_ctas", [0, 3])
+@pytest.mark.parametrize("B,G,window,sinks", [(300, 8, 0, 0), (700, 3, 0, 0), (300, 7, 50, 3)])
+def test_decode_many_short_sequences(pkv, cuda_device, B, G, window, sinks, max_ctas):
+    """Many more (sequence, head) rows than warps, most of them whole, some cut."""
+    rng = np.random.default_rng(B)
+    c = Cache(31, [int(x) for x in rng.choice([0, 1, 20, 64, 90, 250], B)], 2, 16, cuda_device)
+    q, qd = c.queries(B, 2 * G)
+    a = _decode(pkv, c, q, qd, window, sinks, max_ctas=max_ctas)
+    assert torch.equal(_decode(pkv, c, q, qd, window, sinks, max_ctas=max_ctas), a)
+
+
 @pytest.mark.parametrize("spread", [30.0, 1e-4, 1e4])
 def test_decode_large_and_small_scores(pkv, cuda_device, spread):
     """Scores from almost equal to one that takes all the weight, rising and
