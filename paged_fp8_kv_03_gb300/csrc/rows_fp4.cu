@@ -151,7 +151,9 @@ __device__ __forceinline__ void quantise_part(const uint4 (&u)[2], const HeadSca
         auto value = [&](int i) {
             return __uint_as_float(kBf16 ? ((i & 1) ? w[i >> 1] & 0xFFFF0000u : w[i >> 1] << 16) : w[i & 7]);
         };
-        if (huge || scale == 0x7E) {                       // a saturated scale: x / step may be anything
+        if (scale == 0) {
+            // nothing of the block is left: its codes stay 0
+        } else if (huge || scale == 0x7E) {                // a saturated scale: x / step may be anything
 #pragma unroll 1
             for (int i = 0; i < P::kVals; i += 8) {
 #pragma unroll
@@ -159,7 +161,7 @@ __device__ __forceinline__ void quantise_part(const uint4 (&u)[2], const HeadSca
                     q[j] = __fdiv_rn(i ? value(j + P::kVals - 8) : value(j), step);
                 c[i >> 3] = f32x8_to_e2m1x8(q);
             }
-        } else if (scale != 0) {
+        } else {
             // The quotient lies between x y (1 - 2^-20) and x y (1 + 2^-20) (their
             // roundings and the quotient's are off by less than 2^-22), so where both
             // have the same code, it has that too.  Where they differ, in one warp of 700,
