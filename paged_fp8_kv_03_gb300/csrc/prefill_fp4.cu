@@ -21,9 +21,13 @@
 //   warp 1      tcgen05.mma, in the order  S_A(j+1) after O_A += P_A(j) V(j),
 //               S_B(j+1) after O_B += P_B(j) V(j)
 //   warps 2-5   softmax and output of tile A,  warps 6-9 of tile B
-// The accumulation is one chain of MMAs: the tensor cores add with truncation,
-// and a 128K context's 8192 additions of 16 keys leave at most 2^-11 in the
-// accumulator, on average half of that.
+// The tensor cores add with truncation, up to 2^-23 of the sum an addition of 16
+// keys, so a chain of additions must not grow with the context: every kFold2 key
+// tiles (1024 additions, 2^-13) a row's accumulator is added in fp32 to what earlier
+// folds have left, the sum's bf16 rounding is kept in the row's place in the output,
+// and the chain goes on from the rest, which fp32 holds exactly and which is at
+// most 2^-8 of the sum.  (512K tokens of V of one sign, 128 of them two thirds of
+// the sum: 6.8e-5 too small, in one chain 1.07e-3.)
 // Every wait is bounded (2 s): on expiry the CTA sets PKV_DEVERR_TIMEOUT,
 // drains its own copies and MMAs, frees TMEM and exits.
 #include <math.h>
@@ -46,6 +50,8 @@ constexpr int kThreads2 = 32 * (kWarp0 + 8);
 // 128K keys 2^-10 of all, under the output's 2^-9.  (A lift of 6 takes 3% longer with 16K
 // keys, 6% with a window.)
 constexpr float kMoveMax = 15.9f, kLift = 2.f;
+// Key tiles of one tensor-core accumulation (1024 additions, as in decode).
+constexpr int kFold2 = 128;
 constexpr uint32_t kScoreCol = 128, kOutCol = 256;   // tile x: scores at 128 x, accumulator at 256 + 128 x
 
 // Shared memory, offsets from a 1024-byte aligned base.  Operand tiles are
@@ -63,10 +69,11 @@ struct P2 {
     };
     static constexpr int kTmem = kBars + kNumBars * 8;
     static constexpr int kFlag = kTmem + 4;
-    static constexpr int kEnd = kFlag + 4;
-    static constexpr size_t bytes() { return static_cast<size_t>(kEnd) + 1024; }
+    static constexpr int kRow = (kFlag + 4 + 15) / 16 * 16;   // FoldRow [2][kRows]
+    static constexpr int kEnd = kRow + 2 * kRows * 16;
+    static constexpr size_t bytes(bool folds) { return static_cast<size_t>(folds ? kEnd : kFlag + 4) + 1024; }
 };
-static_assert(P2::bytes() <= 232448, "prefill tile buffers exceed the shared memory of one CTA");
+static_assert(P2::bytes(true) <= 232448, "prefill tile buffers exceed the shared memory of one CTA");
 
 // ---------------------------------------------------------------------- widening
 // The 16-bit copies' regions are laid out as the FP8 widening kernel's: tile_off
@@ -212,7 +219,73 @@ __global__ void __launch_bounds__(256) kv_widen_fp4_kernel(const PrefillArgs a, 
 }
 
 // ---------------------------------------------------------------------- attention
-template <bool kWin>
+__device__ __forceinline__ void bf16x8(const uint4 &u, float (&v)[8])
+{
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        v[i] = __uint_as_float((i & 1) ? w[i >> 1] & 0xFFFF0000u : w[i >> 1] << 16);
+}
+
+// What a softmax thread of the folding kernel keeps in shared memory for its row:
+// registers are short, and what the scores' loop does not use costs it time.
+struct FoldRow {
+    uint4 *out;                                            // its place in the output; nullptr: padding
+    float m, pad;                                          // its reference at the last fold
+};
+
+__device__ __forceinline__ volatile FoldRow &fold_row()
+{
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    return reinterpret_cast<volatile FoldRow *>(smem + P2::kRow)[threadIdx.x - 32 * kWarp0];
+}
+
+// Folds a row's accumulator (m: its reference; old: earlier folds have left
+// something in the output): the bf16 rounding of their sum goes to the output,
+// the rest back into the accumulator.  Out of line, for the loop around it.
+__device__ __noinline__ void fold(uint32_t o_tm, float m, bool old)
+{
+    volatile FoldRow &st = fold_row();
+    uint4 *dst = st.out;
+    const float back = old ? ex2_approx(st.m - m) : 0.f;
+    st.m = m;
+#pragma unroll 1
+    for (int c = 0; c < 8; ++c) {
+        uint4 was[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            was[i] = old && dst ? dst[2 * c + i] : make_uint4(0, 0, 0, 0);
+        uint32_t o[16];
+        tc::ld16(o_tm + 16 * c, o);
+        tc::wait_ld();
+        if (dst) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                float y[8];
+                bf16x8(was[i], y);
+                uint32_t w[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    uint32_t &o0 = o[8 * i + 2 * e], &o1 = o[8 * i + 2 * e + 1];
+                    const float s0 = __uint_as_float(o0) + y[2 * e] * back;
+                    const float s1 = __uint_as_float(o1) + y[2 * e + 1] * back;
+                    const __nv_bfloat162 b = __floats2bfloat162_rn(s0, s1);
+                    w[e] = *reinterpret_cast<const uint32_t *>(&b);
+                    o0 = __float_as_uint(s0 - __uint_as_float(w[e] << 16));
+                    o1 = __float_as_uint(s1 - __uint_as_float(w[e] & 0xFFFF0000u));
+                }
+                dst[2 * c + i] = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+        }
+        __syncwarp();
+        tc::st16(o_tm + 16 * c, o);
+    }
+    tc::wait_st();
+}
+
+// kFolds: for calls in which a query tile may visit more than kFold2 key tiles.
+template <bool kWin, bool kFolds>
 __global__ void __launch_bounds__(kThreads2, 1)
     paged_prefill_pair_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                               const __grid_constant__ CUtensorMap tm_v, const PrefillArgs a, const Fp4Window win)
@@ -409,6 +482,12 @@ __global__ void __launch_bounds__(kThreads2, 1)
         const uint32_t s_tm = tm + (static_cast<uint32_t>(qtr * 32) << 16) + kScoreCol * x;
         const uint32_t o_tm = s_tm + kOutCol;
         float m = -INFINITY, l = 0.f;
+        auto place = [&]() {
+            const int64_t orow = (static_cast<int64_t>(q0) + t0 + x * tpt + tl) * a.hq + h * G + g;
+            return reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.out) + orow * kHeadDim);
+        };
+        if (kFolds)
+            fold_row().out = valid ? place() : nullptr;
         bool ok = ntx > 0 && wwait(bar(P2::Q_FULL + x), 0, abort_flag, a.err, lane);
         if (ok) {
             // rows past the G x tpt that the copy fills are zeroed
@@ -427,6 +506,14 @@ __global__ void __launch_bounds__(kThreads2, 1)
                 mbar_arrive(bar(P2::Q_READY + x));
         }
         for (int j = 0; ok && j < ntx; ++j) {
+            if (kFolds && j > 0 && j % kFold2 == 0) {
+                if (!wwait(bar(P2::PV_DONE + x), (j - 1) & 1, abort_flag, a.err, lane)) {
+                    ok = false;
+                    break;
+                }
+                tc::fence_after();
+                fold(o_tm, m, j > kFold2);
+            }
             if (!wwait(bar(P2::S_FULL + x), j & 1, abort_flag, a.err, lane)) {
                 ok = false;
                 break;
@@ -529,19 +616,27 @@ __global__ void __launch_bounds__(kThreads2, 1)
             tc::fence_after();
             const float inv = __ldg(a.v_scale + h) / l;
             const uint32_t nans = nan_blocks<kWin>(a, win, row0 / kKeys, ntx, p_row, lane, key_tile, copy_tile);
-            const int64_t orow = (static_cast<int64_t>(q0) + t0 + x * tpt + tl) * a.hq + h * G + g;
-            uint4 *dst = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.out) + orow * kHeadDim);
+            uint4 *dst = kFolds ? fold_row().out : place();
+            const bool folded = kFolds && ntx > kFold2;
+            const float back = folded ? ex2_approx(fold_row().m - m) : 0.f;
 #pragma unroll 1
             for (int c = 0; c < 4; ++c) {
                 uint32_t o[32];
                 tc::ld32(o_tm + 32 * c, o);
                 tc::wait_ld();
-                if (!valid)
+                if (kFolds ? dst == nullptr : !valid)
                     continue;
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
                     uint32_t w[4];
                     const float f = (nans >> (2 * c + (k >> 1))) & 1u ? NAN : inv;
+                    if (folded) {
+                        float y[8];
+                        bf16x8(dst[4 * c + k], y);
+#pragma unroll
+                        for (int e = 0; e < 8; ++e)
+                            o[8 * k + e] = __float_as_uint(__uint_as_float(o[8 * k + e]) + y[e] * back);
+                    }
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
                         const __nv_bfloat162 b2 = __floats2bfloat162_rn(__uint_as_float(o[8 * k + 2 * e]) * f,
@@ -563,7 +658,7 @@ __global__ void __launch_bounds__(kThreads2, 1)
 }
 
 std::mutex g_pair_mu;
-unsigned long long g_pair_ctx[64][2] = {};   // per device and kernel: the context its limit was raised in
+unsigned long long g_pair_ctx[64][4] = {};   // per device and kernel: the context its limit was raised in
 
 }  // namespace
 
@@ -583,8 +678,21 @@ cudaError_t launch_widen_fp4(const PrefillArgs &a, const Fp4Window &win, cudaStr
 cudaError_t launch_prefill_pair(const PrefillArgs &a, const Fp4Window &win, const CUtensorMap &tm_q,
                                 const CUtensorMap &tm_k16, const CUtensorMap &tm_v16, cudaStream_t stream)
 {
-    const int which = win.window > 0 ? 1 : 0;
-    const auto kernel = which ? paged_prefill_pair_kernel<true> : paged_prefill_pair_kernel<false>;
+    // Key tiles that a pair of query tiles may visit: without a window all of the longest
+    // sequence's, with one the sinks' and those that 2 tokens_per_tile + window - 1 keys touch.
+    int64_t tiles = (static_cast<int64_t>(a.max_kv_len) + kKeys - 1) / kKeys;
+    if (win.window > 0) {
+        const int64_t seen = (static_cast<int64_t>(win.sinks) + kKeys - 1) / kKeys +
+                             (static_cast<int64_t>(win.window) + 2 * a.tokens_per_tile) / kKeys + 2;
+        tiles = seen < tiles ? seen : tiles;
+    }
+    // The folding kernel takes longer even where it folds nothing (4096 of 16384 tokens, 64
+    // query heads: 1172 us instead of 1153), and where it does (2048 of 131072: 5.91 ms, in
+    // one chain 5.70; 1024 of 524288: 12.2 and 11.7).
+    const bool folds = tiles > kFold2;
+    const int which = (win.window > 0 ? 1 : 0) + (folds ? 2 : 0);
+    const auto kernel = win.window > 0 ? (folds ? paged_prefill_pair_kernel<true, true> : paged_prefill_pair_kernel<true, false>)
+                                       : (folds ? paged_prefill_pair_kernel<false, true> : paged_prefill_pair_kernel<false, false>);
     int dev = -1;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess)
@@ -597,14 +705,14 @@ cudaError_t launch_prefill_pair(const PrefillArgs &a, const Fp4Window &win, cons
         std::lock_guard<std::mutex> lk(g_pair_mu);
         if (!known || g_pair_ctx[dev][which] != ctx) {
             e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                     static_cast<int>(P2::bytes()));
+                                     static_cast<int>(P2::bytes(folds)));
             if (e != cudaSuccess)
                 return e;
             g_pair_ctx[dev][which] = known ? ctx : 0;
         }
     }
     const int64_t grid = static_cast<int64_t>(a.batch) * a.hkv * ((a.max_tiles + 1) / 2);
-    kernel<<<static_cast<unsigned>(grid), kThreads2, P2::bytes(), stream>>>(tm_q, tm_k16, tm_v16, a, win);
+    kernel<<<static_cast<unsigned>(grid), kThreads2, P2::bytes(folds), stream>>>(tm_q, tm_k16, tm_v16, a, win);
     return cudaGetLastError();
 }
 
