@@ -531,7 +531,9 @@ pkv_status pkv_kv_read_fp4(const int64_t *slot_mapping, int64_t num_tokens,
  * as pkv_paged_gqa_decode; q may have any finite bf16 values (those below 2^-17
  * of their row's largest are taken to 2^-25 of it).  A bf16 output rounds the
  * softmax weights once to f16 before they meet V (those below 2^-16 of the
- * largest one to multiples of 2^-26 of it); an fp32 output keeps them as two
+ * largest one to multiples of 2^-26 of it, and to finer ones where more than
+ * 128K tokens are seen, so that all tokens' roundings of this kind stay below
+ * 2^-10 of the largest weight); an fp32 output keeps them as two
  * f16 parts (2^-21, or 2^-37 of the largest).  One launch where max_seq_len
  * (or the window) bounds every sequence to short work and max_ctas is 0, else
  * two.

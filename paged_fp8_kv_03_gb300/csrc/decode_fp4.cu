@@ -57,14 +57,19 @@ namespace {
 
 constexpr unsigned kEvery = 0xffffffffu;
 constexpr int kUnitBytes = 4 * kFp4Tile;                   // K tile 0, K tile 1, V tile 0, V tile 1
-// A weight is 2^(score - m) with a reference m that is kLift below the largest
+// A weight is 2^(score - m) with a reference m that is a lift below the largest
 // score so far (log2 units) when it is set, and moves only when a score exceeds it
 // by more than kMoveMax: weights up to 2^15.9 are within f16.  The lift keeps small weights off
 // f16's lower end, where 2^-25 is lost: of the largest weight 2^-27 a token in one part,
 // 2^-10 of all for 128K tokens, under a bf16 output's 2^-9; 2^-37 in two.
 constexpr float kMoveMax = 15.9f;
+// (With more than 128K tokens in sight the lift of one part grows with their logarithm,
+// so that 2^-10 of all stays the most, up to 2^27 tokens.)
 template <int kParts>
-constexpr float kLift = kParts == 1 ? 2.f : 12.f;
+__device__ __forceinline__ float lift_of(int tiles)
+{
+    return kParts == 1 ? 2.f + static_cast<float>(min(max(19 - __clz(tiles - 1), 0), 10)) : 12.f;
+}
 // Units after which a piece's accumulator is added into an fp32 copy: the
 // tensor cores add with truncation, whose error grows with the chain.  1024
 // additions (512 units of one part) may leave 2^-13 under a bf16 output's 2^-8.
@@ -601,8 +606,9 @@ __device__ __forceinline__ void take_unit(uint32_t st, const LaneOffsets &o, con
             t0 = fmaxf(t0, __shfl_xor_sync(kEvery, t0, d));
             t1 = fmaxf(t1, __shfl_xor_sync(kEvery, t1, d));
         }
-        const float n0 = t0 > s.m0 + kMoveMax ? t0 - kLift<kParts> : s.m0;
-        const float n1 = t1 > s.m1 + kMoveMax ? t1 - kLift<kParts> : s.m1;
+        const float lift = lift_of<kParts>(sg.tiles);
+        const float n0 = t0 > s.m0 + kMoveMax ? t0 - lift : s.m0;
+        const float n1 = t1 > s.m1 + kMoveMax ? t1 - lift : s.m1;
         const float g0 = n0 == s.m0 ? 1.f : ex2_approx(s.m0 - n0), g1 = n1 == s.m1 ? 1.f : ex2_approx(s.m1 - n1);
         s.m0 = n0;
         s.m1 = n1;

@@ -48,7 +48,8 @@ constexpr int kThreads2 = 32 * (kWarp0 + 8);
 // 2^15.9 is within f16, and moving it costs a pass over the accumulator.  The lift keeps small
 // weights off f16's lower end, where 2^-25 is lost: 2^-27 of the largest weight a key, for
 // 128K keys 2^-10 of all, under the output's 2^-9.  (A lift of 6 takes 3% longer with 16K
-// keys, 6% with a window.)
+// keys, 6% with a window.)  Beyond them it grows with the keys' logarithm, so that all
+// of them (up to 2^27 keys) still lose 2^-10 at most.
 constexpr float kMoveMax = 15.9f, kLift = 2.f;
 // Key tiles of one tensor-core accumulation (1024 additions, as in decode).
 constexpr int kFold2 = 128;
@@ -282,6 +283,13 @@ __device__ __noinline__ void fold(uint32_t o_tm, float m, bool old)
         tc::st16(o_tm + 16 * c, o);
     }
     tc::wait_st();
+}
+
+// The lift where a row visits nt key tiles: one more from 1025, 2049, .. on.
+template <bool kFolds>
+__device__ __forceinline__ float lift_of(int nt)
+{
+    return kFolds ? kLift + static_cast<float>(min(max(22 - __clz(nt - 1), 0), 10)) : kLift;
 }
 
 // kFolds: for calls in which a query tile may visit more than kFold2 key tiles.
@@ -562,7 +570,7 @@ __global__ void __launch_bounds__(kThreads2, 1)
             const float top = fmaxf(max3(mx[0], mx[1], mx[2]), max3(max3(mx[3], mx[4], mx[5]), mx[6], mx[7])) * sl2;
             const bool need = top > m + kMoveMax;
             if (__any_sync(kAll, need)) {
-                const float mn = need ? top - kLift : m;
+                const float mn = need ? top - lift_of<kFolds>(ntx) : m;
                 const float f = need ? ex2_approx(m - mn) : 1.f;
                 m = mn;
                 l *= f;

@@ -1,5 +1,5 @@
-"""Outputs over hundreds of thousands of tokens: the accumulation may
-not lose more as contexts grow."""
+"""Outputs over hundreds of thousands of tokens: neither the accumulation nor
+the smallest weights may lose more as contexts grow."""
 import numpy as np
 import pytest
 import torch
@@ -87,3 +87,39 @@ def test_prefill_over_several_chains_in_place(pkv, cuda_device):
         g.replay()
         torch.cuda.synchronize()
         assert torch.equal(out, ref)
+
+
+@pytest.mark.parametrize("out_dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("call", ["prefill", "decode", "decode_one_cta"])
+@pytest.mark.parametrize("units", [8.5, 2.5])
+def test_many_small_weights_of_a_long_context(pkv, cuda_device, call, out_dtype, units):
+    """One token takes most of the weight, a million others 2^-e of it each:
+    in f16 with the largest weight at 4 they would be 8.5 (2.5) steps of 2^-24,
+    half a step from the next one."""
+    n, dev = 1 << 20, cuda_device
+
+    def make(t0, t1):
+        k, v = torch.zeros(t1 - t0, 1, 128, device=dev), torch.ones(t1 - t0, 1, 128, device=dev)
+        if t0 == 0:
+            k[0, :, 0] = 6
+            v[0] = 0
+        return k, v
+
+    c = LongCache(pkv, n, 1, dev, make)
+    _, k, _ = next(c.pieces())
+    q = torch.zeros(2, 4, 128, device=dev, dtype=torch.bfloat16)
+    q[:, :, 0] = 1
+    e = 26 - np.log2(units)
+    sm = float(np.float32(e * np.log(2) / float(k[0, 0, 0])))
+    if call == "prefill":
+        ref, _ = c.attend(q, sm, torch.tensor([n - 2, n - 1], device=dev))
+        got = c.prefill(q, sm, out_dtype=out_dtype)
+    else:
+        q = q[:1]
+        ref, _ = c.attend(q, sm)
+        got = c.decode(q, sm, out_dtype=out_dtype, max_ctas=1 if call == "decode_one_cta" else 0)
+    # the tolerance of the other tests, with |v| <= 1 and the largest score of e ln 2
+    tol = fp4_ref.attention_tolerance(q[0].double().cpu().numpy(), k[:1].cpu().numpy(), np.ones((1, 1, 128)),
+                                      ref[0].cpu().numpy(), sm, out_dtype == torch.bfloat16)
+    off = (got.double() - ref).abs().cpu().numpy()
+    assert (off <= tol).all(), (off.max(), tol.min())
