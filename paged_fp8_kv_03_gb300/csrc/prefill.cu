@@ -429,7 +429,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
         const int g = row - tl * G;
         const bool valid = row < G * tpt && tl < nv;
         const int p_row = valid ? pos0 + tl : last;      // padding rows mirror the last row
-        const float sl2 = __ldg(a.k_scale + h) * a.sm_scale_log2;
+        const float sl2 = score_factor(a, h);
         const uint32_t lanes = tm + (static_cast<uint32_t>(qtr * 32) << 16);
         float *red_max = reinterpret_cast<float *>(smem + PS::kRedMax);
         float *red_l = reinterpret_cast<float *>(smem + PS::kRedL);

@@ -161,6 +161,14 @@ __device__ __forceinline__ bool sequence_ok(const PrefillArgs &a, int b, int q0,
     return ok;
 }
 
+// What turns raw scores into exponents of 2.  A product too small for fp32 is its
+// smallest number instead of 0, which would make NaN of a hidden key's -inf.
+__device__ __forceinline__ float score_factor(const PrefillArgs &a, int h)
+{
+    const float f = __ldg(a.k_scale + h) * a.sm_scale_log2;
+    return f == 0.f ? __uint_as_float(1u) : f;
+}
+
 // Key tiles of a sequence that some query of its chunk sees, under a window of
 // the 4-bit cache's calls: tiles 0 .. first - 1 (sinks) and then first + skip ..
 // (keys from `from` on).  Without a window: all of them (first = skip = 0).

@@ -486,7 +486,7 @@ __global__ void __launch_bounds__(kThreads2, 1)
         const int g = row - tl * G;
         const bool valid = row < G * tpt && tl < nvx;
         const int p_row = pos0 + x * tpt + (valid ? tl : nvx - 1);   // padding rows mirror the last row
-        const float sl2 = __ldg(a.k_scale + h) * a.sm_scale_log2;
+        const float sl2 = score_factor(a, h);
         const uint32_t s_tm = tm + (static_cast<uint32_t>(qtr * 32) << 16) + kScoreCol * x;
         const uint32_t o_tm = s_tm + kOutCol;
         float m = -INFINITY, l = 0.f;
