@@ -412,8 +412,8 @@ size_t pkv_decode_noalloc_scratch_bytes(void);
  *                  the workspace: a batch of one long prompt and many short
  *                  chunks needs room for the long one only once).
  *   seq_lens       device int32 [batch]; a sequence with n_b > max_q_len,
- *                  seq_lens[b] < n_b, seq_lens[b] > max_kv_len or beyond
- *                  its table row, or inconsistent cu_q, sets
+ *                  seq_lens[b] < n_b, seq_lens[b] > max_kv_len, beyond
+ *                  its table row or above 2^31 - 128, or inconsistent cu_q, sets
  *                  PKV_DEVERR_SEQLEN and its rows are not written; so does a
  *                  sequence whose widened copy would not fit the workspace
  *                  (the sum bound exceeded).

@@ -9,6 +9,7 @@ namespace pkv {
 
 constexpr int kRows = 128;                       // M: rows of a query tile
 constexpr int kKeys = 128;                       // keys per tile
+constexpr int kMaxKv = INT32_MAX - (kKeys - 1);  // longest sequence: 32 bits hold it rounded up to whole key tiles
 constexpr uint64_t kWaitNs = 2000000000ull;
 constexpr unsigned kAll = 0xffffffffu;
 
@@ -154,8 +155,9 @@ __device__ __forceinline__ bool sequence_ok(const PrefillArgs &a, int b, int q0,
 {
     const int n = q1 - q0;
     const int lp = seq_page_log2(a, b);
-    const bool ok = q0 >= 0 && n >= 0 && q1 <= a.total_q && n <= a.max_q_len && L >= n && L <= a.max_kv_len &&
-                    lp >= 0 && static_cast<int64_t>(L) <= (static_cast<int64_t>(a.max_pages) << lp);
+    const bool ok = q0 >= 0 && n >= 0 && q1 <= a.total_q && n <= a.max_q_len && L >= n &&
+                    L <= min(a.max_kv_len, kMaxKv) && lp >= 0 &&
+                    static_cast<int64_t>(L) <= (static_cast<int64_t>(a.max_pages) << lp);
     if (!ok && report && a.err)
         atomicOr(a.err, lp < 0 ? PKV_DEVERR_PAGESIZE : PKV_DEVERR_SEQLEN);
     return ok;
