@@ -37,6 +37,7 @@ HEAD_DIM = 128
 MAX_GROUP = 8
 MAX_BATCH = 8192
 FP4_ROW_BYTES = 72
+_INT32_MAX = 2 ** 31 - 1
 
 _lib = None
 _lock = threading.Lock()
@@ -717,8 +718,19 @@ def _on(stream, device):
 
 
 def _check_window(window, sinks):
+    """Both as the library's 32-bit arguments; no sequence is longer than the
+    largest of them."""
     if window < 0 or sinks < 0:
         raise ValueError("window and sinks must not be negative")
+    return min(int(window), _INT32_MAX), min(int(sinks), _INT32_MAX)
+
+
+def _int32(value, name):
+    """value as a 32-bit argument (ctypes would keep its low bits)."""
+    value = int(value)
+    if not -_INT32_MAX <= value <= _INT32_MAX:
+        raise ValueError(f"{name} must fit 32 bits, got {value}")
+    return value
 
 
 def fp4_cache(num_pages, num_kv_heads, page_size, device=None) -> torch.Tensor:
@@ -776,7 +788,8 @@ def pkv_decode_fp4_workspace_size(batch, num_q_heads, num_kv_heads, head_dim=HEA
                                   max_ctas=0) -> int:
     """Workspace bytes of a 4-bit decode call of these sizes."""
     return int(load().pkv_decode_fp4_workspace_size(int(batch), int(num_q_heads), int(num_kv_heads), int(head_dim),
-                                                    int(max_seq_len), int(page_size), int(max_ctas)))
+                                                    _int32(max_seq_len, "max_seq_len"), int(page_size),
+                                                    _int32(max_ctas, "max_ctas")))
 
 
 def pkv_paged_gqa_decode_fp4(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, out, workspace,
@@ -792,11 +805,11 @@ def pkv_paged_gqa_decode_fp4(q, k_cache, v_cache, k_scale, v_scale, block_table,
     B, Hq, D = q.shape
     if seq_lens.shape[0] != B:
         raise ValueError("seq_lens must have one entry per row of q")
-    _check_window(window, sinks)
+    window, sinks = _check_window(window, sinks)
     _call("pkv_paged_gqa_decode_fp4", dev, stream, (_lib or load()).pkv_paged_gqa_decode_fp4, qa, kc, vc, ks, vs, bt,
-          block_table.shape[1], lens, int(max_seq_len), psz, B, Hq, Hkv, D, P, NP,
-          1.0 / math.sqrt(D) if sm_scale is None else float(sm_scale), int(window), int(sinks), oa, odt, ws, workspace.numel(),
-          _error_word(device_error, dev), int(max_ctas))
+          block_table.shape[1], lens, _int32(max_seq_len, "max_seq_len"), psz, B, Hq, Hkv, D, P, NP,
+          1.0 / math.sqrt(D) if sm_scale is None else float(sm_scale), window, sinks, oa, odt, ws, workspace.numel(),
+          _error_word(device_error, dev), _int32(max_ctas, "max_ctas"))
 
 
 def paged_gqa_decode_fp4(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, out=None,
@@ -823,8 +836,10 @@ def paged_gqa_decode_fp4(q, k_cache, v_cache, k_scale, v_scale, block_table, seq
 
 def pkv_prefill_fp4_workspace_size(batch, num_kv_heads, max_q_len, max_kv_len, max_total_kv=0, window=0,
                                    sinks=0) -> int:
-    return int(load().pkv_prefill_fp4_workspace_size(int(batch), int(num_kv_heads), int(max_q_len), int(max_kv_len),
-                                                     int(max_total_kv), int(window), int(sinks)))
+    window, sinks = (max(-1, min(int(x), _INT32_MAX)) for x in (window, sinks))
+    return int(load().pkv_prefill_fp4_workspace_size(int(batch), int(num_kv_heads), _int32(max_q_len, "max_q_len"),
+                                                     _int32(max_kv_len, "max_kv_len"), int(max_total_kv), window,
+                                                     sinks))
 
 
 def pkv_paged_prefill_fp4(q, cu_q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, out, max_q_len,
@@ -843,10 +858,11 @@ def pkv_paged_prefill_fp4(q, cu_q, k_cache, v_cache, k_scale, v_scale, block_tab
     B = seq_lens.shape[0]
     if cu_q.shape[0] != B + 1:
         raise ValueError("cu_q must have one entry more than seq_lens")
-    _check_window(window, sinks)
-    _call("pkv_paged_prefill_fp4", dev, stream, (_lib or load()).pkv_paged_prefill_fp4, qa, cu, T, int(max_q_len), kc,
-          vc, ks, vs, bt, block_table.shape[1], lens, psz, B, int(max_kv_len), int(max_total_kv), Hq, Hkv, D, P, NP,
-          1.0 / math.sqrt(D) if sm_scale is None else float(sm_scale), int(window), int(sinks), oa, odt, ws, workspace.numel(),
+    window, sinks = _check_window(window, sinks)
+    _call("pkv_paged_prefill_fp4", dev, stream, (_lib or load()).pkv_paged_prefill_fp4, qa, cu, T,
+          _int32(max_q_len, "max_q_len"), kc, vc, ks, vs, bt, block_table.shape[1], lens, psz, B,
+          _int32(max_kv_len, "max_kv_len"), int(max_total_kv), Hq, Hkv, D, P, NP,
+          1.0 / math.sqrt(D) if sm_scale is None else float(sm_scale), window, sinks, oa, odt, ws, workspace.numel(),
           _error_word(device_error, dev))
 
 
