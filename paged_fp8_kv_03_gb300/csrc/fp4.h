@@ -121,7 +121,8 @@ inline long long prefill_fp4_rows(int batch, int hkv, int max_q_len, int max_kv_
     }
     long long tiles = per * batch;
     if (max_total_kv > 0) {
-        const long long t2 = (max_total_kv + 127) / 128 + batch;   // sum of ceil(L_b / 128) <= sum L_b / 128 + batch
+        // sum of ceil(L_b / 128) <= sum L_b / 128 + batch
+        const long long t2 = max_total_kv / 128 + (max_total_kv % 128 != 0) + batch;
         tiles = t2 < tiles ? t2 : tiles;
     }
     return tiles * 128 * hkv;

@@ -157,7 +157,8 @@ inline long long prefill_rows_bound(int batch, int hkv, int max_kv_len, long lon
 {
     long long tiles = static_cast<long long>(batch) * ((static_cast<long long>(max_kv_len) + 127) / 128);
     if (max_total_kv > 0) {
-        const long long t2 = (max_total_kv + 127) / 128 + batch;   // sum of ceil(L_b / 128) <= sum L_b / 128 + batch
+        // sum of ceil(L_b / 128) <= sum L_b / 128 + batch
+        const long long t2 = max_total_kv / 128 + (max_total_kv % 128 != 0) + batch;
         tiles = t2 < tiles ? t2 : tiles;
     }
     return tiles * 128 * hkv;
