@@ -43,7 +43,7 @@
 // Heads are columns of both results, so the running maximum and sum of a head
 // sit in the lanes that hold its accumulator and a rescale needs no exchange;
 // the reference that takes the maximum's place is moved only when a score exceeds it
-// by more than 2^15.9.
+// by more than 15.9 (log2 units, so a weight of 2^15.9).
 //
 // Every wait on an mbarrier is bounded (2 s): on expiry the kernel raises
 // PKV_DEVERR_TIMEOUT, stops issuing copies, drains those in flight, returns.
@@ -61,7 +61,7 @@ constexpr int kUnitBytes = 4 * kFp4Tile;                   // K tile 0, K tile 1
 // score so far (log2 units) when it is set, and moves only when a score exceeds it
 // by more than kMoveMax: weights up to 2^15.9 are within f16.  The lift keeps small weights off
 // f16's lower end, where 2^-25 is lost: of the largest weight 2^-27 a token in one part,
-// 2^-10 of all for 128K tokens, under a bf16 output's 2^-9; 2^-37 in two.
+// 2^-10 of all for 128K tokens, under a bf16 output's 2^-8; 2^-37 in two.
 constexpr float kMoveMax = 15.9f;
 // (With more than 128K tokens in sight the lift of one part grows with their logarithm,
 // so that 2^-10 of all stays the most, up to 2^27 tokens.)
@@ -71,9 +71,9 @@ __device__ __forceinline__ float lift_of(int tiles)
     return kParts == 1 ? 2.f + static_cast<float>(min(max(19 - __clz(tiles - 1), 0), 10)) : 12.f;
 }
 // Units after which a piece's accumulator is added into an fp32 copy: the
-// tensor cores add with truncation, whose error grows with the chain.  1024
+// tensor cores add with truncation, up to 2^-23 of the sum an addition.  1024
 // additions (512 units of one part) may leave 2^-13 under a bf16 output's 2^-8.
-// Under an fp32 one 64 (16 units of two parts) are kept to 2^-18, and measure
+// Under an fp32 one 64 (16 units of two parts) may leave 2^-17, and measure
 // 1e-6 over 8K to 60K tokens, what a plain fp32 computation has; 256 measured 3e-6.
 template <int kParts>
 constexpr int kFoldUnits = kParts == 1 ? 512 : 16;
@@ -707,8 +707,8 @@ __device__ __forceinline__ float *warp_state(uint8_t *smem, int warp)
 }
 
 // Joins the states of a CTA's warps, whose ranges all lie within one segment,
-// into one (out: [group][kPartialStride]).  Out of line, so that the loop above it
-// is compiled as without it (in line, the mixed batch takes 0.5% longer).
+// into one (out: [group][kPartialStride]).  Out of line, for the loop above it (in
+// line, the mixed batch takes 0.5% longer).
 __device__ __noinline__ void join_warps(float *out, int group, uint8_t *smem, int warp, int lane)
 {
     for (int g = warp; g < group; g += kListWarps) {
@@ -981,8 +981,8 @@ __global__ void __launch_bounds__(kListThreads, kListCtas) paged_gqa_decode_fp4_
     const int total = start[a.batch] * a.hkv;
     const int active = min(static_cast<int>(gridDim.x) * kListWarps, total);
     // A CTA's warps take adjacent ranges, so that those within a segment leave one
-    // state for the join (one 32K sequence 16.7 us instead of 18.5, a 128K one among
-    // 63 of 512 tokens 45 instead of 54, the mixed batch 260.8 instead of 259.8).  The
+    // state for the join (32 query heads, one 32K sequence 16.8 us, with a state a warp
+    // 18.2; a 128K one among 63 of 512 tokens 46.0 and 57.8; 32 x 4K 34.2 and 33.8).  The
     // ranges of a list shorter than the workers spread over the CTAs.
     const bool adjacent = total >= static_cast<int>(gridDim.x) * kListWarps;
     const int worker = adjacent ? static_cast<int>(blockIdx.x) * kListWarps + warp
@@ -1181,11 +1181,11 @@ __global__ void __launch_bounds__(32 * kClusterWarps, 2) paged_gqa_decode_fp4_cl
 // out = v_scale sum_i 2^(m_i - M) A_i / sum_i 2^(m_i - M) l_i.  Warps take the
 // pieces in turns, all of a turn's loads in flight together, and are joined in warp
 // order.  A turn is a round trip to the L2, so turns are long and, with a CTA a
-// (segment, head), up to 16 warps share them (8 states and 8 warps, before CTAs joined
-// their own: one 8K sequence 13.8 us instead of 12.5, a 128K one among 63 of 512 tokens
-// 60 instead of 54).  Warps are as few as an average segment needs, because a CTA of one
-// or two is on its SM before the list's CTAs have left it (four at least: 64 x 2K
-// tokens 37 us instead of 34.5).
+// (segment, head), up to 16 warps share them (32 query heads, a 128K sequence among 63
+// of 512 tokens 46.0 us, with 8 states and 8 warps 48.3; one 128K sequence alone 34.0 and
+// 33.3).  Warps are as few as an average segment needs, because a CTA of one or two is
+// on its SM before the list's CTAs have left it (64 x 2K tokens 35.0 us, with four at
+// least 39.0; 32 x 4K 34.2 and 36.0; the long one among short ones 46.0 and 43.7).
 constexpr int kJoin = 16, kJoinWarps = 16;
 constexpr int kJoinCut = 8;
 

@@ -44,7 +44,8 @@
 //   warps 2-9   online softmax, two warps per TMEM lane quarter: one row per
 //               thread, each warp one half (64 keys) of the tile.  The row
 //               maximum is exchanged through shared memory; exp2 domain, lazy
-//               rescaling (only when the maximum grows by more than 2^8);
+//               rescaling (only when P would exceed 2^8; 4-bit cache:
+//               2^15.9);
 //               P is written over S in TMEM.  Every kFold key tiles they add
 //               O_seg into O (a second TMEM accumulator) in fp32 and the next
 //               PV starts O_seg afresh, so no chain of accumulating MMAs is
@@ -498,7 +499,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
                     mx[(k >> 1) & 7] = max3(mx[(k >> 1) & 7], __uint_as_float(x[c][k]), __uint_as_float(x[c][k + 1]));
             const float mh = fmaxf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])),
                                    fmaxf(fmaxf(mx[4], mx[5]), fmaxf(mx[6], mx[7]))) * sl2;
-            // P = 2^(x sl2 - mm) <= 2^8 as f16 hi + lo, written over each 32-column
+            // P = 2^(x sl2 - mm) <= 2^kMove as f16 hi + lo, written over each 32-column
             // piece of S (hi in its first 16 columns, lo in the last 16); returns
             // the half row's sum of P.
             // Pairs of elements go through the paired fp32 add / fma (fewer
@@ -539,7 +540,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
             // Publish this half's maximum to the other half's warp (same lane
             // quarter).  While it is in flight, compute P with the running
             // maximum: that is the final P unless a row's maximum grows by more
-            // than 2^8 in this tile (then both warps redo it with the new one).
+            // than kMove (log2 units) in this tile (then both warps redo it with the new one).
             red_max[(fb * 2 + half) * kRows + row] = mh;
             mbar_arrive(bar(PS::MX + fb * 4 + qtr));
             const bool spec = j > 0 && !__any_sync(kAll, mh > m + kMove);
@@ -557,9 +558,8 @@ __global__ void __launch_bounds__(kPThreads, 1)
             } else {
                 // Every kFold tiles the segment accumulator (O_seg, TMEM columns
                 // kColO..) is added into O (kColM..) in fp32 and PV_j starts a new
-                // segment: the tensor cores' accumulation rounds toward zero, and
-                // a chain of thousands of accumulating MMAs (a 128K context is
-                // 16K of them) would bias O by ~1e-3 relative.
+                // segment: the tensor cores' accumulation rounds toward zero, by
+                // up to 2^-23 of the sum an MMA, and a 128K context is 16K of them.
                 const bool fold = (j % kFold) == 0;
                 const bool have_o = j > kFold;             // O holds earlier segments
                 const bool need = mloc > m + kMove;

@@ -47,7 +47,7 @@ constexpr int kThreads2 = 32 * (kWarp0 + 8);
 // units) when it is set, and moves only when it is exceeded by more than kMoveMax: P <=
 // 2^15.9 is within f16, and moving it costs a pass over the accumulator.  The lift keeps small
 // weights off f16's lower end, where 2^-25 is lost: 2^-27 of the largest weight a key, for
-// 128K keys 2^-10 of all, under the output's 2^-9.  (A lift of 6 takes 3% longer with 16K
+// 128K keys 2^-10 of all, under the output's 2^-8.  (A lift of 6 takes 3% longer with 16K
 // keys, 6% with a window.)  Beyond them it grows with the keys' logarithm, so that all
 // of them (up to 2^27 keys) still lose 2^-10 at most.
 constexpr float kMoveMax = 15.9f, kLift = 2.f;
