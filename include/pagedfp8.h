@@ -568,7 +568,8 @@ pkv_status pkv_paged_gqa_decode_fp4(const void *q,
  * named above).  Call it after pkv_kv_append_fp4 has written the chunk's own
  * K/V.  Arguments, errors, untouched rows and determinism as
  * pkv_paged_prefill; the softmax weights are rounded as in
- * pkv_paged_gqa_decode_fp4.
+ * pkv_paged_gqa_decode_fp4.  Rows of more than 128 key tiles hold partial sums
+ * while the call runs.
  *
  *   window, sinks  >= 0.
  *   workspace      device, >= pkv_prefill_fp4_workspace_size(batch,

@@ -823,46 +823,61 @@ __device__ __forceinline__ void work_list(const Fp4DecodeArgs &da, uint8_t *smem
         State s;
         clear(s);
         float mf0 = -INFINITY, mf1 = -INFINITY;            // maxima of the units folded so far
-        for (int i = 0; i < take; ++i) {
-            if (!(stage & 1) && !wait_stage(full + 4 * stage, parity, stop, a.err, lane)) {
-                dead = true;
-                break;
-            }
-            take_unit<kParts>(ring + stage * kUnitBytes, offsets, qu, sg, inner, p.unit + i, lane, s, [&]() {
-                if ((stage & 1) && u + i + kStages - 1 < n) {   // the two units just read make room
-                    fence_proxy_async_smem();
-                    __syncwarp();
-                    issue(u + i + kStages - 1, stage - 1);
+        uint64_t sums = 0ull;                              // and their sums
+        for (int i = 0; i < take && !dead;) {              // (folded between loops: in one, 3% longer)
+            const int end = min(take, i + kFoldUnits<kParts>);
+#pragma unroll 1
+            for (; i < end; ++i) {
+                if (!(stage & 1) && !wait_stage(full + 4 * stage, parity, stop, a.err, lane)) {
+                    dead = true;
+                    break;
                 }
-            });
-            if (++stage == kStages) {
-                stage = 0;
-                parity ^= 1u;
+                take_unit<kParts>(ring + stage * kUnitBytes, offsets, qu, sg, inner, p.unit + i, lane, s, [&]() {
+                    if ((stage & 1) && u + i + kStages - 1 < n) {   // the two units just read make room
+                        fence_proxy_async_smem();
+                        __syncwarp();
+                        issue(u + i + kStages - 1, stage - 1);
+                    }
+                });
+                if (++stage == kStages) {
+                    stage = 0;
+                    parity ^= 1u;
+                }
             }
-            if ((i + 1) % kFoldUnits<kParts> == 0 || (i + 1 == take && take > kFoldUnits<kParts>)) {
-                // the piece's own slot of the workspace holds the copy (each lane its own elements)
-                const bool old = i + 1 > kFoldUnits<kParts>, last = i + 1 == take;
+            if (!dead && take >= kFoldUnits<kParts>) {
+                // the piece's own slot of the workspace holds the accumulator's copy (each lane its own elements)
+                const bool old = i > kFoldUnits<kParts>, last = i == take;
                 const float g0 = old ? ex2_approx(mf0 - s.m0) : 0.f, g1 = old ? ex2_approx(mf1 - s.m1) : 0.f;
                 if (slot >= da.num_slots) {
                     if (a.err && lane == 0)
                         atomicOr(a.err, PKV_DEVERR_INTERNAL);
                 } else {
+                    // what a sum's rounding loses stays in the lanes, unless it is the last one
                     float *at0 = da.partials + slot * a.group * kPartialStride;
+                    auto add = [&](float *at, float v, float g) {
+                        float rest;
+                        const float sum = two_sum(old ? *at * g : 0.f, v, rest);
+                        if (!last)
+                            *at = sum;
+                        return last ? sum : rest;
+                    };
 #pragma unroll
                     for (int j = 0; j < 2; ++j) {
                         if (2 * c + j >= a.group)
                             continue;
+                        const float g = j ? g1 : g0;
                         float *at = at0 + (2 * c + j) * kPartialStride + 16 * r;
 #pragma unroll
                         for (int k = 0; k < 16; ++k) {
                             float &v = s.acc[k >> 1][2 * (k & 1) + j];
-                            v += old ? at[k] * (j ? g1 : g0) : 0.f;
-                            if (!last) {
-                                at[k] = v;
-                                v = 0.f;
-                            }
+                            v = add(at + k, v, g);
                         }
                     }
+                    const float2 was = unpack2(sums), now = unpack2(s.sum);
+                    float2 rest;
+                    sums = pack2(two_sum(old ? was.x * g0 : 0.f, now.x, rest.x),
+                                 two_sum(old ? was.y * g1 : 0.f, now.y, rest.y));
+                    s.sum = last ? sums : pack2(rest.x, rest.y);
                 }
                 mf0 = s.m0;
                 mf1 = s.m1;

@@ -37,6 +37,15 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_
         : "memory");
 }
 
+// a + b rounded, and exactly what that loses (Knuth's two-sum).  Long sums of like
+// terms keep it: rounded the same way every time, they drift by up to 2^-24 a term.
+__device__ __forceinline__ float two_sum(float a, float b, float &rest)
+{
+    const float s = __fadd_rn(a, b), t = __fsub_rn(s, a);
+    rest = __fadd_rn(__fsub_rn(a, __fsub_rn(s, t)), __fsub_rn(b, t));
+    return s;
+}
+
 __device__ __forceinline__ float e4m3_value(uint8_t c)
 {
     const __half_raw h = __nv_cvt_fp8_to_halfraw(c, __NV_E4M3);

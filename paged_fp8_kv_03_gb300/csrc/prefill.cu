@@ -65,6 +65,7 @@ namespace {
 
 constexpr int kKStages = 2, kVStages = 3;        // operand rings: K bf16, V f16
 constexpr int kFold8 = 32, kFold4 = 4;           // key tiles per segment of O: FP8 cache; 4-bit cache, fp32 output
+constexpr int kMove4 = 64;                       // key tiles after which O and l move on (4-bit cache)
 constexpr int kSmWarp0 = 2;                      // first softmax warp
 constexpr int kSmWarps = 8;
 constexpr int kPThreads = 32 * (kSmWarp0 + kSmWarps);
@@ -91,10 +92,11 @@ struct PS {
     };
     static constexpr int kTmem = kBars + kNumBars * 8;
     static constexpr int kFlag = kTmem + 4;
-    static constexpr int kEnd = kFlag + 4;
-    static constexpr size_t bytes() { return static_cast<size_t>(kEnd) + 1024; }
+    static constexpr int kMoved = (kFlag + 4 + 15) / 16 * 16;   // MovedRow [2 halves][128 rows] (4-bit cache)
+    static constexpr int kEnd = kMoved + 2 * kRows * static_cast<int>(sizeof(MovedRow));
+    static constexpr size_t bytes(bool moves) { return static_cast<size_t>(moves ? kEnd : kFlag + 4) + 1024; }
 };
-static_assert(PS::bytes() <= 232448, "prefill tile buffers exceed the shared memory of one CTA");
+static_assert(PS::bytes(true) <= 232448, "prefill tile buffers exceed the shared memory of one CTA");
 
 // f16 pair -> bf16 pair (exact for widened E4M3 values: 3 mantissa bits).
 __device__ __forceinline__ uint32_t f16x2_to_bf16x2(uint32_t h)
@@ -209,10 +211,67 @@ __global__ void __launch_bounds__(256) kv_widen_kernel(const PrefillArgs a)
 }
 
 // ---------------------------------------------------------------------- attention
+// What a softmax thread of the 4-bit cache's kernel for long contexts keeps in
+// shared memory.
+__device__ __forceinline__ volatile MovedRow &moved_row()
+{
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    return reinterpret_cast<volatile MovedRow *>(smem + PS::kMoved)[threadIdx.x - 32 * kSmWarp0];
+}
+
+// Adds a half row's O and O_seg (TMEM columns from cm and cs on; m: their
+// reference) and its sum l to what was put into the output before (old).  What the
+// sums' rounding loses stays in O, the last time all of it; O_seg becomes zero.
+// Returns the sum of all.  Out of line, for the loop around it.
+__device__ __noinline__ float move_out(uint32_t cm, uint32_t cs, float m, float l, bool old, bool last)
+{
+    volatile MovedRow &st = moved_row();
+    uint4 *dst = st.out;
+    const float back = old ? ex2_approx(st.m - m) : 0.f;
+    l = old ? st.l * back + l : l;
+    st.m = m;
+    st.l = l;
+#pragma unroll 1
+    for (int c = 0; c < 4; ++c) {
+        uint4 was[4] = {};
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (old && dst)
+                was[i] = dst[4 * c + i];
+        const uint32_t *y = reinterpret_cast<const uint32_t *>(was);
+        uint32_t o[16], t[16];
+        tc::ld16(cs + 16 * c, o);
+        tc::ld16(cm + 16 * c, t);
+        tc::wait_ld();
+#pragma unroll
+        for (int k = 0; k < 16; ++k) {
+            float r0, r1;
+            const float s0 = two_sum(__uint_as_float(t[k]), __uint_as_float(o[k]), r0);
+            const float s1 = two_sum(__uint_as_float(y[k]) * back, s0, r1);
+            o[k] = __float_as_uint(s1);
+            t[k] = __float_as_uint(r0 + r1);
+        }
+        if (dst && !last)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                dst[4 * c + i] = make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+        __syncwarp();
+        tc::st16(cm + 16 * c, last ? o : t);
+#pragma unroll
+        for (int k = 0; k < 16; ++k)
+            t[k] = 0u;
+        tc::st16(cs + 16 * c, t);
+    }
+    tc::wait_st();
+    return l;
+}
+
 // kWin: the 4-bit cache's calls with a window (and an fp32 output); a row may
 // then see nothing of a tile, or of all tiles so far (its running maximum is
-// -inf until it does).  kFp4: the 4-bit cache's.
-template <bool kWin, bool kFp4>
+// -inf until it does).  kFp4: the 4-bit cache's.  kMoves: those of long contexts,
+// whose sums move on every kMove4 key tiles.
+template <bool kWin, bool kFp4, bool kMoves>
 __global__ void __launch_bounds__(kPThreads, 1)
     paged_prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                          const __grid_constant__ CUtensorMap tm_v, const PrefillArgs a, const Fp4Window win)
@@ -435,6 +494,11 @@ __global__ void __launch_bounds__(kPThreads, 1)
         float *red_max = reinterpret_cast<float *>(smem + PS::kRedMax);
         float *red_l = reinterpret_cast<float *>(smem + PS::kRedL);
         float m = -INFINITY, l = 0.f;
+        if (kMoves) {
+            const int64_t orow = (static_cast<int64_t>(q0) + t0 + tl) * a.hq + h * G + g;
+            moved_row().out = valid ? reinterpret_cast<uint4 *>(static_cast<float *>(a.out) + orow * kHeadDim + 64 * half)
+                                    : nullptr;
+        }
         // The query tile is the A operand of S = Q K^T as TMA wrote it (bf16,
         // 128B-swizzled, row = token x G + head).  Rows past the G x tpt the
         // copy fills are zeroed here (this warp: its row, dims 64 half ..).
@@ -458,6 +522,16 @@ __global__ void __launch_bounds__(kPThreads, 1)
                 break;
             }
             tc::fence_after();
+            // (S_j behind PV_{j-2}: so PV_DONE's phase is that of PV_{j-1})
+            if (kMoves && j > 0 && j % kMove4 == 0) {
+                if (!wwait(bar(PS::PV_DONE), (j - 1) & 1, abort_flag, a.err, lane)) {
+                    ok = false;
+                    break;
+                }
+                tc::fence_after();
+                move_out(lanes + kColM + 64 * half, lanes + kColO + 64 * half, m, l, j > kMove4, false);
+                l = 0.f;
+            }
             const uint32_t s_tm = lanes + fb * 128 + 64 * half;
             uint32_t x[2][32];
             tc::ld32(s_tm, x[0]);
@@ -617,6 +691,8 @@ __global__ void __launch_bounds__(kPThreads, 1)
         }
         if (ok && wwait(bar(PS::O_FINAL), 0, abort_flag, a.err, lane)) {
             tc::fence_after();
+            if (kMoves && nt > kMove4)
+                l = move_out(lanes + kColM + 64 * half, lanes + kColO + 64 * half, m, l, true, true);
             red_l[half * kRows + row] = l;
             mbar_arrive(bar(PS::LX + qtr));
             ok = wwait(bar(PS::LX + qtr), 0, abort_flag, a.err, lane);
@@ -676,12 +752,12 @@ __global__ void __launch_bounds__(kPThreads, 1)
 }
 
 std::mutex g_prefill_mu;
-unsigned long long g_prefill_attr_ctx[64][3] = {};   // per device and kernel: the context its limit was raised in
+unsigned long long g_prefill_attr_ctx[64][5] = {};   // per device and kernel: the context its limit was raised in
 
 typedef void (*PrefillKernel)(const CUtensorMap, const CUtensorMap, const CUtensorMap, const PrefillArgs,
                               const Fp4Window);
 
-cudaError_t raise_limit(PrefillKernel kernel, int which)
+cudaError_t raise_limit(PrefillKernel kernel, int which, size_t bytes)
 {
     int dev = -1;
     cudaError_t e = cudaGetDevice(&dev);
@@ -693,7 +769,7 @@ cudaError_t raise_limit(PrefillKernel kernel, int which)
     const bool known = current_context_id(&ctx);
     std::lock_guard<std::mutex> lk(g_prefill_mu);
     if (!known || g_prefill_attr_ctx[dev][which] != ctx) {
-        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(PS::bytes()));
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes));
         if (e != cudaSuccess)
             return e;
         g_prefill_attr_ctx[dev][which] = known ? ctx : 0;
@@ -722,13 +798,12 @@ cudaError_t launch_widen(const PrefillArgs &a, cudaStream_t stream)
     return cudaGetLastError();
 }
 
-template <bool kWin, bool kFp4>
-cudaError_t launch_attention(const PrefillArgs &a, const Fp4Window &win, const CUtensorMap &tm_q,
-                             const CUtensorMap &tm_k16, const CUtensorMap &tm_v16, cudaStream_t stream)
+cudaError_t launch_attention(PrefillKernel kernel, size_t smem, const PrefillArgs &a, const Fp4Window &win,
+                             const CUtensorMap &tm_q, const CUtensorMap &tm_k16, const CUtensorMap &tm_v16,
+                             cudaStream_t stream)
 {
     const int64_t grid = static_cast<int64_t>(a.batch) * a.hkv * a.max_tiles;
-    paged_prefill_kernel<kWin, kFp4><<<static_cast<unsigned>(grid), kPThreads, PS::bytes(), stream>>>(tm_q, tm_k16,
-                                                                                                     tm_v16, a, win);
+    kernel<<<static_cast<unsigned>(grid), kPThreads, smem, stream>>>(tm_q, tm_k16, tm_v16, a, win);
     return cudaGetLastError();
 }
 
@@ -736,7 +811,7 @@ cudaError_t launch_attention(const PrefillArgs &a, const Fp4Window &win, const C
 
 size_t prefill_smem_bytes()
 {
-    return PS::bytes();
+    return PS::bytes(false);
 }
 
 cudaError_t launch_paged_prefill(const PrefillArgs &a, const CUtensorMap &tm_q, const CUtensorMap &tm_k16,
@@ -745,10 +820,11 @@ cudaError_t launch_paged_prefill(const PrefillArgs &a, const CUtensorMap &tm_q, 
     if (static_cast<int64_t>(a.batch) * a.hkv * a.max_tiles <= 0)
         return cudaSuccess;
     const Fp4Window none = {0, 0};
-    cudaError_t e = raise_limit(paged_prefill_kernel<false, false>, 0);
+    const PrefillKernel kernel = paged_prefill_kernel<false, false, false>;
+    cudaError_t e = raise_limit(kernel, 4, PS::bytes(false));
     if (e == cudaSuccess)
         e = launch_widen(a, stream);
-    return e == cudaSuccess ? launch_attention<false, false>(a, none, tm_q, tm_k16, tm_v16, stream) : e;
+    return e == cudaSuccess ? launch_attention(kernel, PS::bytes(false), a, none, tm_q, tm_k16, tm_v16, stream) : e;
 }
 
 cudaError_t launch_paged_prefill_fp4(const PrefillArgs &a, const Fp4Window &win, const CUtensorMap &tm_q,
@@ -756,18 +832,22 @@ cudaError_t launch_paged_prefill_fp4(const PrefillArgs &a, const Fp4Window &win,
 {
     if (static_cast<int64_t>(a.batch) * a.hkv * a.max_tiles <= 0)
         return cudaSuccess;
+    // The moving kernel takes 6% longer (4096 of 16384 tokens, 64 query heads: 2.03 ms
+    // instead of 1.92) or 9% (1024 of 131072: 5.26 ms instead of 4.83); up to 128 key
+    // tiles l has at most 128 additions (2^-17) and O 32 without it.
+    const bool moves = most_key_tiles(a, win) > 2 * kMove4;
+    const PrefillKernel kernel =
+        win.window > 0 ? (moves ? paged_prefill_kernel<true, true, true> : paged_prefill_kernel<true, true, false>)
+                       : (moves ? paged_prefill_kernel<false, true, true> : paged_prefill_kernel<false, true, false>);
     cudaError_t e = cudaSuccess;
     if (a.out_f32)
-        e = win.window > 0 ? raise_limit(paged_prefill_kernel<true, true>, 1)
-                           : raise_limit(paged_prefill_kernel<false, true>, 2);
+        e = raise_limit(kernel, (win.window > 0 ? 1 : 0) + (moves ? 2 : 0), PS::bytes(moves));
     if (e == cudaSuccess)
         e = launch_widen_fp4(a, win, stream);
     if (e != cudaSuccess)
         return e;
-    if (!a.out_f32)
-        return launch_prefill_pair(a, win, tm_q, tm_k16, tm_v16, stream);
-    return win.window > 0 ? launch_attention<true, true>(a, win, tm_q, tm_k16, tm_v16, stream)
-                          : launch_attention<false, true>(a, win, tm_q, tm_k16, tm_v16, stream);
+    return a.out_f32 ? launch_attention(kernel, PS::bytes(moves), a, win, tm_q, tm_k16, tm_v16, stream)
+                     : launch_prefill_pair(a, win, tm_q, tm_k16, tm_v16, stream);
 }
 
 }  // namespace pkv

@@ -171,6 +171,15 @@ __device__ __forceinline__ float score_factor(const PrefillArgs &a, int h)
     return f == 0.f ? __uint_as_float(1u) : f;
 }
 
+// Sums over a long context are kept in levels, so that no chain of additions grows
+// with it; the last level lies where the result will, in the row's place in the
+// output.  What the thread that works for a row (or half of one) keeps of it, in
+// shared memory, where it takes no registers from the scores' loop:
+struct MovedRow {
+    uint4 *out;                                            // the place; nullptr: a padding row
+    float m, l;                                            // reference and sum of what has been moved there
+};
+
 // Key tiles of a sequence that some query of its chunk sees, under a window of
 // the 4-bit cache's calls: tiles 0 .. first - 1 (sinks) and then first + skip ..
 // (keys from `from` on).  Without a window: all of them (first = skip = 0).
@@ -190,6 +199,19 @@ __device__ __forceinline__ KeyTiles key_tiles(const Fp4Window &w, int first_pos)
         k.skip = max(k.from / kKeys, k.first) - k.first;
     }
     return k;
+}
+
+// Key tiles that a query tile, or a pair of them, may visit: without a window all of
+// the longest sequence's, with one the sinks' and those that 2 tokens_per_tile +
+// window - 1 keys touch.
+inline int64_t most_key_tiles(const PrefillArgs &a, const Fp4Window &w)
+{
+    const int64_t all = (static_cast<int64_t>(a.max_kv_len) + kKeys - 1) / kKeys;
+    if (w.window == 0)
+        return all;
+    const int64_t seen = (static_cast<int64_t>(w.sinks) + kKeys - 1) / kKeys +
+                         (static_cast<int64_t>(w.window) + 2 * a.tokens_per_tile) / kKeys + 2;
+    return seen < all ? seen : all;
 }
 
 // NaN blocks of the 4-bit cache's V.  A weight of zero times a NaN is a NaN, so

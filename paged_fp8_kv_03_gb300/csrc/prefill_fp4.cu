@@ -70,8 +70,8 @@ struct P2 {
     };
     static constexpr int kTmem = kBars + kNumBars * 8;
     static constexpr int kFlag = kTmem + 4;
-    static constexpr int kRow = (kFlag + 4 + 15) / 16 * 16;   // FoldRow [2][kRows]
-    static constexpr int kEnd = kRow + 2 * kRows * 16;
+    static constexpr int kMoved = (kFlag + 4 + 15) / 16 * 16;   // MovedRow [2][kRows]
+    static constexpr int kEnd = kMoved + 2 * kRows * static_cast<int>(sizeof(MovedRow));
     static constexpr size_t bytes(bool folds) { return static_cast<size_t>(folds ? kEnd : kFlag + 4) + 1024; }
 };
 static_assert(P2::bytes(true) <= 232448, "prefill tile buffers exceed the shared memory of one CTA");
@@ -228,29 +228,26 @@ __device__ __forceinline__ void bf16x8(const uint4 &u, float (&v)[8])
         v[i] = __uint_as_float((i & 1) ? w[i >> 1] & 0xFFFF0000u : w[i >> 1] << 16);
 }
 
-// What a softmax thread of the folding kernel keeps in shared memory for its row:
-// registers are short, and what the scores' loop does not use costs it time.
-struct FoldRow {
-    uint4 *out;                                            // its place in the output; nullptr: padding
-    float m, pad;                                          // its reference at the last fold
-};
-
-__device__ __forceinline__ volatile FoldRow &fold_row()
+// What a softmax thread of the folding kernel keeps in shared memory.
+__device__ __forceinline__ volatile MovedRow &moved_row()
 {
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    return reinterpret_cast<volatile FoldRow *>(smem + P2::kRow)[threadIdx.x - 32 * kWarp0];
+    return reinterpret_cast<volatile MovedRow *>(smem + P2::kMoved)[threadIdx.x - 32 * kWarp0];
 }
 
-// Folds a row's accumulator (m: its reference; old: earlier folds have left
-// something in the output): the bf16 rounding of their sum goes to the output,
-// the rest back into the accumulator.  Out of line, for the loop around it.
-__device__ __noinline__ void fold(uint32_t o_tm, float m, bool old)
+// Adds a row's accumulator and its sum l of the weights (m: their reference) to what
+// earlier folds have left (old): the bf16 rounding of the accumulators' sum goes
+// to the output, the rest back into the accumulator, the last time all of it.
+// Returns the sum of all.  Out of line, for the loop around it.
+__device__ __noinline__ float fold(uint32_t o_tm, float m, float l, bool old, bool last)
 {
-    volatile FoldRow &st = fold_row();
+    volatile MovedRow &st = moved_row();
     uint4 *dst = st.out;
     const float back = old ? ex2_approx(st.m - m) : 0.f;
+    l = old ? st.l * back + l : l;
     st.m = m;
+    st.l = l;
 #pragma unroll 1
     for (int c = 0; c < 8; ++c) {
         uint4 was[2];
@@ -260,29 +257,29 @@ __device__ __noinline__ void fold(uint32_t o_tm, float m, bool old)
         uint32_t o[16];
         tc::ld16(o_tm + 16 * c, o);
         tc::wait_ld();
-        if (dst) {
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                float y[8];
-                bf16x8(was[i], y);
-                uint32_t w[4];
+        for (int i = 0; i < 2; ++i) {
+            float y[8];
+            bf16x8(was[i], y);
+            uint32_t w[4];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    uint32_t &o0 = o[8 * i + 2 * e], &o1 = o[8 * i + 2 * e + 1];
-                    const float s0 = __uint_as_float(o0) + y[2 * e] * back;
-                    const float s1 = __uint_as_float(o1) + y[2 * e + 1] * back;
-                    const __nv_bfloat162 b = __floats2bfloat162_rn(s0, s1);
-                    w[e] = *reinterpret_cast<const uint32_t *>(&b);
-                    o0 = __float_as_uint(s0 - __uint_as_float(w[e] << 16));
-                    o1 = __float_as_uint(s1 - __uint_as_float(w[e] & 0xFFFF0000u));
-                }
-                dst[2 * c + i] = make_uint4(w[0], w[1], w[2], w[3]);
+            for (int e = 0; e < 4; ++e) {
+                uint32_t &o0 = o[8 * i + 2 * e], &o1 = o[8 * i + 2 * e + 1];
+                const float s0 = __uint_as_float(o0) + y[2 * e] * back;
+                const float s1 = __uint_as_float(o1) + y[2 * e + 1] * back;
+                const __nv_bfloat162 b = __floats2bfloat162_rn(s0, s1);
+                w[e] = last ? 0u : *reinterpret_cast<const uint32_t *>(&b);
+                o0 = __float_as_uint(s0 - __uint_as_float(w[e] << 16));
+                o1 = __float_as_uint(s1 - __uint_as_float(w[e] & 0xFFFF0000u));
             }
+            if (dst && !last)
+                dst[2 * c + i] = make_uint4(w[0], w[1], w[2], w[3]);
         }
         __syncwarp();
         tc::st16(o_tm + 16 * c, o);
     }
     tc::wait_st();
+    return l;
 }
 
 // The lift where a row visits nt key tiles: one more from 1025, 2049, .. on.
@@ -490,12 +487,11 @@ __global__ void __launch_bounds__(kThreads2, 1)
         const uint32_t s_tm = tm + (static_cast<uint32_t>(qtr * 32) << 16) + kScoreCol * x;
         const uint32_t o_tm = s_tm + kOutCol;
         float m = -INFINITY, l = 0.f;
-        auto place = [&]() {
+        if (kFolds) {
             const int64_t orow = (static_cast<int64_t>(q0) + t0 + x * tpt + tl) * a.hq + h * G + g;
-            return reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.out) + orow * kHeadDim);
-        };
-        if (kFolds)
-            fold_row().out = valid ? place() : nullptr;
+            moved_row().out =
+                valid ? reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.out) + orow * kHeadDim) : nullptr;
+        }
         bool ok = ntx > 0 && wwait(bar(P2::Q_FULL + x), 0, abort_flag, a.err, lane);
         if (ok) {
             // rows past the G x tpt that the copy fills are zeroed
@@ -514,13 +510,15 @@ __global__ void __launch_bounds__(kThreads2, 1)
                 mbar_arrive(bar(P2::Q_READY + x));
         }
         for (int j = 0; ok && j < ntx; ++j) {
+            // (S_{j-1} came behind PV_{j-2}: so PV_DONE's phase is that of PV_{j-1})
             if (kFolds && j > 0 && j % kFold2 == 0) {
                 if (!wwait(bar(P2::PV_DONE + x), (j - 1) & 1, abort_flag, a.err, lane)) {
                     ok = false;
                     break;
                 }
                 tc::fence_after();
-                fold(o_tm, m, j > kFold2);
+                fold(o_tm, m, l, j > kFold2, false);
+                l = 0.f;
             }
             if (!wwait(bar(P2::S_FULL + x), j & 1, abort_flag, a.err, lane)) {
                 ok = false;
@@ -622,29 +620,23 @@ __global__ void __launch_bounds__(kThreads2, 1)
         }
         if (ok && wwait(bar(P2::PV_DONE + x), (ntx - 1) & 1, abort_flag, a.err, lane)) {
             tc::fence_after();
+            if (kFolds && ntx > kFold2)
+                l = fold(o_tm, m, l, true, true);
             const float inv = __ldg(a.v_scale + h) / l;
             const uint32_t nans = nan_blocks<kWin>(a, win, row0 / kKeys, ntx, p_row, lane, key_tile, copy_tile);
-            uint4 *dst = kFolds ? fold_row().out : place();
-            const bool folded = kFolds && ntx > kFold2;
-            const float back = folded ? ex2_approx(fold_row().m - m) : 0.f;
+            const int64_t orow = (static_cast<int64_t>(q0) + t0 + x * tpt + tl) * a.hq + h * G + g;
+            uint4 *dst = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.out) + orow * kHeadDim);
 #pragma unroll 1
             for (int c = 0; c < 4; ++c) {
                 uint32_t o[32];
                 tc::ld32(o_tm + 32 * c, o);
                 tc::wait_ld();
-                if (kFolds ? dst == nullptr : !valid)
+                if (!valid)
                     continue;
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
                     uint32_t w[4];
                     const float f = (nans >> (2 * c + (k >> 1))) & 1u ? NAN : inv;
-                    if (folded) {
-                        float y[8];
-                        bf16x8(dst[4 * c + k], y);
-#pragma unroll
-                        for (int e = 0; e < 8; ++e)
-                            o[8 * k + e] = __float_as_uint(__uint_as_float(o[8 * k + e]) + y[e] * back);
-                    }
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
                         const __nv_bfloat162 b2 = __floats2bfloat162_rn(__uint_as_float(o[8 * k + 2 * e]) * f,
@@ -686,18 +678,10 @@ cudaError_t launch_widen_fp4(const PrefillArgs &a, const Fp4Window &win, cudaStr
 cudaError_t launch_prefill_pair(const PrefillArgs &a, const Fp4Window &win, const CUtensorMap &tm_q,
                                 const CUtensorMap &tm_k16, const CUtensorMap &tm_v16, cudaStream_t stream)
 {
-    // Key tiles that a pair of query tiles may visit: without a window all of the longest
-    // sequence's, with one the sinks' and those that 2 tokens_per_tile + window - 1 keys touch.
-    int64_t tiles = (static_cast<int64_t>(a.max_kv_len) + kKeys - 1) / kKeys;
-    if (win.window > 0) {
-        const int64_t seen = (static_cast<int64_t>(win.sinks) + kKeys - 1) / kKeys +
-                             (static_cast<int64_t>(win.window) + 2 * a.tokens_per_tile) / kKeys + 2;
-        tiles = seen < tiles ? seen : tiles;
-    }
     // The folding kernel takes longer even where it folds nothing (4096 of 16384 tokens, 64
-    // query heads: 1172 us instead of 1153), and where it does (2048 of 131072: 5.91 ms, in
-    // one chain 5.70; 1024 of 524288: 12.2 and 11.7).
-    const bool folds = tiles > kFold2;
+    // query heads: 1172 us instead of 1153), and where it does (2048 of 131072: 6.01 ms, in
+    // one chain 5.74; 1024 of 524288: 12.4 and 11.8).
+    const bool folds = most_key_tiles(a, win) > kFold2;
     const int which = (win.window > 0 ? 1 : 0) + (folds ? 2 : 0);
     const auto kernel = win.window > 0 ? (folds ? paged_prefill_pair_kernel<true, true> : paged_prefill_pair_kernel<true, false>)
                                        : (folds ? paged_prefill_pair_kernel<false, true> : paged_prefill_pair_kernel<false, false>);
