@@ -91,11 +91,13 @@ def test_prefill_over_several_chains_in_place(pkv, cuda_device):
 
 
 @pytest.mark.parametrize("lens,ns", [([20000], [300]), ([33000, 500], [200, 3])])
-def test_prefill_nan_rows_over_several_chains(pkv, cuda_device, lens, ns):
-    _nan_rows(pkv, cuda_device, torch.bfloat16, lens, ns)
+@pytest.mark.parametrize("out_dtype", [torch.bfloat16, torch.float32])
+def test_prefill_nan_rows_over_several_chains(pkv, cuda_device, lens, ns, out_dtype):
+    _nan_rows(pkv, cuda_device, out_dtype, lens, ns)
 
 
-def test_prefill_bound_of_a_long_context(pkv, cuda_device):
+@pytest.mark.parametrize("out_dtype", [torch.bfloat16, torch.float32])
+def test_prefill_bound_of_a_long_context(pkv, cuda_device, out_dtype):
     """The kernel of long contexts on short ones: the bits of the other one."""
     lens, ns = [400, 1, 300], [40, 1, 170]
     c = Cache(58, lens, 1, 16, cuda_device)
@@ -105,7 +107,7 @@ def test_prefill_bound_of_a_long_context(pkv, cuda_device):
     def call(bound, window):
         e = torch.zeros(1, dtype=torch.int32, device=cuda_device)
         out = pkv.paged_prefill_fp4(qd, cu, c.kc, c.vc, c.ksd, c.vsd, c.tabled, c.lensd, 170, max_kv_len=bound,
-                                    device_error=e, window=window, sinks=2)
+                                    out_dtype=out_dtype, device_error=e, window=window, sinks=2)
         return out, e
 
     for window in (0, 39000):
@@ -116,15 +118,16 @@ def test_prefill_bound_of_a_long_context(pkv, cuda_device):
         assert torch.equal(got, ref)
 
 
+@pytest.mark.parametrize("out_dtype", [torch.bfloat16, torch.float32])
 @pytest.mark.parametrize("window", [0, 39000])
-def test_prefill_of_a_long_context_times_out_and_recovers(pkv, cuda_device, window):
+def test_prefill_of_a_long_context_times_out_and_recovers(pkv, cuda_device, window, out_dtype):
     c = Cache(59, [20000], 1, 64, cuda_device)
     _, qd = c.queries(40, 8)
     cu = torch.tensor([0, 40], dtype=torch.int32, device=cuda_device)
 
     def call(e):
         return pkv.paged_prefill_fp4(qd, cu, c.kc, c.vc, c.ksd, c.vsd, c.tabled, c.lensd, 40, max_kv_len=40000,
-                                     device_error=e, window=window, sinks=2)
+                                     out_dtype=out_dtype, device_error=e, window=window, sinks=2)
 
     def withheld():
         e = torch.zeros(1, dtype=torch.int32, device=cuda_device)
