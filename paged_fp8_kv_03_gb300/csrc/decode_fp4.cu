@@ -1147,16 +1147,15 @@ __global__ void __launch_bounds__(32 * kClusterWarps, 2) paged_gqa_decode_fp4_cl
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1)
             M = fmaxf(M, __shfl_xor_sync(kEvery, M, o));
-        const float e = m == -INFINITY ? 0.f : ex2_approx(m - M);
+        // (not 0 where there is a state: a NaN of V in it is seen whatever its weight)
+        const float e = m == -INFINITY ? 0.f : fmaxf(ex2_approx(m - M), 0x1p-126f);
         float sum = e * l;
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1)
             sum += __shfl_xor_sync(kEvery, sum, o);
         const float f = units == 0 ? 0.f : v_scale / sum;
         const int64_t row = static_cast<int64_t>(b) * a.hq + static_cast<int64_t>(h) * a.group + g;
-        // (what a warp without units left is read, but not used; a state of no weight
-        // is: a NaN of V in it is seen)
-        const uint32_t real = __ballot_sync(kEvery, l != 0.f);
+        // (what a warp without units left is read, but not used)
         if (one) {
             float4 A = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
@@ -1164,11 +1163,10 @@ __global__ void __launch_bounds__(32 * kClusterWarps, 2) paged_gqa_decode_fp4_cl
                 const float ei = __shfl_sync(kEvery, e, i);
                 const float4 v =
                     *reinterpret_cast<const float4 *>(smem + i * S::kWarp + (g * kPartialStride + 4 * lane) * 4);
-                const bool on = (real >> i) & 1u;
-                A.x += on ? ei * v.x : 0.f;
-                A.y += on ? ei * v.y : 0.f;
-                A.z += on ? ei * v.z : 0.f;
-                A.w += on ? ei * v.w : 0.f;
+                A.x += ei != 0.f ? ei * v.x : 0.f;
+                A.y += ei != 0.f ? ei * v.y : 0.f;
+                A.z += ei != 0.f ? ei * v.z : 0.f;
+                A.w += ei != 0.f ? ei * v.w : 0.f;
             }
             store4(a, row, 4 * lane, make_float4(A.x * f, A.y * f, A.z * f, A.w * f));
         } else {
@@ -1181,7 +1179,7 @@ __global__ void __launch_bounds__(32 * kClusterWarps, 2) paged_gqa_decode_fp4_cl
 #pragma unroll
             for (int i = 0; i < 32; ++i) {
                 const float ei = __shfl_sync(kEvery, e, i);
-                A += (real >> i) & 1u ? ei * v[i] : 0.f;
+                A += ei != 0.f ? ei * v[i] : 0.f;
             }
             if (a.out_f32)
                 static_cast<float *>(a.out)[row * kHeadDim + d] = A * f;
