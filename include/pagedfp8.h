@@ -52,6 +52,9 @@
  *   PKV_DEVERR_INTERNAL  the decode's own split-K bookkeeping pointed outside
  *                        the workspace (the access was skipped; outputs are
  *                        not valid; not expected to happen)
+ *   PKV_DEVERR_POOL      the page pool has fewer free pages than a plan needs,
+ *                        its free count cannot be, or a release would overfill
+ *                        it (nothing was planned, or released)
  * The word is sticky: clear it (pkv_read_device_error with clear = 1, or
  * cudaMemsetAsync) before a call whose errors you want to attribute.
  */
@@ -90,7 +93,8 @@ enum {
     PKV_DEVERR_SEQLEN = 4,
     PKV_DEVERR_TIMEOUT = 8,
     PKV_DEVERR_PAGESIZE = 16,
-    PKV_DEVERR_INTERNAL = 32
+    PKV_DEVERR_INTERNAL = 32,
+    PKV_DEVERR_POOL = 64
 };
 
 /* Build limits. */
@@ -593,6 +597,191 @@ pkv_status pkv_paged_prefill_fp4(const void *q, const int32_t *cu_q, int total_q
                                  void *out, int out_dtype,
                                  void *workspace, size_t workspace_bytes,
                                  int32_t *device_error, cudaStream_t stream);
+
+/*
+ * The block-scaled FP8 cache -- a third cache format: 8 bits a value and no scale
+ * to calibrate.  16 consecutive tokens of a kv head are a block.  It holds 16 rows
+ * of 128 E4M3 codes and one byte x, and a value is
+ *     code * 2^(x - 127).
+ * A power of two costs E4M3 no precision, and a block can be given a larger one
+ * later at the cost of its smallest values only.
+ *
+ *   k_cache, v_cache : uint8 [num_pages][num_kv_heads][page_size][head_dim], the
+ *                      FP8 cache's pools.
+ *   k_exp, v_exp     : uint8 [num_pages][num_kv_heads][page_size / 16], x of each
+ *                      block.  Appended blocks have x in [10, 246] (2^-117 ..
+ *                      2^119); blocks with other bytes read as the formula says, as
+ *                      far as the results' types go, but for x = 255, which is
+ *                      no scale (values of such a block are undefined).
+ * Slots, block tables, per-sequence page sizes, ownership and device errors are
+ * those of the FP8 cache; window and sinks, and which pages are not looked at,
+ * those of the 4-bit cache.  A NaN code reaches only the outputs that see it: one
+ * of K the whole row, one of V its own dim.
+ */
+
+/*
+ * kv_append_fp8b -- quantise new K and V tokens into the blocks of their slots.
+ * For a block that gets rows in this call, per kv head and for K and V each, with
+ * amax the largest finite |x| of these rows:
+ *     e = the smallest integer with amax <= 448 * 2^e, within [-117, 119]
+ * If the call writes the block's row 0, it begins the block: x = e + 127, and what
+ * its other rows held means nothing any more.  Else x = max(old x, e + 127), and where
+ * that is larger than the old x, the rows not written in this call are rounded to it:
+ * code = E4M3(code * 2^(old x - x)).  Rows of the call: code = E4M3(value * 2^(127 - x)).
+ * E4M3 rounds to nearest, ties to even, and saturates (+-Inf reads back as +-448 *
+ * 2^(x - 127), NaN as NaN).
+ *
+ *   slot_mapping   device int64 [num_tokens]; negative = do not write.  The tokens
+ *                  of one block have to lie within 32 consecutive ones of the call,
+ *                  in any order (those of a sequence, back to back, do); what a block
+ *                  holds whose tokens lie further apart is undefined, and two tokens
+ *                  with the same slot race.
+ *   k_new, v_new, in_dtype, page_size, device_error: as pkv_kv_append_fp8; the pools
+ *                  as above.
+ * num_tokens == 0 is a no-op.
+ */
+pkv_status pkv_kv_append_fp8b(const void *k_new, const void *v_new, int in_dtype,
+                              int64_t num_tokens, int num_kv_heads, int head_dim,
+                              const int64_t *slot_mapping,
+                              uint8_t *k_cache, uint8_t *v_cache, uint8_t *k_exp, uint8_t *v_exp,
+                              int64_t num_pages, int page_size,
+                              int32_t *device_error, cudaStream_t stream);
+
+/*
+ * kv_read_fp8b -- read rows back: for every token t with slot = slot_mapping[t] >=
+ * 0 the values of the row at that slot, exact in either output type (values beyond
+ * 3.4e38 become Inf).  Rows of negative slots are left as they were; a slot outside
+ * the pool sets PKV_DEVERR_SLOT and reads as zeros.  A slot may occur more than once.
+ * Outputs as pkv_kv_read_fp4.
+ */
+pkv_status pkv_kv_read_fp8b(const int64_t *slot_mapping, int64_t num_tokens,
+                            int num_kv_heads, int head_dim,
+                            const uint8_t *k_cache, const uint8_t *v_cache,
+                            const uint8_t *k_exp, const uint8_t *v_exp,
+                            int64_t num_pages, int page_size,
+                            void *k_out, void *v_out, int out_dtype,
+                            int32_t *device_error, cudaStream_t stream);
+
+/*
+ * paged_gqa_decode_fp8b -- pkv_paged_gqa_decode_fp4 over the block-scaled cache: the
+ * same window and sinks, queries, clamping, zero rows, determinism, errors and
+ * launches.
+ *
+ *   workspace      device, >= pkv_decode_fp8b_workspace_size(...) bytes for the same
+ *                  sizes, 256-byte aligned; needs no initialisation, not to be shared
+ *                  by calls that overlap on the GPU.
+ * num_pages * num_kv_heads * page_size / 16 must be below 2^31, and so must
+ * num_kv_heads times the sum over the batch of the 32-token units that max_seq_len, or
+ * the window and the sinks, allow a sequence (plus one each).
+ */
+size_t pkv_decode_fp8b_workspace_size(int batch, int num_q_heads, int num_kv_heads,
+                                      int head_dim, int max_seq_len, int page_size, int max_ctas);
+
+pkv_status pkv_paged_gqa_decode_fp8b(const void *q,
+                                     const uint8_t *k_cache, const uint8_t *v_cache,
+                                     const uint8_t *k_exp, const uint8_t *v_exp,
+                                     const int32_t *block_table, int max_pages_per_seq,
+                                     const int32_t *seq_lens, int max_seq_len,
+                                     const int32_t *seq_page_sizes,
+                                     int batch, int num_q_heads, int num_kv_heads, int head_dim,
+                                     int page_size, int64_t num_pages, float sm_scale,
+                                     int window, int sinks,
+                                     void *out, int out_dtype,
+                                     void *workspace, size_t workspace_bytes,
+                                     int32_t *device_error, int max_ctas, cudaStream_t stream);
+
+/*
+ * paged_prefill_fp8b -- pkv_paged_prefill_fp4 over the block-scaled cache: the same
+ * window and sinks, arguments, errors, untouched rows and determinism.  V is widened
+ * in units of its own: of a sequence's kv head, blocks whose scale is less than 2^-21
+ * of the largest one that the chunk sees are rounded to 2^-40 of that block's largest
+ * value.  Three launches.  num_kv_heads is at most 8192.
+ *
+ *   workspace      device, >= pkv_prefill_fp8b_workspace_size(...) bytes for the same
+ *                  bounds, 256-byte aligned.
+ */
+size_t pkv_prefill_fp8b_workspace_size(int batch, int num_kv_heads, int max_q_len, int max_kv_len,
+                                       int64_t max_total_kv, int window, int sinks);
+
+pkv_status pkv_paged_prefill_fp8b(const void *q, const int32_t *cu_q, int total_q, int max_q_len,
+                                  const uint8_t *k_cache, const uint8_t *v_cache,
+                                  const uint8_t *k_exp, const uint8_t *v_exp,
+                                  const int32_t *block_table, int max_pages_per_seq,
+                                  const int32_t *seq_lens, const int32_t *seq_page_sizes,
+                                  int batch, int max_kv_len, int64_t max_total_kv,
+                                  int num_q_heads, int num_kv_heads, int head_dim,
+                                  int page_size, int64_t num_pages, float sm_scale,
+                                  int window, int sinks,
+                                  void *out, int out_dtype,
+                                  void *workspace, size_t workspace_bytes,
+                                  int32_t *device_error, cudaStream_t stream);
+
+/*
+ * The page pool and the page plan -- what the calls above take as block tables,
+ * slots, row offsets and lengths, built on the GPU from the requests' lengths, so that
+ * a step needs no host synchronisation and a captured graph of it stays valid while
+ * the lengths change.
+ *
+ *   page_pool      device int32 [PKV_PAGE_POOL_HEADER + num_pages]: word 0 the number F
+ *                  of free pages, word 1 the library's (0 between calls), words 2 and 3
+ *                  not used, then the list whose first F entries are the free pages.
+ *                  The caller fills it once (pages that it keeps for itself are not in
+ *                  the list) and may do so again between calls.  Calls on one pool must
+ *                  not overlap on the GPU.
+ */
+#define PKV_PAGE_POOL_HEADER 4
+
+/*
+ * plan_pages -- sequence b holds past_lens[b] tokens in the first ceil(past_lens[b] /
+ * P) entries of its block-table row and brings new_lens[b] more.  It gets the pages
+ * that it lacks: page by page and sequence after sequence the last entry of the free
+ * list, which goes into its block-table row.  Then, with n = the sum of new_lens:
+ *     seq_lens[b]     = past_lens[b] + new_lens[b]
+ *     cu_q[b]         = new_lens[0] + .. + new_lens[b - 1]   (b <= batch)
+ *     positions[cu_q[b] + j]    = past_lens[b] + j
+ *     slot_mapping[cu_q[b] + j] = page of that position * P + its row
+ * and rows n .. max_tokens - 1 get slot -1 and position 0.  Table entries behind a
+ * sequence's last page are left as they were.
+ *
+ * All or nothing: if a length is negative or beyond the table's row, or n is above
+ * max_tokens (PKV_DEVERR_SEQLEN), or the list is too short (PKV_DEVERR_POOL), no page
+ * moves, no table entry is written, seq_lens = past_lens, cu_q = 0 and all slots are -1.
+ * A page outside the pool, in the list or in the table, sets PKV_DEVERR_PAGE; tokens in
+ * it get slot -1.
+ *
+ *   past_lens, new_lens  device int32 [batch].
+ *   block_table    device int32 [batch][max_pages_per_seq], updated in place.
+ *   page_size      P = 16, 32, 64, 128 or 256 (every sequence's).
+ *   seq_lens       device int32 [batch]; may be past_lens itself.
+ *   cu_q           device int32 [batch + 1].
+ *   slot_mapping   device int64 [max_tokens].
+ *   positions      device int32 [max_tokens] or NULL.
+ * batch is at most PKV_MAX_BATCH.  One launch.
+ */
+pkv_status pkv_plan_pages(const int32_t *past_lens, const int32_t *new_lens, int batch,
+                          int32_t *block_table, int max_pages_per_seq, int page_size,
+                          int32_t *page_pool, int64_t num_pages,
+                          int32_t *seq_lens, int32_t *cu_q, int64_t *slot_mapping,
+                          int32_t *positions, int max_tokens,
+                          int32_t *device_error, cudaStream_t stream);
+
+/*
+ * release_pages -- the pages behind keep_lens[b] tokens (NULL: all) of a sequence of
+ * seq_lens[b] go back to the pool: entries ceil(keep_lens[b] / P) .. ceil(seq_lens[b] /
+ * P) - 1 of its row, which is left as it was.  The last one of the last sequence
+ * becomes the list's next entry, the first one of the first its last, so that
+ * releasing what one plan took restores the list.  A page that sequences share must not
+ * be released while another holds it.
+ *
+ * All or nothing: lengths that are negative, beyond the row, or smaller than what is
+ * kept set PKV_DEVERR_SEQLEN, more pages than the pool has PKV_DEVERR_POOL.  An entry
+ * outside the pool sets PKV_DEVERR_PAGE and goes into the list as it is.
+ * One launch.
+ */
+pkv_status pkv_release_pages(const int32_t *seq_lens, const int32_t *keep_lens, int batch,
+                             const int32_t *block_table, int max_pages_per_seq, int page_size,
+                             int32_t *page_pool, int64_t num_pages,
+                             int32_t *device_error, cudaStream_t stream);
 
 /*
  * read_device_error -- read (and optionally clear) a device error word after

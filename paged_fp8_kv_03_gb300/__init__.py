@@ -14,6 +14,10 @@ stream.  The entry points mirror the C ABI in ``include/pagedfp8.h``:
 * ``pkv_kv_append_fp4``, ``pkv_kv_read_fp4``, ``pkv_paged_gqa_decode_fp4``,
   ``pkv_paged_prefill_fp4`` -- the 4-bit cache: writing it, reading it back,
   and decode and prefill attention over it with an optional sliding window
+* ``pkv_kv_append_fp8b``, ``pkv_kv_read_fp8b``, ``pkv_paged_gqa_decode_fp8b``,
+  ``pkv_paged_prefill_fp8b`` -- the same calls for the block-scaled FP8 cache
+* ``pkv_plan_pages``, ``pkv_release_pages`` -- a step's pages, block tables,
+  slots and positions from its requests' lengths, on the GPU
 
 ``kv_append_fp8`` / ``paged_gqa_decode`` are the same calls with the output
 and workspace allocated by torch when not given.  There is no CPU fallback:
@@ -33,10 +37,13 @@ from . import build as _build
 
 PKV_F32, PKV_BF16 = 0, 1
 DEVERR_SLOT, DEVERR_PAGE, DEVERR_SEQLEN, DEVERR_TIMEOUT, DEVERR_PAGESIZE, DEVERR_INTERNAL = 1, 2, 4, 8, 16, 32
+DEVERR_POOL = 64
 HEAD_DIM = 128
 MAX_GROUP = 8
 MAX_BATCH = 8192
 FP4_ROW_BYTES = 72
+FP8B_BLOCK = 16
+PAGE_POOL_HEADER = 4
 _INT32_MAX = 2 ** 31 - 1
 
 _lib = None
@@ -105,6 +112,22 @@ def load() -> ctypes.CDLL:
         lib.pkv_paged_prefill_fp4.restype = i32
         lib.pkv_paged_prefill_fp4.argtypes = [vp, vp, i32, i32, vp, vp, vp, vp, vp, i32, vp, vp, i32, i32, i64, i32,
                                               i32, i32, i32, i64, f32, i32, i32, vp, i32, vp, sz, vp, vp]
+        lib.pkv_kv_append_fp8b.restype = i32
+        lib.pkv_kv_append_fp8b.argtypes = [vp, vp, i32, i64, i32, i32, vp, vp, vp, vp, vp, i64, i32, vp, vp]
+        lib.pkv_kv_read_fp8b.restype = i32
+        lib.pkv_kv_read_fp8b.argtypes = [vp, i64, i32, i32, vp, vp, vp, vp, i64, i32, vp, vp, i32, vp, vp]
+        lib.pkv_decode_fp8b_workspace_size.restype = sz
+        lib.pkv_decode_fp8b_workspace_size.argtypes = lib.pkv_decode_fp4_workspace_size.argtypes
+        lib.pkv_paged_gqa_decode_fp8b.restype = i32
+        lib.pkv_paged_gqa_decode_fp8b.argtypes = lib.pkv_paged_gqa_decode_fp4.argtypes
+        lib.pkv_prefill_fp8b_workspace_size.restype = sz
+        lib.pkv_prefill_fp8b_workspace_size.argtypes = lib.pkv_prefill_fp4_workspace_size.argtypes
+        lib.pkv_paged_prefill_fp8b.restype = i32
+        lib.pkv_paged_prefill_fp8b.argtypes = lib.pkv_paged_prefill_fp4.argtypes
+        lib.pkv_plan_pages.restype = i32
+        lib.pkv_plan_pages.argtypes = [vp, vp, i32, vp, i32, i32, vp, i64, vp, vp, vp, vp, i32, vp, vp]
+        lib.pkv_release_pages.restype = i32
+        lib.pkv_release_pages.argtypes = [vp, vp, i32, vp, i32, i32, vp, i64, vp, vp]
         lib.pkv_read_device_error.restype = i32
         lib.pkv_read_device_error.argtypes = [vp, i32, ctypes.POINTER(ctypes.c_int32), vp]
         lib.pkv_decode_set_split_weights.restype = i32
@@ -890,6 +913,296 @@ def paged_prefill_fp4(q, cu_q, k_cache, v_cache, k_scale, v_scale, block_table, 
     return out
 
 
+# ---------------------------------------------------------------------------
+# the block-scaled FP8 cache
+# ---------------------------------------------------------------------------
+def fp8b_cache(num_pages, num_kv_heads, page_size, device=None) -> tuple:
+    """One zeroed block-scaled pool (K or V): codes uint8 [num_pages, Hkv, P, 128]
+    and exponent bytes uint8 [num_pages, Hkv, P / 16]."""
+    device = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
+    return (torch.zeros((num_pages, num_kv_heads, page_size, HEAD_DIM), dtype=torch.uint8, device=device),
+            torch.zeros((num_pages, num_kv_heads, page_size // FP8B_BLOCK), dtype=torch.uint8, device=device))
+
+
+def _fp8b_pools(k_cache, v_cache, k_exp, v_exp, dev):
+    """Addresses, pages, kv heads and page size of the pools."""
+    k, v = _addr(k_cache, "k_cache", torch.uint8, 4, dev), _addr(v_cache, "v_cache", torch.uint8, 4, dev)
+    ke, ve = _addr(k_exp, "k_exp", torch.uint8, 3, dev), _addr(v_exp, "v_exp", torch.uint8, 3, dev)
+    shape = k_cache.shape
+    if v_cache.shape != shape or shape[3] != HEAD_DIM:
+        raise ValueError(f"caches must be uint8 [num_pages, Hkv, P, {HEAD_DIM}], both alike")
+    if k_exp.shape != v_exp.shape or tuple(k_exp.shape) != (shape[0], shape[1], shape[2] // FP8B_BLOCK):
+        raise ValueError(f"k_exp and v_exp must be uint8 [num_pages, Hkv, P / {FP8B_BLOCK}]")
+    return k, v, ke, ve, shape[0], shape[1], shape[2]
+
+
+def _fp8b_rows(slot_mapping, k, v, H, dev):
+    """What append and read back share: the slots' address, tokens and head_dim."""
+    slots = _addr(slot_mapping, "slot_mapping", torch.int64, 1, dev)
+    if v.shape != k.shape or k.shape[1] != H:
+        raise ValueError("k/v shapes disagree")
+    if slot_mapping.shape[0] != k.shape[0]:
+        raise ValueError("slot_mapping must have one entry per token")
+    return slots, k.shape[0], k.shape[2]
+
+
+def pkv_kv_append_fp8b(k_new, v_new, slot_mapping, k_cache, v_cache, k_exp, v_exp, device_error=None,
+                       stream=None) -> None:
+    """k_new/v_new [T, Hkv, 128] fp32|bf16; slot_mapping int64 [T] (negative: not
+    written; a block's tokens within 32 consecutive ones); caches uint8
+    [num_pages, Hkv, P, 128] and k_exp/v_exp uint8 [num_pages, Hkv, P / 16]
+    (written in place)."""
+    dev = _cuda_index(k_new, "k_new")
+    k, v = _addr(k_new, "k_new", k_new.dtype, 3, dev), _addr(v_new, "v_new", k_new.dtype, 3, dev)
+    kc, vc, ke, ve, NP, H, P = _fp8b_pools(k_cache, v_cache, k_exp, v_exp, dev)
+    slots, T, D = _fp8b_rows(slot_mapping, k_new, v_new, H, dev)
+    _call("pkv_kv_append_fp8b", dev, stream, (_lib or load()).pkv_kv_append_fp8b, k, v, _act(k_new, "k_new"), T, H, D,
+          slots, kc, vc, ke, ve, NP, P, _error_word(device_error, dev))
+
+
+def kv_append_fp8b(k_new, v_new, slot_mapping, k_cache, v_cache, k_exp, v_exp, device_error=None,
+                   stream=None) -> None:
+    pkv_kv_append_fp8b(k_new, v_new, slot_mapping, k_cache, v_cache, k_exp, v_exp, device_error, stream)
+
+
+def pkv_kv_read_fp8b(slot_mapping, k_cache, v_cache, k_exp, v_exp, k_out, v_out, device_error=None,
+                     stream=None) -> None:
+    """The rows at slot_mapping (int64 [T]) as values, into k_out/v_out
+    [T, Hkv, 128] fp32|bf16; rows of negative slots are left as they were."""
+    dev = _cuda_index(k_out, "k_out")
+    k, v = _addr(k_out, "k_out", k_out.dtype, 3, dev), _addr(v_out, "v_out", k_out.dtype, 3, dev)
+    kc, vc, ke, ve, NP, H, P = _fp8b_pools(k_cache, v_cache, k_exp, v_exp, dev)
+    slots, T, D = _fp8b_rows(slot_mapping, k_out, v_out, H, dev)
+    _call("pkv_kv_read_fp8b", dev, stream, (_lib or load()).pkv_kv_read_fp8b, slots, T, H, D, kc, vc, ke, ve, NP, P, k,
+          v, _act(k_out, "k_out"), _error_word(device_error, dev))
+
+
+def kv_read_fp8b(slot_mapping, k_cache, v_cache, k_exp, v_exp, k_out=None, v_out=None, out_dtype=torch.bfloat16,
+                 device_error=None, stream=None) -> tuple:
+    """Allocating form of pkv_kv_read_fp8b: (K, V) [T, Hkv, 128]; without
+    outputs given, rows of negative slots are zeros."""
+    if (k_out is None) != (v_out is None):
+        raise ValueError("give both outputs or neither")
+    if k_out is None:
+        shape = (slot_mapping.shape[0], k_cache.shape[1], HEAD_DIM)
+        with _on(stream, slot_mapping.device):
+            k_out = torch.zeros(shape, dtype=out_dtype, device=slot_mapping.device)
+            v_out = torch.zeros_like(k_out)
+    pkv_kv_read_fp8b(slot_mapping, k_cache, v_cache, k_exp, v_exp, k_out, v_out, device_error, stream)
+    return k_out, v_out
+
+
+def _fp8b_attention(q, out, block_table, seq_lens, seq_page_sizes, workspace, dev):
+    """What decode and prefill share: the tensors' addresses."""
+    addrs = (_addr(q, "q", torch.bfloat16, 3, dev), _addr(out, "out", getattr(out, "dtype", None), 3, dev),
+             _act(out, "out"), _addr(block_table, "block_table", torch.int32, 2, dev),
+             _addr(seq_lens, "seq_lens", torch.int32, 1, dev),
+             None if seq_page_sizes is None else _addr(seq_page_sizes, "seq_page_sizes", torch.int32, 1, dev),
+             _addr(workspace, "workspace", torch.uint8, None, dev))
+    if out.shape != q.shape:
+        raise ValueError("q / out shapes disagree")
+    B = seq_lens.shape[0]
+    if block_table.shape[0] != B or (seq_page_sizes is not None and seq_page_sizes.shape[0] != B):
+        raise ValueError("block_table, seq_lens and seq_page_sizes must have one entry per sequence")
+    return addrs
+
+
+def pkv_decode_fp8b_workspace_size(batch, num_q_heads, num_kv_heads, head_dim=HEAD_DIM, max_seq_len=0, page_size=16,
+                                   max_ctas=0) -> int:
+    """Workspace bytes of a block-scaled decode call of these sizes."""
+    return int(load().pkv_decode_fp8b_workspace_size(int(batch), int(num_q_heads), int(num_kv_heads), int(head_dim),
+                                                     _int32(max_seq_len, "max_seq_len"), int(page_size),
+                                                     _int32(max_ctas, "max_ctas")))
+
+
+def pkv_paged_gqa_decode_fp8b(q, k_cache, v_cache, k_exp, v_exp, block_table, seq_lens, out, workspace,
+                              sm_scale=None, device_error=None, max_ctas=0, stream=None, max_seq_len=0,
+                              seq_page_sizes=None, window=0, sinks=0) -> None:
+    """pkv_paged_gqa_decode over block-scaled caches (see pkv_kv_append_fp8b);
+    window > 0: only the last `window` tokens and the first `sinks` are
+    attended.  workspace uint8 (pkv_decode_fp8b_workspace_size bytes)."""
+    dev = _cuda_index(q, "q")
+    kc, vc, ke, ve, NP, Hkv, P = _fp8b_pools(k_cache, v_cache, k_exp, v_exp, dev)
+    qa, oa, odt, bt, lens, psz, ws = _fp8b_attention(q, out, block_table, seq_lens, seq_page_sizes, workspace, dev)
+    B, Hq, D = q.shape
+    if seq_lens.shape[0] != B:
+        raise ValueError("seq_lens must have one entry per row of q")
+    window, sinks = _check_window(window, sinks)
+    _call("pkv_paged_gqa_decode_fp8b", dev, stream, (_lib or load()).pkv_paged_gqa_decode_fp8b, qa, kc, vc, ke, ve, bt,
+          block_table.shape[1], lens, _int32(max_seq_len, "max_seq_len"), psz, B, Hq, Hkv, D, P, NP,
+          1.0 / math.sqrt(D) if sm_scale is None else float(sm_scale), window, sinks, oa, odt, ws, workspace.numel(),
+          _error_word(device_error, dev), _int32(max_ctas, "max_ctas"))
+
+
+def paged_gqa_decode_fp8b(q, k_cache, v_cache, k_exp, v_exp, block_table, seq_lens, out=None,
+                          out_dtype=torch.bfloat16, workspace=None, sm_scale=None, device_error=None, max_ctas=0,
+                          stream=None, max_seq_len=0, seq_page_sizes=None, window=0, sinks=0) -> torch.Tensor:
+    """Allocating form of pkv_paged_gqa_decode_fp8b (on the stream it runs on)."""
+    if out is None:
+        with _on(stream, q.device):
+            out = torch.empty(q.shape, dtype=out_dtype, device=q.device)
+    max_seq_len = _default_max_len(block_table, k_cache, max_seq_len, seq_page_sizes)
+    if workspace is None:
+        _cuda_index(q, "q")
+        with _device_of(q):
+            n = pkv_decode_fp8b_workspace_size(q.shape[0], q.shape[1], k_cache.shape[1], q.shape[2], max_seq_len,
+                                               k_cache.shape[2], max_ctas)
+        if n == 0:
+            raise PkvError(4, "pkv_decode_fp8b_workspace_size")
+        with _on(stream, q.device):
+            workspace = torch.empty(n, dtype=torch.uint8, device=q.device)
+    pkv_paged_gqa_decode_fp8b(q, k_cache, v_cache, k_exp, v_exp, block_table, seq_lens, out, workspace, sm_scale,
+                              device_error, max_ctas, stream, max_seq_len, seq_page_sizes, window, sinks)
+    return out
+
+
+def pkv_prefill_fp8b_workspace_size(batch, num_kv_heads, max_q_len, max_kv_len, max_total_kv=0, window=0,
+                                    sinks=0) -> int:
+    window, sinks = (max(-1, min(int(x), _INT32_MAX)) for x in (window, sinks))
+    return int(load().pkv_prefill_fp8b_workspace_size(int(batch), int(num_kv_heads), _int32(max_q_len, "max_q_len"),
+                                                      _int32(max_kv_len, "max_kv_len"), int(max_total_kv), window,
+                                                      sinks))
+
+
+def pkv_paged_prefill_fp8b(q, cu_q, k_cache, v_cache, k_exp, v_exp, block_table, seq_lens, out, max_q_len,
+                           max_kv_len, workspace, sm_scale=None, device_error=None, stream=None, max_total_kv=0,
+                           seq_page_sizes=None, window=0, sinks=0) -> None:
+    """pkv_paged_prefill over block-scaled caches (see pkv_kv_append_fp8b);
+    window > 0: a query sees itself, the window - 1 tokens before it and the
+    first `sinks` tokens.  workspace uint8 (pkv_prefill_fp8b_workspace_size
+    bytes for the same bounds)."""
+    dev = _cuda_index(q, "q")
+    kc, vc, ke, ve, NP, Hkv, P = _fp8b_pools(k_cache, v_cache, k_exp, v_exp, dev)
+    qa, oa, odt, bt, lens, psz, ws = _fp8b_attention(q, out, block_table, seq_lens, seq_page_sizes, workspace, dev)
+    cu = _addr(cu_q, "cu_q", torch.int32, 1, dev)
+    T, Hq, D = q.shape
+    B = seq_lens.shape[0]
+    if cu_q.shape[0] != B + 1:
+        raise ValueError("cu_q must have one entry more than seq_lens")
+    window, sinks = _check_window(window, sinks)
+    _call("pkv_paged_prefill_fp8b", dev, stream, (_lib or load()).pkv_paged_prefill_fp8b, qa, cu, T,
+          _int32(max_q_len, "max_q_len"), kc, vc, ke, ve, bt, block_table.shape[1], lens, psz, B,
+          _int32(max_kv_len, "max_kv_len"), int(max_total_kv), Hq, Hkv, D, P, NP,
+          1.0 / math.sqrt(D) if sm_scale is None else float(sm_scale), window, sinks, oa, odt, ws, workspace.numel(),
+          _error_word(device_error, dev))
+
+
+def paged_prefill_fp8b(q, cu_q, k_cache, v_cache, k_exp, v_exp, block_table, seq_lens, max_q_len, out=None,
+                       out_dtype=torch.bfloat16, max_kv_len=None, workspace=None, sm_scale=None, device_error=None,
+                       stream=None, max_total_kv=0, seq_page_sizes=None, window=0, sinks=0) -> torch.Tensor:
+    """Allocating form of pkv_paged_prefill_fp8b (on the stream it runs on):
+    max_kv_len defaults to the block table's capacity, as in paged_prefill."""
+    if out is None:
+        with _on(stream, q.device):
+            out = torch.empty(q.shape, dtype=out_dtype, device=q.device)
+    if max_kv_len is None:
+        if seq_page_sizes is not None:
+            raise ValueError("give max_kv_len when seq_page_sizes is given")
+        max_kv_len = block_table.shape[1] * k_cache.shape[2]
+    if workspace is None:
+        _check_window(window, sinks)
+        n = pkv_prefill_fp8b_workspace_size(seq_lens.shape[0], k_cache.shape[1], max_q_len, max_kv_len, max_total_kv,
+                                            window, sinks)
+        with _on(stream, q.device):
+            workspace = torch.empty(n, dtype=torch.uint8, device=q.device)
+    pkv_paged_prefill_fp8b(q, cu_q, k_cache, v_cache, k_exp, v_exp, block_table, seq_lens, out, max_q_len, max_kv_len,
+                           workspace, sm_scale, device_error, stream, max_total_kv, seq_page_sizes, window, sinks)
+    return out
+
+
+# ---------------------------------------------------------------------------
+# the page pool and the page plan
+# ---------------------------------------------------------------------------
+def page_pool(num_pages, device=None, pages=None) -> torch.Tensor:
+    """A pool for plan_pages: int32 [4 + num_pages], its free pages all of
+    0 .. num_pages - 1, or the ones given (handed out from the last one on)."""
+    device = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
+    free = torch.arange(num_pages, dtype=torch.int32) if pages is None else torch.as_tensor(pages).to("cpu", torch.int32)
+    if free.dim() != 1 or free.numel() > num_pages:
+        raise ValueError("pages must be a list of at most num_pages pages")
+    pool = torch.zeros(PAGE_POOL_HEADER + num_pages, dtype=torch.int32)
+    pool[0] = free.numel()
+    pool[PAGE_POOL_HEADER:PAGE_POOL_HEADER + free.numel()] = free
+    return pool.to(device)
+
+
+def _plan_table(block_table, pool, batch, dev):
+    """Addresses of table and pool, entries a row, and pages of the pool."""
+    bt, pa = _addr(block_table, "block_table", torch.int32, 2, dev), _addr(pool, "pool", torch.int32, 1, dev)
+    if block_table.shape[0] != batch:
+        raise ValueError("block_table must have one row per sequence")
+    if pool.shape[0] <= PAGE_POOL_HEADER:
+        raise ValueError(f"pool must be int32 [{PAGE_POOL_HEADER} + num_pages]")
+    return bt, pa, block_table.shape[1], pool.shape[0] - PAGE_POOL_HEADER
+
+
+def pkv_plan_pages(past_lens, new_lens, block_table, pool, page_size, seq_lens, cu_q, slot_mapping, positions=None,
+                   device_error=None, stream=None) -> None:
+    """Sequence b holds past_lens[b] tokens and brings new_lens[b] (int32 [B]):
+    takes the pages it lacks from the pool into block_table [B, max_pages], and
+    writes seq_lens [B] (may be past_lens), cu_q [B + 1], slot_mapping int64 [T]
+    and positions int32 [T] of the new tokens, back to back; rows behind them get
+    slot -1.  All or nothing (see device_error)."""
+    dev = _cuda_index(past_lens, "past_lens")
+    past, new = _addr(past_lens, "past_lens", torch.int32, 1, dev), _addr(new_lens, "new_lens", torch.int32, 1, dev)
+    B = past_lens.shape[0]
+    bt, pa, mp, NP = _plan_table(block_table, pool, B, dev)
+    lens, cu = _addr(seq_lens, "seq_lens", torch.int32, 1, dev), _addr(cu_q, "cu_q", torch.int32, 1, dev)
+    slots = _addr(slot_mapping, "slot_mapping", torch.int64, 1, dev)
+    pos = None if positions is None else _addr(positions, "positions", torch.int32, 1, dev)
+    if new_lens.shape[0] != B or seq_lens.shape[0] != B or cu_q.shape[0] != B + 1:
+        raise ValueError("new_lens and seq_lens must have one entry per sequence, cu_q one more")
+    if positions is not None and positions.shape != slot_mapping.shape:
+        raise ValueError("positions must have one entry per slot")
+    _call("pkv_plan_pages", dev, stream, (_lib or load()).pkv_plan_pages, past, new, B, bt, mp, int(page_size), pa, NP,
+          lens, cu, slots, pos, _int32(slot_mapping.shape[0], "max_tokens"), _error_word(device_error, dev))
+
+
+def plan_pages(past_lens, new_lens, block_table, pool, page_size, max_tokens=None, seq_lens=None, cu_q=None,
+               slot_mapping=None, positions=None, device_error=None, stream=None) -> tuple:
+    """Allocating form of pkv_plan_pages (on the stream it runs on): give
+    slot_mapping or max_tokens.  Returns (seq_lens, cu_q, slot_mapping, positions)."""
+    if slot_mapping is None and max_tokens is None:
+        raise ValueError("give slot_mapping or max_tokens")
+    if slot_mapping is not None and max_tokens is not None and max_tokens != slot_mapping.shape[0]:
+        raise ValueError("max_tokens must be slot_mapping's length")
+    if seq_lens is None or cu_q is None or slot_mapping is None or positions is None:
+        _cuda_index(past_lens, "past_lens")
+        with _on(stream, past_lens.device):
+            B, device = past_lens.shape[0], past_lens.device
+            n = slot_mapping.shape[0] if max_tokens is None else max_tokens
+            if seq_lens is None:
+                seq_lens = torch.empty(B, dtype=torch.int32, device=device)
+            if cu_q is None:
+                cu_q = torch.empty(B + 1, dtype=torch.int32, device=device)
+            if slot_mapping is None:
+                slot_mapping = torch.empty(n, dtype=torch.int64, device=device)
+            if positions is None:
+                positions = torch.empty(n, dtype=torch.int32, device=device)
+    pkv_plan_pages(past_lens, new_lens, block_table, pool, page_size, seq_lens, cu_q, slot_mapping, positions,
+                   device_error, stream)
+    return seq_lens, cu_q, slot_mapping, positions
+
+
+def pkv_release_pages(seq_lens, block_table, pool, page_size, keep_lens=None, device_error=None, stream=None) -> None:
+    """The pages behind keep_lens[b] tokens (None: all) of sequences of
+    seq_lens[b] tokens (int32 [B]) go back to the pool.  All or nothing."""
+    dev = _cuda_index(seq_lens, "seq_lens")
+    lens = _addr(seq_lens, "seq_lens", torch.int32, 1, dev)
+    keep = None if keep_lens is None else _addr(keep_lens, "keep_lens", torch.int32, 1, dev)
+    B = seq_lens.shape[0]
+    bt, pa, mp, NP = _plan_table(block_table, pool, B, dev)
+    if keep_lens is not None and keep_lens.shape[0] != B:
+        raise ValueError("keep_lens must have one entry per sequence")
+    _call("pkv_release_pages", dev, stream, (_lib or load()).pkv_release_pages, lens, keep, B, bt, mp, int(page_size),
+          pa, NP, _error_word(device_error, dev))
+
+
+def release_pages(seq_lens, block_table, pool, page_size, keep_lens=None, device_error=None, stream=None) -> None:
+    pkv_release_pages(seq_lens, block_table, pool, page_size, keep_lens, device_error, stream)
+
+
+
 __all__ = ["load", "lib_path", "pkv_kv_append_fp8", "pkv_paged_gqa_decode", "pkv_decode_workspace_size",
            "pkv_paged_gqa_decode_noalloc", "pkv_decode_noalloc_scratch_bytes", "pkv_append_decode_fp8",
            "append_decode_fp8", "pkv_kv_calibrate", "pkv_paged_prefill", "paged_prefill", "pkv_prefill_workspace_size",
@@ -900,4 +1213,9 @@ __all__ = ["load", "lib_path", "pkv_kv_append_fp8", "pkv_paged_gqa_decode", "pkv
            "DEVERR_TIMEOUT", "DEVERR_PAGESIZE", "DEVERR_INTERNAL", "pkv_last_cuda_error",
            "FP4_ROW_BYTES", "fp4_cache", "pkv_kv_append_fp4", "pkv_kv_read_fp4", "kv_append_fp4", "kv_read_fp4",
            "pkv_decode_fp4_workspace_size", "pkv_paged_gqa_decode_fp4", "paged_gqa_decode_fp4",
-           "pkv_prefill_fp4_workspace_size", "pkv_paged_prefill_fp4", "paged_prefill_fp4"]
+           "pkv_prefill_fp4_workspace_size", "pkv_paged_prefill_fp4", "paged_prefill_fp4",
+           "FP8B_BLOCK", "fp8b_cache", "pkv_kv_append_fp8b", "pkv_kv_read_fp8b", "kv_append_fp8b", "kv_read_fp8b",
+           "pkv_decode_fp8b_workspace_size", "pkv_paged_gqa_decode_fp8b", "paged_gqa_decode_fp8b",
+           "pkv_prefill_fp8b_workspace_size", "pkv_paged_prefill_fp8b", "paged_prefill_fp8b",
+           "DEVERR_POOL", "PAGE_POOL_HEADER", "page_pool", "pkv_plan_pages", "plan_pages", "pkv_release_pages",
+           "release_pages"]

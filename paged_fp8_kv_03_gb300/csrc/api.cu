@@ -752,7 +752,7 @@ pkv_status pkv_paged_prefill(const void *q, const int32_t *cu_q, int total_q, in
         !make_kv16_map(&tm_v, v16, rows, CU_TENSOR_MAP_DATA_TYPE_FLOAT16))
         return cuda_failed(cudaErrorInvalidValue);
 
-    PrefillArgs a;
+    PrefillArgs a = {};                                  // (no scales a block: v_refs stays null)
     a.cu_q = cu_q;
     a.total_q = total_q;
     a.max_q_len = max_q_len;

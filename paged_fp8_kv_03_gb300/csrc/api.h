@@ -2,7 +2,7 @@
 // in api.cu).
 #pragma once
 
-#include "internal.h"
+#include "attn.h"
 
 namespace pkv {
 
@@ -17,6 +17,46 @@ inline bool aligned(const void *p, uintptr_t a)
 // Sizes every attention call checks.
 pkv_status check_decode_shape(int batch, int hq, int hkv, int head_dim, int page_size, int max_pages,
                               int64_t num_pages);
+
+// What append and read back check of the caches with a window.
+inline pkv_status check_rows(int64_t num_tokens, int hkv, int head_dim, int64_t num_pages, int page_size, int dtype)
+{
+    if (num_tokens < 0 || hkv <= 0 || num_pages <= 0)
+        return PKV_ERR_SHAPE;
+    if (dtype != PKV_F32 && dtype != PKV_BF16)
+        return PKV_ERR_DTYPE;
+    if (head_dim != kHeadDim || !page_size_ok(page_size))
+        return PKV_ERR_UNSUPPORTED;
+    return PKV_OK;
+}
+
+// What their decode and prefill check.
+inline pkv_status check_attn(int batch, int hq, int hkv, int head_dim, int page_size, int max_pages, int64_t num_pages,
+                      const int32_t *seq_page_sizes, int window, int sinks, int out_dtype)
+{
+    const pkv_status st = check_decode_shape(batch, hq, hkv, head_dim, page_size, max_pages, num_pages);
+    if (st != PKV_OK)
+        return st;
+    if (window < 0 || sinks < 0)
+        return PKV_ERR_SHAPE;
+    if (num_pages * hkv * (page_size / 16) >= (int64_t(1) << 31))
+        return PKV_ERR_UNSUPPORTED;
+    if (seq_page_sizes && static_cast<int64_t>(max_pages) * 256 >= (int64_t(1) << 31))
+        return PKV_ERR_UNSUPPORTED;
+    if (out_dtype != PKV_F32 && out_dtype != PKV_BF16)
+        return PKV_ERR_DTYPE;
+    return PKV_OK;
+}
+
+// A window no sequence outgrows is none; sinks past the longest sequence say
+// nothing more (so the kernels' sums of positions stay within 32 bits).
+inline KeyWindow clamp_window(int window, int sinks, long long max_len)
+{
+    KeyWindow w;
+    w.window = window >= max_len ? 0 : window;
+    w.sinks = w.window == 0 ? 0 : static_cast<int>(sinks < max_len ? sinks : max_len);
+    return w;
+}
 
 // Effective bound of seq_lens: max_seq_len, or the table's capacity at the
 // pool page size when max_seq_len is 0.

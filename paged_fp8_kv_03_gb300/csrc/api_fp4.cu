@@ -8,17 +8,6 @@ using namespace pkv;
 
 namespace {
 
-pkv_status check_rows(int64_t num_tokens, int hkv, int head_dim, int64_t num_pages, int page_size, int dtype)
-{
-    if (num_tokens < 0 || hkv <= 0 || num_pages <= 0)
-        return PKV_ERR_SHAPE;
-    if (dtype != PKV_F32 && dtype != PKV_BF16)
-        return PKV_ERR_DTYPE;
-    if (head_dim != kHeadDim || !page_size_ok(page_size))
-        return PKV_ERR_UNSUPPORTED;
-    return PKV_OK;
-}
-
 pkv_status rows_args(Fp4RowArgs &a, const void *k, const void *v, int dtype, int64_t num_tokens, int hkv,
                      const int64_t *slots, const float *k_scale, const float *v_scale, const uint8_t *k_cache,
                      const uint8_t *v_cache, int64_t num_pages, int page_size, int32_t *device_error)
@@ -42,34 +31,6 @@ pkv_status rows_args(Fp4RowArgs &a, const void *k, const void *v, int dtype, int
     a.page_log2 = 31 - __builtin_clz(static_cast<unsigned>(page_size));
     a.err = device_error;
     return PKV_OK;
-}
-
-// Checks that decode and prefill share.
-pkv_status check_attn(int batch, int hq, int hkv, int head_dim, int page_size, int max_pages, int64_t num_pages,
-                      const int32_t *seq_page_sizes, int window, int sinks, int out_dtype)
-{
-    const pkv_status st = check_decode_shape(batch, hq, hkv, head_dim, page_size, max_pages, num_pages);
-    if (st != PKV_OK)
-        return st;
-    if (window < 0 || sinks < 0)
-        return PKV_ERR_SHAPE;
-    if (num_pages * hkv * (page_size / 16) >= (int64_t(1) << 31))
-        return PKV_ERR_UNSUPPORTED;
-    if (seq_page_sizes && static_cast<int64_t>(max_pages) * 256 >= (int64_t(1) << 31))
-        return PKV_ERR_UNSUPPORTED;
-    if (out_dtype != PKV_F32 && out_dtype != PKV_BF16)
-        return PKV_ERR_DTYPE;
-    return PKV_OK;
-}
-
-// A window no sequence outgrows is none; sinks past the longest sequence say
-// nothing more (so the kernels' sums of positions stay within 32 bits).
-Fp4Window clamp_window(int window, int sinks, long long max_len)
-{
-    Fp4Window w;
-    w.window = window >= max_len ? 0 : window;
-    w.sinks = w.window == 0 ? 0 : static_cast<int>(sinks < max_len ? sinks : max_len);
-    return w;
 }
 
 // CTAs of the decode grid (of the kernel with one part a weight and of that
@@ -171,7 +132,7 @@ pkv_status pkv_paged_gqa_decode_fp4(const void *q, const uint8_t *k_cache, const
     const long long max_len = effective_max_len(max_seq_len, max_pages_per_seq, page_size);
     if (max_len >= (int64_t(1) << 31))
         return PKV_ERR_UNSUPPORTED;
-    Fp4AttnArgs a = {};
+    CacheAttnArgs a = {};
     a.q = static_cast<const __nv_bfloat16 *>(q);
     a.k_scale = k_scale;
     a.v_scale = v_scale;
@@ -238,7 +199,7 @@ size_t pkv_prefill_fp4_workspace_size(int batch, int num_kv_heads, int max_q_len
     if (batch < 0 || num_kv_heads <= 0 || max_q_len < 0 || max_kv_len < 0 || max_total_kv < 0 || window < 0 ||
         sinks < 0)
         return 0;
-    return prefill_fp4_bytes(batch, prefill_fp4_rows(batch, num_kv_heads, max_q_len, max_kv_len, max_total_kv, window,
+    return prefill_fp4_bytes(batch, windowed_rows(batch, num_kv_heads, max_q_len, max_kv_len, max_total_kv, window,
                                                      sinks));
 }
 
@@ -274,7 +235,7 @@ pkv_status pkv_paged_prefill_fp4(const void *q, const int32_t *cu_q, int total_q
         return PKV_ERR_UNSUPPORTED;
     if (max_kv_len == 0)
         return PKV_OK;                                   // no sequence can hold a query
-    const long long rows = prefill_fp4_rows(batch, num_kv_heads, max_q_len, max_kv_len, max_total_kv, window, sinks);
+    const long long rows = windowed_rows(batch, num_kv_heads, max_q_len, max_kv_len, max_total_kv, window, sinks);
     if (rows >= (int64_t(1) << 31))
         return PKV_ERR_UNSUPPORTED;
     if (!workspace || !aligned(workspace, 256) || workspace_bytes < prefill_fp4_bytes(batch, rows))
@@ -319,7 +280,8 @@ pkv_status pkv_paged_prefill_fp4(const void *q, const int32_t *cu_q, int total_q
     a.out = out;
     a.out_f32 = out_dtype == PKV_F32;
     a.err = device_error;
-    const cudaError_t e = launch_paged_prefill_fp4(a, clamp_window(window, sinks, max_kv_len), tm_q, tm_k, tm_v, stream);
+    const cudaError_t e = launch_prefill_windowed(a, clamp_window(window, sinks, max_kv_len), tm_q, tm_k, tm_v,
+                                                   launch_widen_fp4, stream);
     return e == cudaSuccess ? PKV_OK : cuda_failed(e, "4-bit prefill kernel launch");
 }
 

@@ -50,12 +50,12 @@
 #include <math.h>
 
 #include "fp4.cuh"
+#include "split.cuh"
 
 namespace pkv {
 
 namespace {
 
-constexpr unsigned kEvery = 0xffffffffu;
 constexpr int kUnitBytes = 4 * kFp4Tile;                   // K tile 0, K tile 1, V tile 0, V tile 1
 // A weight is 2^(score - m) with a reference m that is a lift below the largest
 // score so far (log2 units) when it is set, and moves only when a score exceeds it
@@ -77,7 +77,6 @@ __device__ __forceinline__ float lift_of(int tiles)
 // 1e-6 over 8K to 60K tokens, what a plain fp32 computation has; 256 measured 3e-6.
 template <int kParts>
 constexpr int kFoldUnits = kParts == 1 ? 512 : 16;
-constexpr uint64_t kLimitNs = 2000000000ull;
 
 // The list's kernel: every warp is a worker with its own ring, whose stages are
 // filled and waited for in pairs (one by one, the copies' issue and the waits cost
@@ -103,191 +102,12 @@ struct ClusterSmem {                                       // [warps][kClusterUn
     static constexpr int kBytes = kFlag + 16;
 };
 
-// What one sequence shows its query: tokens [0, sinks) and [from, len), as
-// tiles 0 .. first - 1 and then first + skip .. (tiles in all).
-struct Sight {
-    int len, sinks, from, first, skip, tiles;
-};
-
-__device__ __forceinline__ Sight sight_of(const Fp4AttnArgs &a, int b)
-{
-    Sight s;
-    const int lp = seq_page_log2(a, b);
-    const long long cap = lp < 0 ? 0 : static_cast<long long>(a.max_pages) << lp;
-    const int most = cap < a.max_len ? static_cast<int>(cap) : a.max_len;
-    const int L = __ldg(a.seq_lens + b);
-    s.len = L < 0 ? 0 : min(L, most);
-    s.from = a.win.window == 0 ? 0 : max(0, s.len - a.win.window);
-    s.sinks = min(a.win.sinks, s.from);
-    s.first = (s.sinks + 15) >> 4;
-    s.skip = max(s.from >> 4, s.first) - s.first;
-    s.tiles = ((s.len + 15) >> 4) - s.skip;
-    return s;
-}
-
-// Tile of the sequence that is tile i of its visible ones.
-__device__ __forceinline__ int tile_at(const Sight &s, int i)
-{
-    return i < s.first ? i : i + s.skip;
-}
-
-struct Place {
-    int b, h, unit;
-};
-
-__device__ __forceinline__ Place place_of(const int *start, int batch, int x)
-{
-    const int per_head = start[batch];
-    Place p;
-    p.h = x / per_head;
-    const int rem = x - p.h * per_head;
-    int lo = 0, hi = batch - 1;
-    while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (start[mid] <= rem)
-            lo = mid;
-        else
-            hi = mid - 1;
-    }
-    p.b = lo;
-    p.unit = rem - start[lo];
-    return p;
-}
-
-// Bounded wait by a whole warp.
-__device__ __noinline__ bool wait_slow(uint32_t bar, uint32_t parity, volatile int *stop, int32_t *err, int lane)
-{
-    uint64_t t0 = 0;
-    for (uint32_t it = 0;; ++it) {
-        if (__all_sync(kEvery, mbar_try_wait(bar, parity)))
-            return true;
-        if ((it & 15u) == 15u) {
-            int quit = 0;
-            if (lane == 0) {
-                if (t0 == 0)
-                    t0 = global_timer_ns();
-                if (*stop) {
-                    quit = 1;
-                } else if (global_timer_ns() - t0 > kLimitNs) {
-                    *stop = 1;
-                    if (err)
-                        atomicOr(err, PKV_DEVERR_TIMEOUT);
-                    quit = 1;
-                }
-            }
-            if (__shfl_sync(kEvery, quit, 0))
-                return false;
-        }
-    }
-}
-
-// The list's position of position x of the same list with one more, empty unit
-// after every segment: an empty one counts as the next segment's first.
-__device__ __forceinline__ int real_position(const int *start, int batch, int hkv, int x)
-{
-    const int per_head = start[batch], wide = per_head + batch;
-    const int h = x / wide;
-    if (h >= hkv)
-        return per_head * hkv;
-    const int rem = x - h * wide;
-    int lo = 0, hi = batch - 1;
-    while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (start[mid] + mid <= rem)
-            lo = mid;
-        else
-            hi = mid - 1;
-    }
-    return h * per_head + min(rem - lo, start[lo + 1]);
-}
-
-__device__ __forceinline__ bool wait_stage(uint32_t bar, uint32_t parity, volatile int *stop, int32_t *err, int lane)
-{
-    return __all_sync(kEvery, mbar_try_wait(bar, parity)) || wait_slow(bar, parity, stop, err, lane);
-}
-
-__device__ __forceinline__ void lds128(uint32_t at, uint32_t (&r)[4])
-{
-    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(at));
-}
-__device__ __forceinline__ void lds64(uint32_t at, uint32_t (&r)[2])
-{
-    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(r[0]), "=r"(r[1]) : "r"(at));
-}
-__device__ __forceinline__ uint32_t lds16(uint32_t at)
-{
-    uint16_t v;
-    asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(at));
-    return v;
-}
-__device__ __forceinline__ uint32_t lds8(uint32_t at)
-{
-    uint32_t v;
-    asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(at));
-    return v;
-}
-
-__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b)
-{
-    uint32_t d;
-    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
-    return d;
-}
-
-__device__ __forceinline__ uint32_t transpose8x8(uint32_t a)
-{
-    uint32_t d;
-    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
-    return d;
-}
-
-// Two E4M3 bytes (low 16 bits) -> f16 pair.
-__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t s)
-{
-    uint32_t d;
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(d) : "h"(static_cast<uint16_t>(s)));
-    return d;
-}
-
 // Row n of a fragment is token order(n) of its tile (8 + order(n - 8) for the
 // upper half): adjacent lanes' K rows then differ in parity (conflict-free
 // 16-byte reads) and a quad's V rows pair up even and odd (2-way).
 __device__ __forceinline__ int order(int n)
 {
     return n ^ ((n >> 1) & 1);
-}
-
-// Two fp32 values in one 64-bit register pair; each half rounds like the
-// scalar operation.
-__device__ __forceinline__ uint64_t pack2(float a, float b)
-{
-    uint64_t r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
-    return r;
-}
-__device__ __forceinline__ float2 unpack2(uint64_t r)
-{
-    float2 v;
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(v.x), "=f"(v.y) : "l"(r));
-    return v;
-}
-__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b)
-{
-    uint64_t d;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-    return d;
-}
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c)
-{
-    uint64_t d;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
-    return d;
-}
-__device__ __forceinline__ float max3(float a, float b, float c)
-{
-    float d;
-    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
-    return d;
 }
 
 // Where a lane (r, c) reads within a tile.
@@ -394,64 +214,6 @@ __device__ __forceinline__ void accumulate(const RawV &x, const uint32_t (&b)[kP
     }
 }
 
-// 16 consecutive dims of one output row.
-__device__ __forceinline__ void store16(const Fp4AttnArgs &a, int64_t row, int d, const float (&v)[16])
-{
-    if (a.out_f32) {
-        float4 *p = reinterpret_cast<float4 *>(static_cast<float *>(a.out) + row * kHeadDim + d);
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            p[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
-    } else {
-        uint4 *p = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.out) + row * kHeadDim + d);
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            uint32_t w[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const __nv_bfloat162 b = __floats2bfloat162_rn(v[8 * i + 2 * j], v[8 * i + 2 * j + 1]);
-                w[j] = *reinterpret_cast<const uint32_t *>(&b);
-            }
-            p[i] = make_uint4(w[0], w[1], w[2], w[3]);
-        }
-    }
-}
-
-__device__ __forceinline__ void store4(const Fp4AttnArgs &a, int64_t row, int d, float4 v)
-{
-    if (a.out_f32) {
-        *reinterpret_cast<float4 *>(static_cast<float *>(a.out) + row * kHeadDim + d) = v;
-    } else {
-        const __nv_bfloat162 x = __floats2bfloat162_rn(v.x, v.y), y = __floats2bfloat162_rn(v.z, v.w);
-        *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(a.out) + row * kHeadDim + d) =
-            make_uint2(*reinterpret_cast<const uint32_t *>(&x), *reinterpret_cast<const uint32_t *>(&y));
-    }
-}
-
-// All threads of the cluster (one CTA: of the CTA).
-__device__ __forceinline__ void cluster_sync(int ctas)
-{
-    if (ctas > 1)
-        asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-    else
-        __syncthreads();
-}
-
-// The float at address `at` of this CTA's shared memory in CTA `cta` of the
-// cluster (own: in this one).
-__device__ __forceinline__ float cluster_load(uint32_t at, int cta, bool own)
-{
-    float v;
-    if (own) {
-        asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(at) : "memory");
-    } else {
-        uint32_t there;
-        asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(there) : "r"(at), "r"(cta));
-        asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(there) : "memory");
-    }
-    return v;
-}
-
 // kParts: f16 parts of a softmax weight.  One (rounded to f16, 2^-11) is enough
 // under a bf16 output's 2^-8; two keep an fp32 output to 2^-21.  The sum that
 // normalises them is of the fp32 weights.
@@ -486,59 +248,6 @@ __device__ __forceinline__ void whole_sums(const State &s, float (&l)[2])
         l[0] += __shfl_xor_sync(kEvery, l[0], o);
         l[1] += __shfl_xor_sync(kEvery, l[1], o);
     }
-}
-
-// Q as B fragment: head r, dims 32c + 4 kk + {0, 1} and {2, 3}, brought to [1, 2)
-// by a power of two, so that f16 holds all bits of what is at least 2^-17 of the
-// row's largest |q|, and the rest to 2^-25 of that; f0, f1 turn unscaled scores of
-// heads 2c, 2c + 1 into exponents of 2.
-struct Query {
-    uint32_t q[8][2];
-    float f0, f1;
-};
-
-__device__ __forceinline__ void load_rows(const Fp4AttnArgs &a, int b, int h, int r, int c, uint4 (&raw)[4])
-{
-    const int64_t row = static_cast<int64_t>(b) * a.hq + static_cast<int64_t>(h) * a.group + (r < a.group ? r : 0);
-    const uint4 *src = reinterpret_cast<const uint4 *>(a.q + row * kHeadDim + 32 * c);
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-        raw[i] = __ldg(src + i);
-}
-
-__device__ __forceinline__ void make_query(const Fp4AttnArgs &a, const uint4 (&raw)[4], float k_scale, int r, int c,
-                                           Query &o)
-{
-    const uint32_t *w = reinterpret_cast<const uint32_t *>(raw);
-    uint32_t top = 0;                                      // largest |q|, as its bits
-#pragma unroll
-    for (int i = 0; i < 16; ++i)
-        top = max(top, max((w[i] << 16) & 0x7FFFFFFFu, w[i] & 0x7FFF0000u));
-    top = max(top, __shfl_xor_sync(kEvery, top, 1));
-    top = max(top, __shfl_xor_sync(kEvery, top, 2));
-    const int ex = min(max(static_cast<int>(top >> 23), 1), 253);
-    const float down = __uint_as_float(static_cast<uint32_t>(254 - ex) << 23);
-    const float up = __uint_as_float(static_cast<uint32_t>(ex) << 23) * (k_scale * a.sm_scale_log2);
-    const bool on = r < a.group;
-#pragma unroll
-    for (int i = 0; i < 16; ++i)
-        o.q[i >> 1][i & 1] = f32x2_to_f16x2(on ? __uint_as_float(w[i] << 16) * down : 0.f,
-                                            on ? __uint_as_float(w[i] & 0xFFFF0000u) * down : 0.f);
-    o.f0 = __shfl_sync(kEvery, up, 8 * c);
-    o.f1 = __shfl_sync(kEvery, up, 8 * c + 4);
-}
-
-// Units of a segment of which every token is visible: past the sinks and the
-// window's first tile, before the last tokens.
-struct Inner {
-    int lo;
-    uint32_t n;
-};
-
-__device__ __forceinline__ Inner inner_units(const Sight &s)
-{
-    const int lo = (s.from > 0 ? s.first + 2 : 1) >> 1, hi = ((s.len >> 4) - s.skip) >> 1;
-    return Inner{lo, hi > lo ? static_cast<uint32_t>(hi - lo) : 0u};
 }
 
 // One unit: the 32 tokens of unit `unit` at shared address st.  done() is
@@ -666,21 +375,6 @@ __device__ __forceinline__ void store_state(float *row, const State &s, const fl
         *reinterpret_cast<float2 *>(row + kHeadDim) = make_float2(j ? s.m1 : s.m0, l[j]);
 }
 
-// Tile number in the pools of visible tile i of segment (b, h); -1: its page
-// lies outside the pool (flagged), -2: there is no such tile.
-__device__ __forceinline__ int tile_number(const Fp4AttnArgs &a, const Sight &s, int b, int h, int i)
-{
-    if (i >= s.tiles)
-        return -2;
-    int phys, row;
-    if (!seq_token_page(a, b, seq_page_log2(a, b), 16 * tile_at(s, i), phys, row)) {
-        if (a.err)
-            atomicOr(a.err, PKV_DEVERR_PAGE);
-        return -1;
-    }
-    return (phys * a.hkv + h) * (a.page_size >> 4) + (row >> 4);
-}
-
 // A tile that reads as zeros: the scales of its K and V (the whole warp; st:
 // the unit's address, j: the tile's place in it).
 __device__ __forceinline__ void zero_tile(uint32_t st, int j, int lane)
@@ -688,16 +382,6 @@ __device__ __forceinline__ void zero_tile(uint32_t st, int j, int lane)
     const uint32_t at = st + j * kFp4Tile + kFp4Codes + 4 * lane;
     asm volatile("st.shared.u32 [%0], %1;" ::"r"(at), "r"(0u) : "memory");
     asm volatile("st.shared.u32 [%0], %1;" ::"r"(at + 2 * kFp4Tile), "r"(0u) : "memory");
-}
-
-__device__ __forceinline__ void flag_sequence(const Fp4AttnArgs &a, int b, const Sight &s)
-{
-    if (a.err == nullptr)
-        return;
-    if (seq_page_log2(a, b) < 0)
-        atomicOr(a.err, PKV_DEVERR_PAGESIZE);
-    else if (__ldg(a.seq_lens + b) != s.len)
-        atomicOr(a.err, PKV_DEVERR_SEQLEN);
 }
 
 // ---------------------------------------------------------------------- the list
@@ -742,7 +426,7 @@ template <int kParts>
 __device__ __forceinline__ void work_list(const Fp4DecodeArgs &da, uint8_t *smem, int warp, int lane, int worker, int lo,
                                           int n)
 {
-    const Fp4AttnArgs &a = da.a;
+    const CacheAttnArgs &a = da.a;
     const int *start = reinterpret_cast<const int *>(smem + ListSmem::kStart);
     volatile int *stop = reinterpret_cast<volatile int *>(smem + ListSmem::kFlag);
     const uint32_t ring = smem_addr(smem) + warp * kStages * kUnitBytes;
@@ -927,7 +611,7 @@ __device__ __forceinline__ void work_list(const Fp4DecodeArgs &da, uint8_t *smem
 template <int kParts>
 __global__ void __launch_bounds__(kListThreads, kListCtas) paged_gqa_decode_fp4_kernel(const Fp4DecodeArgs da)
 {
-    const Fp4AttnArgs &a = da.a;
+    const CacheAttnArgs &a = da.a;
     extern __shared__ __align__(128) uint8_t smem[];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     int *start = reinterpret_cast<int *>(smem + ListSmem::kStart);
@@ -1050,7 +734,7 @@ template <int kParts>
 __global__ void __launch_bounds__(32 * kClusterWarps, 2) paged_gqa_decode_fp4_cluster_kernel(const Fp4DecodeArgs da)
 {
     using S = ClusterSmem;
-    const Fp4AttnArgs &a = da.a;
+    const CacheAttnArgs &a = da.a;
     extern __shared__ __align__(128) uint8_t smem[];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int r = lane >> 2, c = lane & 3;
@@ -1208,7 +892,7 @@ template <int kTurn>
 __device__ __forceinline__ void join_head(const Fp4DecodeArgs &da, int sg, int g, int warp, int warps, int lane,
                                           float (*ra)[kHeadDim], float2 *rm)
 {
-    const Fp4AttnArgs &a = da.a;
+    const CacheAttnArgs &a = da.a;
     const int b = sg / a.hkv, h = sg % a.hkv;
     const float vs = __ldg(a.v_scale + h);
     int2 j = da.joins[sg];

@@ -161,6 +161,14 @@ __device__ __forceinline__ float ex2_approx(float x)
     return y;
 }
 
+// max(a, b, c) in one instruction (exact, like two fmaxf).
+__device__ __forceinline__ float max3(float a, float b, float c)
+{
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+
 __device__ __forceinline__ uint32_t f32x2_to_f16x2(float lo, float hi)
 {
     __half2 h = __floats2half2_rn(lo, hi);

@@ -5,19 +5,9 @@
 #include <cuda_fp4.h>
 
 #include "fp4.h"
+#include "grid.cuh"
 
 namespace pkv {
-
-// Waits until the kernels ahead in the stream have ended and their writes are
-// seen; lets the next kernel be brought onto the GPU (it waits in turn).
-__device__ __forceinline__ void grid_wait()
-{
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-}
-__device__ __forceinline__ void launch_dependents()
-{
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-}
 
 // Byte offset in a pool of the tile holding row `row` of pool page `page`.
 __device__ __forceinline__ int64_t fp4_tile_offset(int64_t page, int h, int row, int hkv, int page_size)
@@ -35,15 +25,6 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_
             dst),
         "l"(src), "r"(bytes), "r"(bar), "l"(policy)
         : "memory");
-}
-
-// a + b rounded, and exactly what that loses (Knuth's two-sum).  Long sums of like
-// terms keep it: rounded the same way every time, they drift by up to 2^-24 a term.
-__device__ __forceinline__ float two_sum(float a, float b, float &rest)
-{
-    const float s = __fadd_rn(a, b), t = __fsub_rn(s, a);
-    rest = __fadd_rn(__fsub_rn(a, __fsub_rn(s, t)), __fsub_rn(b, t));
-    return s;
 }
 
 __device__ __forceinline__ float e4m3_value(uint8_t c)

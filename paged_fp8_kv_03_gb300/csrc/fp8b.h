@@ -1,0 +1,67 @@
+// Declarations of the block-scaled FP8 cache's translation units (not
+// installed): the block, the arguments of the kernels and their launchers.
+#pragma once
+
+#include "attn.h"
+
+namespace pkv {
+
+// A block: 16 consecutive tokens of one kv head.  Its codes are 16 rows of 128
+// E4M3 bytes; its byte x, at the block's number in its own pool, stands for
+// 2^(x - 127).  Appended blocks have x - 127 within [kExpMin, kExpMax]: from there
+// on every value, code * 2^(x - 127), is a normal bf16 number, or 0.
+constexpr int kBlock = 16;
+constexpr int kExpBias = 127, kExpMin = -117, kExpMax = 119;
+
+struct Fp8bRowArgs {                                       // append and read back
+    const void *k_in, *v_in;                               // append: rows to quantise
+    void *k_out, *v_out;                                   // read back: rows to write
+    int64_t num_tokens;
+    int hkv;
+    const int64_t *slots;
+    uint8_t *k_cache, *v_cache, *k_exp, *v_exp;
+    int64_t num_slots;
+    int page_size, page_log2;
+    int32_t *err;
+};
+
+cudaError_t launch_kv_append_fp8b(const Fp8bRowArgs &a, bool bf16, cudaStream_t stream);
+cudaError_t launch_kv_read_fp8b(const Fp8bRowArgs &a, bool bf16, cudaStream_t stream);
+
+// Decode: workers of the split (warps) a CTA.
+constexpr int kFp8bDecodeWorkers = 4;
+
+struct Fp8bDecodeArgs {
+    CacheAttnArgs a;                                       // (k_scale, v_scale: not used)
+    const uint8_t *k_exp, *v_exp;
+    int2 *joins;                                           // as in Fp4DecodeArgs
+    int *firsts;
+    float *partials;
+    long long num_slots;
+    int cluster;
+    int withhold;
+};
+
+cudaError_t launch_paged_decode_fp8b(const Fp8bDecodeArgs &da, cudaStream_t stream);
+
+// Prefill's workspace: the header, a float a sequence and kv head (what a value of V's
+// copy stands for), the 16-bit copies of K and V, a word a tile (as the 4-bit
+// cache's), and 16 bytes a row, a bit a NaN of V.
+// (The maxima of a sequence's heads stand in shared memory.)
+constexpr int kFp8bMaxPrefillHeads = 8192;
+
+inline size_t prefill_fp8b_refs_bytes(int batch, int hkv)
+{
+    return (static_cast<size_t>(batch) * hkv * sizeof(float) + 255) & ~size_t(255);
+}
+
+inline size_t prefill_fp8b_bytes(int batch, int hkv, long long rows)
+{
+    return prefill_header_bytes(batch) + prefill_fp8b_refs_bytes(batch, hkv) +
+           static_cast<size_t>(rows) * (2 * kHeadDim * sizeof(__half) + kHeadDim / 8) +
+           static_cast<size_t>(rows / 128) * sizeof(uint32_t);
+}
+
+cudaError_t launch_widen_fp8b(const PrefillArgs &a, const KeyWindow &win, cudaStream_t stream);
+
+}  // namespace pkv

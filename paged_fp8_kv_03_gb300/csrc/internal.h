@@ -119,7 +119,10 @@ struct PrefillArgs {
     int total_q, max_q_len;
     int tokens_per_tile;            // 128 / group query tokens per CTA tile
     int max_tiles;                  // ceil(max_q_len / tokens_per_tile)
-    const float *k_scale, *v_scale;
+    const float *k_scale, *v_scale; // [hkv] (FP8 and 4-bit caches)
+    const uint8_t *k_exp, *v_exp;   // block-scaled FP8 cache: its blocks' exponents
+    float *v_refs;                  // block-scaled FP8 cache: [batch][hkv] what a value of v16 stands for (caller
+                                    // workspace, written ahead of the widening); else nullptr
     const int32_t *block_table;
     int max_pages;
     const int32_t *seq_lens;

@@ -126,7 +126,7 @@ __global__ void __launch_bounds__(256) kv_widen_kernel(const PrefillArgs a)
         const int b0 = min(a.batch, tid * chunk), b1 = min(a.batch, b0 + chunk);
         long long local = 0;
         for (int b = b0; b < b1; ++b)
-            local += region_tiles<false>(a, Fp4Window{0, 0}, b);
+            local += region_tiles<false>(a, KeyWindow{0, 0}, b);
         // saturate: nothing past cap_tiles + 1 matters
         int loc = static_cast<int>(local < cap_tiles + 1 ? local : cap_tiles + 1);
         int incl = loc;
@@ -145,7 +145,7 @@ __global__ void __launch_bounds__(256) kv_widen_kernel(const PrefillArgs a)
         int run = min(base + incl - loc, static_cast<int>(cap_tiles + 1));
         for (int b = b0; b < b1; ++b) {
             off[b] = run;
-            run = static_cast<int>(min(run + region_tiles<false>(a, Fp4Window{0, 0}, b), cap_tiles + 1));
+            run = static_cast<int>(min(run + region_tiles<false>(a, KeyWindow{0, 0}, b), cap_tiles + 1));
         }
         if (tid == 255)
             off[a.batch] = min(base + incl, static_cast<int>(cap_tiles + 1));
@@ -274,7 +274,7 @@ __device__ __noinline__ float move_out(uint32_t cm, uint32_t cs, float m, float 
 template <bool kWin, bool kFp4, bool kMoves>
 __global__ void __launch_bounds__(kPThreads, 1)
     paged_prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
-                         const __grid_constant__ CUtensorMap tm_v, const PrefillArgs a, const Fp4Window win)
+                         const __grid_constant__ CUtensorMap tm_v, const PrefillArgs a, const KeyWindow win)
 {
     constexpr int kFold = kFp4 ? kFold4 : kFold8;
     // (4-bit cache: the reference of P's exponents is set well below the maximum, so that
@@ -700,10 +700,10 @@ __global__ void __launch_bounds__(kPThreads, 1)
             ok = false;
         }
         if (ok) {
-            const float inv = __ldg(a.v_scale + h) / (l + red_l[(half ^ 1) * kRows + row]);
+            const float inv = value_factor(a, b, h) / (l + red_l[(half ^ 1) * kRows + row]);
             const int64_t orow = (static_cast<int64_t>(q0) + t0 + tl) * a.hq + h * G + g;
             uint32_t nans = 0;
-            if (kFp4)
+            if (kFp4 && !a.v_refs)
                 nans = nan_blocks<kWin>(a, win, row0 / kKeys, nt, valid ? pos0 + tl : last, lane, key_tile, copy_tile);
             const bool have_o = nt > kFold;                // at least one segment was folded into O
 #pragma unroll 1
@@ -740,6 +740,9 @@ __global__ void __launch_bounds__(kPThreads, 1)
                     }
                 }
             }
+            if (kFp4 && a.v_refs)
+                put_nans<kWin>(a, win, row0 / kKeys, nt, valid ? pos0 + tl : last, lane, key_tile, copy_tile, valid, orow,
+                               64 * half, 64);
         }
     }
 
@@ -755,7 +758,7 @@ std::mutex g_prefill_mu;
 unsigned long long g_prefill_attr_ctx[64][5] = {};   // per device and kernel: the context its limit was raised in
 
 typedef void (*PrefillKernel)(const CUtensorMap, const CUtensorMap, const CUtensorMap, const PrefillArgs,
-                              const Fp4Window);
+                              const KeyWindow);
 
 cudaError_t raise_limit(PrefillKernel kernel, int which, size_t bytes)
 {
@@ -798,7 +801,7 @@ cudaError_t launch_widen(const PrefillArgs &a, cudaStream_t stream)
     return cudaGetLastError();
 }
 
-cudaError_t launch_attention(PrefillKernel kernel, size_t smem, const PrefillArgs &a, const Fp4Window &win,
+cudaError_t launch_attention(PrefillKernel kernel, size_t smem, const PrefillArgs &a, const KeyWindow &win,
                              const CUtensorMap &tm_q, const CUtensorMap &tm_k16, const CUtensorMap &tm_v16,
                              cudaStream_t stream)
 {
@@ -819,7 +822,7 @@ cudaError_t launch_paged_prefill(const PrefillArgs &a, const CUtensorMap &tm_q, 
 {
     if (static_cast<int64_t>(a.batch) * a.hkv * a.max_tiles <= 0)
         return cudaSuccess;
-    const Fp4Window none = {0, 0};
+    const KeyWindow none = {0, 0};
     const PrefillKernel kernel = paged_prefill_kernel<false, false, false>;
     cudaError_t e = raise_limit(kernel, 4, PS::bytes(false));
     if (e == cudaSuccess)
@@ -827,8 +830,9 @@ cudaError_t launch_paged_prefill(const PrefillArgs &a, const CUtensorMap &tm_q, 
     return e == cudaSuccess ? launch_attention(kernel, PS::bytes(false), a, none, tm_q, tm_k16, tm_v16, stream) : e;
 }
 
-cudaError_t launch_paged_prefill_fp4(const PrefillArgs &a, const Fp4Window &win, const CUtensorMap &tm_q,
-                                     const CUtensorMap &tm_k16, const CUtensorMap &tm_v16, cudaStream_t stream)
+cudaError_t launch_prefill_windowed(const PrefillArgs &a, const KeyWindow &win, const CUtensorMap &tm_q,
+                                    const CUtensorMap &tm_k16, const CUtensorMap &tm_v16, WidenLaunch widen,
+                                    cudaStream_t stream)
 {
     if (static_cast<int64_t>(a.batch) * a.hkv * a.max_tiles <= 0)
         return cudaSuccess;
@@ -843,7 +847,7 @@ cudaError_t launch_paged_prefill_fp4(const PrefillArgs &a, const Fp4Window &win,
     if (a.out_f32)
         e = raise_limit(kernel, (win.window > 0 ? 1 : 0) + (moves ? 2 : 0), PS::bytes(moves));
     if (e == cudaSuccess)
-        e = launch_widen_fp4(a, win, stream);
+        e = widen(a, win, stream);
     if (e != cudaSuccess)
         return e;
     return a.out_f32 ? launch_attention(kernel, PS::bytes(moves), a, win, tm_q, tm_k16, tm_v16, stream)

@@ -2,6 +2,8 @@
 // paired fp32 arithmetic, and which keys a chunk of queries sees.
 #pragma once
 
+#include <math.h>
+
 #include "fp4.cuh"
 #include "tcgen05.cuh"
 
@@ -129,14 +131,6 @@ __device__ __forceinline__ uint64_t f2_fma(uint64_t a, uint64_t b, uint64_t c)
     return d;
 }
 
-// max(a, b, c) in one instruction (exact, like two fmaxf).
-__device__ __forceinline__ float max3(float a, float b, float c)
-{
-    float d;
-    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
-    return d;
-}
-
 // True in exactly one lane of the (converged) warp.
 __device__ __forceinline__ bool elect_one()
 {
@@ -167,8 +161,14 @@ __device__ __forceinline__ bool sequence_ok(const PrefillArgs &a, int b, int q0,
 // smallest number instead of 0, which would make NaN of a hidden key's -inf.
 __device__ __forceinline__ float score_factor(const PrefillArgs &a, int h)
 {
-    const float f = __ldg(a.k_scale + h) * a.sm_scale_log2;
+    const float f = (a.v_refs ? 1.f : __ldg(a.k_scale + h)) * a.sm_scale_log2;
     return f == 0.f ? __uint_as_float(1u) : f;
+}
+
+// What a value of the 16-bit copy of V stands for.
+__device__ __forceinline__ float value_factor(const PrefillArgs &a, int b, int h)
+{
+    return a.v_refs ? __ldg(a.v_refs + b * a.hkv + h) : __ldg(a.v_scale + h);
 }
 
 // Sums over a long context are kept in levels, so that no chain of additions grows
@@ -189,7 +189,7 @@ struct KeyTiles {
 };
 
 template <bool kWin>
-__device__ __forceinline__ KeyTiles key_tiles(const Fp4Window &w, int first_pos)
+__device__ __forceinline__ KeyTiles key_tiles(const KeyWindow &w, int first_pos)
 {
     KeyTiles k = {0, 0, 0, 0};
     if (kWin && w.window > 0) {
@@ -204,7 +204,7 @@ __device__ __forceinline__ KeyTiles key_tiles(const Fp4Window &w, int first_pos)
 // Key tiles that a query tile, or a pair of them, may visit: without a window all of
 // the longest sequence's, with one the sinks' and those that 2 tokens_per_tile +
 // window - 1 keys touch.
-inline int64_t most_key_tiles(const PrefillArgs &a, const Fp4Window &w)
+inline int64_t most_key_tiles(const PrefillArgs &a, const KeyWindow &w)
 {
     const int64_t all = (static_cast<int64_t>(a.max_kv_len) + kKeys - 1) / kKeys;
     if (w.window == 0)
@@ -231,7 +231,7 @@ __device__ __forceinline__ uint8_t *nan_rows(const PrefillArgs &a)
 // key tiles, the i-th one is key_tile(i) of the sequence and copy_tile(i) of the
 // copy, which starts at tile `tile0` (the whole warp).
 template <bool kWin, typename KeyTile, typename CopyTile>
-__device__ __forceinline__ uint32_t nan_blocks(const PrefillArgs &a, const Fp4Window &w, int tile0, int nt, int p, int lane,
+__device__ __forceinline__ uint32_t nan_blocks(const PrefillArgs &a, const KeyWindow &w, int tile0, int nt, int p, int lane,
                                                KeyTile key_tile, CopyTile copy_tile)
 {
     const uint32_t *tiles = nan_tiles(a);
@@ -257,10 +257,55 @@ __device__ __forceinline__ uint32_t nan_blocks(const PrefillArgs &a, const Fp4Wi
     return hit;
 }
 
+// The same for NaN values of the block-scaled FP8 cache's V, whose rows have 16
+// bytes, a bit a dim: puts NaNs into dims d0 .. d0 + dims - 1 of the row `orow` of
+// the output where the row at position p sees one (the whole warp; valid: the
+// lane has a row).  Out of line: it runs once a tile, and mostly finds nothing.
+template <bool kWin, typename KeyTile, typename CopyTile>
+__device__ __noinline__ void put_nans(const PrefillArgs &a, const KeyWindow &w, int tile0, int nt, int p, int lane,
+                                      KeyTile key_tile, CopyTile copy_tile, bool valid, int64_t orow, int d0, int dims)
+{
+    const uint32_t *tiles = nan_tiles(a);
+    bool some = false;
+    for (int i = lane; i < nt; i += 32)
+        some = some || __ldg(tiles + tile0 + copy_tile(i)) != 0;
+    if (!__any_sync(kAll, some))
+        return;
+    const uint32_t *rows = reinterpret_cast<const uint32_t *>(nan_rows(a));
+    uint32_t hit[4] = {0, 0, 0, 0};
+#pragma unroll 1
+    for (int i = 0; i < nt; ++i) {
+        const int64_t tile = tile0 + copy_tile(i);
+        const uint32_t word = __ldg(tiles + tile);
+        if (word == 0)
+            continue;
+#pragma unroll 1
+        for (int k = 0; k < kKeys; ++k) {
+            const int t = key_tile(i) * kKeys + k;
+            if ((word >> (8 * (k >> 5)) & 0xFFu) != 0 && t <= p && (!kWin || t > p - w.window || t < w.sinks))
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    hit[j] |= __ldg(rows + (tile * kKeys + k) * 4 + j);
+        }
+    }
+    if (!valid)
+        return;
+#pragma unroll 1
+    for (int d = d0; d < d0 + dims; ++d) {
+        const uint32_t x = d < 64 ? (d < 32 ? hit[0] : hit[1]) : (d < 96 ? hit[2] : hit[3]);
+        if ((x >> (d & 31)) & 1u) {
+            if (a.out_f32)
+                static_cast<float *>(a.out)[orow * kHeadDim + d] = NAN;
+            else
+                static_cast<__nv_bfloat16 *>(a.out)[orow * kHeadDim + d] = __float2bfloat16_rn(NAN);
+        }
+    }
+}
+
 // 128-row tiles of sequence b's widened region (all its kv heads): zero for a
 // sequence with an empty or inconsistent chunk.
 template <bool kWin>
-__device__ __forceinline__ long long region_tiles(const PrefillArgs &a, const Fp4Window &w, int b)
+__device__ __forceinline__ long long region_tiles(const PrefillArgs &a, const KeyWindow &w, int b)
 {
     const int q0 = __ldg(a.cu_q + b), q1 = __ldg(a.cu_q + b + 1);
     const int L = __ldg(a.seq_lens + b);

@@ -89,7 +89,7 @@ static_assert(P2::bytes(true) <= 232448, "prefill tile buffers exceed the shared
 // found once; a thread takes 8 values of kRowsEach of its rows, of K and of V, 16
 // lanes write a row's 256 bytes.
 template <int kRowsEach>
-__global__ void __launch_bounds__(256) kv_widen_fp4_kernel(const PrefillArgs a, const Fp4Window win)
+__global__ void __launch_bounds__(256) kv_widen_fp4_kernel(const PrefillArgs a, const KeyWindow win)
 {
     constexpr int kPieces = 8 / kRowsEach;               // CTAs' steps a tile
     static_assert(kPieces == 1 || kPieces == 4, "a tile's word has a byte a piece");
@@ -293,7 +293,7 @@ __device__ __forceinline__ float lift_of(int nt)
 template <bool kWin, bool kFolds>
 __global__ void __launch_bounds__(kThreads2, 1)
     paged_prefill_pair_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
-                              const __grid_constant__ CUtensorMap tm_v, const PrefillArgs a, const Fp4Window win)
+                              const __grid_constant__ CUtensorMap tm_v, const PrefillArgs a, const KeyWindow win)
 {
     // (sequence, kv head)-major, heaviest pairs of tiles first within each
     const int pairs = (a.max_tiles + 1) >> 1;
@@ -622,8 +622,8 @@ __global__ void __launch_bounds__(kThreads2, 1)
             tc::fence_after();
             if (kFolds && ntx > kFold2)
                 l = fold(o_tm, m, l, true, true);
-            const float inv = __ldg(a.v_scale + h) / l;
-            const uint32_t nans = nan_blocks<kWin>(a, win, row0 / kKeys, ntx, p_row, lane, key_tile, copy_tile);
+            const float inv = value_factor(a, b, h) / l;
+            const uint32_t nans = a.v_refs ? 0u : nan_blocks<kWin>(a, win, row0 / kKeys, ntx, p_row, lane, key_tile, copy_tile);
             const int64_t orow = (static_cast<int64_t>(q0) + t0 + x * tpt + tl) * a.hq + h * G + g;
             uint4 *dst = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.out) + orow * kHeadDim);
 #pragma unroll 1
@@ -646,6 +646,8 @@ __global__ void __launch_bounds__(kThreads2, 1)
                     dst[4 * c + k] = make_uint4(w[0], w[1], w[2], w[3]);
                 }
             }
+            if (a.v_refs)
+                put_nans<kWin>(a, win, row0 / kKeys, ntx, p_row, lane, key_tile, copy_tile, valid, orow, 0, kHeadDim);
         }
     }
 
@@ -663,7 +665,7 @@ unsigned long long g_pair_ctx[64][4] = {};   // per device and kernel: the conte
 }  // namespace
 
 // The widening launch of the 4-bit calls.
-cudaError_t launch_widen_fp4(const PrefillArgs &a, const Fp4Window &win, cudaStream_t stream)
+cudaError_t launch_widen_fp4(const PrefillArgs &a, const KeyWindow &win, cudaStream_t stream)
 {
     const int64_t tiles = a.rows_cap / kKeys, most = static_cast<int64_t>(device_sm_count()) * 8;
     const size_t smem = (static_cast<size_t>(a.batch) + 1 + 8) * sizeof(int);
@@ -675,7 +677,7 @@ cudaError_t launch_widen_fp4(const PrefillArgs &a, const Fp4Window &win, cudaStr
 }
 
 // The attention launch alone: the widening kernel has been enqueued before.
-cudaError_t launch_prefill_pair(const PrefillArgs &a, const Fp4Window &win, const CUtensorMap &tm_q,
+cudaError_t launch_prefill_pair(const PrefillArgs &a, const KeyWindow &win, const CUtensorMap &tm_q,
                                 const CUtensorMap &tm_k16, const CUtensorMap &tm_v16, cudaStream_t stream)
 {
     // The folding kernel takes longer even where it folds nothing (4096 of 16384 tokens, 64

@@ -1,0 +1,229 @@
+// The widening of the block-scaled FP8 cache to the 16-bit copies that the prefill
+// attention reads: K as bf16, code * 2^ek (exact: 4 significant bits), V as f16 in
+// units of its own reference,
+//   v16 = code * 2^(ev - E) * 2^6,   E = the largest ev among the sequence's blocks
+//                                    of this kv head that some query of the chunk sees,
+// so that 448 comes out as 28672.  Exact for blocks down to 2^-21 of the largest
+// one's scale; below that f16's lower end rounds to 2^-25, 2^-40 of the head's
+// largest V.  The output is multiplied by 2^(E - 6).  NaN codes of V become zeros
+// and are recorded, a bit a value.
+//
+// Two launches.  kv_refs_fp8b_kernel: a cluster of CTAs a sequence takes the maximum
+// of the bytes (a sixteenth of a byte a token and head), and CTA 0 lays out the
+// regions.  kv_widen_fp8b_kernel: a CTA a tile of 128 rows (or a quarter of one, where
+// there are few); a thread takes 8 values of kRowsEach of its rows, of K and of V, 16
+// lanes write a row's 256 bytes.  Bytes bound it: 256 of the cache to 512 of the
+// copies a row.
+#include "fp8b.h"
+#include "prefill.cuh"
+#include "split.cuh"
+
+namespace pkv {
+
+namespace {
+
+constexpr int kRefThreads = 512, kRefCtas = 8;
+
+// The prefix sum of the sequences' 128-row tiles (the whole CTA): tile_off, and a
+// flag for a region past the workspace.
+__device__ __forceinline__ void lay_out(const PrefillArgs &a, const KeyWindow &win, int *warp_sum)
+{
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const long long cap_tiles = a.rows_cap / kKeys;
+    const int most = static_cast<int>(cap_tiles + 1);    // sums saturate just past the workspace
+    const int chunk = (a.batch + kRefThreads - 1) / kRefThreads;
+    const int b0 = min(a.batch, tid * chunk), b1 = min(a.batch, b0 + chunk);
+    long long local = 0;
+    for (int b = b0; b < b1; ++b)
+        local += region_tiles<true>(a, win, b);
+    const int loc = static_cast<int>(local < most ? local : most);
+    int incl = loc;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(kAll, incl, o);
+        if (lane >= o)
+            incl = min(incl + v, most);
+    }
+    if (lane == 31)
+        warp_sum[warp] = incl;
+    __syncthreads();
+    int base = 0;
+    for (int w = 0; w < warp; ++w)
+        base = min(base + warp_sum[w], most);
+    int run = min(base + incl - loc, most);
+    for (int b = b0; b < b1; ++b) {
+        a.tile_off[b] = run;
+        const int next = static_cast<int>(min(run + region_tiles<true>(a, win, b), static_cast<long long>(most)));
+        if (next > cap_tiles && next > run && a.err)
+            atomicOr(a.err, PKV_DEVERR_SEQLEN);          // its region does not fit the workspace
+        run = next;
+    }
+    if (tid == kRefThreads - 1)
+        a.tile_off[a.batch] = min(base + incl, most);
+}
+
+// A cluster of `ctas` CTAs a sequence, and one cluster more for the layout.
+__global__ void __launch_bounds__(kRefThreads) kv_refs_fp8b_kernel(const PrefillArgs a, const KeyWindow win, int ctas)
+{
+    extern __shared__ int top[];                         // [hkv]: largest byte
+    __shared__ int warp_sum[kRefThreads / 32];
+    launch_dependents();
+    const int rank = static_cast<int>(blockIdx.x) % ctas, b = static_cast<int>(blockIdx.x) / ctas;
+    if (b == a.batch) {
+        if (rank == 0)
+            lay_out(a, win, warp_sum);
+        return;
+    }
+    const int q0 = __ldg(a.cu_q + b), q1 = __ldg(a.cu_q + b + 1), L = __ldg(a.seq_lens + b);
+    if (q1 - q0 <= 0 || !sequence_ok(a, b, q0, q1, L, false))
+        return;                                          // (the whole cluster)
+    for (int h = threadIdx.x; h < a.hkv; h += kRefThreads)
+        top[h] = 0;
+    __syncthreads();
+    const int lp = seq_page_log2(a, b), per_page = a.page_size / kBlock;
+    const KeyTiles kt = key_tiles<true>(win, L - (q1 - q0));
+    const int blocks = (L + kBlock - 1) / kBlock, sink_blocks = (kt.sinks + kBlock - 1) / kBlock;
+    const int skip = max(kt.from / kBlock, sink_blocks) - sink_blocks;   // blocks that no query sees
+    for (int i = rank * kRefThreads + threadIdx.x; i < blocks - skip; i += ctas * kRefThreads) {
+        int pg, row;
+        if (!seq_token_page(a, b, lp, (i < sink_blocks ? i : i + skip) * kBlock, pg, row))
+            continue;                                    // (the widening flags it)
+        const uint8_t *x = a.v_exp + static_cast<int64_t>(pg) * a.hkv * per_page + row / kBlock;
+        for (int h = 0; h < a.hkv; ++h) {
+            const int v = __ldg(x + static_cast<int64_t>(h) * per_page);
+            if (v > *const_cast<volatile int *>(top + h))
+                atomicMax(top + h, v);
+        }
+    }
+    cluster_sync(ctas);
+    if (rank == 0) {
+        for (int h = threadIdx.x; h < a.hkv; h += kRefThreads) {
+            int most = top[h];
+            for (int k = 1; k < ctas; ++k)
+                most = max(most, __float_as_int(cluster_load(smem_addr(top + h), k, false)));
+            // 2^(E - 6); a byte below kExpMin's (no appended block has it) counts as that
+            a.v_refs[b * a.hkv + h] = __int_as_float((max(most, kExpMin + kExpBias) - 6) << 23);
+        }
+    }
+    cluster_sync(ctas);                                  // no CTA leaves while its maxima are read
+}
+
+__device__ __forceinline__ float scale_of(uint32_t x)    // 2^(x - 127)
+{
+    return __uint_as_float(x == 0 ? 0x00400000u : x << 23);
+}
+
+template <int kRowsEach>
+__global__ void __launch_bounds__(256) kv_widen_fp8b_kernel(const PrefillArgs a, const KeyWindow win)
+{
+    constexpr int kPieces = 8 / kRowsEach;               // CTAs' steps a tile
+    static_assert(kPieces == 1 || kPieces == 4, "a tile's word has a byte a piece");
+    const int tid = threadIdx.x;
+    const int part = tid & 15;                           // dims 8 part .. 8 part + 7
+    grid_wait();
+    const long long cap_tiles = a.rows_cap / kKeys;
+    const int *off = a.tile_off;
+    const int tiles = static_cast<int>(min(static_cast<long long>(off[a.batch]), cap_tiles));
+    for (int piece = blockIdx.x; piece < tiles * kPieces; piece += gridDim.x) {
+        const int tile = piece / kPieces, first = (piece % kPieces) * 16 * kRowsEach + (tid >> 4);   // first row
+        int lo = 0, hi = a.batch - 1;                    // the sequence whose region holds the tile
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            if (off[mid] <= tile)
+                lo = mid;
+            else
+                hi = mid - 1;
+        }
+        const int b = lo, off0 = off[b], off1 = off[b + 1];
+        if (off1 > cap_tiles)
+            continue;                                    // region past the workspace: flagged above
+        const int L = __ldg(a.seq_lens + b), lp = seq_page_log2(a, b);
+        const KeyTiles kt = key_tiles<true>(win, L - (__ldg(a.cu_q + b + 1) - __ldg(a.cu_q + b)));
+        const int per_head = (off1 - off0) / a.hkv;
+        const int h = (tile - off0) / per_head, vt = (tile - off0) - h * per_head;
+        const int key0 = (vt < kt.first ? vt : vt + kt.skip) * kKeys;
+        const int ref = __float_as_int(a.v_refs[b * a.hkv + h]) >> 23;
+        uint2 kc[kRowsEach], vc[kRowsEach];
+        float ks[kRowsEach], vs[kRowsEach];
+        uint32_t nans[kRowsEach];                        // V's, 8 bits a row
+        bool some = false;
+#pragma unroll
+        for (int i = 0; i < kRowsEach; ++i) {
+            const int t = key0 + first + 16 * i;
+            kc[i] = vc[i] = make_uint2(0u, 0u);
+            ks[i] = vs[i] = 0.f;
+            if (t < L && (t < kt.sinks || t >= kt.from)) {
+                int pg, row;
+                if (seq_token_page(a, b, lp, t, pg, row)) {
+                    const int64_t at = (static_cast<int64_t>(pg) * a.hkv + h) * a.page_size + row;
+                    kc[i] = __ldg(reinterpret_cast<const uint2 *>(a.k_cache + at * kHeadDim) + part);
+                    vc[i] = __ldg(reinterpret_cast<const uint2 *>(a.v_cache + at * kHeadDim) + part);
+                    ks[i] = scale_of(__ldg(a.k_exp + at / kBlock));
+                    vs[i] = __int_as_float(max(static_cast<int>(__ldg(a.v_exp + at / kBlock)) - ref + 127, 1) << 23);
+                } else if (part == 0 && a.err) {
+                    atomicOr(a.err, PKV_DEVERR_PAGE);
+                }
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < kRowsEach; ++i) {
+            const int64_t at = (static_cast<int64_t>(tile) * kKeys + first + 16 * i) * kHeadDim + 8 * part;
+            const uint32_t n0 = __vcmpeq4(vc[i].x & 0x7F7F7F7Fu, 0x7F7F7F7Fu), n1 = __vcmpeq4(vc[i].y & 0x7F7F7F7Fu, 0x7F7F7F7Fu);
+            nans[i] = 0;
+            if ((n0 | n1) != 0) {
+                vc[i].x &= ~n0;
+                vc[i].y &= ~n1;
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    nans[i] |= ((n0 >> (8 * e)) & 1u) << e | ((n1 >> (8 * e)) & 1u) << (4 + e);
+                some = true;
+            }
+            uint32_t k[4], v[4];
+            e4m3x4_to_f16x4(kc[i].x, k[0], k[1]);
+            e4m3x4_to_f16x4(kc[i].y, k[2], k[3]);
+            e4m3x4_to_f16x4(vc[i].x, v[0], v[1]);
+            e4m3x4_to_f16x4(vc[i].y, v[2], v[3]);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const float2 kf = f16x2_to_f32x2(k[e]), vf = f16x2_to_f32x2(v[e]);
+                const __nv_bfloat162 kb = __floats2bfloat162_rn(kf.x * ks[i], kf.y * ks[i]);
+                k[e] = *reinterpret_cast<const uint32_t *>(&kb);
+                v[e] = f32x2_to_f16x2(vf.x * vs[i], vf.y * vs[i]);
+            }
+            *reinterpret_cast<uint4 *>(a.k16 + at) = make_uint4(k[0], k[1], k[2], k[3]);
+            *reinterpret_cast<uint4 *>(a.v16 + at) = make_uint4(v[0], v[1], v[2], v[3]);
+        }
+        const bool any = __syncthreads_or(some) != 0;
+        if (tid == 0) {
+            if (kPieces == 1)
+                nan_tiles(a)[tile] = any ? 0x01010101u : 0u;
+            else
+                reinterpret_cast<uint8_t *>(nan_tiles(a) + tile)[piece % kPieces] = any;
+        }
+        if (any) {
+#pragma unroll
+            for (int i = 0; i < kRowsEach; ++i)
+                nan_rows(a)[(static_cast<int64_t>(tile) * kKeys + first + 16 * i) * 16 + part] = static_cast<uint8_t>(nans[i]);
+        }
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_widen_fp8b(const PrefillArgs &a, const KeyWindow &win, cudaStream_t stream)
+{
+    // (clusters pay from a few thousand tokens on)
+    const int ctas = a.max_kv_len <= 4096 ? 1 : kRefCtas;
+    const cudaError_t e = launch_with(kv_refs_fp8b_kernel, dim3(static_cast<unsigned>((a.batch + 1) * ctas)), kRefThreads,
+                                      static_cast<size_t>(a.hkv) * sizeof(int), ctas, false, stream, a, win, ctas);
+    if (e != cudaSuccess)
+        return e;
+    const int64_t tiles = a.rows_cap / kKeys, most = static_cast<int64_t>(device_sm_count()) * 8;
+    if (tiles * 4 <= most)
+        return launch_with(kv_widen_fp8b_kernel<2>, dim3(static_cast<unsigned>(tiles < 1 ? 1 : tiles * 4)), 256, 0, 1, true,
+                           stream, a, win);
+    return launch_with(kv_widen_fp8b_kernel<8>, dim3(static_cast<unsigned>(tiles < most ? tiles : most)), 256, 0, 1, true,
+                       stream, a, win);
+}
+
+}  // namespace pkv
