@@ -76,6 +76,15 @@ EncodeTiledFn encode_fn()
     return g_encode;
 }
 
+}  // namespace
+
+pkv_status cuda_failed(cudaError_t e, const char *site)
+{
+    t_last_cuda = e == cudaSuccess ? static_cast<int>(cudaErrorUnknown) : static_cast<int>(e);
+    t_last_site = site;
+    return PKV_ERR_CUDA;
+}
+
 // A pool [num_pages][hkv][P][128] bytes seen as a 3-D tensor (128 bytes, P rows,
 // num_pages*hkv tiles); one box = 16 rows (one chunk) of one page of one kv
 // head, 128-byte swizzled.
@@ -92,15 +101,6 @@ bool make_page_map(CUtensorMap *tm, const uint8_t *pool, int64_t num_pages, int 
     return fn(tm, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<uint8_t *>(pool), dims, strides, box, estr,
               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
-}  // namespace
-
-pkv_status cuda_failed(cudaError_t e, const char *site)
-{
-    t_last_cuda = e == cudaSuccess ? static_cast<int>(cudaErrorUnknown) : static_cast<int>(e);
-    t_last_site = site;
-    return PKV_ERR_CUDA;
 }
 
 // Queries [total_q][hq][128] bf16 as a 3-D tensor (128 dims, hq heads, total_q

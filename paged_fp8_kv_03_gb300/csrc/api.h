@@ -75,6 +75,9 @@ int withheld_load();
 // failure.
 int resident_ctas(const void *kernel, int threads, size_t smem, int max_ctas);
 
+// Tensor map of an FP8 pool: a box is 16 rows of a page of a kv head, 128-byte swizzled.
+bool make_page_map(CUtensorMap *tm, const uint8_t *pool, int64_t num_pages, int hkv, int P);
+
 // Tensor maps of the prefill's query rows and of its 16-bit copies.
 bool make_q_map(CUtensorMap *tm, const void *q, int total_q, int hq, int group, int tpt);
 bool make_kv16_map(CUtensorMap *tm, const void *base, long long rows, CUtensorMapDataType dtype);

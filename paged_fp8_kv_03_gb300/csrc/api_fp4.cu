@@ -43,16 +43,6 @@ int decode_ctas(int batch, int max_ctas)
     return two < one ? two : one;
 }
 
-// Workspace: the segments' first and last workers, the workers' cut segments, then one state a worker
-// and one a segment (a piece's slot is worker + rank of its segment, distinct
-// because both grow along the list).
-size_t decode_workspace(int batch, int hq, int hkv, int ctas)
-{
-    const size_t slots = static_cast<size_t>(ctas) * kFp4DecodeWorkers + static_cast<size_t>(batch) * hkv;
-    const size_t bytes = slots * static_cast<size_t>(hq / hkv) * kPartialStride * sizeof(float);
-    return decode_fp4_join_bytes(batch, hkv, ctas) + ((bytes + 255) & ~size_t(255));
-}
-
 }  // namespace
 
 extern "C" {
@@ -102,7 +92,7 @@ size_t pkv_decode_fp4_workspace_size(int batch, int num_q_heads, int num_kv_head
         max_seq_len < 0 || max_ctas < 0)
         return 0;
     const int ctas = decode_ctas(batch, max_ctas);
-    return ctas <= 0 ? 0 : decode_workspace(batch, num_q_heads, num_kv_heads, ctas);
+    return ctas <= 0 ? 0 : split_workspace(batch, num_q_heads, num_kv_heads, ctas);
 }
 
 pkv_status pkv_paged_gqa_decode_fp4(const void *q, const uint8_t *k_cache, const uint8_t *v_cache,
@@ -168,9 +158,9 @@ pkv_status pkv_paged_gqa_decode_fp4(const void *q, const uint8_t *k_cache, const
     int ctas = decode_ctas(batch, max_ctas);
     if (ctas <= 0)
         return PKV_ERR_CUDA;                             // resident_ctas recorded the failing call
-    if (workspace_bytes < decode_workspace(batch, num_q_heads, num_kv_heads, ctas))
+    if (workspace_bytes < split_workspace(batch, num_q_heads, num_kv_heads, ctas))
         return PKV_ERR_WORKSPACE;
-    Fp4DecodeArgs da;
+    SplitArgs da;
     da.a = a;
     da.cluster = 0;
     if (max_ctas == 0) {
@@ -183,7 +173,7 @@ pkv_status pkv_paged_gqa_decode_fp4(const void *q, const uint8_t *k_cache, const
     if (units < ctas)
         ctas = static_cast<int>(units > 0 ? units : 1);
     da.joins = static_cast<int2 *>(workspace);
-    const size_t joins = decode_fp4_join_bytes(batch, num_kv_heads, ctas);
+    const size_t joins = split_join_bytes(batch, num_kv_heads, ctas);
     da.firsts = reinterpret_cast<int *>(da.joins + static_cast<size_t>(batch) * num_kv_heads);
     da.partials = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + joins);
     da.num_slots = static_cast<long long>((workspace_bytes - joins) / (sizeof(float) * a.group * kPartialStride));

@@ -33,6 +33,16 @@ pkv_status rows_args(Fp8bRowArgs &a, const void *k, const void *v, int64_t num_t
     return PKV_OK;
 }
 
+// CTAs of the decode grid (of the kernel with one part a weight and of that
+// with two, whichever has fewer resident).
+int decode_ctas(int batch, int max_ctas)
+{
+    const size_t smem = decode_fp8b_smem(batch);
+    const int one = resident_ctas(decode_fp8b_kernel(false, false), decode_fp8b_threads(false), smem, max_ctas);
+    const int two = one <= 0 ? 0 : resident_ctas(decode_fp8b_kernel(true, false), decode_fp8b_threads(false), smem, max_ctas);
+    return two < one ? two : one;
+}
+
 }  // namespace
 
 extern "C" {
@@ -81,7 +91,8 @@ size_t pkv_decode_fp8b_workspace_size(int batch, int num_q_heads, int num_kv_hea
     if (check_decode_shape(batch, num_q_heads, num_kv_heads, head_dim, page_size, 1, 1) != PKV_OK ||
         max_seq_len < 0 || max_ctas < 0)
         return 0;
-    return 256;
+    const int ctas = decode_ctas(batch, max_ctas);
+    return ctas <= 0 ? 0 : split_workspace(batch, num_q_heads, num_kv_heads, ctas);
 }
 
 pkv_status pkv_paged_gqa_decode_fp8b(const void *q, const uint8_t *k_cache, const uint8_t *v_cache,
@@ -134,10 +145,44 @@ pkv_status pkv_paged_gqa_decode_fp8b(const void *q, const uint8_t *k_cache, cons
     a.err = device_error;
     da.k_exp = k_exp;
     da.v_exp = v_exp;
-    if (workspace_bytes < 256)
+    // Units of 32 tokens that the longest sequence can show; a list with fewer
+    // units than the device has workers needs no more CTAs than it has units.
+    long long tiles = (max_len + 15) / 16;
+    if (a.win.window > 0) {
+        const long long seen = (static_cast<long long>(sinks) + 15) / 16 + (static_cast<long long>(window) + 15) / 16 + 1;
+        tiles = seen < tiles ? seen : tiles;
+    }
+    const long long units = (tiles + 1) / 2 * batch * num_kv_heads;
+    if (units + static_cast<int64_t>(batch) * num_kv_heads >= (int64_t(1) << 31))
+        return PKV_ERR_UNSUPPORTED;
+    int ctas = decode_ctas(batch, max_ctas);
+    if (ctas <= 0)
+        return PKV_ERR_CUDA;                             // resident_ctas recorded the failing call
+    if (workspace_bytes < split_workspace(batch, num_q_heads, num_kv_heads, ctas))
         return PKV_ERR_WORKSPACE;
-    const cudaError_t e = launch_paged_decode_fp8b(da, stream);
-    return e == cudaSuccess ? PKV_OK : cuda_failed(e, "block-scaled decode kernel launch");
+    if (max_ctas == 0) {
+        const int slots = resident_ctas(decode_fp8b_kernel(a.out_f32, true), decode_fp8b_threads(true),
+                                        decode_fp8b_cluster_smem(), 0);
+        if (slots <= 0)
+            return PKV_ERR_CUDA;
+        da.cluster = decode_fp8b_cluster((tiles + 1) / 2, static_cast<long long>(batch) * num_kv_heads, slots);
+    }
+    if (units < ctas)
+        ctas = static_cast<int>(units > 0 ? units : 1);
+    da.joins = static_cast<int2 *>(workspace);
+    const size_t joins = split_join_bytes(batch, num_kv_heads, ctas);
+    da.firsts = reinterpret_cast<int *>(da.joins + static_cast<size_t>(batch) * num_kv_heads);
+    da.partials = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + joins);
+    da.num_slots = static_cast<long long>((workspace_bytes - joins) / (sizeof(float) * a.group * kPartialStride));
+    da.withhold = withheld_load();
+    alignas(64) CUtensorMap tm_k;
+    alignas(64) CUtensorMap tm_v;
+    if (!make_page_map(&tm_k, k_cache, num_pages, num_kv_heads, page_size) ||
+        !make_page_map(&tm_v, v_cache, num_pages, num_kv_heads, page_size))
+        return cuda_failed(cudaErrorInvalidValue, "cuTensorMapEncodeTiled (page pools)");
+    const char *site = "";
+    const cudaError_t e = launch_paged_decode_fp8b(da, tm_k, tm_v, ctas, stream, &site);
+    return e == cudaSuccess ? PKV_OK : cuda_failed(e, site);
 }
 
 size_t pkv_prefill_fp8b_workspace_size(int batch, int num_kv_heads, int max_q_len, int max_kv_len,

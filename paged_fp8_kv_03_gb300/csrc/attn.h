@@ -34,6 +34,38 @@ struct CacheAttnArgs {
     int32_t *err;
 };
 
+// Decode over a list of units: workers of the split (warps) a CTA, and what the
+// kernels get.
+constexpr int kSplitWarps = 4;
+
+struct SplitArgs {
+    CacheAttnArgs a;
+    int2 *joins;                                           // [batch * hkv]: workers of the segment's first and last
+                                                           // piece; x = -1: nothing to join
+    int *firsts;                                           // [workers]: the segment that a worker's range begins and
+                                                           // does not end; -1: none
+    float *partials;                                       // [num_slots][group][kPartialStride]
+    long long num_slots;
+    int cluster;                                           // CTAs a segment; 0: one list for all segments
+    int withhold;                                          // failure-detection test hook (-1 = off)
+};
+
+// Workspace: the segments' first and last workers, the workers' cut segments, then one
+// state a worker and one a segment (a piece's slot is worker + rank of its segment,
+// distinct because both grow along the list).
+inline size_t split_join_bytes(int batch, int hkv, int ctas)
+{
+    return (static_cast<size_t>(batch) * hkv * sizeof(int2) + static_cast<size_t>(ctas) * kSplitWarps * sizeof(int) + 255) &
+           ~size_t(255);
+}
+
+inline size_t split_workspace(int batch, int hq, int hkv, int ctas)
+{
+    const size_t slots = static_cast<size_t>(ctas) * kSplitWarps + static_cast<size_t>(batch) * hkv;
+    const size_t bytes = slots * static_cast<size_t>(hq / hkv) * kPartialStride * sizeof(float);
+    return split_join_bytes(batch, hkv, ctas) + ((bytes + 255) & ~size_t(255));
+}
+
 // Rows of the 16-bit copies that prefill with a window can need.  Under a
 // window a chunk of n queries sees the sinks and the n + window - 1 keys
 // before its end, which touch at most (n + window - 2) / 128 + 2 tiles.

@@ -50,7 +50,7 @@
 #include <math.h>
 
 #include "fp4.cuh"
-#include "split.cuh"
+#include "list.cuh"
 
 namespace pkv {
 
@@ -81,14 +81,13 @@ constexpr int kFoldUnits = kParts == 1 ? 512 : 16;
 // The list's kernel: every warp is a worker with its own ring, whose stages are
 // filled and waited for in pairs (one by one, the copies' issue and the waits cost
 // 4% more of the whole).
-constexpr int kListWarps = kFp4DecodeWorkers, kListThreads = 32 * kListWarps, kListCtas = 3, kStages = 4;
+constexpr int kListWarps = kSplitWarps, kListThreads = 32 * kListWarps, kListCtas = 3, kStages = 4;
 struct ListSmem {                                          // the rings, [warps][kStages][kUnitBytes], come first
     static constexpr int kFull = kListWarps * kStages * kUnitBytes;
     static constexpr int kFlag = kFull + kListWarps * kStages * 8;
     static constexpr int kSums = kFlag + 16;
     static constexpr int kHow = kSums + 16;                // int [warps]: slot of the CTA's one state, or one of
     static constexpr int kStart = kHow + 16;               // these; int [batch + 1]
-    enum { SPREAD = -1, ADJACENT = -2 };
     static size_t bytes(int batch) { return static_cast<size_t>(kStart) + 4u * (batch + 1); }
 };
 
@@ -385,45 +384,8 @@ __device__ __forceinline__ void zero_tile(uint32_t st, int j, int lane)
 }
 
 // ---------------------------------------------------------------------- the list
-__device__ __forceinline__ float *warp_state(uint8_t *smem, int warp)
-{
-    return reinterpret_cast<float *>(smem + warp * kStages * kUnitBytes);
-}
-
-// Joins the states of a CTA's warps, whose ranges all lie within one segment,
-// into one (out: [group][kPartialStride]).  Out of line, for the loop above it (in
-// line, the mixed batch takes 0.5% longer).
-__device__ __noinline__ void join_warps(float *out, int group, uint8_t *smem, int warp, int lane)
-{
-    for (int g = warp; g < group; g += kListWarps) {
-        float m[kListWarps], l[kListWarps], M = -INFINITY, L = 0.f;
-        float4 A = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-        for (int w = 0; w < kListWarps; ++w) {
-            const float2 ml = *reinterpret_cast<const float2 *>(warp_state(smem, w) + g * kPartialStride + kHeadDim);
-            m[w] = ml.x;
-            l[w] = ml.y;
-            M = fmaxf(M, ml.x);
-        }
-#pragma unroll
-        for (int w = 0; w < kListWarps; ++w) {
-            const float e = ex2_approx(m[w] - M);
-            const float4 v = *reinterpret_cast<const float4 *>(warp_state(smem, w) + g * kPartialStride + 4 * lane);
-            L += e * l[w];
-            A.x += e * v.x;
-            A.y += e * v.y;
-            A.z += e * v.z;
-            A.w += e * v.w;
-        }
-        float *row = out + g * kPartialStride;
-        *reinterpret_cast<float4 *>(row + 4 * lane) = A;
-        if (lane == 0)
-            *reinterpret_cast<float2 *>(row + kHeadDim) = make_float2(M, L);
-    }
-}
-
 template <int kParts>
-__device__ __forceinline__ void work_list(const Fp4DecodeArgs &da, uint8_t *smem, int warp, int lane, int worker, int lo,
+__device__ __forceinline__ void work_list(const SplitArgs &da, uint8_t *smem, int warp, int lane, int worker, int lo,
                                           int n)
 {
     const CacheAttnArgs &a = da.a;
@@ -491,7 +453,7 @@ __device__ __forceinline__ void work_list(const Fp4DecodeArgs &da, uint8_t *smem
             if (p.unit == 0 && !whole)
                 da.firsts[worker] = p.b * a.hkv + p.h;
             if (p.unit + take == units)
-                j->y = how() == ListSmem::SPREAD ? worker : ~worker;
+                j->y = how() == ListRange::SPREAD ? worker : ~worker;
         }
         Query qu;
         {
@@ -589,7 +551,7 @@ __device__ __forceinline__ void work_list(const Fp4DecodeArgs &da, uint8_t *smem
                     v[k] *= f;
                 store16(a, row0 + g, 16 * r, v);
             } else if (how() >= 0) {                       // over the ring, which nothing more is brought into
-                store_state(warp_state(smem, warp) + g * kPartialStride, s, l, j, r);
+                store_state(reinterpret_cast<float *>(smem + warp * kStages * kUnitBytes) + g * kPartialStride, s, l, j, r);
             } else if (slot < da.num_slots) {
                 store_state(da.partials + (slot * a.group + g) * kPartialStride, s, l, j, r);
             } else if (a.err && r == 0) {
@@ -609,7 +571,7 @@ __device__ __forceinline__ void work_list(const Fp4DecodeArgs &da, uint8_t *smem
 }
 
 template <int kParts>
-__global__ void __launch_bounds__(kListThreads, kListCtas) paged_gqa_decode_fp4_kernel(const Fp4DecodeArgs da)
+__global__ void __launch_bounds__(kListThreads, kListCtas) paged_gqa_decode_fp4_kernel(const SplitArgs da)
 {
     const CacheAttnArgs &a = da.a;
     extern __shared__ __align__(128) uint8_t smem[];
@@ -617,109 +579,27 @@ __global__ void __launch_bounds__(kListThreads, kListCtas) paged_gqa_decode_fp4_
     int *start = reinterpret_cast<int *>(smem + ListSmem::kStart);
     int *sums = reinterpret_cast<int *>(smem + ListSmem::kSums);
 
-    bool no_empty;
-    // ---- first unit of every sequence (of one kv head): a prefix sum over the batch
-    {
-        const int per = (a.batch + kListThreads - 1) / kListThreads;
-        const int b0 = min(a.batch, tid * per), b1 = min(a.batch, b0 + per);
-        int mine = 0;
-        for (int b = b0; b < b1; ++b)
-            mine += (sight_of(a, b).tiles + 1) >> 1;
-        int incl = mine;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int v = __shfl_up_sync(kEvery, incl, o);
-            if (lane >= o)
-                incl += v;
-        }
-        if (lane == 31)
-            sums[warp] = incl;
-        if (tid == 0) {
-            *reinterpret_cast<volatile int *>(smem + ListSmem::kFlag) = 0;
-            const uint32_t bars = smem_addr(smem) + ListSmem::kFull;
-            for (int i = 0; i < kListWarps * kStages; ++i)
-                mbar_init(bars + 8 * i, 1);
-            fence_barrier_init();
-        }
-        __syncthreads();
-        int run = incl - mine;
-        for (int w = 0; w < warp; ++w)
-            run += sums[w];
-        for (int b = b0; b < b1; ++b) {
-            const Sight s = sight_of(a, b);
-            start[b] = run;
-            run += (s.tiles + 1) >> 1;
-            if (blockIdx.x == 0)
-                flag_sequence(a, b, s);
-        }
-        if (tid == kListThreads - 1)
-            start[a.batch] = run;
-        bool some = true;                                  // this thread's sequences all have tokens
-        for (int b = b0; b < b1; ++b)
-            some = some && (b + 1 < b1 ? start[b + 1] : run) > start[b];
-        no_empty = __syncthreads_and(some) != 0;
-    }
-
-    // ---- sequences with no tokens: zero rows, and nothing to join
-    for (int sg = blockIdx.x; sg < a.batch * a.hkv; sg += gridDim.x) {
-        const int b = sg / a.hkv;
-        if (start[b + 1] == start[b]) {
-            const int64_t row0 = static_cast<int64_t>(b) * a.hq + static_cast<int64_t>(sg % a.hkv) * a.group;
-            for (int e = tid; e < a.group * kHeadDim; e += kListThreads) {
-                if (a.out_f32)
-                    static_cast<float *>(a.out)[row0 * kHeadDim + e] = 0.f;
-                else
-                    static_cast<__nv_bfloat16 *>(a.out)[row0 * kHeadDim + e] = __float2bfloat16_rn(0.f);
-            }
-            if (tid == 0)
-                da.joins[sg] = make_int2(-1, -1);
-        }
-    }
+    const bool no_empty = list_starts<kListWarps>(a, start, sums, [&]() {
+        *reinterpret_cast<volatile int *>(smem + ListSmem::kFlag) = 0;
+        const uint32_t bars = smem_addr(smem) + ListSmem::kFull;
+        for (int i = 0; i < kListWarps * kStages; ++i)
+            mbar_init(bars + 8 * i, 1);
+        fence_barrier_init();
+    });
+    zero_rows<kListThreads>(da, start);
     launch_dependents();
 
-    const int total = start[a.batch] * a.hkv;
-    const int active = min(static_cast<int>(gridDim.x) * kListWarps, total);
-    // A CTA's warps take adjacent ranges, so that those within a segment leave one
-    // state for the join (32 query heads, one 32K sequence 16.8 us, with a state a warp
-    // 18.2; a 128K one among 63 of 512 tokens 46.0 and 57.8; 32 x 4K 34.2 and 33.8).  The
-    // ranges of a list shorter than the workers spread over the CTAs.
-    const bool adjacent = total >= static_cast<int>(gridDim.x) * kListWarps;
-    const int worker = adjacent ? static_cast<int>(blockIdx.x) * kListWarps + warp
-                                : warp * static_cast<int>(gridDim.x) + static_cast<int>(blockIdx.x);
-    if (lane == 0)
-        da.firsts[worker] = -1;
-    if (worker < active) {
-        // A range with a segment's end in it has one more piece to set up and to
-        // store, which costs about a unit's time: the ranges are equal in a list
-        // with an empty unit after every segment.  (Two units a range, and no
-        // empty sequence: then every range still holds a unit, as the join needs.)
-        const bool wide = no_empty && total >= 2 * active;
-        const int length = total + (wide ? a.batch * a.hkv : 0);
-        const int each = length / active, more = length - each * active;   // the first `more` ranges: one longer
-        // lanes 4i, 4i + 1: where the range begins and ends; 4i + 2, 4i + 3: the CTA's ranges
-        const int w = (lane & 2 ? worker - warp : worker) + (lane & 1) * (lane & 2 ? kListWarps : 1);
-        int edge = w * each + min(w, more);
-        if (wide)
-            edge = real_position(start, a.batch, a.hkv, edge);
-        const int lo = __shfl_sync(kEvery, edge, 0), n = __shfl_sync(kEvery, edge, 1) - lo;
+    const ListRange range = list_range<kListWarps>(da, start, no_empty, warp, lane);
+    if (range.on) {
         volatile int *how = reinterpret_cast<volatile int *>(smem + ListSmem::kHow + 4 * warp);
-        {
-            const int first = __shfl_sync(kEvery, edge, 2), last = __shfl_sync(kEvery, edge, 3);
-            int h = ListSmem::SPREAD;
-            if (adjacent) {
-                const Place p = place_of(start, a.batch, first);
-                const bool within = p.unit > 0 && last - first < start[p.b + 1] - start[p.b] - p.unit;
-                h = within ? worker - warp + p.h * a.batch + p.b : static_cast<int>(ListSmem::ADJACENT);
-            }
-            if (lane == 0)
-                *how = h;
-            __syncwarp();
-        }
-        work_list<kParts>(da, smem, warp, lane, worker, lo, n);
+        if (lane == 0)
+            *how = range.how;
+        __syncwarp();
+        work_list<kParts>(da, smem, warp, lane, range.worker, range.lo, range.n);
         if (*how >= 0) {                                   // the segment begins before and ends behind the CTA's ranges
             __syncthreads();
             if (*how < da.num_slots)
-                join_warps(da.partials + static_cast<int64_t>(*how) * a.group * kPartialStride, a.group, smem, warp, lane);
+                join_warps<false, kListWarps, kStages * kUnitBytes>(da.partials + static_cast<int64_t>(*how) * a.group * kPartialStride, a.group, smem, warp, lane);
             else if (a.err && lane == 0)
                 atomicOr(a.err, PKV_DEVERR_INTERNAL);
         }
@@ -731,7 +611,7 @@ __global__ void __launch_bounds__(kListThreads, kListCtas) paged_gqa_decode_fp4_
 // units evenly (at most kClusterUnits each, all brought in at once), leave their
 // states in shared memory and join them there.
 template <int kParts>
-__global__ void __launch_bounds__(32 * kClusterWarps, 2) paged_gqa_decode_fp4_cluster_kernel(const Fp4DecodeArgs da)
+__global__ void __launch_bounds__(32 * kClusterWarps, 2) paged_gqa_decode_fp4_cluster_kernel(const SplitArgs da)
 {
     using S = ClusterSmem;
     const CacheAttnArgs &a = da.a;
@@ -874,129 +754,6 @@ __global__ void __launch_bounds__(32 * kClusterWarps, 2) paged_gqa_decode_fp4_cl
     cluster_sync(da.cluster);                              // no CTA leaves while its states are read
 }
 
-// Joins the states of a segment's pieces for one query head, in worker order:
-// out = v_scale sum_i 2^(m_i - M) A_i / sum_i 2^(m_i - M) l_i.  Warps take the
-// pieces in turns, all of a turn's loads in flight together, and are joined in warp
-// order.  A turn is a round trip to the L2, so turns are long and, with a CTA a
-// (segment, head), up to 16 warps share them (32 query heads, a 128K sequence among 63
-// of 512 tokens 46.0 us, with 8 states and 8 warps 48.3; one 128K sequence alone 34.0 and
-// 33.3).  Warps are as few as an average segment needs, because a CTA of one or two is
-// on its SM before the list's CTAs have left it (64 x 2K tokens 35.0 us, with four at
-// least 39.0; 32 x 4K 34.2 and 36.0; the long one among short ones 46.0 and 43.7).
-constexpr int kJoin = 16, kJoinWarps = 16;
-constexpr int kJoinCut = 8;
-
-// Head g of segment sg, by `warps` warps of the CTA (ra, rm: theirs), kTurn pieces
-// a turn.
-template <int kTurn>
-__device__ __forceinline__ void join_head(const Fp4DecodeArgs &da, int sg, int g, int warp, int warps, int lane,
-                                          float (*ra)[kHeadDim], float2 *rm)
-{
-    const CacheAttnArgs &a = da.a;
-    const int b = sg / a.hkv, h = sg % a.hkv;
-    const float vs = __ldg(a.v_scale + h);
-    int2 j = da.joins[sg];
-    if (j.x < 0)
-        return;
-    // Of the workers x .. y, the CTAs strictly between have left one state, in the first
-    // of their slots (y = ~the last worker; else every worker has its own).
-    int head = 0, full = 0;
-    if (j.y < 0) {
-        j.y = ~j.y;
-        head = kListWarps - j.x % kListWarps;
-        full = max(0, j.y / kListWarps - 1 - j.x / kListWarps);
-    }
-    const int64_t slot0 = static_cast<int64_t>(j.x) + h * a.batch + b;
-    if (j.y < j.x || slot0 + (j.y - j.x) >= da.num_slots)
-        return;                                            // an aborted call, or flagged by the decode kernel
-    const int pieces = j.y - j.x + 1 - (kListWarps - 1) * full;
-    auto worker = [&](int i) {                             // beyond x
-        return i < head || full == 0 ? i : (i < head + full ? head + kListWarps * (i - head) : i + (kListWarps - 1) * full);
-    };
-    const float *base = da.partials + (slot0 * a.group + g) * kPartialStride;
-    const int64_t stride = static_cast<int64_t>(a.group) * kPartialStride;
-    float M = -INFINITY, L = 0.f;
-    float4 A = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int i0 = warp * kTurn; i0 < pieces; i0 += warps * kTurn) {
-        float4 v[kTurn];
-        float2 ml[kTurn];
-#pragma unroll
-        for (int i = 0; i < kTurn; ++i) {
-            const bool on = i0 + i < pieces;
-            const float *s = base + (on ? worker(i0 + i) : 0) * stride;
-            ml[i] = on ? *reinterpret_cast<const float2 *>(s + kHeadDim) : make_float2(-INFINITY, 0.f);
-            v[i] = on ? *reinterpret_cast<const float4 *>(s + 4 * lane) : make_float4(0.f, 0.f, 0.f, 0.f);
-        }
-        float mn = M;
-#pragma unroll
-        for (int i = 0; i < kTurn; ++i)
-            mn = fmaxf(mn, ml[i].x);
-        const float f = ex2_approx(M - mn);
-        M = mn;
-        L *= f;
-        A = make_float4(A.x * f, A.y * f, A.z * f, A.w * f);
-#pragma unroll
-        for (int i = 0; i < kTurn; ++i) {
-            const float e = i0 + i < pieces ? ex2_approx(ml[i].x - mn) : 0.f;
-            L += e * ml[i].y;
-            A.x += e * v[i].x;
-            A.y += e * v[i].y;
-            A.z += e * v[i].z;
-            A.w += e * v[i].w;
-        }
-    }
-    if (warps > 1) {
-        *reinterpret_cast<float4 *>(&ra[warp][4 * lane]) = A;
-        if (lane == 0)
-            rm[warp] = make_float2(M, L);
-        __syncthreads();
-        if (warp != 0)
-            return;
-        float mn = M;
-        for (int w = 1; w < warps; ++w)
-            mn = fmaxf(mn, rm[w].x);
-        L = 0.f;
-        A = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int w = 0; w < warps; ++w) {
-            if (w * kTurn >= pieces)
-                break;                                     // a warp with no pieces
-            const float e = ex2_approx(rm[w].x - mn);
-            const float4 v = *reinterpret_cast<const float4 *>(&ra[w][4 * lane]);
-            L += e * rm[w].y;
-            A.x += e * v.x;
-            A.y += e * v.y;
-            A.z += e * v.z;
-            A.w += e * v.w;
-        }
-    }
-    const float f = vs / L;
-    store4(a, static_cast<int64_t>(b) * a.hq + static_cast<int64_t>(h) * a.group + g, 4 * lane,
-           make_float4(A.x * f, A.y * f, A.z * f, A.w * f));
-}
-
-__global__ void __launch_bounds__(32 * kJoinWarps) join_fp4_kernel(const Fp4DecodeArgs da)
-{
-    __shared__ __align__(16) float ra[kJoinWarps][kHeadDim];
-    __shared__ float2 rm[kJoinWarps];
-    grid_wait();
-    join_head<kJoin>(da, blockIdx.x / da.a.group, blockIdx.x % da.a.group, threadIdx.x >> 5, blockDim.x >> 5,
-                     threadIdx.x & 31, ra, rm);
-}
-
-// The same for lists of many segments, of which at most one a worker is cut: a CTA a
-// worker, for the segment that its range begins and does not end; a warp a head.  A
-// CTA a (segment, head) is what such lists spend their time on: 64 query heads, 512 x
-// 128 tokens 43 us, this way 31; 1024 x 128 84 and 55; 128 x 512 29.4 and 26.8; 64 x
-// 1024 25.2 and 24.6.  With few segments it is the slower one (32 query heads, 64 x 2048: 35.4,
-// 35.1; 16 x 4096: 22.7, 21.7), as long segments have more pieces than a warp's turn.
-__global__ void __launch_bounds__(32 * PKV_MAX_GROUP) join_cut_fp4_kernel(const Fp4DecodeArgs da)
-{
-    grid_wait();
-    const int sg = da.firsts[blockIdx.x];
-    if (sg >= 0)
-        join_head<kJoinCut>(da, sg, threadIdx.x >> 5, 0, 1, threadIdx.x & 31, nullptr, nullptr);
-}
-
 }  // namespace
 
 size_t decode_fp4_smem(int batch)
@@ -1037,7 +794,7 @@ int decode_fp4_cluster(long long units, long long segments, int slots)
     return 0;
 }
 
-cudaError_t launch_paged_decode_fp4(const Fp4DecodeArgs &da, int ctas, cudaStream_t stream, const char **site)
+cudaError_t launch_paged_decode_fp4(const SplitArgs &da, int ctas, cudaStream_t stream, const char **site)
 {
     *site = "4-bit decode kernel launch";
     const bool two = da.a.out_f32;
@@ -1052,17 +809,7 @@ cudaError_t launch_paged_decode_fp4(const Fp4DecodeArgs &da, int ctas, cudaStrea
     if (e != cudaSuccess)
         return e;
     *site = "4-bit join kernel launch";
-    const long long segs = static_cast<long long>(da.a.batch) * da.a.hkv;
-    const int workers = ctas * kListWarps;
-    if (segs * da.a.group >= 2ll * workers)
-        return launch_with(join_cut_fp4_kernel, dim3(static_cast<unsigned>(workers)), 32 * da.a.group, 0, 1, true, stream,
-                           da);
-    const long long pieces = (workers + segs - 1) / segs + 1;   // a segment's, on average
-    int warps = 1;
-    while (warps < kJoinWarps && warps * kJoin < pieces)
-        warps *= 2;
-    return launch_with(join_fp4_kernel, dim3(static_cast<unsigned>(segs * da.a.group)), 32 * warps, 0, 1, true, stream,
-                       da);
+    return launch_join<false>(da, ctas, stream);
 }
 
 }  // namespace pkv

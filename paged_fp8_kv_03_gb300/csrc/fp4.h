@@ -27,27 +27,6 @@ struct Fp4RowArgs {                                        // append and read ba
     int32_t *err;
 };
 
-// Decode: workers of the split (warps) a CTA.
-constexpr int kFp4DecodeWorkers = 4;
-
-struct Fp4DecodeArgs {
-    CacheAttnArgs a;
-    int2 *joins;                                           // [batch * hkv]: workers of the segment's first and last
-                                                           // piece; x = -1: nothing to join
-    int *firsts;                                           // [workers]: the segment that a worker's range begins and
-                                                           // does not end; -1: none
-    float *partials;                                       // [num_slots][group][kPartialStride]
-    long long num_slots;
-    int cluster;                                           // CTAs a segment; 0: one list for all segments
-    int withhold;                                          // failure-detection test hook (-1 = off)
-};
-
-inline size_t decode_fp4_join_bytes(int batch, int hkv, int ctas)
-{
-    return (static_cast<size_t>(batch) * hkv * sizeof(int2) +
-            static_cast<size_t>(ctas) * kFp4DecodeWorkers * sizeof(int) + 255) & ~size_t(255);
-}
-
 // Prefill's workspace: laid out as pkv_paged_prefill's, then a word a
 // tile, each byte of it not zero where one of 32 V rows holds a NaN block, then a
 // byte a row, a bit a NaN block (written where the 32 rows' byte is not zero).
@@ -62,7 +41,7 @@ size_t decode_fp4_cluster_smem();
 const void *decode_fp4_kernel(bool two_parts, bool cluster);
 int decode_fp4_threads(bool cluster);
 int decode_fp4_cluster(long long units, long long segments, int slots);
-cudaError_t launch_paged_decode_fp4(const Fp4DecodeArgs &da, int ctas, cudaStream_t stream, const char **site);
+cudaError_t launch_paged_decode_fp4(const SplitArgs &da, int ctas, cudaStream_t stream, const char **site);
 cudaError_t launch_widen_fp4(const PrefillArgs &a, const KeyWindow &win, cudaStream_t stream);
 cudaError_t launch_prefill_pair(const PrefillArgs &a, const KeyWindow &win, const CUtensorMap &tm_q,
                                 const CUtensorMap &tm_k16, const CUtensorMap &tm_v16, cudaStream_t stream);

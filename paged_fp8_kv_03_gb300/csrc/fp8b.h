@@ -28,21 +28,20 @@ struct Fp8bRowArgs {                                       // append and read ba
 cudaError_t launch_kv_append_fp8b(const Fp8bRowArgs &a, bool bf16, cudaStream_t stream);
 cudaError_t launch_kv_read_fp8b(const Fp8bRowArgs &a, bool bf16, cudaStream_t stream);
 
-// Decode: workers of the split (warps) a CTA.
-constexpr int kFp8bDecodeWorkers = 4;
+// Decode: as the 4-bit cache's, and the blocks' bytes.
+constexpr int kFp8bListWarps = kSplitWarps;
 
-struct Fp8bDecodeArgs {
-    CacheAttnArgs a;                                       // (k_scale, v_scale: not used)
+struct Fp8bDecodeArgs : SplitArgs {
     const uint8_t *k_exp, *v_exp;
-    int2 *joins;                                           // as in Fp4DecodeArgs
-    int *firsts;
-    float *partials;
-    long long num_slots;
-    int cluster;
-    int withhold;
 };
 
-cudaError_t launch_paged_decode_fp8b(const Fp8bDecodeArgs &da, cudaStream_t stream);
+size_t decode_fp8b_smem(int batch);
+size_t decode_fp8b_cluster_smem();
+const void *decode_fp8b_kernel(bool two_parts, bool cluster);
+int decode_fp8b_threads(bool cluster);
+int decode_fp8b_cluster(long long units, long long segments, int slots);
+cudaError_t launch_paged_decode_fp8b(const Fp8bDecodeArgs &da, const CUtensorMap &tm_k, const CUtensorMap &tm_v, int ctas,
+                                     cudaStream_t stream, const char **site);
 
 // Prefill's workspace: the header, a float a sequence and kv head (what a value of V's
 // copy stands for), the 16-bit copies of K and V, a word a tile (as the 4-bit
