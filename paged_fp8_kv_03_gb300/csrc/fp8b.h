@@ -45,7 +45,7 @@ cudaError_t launch_paged_decode_fp8b(const Fp8bDecodeArgs &da, const CUtensorMap
 
 // Prefill's workspace: the header, a float a sequence and kv head (what a value of V's
 // copy stands for), the 16-bit copies of K and V, a word a tile (as the 4-bit
-// cache's), and 16 bytes a row, a bit a NaN of V.
+// cache's, zeros), another one, and 16 bytes a row, a bit a NaN of V.
 // (The maxima of a sequence's heads stand in shared memory.)
 constexpr int kFp8bMaxPrefillHeads = 8192;
 
@@ -58,7 +58,7 @@ inline size_t prefill_fp8b_bytes(int batch, int hkv, long long rows)
 {
     return prefill_header_bytes(batch) + prefill_fp8b_refs_bytes(batch, hkv) +
            static_cast<size_t>(rows) * (2 * kHeadDim * sizeof(__half) + kHeadDim / 8) +
-           static_cast<size_t>(rows / 128) * sizeof(uint32_t);
+           static_cast<size_t>(rows / 128) * 2 * sizeof(uint32_t);
 }
 
 cudaError_t launch_widen_fp8b(const PrefillArgs &a, const KeyWindow &win, cudaStream_t stream);

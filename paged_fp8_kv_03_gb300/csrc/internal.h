@@ -122,7 +122,8 @@ struct PrefillArgs {
     const float *k_scale, *v_scale; // [hkv] (FP8 and 4-bit caches)
     const uint8_t *k_exp, *v_exp;   // block-scaled FP8 cache: its blocks' exponents
     float *v_refs;                  // block-scaled FP8 cache: [batch][hkv] what a value of v16 stands for (caller
-                                    // workspace, written ahead of the widening); else nullptr
+                                    // workspace, written ahead of the widening, which makes it negative where V
+                                    // holds a NaN); else nullptr
     const int32_t *block_table;
     int max_pages;
     const int32_t *seq_lens;

@@ -92,9 +92,10 @@ struct PS {
     };
     static constexpr int kTmem = kBars + kNumBars * 8;
     static constexpr int kFlag = kTmem + 4;
-    static constexpr int kMoved = (kFlag + 4 + 15) / 16 * 16;   // MovedRow [2 halves][128 rows] (4-bit cache)
+    static constexpr int kFactor = kFlag + 4;              // kBlocks: its entry of v_refs
+    static constexpr int kMoved = (kFactor + 4 + 15) / 16 * 16;   // MovedRow [2 halves][128 rows] (4-bit cache)
     static constexpr int kEnd = kMoved + 2 * kRows * static_cast<int>(sizeof(MovedRow));
-    static constexpr size_t bytes(bool moves) { return static_cast<size_t>(moves ? kEnd : kFlag + 4) + 1024; }
+    static constexpr size_t bytes(bool moves) { return static_cast<size_t>(moves ? kEnd : kFactor + 4) + 1024; }
 };
 static_assert(PS::bytes(true) <= 232448, "prefill tile buffers exceed the shared memory of one CTA");
 
@@ -269,9 +270,10 @@ __device__ __noinline__ float move_out(uint32_t cm, uint32_t cs, float m, float 
 
 // kWin: the 4-bit cache's calls with a window (and an fp32 output); a row may
 // then see nothing of a tile, or of all tiles so far (its running maximum is
-// -inf until it does).  kFp4: the 4-bit cache's.  kMoves: those of long contexts,
+// -inf until it does).  kFp4: the 4-bit cache's and, with kBlocks,
+// the block-scaled FP8 cache's.  kMoves: those of long contexts,
 // whose sums move on every kMove4 key tiles.
-template <bool kWin, bool kFp4, bool kMoves>
+template <bool kWin, bool kFp4, bool kMoves, bool kBlocks>
 __global__ void __launch_bounds__(kPThreads, 1)
     paged_prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                          const __grid_constant__ CUtensorMap tm_v, const PrefillArgs a, const KeyWindow win)
@@ -349,6 +351,8 @@ __global__ void __launch_bounds__(kPThreads, 1)
         for (int i = 0; i < 4; ++i)
             mbar_init(bar(PS::LX + i), 64);
         *abort_flag = 0;
+        if (kBlocks)
+            *reinterpret_cast<volatile float *>(smem + PS::kFactor) = __ldg(a.v_refs + bh);
         fence_barrier_init();
     }
     if (warp == 1) {
@@ -489,7 +493,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
         const int g = row - tl * G;
         const bool valid = row < G * tpt && tl < nv;
         const int p_row = valid ? pos0 + tl : last;      // padding rows mirror the last row
-        const float sl2 = score_factor(a, h);
+        const float sl2 = score_factor<kBlocks>(a, h);
         const uint32_t lanes = tm + (static_cast<uint32_t>(qtr * 32) << 16);
         float *red_max = reinterpret_cast<float *>(smem + PS::kRedMax);
         float *red_l = reinterpret_cast<float *>(smem + PS::kRedL);
@@ -700,10 +704,10 @@ __global__ void __launch_bounds__(kPThreads, 1)
             ok = false;
         }
         if (ok) {
-            const float inv = value_factor(a, b, h) / (l + red_l[(half ^ 1) * kRows + row]);
+            const float inv = (kBlocks ? fabsf(*reinterpret_cast<volatile float *>(smem + PS::kFactor)) : __ldg(a.v_scale + h)) / (l + red_l[(half ^ 1) * kRows + row]);
             const int64_t orow = (static_cast<int64_t>(q0) + t0 + tl) * a.hq + h * G + g;
             uint32_t nans = 0;
-            if (kFp4 && !a.v_refs)
+            if (kFp4)
                 nans = nan_blocks<kWin>(a, win, row0 / kKeys, nt, valid ? pos0 + tl : last, lane, key_tile, copy_tile);
             const bool have_o = nt > kFold;                // at least one segment was folded into O
 #pragma unroll 1
@@ -740,9 +744,6 @@ __global__ void __launch_bounds__(kPThreads, 1)
                     }
                 }
             }
-            if (kFp4 && a.v_refs)
-                put_nans<kWin>(a, win, row0 / kKeys, nt, valid ? pos0 + tl : last, lane, key_tile, copy_tile, valid, orow,
-                               64 * half, 64);
         }
     }
 
@@ -752,10 +753,12 @@ __global__ void __launch_bounds__(kPThreads, 1)
         tc::fence_after();
         tc::tmem_dealloc(tm, 512);
     }
+    if (kBlocks && *reinterpret_cast<volatile float *>(smem + PS::kFactor) < 0.f)
+        put_nans<kWin>(a, win, 1, kPThreads);
 }
 
 std::mutex g_prefill_mu;
-unsigned long long g_prefill_attr_ctx[64][5] = {};   // per device and kernel: the context its limit was raised in
+unsigned long long g_prefill_attr_ctx[64][9] = {};   // per device and kernel: the context its limit was raised in
 
 typedef void (*PrefillKernel)(const CUtensorMap, const CUtensorMap, const CUtensorMap, const PrefillArgs,
                               const KeyWindow);
@@ -823,8 +826,8 @@ cudaError_t launch_paged_prefill(const PrefillArgs &a, const CUtensorMap &tm_q, 
     if (static_cast<int64_t>(a.batch) * a.hkv * a.max_tiles <= 0)
         return cudaSuccess;
     const KeyWindow none = {0, 0};
-    const PrefillKernel kernel = paged_prefill_kernel<false, false, false>;
-    cudaError_t e = raise_limit(kernel, 4, PS::bytes(false));
+    const PrefillKernel kernel = paged_prefill_kernel<false, false, false, false>;
+    cudaError_t e = raise_limit(kernel, 8, PS::bytes(false));
     if (e == cudaSuccess)
         e = launch_widen(a, stream);
     return e == cudaSuccess ? launch_attention(kernel, PS::bytes(false), a, none, tm_q, tm_k16, tm_v16, stream) : e;
@@ -840,12 +843,16 @@ cudaError_t launch_prefill_windowed(const PrefillArgs &a, const KeyWindow &win, 
     // instead of 1.92) or 9% (1024 of 131072: 5.26 ms instead of 4.83); up to 128 key
     // tiles l has at most 128 additions (2^-17) and O 32 without it.
     const bool moves = most_key_tiles(a, win) > 2 * kMove4;
-    const PrefillKernel kernel =
-        win.window > 0 ? (moves ? paged_prefill_kernel<true, true, true> : paged_prefill_kernel<true, true, false>)
-                       : (moves ? paged_prefill_kernel<false, true, true> : paged_prefill_kernel<false, true, false>);
+    const int which = (win.window > 0 ? 1 : 0) + (moves ? 2 : 0) + (a.v_refs ? 4 : 0);
+    static const PrefillKernel kernels[8] = {
+        paged_prefill_kernel<false, true, false, false>, paged_prefill_kernel<true, true, false, false>,
+        paged_prefill_kernel<false, true, true, false>,  paged_prefill_kernel<true, true, true, false>,
+        paged_prefill_kernel<false, true, false, true>,  paged_prefill_kernel<true, true, false, true>,
+        paged_prefill_kernel<false, true, true, true>,   paged_prefill_kernel<true, true, true, true>};
+    const PrefillKernel kernel = kernels[which];
     cudaError_t e = cudaSuccess;
     if (a.out_f32)
-        e = raise_limit(kernel, (win.window > 0 ? 1 : 0) + (moves ? 2 : 0), PS::bytes(moves));
+        e = raise_limit(kernel, which, PS::bytes(moves));
     if (e == cudaSuccess)
         e = widen(a, win, stream);
     if (e != cudaSuccess)

@@ -159,16 +159,11 @@ __device__ __forceinline__ bool sequence_ok(const PrefillArgs &a, int b, int q0,
 
 // What turns raw scores into exponents of 2.  A product too small for fp32 is its
 // smallest number instead of 0, which would make NaN of a hidden key's -inf.
+template <bool kBlocks>
 __device__ __forceinline__ float score_factor(const PrefillArgs &a, int h)
 {
-    const float f = (a.v_refs ? 1.f : __ldg(a.k_scale + h)) * a.sm_scale_log2;
+    const float f = (kBlocks ? 1.f : __ldg(a.k_scale + h)) * a.sm_scale_log2;
     return f == 0.f ? __uint_as_float(1u) : f;
-}
-
-// What a value of the 16-bit copy of V stands for.
-__device__ __forceinline__ float value_factor(const PrefillArgs &a, int b, int h)
-{
-    return a.v_refs ? __ldg(a.v_refs + b * a.hkv + h) : __ldg(a.v_scale + h);
 }
 
 // Sums over a long context are kept in levels, so that no chain of additions grows
@@ -257,48 +252,71 @@ __device__ __forceinline__ uint32_t nan_blocks(const PrefillArgs &a, const KeyWi
     return hit;
 }
 
-// The same for NaN values of the block-scaled FP8 cache's V, whose rows have 16
-// bytes, a bit a dim: puts NaNs into dims d0 .. d0 + dims - 1 of the row `orow` of
-// the output where the row at position p sees one (the whole warp; valid: the
-// lane has a row).  Out of line: it runs once a tile, and mostly finds nothing.
-template <bool kWin, typename KeyTile, typename CopyTile>
-__device__ __noinline__ void put_nans(const PrefillArgs &a, const KeyWindow &w, int tile0, int nt, int p, int lane,
-                                      KeyTile key_tile, CopyTile copy_tile, bool valid, int64_t orow, int d0, int dims)
+// The block-scaled FP8 cache's copies record single NaNs of V, behind the words above
+// (which are zeros there): a word a tile, then 16 bytes a row, a bit a dim.
+__device__ __forceinline__ uint32_t *nan_value_tiles(const PrefillArgs &a)
 {
-    const uint32_t *tiles = nan_tiles(a);
+    return nan_tiles(a) + a.rows_cap / kKeys;
+}
+
+__device__ __forceinline__ uint8_t *nan_value_rows(const PrefillArgs &a)
+{
+    return reinterpret_cast<uint8_t *>(nan_value_tiles(a) + a.rows_cap / kKeys);
+}
+
+// What they do to the outputs: puts NaNs into the output rows of a CTA's query tiles, which have
+// been written, where they see one (the whole CTA of `threads`; `tiles`: query tiles a CTA).
+// Out of line, and from the block's number on, so that the attention's loop keeps
+// nothing for it.
+template <bool kWin>
+__device__ __noinline__ void put_nans(const PrefillArgs &a, const KeyWindow &w, int tiles, int threads)
+{
+    const int per = (a.max_tiles + tiles - 1) / tiles;
+    const int bh = blockIdx.x / per, first = (per - 1 - (static_cast<int>(blockIdx.x) - bh * per)) * tiles;
+    const int b = bh / a.hkv, h = bh - b * a.hkv;
+    const int q0 = __ldg(a.cu_q + b), n = __ldg(a.cu_q + b + 1) - q0, L = __ldg(a.seq_lens + b);
+    const int off0 = __ldg(a.tile_off + b), off1 = __ldg(a.tile_off + b + 1);
+    const int t0 = first * a.tokens_per_tile, t1 = min(n, (first + tiles) * a.tokens_per_tile);   // tokens of the chunk
+    const KeyTiles seq_kt = key_tiles<kWin>(w, L - n), kt = key_tiles<kWin>(w, L - n + t0);
+    const int64_t tile0 = off0 + h * ((off1 - off0) / a.hkv);
+    const int nt = (L - n + t1 - 1) / kKeys + 1 - kt.skip;
+    auto key_tile = [&](int i) { return !kWin || i < kt.first ? i : i + kt.skip; };
+    auto copy_tile = [&](int i) {
+        const int t = key_tile(i);
+        return !kWin || t < seq_kt.first ? t : t - seq_kt.skip;
+    };
     bool some = false;
-    for (int i = lane; i < nt; i += 32)
-        some = some || __ldg(tiles + tile0 + copy_tile(i)) != 0;
-    if (!__any_sync(kAll, some))
+    for (int i = threadIdx.x; i < nt; i += threads)
+        some = some || __ldg(nan_value_tiles(a) + tile0 + copy_tile(i)) != 0;
+    if (!__syncthreads_or(some))
         return;
-    const uint32_t *rows = reinterpret_cast<const uint32_t *>(nan_rows(a));
-    uint32_t hit[4] = {0, 0, 0, 0};
+    const uint32_t *rows = reinterpret_cast<const uint32_t *>(nan_value_rows(a));
+    // a thread a (token, 32 dims)
+    for (int x = threadIdx.x; x < 4 * (t1 - t0); x += threads) {
+        const int t = t0 + (x >> 2), p = L - n + t, j = x & 3;
+        uint32_t hit = 0;
 #pragma unroll 1
-    for (int i = 0; i < nt; ++i) {
-        const int64_t tile = tile0 + copy_tile(i);
-        const uint32_t word = __ldg(tiles + tile);
-        if (word == 0)
-            continue;
+        for (int i = 0; i < nt; ++i) {
+            const int64_t tile = tile0 + copy_tile(i);
+            const uint32_t word = __ldg(nan_value_tiles(a) + tile);
+            if (word == 0)
+                continue;
 #pragma unroll 1
-        for (int k = 0; k < kKeys; ++k) {
-            const int t = key_tile(i) * kKeys + k;
-            if ((word >> (8 * (k >> 5)) & 0xFFu) != 0 && t <= p && (!kWin || t > p - w.window || t < w.sinks))
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    hit[j] |= __ldg(rows + (tile * kKeys + k) * 4 + j);
+            for (int k = 0; k < kKeys; ++k) {
+                const int key = key_tile(i) * kKeys + k;
+                if ((word >> (8 * (k >> 5)) & 0xFFu) != 0 && key <= p && (!kWin || key > p - w.window || key < w.sinks))
+                    hit |= __ldg(rows + (tile * kKeys + k) * 4 + j);
+            }
         }
-    }
-    if (!valid)
-        return;
+        const int64_t row = (static_cast<int64_t>(q0) + t) * a.hq + static_cast<int64_t>(h) * a.group;
 #pragma unroll 1
-    for (int d = d0; d < d0 + dims; ++d) {
-        const uint32_t x = d < 64 ? (d < 32 ? hit[0] : hit[1]) : (d < 96 ? hit[2] : hit[3]);
-        if ((x >> (d & 31)) & 1u) {
-            if (a.out_f32)
-                static_cast<float *>(a.out)[orow * kHeadDim + d] = NAN;
-            else
-                static_cast<__nv_bfloat16 *>(a.out)[orow * kHeadDim + d] = __float2bfloat16_rn(NAN);
-        }
+        for (int d = 0; hit != 0 && d < 32; ++d)
+            for (int g = 0; ((hit >> d) & 1u) && g < a.group; ++g) {
+                if (a.out_f32)
+                    static_cast<float *>(a.out)[(row + g) * kHeadDim + 32 * j + d] = NAN;
+                else
+                    static_cast<__nv_bfloat16 *>(a.out)[(row + g) * kHeadDim + 32 * j + d] = __float2bfloat16_rn(NAN);
+            }
     }
 }
 

@@ -70,9 +70,10 @@ struct P2 {
     };
     static constexpr int kTmem = kBars + kNumBars * 8;
     static constexpr int kFlag = kTmem + 4;
-    static constexpr int kMoved = (kFlag + 4 + 15) / 16 * 16;   // MovedRow [2][kRows]
+    static constexpr int kFactor = kFlag + 4;              // kBlocks: its entry of v_refs
+    static constexpr int kMoved = (kFactor + 4 + 15) / 16 * 16;   // MovedRow [2][kRows]
     static constexpr int kEnd = kMoved + 2 * kRows * static_cast<int>(sizeof(MovedRow));
-    static constexpr size_t bytes(bool folds) { return static_cast<size_t>(folds ? kEnd : kFlag + 4) + 1024; }
+    static constexpr size_t bytes(bool folds) { return static_cast<size_t>(folds ? kEnd : kFactor + 4) + 1024; }
 };
 static_assert(P2::bytes(true) <= 232448, "prefill tile buffers exceed the shared memory of one CTA");
 
@@ -290,7 +291,8 @@ __device__ __forceinline__ float lift_of(int nt)
 }
 
 // kFolds: for calls in which a query tile may visit more than kFold2 key tiles.
-template <bool kWin, bool kFolds>
+// kBlocks: the block-scaled FP8 cache's.
+template <bool kWin, bool kFolds, bool kBlocks>
 __global__ void __launch_bounds__(kThreads2, 1)
     paged_prefill_pair_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                               const __grid_constant__ CUtensorMap tm_v, const PrefillArgs a, const KeyWindow win)
@@ -341,6 +343,8 @@ __global__ void __launch_bounds__(kThreads2, 1)
         for (int i = 0; i < P2::kNumBars; ++i)
             mbar_init(bar(i), i >= P2::Q_READY && i < P2::K_FULL ? 4 : (i >= P2::P_FULL && i < P2::PV_DONE ? 4 : 1));
         *abort_flag = 0;
+        if (kBlocks)
+            *reinterpret_cast<volatile float *>(smem + P2::kFactor) = __ldg(a.v_refs + bh);
         fence_barrier_init();
     }
     if (warp == 1) {
@@ -483,7 +487,7 @@ __global__ void __launch_bounds__(kThreads2, 1)
         const int g = row - tl * G;
         const bool valid = row < G * tpt && tl < nvx;
         const int p_row = pos0 + x * tpt + (valid ? tl : nvx - 1);   // padding rows mirror the last row
-        const float sl2 = score_factor(a, h);
+        const float sl2 = score_factor<kBlocks>(a, h);
         const uint32_t s_tm = tm + (static_cast<uint32_t>(qtr * 32) << 16) + kScoreCol * x;
         const uint32_t o_tm = s_tm + kOutCol;
         float m = -INFINITY, l = 0.f;
@@ -622,8 +626,8 @@ __global__ void __launch_bounds__(kThreads2, 1)
             tc::fence_after();
             if (kFolds && ntx > kFold2)
                 l = fold(o_tm, m, l, true, true);
-            const float inv = value_factor(a, b, h) / l;
-            const uint32_t nans = a.v_refs ? 0u : nan_blocks<kWin>(a, win, row0 / kKeys, ntx, p_row, lane, key_tile, copy_tile);
+            const float inv = (kBlocks ? fabsf(*reinterpret_cast<volatile float *>(smem + P2::kFactor)) : __ldg(a.v_scale + h)) / l;
+            const uint32_t nans = nan_blocks<kWin>(a, win, row0 / kKeys, ntx, p_row, lane, key_tile, copy_tile);
             const int64_t orow = (static_cast<int64_t>(q0) + t0 + x * tpt + tl) * a.hq + h * G + g;
             uint4 *dst = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.out) + orow * kHeadDim);
 #pragma unroll 1
@@ -646,8 +650,6 @@ __global__ void __launch_bounds__(kThreads2, 1)
                     dst[4 * c + k] = make_uint4(w[0], w[1], w[2], w[3]);
                 }
             }
-            if (a.v_refs)
-                put_nans<kWin>(a, win, row0 / kKeys, ntx, p_row, lane, key_tile, copy_tile, valid, orow, 0, kHeadDim);
         }
     }
 
@@ -657,10 +659,13 @@ __global__ void __launch_bounds__(kThreads2, 1)
         tc::fence_after();
         tc::tmem_dealloc(tm, 512);
     }
+    if (kBlocks && *reinterpret_cast<volatile float *>(smem + P2::kFactor) < 0.f)
+        put_nans<kWin>(a, win, 2, kThreads2);
 }
 
 std::mutex g_pair_mu;
-unsigned long long g_pair_ctx[64][4] = {};   // per device and kernel: the context its limit was raised in
+typedef void (*PairKernel)(const CUtensorMap, const CUtensorMap, const CUtensorMap, const PrefillArgs, const KeyWindow);
+unsigned long long g_pair_ctx[64][8] = {};   // per device and kernel: the context its limit was raised in
 
 }  // namespace
 
@@ -684,9 +689,13 @@ cudaError_t launch_prefill_pair(const PrefillArgs &a, const KeyWindow &win, cons
     // query heads: 1172 us instead of 1153), and where it does (2048 of 131072: 6.01 ms, in
     // one chain 5.74; 1024 of 524288: 12.4 and 11.8).
     const bool folds = most_key_tiles(a, win) > kFold2;
-    const int which = (win.window > 0 ? 1 : 0) + (folds ? 2 : 0);
-    const auto kernel = win.window > 0 ? (folds ? paged_prefill_pair_kernel<true, true> : paged_prefill_pair_kernel<true, false>)
-                                       : (folds ? paged_prefill_pair_kernel<false, true> : paged_prefill_pair_kernel<false, false>);
+    const int which = (win.window > 0 ? 1 : 0) + (folds ? 2 : 0) + (a.v_refs ? 4 : 0);
+    static const PairKernel kernels[8] = {
+        paged_prefill_pair_kernel<false, false, false>, paged_prefill_pair_kernel<true, false, false>,
+        paged_prefill_pair_kernel<false, true, false>,  paged_prefill_pair_kernel<true, true, false>,
+        paged_prefill_pair_kernel<false, false, true>,  paged_prefill_pair_kernel<true, false, true>,
+        paged_prefill_pair_kernel<false, true, true>,   paged_prefill_pair_kernel<true, true, true>};
+    const PairKernel kernel = kernels[which];
     int dev = -1;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess)

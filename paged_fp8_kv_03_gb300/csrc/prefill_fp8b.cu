@@ -142,7 +142,7 @@ __global__ void __launch_bounds__(256) kv_widen_fp8b_kernel(const PrefillArgs a,
         const int per_head = (off1 - off0) / a.hkv;
         const int h = (tile - off0) / per_head, vt = (tile - off0) - h * per_head;
         const int key0 = (vt < kt.first ? vt : vt + kt.skip) * kKeys;
-        const int ref = __float_as_int(a.v_refs[b * a.hkv + h]) >> 23;
+        const int ref = (__float_as_int(*const_cast<volatile float *>(a.v_refs + b * a.hkv + h)) >> 23) & 0xFF;
         uint2 kc[kRowsEach], vc[kRowsEach];
         float ks[kRowsEach], vs[kRowsEach];
         uint32_t nans[kRowsEach];                        // V's, 8 bits a row
@@ -195,15 +195,19 @@ __global__ void __launch_bounds__(256) kv_widen_fp8b_kernel(const PrefillArgs a,
         }
         const bool any = __syncthreads_or(some) != 0;
         if (tid == 0) {
+            if (kPieces == 1 || piece % kPieces == 0)
+                nan_tiles(a)[tile] = 0u;                 // (no NaN block of the 4-bit cache's kind)
             if (kPieces == 1)
-                nan_tiles(a)[tile] = any ? 0x01010101u : 0u;
+                nan_value_tiles(a)[tile] = any ? 0x01010101u : 0u;
             else
-                reinterpret_cast<uint8_t *>(nan_tiles(a) + tile)[piece % kPieces] = any;
+                reinterpret_cast<uint8_t *>(nan_value_tiles(a) + tile)[piece % kPieces] = any;
         }
         if (any) {
+            if (tid == 0)                                // (several tiles' CTAs may: all store the same)
+                *const_cast<volatile float *>(a.v_refs + b * a.hkv + h) = __int_as_float(ref << 23 | static_cast<int>(0x80000000u));
 #pragma unroll
             for (int i = 0; i < kRowsEach; ++i)
-                nan_rows(a)[(static_cast<int64_t>(tile) * kKeys + first + 16 * i) * 16 + part] = static_cast<uint8_t>(nans[i]);
+                nan_value_rows(a)[(static_cast<int64_t>(tile) * kKeys + first + 16 * i) * 16 + part] = static_cast<uint8_t>(nans[i]);
         }
     }
 }
