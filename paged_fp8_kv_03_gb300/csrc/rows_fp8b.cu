@@ -11,10 +11,12 @@
 // code' = E4M3(code * 2^(e_old - e)), which changes none that stays a normal E4M3
 // number.
 //
-// Who works for a block: the warp that finds the block's first token in the call.
-// A token is the first if none of the 31 before it has its block; the block's
-// other tokens are among the 31 behind it.  So a block's tokens need not be next
-// to one another nor in order, only within 32 of the call's.
+// Who works for a block: the warp that finds the block's first token in the call
+// among the few that it looks at.  A token is the first if none of the 31 before it has
+// its block; the block's other tokens are among the 31 behind it.  So a block's tokens
+// need not be next to one another nor in order, only within 32 of the call's.
+// (Sixteen tokens that are a whole block's rows, as most of a prompt's are, need no
+// search.)  A warp loads the block's rows of one kv head, of K or of V, at once.
 //
 // What bounds them: the bytes, 256 or 512 a row of the call and 128 of the cache.
 #include "fp8b.h"
@@ -24,7 +26,7 @@ namespace pkv {
 namespace {
 
 constexpr unsigned kWarp = 0xffffffffu;
-constexpr int kAppendThreads = 256, kReach = 32;
+constexpr int kRowThreads = 256;
 
 // The exponent of a block whose largest |value| has these bits (finite).
 __device__ __forceinline__ int block_exponent(uint32_t top)
@@ -88,65 +90,96 @@ __device__ __forceinline__ void values_of(const Eight<kBf16> &x, float (&v)[8])
         v[i] = kBf16 ? __uint_as_float(i & 1 ? w[i >> 1] & 0xFFFF0000u : w[i >> 1] << 16) : __uint_as_float(w[i]);
 }
 
-// A block's new rows in one call.
-struct Members {
-    int count;                                             // rows found (at most 16)
-    uint32_t rows;                                         // a bit a row of the block
-    uint8_t token[kBlock], row[kBlock];                    // beyond the first one's token; row of the block
-};
-
-// One block of K or of V (the whole warp): its new rows' tokens are t0 + m.token[i].
+// The bits of the largest |value| of eight, sign aside (bf16: in the high half of
+// either half's place, see top_bits).
 template <bool kBf16>
-__device__ __forceinline__ void append_block(const Fp8bRowArgs &a, const void *rows, uint8_t *cache, uint8_t *exps, int64_t t0,
-                                             int64_t slot, int h, const Members &m, int lane)
+__device__ __forceinline__ uint32_t max_bits(const Eight<kBf16> &x, uint32_t top)
+{
+    const uint32_t *w = reinterpret_cast<const uint32_t *>(x.u);
+#pragma unroll
+    for (int i = 0; i < (kBf16 ? 4 : 8); ++i) {
+        if (kBf16)
+            asm("max.u16x2 %0, %1, %2;" : "=r"(top) : "r"(top), "r"(w[i] & 0x7FFF7FFFu));
+        else
+            top = max(top, w[i] & 0x7FFFFFFFu);
+    }
+    return top;
+}
+
+// The fp32 bits of what max_bits has left.
+template <bool kBf16>
+__device__ __forceinline__ uint32_t top_bits(uint32_t top)
+{
+    return kBf16 ? max(top << 16, top & 0xFFFF0000u) : top;
+}
+
+// The same of the finite ones, by each value.
+template <bool kBf16>
+__device__ __forceinline__ uint32_t finite_bits(const Eight<kBf16> &x, uint32_t top)
+{
+    float v[8];
+    values_of<kBf16>(x, v);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        const uint32_t bits = __float_as_uint(v[j]) & 0x7FFFFFFFu;
+        top = max(top, bits < 0x7F800000u ? bits : 0u);
+    }
+    return top;
+}
+
+// One block of K or of V (the whole warp).  Its `count` new rows: lane k (and 16 + k) has
+// the token and the row of the k-th, `rows` a bit a row; kFull: all 16, token k in row k.
+template <bool kBf16, bool kFull>
+__device__ __forceinline__ void append_block(const Fp8bRowArgs &a, const void *in, uint8_t *cache, uint8_t *exps, int64_t t0,
+                                             int64_t slot, int h, int count, int token, int row, uint32_t rows, int lane)
 {
     const int64_t page = slot >> a.page_log2;
     const int row0 = static_cast<int>(slot & (a.page_size - 1)) & ~(kBlock - 1);
     uint8_t *block = cache + ((page * a.hkv + h) * a.page_size + row0) * kHeadDim;
     uint8_t *exp = exps + (page * a.hkv + h) * (a.page_size / kBlock) + row0 / kBlock;
-    const bool begins = m.rows & 1u;
-    const int old = begins ? kExpMin : min(static_cast<int>(*exp) - kExpBias, kExpMax);
+    const bool begins = kFull || (rows & 1u);
     const int part = lane & 15, half = lane >> 4;          // 8 dims of two rows at a time
     Eight<kBf16> x[kBlock / 2];
 #pragma unroll
     for (int i = 0; i < kBlock / 2; ++i) {
-        const int k = 2 * i + half;
-        if (k < m.count)
-            load_eight<kBf16>(rows, ((t0 + m.token[k]) * a.hkv + h) * kHeadDim + 8 * part, x[i]);
+        const int k = 2 * i + half, t = kFull ? k : __shfl_sync(kWarp, token, k);
+        if (kFull || k < count)
+            load_eight<kBf16>(in, ((t0 + t) * a.hkv + h) * kHeadDim + 8 * part, x[i]);
     }
+    const int old = begins ? kExpMin : min(static_cast<int>(*exp) - kExpBias, kExpMax);
     uint32_t top = 0;
 #pragma unroll
-    for (int i = 0; i < kBlock / 2; ++i) {
-        if (2 * i + half < m.count) {
-            float v[8];
-            values_of<kBf16>(x[i], v);
+    for (int i = 0; i < kBlock / 2; ++i)
+        if (kFull || 2 * i + half < count)
+            top = max_bits<kBf16>(x[i], top);
+    top = __reduce_max_sync(kWarp, top_bits<kBf16>(top));
+    if (top >= 0x7F800000u) {                              // an infinity or a NaN
+        top = 0;
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const uint32_t bits = __float_as_uint(v[j]) & 0x7FFFFFFFu;
-                top = max(top, bits < 0x7F800000u ? bits : 0u);
-            }
-        }
+        for (int i = 0; i < kBlock / 2; ++i)
+            if (kFull || 2 * i + half < count)
+                top = finite_bits<kBf16>(x[i], top);
+        top = __reduce_max_sync(kWarp, top);
     }
-    top = __reduce_max_sync(kWarp, top);
     const int e = max(block_exponent(top), old);
     const float down = two_to(-e);
 #pragma unroll
     for (int i = 0; i < kBlock / 2; ++i) {
-        const int k = 2 * i + half;
-        if (k < m.count) {
+        const int k = 2 * i + half, r = kFull ? k : __shfl_sync(kWarp, row, k);
+        if (kFull || k < count) {
             float v[8];
             values_of<kBf16>(x[i], v);
 #pragma unroll
             for (int j = 0; j < 8; ++j)
                 v[j] *= down;
-            *reinterpret_cast<uint2 *>(block + m.row[k] * kHeadDim + 8 * part) =
+            *reinterpret_cast<uint2 *>(block + r * kHeadDim + 8 * part) =
                 make_uint2(to_e4m3x4(v[0], v[1], v[2], v[3]), to_e4m3x4(v[4], v[5], v[6], v[7]));
         }
     }
     if (!begins && e > old) {                              // the rows that were there, to the larger power of two
         const float f = two_to(max(old - e, -126));
         for (int r = lane >> 3; r < kBlock; r += 4) {
-            if ((m.rows >> r) & 1u)
+            if ((rows >> r) & 1u)
                 continue;
             uint4 *p = reinterpret_cast<uint4 *>(block + r * kHeadDim) + (lane & 7);
             uint4 u = *p;
@@ -164,118 +197,134 @@ __device__ __forceinline__ void append_block(const Fp8bRowArgs &a, const void *r
         *exp = static_cast<uint8_t>(e + kExpBias);
 }
 
-// A CTA looks at `tokens` of the call's tokens; the blocks that these begin in the
-// call, times heads, times K and V, are shared among its warps and those of the
-// gridDim.y CTAs beside it.
-template <bool kBf16>
-__global__ void __launch_bounds__(kAppendThreads) kv_append_fp8b_kernel(const Fp8bRowArgs a, int tokens)
+// Position of the k-th set bit (k < popcount).
+__device__ __forceinline__ int nth_bit(uint64_t m, int k)
 {
-    __shared__ Members members[kBlock];
-    __shared__ int64_t slots[kBlock];
-    __shared__ int place[kBlock + 1];                      // tokens that come first, and how many
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int64_t first = static_cast<int64_t>(blockIdx.x) * tokens;
-    auto slot_at = [&](int64_t t) { return t >= 0 && t < a.num_tokens ? __ldg(a.slots + t) : int64_t(-1); };
-    for (int i = warp; i < tokens; i += kAppendThreads / 32) {
-        const int64_t t = first + i, slot = slot_at(t);
-        const int64_t behind = slot_at(t + lane), before = slot_at(t - kReach + 1 + lane);   // (lane 31: t itself)
-        const bool in = slot >= 0 && slot < a.num_slots;
-        if (slot >= a.num_slots && lane == 0 && blockIdx.y == 0 && a.err)
-            atomicOr(a.err, PKV_DEVERR_SLOT);
-        const bool again = lane < kReach - 1 && before >= 0 && before / kBlock == slot / kBlock;
-        const bool mine = in && behind >= 0 && behind / kBlock == slot / kBlock;
-        const uint32_t mask = __ballot_sync(kWarp, mine);
-        const bool leads = in && !__any_sync(kWarp, again);
-        if (leads) {
-            const int rank = __popc(mask & ((1u << lane) - 1u));
-            const int row = static_cast<int>(behind & (kBlock - 1));
-            const uint32_t rows = __reduce_or_sync(kWarp, mine ? 1u << row : 0u);
-            if (mine && rank < kBlock) {                   // (more: a slot occurs twice)
-                members[i].token[rank] = static_cast<uint8_t>(lane);
-                members[i].row[rank] = static_cast<uint8_t>(row);
-            }
-            if (lane == 0) {
-                members[i].count = min(__popc(mask), kBlock);
-                members[i].rows = rows;
-            }
+    int at = 0;
+#pragma unroll
+    for (int w = 32; w > 0; w >>= 1) {
+        const int n = __popcll(m & ((uint64_t(1) << w) - 1));
+        if (k >= n) {
+            k -= n;
+            m >>= w;
+            at += w;
         }
-        if (lane == 0)
-            slots[i] = leads ? slot : -1;
     }
-    __syncthreads();
-    if (threadIdx.x == 0) {
-        int n = 0;
-        for (int i = 0; i < tokens; ++i)
-            if (slots[i] >= 0)
-                place[n++] = i;
-        place[kBlock] = n;
+    return at;
+}
+
+// A warp looks at `tokens` (at most 16) of the call's tokens, for one kv head's K or V.
+template <bool kBf16>
+__global__ void __launch_bounds__(kRowThreads, kBf16 ? 4 : 2) kv_append_fp8b_kernel(const Fp8bRowArgs a, int tokens)
+{
+    const int lane = threadIdx.x & 31;
+    const uint32_t id = blockIdx.x * (kRowThreads / 32) + (threadIdx.x >> 5), per = 2 * a.hkv;
+    const uint32_t group = id / per, rest = id - group * per;
+    const int h = static_cast<int>(rest >> 1);
+    const int64_t first = static_cast<int64_t>(group) * tokens;
+    if (first >= a.num_tokens)
+        return;
+    const void *in = rest & 1 ? a.v_in : a.k_in;
+    uint8_t *cache = rest & 1 ? a.v_cache : a.k_cache, *exps = rest & 1 ? a.v_exp : a.k_exp;
+    auto slot_at = [&](int64_t t) { return t >= 0 && t < a.num_tokens ? __ldg(a.slots + t) : int64_t(-1); };
+    const int64_t s = slot_at(first + lane), s0 = __shfl_sync(kWarp, s, 0);
+    if (tokens == kBlock && s0 >= 0 && s0 < a.num_slots && (s0 & (kBlock - 1)) == 0 &&
+        __all_sync(kWarp, lane >= kBlock || s == s0 + lane)) {
+        append_block<kBf16, true>(a, in, cache, exps, first, s0, h, kBlock, 0, 0, 0xFFFFu, lane);
+        return;
     }
-    __syncthreads();
-    const int items = place[kBlock] * a.hkv * 2;
-    for (int k = blockIdx.y * (kAppendThreads / 32) + warp; k < items; k += gridDim.y * (kAppendThreads / 32)) {
-        const int i = place[k / (2 * a.hkv)], rest = k % (2 * a.hkv);
-        const int h = rest >> 1;
-        if (rest & 1)
-            append_block<kBf16>(a, a.v_in, a.v_cache, a.v_exp, first + i, slots[i], h, members[i], lane);
-        else
-            append_block<kBf16>(a, a.k_in, a.k_cache, a.k_exp, first + i, slots[i], h, members[i], lane);
+    const int64_t before = slot_at(first - 32 + lane), behind = slot_at(first + 32 + lane);
+    const bool mine = lane < tokens && s >= 0;             // (beyond the call: -1)
+    if (mine && s >= a.num_slots && rest == 0 && a.err)
+        atomicOr(a.err, PKV_DEVERR_SLOT);
+    // (no token: a block of its own)
+    const int64_t block = s >= 0 ? s / kBlock : -1 - lane;
+    const uint32_t same = __match_any_sync(kWarp, block);
+    uint32_t leaders = __ballot_sync(kWarp, mine && s < a.num_slots && (same & ((1u << lane) - 1u)) == 0);
+    while (leaders != 0) {
+        const int L = __ffs(leaders) - 1;
+        leaders &= leaders - 1;
+        const int64_t slot = __shfl_sync(kWarp, s, L), b = slot / kBlock;
+        if (__any_sync(kWarp, lane > L && before >= 0 && before / kBlock == b))
+            continue;                                      // begun by an earlier token
+        const uint32_t lo = __shfl_sync(kWarp, same, L);
+        const uint32_t hi = __ballot_sync(kWarp, lane < L && behind >= 0 && behind / kBlock == b);
+        const uint64_t members = static_cast<uint64_t>(hi) << 32 | lo;
+        const int count = min(__popcll(members), kBlock);  // (more: a slot occurs twice)
+        const uint32_t rows = __reduce_or_sync(kWarp, ((lo >> lane) & 1u ? 1u << (s & (kBlock - 1)) : 0u) |
+                                                          ((hi >> lane) & 1u ? 1u << (behind & (kBlock - 1)) : 0u));
+        const int token = (lane & 15) < count ? nth_bit(members, lane & 15) : L;
+        const int from_s = __shfl_sync(kWarp, static_cast<int>(s & (kBlock - 1)), token & 31);
+        const int from_behind = __shfl_sync(kWarp, static_cast<int>(behind & (kBlock - 1)), token & 31);
+        append_block<kBf16, false>(a, in, cache, exps, first, slot, h, count, token, token < 32 ? from_s : from_behind, rows,
+                                   lane);
     }
 }
 
-// 16 bytes of a row of K and of V a thread.
-template <bool kBf16>
-__global__ void __launch_bounds__(256) kv_read_fp8b_kernel(const Fp8bRowArgs a)
+// 16 bytes of a row of K and of V of kTokens tokens a thread, whose loads are in flight
+// together.
+template <bool kBf16, int kTokens>
+__global__ void __launch_bounds__(kRowThreads) kv_read_fp8b_kernel(const Fp8bRowArgs a)
 {
     constexpr int kVals = kBf16 ? 8 : 4, kPerRow = kHeadDim / kVals;
-    const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
-    const int part = static_cast<int>(i % kPerRow);
-    const int64_t row = i / kPerRow, t = row / a.hkv;
-    const int h = static_cast<int>(row - t * a.hkv);
-    if (t >= a.num_tokens)
+    const uint32_t i = blockIdx.x * kRowThreads + threadIdx.x, row = i / kPerRow, part = i % kPerRow;
+    const uint32_t group = row / static_cast<uint32_t>(a.hkv), h = row - group * a.hkv;
+    const int64_t token = static_cast<int64_t>(group) * kTokens;
+    if (token >= a.num_tokens)
         return;
-    const int64_t slot = __ldg(a.slots + t);
-    if (slot < 0)
-        return;
-    const bool in = slot < a.num_slots;
-    if (!in && a.err)
-        atomicOr(a.err, PKV_DEVERR_SLOT);
-    const int64_t page = slot >> a.page_log2, r = slot & (a.page_size - 1);
-    const int64_t at = ((page * a.hkv + h) * a.page_size + r) * kHeadDim + part * kVals;
-    const int64_t x_at = (page * a.hkv + h) * (a.page_size / kBlock) + r / kBlock;
+    int64_t slot[kTokens];
+    uint32_t w[kTokens][2][kVals / 4], x[kTokens][2];
 #pragma unroll
-    for (int kv = 0; kv < 2; ++kv) {
-        const uint8_t *cache = kv ? a.v_cache : a.k_cache, *exps = kv ? a.v_exp : a.k_exp;
-        void *out = kv ? a.v_out : a.k_out;
-        uint32_t w[kVals / 4];
-        float f = 0.f;
+    for (int n = 0; n < kTokens; ++n)
+        slot[n] = token + n < a.num_tokens ? __ldg(a.slots + token + n) : -1;
 #pragma unroll
-        for (int j = 0; j < kVals / 4; ++j)
-            w[j] = in ? __ldg(reinterpret_cast<const uint32_t *>(cache + at) + j) : 0u;
-        if (in) {
-            const uint32_t x = __ldg(exps + x_at);
-            f = __uint_as_float(x == 0 ? 0x00400000u : x << 23);   // 2^(x - 127)
-        }
-        float v[kVals];
+    for (int n = 0; n < kTokens; ++n) {
+        const bool in = slot[n] >= 0 && slot[n] < a.num_slots;
+        const int64_t page = slot[n] >> a.page_log2, at = (page * a.hkv + h) * a.page_size + (slot[n] & (a.page_size - 1));
 #pragma unroll
-        for (int j = 0; j < kVals / 4; ++j) {
-            float y[4];
-            from_e4m3x4(w[j], y);
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-                v[4 * j + k] = y[k] * f;
-        }
-        if constexpr (kBf16) {
-            uint32_t o[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * j], v[2 * j + 1]);
-                o[j] = *reinterpret_cast<const uint32_t *>(&b);
+        for (int kv = 0; kv < 2; ++kv) {
+            const uint8_t *src = (kv ? a.v_cache : a.k_cache) + at * kHeadDim + part * kVals;
+            if (kBf16) {
+                const uint2 u = in ? __ldg(reinterpret_cast<const uint2 *>(src)) : make_uint2(0u, 0u);
+                w[n][kv][0] = u.x;
+                w[n][kv][kVals / 4 - 1] = u.y;
+            } else {
+                w[n][kv][0] = in ? __ldg(reinterpret_cast<const uint32_t *>(src)) : 0u;
             }
-            *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(out) + row * kHeadDim + part * kVals) =
-                make_uint4(o[0], o[1], o[2], o[3]);
-        } else {
-            *reinterpret_cast<float4 *>(static_cast<float *>(out) + row * kHeadDim + part * kVals) =
-                make_float4(v[0], v[1], v[2], v[3]);
+            x[n][kv] = in ? __ldg((kv ? a.v_exp : a.k_exp) + at / kBlock) : kExpBias;
+        }
+    }
+#pragma unroll
+    for (int n = 0; n < kTokens; ++n) {
+        if (slot[n] < 0)
+            continue;
+        if (slot[n] >= a.num_slots && a.err)
+            atomicOr(a.err, PKV_DEVERR_SLOT);
+        const int64_t to = (((token + n) * a.hkv + h) * kHeadDim + part * kVals);
+#pragma unroll
+        for (int kv = 0; kv < 2; ++kv) {
+            void *out = kv ? a.v_out : a.k_out;
+            const float f = __uint_as_float(x[n][kv] == 0 ? 0x00400000u : x[n][kv] << 23);   // 2^(x - 127)
+            float v[kVals];
+#pragma unroll
+            for (int j = 0; j < kVals / 4; ++j) {
+                float y[4];
+                from_e4m3x4(w[n][kv][j], y);
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    v[4 * j + k] = y[k] * f;
+            }
+            if constexpr (kBf16) {
+                uint32_t o[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * j], v[2 * j + 1]);
+                    o[j] = *reinterpret_cast<const uint32_t *>(&b);
+                }
+                *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(out) + to) = make_uint4(o[0], o[1], o[2], o[3]);
+            } else {
+                *reinterpret_cast<float4 *>(static_cast<float *>(out) + to) = make_float4(v[0], v[1], v[2], v[3]);
+            }
         }
     }
 }
@@ -284,26 +333,48 @@ __global__ void __launch_bounds__(256) kv_read_fp8b_kernel(const Fp8bRowArgs a)
 
 cudaError_t launch_kv_append_fp8b(const Fp8bRowArgs &a, bool bf16, cudaStream_t stream)
 {
-    const int tokens = a.num_tokens <= 512 ? 1 : (a.num_tokens <= 4096 ? 4 : kBlock);
-    const int64_t grid = (a.num_tokens + tokens - 1) / tokens;
-    const int share = tokens == 1 ? (2 * a.hkv + kAppendThreads / 32 - 1) / (kAppendThreads / 32) : 1;
-    const dim3 g(static_cast<unsigned>(grid), static_cast<unsigned>(share > 64 ? 64 : share));
+    // tokens a warp looks at: a block's 16 where that leaves enough warps
+    int tokens = kBlock;
+    while (tokens > 1 && a.num_tokens * 2 * a.hkv < static_cast<int64_t>(device_sm_count()) * 16 * tokens)
+        tokens /= 2;
+    const int64_t warps = (a.num_tokens + tokens - 1) / tokens * 2 * a.hkv;
+    const int64_t grid = (warps + kRowThreads / 32 - 1) / (kRowThreads / 32);
+    if (warps > UINT32_MAX - kRowThreads)
+        return cudaErrorInvalidValue;
     if (bf16)
-        kv_append_fp8b_kernel<true><<<g, kAppendThreads, 0, stream>>>(a, tokens);
+        kv_append_fp8b_kernel<true><<<static_cast<unsigned>(grid), kRowThreads, 0, stream>>>(a, tokens);
     else
-        kv_append_fp8b_kernel<false><<<g, kAppendThreads, 0, stream>>>(a, tokens);
+        kv_append_fp8b_kernel<false><<<static_cast<unsigned>(grid), kRowThreads, 0, stream>>>(a, tokens);
     return cudaGetLastError();
 }
 
-cudaError_t launch_kv_read_fp8b(const Fp8bRowArgs &a, bool bf16, cudaStream_t stream)
+typedef void (*ReadKernel)(const Fp8bRowArgs);
+
+// Several tokens a thread where that still fills the GPU with threads.  Threads count in
+// 32 bits: longer calls are several launches.
+cudaError_t launch_kv_read_fp8b(const Fp8bRowArgs &args, bool bf16, cudaStream_t stream)
 {
-    const int64_t threads = a.num_tokens * a.hkv * (kHeadDim / (bf16 ? 8 : 4));
-    const int64_t grid = (threads + 255) / 256;
-    if (bf16)
-        kv_read_fp8b_kernel<true><<<static_cast<unsigned>(grid), 256, 0, stream>>>(a);
-    else
-        kv_read_fp8b_kernel<false><<<static_cast<unsigned>(grid), 256, 0, stream>>>(a);
-    return cudaGetLastError();
+    constexpr int kMany = 4;
+    const int64_t per_token = static_cast<int64_t>(args.hkv) * (bf16 ? 16 : 32);
+    const bool many = args.num_tokens * per_token >= static_cast<int64_t>(device_sm_count()) * 2048 * kMany;
+    const ReadKernel kernel = bf16 ? (many ? kv_read_fp8b_kernel<true, kMany> : kv_read_fp8b_kernel<true, 1>)
+                                   : (many ? kv_read_fp8b_kernel<false, kMany> : kv_read_fp8b_kernel<false, 1>);
+    const int64_t most = (int64_t(1) << 31) / per_token / kMany * kMany;
+    if (most < 1)
+        return cudaErrorInvalidValue;
+    for (int64_t t = 0; t < args.num_tokens; t += most) {
+        Fp8bRowArgs a = args;
+        a.num_tokens = args.num_tokens - t < most ? args.num_tokens - t : most;
+        a.slots += t;
+        a.k_out = static_cast<uint8_t *>(args.k_out) + t * args.hkv * kHeadDim * (bf16 ? 2 : 4);
+        a.v_out = static_cast<uint8_t *>(args.v_out) + t * args.hkv * kHeadDim * (bf16 ? 2 : 4);
+        const int64_t threads = (a.num_tokens + (many ? kMany : 1) - 1) / (many ? kMany : 1) * per_token;
+        kernel<<<static_cast<unsigned>((threads + kRowThreads - 1) / kRowThreads), kRowThreads, 0, stream>>>(a);
+        const cudaError_t e = cudaGetLastError();
+        if (e != cudaSuccess)
+            return e;
+    }
+    return cudaSuccess;
 }
 
 }  // namespace pkv
