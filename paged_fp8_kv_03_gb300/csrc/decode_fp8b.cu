@@ -87,13 +87,12 @@ struct ListInit {
     }
 };
 
-// The cluster's kernel: a warp's units are all on their way at once.
-constexpr int kClusterWarps = 4;
-constexpr int kClusterUnits = 3;
-struct ClusterSmem {                                       // [warps][kClusterUnits][kUnitBytes] first
-    static constexpr int kWarp = kClusterUnits * kUnitBytes;
+// The cluster's kernel.
+constexpr int kClusterWarps = 4, kClusterStages = 3;
+struct ClusterSmem {                                       // [warps][kClusterStages][kUnitBytes] first
+    static constexpr int kWarp = kClusterStages * kUnitBytes;
     static constexpr int kFull = kClusterWarps * kWarp;
-    static constexpr int kFlag = kFull + kClusterWarps * kClusterUnits * 8;
+    static constexpr int kFlag = kFull + kClusterWarps * kClusterStages * 8;
     static constexpr int kBytes = kFlag + 16 + 1024;
 };
 
@@ -624,8 +623,7 @@ __global__ void __launch_bounds__(kListThreads, kListCtas)
 
 // ---------------------------------------------------------------------- the cluster
 // One cluster of da.cluster CTAs a segment.  Its warps share the segment's
-// units evenly (at most kClusterUnits each, all brought in at once), leave their
-// states in shared memory and join them there.
+// units evenly, leave their states in shared memory and join them there.
 template <int kParts>
 __global__ void __launch_bounds__(32 * kClusterWarps, 2)
     paged_gqa_decode_fp8b_cluster_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
@@ -648,7 +646,7 @@ __global__ void __launch_bounds__(32 * kClusterWarps, 2)
     load_rows(a, b, h, r, c, raw);
     if (tid == 0) {
         *stop = 0;
-        for (int i = 0; i < kClusterWarps * kClusterUnits; ++i)
+        for (int i = 0; i < kClusterWarps * kClusterStages; ++i)
             mbar_init(smem_addr(smem) + S::kFull + 8 * i, 1);
         fence_barrier_init();
         if (rank == 0 && h == 0)
@@ -656,28 +654,44 @@ __global__ void __launch_bounds__(32 * kClusterWarps, 2)
     }
     const int units = (sg.tiles + 1) >> 1, workers = da.cluster * kClusterWarps, at = rank * kClusterWarps + warp;
     const int lo = units * at / workers;
-    const int n = min(units * (at + 1) / workers - lo, kClusterUnits);
-    int t = -2;                                            // lane 2i + j: tile j of unit i
-    if ((lane >> 1) < n)
-        t = tile_number(a, sg, b, h, 2 * (lo + (lane >> 1)) + (lane & 1));
+    const int n = units * (at + 1) / workers - lo;
+    // tile numbers as in the list: lane 2i + j has tile j of unit i of the 16 at hand
+    auto look_up = [&](int u0) -> int {
+        const int u = u0 + (lane >> 1);
+        return u < n ? tile_number(a, sg, b, h, 2 * (lo + u) + (lane & 1)) : -2;
+    };
+    int now = look_up(0), next = -2;
+    uint32_t bytes_next = 0;
     __syncthreads();
     const uint32_t ring = smem_addr(smem) + warp * S::kWarp;
-    const uint32_t full = smem_addr(smem) + S::kFull + warp * kClusterUnits * 8;
-    const uint32_t have = __ballot_sync(kEvery, t != -2);
-    // (test facility: the withheld warp never loads its first unit)
-    const bool withheld = lane < 2 && static_cast<int>(blockIdx.x) * kClusterWarps + warp == da.withhold;
-    if ((lane >> 1) < n && !(lane & 1) && !withheld)
-        mbar_arrive_expect_tx(full + 4 * lane, 2 * kTile * __popc((have >> lane) & 3u));
-    __syncwarp();
-    if (t != -2 && !withheld) {
-        const uint32_t dst = ring + (lane >> 1) * kUnitBytes + (lane & 1) * kTile, bar = full + 8 * (lane >> 1);
-        const uint64_t policy = l2_policy_evict_first();
-        const int zeros = static_cast<int>(a.num_pages * a.hkv);
-        load_tile(dst, &tm_k, t, a.pool_log2 - 4, zeros, bar, policy);
-        load_tile(dst + 2 * kTile, &tm_v, t, a.pool_log2 - 4, zeros, bar, policy);
-    }
-    __syncwarp();
-    const float2 mine = tile_scales(tile_bytes(da, t));
+    const uint32_t full = smem_addr(smem) + S::kFull + warp * kClusterStages * 8;
+    const uint64_t policy = l2_policy_evict_first();
+    const int zeros = static_cast<int>(a.num_pages * a.hkv), my = lane >> 1;
+    // units from .. to - 1 (of the 16 at hand) into their stages, by the lanes that have their tiles
+    auto issue = [&](int from, int to) {
+        if ((from & 15) == 0 && from > 0)
+            now = next;
+        if ((from & 15) == 8)
+            next = look_up(from + 8);
+        if ((from & 15) == 12)
+            bytes_next = tile_bytes(da, next);
+        const int u = (from & ~15) + my, stage = u % kClusterStages;
+        const uint32_t have = __ballot_sync(kEvery, now != -2), bar = full + 8 * stage;
+        // (test facility: the withheld warp never loads its first unit)
+        const bool on = u >= from && u < to &&
+                        !(u == 0 && static_cast<int>(blockIdx.x) * kClusterWarps + warp == da.withhold);
+        if (on && !(lane & 1))
+            mbar_arrive_expect_tx(bar, 2 * kTile * __popc((have >> lane) & 3u));
+        __syncwarp();
+        if (on && now != -2) {
+            const uint32_t dst = ring + stage * kUnitBytes + (lane & 1) * kTile;
+            load_tile(dst, &tm_k, now, a.pool_log2 - 4, zeros, bar, policy);
+            load_tile(dst + 2 * kTile, &tm_v, now, a.pool_log2 - 4, zeros, bar, policy);
+        }
+        __syncwarp();
+    };
+    issue(0, min(n, kClusterStages));
+    float2 mine = tile_scales(tile_bytes(da, now));
 
     const LaneOffsets offsets = lane_offsets(r, c);
     const Inner inner = inner_units(sg);
@@ -686,21 +700,38 @@ __global__ void __launch_bounds__(32 * kClusterWarps, 2)
     State s;
     clear(s);
     bool dead = false;
+    int stage = 0;
+    uint32_t parity = 0;
+#pragma unroll 1
     for (int u = 0; u < n; ++u) {
-        const float4 sc = make_float4(__shfl_sync(kEvery, mine.x, 2 * u), __shfl_sync(kEvery, mine.y, 2 * u),
-                                      __shfl_sync(kEvery, mine.x, 2 * u + 1), __shfl_sync(kEvery, mine.y, 2 * u + 1));
-        if (!wait_stage(full + 8 * u, 0, stop, a.err, lane)) {
+        const int i = u & 15;
+        if (i == 0 && u > 0)
+            mine = tile_scales(bytes_next);
+        const float4 sc = make_float4(__shfl_sync(kEvery, mine.x, 2 * i), __shfl_sync(kEvery, mine.y, 2 * i),
+                                      __shfl_sync(kEvery, mine.x, 2 * i + 1), __shfl_sync(kEvery, mine.y, 2 * i + 1));
+        if (!wait_stage(full + 8 * stage, parity, stop, a.err, lane)) {
             dead = true;
+            if (lane == 0)                                 // no copy may land in what the states overwrite
+                for (int v = u; v < min(n, u + kClusterStages); ++v) {
+                    const uint64_t t0 = global_timer_ns();
+                    while (!mbar_try_wait(full + 8 * (v % kClusterStages), (v / kClusterStages) & 1) &&
+                           global_timer_ns() - t0 < kLimitNs) {
+                    }
+                }
             break;
         }
-        take_unit<kParts>(ring + u * kUnitBytes, sc, offsets, qu, sg, inner, lo + u, lane, s, []() {});
-    }
-    if (dead && lane == 0)                                 // no copy may land in what the states overwrite
-        for (int u = 0; u < n; ++u) {
-            const uint64_t t0 = global_timer_ns();
-            while (!mbar_try_wait(full + 8 * u, 0) && global_timer_ns() - t0 < kLimitNs) {
+        take_unit<kParts>(ring + stage * kUnitBytes, sc, offsets, qu, sg, inner, lo + u, lane, s, [&]() {
+            if (u + kClusterStages < n) {                  // the unit just read makes room
+                fence_proxy_async_smem();
+                __syncwarp();
+                issue(u + kClusterStages, u + kClusterStages + 1);
             }
+        });
+        if (++stage == kClusterStages) {
+            stage = 0;
+            parity ^= 1u;
         }
+    }
     __syncwarp();
     float *state = reinterpret_cast<float *>(smem + warp * S::kWarp);   // over the ring
     if (n > 0 && !dead) {
@@ -803,15 +834,31 @@ int decode_fp8b_threads(bool cluster)
     return cluster ? 32 * kClusterWarps : kListThreads;
 }
 
-// CTAs a segment for the cluster kernel: the fewest (1, 2, 4, 8) that leave a
-// warp at most kClusterUnits units, if all of them are resident at once; 0: the list.
-// (`units`: of the longest sequence, `slots`: resident CTAs.)
+// CTAs a segment for the cluster kernel, 0: the list.  (`units`: of the longest sequence,
+// `slots`: resident CTAs.)  Where all are resident at once, the fewest (1, 2, 4, 8) that
+// leave a warp at most kClusterStages units, else the most; where they are not, 1.
+// A cluster spares the list's start and join, 7 to 10 us (32 x 4096 tokens of 8 kv
+// heads in one launch of single CTAs 42.9 us, by the list 49.9), but shares a segment's
+// units among its own warps only: what one long sequence among short ones takes
+// is its own units' time, 0.85 us one of a warp's 32 tokens.  So a warp has 16 of them at
+// most (32 x 2048: 24.1 us, list 30.4; 16 x 4096 in twos 27.2, 29.9; 4 x 16384 in eights 25.4,
+// 29.4), 10 where not even half of the GPU has a CTA (1 x 10240: 12.3 and 12.8; 1 x 12288: 14.1 and
+// 13.4).  More segments than CTAs run in rounds, the last of which should be well filled (64 x 1024, 1.7
+// rounds: 27.5 and 31.9; 40 x 2048, 1.1 rounds: 42.9 and 36.0; 40 x 1024: 22.4 and 22.9) or short (75 x 500: 16.8
+// and 22.7), and rounds of less than two units a warp few (128 x 128, 3.4 rounds: 16.8 and
+// 19.3; 256 x 128, 6.7 rounds: 28.7 and 22.4).
 int decode_fp8b_cluster(long long units, long long segments, int slots)
 {
-    for (int c = 1; c <= 8; c *= 2)
-        if (units <= static_cast<long long>(c) * kClusterWarps * kClusterUnits)
-            return segments * c <= slots ? c : 0;
-    return 0;
+    auto each = [&](int c) { return (units + c * kClusterWarps - 1) / (c * kClusterWarps); };
+    if (segments > slots) {
+        const long long rounds = (segments + slots - 1) / slots;
+        const bool filled = 3 * rounds * slots <= 4 * segments || each(1) <= 4;
+        return each(1) <= 16 && filled && (each(1) >= 2 || rounds <= 4) ? 1 : 0;
+    }
+    int best = 1;
+    while (best < 8 && segments * best * 2 <= slots && each(best) > kClusterStages)
+        best *= 2;
+    return each(best) <= (4 * segments * best >= 3ll * slots ? 16 : 8) ? best : 0;
 }
 
 cudaError_t launch_paged_decode_fp8b(const Fp8bDecodeArgs &da, const CUtensorMap &tm_k, const CUtensorMap &tm_v, int ctas,
