@@ -27,6 +27,8 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import importlib.machinery
+import importlib.util
 import math
 import os
 import threading
@@ -47,6 +49,7 @@ PAGE_POOL_HEADER = 4
 _INT32_MAX = 2 ** 31 - 1
 
 _lib = None
+_fast = None                         # the fast path of the block-scaled cache's and the plan's calls
 _lock = threading.Lock()
 
 
@@ -146,8 +149,31 @@ def load() -> ctypes.CDLL:
         lib.pkv_status_string.argtypes = [i32]
         lib.pkv_version.restype = i32
         lib.pkv_version.argtypes = []
+        _load_fast()
         _lib = lib
         return lib
+
+
+def _load_fast() -> None:
+    global _fast
+    path = _build.BINDING
+    if not os.path.exists(path):
+        raise RuntimeError(f"{path} is missing: build it first (python -m paged_fp8_kv_03_gb300.build)")
+    name = __name__ + "._binding"
+    loader = importlib.machinery.ExtensionFileLoader(name, path)
+    module = importlib.util.module_from_spec(importlib.util.spec_from_file_location(name, path, loader=loader))
+    loader.exec_module(module)
+    _fast = module
+
+
+def _load_and_fast():
+    load()
+    return _fast
+
+
+def _done(st, what) -> None:
+    if st != 0:
+        raise PkvError(st, what)
 
 
 def pkv_read_device_error(device_error, clear: bool = False, stream=None) -> int:
@@ -916,6 +942,10 @@ def paged_prefill_fp4(q, cu_q, k_cache, v_cache, k_scale, v_scale, block_table, 
 # ---------------------------------------------------------------------------
 # the block-scaled FP8 cache
 # ---------------------------------------------------------------------------
+# These calls, and the page plan's, go through the compiled binding where their
+# tensors are plain, on the current device, and the stream is the current one.  It
+# returns None for anything else, and for whatever is wrong, and the checks below say
+# what, or make the call.
 def fp8b_cache(num_pages, num_kv_heads, page_size, device=None) -> tuple:
     """One zeroed block-scaled pool (K or V): codes uint8 [num_pages, Hkv, P, 128]
     and exponent bytes uint8 [num_pages, Hkv, P / 16]."""
@@ -952,6 +982,9 @@ def pkv_kv_append_fp8b(k_new, v_new, slot_mapping, k_cache, v_cache, k_exp, v_ex
     written; a block's tokens within 32 consecutive ones); caches uint8
     [num_pages, Hkv, P, 128] and k_exp/v_exp uint8 [num_pages, Hkv, P / 16]
     (written in place)."""
+    st = (_fast or _load_and_fast()).append(k_new, v_new, slot_mapping, k_cache, v_cache, k_exp, v_exp, device_error, stream)
+    if st is not None:
+        return _done(st, "pkv_kv_append_fp8b")
     dev = _cuda_index(k_new, "k_new")
     k, v = _addr(k_new, "k_new", k_new.dtype, 3, dev), _addr(v_new, "v_new", k_new.dtype, 3, dev)
     kc, vc, ke, ve, NP, H, P = _fp8b_pools(k_cache, v_cache, k_exp, v_exp, dev)
@@ -969,6 +1002,9 @@ def pkv_kv_read_fp8b(slot_mapping, k_cache, v_cache, k_exp, v_exp, k_out, v_out,
                      stream=None) -> None:
     """The rows at slot_mapping (int64 [T]) as values, into k_out/v_out
     [T, Hkv, 128] fp32|bf16; rows of negative slots are left as they were."""
+    st = (_fast or _load_and_fast()).read(slot_mapping, k_cache, v_cache, k_exp, v_exp, k_out, v_out, device_error, stream)
+    if st is not None:
+        return _done(st, "pkv_kv_read_fp8b")
     dev = _cuda_index(k_out, "k_out")
     k, v = _addr(k_out, "k_out", k_out.dtype, 3, dev), _addr(v_out, "v_out", k_out.dtype, 3, dev)
     kc, vc, ke, ve, NP, H, P = _fp8b_pools(k_cache, v_cache, k_exp, v_exp, dev)
@@ -1021,6 +1057,10 @@ def pkv_paged_gqa_decode_fp8b(q, k_cache, v_cache, k_exp, v_exp, block_table, se
     """pkv_paged_gqa_decode over block-scaled caches (see pkv_kv_append_fp8b);
     window > 0: only the last `window` tokens and the first `sinks` are
     attended.  workspace uint8 (pkv_decode_fp8b_workspace_size bytes)."""
+    st = (_fast or _load_and_fast()).decode(q, k_cache, v_cache, k_exp, v_exp, block_table, seq_lens, out, workspace, sm_scale,
+                                            device_error, max_ctas, stream, max_seq_len, seq_page_sizes, window, sinks)
+    if st is not None:
+        return _done(st, "pkv_paged_gqa_decode_fp8b")
     dev = _cuda_index(q, "q")
     kc, vc, ke, ve, NP, Hkv, P = _fp8b_pools(k_cache, v_cache, k_exp, v_exp, dev)
     qa, oa, odt, bt, lens, psz, ws = _fp8b_attention(q, out, block_table, seq_lens, seq_page_sizes, workspace, dev)
@@ -1071,6 +1111,11 @@ def pkv_paged_prefill_fp8b(q, cu_q, k_cache, v_cache, k_exp, v_exp, block_table,
     window > 0: a query sees itself, the window - 1 tokens before it and the
     first `sinks` tokens.  workspace uint8 (pkv_prefill_fp8b_workspace_size
     bytes for the same bounds)."""
+    st = (_fast or _load_and_fast()).prefill(q, cu_q, k_cache, v_cache, k_exp, v_exp, block_table, seq_lens, out, max_q_len,
+                                             max_kv_len, workspace, sm_scale, device_error, stream, max_total_kv,
+                                             seq_page_sizes, window, sinks)
+    if st is not None:
+        return _done(st, "pkv_paged_prefill_fp8b")
     dev = _cuda_index(q, "q")
     kc, vc, ke, ve, NP, Hkv, P = _fp8b_pools(k_cache, v_cache, k_exp, v_exp, dev)
     qa, oa, odt, bt, lens, psz, ws = _fp8b_attention(q, out, block_table, seq_lens, seq_page_sizes, workspace, dev)
@@ -1143,6 +1188,10 @@ def pkv_plan_pages(past_lens, new_lens, block_table, pool, page_size, seq_lens, 
     writes seq_lens [B] (may be past_lens), cu_q [B + 1], slot_mapping int64 [T]
     and positions int32 [T] of the new tokens, back to back; rows behind them get
     slot -1.  All or nothing (see device_error)."""
+    st = (_fast or _load_and_fast()).plan(past_lens, new_lens, block_table, pool, page_size, seq_lens, cu_q, slot_mapping, positions,
+                                          device_error, stream)
+    if st is not None:
+        return _done(st, "pkv_plan_pages")
     dev = _cuda_index(past_lens, "past_lens")
     past, new = _addr(past_lens, "past_lens", torch.int32, 1, dev), _addr(new_lens, "new_lens", torch.int32, 1, dev)
     B = past_lens.shape[0]
@@ -1187,6 +1236,9 @@ def plan_pages(past_lens, new_lens, block_table, pool, page_size, max_tokens=Non
 def pkv_release_pages(seq_lens, block_table, pool, page_size, keep_lens=None, device_error=None, stream=None) -> None:
     """The pages behind keep_lens[b] tokens (None: all) of sequences of
     seq_lens[b] tokens (int32 [B]) go back to the pool.  All or nothing."""
+    st = (_fast or _load_and_fast()).release(seq_lens, block_table, pool, page_size, keep_lens, device_error, stream)
+    if st is not None:
+        return _done(st, "pkv_release_pages")
     dev = _cuda_index(seq_lens, "seq_lens")
     lens = _addr(seq_lens, "seq_lens", torch.int32, 1, dev)
     keep = None if keep_lens is None else _addr(keep_lens, "keep_lens", torch.int32, 1, dev)

@@ -9,6 +9,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -17,6 +18,7 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB_DIR = os.path.join(PKG, "lib")
 LIB = os.path.join(LIB_DIR, "libpagedfp8.so")
+BINDING = os.path.join(LIB_DIR, "_binding.so")      # the Python binding's fast path (needs torch's headers)
 
 SOURCES = ["append.cu", "decode.cu", "api.cu", "noalloc.cu", "calibrate.cu", "prefill.cu",
            "rows_fp4.cu", "prefill_fp4.cu", "decode_fp4.cu", "api_fp4.cu",
@@ -41,10 +43,27 @@ def _deps() -> list:
 
 
 def needs_build() -> bool:
-    if not os.path.exists(LIB):
+    if not os.path.exists(LIB) or not os.path.exists(BINDING):
         return True
-    t = os.path.getmtime(LIB)
+    t = min(os.path.getmtime(LIB), os.path.getmtime(BINDING))
     return any(os.path.getmtime(f) > t for f in _deps())
+
+
+def _binding_commands() -> tuple:
+    """The commands that compile and link the binding's fast path."""
+    import torch
+    base = os.path.dirname(torch.__file__)
+    obj, tmp = os.path.join(BUILD, "binding.o"), BINDING + f".tmp{os.getpid()}"
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(_nvcc())))
+    cxx = shutil.which("g++") or "c++"
+    compile_ = [cxx, "-O2", "-std=c++17", "-fPIC", "-Wall", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+                "-I", INCLUDE, "-I", sysconfig.get_paths()["include"], "-I", os.path.join(cuda, "include"),
+                "-isystem", os.path.join(base, "include"),
+                "-isystem", os.path.join(base, "include", "torch", "csrc", "api", "include"),
+                "-c", os.path.join(CSRC, "binding.cpp"), "-o", obj]
+    link = [cxx, "-shared", "-o", tmp, obj, "-L", LIB_DIR, "-lpagedfp8", "-Wl,-rpath,$ORIGIN", "-L",
+            os.path.join(base, "lib"), "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python"]
+    return compile_, link, tmp
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
@@ -62,6 +81,8 @@ def build(force: bool = False, verbose: bool = False) -> str:
         if verbose:
             cmd.insert(1, "-Xptxas=-v")
         procs.append((src, subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True)))
+    compile_, link, binding_tmp = _binding_commands()
+    procs.append(("binding.cpp", subprocess.Popen(compile_, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True)))
     failed = []
     for src, p in procs:
         out, _ = p.communicate()
@@ -70,10 +91,12 @@ def build(force: bool = False, verbose: bool = False) -> str:
         if p.returncode != 0:
             failed.append(src)
     if failed:
-        raise RuntimeError(f"nvcc failed for {failed}")
+        raise RuntimeError(f"compilation failed for {failed}")
     tmp = LIB + f".tmp{os.getpid()}"
     subprocess.run([nvcc, *ARCH, "-shared", "-o", tmp, *objs], check=True)
     os.replace(tmp, LIB)
+    subprocess.run(link, check=True)
+    os.replace(binding_tmp, BINDING)
     return LIB
 
 
