@@ -730,6 +730,7 @@ pkv_status pkv_paged_prefill_fp8b(const void *q, const int32_t *cu_q, int total_
  *                  not overlap on the GPU.
  */
 #define PKV_PAGE_POOL_HEADER 4
+#define PKV_MAX_PLAN_ROWS (1 << 30) /* rows of a plan, pages of a pool */
 
 /*
  * plan_pages -- sequence b holds past_lens[b] tokens in the first ceil(past_lens[b] /
@@ -756,7 +757,7 @@ pkv_status pkv_paged_prefill_fp8b(const void *q, const int32_t *cu_q, int total_
  *   cu_q           device int32 [batch + 1].
  *   slot_mapping   device int64 [max_tokens].
  *   positions      device int32 [max_tokens] or NULL.
- * batch is at most PKV_MAX_BATCH.  One launch.
+ * batch is at most PKV_MAX_BATCH, max_tokens and num_pages PKV_MAX_PLAN_ROWS.  One launch.
  */
 pkv_status pkv_plan_pages(const int32_t *past_lens, const int32_t *new_lens, int batch,
                           int32_t *block_table, int max_pages_per_seq, int page_size,

@@ -119,6 +119,7 @@ def test_plan_calls_refuse(lib):
     for call in (_plan, _release):
         for bad, status in ((dict(B=-1), SHAPE), (dict(maxp=0), SHAPE), (dict(np_=0), SHAPE), (dict(P=8), UNSUPPORTED),
                             (dict(P=24), UNSUPPORTED), (dict(B=8193), UNSUPPORTED), (dict(np_=1 << 31), UNSUPPORTED),
+                            (dict(np_=(1 << 30) + 1), UNSUPPORTED),
                             (dict(maxp=1 << 27), UNSUPPORTED), (dict(bt=None), NULL), (dict(pool=None), NULL),
                             (dict(lens=None), NULL), (dict(bt=_off(2)), ALIGN), (dict(pool=_off(2)), ALIGN),
                             (dict(lens=_off(1)), ALIGN), (dict(err=_off(2)), ALIGN)):
@@ -126,6 +127,7 @@ def test_plan_calls_refuse(lib):
     for bad, status in ((dict(T=-1), SHAPE), (dict(past=None), NULL), (dict(new=None), NULL), (dict(cu=None), NULL),
                         (dict(slots=None), NULL), (dict(slots=_off(4)), ALIGN), (dict(pos=_off(2)), ALIGN)):
         assert _plan(lib, **bad) == status, bad
+    assert _plan(lib, T=(1 << 30) + 1) == UNSUPPORTED
     assert _release(lib, keep=_off(2)) == ALIGN
     assert _release(lib, B=0, lens=None, bt=None, pool=None) == OK
 
