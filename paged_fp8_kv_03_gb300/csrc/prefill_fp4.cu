@@ -572,8 +572,11 @@ __global__ void __launch_bounds__(kThreads2, 1)
             const float top = fmaxf(max3(mx[0], mx[1], mx[2]), max3(max3(mx[3], mx[4], mx[5]), mx[6], mx[7])) * sl2;
             const bool need = top > m + kMoveMax;
             if (__any_sync(kAll, need)) {
-                const float mn = need ? top - lift_of<kFolds>(ntx) : m;
-                const float f = need ? ex2_approx(m - mn) : 1.f;
+                // (kBlocks, whose keys may differ much in size, so that rows move often: the warp's other rows
+                // move along; 4096 of 16384 tokens with sizes spread by e^0.7 1243 us, else 1265)
+                const bool moves = kBlocks ? top > m + lift_of<kFolds>(ntx) : need;
+                const float mn = moves ? top - lift_of<kFolds>(ntx) : m;
+                const float f = moves ? ex2_approx(m - mn) : 1.f;
                 m = mn;
                 l *= f;
                 if (j > 0) {                               // the accumulator holds tiles 0 .. j-1
