@@ -60,8 +60,10 @@ __device__ __forceinline__ float lift_of(int tiles)
 template <int kParts>
 constexpr int kFoldUnits = kParts == 1 ? 512 : 16;
 
-// The list's kernel.
-constexpr int kListWarps = kFp8bListWarps, kListThreads = 32 * kListWarps, kListCtas = 3, kStages = 2;
+// The list's kernel.  Two CTAs an SM with rings of three units bring as much at once as
+// three with rings of two, and still do where not every SM has its second (32 x 4096 tokens, a
+// segment a CTA, 46.8 us; three by two 55.1; 64 sequences of 512 to 131072 tokens 438 and 440).
+constexpr int kListWarps = kFp8bListWarps, kListThreads = 32 * kListWarps, kListCtas = 2, kStages = 3;
 struct ListSmem {                                          // the rings, [warps][kStages][kUnitBytes], come first,
     static constexpr int kFull = kListWarps * kStages * kUnitBytes;   // from a 1024-byte aligned base
     static constexpr int kScales = kFull + kListWarps * kStages * 8;  // float4 [warps][kStages]: 2^ek, ev of either block
@@ -86,6 +88,9 @@ struct ListInit {
         fence_barrier_init();
     }
 };
+
+// ListRange::how of a CTA that has a segment to itself.
+constexpr int kWholeSegment = INT32_MAX;
 
 // The cluster's kernel.
 constexpr int kClusterWarps = 4, kClusterStages = 3;
@@ -458,8 +463,8 @@ __device__ __forceinline__ void work_list(const Fp8bDecodeArgs &da, const CUtens
         if (lane == 0) {                                   // who holds the segment's first and last unit
             int2 *j = da.joins + p.b * a.hkv + p.h;
             if (p.unit == 0)
-                j->x = whole ? -1 : worker;
-            if (p.unit == 0 && !whole)
+                j->x = whole || how() == kWholeSegment ? -1 : worker;
+            if (p.unit == 0 && !whole && how() != kWholeSegment)
                 da.firsts[worker] = p.b * a.hkv + p.h;
             if (p.unit + take == units)
                 j->y = how() == ListRange::SPREAD ? worker : ~worker;
@@ -586,6 +591,47 @@ __device__ __forceinline__ void work_list(const Fp8bDecodeArgs &da, const CUtens
         }
 }
 
+// Every sequence has about as many units as the others, at least one for each warp, and
+// the segments, one a CTA, fill the SMs about evenly (whole CTA).  Then a CTA takes a
+// segment, and nothing is left to join: 32 x 4096 tokens of 8 kv heads 46.8 us, cut into equal
+// ranges 49.9.
+__device__ __forceinline__ bool segment_a_cta(const CacheAttnArgs &a, const int *start)
+{
+    const int segments = a.batch * a.hkv, sms = static_cast<int>(gridDim.x) / kListCtas;
+    bool like = segments > sms && segments <= sms * kListCtas && 5 * ((segments + sms - 1) / sms * sms) <= 6 * segments;
+    for (int b = threadIdx.x; b < a.batch && like; b += kListThreads) {
+        const int units = start[b + 1] - start[b];
+        like = units >= kListWarps && 10ll * units * a.batch <= 11ll * start[a.batch];
+    }
+    return __syncthreads_and(like) != 0;
+}
+
+// Joins the states of a CTA's warps, which share a segment, and writes its rows.
+__device__ __noinline__ void join_segment(void *out, bool f32, int64_t row0, int group, const uint8_t *smem, int warp, int lane)
+{
+    auto state = [&](int w, int g) {
+        return reinterpret_cast<const float *>(smem + w * kStages * kUnitBytes) + g * kPartialStride;
+    };
+    for (int g = warp; g < group; g += kListWarps) {
+        float M = -INFINITY, N = -INFINITY, L = 0.f;
+        float4 A = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int w = 0; w < kListWarps; ++w) {
+            M = fmaxf(M, state(w, g)[kRowM]);
+            N = fmaxf(N, state(w, g)[kRowRef]);
+        }
+#pragma unroll
+        for (int w = 0; w < kListWarps; ++w) {
+            const float4 v = *reinterpret_cast<const float4 *>(state(w, g) + 4 * lane);
+            const float e = ex2_approx(state(w, g)[kRowRef] - N);
+            L += ex2_approx(state(w, g)[kRowM] - M) * state(w, g)[kRowM + 1];
+            A = make_float4(A.x + e * v.x, A.y + e * v.y, A.z + e * v.z, A.w + e * v.w);
+        }
+        const float f = ex2_approx(N - M) / L;
+        store4(out, f32, row0 + g, 4 * lane, make_float4(A.x * f, A.y * f, A.z * f, A.w * f));
+    }
+}
+
 template <int kParts>
 __global__ void __launch_bounds__(kListThreads, kListCtas)
     paged_gqa_decode_fp8b_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
@@ -603,16 +649,33 @@ __global__ void __launch_bounds__(kListThreads, kListCtas)
     zero_rows<kListThreads>(da, start);
     launch_dependents();
 
-    const ListRange range = list_range<kListWarps>(da, start, no_empty, warp, lane);
+    ListRange range;
+    if (segment_a_cta(a, start)) {
+        const int segment = static_cast<int>(blockIdx.x), b = segment % a.batch, h = segment / a.batch;
+        range = ListRange{segment < a.batch * a.hkv, segment * kListWarps + warp, 0, 0, kWholeSegment};
+        if (lane == 0)
+            da.firsts[range.worker] = -1;
+        if (range.on) {
+            const int units = start[b + 1] - start[b], lo = units * warp / kListWarps;
+            range.lo = h * start[a.batch] + start[b] + lo;
+            range.n = units * (warp + 1) / kListWarps - lo;
+        }
+    } else {
+        range = list_range<kListWarps>(da, start, no_empty, warp, lane);
+    }
     if (range.on) {
         volatile int *how = reinterpret_cast<volatile int *>(smem + ListSmem::kHow + 4 * warp);
         if (lane == 0)
             how[0] = range.how;
         __syncwarp();
         work_list<kParts>(da, tm_k, tm_v, smem, warp, lane, range.worker, range.lo, range.n);
-        if (how[0] >= 0) {                                   // the segment begins before and ends behind the CTA's ranges
+        if (how[0] >= 0) {                                 // the warps' states lie in shared memory
             __syncthreads();
-            if (how[0] < da.num_slots)
+            if (how[0] == kWholeSegment)
+                join_segment(a.out, a.out_f32 != 0,
+                             static_cast<int64_t>(blockIdx.x % a.batch) * a.hq + static_cast<int64_t>(blockIdx.x / a.batch) * a.group,
+                             a.group, smem, warp, lane);
+            else if (how[0] < da.num_slots)                // the segment begins before and ends behind the CTA's ranges
                 join_warps<true, kListWarps, kStages * kUnitBytes>(
                     da.partials + static_cast<int64_t>(how[0]) * a.group * kPartialStride, a.group, smem, warp, lane);
             else if (a.err && lane == 0)
@@ -837,28 +900,28 @@ int decode_fp8b_threads(bool cluster)
 // CTAs a segment for the cluster kernel, 0: the list.  (`units`: of the longest sequence,
 // `slots`: resident CTAs.)  Where all are resident at once, the fewest (1, 2, 4, 8) that
 // leave a warp at most kClusterStages units, else the most; where they are not, 1.
-// A cluster spares the list's start and join, 7 to 10 us (32 x 4096 tokens of 8 kv
-// heads in one launch of single CTAs 42.9 us, by the list 49.9), but shares a segment's
-// units among its own warps only: what one long sequence among short ones takes
-// is its own units' time, 0.85 us one of a warp's 32 tokens.  So a warp has 16 of them at
-// most (32 x 2048: 24.1 us, list 30.4; 16 x 4096 in twos 27.2, 29.9; 4 x 16384 in eights 25.4,
-// 29.4), 10 where not even half of the GPU has a CTA (1 x 10240: 12.3 and 12.8; 1 x 12288: 14.1 and
-// 13.4).  More segments than CTAs run in rounds, the last of which should be well filled (64 x 1024, 1.7
-// rounds: 27.5 and 31.9; 40 x 2048, 1.1 rounds: 42.9 and 36.0; 40 x 1024: 22.4 and 22.9) or short (75 x 500: 16.8
-// and 22.7), and rounds of less than two units a warp few (128 x 128, 3.4 rounds: 16.8 and
-// 19.3; 256 x 128, 6.7 rounds: 28.7 and 22.4).
+// A cluster spares the list's start and join, 3 to 4 us (8 kv heads, 32 x 512 tokens 8.9 us, by
+// the list 12.7; 32 x 1024 14.7 and 18.3; 8 x 2048 in fours 11.2 and 14.5; 4 x 4096 in eights 11.0 and
+// 14.0), but shares a segment's units among its own warps only: what one long sequence among
+// short ones takes is its own units' time, 0.85 us one of a warp's 32 tokens.  So a warp has
+// 12 of them at most (32 x 1400: 17.3 and 21.1; with 16, 32 x 2048 of equal length 24.4 and 28.7, but
+// spread over 128 .. 2048 20.5 and 16.6), 8 where a quarter of the slots and more are empty (1 x 8192:
+// 11.7 and 11.9; 2 x 8192 14.4 and 14.2; 2 x 10000 16.4 and 15.0).  More segments than CTAs run in rounds,
+// the last of which should be well filled (64 x 1024, 1.7 rounds: 28.4 and 33.1; 40 x 2048, 1.1
+// rounds: 42.9 and 36.0) or short (75 x 500: 20.3 and 24.1), and rounds of less than two units a warp
+// few (128 x 128, 3.4 rounds: 16.8 and 17.4; 256 x 128, 6.7 rounds: 28.7 and 25.9).
 int decode_fp8b_cluster(long long units, long long segments, int slots)
 {
     auto each = [&](int c) { return (units + c * kClusterWarps - 1) / (c * kClusterWarps); };
     if (segments > slots) {
         const long long rounds = (segments + slots - 1) / slots;
         const bool filled = 3 * rounds * slots <= 4 * segments || each(1) <= 4;
-        return each(1) <= 16 && filled && (each(1) >= 2 || rounds <= 4) ? 1 : 0;
+        return each(1) <= 12 && filled && (each(1) >= 2 || rounds <= 4) ? 1 : 0;
     }
     int best = 1;
     while (best < 8 && segments * best * 2 <= slots && each(best) > kClusterStages)
         best *= 2;
-    return each(best) <= (4 * segments * best >= 3ll * slots ? 16 : 8) ? best : 0;
+    return each(best) <= (4 * segments * best >= 3ll * slots ? 12 : 8) ? best : 0;
 }
 
 cudaError_t launch_paged_decode_fp8b(const Fp8bDecodeArgs &da, const CUtensorMap &tm_k, const CUtensorMap &tm_v, int ctas,

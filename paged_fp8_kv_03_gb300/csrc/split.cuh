@@ -206,15 +206,20 @@ __device__ __forceinline__ void store16(const CacheAttnArgs &a, int64_t row, int
     }
 }
 
-__device__ __forceinline__ void store4(const CacheAttnArgs &a, int64_t row, int d, float4 v)
+__device__ __forceinline__ void store4(void *out, bool f32, int64_t row, int d, float4 v)
 {
-    if (a.out_f32) {
-        *reinterpret_cast<float4 *>(static_cast<float *>(a.out) + row * kHeadDim + d) = v;
+    if (f32) {
+        *reinterpret_cast<float4 *>(static_cast<float *>(out) + row * kHeadDim + d) = v;
     } else {
         const __nv_bfloat162 x = __floats2bfloat162_rn(v.x, v.y), y = __floats2bfloat162_rn(v.z, v.w);
-        *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(a.out) + row * kHeadDim + d) =
+        *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(out) + row * kHeadDim + d) =
             make_uint2(*reinterpret_cast<const uint32_t *>(&x), *reinterpret_cast<const uint32_t *>(&y));
     }
+}
+
+__device__ __forceinline__ void store4(const CacheAttnArgs &a, int64_t row, int d, float4 v)
+{
+    store4(a.out, a.out_f32 != 0, row, d, v);
 }
 
 // All threads of the cluster (one CTA: of the CTA).

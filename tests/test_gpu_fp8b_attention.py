@@ -150,6 +150,28 @@ def test_decode_many_short_sequences(pkv, cuda_device, B, G, window, sinks, max_
     assert torch.equal(_decode(pkv, c, q, qd, window, sinks, max_ctas=max_ctas), a)
 
 
+@pytest.mark.parametrize("out_dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("lens,G,window,sinks", [([2100, 2090, 2110, 2080], 4, 0, 0), ([130, 160, 150, 129], 8, 0, 0),
+                                                 ([2100, 2090, 2110, 2080], 3, 500, 9), ([2100, 100, 2110, 1], 4, 0, 0)])
+def test_decode_sequences_of_like_length(pkv, cuda_device, lens, G, window, sinks, out_dtype):
+    """A list whose segments get a CTA each (256 of them, four sequences' pages by turns),
+    and one of as many whose lengths differ."""
+    c = Cache(33, lens, 1, 16, cuda_device)
+    rows = [i % 4 for i in range(256)]
+    q, qd = c.queries(256, G)
+    e = torch.zeros(1, dtype=torch.int32, device=c.dev)
+    call = dict(out_dtype=out_dtype, max_seq_len=max(lens), max_ctas=1 << 20, window=window, sinks=sinks, device_error=e)
+    got = pkv.paged_gqa_decode_fp8b(qd, *c.args, c.tabled[rows].contiguous(), c.lensd[rows].contiguous(), **call)
+    for i in range(0, 256, 5):
+        b, x = rows[i], q[i].astype(np.float64)
+        ref = fp4_ref.attend(x, c.k[b], c.v[b], lens[b] - 1, window, sinks, SM)
+        tol = _tight_decode(c, b, x, lens[b] - 1, window, sinks, SM) if out_dtype == torch.float32 else \
+            fp4_ref.attention_tolerance(x, c.k[b], c.v[b], ref, SM, True)
+        _check(got[i], ref, tol, (i, lens[b]))
+    again = pkv.paged_gqa_decode_fp8b(qd, *c.args, c.tabled[rows].contiguous(), c.lensd[rows].contiguous(), **call)
+    assert torch.equal(got, again) and int(e.item()) == 0
+
+
 @pytest.mark.parametrize("spread", [30.0, 1e-4, 1e4])
 def test_decode_large_and_small_scores(pkv, cuda_device, spread):
     """Scores from almost equal to one that takes all the weight, rising and
