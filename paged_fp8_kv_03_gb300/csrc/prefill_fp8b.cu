@@ -10,8 +10,8 @@
 //
 // Two launches.  kv_refs_fp8b_kernel: a cluster of CTAs a sequence takes the maximum
 // of the bytes (a sixteenth of a byte a token and head), and CTA 0 lays out the
-// regions.  kv_widen_fp8b_kernel: a CTA a tile of 128 rows (or a quarter of one, where
-// there are few); a thread takes 8 values of kRowsEach of its rows, of K and of V, 16
+// regions.  kv_widen_fp8b_kernel: a CTA half a tile of 128 rows (or a quarter of one,
+// where there are few); a thread takes 8 values of kRowsEach of its rows, of K and of V, 16
 // lanes write a row's 256 bytes.  Bytes bound it: 256 of the cache to 512 of the
 // copies a row.
 #include "fp8b.h"
@@ -117,7 +117,7 @@ template <int kRowsEach>
 __global__ void __launch_bounds__(256) kv_widen_fp8b_kernel(const PrefillArgs a, const KeyWindow win)
 {
     constexpr int kPieces = 8 / kRowsEach;               // CTAs' steps a tile
-    static_assert(kPieces == 1 || kPieces == 4, "a tile's word has a byte a piece");
+    static_assert(kPieces == 2 || kPieces == 4, "a tile's word has two bytes or one a piece");
     const int tid = threadIdx.x;
     const int part = tid & 15;                           // dims 8 part .. 8 part + 7
     grid_wait();
@@ -195,10 +195,10 @@ __global__ void __launch_bounds__(256) kv_widen_fp8b_kernel(const PrefillArgs a,
         }
         const bool any = __syncthreads_or(some) != 0;
         if (tid == 0) {
-            if (kPieces == 1 || piece % kPieces == 0)
+            if (piece % kPieces == 0)
                 nan_tiles(a)[tile] = 0u;                 // (no NaN block of the 4-bit cache's kind)
-            if (kPieces == 1)
-                nan_value_tiles(a)[tile] = any ? 0x01010101u : 0u;
+            if (kPieces == 2)
+                reinterpret_cast<uint16_t *>(nan_value_tiles(a) + tile)[piece % kPieces] = any ? 0x0101 : 0;
             else
                 reinterpret_cast<uint8_t *>(nan_value_tiles(a) + tile)[piece % kPieces] = any;
         }
@@ -226,8 +226,8 @@ cudaError_t launch_widen_fp8b(const PrefillArgs &a, const KeyWindow &win, cudaSt
     if (tiles * 4 <= most)
         return launch_with(kv_widen_fp8b_kernel<2>, dim3(static_cast<unsigned>(tiles < 1 ? 1 : tiles * 4)), 256, 0, 1, true,
                            stream, a, win);
-    return launch_with(kv_widen_fp8b_kernel<8>, dim3(static_cast<unsigned>(tiles < most ? tiles : most)), 256, 0, 1, true,
-                       stream, a, win);
+    return launch_with(kv_widen_fp8b_kernel<4>, dim3(static_cast<unsigned>(tiles * 2 < most ? tiles * 2 : most)), 256, 0, 1,
+                       true, stream, a, win);
 }
 
 }  // namespace pkv
