@@ -665,7 +665,9 @@ pkv_status pkv_kv_read_fp8b(const int64_t *slot_mapping, int64_t num_tokens,
 /*
  * paged_gqa_decode_fp8b -- pkv_paged_gqa_decode_fp4 over the block-scaled cache: the
  * same window and sinks, queries, clamping, zero rows, determinism, errors and
- * launches.
+ * launches.  The weights are rounded as there, but each by what it contributes: what
+ * meets a block of V with scale 2^e counts as w 2^e, and small ones are rounded to
+ * multiples of 2^-26 (an fp32 output: 2^-37) of the largest w 2^e.
  *
  *   workspace      device, >= pkv_decode_fp8b_workspace_size(...) bytes for the same
  *                  sizes, 256-byte aligned; needs no initialisation, not to be shared

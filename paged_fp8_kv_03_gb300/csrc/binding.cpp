@@ -108,14 +108,21 @@ struct Args {
     }
 };
 
-// Makes the call without the interpreter's lock (a full launch queue blocks it).
+// The interpreter's lock, let go for as long as this lives (a full launch queue blocks a call).
+struct Unlocked {
+    PyThreadState *state;
+    Unlocked() : state(PyEval_SaveThread()) {}
+    ~Unlocked() { PyEval_RestoreThread(state); }
+};
+
 template <typename Call>
 PyObject *status(Call call)
 {
     pkv_status st;
-    Py_BEGIN_ALLOW_THREADS;
-    st = call();
-    Py_END_ALLOW_THREADS;
+    {
+        const Unlocked unlocked;
+        st = call();
+    }
     return PyLong_FromLong(st);
 }
 

@@ -27,6 +27,8 @@
 // reference n is taken from the largest contribution, s + ev, so that a weight is not
 // lost to another one that meets smaller values.  The sum of the weights has its
 // own reference m, from the largest s.  Both move only when exceeded by more than 15.9.
+// n is kept less a whole number e, the larger ev of the unit that moved it last: exponents
+// are then small wherever the values lie, and no bits of s are lost to ev.
 //
 // Every wait on an mbarrier is bounded (2 s): on expiry the kernel raises
 // PKV_DEVERR_TIMEOUT, stops issuing copies, drains those in flight, returns.
@@ -192,16 +194,17 @@ __device__ __forceinline__ void accumulate(const RawV &x, const uint32_t (&b)[kP
 
 // A piece's running state: lane (r, c) holds dims 16r .. 16r + 15 of heads 2c,
 // 2c + 1 (acc[i][j]: dim 2i of head 2c + j, acc[i][2 + j]: dim 2i + 1), the heads' references
-// of weights (m) and contributions (n), and the weights' sums (both heads') over its
-// own tokens.
+// of weights (m) and contributions (n + e), and the weights' sums (both heads') over
+// its own tokens.
 struct State {
-    float m0, m1, n0, n1, acc[8][4];
+    float m0, m1, n0, n1, e, acc[8][4];
     uint64_t sum;
 };
 
 __device__ __forceinline__ void clear(State &s)
 {
     s.m0 = s.m1 = s.n0 = s.n1 = -INFINITY;
+    s.e = 0.f;
     s.sum = 0ull;
 #pragma unroll
     for (int k = 0; k < 4; ++k)
@@ -248,7 +251,7 @@ __device__ __forceinline__ void take_unit(uint32_t st, const float4 &sc, const L
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
         const uint64_t f = pack2(qu.f0 * ek[j], qu.f1 * ek[j]), nm = pack2(-s.m0, -s.m1);
-        const uint64_t d = pack2(s.m0 - s.n0 + ev[j], s.m1 - s.n1 + ev[j]);
+        const uint64_t d = pack2(s.m0 - s.n0 + (ev[j] - s.e), s.m1 - s.n1 + (ev[j] - s.e));
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
             const uint64_t v = fma2(y[j][k], f, nm);
@@ -285,12 +288,19 @@ __device__ __forceinline__ void take_unit(uint32_t st, const float4 &sc, const L
                 const bool on = (seen >> (16 * j + 8 * k + r)) & 1u;
                 z[j][k].x = on ? w.x * (qu.f0 * ek[j]) : -INFINITY;
                 z[j][k].y = on ? w.y * (qu.f1 * ek[j]) : -INFINITY;
-                zn[j][k] = make_float2(z[j][k].x + ev[j], z[j][k].y + ev[j]);
                 t0 = fmaxf(t0, z[j][k].x);
                 t1 = fmaxf(t1, z[j][k].y);
-                c0 = fmaxf(c0, zn[j][k].x);
-                c1 = fmaxf(c1, zn[j][k].y);
+                c0 = fmaxf(c0, z[j][k].x + (ev[j] - s.e));
+                c1 = fmaxf(c1, z[j][k].y + (ev[j] - s.e));
             }
+        if (__any_sync(kEvery, c0 > s.n0 + kMoveMax || c1 > s.n1 + kMoveMax)) {
+            const float e = fmaxf(ev[0], ev[1]);
+            s.n0 += s.e - e;
+            s.n1 += s.e - e;
+            s.e = e;
+            c0 = fmaxf(fmaxf(z[0][0].x, z[0][1].x) + (ev[0] - e), fmaxf(z[1][0].x, z[1][1].x) + (ev[1] - e));
+            c1 = fmaxf(fmaxf(z[0][0].y, z[0][1].y) + (ev[0] - e), fmaxf(z[1][0].y, z[1][1].y) + (ev[1] - e));
+        }
 #pragma unroll
         for (int d = 4; d < 32; d <<= 1) {
             t0 = fmaxf(t0, __shfl_xor_sync(kEvery, t0, d));
@@ -318,8 +328,8 @@ __device__ __forceinline__ void take_unit(uint32_t st, const float4 &sc, const L
         for (int j = 0; j < 2; ++j)
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
+                zn[j][k] = make_float2(z[j][k].x + (ev[j] - s.e) - s.n0, z[j][k].y + (ev[j] - s.e) - s.n1);
                 z[j][k] = make_float2(z[j][k].x - s.m0, z[j][k].y - s.m1);
-                zn[j][k] = make_float2(zn[j][k].x - s.n0, zn[j][k].y - s.n1);
             }
     }
 #pragma unroll
@@ -351,7 +361,7 @@ __device__ __forceinline__ void lane_dims(const State &s, int j, float (&v)[16])
     }
 }
 
-// A state's row of one head: 128 dims, m, sum, n.
+// A state's row of one head: 128 dims, m, sum, n, e.
 __device__ __forceinline__ void store_state(float *row, const State &s, const float (&l)[2], int j, int r)
 {
     float v[16];
@@ -360,7 +370,7 @@ __device__ __forceinline__ void store_state(float *row, const State &s, const fl
     for (int k = 0; k < 4; ++k)
         reinterpret_cast<float4 *>(row + 16 * r)[k] = make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
     if (r == 0)
-        *reinterpret_cast<float4 *>(row + kRowM) = make_float4(j ? s.m1 : s.m0, l[j], j ? s.n1 : s.n0, 0.f);
+        *reinterpret_cast<float4 *>(row + kRowM) = make_float4(j ? s.m1 : s.m0, l[j], j ? s.n1 : s.n0, s.e);
 }
 
 // The bytes x of a tile's blocks of K (low) and V: of a tile outside the pool (it reads
@@ -482,7 +492,7 @@ __device__ __forceinline__ void work_list(const Fp8bDecodeArgs &da, const CUtens
         const int64_t slot = static_cast<int64_t>(worker) + p.h * a.batch + p.b;
         State s;
         clear(s);
-        float mf0 = -INFINITY, mf1 = -INFINITY, nf0 = -INFINITY, nf1 = -INFINITY;   // references of what has been folded
+        float mf0 = -INFINITY, mf1 = -INFINITY, nf0 = -INFINITY, nf1 = -INFINITY, ef = 0.f;   // references of what has been folded
         uint64_t sums = 0ull;                              // and its sums
         for (int i = 0; i < take && !dead;) {              // (folded between loops)
             const int end = min(take, i + kFoldUnits<kParts>);
@@ -512,7 +522,8 @@ __device__ __forceinline__ void work_list(const Fp8bDecodeArgs &da, const CUtens
             if (!dead && take >= kFoldUnits<kParts>) {
                 // the piece's own slot of the workspace holds the accumulator's copy (each lane its own elements)
                 const bool old = i > kFoldUnits<kParts>, last = i == take;
-                const float g0 = old ? ex2_approx(nf0 - s.n0) : 0.f, g1 = old ? ex2_approx(nf1 - s.n1) : 0.f;
+                const float g0 = old ? ex2_approx((nf0 - s.n0) + (ef - s.e)) : 0.f;
+                const float g1 = old ? ex2_approx((nf1 - s.n1) + (ef - s.e)) : 0.f;
                 if (slot >= da.num_slots) {
                     if (a.err && lane == 0)
                         atomicOr(a.err, PKV_DEVERR_INTERNAL);
@@ -548,6 +559,7 @@ __device__ __forceinline__ void work_list(const Fp8bDecodeArgs &da, const CUtens
                 mf1 = s.m1;
                 nf0 = s.n0;
                 nf1 = s.n1;
+                ef = s.e;
             }
         }
         if (dead)
@@ -564,12 +576,12 @@ __device__ __forceinline__ void work_list(const Fp8bDecodeArgs &da, const CUtens
             if (g >= a.group)
                 continue;
             if (whole) {
-                const float f = ex2_approx(j ? s.n1 - s.m1 : s.n0 - s.m0) / l[j];
+                const Quotient f(j ? s.n1 - s.m1 : s.n0 - s.m0, s.e, l[j]);
                 float v[16];
                 lane_dims(s, j, v);
 #pragma unroll
                 for (int k = 0; k < 16; ++k)
-                    v[k] *= f;
+                    v[k] = f(v[k]);
                 store16(a, row0 + g, 16 * r, v);
             } else if (how() >= 0) {                       // over the ring, which nothing more is brought into
                 store_state(reinterpret_cast<float *>(smem + warp * kStages * kUnitBytes) + g * kPartialStride, s, l, j, r);
@@ -613,22 +625,23 @@ __device__ __noinline__ void join_segment(void *out, bool f32, int64_t row0, int
         return reinterpret_cast<const float *>(smem + w * kStages * kUnitBytes) + g * kPartialStride;
     };
     for (int g = warp; g < group; g += kListWarps) {
-        float M = -INFINITY, N = -INFINITY, L = 0.f;
+        auto ref = [&](int w) { return Reference{state(w, g)[kRowRef], state(w, g)[kRowRef + 1]}; };
+        float M = -INFINITY, L = 0.f;
+        Reference N = {-INFINITY, 0.f};
         float4 A = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
         for (int w = 0; w < kListWarps; ++w) {
             M = fmaxf(M, state(w, g)[kRowM]);
-            N = fmaxf(N, state(w, g)[kRowRef]);
+            N = larger(ref(w), N);
         }
 #pragma unroll
         for (int w = 0; w < kListWarps; ++w) {
             const float4 v = *reinterpret_cast<const float4 *>(state(w, g) + 4 * lane);
-            const float e = ex2_approx(state(w, g)[kRowRef] - N);
+            const float e = ex2_approx(ref(w).over(N));
             L += ex2_approx(state(w, g)[kRowM] - M) * state(w, g)[kRowM + 1];
             A = make_float4(A.x + e * v.x, A.y + e * v.y, A.z + e * v.z, A.w + e * v.w);
         }
-        const float f = ex2_approx(N - M) / L;
-        store4(out, f32, row0 + g, 4 * lane, make_float4(A.x * f, A.y * f, A.z * f, A.w * f));
+        store4(out, f32, row0 + g, 4 * lane, Quotient(N.n - M, N.e, L)(A));
     }
 }
 
@@ -815,26 +828,29 @@ __global__ void __launch_bounds__(32 * kClusterWarps, 2)
     const bool one = da.cluster == 1;
     for (int g = one ? warp : rank; g < a.group; g += one ? kClusterWarps : da.cluster) {
         const uint32_t mine0 = smem_addr(smem) + g * kPartialStride * 4;       // warp 0's state of this head, this CTA
-        float m = -INFINITY, l = 0.f, ref = -INFINITY;
+        float m = -INFINITY, l = 0.f;
+        Reference ref = {-INFINITY, 0.f};
         if (lane < workers) {
-            const uint32_t ml = mine0 + (lane & 3) * S::kWarp + kRowM * 4;
-            m = cluster_load(ml, lane >> 2, one);
-            l = cluster_load(ml + 4, lane >> 2, one);
-            ref = cluster_load(ml + 8, lane >> 2, one);
+            const float4 v = cluster_load4(mine0 + (lane & 3) * S::kWarp + kRowM * 4, lane >> 2, one);
+            m = v.x;
+            l = v.y;
+            ref = Reference{v.z, v.w};
         }
-        float M = m, N = ref;
+        float M = m;
+        Reference N = ref;
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) {
             M = fmaxf(M, __shfl_xor_sync(kEvery, M, o));
-            N = fmaxf(N, __shfl_xor_sync(kEvery, N, o));
+            N = larger(Reference{__shfl_xor_sync(kEvery, N.n, o), __shfl_xor_sync(kEvery, N.e, o)}, N);
         }
+        N = Reference{__shfl_sync(kEvery, N.n, 0), __shfl_sync(kEvery, N.e, 0)};
         float sum = m == -INFINITY ? 0.f : ex2_approx(m - M) * l;
         // (not 0 where there is a state: a NaN of V in it is seen whatever its weight)
-        const float e = m == -INFINITY ? 0.f : fmaxf(ex2_approx(ref - N), 0x1p-126f);
+        const float e = m == -INFINITY ? 0.f : fmaxf(ex2_approx(ref.over(N)), 0x1p-126f);
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1)
             sum += __shfl_xor_sync(kEvery, sum, o);
-        const float f = units == 0 ? 0.f : ex2_approx(N - M) / sum;
+        const Quotient f(units == 0 ? 0.f : N.n - M, N.e, units == 0 ? 1.f : sum);   // (of no units: of zeros)
         const int64_t row = static_cast<int64_t>(b) * a.hq + static_cast<int64_t>(h) * a.group + g;
         // (what a warp without units left is read, but not used)
         if (one) {
@@ -849,7 +865,7 @@ __global__ void __launch_bounds__(32 * kClusterWarps, 2)
                 A.z += ei != 0.f ? ei * v.z : 0.f;
                 A.w += ei != 0.f ? ei * v.w : 0.f;
             }
-            store4(a, row, 4 * lane, make_float4(A.x * f, A.y * f, A.z * f, A.w * f));
+            store4(a, row, 4 * lane, f(A));
         } else {
             const int d = 32 * warp + lane;
             float A = 0.f;
@@ -863,9 +879,9 @@ __global__ void __launch_bounds__(32 * kClusterWarps, 2)
                 A += ei != 0.f ? ei * v[i] : 0.f;
             }
             if (a.out_f32)
-                static_cast<float *>(a.out)[row * kHeadDim + d] = A * f;
+                static_cast<float *>(a.out)[row * kHeadDim + d] = f(A);
             else
-                static_cast<__nv_bfloat16 *>(a.out)[row * kHeadDim + d] = __float2bfloat16_rn(A * f);
+                static_cast<__nv_bfloat16 *>(a.out)[row * kHeadDim + d] = __float2bfloat16_rn(f(A));
         }
     }
     cluster_sync(da.cluster);                              // no CTA leaves while its states are read

@@ -16,7 +16,7 @@ constexpr int kHeadDim = PKV_HEAD_DIM;
 constexpr int kWarps = 4;                               // independent workers per CTA
 constexpr int kThreads = kWarps * 32;
 constexpr int kCtasPerSm = 3;                           // resident decode CTAs per SM
-constexpr int kPartialStride = kHeadDim + 4;            // floats per (slot, head): acc, m, l, pad
+constexpr int kPartialStride = kHeadDim + 4;            // floats per (slot, head): acc, m, l, and two more
 
 // Page sizes the library accepts (tokens per page).
 inline bool page_size_ok(int p)

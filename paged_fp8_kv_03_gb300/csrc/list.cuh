@@ -4,7 +4,8 @@
 //
 // A piece's state of a head is a row of kPartialStride floats: the accumulator, the
 // reference m of its weights' exponents and their sum, and, with kOwnRef, the
-// reference of the accumulator where that is another one.
+// reference of the accumulator where that is another one: n + e, e a whole number, kept
+// apart so that exponents around it stay small and their differences exact.
 #pragma once
 
 #include "grid.cuh"
@@ -12,7 +13,18 @@
 
 namespace pkv {
 
-constexpr int kRowM = kHeadDim, kRowRef = kHeadDim + 2;
+struct Reference {
+    float n, e;
+    __device__ __forceinline__ float over(const Reference &o) const { return (n - o.n) + (e - o.e); }
+};
+
+// The larger of two.
+__device__ __forceinline__ Reference larger(const Reference &a, const Reference &b)
+{
+    return a.n + a.e >= b.n + b.e ? a : b;
+}
+
+constexpr int kRowM = kHeadDim, kRowRef = kHeadDim + 2;   // m, sum; n, e
 
 // start[b]: the first unit of sequence b (of one kv head), start[batch]: how many
 // there are (the whole CTA; sums: kWarps ints of shared memory; init: what thread
@@ -138,7 +150,8 @@ __device__ __noinline__ void join_warps(float *out, int group, uint8_t *smem, in
 {
     auto state = [&](int w) { return reinterpret_cast<const float *>(smem + w * kWarpBytes); };
     for (int g = warp; g < group; g += kWarps) {
-        float m[kWarps], l[kWarps], n[kWarps], M = -INFINITY, N = -INFINITY, L = 0.f;
+        float m[kWarps], l[kWarps], M = -INFINITY, L = 0.f;
+        Reference n[kWarps], N = {-INFINITY, 0.f};
         float4 A = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) {
@@ -146,15 +159,17 @@ __device__ __noinline__ void join_warps(float *out, int group, uint8_t *smem, in
             m[w] = ml.x;
             l[w] = ml.y;
             M = fmaxf(M, ml.x);
-            n[w] = kOwnRef ? state(w)[g * kPartialStride + kRowRef] : ml.x;
-            if (kOwnRef)
-                N = fmaxf(N, n[w]);
+            if (kOwnRef) {
+                const float2 ref = *reinterpret_cast<const float2 *>(state(w) + g * kPartialStride + kRowRef);
+                n[w] = Reference{ref.x, ref.y};
+                N = larger(n[w], N);
+            }
         }
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) {
             const float e = ex2_approx(m[w] - M);
             const float4 v = *reinterpret_cast<const float4 *>(state(w) + g * kPartialStride + 4 * lane);
-            const float ea = kOwnRef ? ex2_approx(n[w] - N) : e;
+            const float ea = kOwnRef ? ex2_approx(n[w].over(N)) : e;
             L += e * l[w];
             A.x += ea * v.x;
             A.y += ea * v.y;
@@ -166,7 +181,7 @@ __device__ __noinline__ void join_warps(float *out, int group, uint8_t *smem, in
         if (lane == 0) {
             *reinterpret_cast<float2 *>(row + kRowM) = make_float2(M, L);
             if (kOwnRef)
-                row[kRowRef] = N;
+                *reinterpret_cast<float2 *>(row + kRowRef) = make_float2(N.n, N.e);
         }
     }
 }
@@ -180,14 +195,17 @@ __device__ __noinline__ void join_warps(float *out, int group, uint8_t *smem, in
 // 33.3).  Warps are as few as an average segment needs, because a CTA of one or two is
 // on its SM before the list's CTAs have left it (64 x 2K tokens 35.0 us, with four at
 // least 39.0; 32 x 4K 34.2 and 36.0; the long one among short ones 46.0 and 43.7).
-constexpr int kJoin = 16, kJoinWarps = 16;
+// (kOwnRef: 12 states, as many as the registers hold.)
+template <bool kOwnRef>
+constexpr int kJoin = kOwnRef ? 12 : 16;
+constexpr int kJoinWarps = 16;
 constexpr int kJoinCut = 8;
 
 // Head g of segment sg, by `warps` warps of the CTA (ra, rm: theirs), kTurn pieces
 // a turn.
 template <bool kOwnRef, int kTurn>
 __device__ __forceinline__ void join_head(const SplitArgs &da, int sg, int g, int warp, int warps, int lane,
-                                          float (*ra)[kHeadDim], float3 *rm)
+                                          float (*ra)[kHeadDim], float4 *rm)
 {
     const CacheAttnArgs &a = da.a;
     const int b = sg / a.hkv, h = sg % a.hkv;
@@ -212,28 +230,33 @@ __device__ __forceinline__ void join_head(const SplitArgs &da, int sg, int g, in
     };
     const float *base = da.partials + (slot0 * a.group + g) * kPartialStride;
     const int64_t stride = static_cast<int64_t>(a.group) * kPartialStride;
-    float M = -INFINITY, N = -INFINITY, L = 0.f;
+    float M = -INFINITY, L = 0.f;
+    Reference N = {-INFINITY, 0.f};
     float4 A = make_float4(0.f, 0.f, 0.f, 0.f);
     for (int i0 = warp * kTurn; i0 < pieces; i0 += warps * kTurn) {
         float4 v[kTurn];
         float2 ml[kTurn];
-        float n[kTurn];
+        Reference n[kTurn];
 #pragma unroll
         for (int i = 0; i < kTurn; ++i) {
             const bool on = i0 + i < pieces;
             const float *s = base + (on ? worker(i0 + i) : 0) * stride;
             ml[i] = on ? *reinterpret_cast<const float2 *>(s + kRowM) : make_float2(-INFINITY, 0.f);
-            n[i] = kOwnRef ? (on ? s[kRowRef] : -INFINITY) : ml[i].x;
+            if (kOwnRef) {
+                const float2 ref = on ? *reinterpret_cast<const float2 *>(s + kRowRef) : make_float2(-INFINITY, 0.f);
+                n[i] = Reference{ref.x, ref.y};
+            }
             v[i] = on ? *reinterpret_cast<const float4 *>(s + 4 * lane) : make_float4(0.f, 0.f, 0.f, 0.f);
         }
-        float mn = M, nn = N;
+        float mn = M;
+        Reference nn = N;
 #pragma unroll
         for (int i = 0; i < kTurn; ++i) {
             mn = fmaxf(mn, ml[i].x);
             if (kOwnRef)
-                nn = fmaxf(nn, n[i]);
+                nn = larger(n[i], nn);
         }
-        const float f = ex2_approx(M - mn), fa = kOwnRef ? ex2_approx(N - nn) : f;
+        const float f = ex2_approx(M - mn), fa = kOwnRef ? ex2_approx(N.over(nn)) : f;
         M = mn;
         N = nn;
         L *= f;
@@ -241,7 +264,7 @@ __device__ __forceinline__ void join_head(const SplitArgs &da, int sg, int g, in
 #pragma unroll
         for (int i = 0; i < kTurn; ++i) {
             const float e = i0 + i < pieces ? ex2_approx(ml[i].x - mn) : 0.f;
-            const float ea = kOwnRef ? (i0 + i < pieces ? ex2_approx(n[i] - nn) : 0.f) : e;
+            const float ea = kOwnRef ? (i0 + i < pieces ? ex2_approx(n[i].over(nn)) : 0.f) : e;
             L += e * ml[i].y;
             A.x += ea * v[i].x;
             A.y += ea * v[i].y;
@@ -252,15 +275,16 @@ __device__ __forceinline__ void join_head(const SplitArgs &da, int sg, int g, in
     if (warps > 1) {
         *reinterpret_cast<float4 *>(&ra[warp][4 * lane]) = A;
         if (lane == 0)
-            rm[warp] = make_float3(M, L, N);
+            rm[warp] = make_float4(M, L, N.n, N.e);
         __syncthreads();
         if (warp != 0)
             return;
-        float mn = M, nn = N;
+        float mn = M;
+        Reference nn = N;
         for (int w = 1; w < warps; ++w) {
             mn = fmaxf(mn, rm[w].x);
             if (kOwnRef)
-                nn = fmaxf(nn, rm[w].z);
+                nn = larger(Reference{rm[w].z, rm[w].w}, nn);
         }
         M = mn;
         N = nn;
@@ -269,7 +293,7 @@ __device__ __forceinline__ void join_head(const SplitArgs &da, int sg, int g, in
         for (int w = 0; w < warps; ++w) {
             if (w * kTurn >= pieces)
                 break;                                     // a warp with no pieces
-            const float e = ex2_approx(rm[w].x - mn), ea = kOwnRef ? ex2_approx(rm[w].z - nn) : e;
+            const float e = ex2_approx(rm[w].x - mn), ea = kOwnRef ? ex2_approx(Reference{rm[w].z, rm[w].w}.over(nn)) : e;
             const float4 v = *reinterpret_cast<const float4 *>(&ra[w][4 * lane]);
             L += e * rm[w].y;
             A.x += ea * v.x;
@@ -278,18 +302,22 @@ __device__ __forceinline__ void join_head(const SplitArgs &da, int sg, int g, in
             A.w += ea * v.w;
         }
     }
-    const float f = (kOwnRef ? ex2_approx(N - M) : vs) / L;
-    store4(a, static_cast<int64_t>(b) * a.hq + static_cast<int64_t>(h) * a.group + g, 4 * lane,
-           make_float4(A.x * f, A.y * f, A.z * f, A.w * f));
+    const int64_t row = static_cast<int64_t>(b) * a.hq + static_cast<int64_t>(h) * a.group + g;
+    if (kOwnRef) {
+        store4(a, row, 4 * lane, Quotient(N.n - M, N.e, L)(A));
+    } else {
+        const float f = vs / L;
+        store4(a, row, 4 * lane, make_float4(A.x * f, A.y * f, A.z * f, A.w * f));
+    }
 }
 
 template <bool kOwnRef>
 __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const SplitArgs da)
 {
     __shared__ __align__(16) float ra[kJoinWarps][kHeadDim];
-    __shared__ float3 rm[kJoinWarps];
+    __shared__ float4 rm[kJoinWarps];
     grid_wait();
-    join_head<kOwnRef, kJoin>(da, blockIdx.x / da.a.group, blockIdx.x % da.a.group, threadIdx.x >> 5, blockDim.x >> 5,
+    join_head<kOwnRef, kJoin<kOwnRef>>(da, blockIdx.x / da.a.group, blockIdx.x % da.a.group, threadIdx.x >> 5, blockDim.x >> 5,
                      threadIdx.x & 31, ra, rm);
 }
 
@@ -319,7 +347,7 @@ cudaError_t launch_join(const SplitArgs &da, int ctas, cudaStream_t stream)
                            da);
     const long long pieces = (workers + segs - 1) / segs + 1;   // a segment's, on average
     int warps = 1;
-    while (warps < kJoinWarps && warps * kJoin < pieces)
+    while (warps < kJoinWarps && warps * kJoin<kOwnRef> < pieces)
         warps *= 2;
     return launch_with(join_kernel<kOwnRef>, dim3(static_cast<unsigned>(segs * da.a.group)), 32 * warps, 0, 1, true, stream,
                        da);

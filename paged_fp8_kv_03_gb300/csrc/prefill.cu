@@ -704,7 +704,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
             ok = false;
         }
         if (ok) {
-            const float inv = (kBlocks ? fabsf(*reinterpret_cast<volatile float *>(smem + PS::kFactor)) : __ldg(a.v_scale + h)) / (l + red_l[(half ^ 1) * kRows + row]);
+            const float inv = (kBlocks ? 1.f : __ldg(a.v_scale + h)) / (l + red_l[(half ^ 1) * kRows + row]);
             const int64_t orow = (static_cast<int64_t>(q0) + t0 + tl) * a.hq + h * G + g;
             uint32_t nans = 0;
             if (kFp4)
@@ -724,6 +724,12 @@ __global__ void __launch_bounds__(kPThreads, 1)
 #pragma unroll
                 for (int k = 0; k < 16; ++k)
                     v[k] = ((have_o ? __uint_as_float(t[k]) : 0.f) + __uint_as_float(o[k])) * f;
+                if (kBlocks) {                           // (apart: their product may lie below fp32's range)
+                    const float unit = fabsf(*reinterpret_cast<const float *>(smem + PS::kFactor));
+#pragma unroll
+                    for (int k = 0; k < 16; ++k)
+                        v[k] *= unit;
+                }
                 const int d0 = 64 * half + 16 * c;
                 if (a.out_f32) {
                     float4 *dst = reinterpret_cast<float4 *>(static_cast<float *>(a.out) + orow * kHeadDim + d0);

@@ -629,7 +629,7 @@ __global__ void __launch_bounds__(kThreads2, 1)
             tc::fence_after();
             if (kFolds && ntx > kFold2)
                 l = fold(o_tm, m, l, true, true);
-            const float inv = (kBlocks ? fabsf(*reinterpret_cast<volatile float *>(smem + P2::kFactor)) : __ldg(a.v_scale + h)) / l;
+            const float inv = (kBlocks ? 1.f : __ldg(a.v_scale + h)) / l;
             const uint32_t nans = nan_blocks<kWin>(a, win, row0 / kKeys, ntx, p_row, lane, key_tile, copy_tile);
             const int64_t orow = (static_cast<int64_t>(q0) + t0 + x * tpt + tl) * a.hq + h * G + g;
             uint4 *dst = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.out) + orow * kHeadDim);
@@ -646,8 +646,13 @@ __global__ void __launch_bounds__(kThreads2, 1)
                     const float f = (nans >> (2 * c + (k >> 1))) & 1u ? NAN : inv;
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        const __nv_bfloat162 b2 = __floats2bfloat162_rn(__uint_as_float(o[8 * k + 2 * e]) * f,
-                                                                        __uint_as_float(o[8 * k + 2 * e + 1]) * f);
+                        float v0 = __uint_as_float(o[8 * k + 2 * e]) * f, v1 = __uint_as_float(o[8 * k + 2 * e + 1]) * f;
+                        if (kBlocks) {                   // (apart: their product may lie below fp32's range)
+                            const float unit = fabsf(*reinterpret_cast<const float *>(smem + P2::kFactor));
+                            v0 *= unit;
+                            v1 *= unit;
+                        }
+                        const __nv_bfloat162 b2 = __floats2bfloat162_rn(v0, v1);
                         w[e] = *reinterpret_cast<const uint32_t *>(&b2);
                     }
                     dst[4 * c + k] = make_uint4(w[0], w[1], w[2], w[3]);

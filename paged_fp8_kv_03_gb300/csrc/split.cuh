@@ -222,6 +222,23 @@ __device__ __forceinline__ void store4(const CacheAttnArgs &a, int64_t row, int 
     store4(a.out, a.out_f32 != 0, row, d, v);
 }
 
+// a 2^d 2^e / l for a whole number e, whose power may lie at either end of fp32's
+// range where the result does not: it is multiplied in two halves, exactly.
+struct Quotient {
+    float rest, low, high;
+    __device__ __forceinline__ Quotient(float d, float e, float l) : rest(ex2_approx(d) / l)
+    {
+        const int whole = static_cast<int>(e), half = whole >> 1;
+        low = __int_as_float((half + 127) << 23);
+        high = __int_as_float((whole - half + 127) << 23);
+    }
+    __device__ __forceinline__ float operator()(float a) const { return a * rest * low * high; }
+    __device__ __forceinline__ float4 operator()(float4 a) const
+    {
+        return make_float4((*this)(a.x), (*this)(a.y), (*this)(a.z), (*this)(a.w));
+    }
+};
+
 // All threads of the cluster (one CTA: of the CTA).
 __device__ __forceinline__ void cluster_sync(int ctas)
 {
@@ -242,6 +259,23 @@ __device__ __forceinline__ float cluster_load(uint32_t at, int cta, bool own)
         uint32_t there;
         asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(there) : "r"(at), "r"(cta));
         asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(there) : "memory");
+    }
+    return v;
+}
+
+// The same for four floats, 16-byte aligned.
+__device__ __forceinline__ float4 cluster_load4(uint32_t at, int cta, bool own)
+{
+    float4 v;
+    if (own) {
+        asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(at) : "memory");
+    } else {
+        uint32_t there;
+        asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(there) : "r"(at), "r"(cta));
+        asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                     : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                     : "r"(there)
+                     : "memory");
     }
     return v;
 }

@@ -232,6 +232,41 @@ def test_decode_blocks_of_different_sizes(pkv, cuda_device, sizes, max_ctas):
             _check(got[b], ref, _tight_decode(c, b, x, L - 1, window, sinks, SM), (sizes, b, window))
 
 
+def _at_the_ends(pkv, dev, e, out_dtype, run):
+    """run(cache) over V of the size 2^e (an end of what blocks can hold), and what it
+    gives over the same V at 1: outputs 2^e apart, exactly but for the last rounding."""
+    got, codes = [], []
+    for size in (2.0 ** e, 1.0):
+        c = Cache(34, [40, 700], 2, 16, dev, sizes=lambda rng, L: np.full((L, 1, 1), size))
+        got.append(run(c).double().cpu().numpy())
+        codes.append(c.cache[1])
+    assert (codes[0] == codes[1]).all()                          # no block's exponent has met its end
+    want = got[1] * 2.0 ** e
+    assert np.isfinite(got[0]).all() and (got[0] != 0).any()
+    # the codes are the same, and the size enters by exact factors: the results are the same but for fp32's
+    # (bf16's) smallest step below its normal numbers
+    least = 2.0 ** (-133 if out_dtype == torch.bfloat16 else -149)
+    bad = ~(np.abs(got[0] - want) <= least)
+    assert not bad.any(), (int(bad.sum()), got[0][bad][:4], want[bad][:4])
+
+
+@pytest.mark.parametrize("out_dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("e", [-110, 120])
+@pytest.mark.parametrize("max_ctas", [0, 1, 5])
+def test_decode_at_the_ends_of_the_exponents(pkv, cuda_device, e, max_ctas, out_dtype):
+    q = torch.randn(2, 8, 128, generator=torch.Generator().manual_seed(3)).to(cuda_device).bfloat16()
+    _at_the_ends(pkv, cuda_device, e, out_dtype, lambda c: _raw(pkv, c, q, 0, out_dtype=out_dtype, max_ctas=max_ctas))
+
+
+@pytest.mark.parametrize("out_dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("e", [-110, 120])
+def test_prefill_at_the_ends_of_the_exponents(pkv, cuda_device, e, out_dtype):
+    q = torch.randn(90, 8, 128, generator=torch.Generator().manual_seed(4)).to(cuda_device).bfloat16()
+    cu = torch.tensor([0, 30, 90], dtype=torch.int32, device=cuda_device)
+    _at_the_ends(pkv, cuda_device, e, out_dtype, lambda c: pkv.paged_prefill_fp8b(
+        q, cu, *c.args, c.tabled, c.lensd, 60, max_kv_len=700, out_dtype=out_dtype))
+
+
 def test_decode_page_sizes_per_sequence(pkv, cuda_device):
     lens = [700, 33, 1, 256, 90]
     c = Cache(8, lens, 2, 16, cuda_device, page_sizes=[64, 16, 256, 128, 32])
