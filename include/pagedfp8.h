@@ -697,10 +697,13 @@ pkv_status pkv_paged_gqa_decode_fp8b(const void *q,
  * window and sinks, arguments, errors, untouched rows and determinism.  V is widened
  * in units of its own: of a sequence's kv head, blocks whose scale is less than 2^-21
  * of the largest one that the chunk sees are rounded to 2^-40 of that block's largest
- * value.  Three launches.  num_kv_heads is at most 8192.
+ * value.  Three launches; a fourth where few rows have a long past: several CTAs then
+ * share a query tile's keys (as many as batch, the bounds, the heads and the output's
+ * type say), and their sums are joined in order.  num_kv_heads is at most 8192.
  *
  *   workspace      device, >= pkv_prefill_fp8b_workspace_size(...) bytes for the same
- *                  bounds, 256-byte aligned.
+ *                  bounds, 256-byte aligned.  Where CTAs may share keys it has 41 MB for
+ *                  them, or more for long contexts.
  */
 size_t pkv_prefill_fp8b_workspace_size(int batch, int num_kv_heads, int max_q_len, int max_kv_len,
                                        int64_t max_total_kv, int window, int sinks);

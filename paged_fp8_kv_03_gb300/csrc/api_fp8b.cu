@@ -43,6 +43,12 @@ int decode_ctas(int batch, int max_ctas)
     return two < one ? two : one;
 }
 
+// What the longest sequence's length is at most (max_total_kv 0: not given).
+int longest_of(int max_kv_len, int64_t max_total_kv)
+{
+    return max_total_kv > 0 && max_total_kv < max_kv_len ? static_cast<int>(max_total_kv) : max_kv_len;
+}
+
 }  // namespace
 
 extern "C" {
@@ -192,7 +198,9 @@ size_t pkv_prefill_fp8b_workspace_size(int batch, int num_kv_heads, int max_q_le
         sinks < 0)
         return 0;
     return prefill_fp8b_bytes(batch, num_kv_heads,
-                              windowed_rows(batch, num_kv_heads, max_q_len, max_kv_len, max_total_kv, window, sinks));
+                              windowed_rows(batch, num_kv_heads, max_q_len, max_kv_len, max_total_kv, window, sinks)) +
+           prefill_fp8b_split_bytes(batch, num_kv_heads, max_q_len, longest_of(max_kv_len, max_total_kv),
+                                    clamp_window(window, sinks, max_kv_len));
 }
 
 pkv_status pkv_paged_prefill_fp8b(const void *q, const int32_t *cu_q, int total_q, int max_q_len,
@@ -232,7 +240,11 @@ pkv_status pkv_paged_prefill_fp8b(const void *q, const int32_t *cu_q, int total_
     const long long rows = windowed_rows(batch, num_kv_heads, max_q_len, max_kv_len, max_total_kv, window, sinks);
     if (rows >= (int64_t(1) << 31))
         return PKV_ERR_UNSUPPORTED;
-    if (!workspace || !aligned(workspace, 256) || workspace_bytes < prefill_fp8b_bytes(batch, num_kv_heads, rows))
+    const KeyWindow win = clamp_window(window, sinks, max_kv_len);
+    const int longest = longest_of(max_kv_len, max_total_kv);
+    const size_t copies = prefill_fp8b_bytes(batch, num_kv_heads, rows);
+    if (!workspace || !aligned(workspace, 256) ||
+        workspace_bytes < copies + prefill_fp8b_split_bytes(batch, num_kv_heads, max_q_len, longest, win))
         return PKV_ERR_WORKSPACE;
     uint8_t *base = static_cast<uint8_t *>(workspace) + prefill_header_bytes(batch);
     float *refs = reinterpret_cast<float *>(base);
@@ -277,7 +289,9 @@ pkv_status pkv_paged_prefill_fp8b(const void *q, const int32_t *cu_q, int total_
     a.out = out;
     a.out_f32 = out_dtype == PKV_F32;
     a.err = device_error;
-    const cudaError_t e = launch_prefill_windowed(a, clamp_window(window, sinks, max_kv_len), tm_q, tm_k, tm_v,
+    a.split = prefill_fp8b_split(a, win, longest);
+    a.partials = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + ((copies + 255) & ~size_t(255)));
+    const cudaError_t e = launch_prefill_windowed(a, win, tm_q, tm_k, tm_v,
                                                   launch_widen_fp8b, stream);
     return e == cudaSuccess ? PKV_OK : cuda_failed(e, "block-scaled prefill kernel launch");
 }

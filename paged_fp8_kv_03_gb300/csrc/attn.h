@@ -94,6 +94,9 @@ cudaError_t launch_prefill_windowed(const PrefillArgs &a, const KeyWindow &win, 
                                     const CUtensorMap &tm_k16, const CUtensorMap &tm_v16, WidenLaunch widen,
                                     cudaStream_t stream);
 
+// Joins what the CTAs of a split prefill have left, and writes the output.
+cudaError_t launch_prefill_join(const PrefillArgs &a, const KeyWindow &win, cudaStream_t stream);
+
 // Launches clusters of `cluster` CTAs (1: none), and, if `early`, with
 // programmatic stream serialization: the kernel may be brought onto the GPU
 // before the one ahead of it has ended, and waits for that with grid_wait().

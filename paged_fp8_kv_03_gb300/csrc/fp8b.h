@@ -61,6 +61,12 @@ inline size_t prefill_fp8b_bytes(int batch, int hkv, long long rows)
            static_cast<size_t>(rows / 128) * 2 * sizeof(uint32_t);
 }
 
+// CTAs that share the keys of a query tile (or of a pair of them) where no sequence has more
+// than `longest` tokens, 1 where one has them all; and the bytes that their rows' states
+// can take whatever the heads a kv head has and the output's type.
+int prefill_fp8b_split(const PrefillArgs &a, const KeyWindow &win, int longest);
+size_t prefill_fp8b_split_bytes(int batch, int hkv, int max_q_len, int longest, const KeyWindow &win);
+
 cudaError_t launch_widen_fp8b(const PrefillArgs &a, const KeyWindow &win, cudaStream_t stream);
 
 }  // namespace pkv

@@ -124,6 +124,8 @@ struct PrefillArgs {
     float *v_refs;                  // block-scaled FP8 cache: [batch][hkv] what a value of v16 stands for (caller
                                     // workspace, written ahead of the widening, which makes it negative where V
                                     // holds a NaN); else nullptr
+    int split;                      // block-scaled FP8 cache: CTAs that share a query tile's keys (1: one has them all)
+    float *partials;                // their rows: [query tiles or pairs][split][rows][kPartialStride]
     const int32_t *block_table;
     int max_pages;
     const int32_t *seq_lens;

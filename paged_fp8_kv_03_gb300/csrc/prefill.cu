@@ -272,8 +272,9 @@ __device__ __noinline__ float move_out(uint32_t cm, uint32_t cs, float m, float 
 // then see nothing of a tile, or of all tiles so far (its running maximum is
 // -inf until it does).  kFp4: the 4-bit cache's and, with kBlocks,
 // the block-scaled FP8 cache's.  kMoves: those of long contexts,
-// whose sums move on every kMove4 key tiles.
-template <bool kWin, bool kFp4, bool kMoves, bool kBlocks>
+// whose sums move on every kMove4 key tiles.  kSplit (with kWin and kBlocks): a query tile's
+// keys are shared by a.split CTAs, which leave their rows' states.
+template <bool kWin, bool kFp4, bool kMoves, bool kBlocks, bool kSplit>
 __global__ void __launch_bounds__(kPThreads, 1)
     paged_prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                          const __grid_constant__ CUtensorMap tm_v, const PrefillArgs a, const KeyWindow win)
@@ -311,9 +312,16 @@ __global__ void __launch_bounds__(kPThreads, 1)
     const int pos0 = L - n + t0;                         // position of its first token
     const int last = pos0 + nv - 1;                      // largest position in the tile
     const KeyTiles kt = key_tiles<kWin>(win, pos0);      // what some row of this tile sees
-    const int nt = last / kKeys + 1 - kt.skip;           // key tiles to visit
+    const int all = last / kKeys + 1 - kt.skip;          // key tiles to visit
+    const KeyShare share = kSplit ? key_share(all, blockIdx.y, a.split) : KeyShare{1, 0, all};
+    if (kSplit && static_cast<int>(blockIdx.y) >= share.parts)
+        return;
+    const int nt = share.end - share.begin;
     // the i-th one, and where it lies in the sequence's copy
-    auto key_tile = [&](int i) { return !kWin || i < kt.first ? i : i + kt.skip; };
+    auto key_tile = [&](int j) {
+        const int i = kSplit ? share.begin + j : j;
+        return !kWin || i < kt.first ? i : i + kt.skip;
+    };
     auto copy_tile = [&](int i) {
         const int t = key_tile(i);
         return !kWin || t < seq_kt.first ? t : t - seq_kt.skip;
@@ -707,7 +715,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
             const float inv = (kBlocks ? 1.f : __ldg(a.v_scale + h)) / (l + red_l[(half ^ 1) * kRows + row]);
             const int64_t orow = (static_cast<int64_t>(q0) + t0 + tl) * a.hq + h * G + g;
             uint32_t nans = 0;
-            if (kFp4)
+            if (kFp4 && !kSplit)
                 nans = nan_blocks<kWin>(a, win, row0 / kKeys, nt, valid ? pos0 + tl : last, lane, key_tile, copy_tile);
             const bool have_o = nt > kFold;                // at least one segment was folded into O
 #pragma unroll 1
@@ -720,18 +728,25 @@ __global__ void __launch_bounds__(kPThreads, 1)
                 if (!valid)
                     continue;
                 float v[16];
-                const float f = kFp4 && ((nans >> (4 * half + c)) & 1u) ? NAN : inv;
+                const float f = kSplit ? 1.f : (kFp4 && ((nans >> (4 * half + c)) & 1u) ? NAN : inv);
 #pragma unroll
                 for (int k = 0; k < 16; ++k)
                     v[k] = ((have_o ? __uint_as_float(t[k]) : 0.f) + __uint_as_float(o[k])) * f;
-                if (kBlocks) {                           // (apart: their product may lie below fp32's range)
+                if (kBlocks && !kSplit) {                // (apart: their product may lie below fp32's range)
                     const float unit = fabsf(*reinterpret_cast<const float *>(smem + PS::kFactor));
 #pragma unroll
                     for (int k = 0; k < 16; ++k)
                         v[k] *= unit;
                 }
                 const int d0 = 64 * half + 16 * c;
-                if (a.out_f32) {
+                if (kSplit) {
+                    float *to = split_row(a, 1, blockIdx.x, blockIdx.y, row);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        reinterpret_cast<float4 *>(to + d0)[k] = make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
+                    if (d0 == 0)
+                        *reinterpret_cast<float2 *>(to + kHeadDim) = make_float2(m, l + red_l[kRows + row]);
+                } else if (a.out_f32) {
                     float4 *dst = reinterpret_cast<float4 *>(static_cast<float *>(a.out) + orow * kHeadDim + d0);
 #pragma unroll
                     for (int k = 0; k < 4; ++k)
@@ -759,12 +774,12 @@ __global__ void __launch_bounds__(kPThreads, 1)
         tc::fence_after();
         tc::tmem_dealloc(tm, 512);
     }
-    if (kBlocks && *reinterpret_cast<volatile float *>(smem + PS::kFactor) < 0.f)
+    if (kBlocks && !kSplit && *reinterpret_cast<volatile float *>(smem + PS::kFactor) < 0.f)
         put_nans<kWin>(a, win, 1, kPThreads);
 }
 
 std::mutex g_prefill_mu;
-unsigned long long g_prefill_attr_ctx[64][9] = {};   // per device and kernel: the context its limit was raised in
+unsigned long long g_prefill_attr_ctx[64][10] = {};   // per device and kernel: the context its limit was raised in
 
 typedef void (*PrefillKernel)(const CUtensorMap, const CUtensorMap, const CUtensorMap, const PrefillArgs,
                               const KeyWindow);
@@ -815,7 +830,8 @@ cudaError_t launch_attention(PrefillKernel kernel, size_t smem, const PrefillArg
                              cudaStream_t stream)
 {
     const int64_t grid = static_cast<int64_t>(a.batch) * a.hkv * a.max_tiles;
-    kernel<<<static_cast<unsigned>(grid), kPThreads, smem, stream>>>(tm_q, tm_k16, tm_v16, a, win);
+    const unsigned parts = a.v_refs && a.split > 1 ? static_cast<unsigned>(a.split) : 1u;
+    kernel<<<dim3(static_cast<unsigned>(grid), parts), kPThreads, smem, stream>>>(tm_q, tm_k16, tm_v16, a, win);
     return cudaGetLastError();
 }
 
@@ -832,8 +848,8 @@ cudaError_t launch_paged_prefill(const PrefillArgs &a, const CUtensorMap &tm_q, 
     if (static_cast<int64_t>(a.batch) * a.hkv * a.max_tiles <= 0)
         return cudaSuccess;
     const KeyWindow none = {0, 0};
-    const PrefillKernel kernel = paged_prefill_kernel<false, false, false, false>;
-    cudaError_t e = raise_limit(kernel, 8, PS::bytes(false));
+    const PrefillKernel kernel = paged_prefill_kernel<false, false, false, false, false>;
+    cudaError_t e = raise_limit(kernel, 9, PS::bytes(false));
     if (e == cudaSuccess)
         e = launch_widen(a, stream);
     return e == cudaSuccess ? launch_attention(kernel, PS::bytes(false), a, none, tm_q, tm_k16, tm_v16, stream) : e;
@@ -848,14 +864,18 @@ cudaError_t launch_prefill_windowed(const PrefillArgs &a, const KeyWindow &win, 
     // The moving kernel takes 6% longer (4096 of 16384 tokens, 64 query heads: 2.03 ms
     // instead of 1.92) or 9% (1024 of 131072: 5.26 ms instead of 4.83); up to 128 key
     // tiles l has at most 128 additions (2^-17) and O 32 without it.
-    const bool moves = most_key_tiles(a, win) > 2 * kMove4;
-    const int which = (win.window > 0 ? 1 : 0) + (moves ? 2 : 0) + (a.v_refs ? 4 : 0);
-    static const PrefillKernel kernels[8] = {
-        paged_prefill_kernel<false, true, false, false>, paged_prefill_kernel<true, true, false, false>,
-        paged_prefill_kernel<false, true, true, false>,  paged_prefill_kernel<true, true, true, false>,
-        paged_prefill_kernel<false, true, false, true>,  paged_prefill_kernel<true, true, false, true>,
-        paged_prefill_kernel<false, true, true, true>,   paged_prefill_kernel<true, true, true, true>};
+    const bool split = a.v_refs && a.split > 1;          // (then no CTA has as many key tiles)
+    const bool moves = !split && most_key_tiles(a, win) > 2 * kMove4;
+    const int which = split ? 8 : (win.window > 0 ? 1 : 0) + (moves ? 2 : 0) + (a.v_refs ? 4 : 0);
+    static const PrefillKernel kernels[9] = {
+        paged_prefill_kernel<false, true, false, false, false>, paged_prefill_kernel<true, true, false, false, false>,
+        paged_prefill_kernel<false, true, true, false, false>,  paged_prefill_kernel<true, true, true, false, false>,
+        paged_prefill_kernel<false, true, false, true, false>,  paged_prefill_kernel<true, true, false, true, false>,
+        paged_prefill_kernel<false, true, true, true, false>,   paged_prefill_kernel<true, true, true, true, false>,
+        paged_prefill_kernel<true, true, false, true, true>};
     const PrefillKernel kernel = kernels[which];
+    // (the split kernels mask as under a window)
+    const KeyWindow seen = split && win.window == 0 ? KeyWindow{kNoWindow, 0} : win;
     cudaError_t e = cudaSuccess;
     if (a.out_f32)
         e = raise_limit(kernel, which, PS::bytes(moves));
@@ -863,8 +883,9 @@ cudaError_t launch_prefill_windowed(const PrefillArgs &a, const KeyWindow &win, 
         e = widen(a, win, stream);
     if (e != cudaSuccess)
         return e;
-    return a.out_f32 ? launch_attention(kernel, PS::bytes(moves), a, win, tm_q, tm_k16, tm_v16, stream)
-                     : launch_prefill_pair(a, win, tm_q, tm_k16, tm_v16, stream);
+    e = a.out_f32 ? launch_attention(kernel, PS::bytes(moves), a, seen, tm_q, tm_k16, tm_v16, stream)
+                  : launch_prefill_pair(a, seen, tm_q, tm_k16, tm_v16, stream);
+    return e == cudaSuccess && split ? launch_prefill_join(a, seen, stream) : e;
 }
 
 }  // namespace pkv

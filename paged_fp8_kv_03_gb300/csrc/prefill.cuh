@@ -196,6 +196,31 @@ __device__ __forceinline__ KeyTiles key_tiles(const KeyWindow &w, int first_pos)
     return k;
 }
 
+// The share of a query tile's nt key tiles (or of a pair's) that CTA `part` of `split`
+// has: at least two each, so that both tiles of a pair have one (they visit as many, but
+// for one); `parts` CTAs share them.
+struct KeyShare {
+    int parts, begin, end;
+};
+
+__device__ __forceinline__ KeyShare key_share(int nt, int part, int split)
+{
+    KeyShare s;
+    s.parts = max(1, min(split, nt >> 1));
+    s.begin = static_cast<int>(static_cast<long long>(nt) * part / s.parts);
+    s.end = static_cast<int>(static_cast<long long>(nt) * (part + 1) / s.parts);
+    return s;
+}
+
+// The state (O, then m and l) that such a CTA leaves of row `row` of its `tiles` query tiles.
+__device__ __forceinline__ float *split_row(const PrefillArgs &a, int tiles, unsigned block, unsigned part, int row)
+{
+    return a.partials + ((static_cast<int64_t>(block) * a.split + part) * (tiles * kRows) + row) * kPartialStride;
+}
+
+// For such CTAs' kernels, which mask as under a window: one that hides nothing.
+constexpr int kNoWindow = 1 << 30;
+
 // Key tiles that a query tile, or a pair of them, may visit: without a window all of
 // the longest sequence's, with one the sinks' and those that 2 tokens_per_tile +
 // window - 1 keys touch.
@@ -264,19 +289,13 @@ __device__ __forceinline__ uint8_t *nan_value_rows(const PrefillArgs &a)
     return reinterpret_cast<uint8_t *>(nan_value_tiles(a) + a.rows_cap / kKeys);
 }
 
-// What they do to the outputs: puts NaNs into the output rows of a CTA's query tiles, which have
-// been written, where they see one (the whole CTA of `threads`; `tiles`: query tiles a CTA).
-// Out of line, and from the block's number on, so that the attention's loop keeps
-// nothing for it.
+// What they do to the outputs: puts NaNs into the rows of tokens t0 .. t1 - 1 of a chunk, which have
+// been written, where they see one (the whole CTA of `threads`).
 template <bool kWin>
-__device__ __noinline__ void put_nans(const PrefillArgs &a, const KeyWindow &w, int tiles, int threads)
+__device__ __forceinline__ void put_nans_of(const PrefillArgs &a, const KeyWindow &w, int b, int h, int t0, int t1, int threads)
 {
-    const int per = (a.max_tiles + tiles - 1) / tiles;
-    const int bh = blockIdx.x / per, first = (per - 1 - (static_cast<int>(blockIdx.x) - bh * per)) * tiles;
-    const int b = bh / a.hkv, h = bh - b * a.hkv;
     const int q0 = __ldg(a.cu_q + b), n = __ldg(a.cu_q + b + 1) - q0, L = __ldg(a.seq_lens + b);
     const int off0 = __ldg(a.tile_off + b), off1 = __ldg(a.tile_off + b + 1);
-    const int t0 = first * a.tokens_per_tile, t1 = min(n, (first + tiles) * a.tokens_per_tile);   // tokens of the chunk
     const KeyTiles seq_kt = key_tiles<kWin>(w, L - n), kt = key_tiles<kWin>(w, L - n + t0);
     const int64_t tile0 = off0 + h * ((off1 - off0) / a.hkv);
     const int nt = (L - n + t1 - 1) / kKeys + 1 - kt.skip;
@@ -318,6 +337,18 @@ __device__ __noinline__ void put_nans(const PrefillArgs &a, const KeyWindow &w, 
                     static_cast<__nv_bfloat16 *>(a.out)[(row + g) * kHeadDim + 32 * j + d] = __float2bfloat16_rn(NAN);
             }
     }
+}
+
+// Those of an attention CTA's query tiles (`tiles` of them).  Out of line, and from the block's
+// number on, so that the attention's loop keeps nothing for it.
+template <bool kWin>
+__device__ __noinline__ void put_nans(const PrefillArgs &a, const KeyWindow &w, int tiles, int threads)
+{
+    const int per = (a.max_tiles + tiles - 1) / tiles;
+    const int bh = blockIdx.x / per, first = (per - 1 - (static_cast<int>(blockIdx.x) - bh * per)) * tiles;
+    const int b = bh / a.hkv, h = bh - b * a.hkv;
+    const int n = __ldg(a.cu_q + b + 1) - __ldg(a.cu_q + b);
+    put_nans_of<kWin>(a, w, b, h, first * a.tokens_per_tile, min(n, (first + tiles) * a.tokens_per_tile), threads);
 }
 
 // 128-row tiles of sequence b's widened region (all its kv heads): zero for a

@@ -291,8 +291,9 @@ __device__ __forceinline__ float lift_of(int nt)
 }
 
 // kFolds: for calls in which a query tile may visit more than kFold2 key tiles.
-// kBlocks: the block-scaled FP8 cache's.
-template <bool kWin, bool kFolds, bool kBlocks>
+// kBlocks: the block-scaled FP8 cache's.  kSplit (with kWin, as rows may see nothing of a
+// CTA's keys): a pair's keys are shared by a.split CTAs, which leave their rows' states.
+template <bool kWin, bool kFolds, bool kBlocks, bool kSplit>
 __global__ void __launch_bounds__(kThreads2, 1)
     paged_prefill_pair_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                               const __grid_constant__ CUtensorMap tm_v, const PrefillArgs a, const KeyWindow win)
@@ -320,11 +321,19 @@ __global__ void __launch_bounds__(kThreads2, 1)
     const int nv0 = min(tpt, n - t0), nv1 = max(0, min(tpt, n - t0 - tpt));   // tokens of A and of B
     const int pos0 = L - n + t0;                         // position of the first one
     const KeyTiles kt = key_tiles<kWin>(win, pos0);      // what some row of the pair sees
-    const int nt0 = (pos0 + nv0 - 1) / kKeys + 1 - kt.skip;   // key tiles that A visits
-    const int nt1 = nv1 > 0 ? (pos0 + tpt + nv1 - 1) / kKeys + 1 - kt.skip : 0;
+    const int all0 = (pos0 + nv0 - 1) / kKeys + 1 - kt.skip;  // key tiles that A visits
+    const int all1 = nv1 > 0 ? (pos0 + tpt + nv1 - 1) / kKeys + 1 - kt.skip : 0;
+    const KeyShare share = kSplit ? key_share(max(all0, all1), blockIdx.y, a.split) : KeyShare{1, 0, 0};
+    if (kSplit && static_cast<int>(blockIdx.y) >= share.parts)
+        return;
+    const int nt0 = kSplit ? min(all0, share.end) - share.begin : all0;
+    const int nt1 = kSplit && nv1 > 0 ? min(all1, share.end) - share.begin : all1;
     const int nt = max(nt0, nt1);
     // the i-th one, and where it lies in the sequence's copy
-    auto key_tile = [&](int i) { return !kWin || i < kt.first ? i : i + kt.skip; };
+    auto key_tile = [&](int j) {
+        const int i = kSplit ? share.begin + j : j;
+        return !kWin || i < kt.first ? i : i + kt.skip;
+    };
     auto copy_tile = [&](int i) {
         const int t = key_tile(i);
         return !kWin || t < seq_kt.first ? t : t - seq_kt.skip;
@@ -629,33 +638,50 @@ __global__ void __launch_bounds__(kThreads2, 1)
             tc::fence_after();
             if (kFolds && ntx > kFold2)
                 l = fold(o_tm, m, l, true, true);
-            const float inv = (kBlocks ? 1.f : __ldg(a.v_scale + h)) / l;
-            const uint32_t nans = nan_blocks<kWin>(a, win, row0 / kKeys, ntx, p_row, lane, key_tile, copy_tile);
-            const int64_t orow = (static_cast<int64_t>(q0) + t0 + x * tpt + tl) * a.hq + h * G + g;
-            uint4 *dst = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.out) + orow * kHeadDim);
+            if constexpr (kSplit) {
+                float *to = split_row(a, 2, blockIdx.x, blockIdx.y, x * kRows + row);
 #pragma unroll 1
-            for (int c = 0; c < 4; ++c) {
-                uint32_t o[32];
-                tc::ld32(o_tm + 32 * c, o);
-                tc::wait_ld();
-                if (!valid)
-                    continue;
+                for (int c = 0; c < 4; ++c) {
+                    uint32_t o[32];
+                    tc::ld32(o_tm + 32 * c, o);
+                    tc::wait_ld();
+                    if (valid)
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    uint32_t w[4];
-                    const float f = (nans >> (2 * c + (k >> 1))) & 1u ? NAN : inv;
+                        for (int k = 0; k < 8; ++k)
+                            reinterpret_cast<uint4 *>(to + 32 * c)[k] =
+                                make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+                }
+                if (valid)
+                    *reinterpret_cast<float2 *>(to + kHeadDim) = make_float2(m, l);
+            } else {
+                const float inv = (kBlocks ? 1.f : __ldg(a.v_scale + h)) / l;
+                const uint32_t nans = nan_blocks<kWin>(a, win, row0 / kKeys, ntx, p_row, lane, key_tile, copy_tile);
+                const int64_t orow = (static_cast<int64_t>(q0) + t0 + x * tpt + tl) * a.hq + h * G + g;
+                uint4 *dst = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.out) + orow * kHeadDim);
+#pragma unroll 1
+                for (int c = 0; c < 4; ++c) {
+                    uint32_t o[32];
+                    tc::ld32(o_tm + 32 * c, o);
+                    tc::wait_ld();
+                    if (!valid)
+                        continue;
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        float v0 = __uint_as_float(o[8 * k + 2 * e]) * f, v1 = __uint_as_float(o[8 * k + 2 * e + 1]) * f;
-                        if (kBlocks) {                   // (apart: their product may lie below fp32's range)
-                            const float unit = fabsf(*reinterpret_cast<const float *>(smem + P2::kFactor));
-                            v0 *= unit;
-                            v1 *= unit;
+                    for (int k = 0; k < 4; ++k) {
+                        uint32_t w[4];
+                        const float f = (nans >> (2 * c + (k >> 1))) & 1u ? NAN : inv;
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            float v0 = __uint_as_float(o[8 * k + 2 * e]) * f, v1 = __uint_as_float(o[8 * k + 2 * e + 1]) * f;
+                            if (kBlocks) {                   // (apart: their product may lie below fp32's range)
+                                const float unit = fabsf(*reinterpret_cast<const float *>(smem + P2::kFactor));
+                                v0 *= unit;
+                                v1 *= unit;
+                            }
+                            const __nv_bfloat162 b2 = __floats2bfloat162_rn(v0, v1);
+                            w[e] = *reinterpret_cast<const uint32_t *>(&b2);
                         }
-                        const __nv_bfloat162 b2 = __floats2bfloat162_rn(v0, v1);
-                        w[e] = *reinterpret_cast<const uint32_t *>(&b2);
+                        dst[4 * c + k] = make_uint4(w[0], w[1], w[2], w[3]);
                     }
-                    dst[4 * c + k] = make_uint4(w[0], w[1], w[2], w[3]);
                 }
             }
         }
@@ -667,13 +693,13 @@ __global__ void __launch_bounds__(kThreads2, 1)
         tc::fence_after();
         tc::tmem_dealloc(tm, 512);
     }
-    if (kBlocks && *reinterpret_cast<volatile float *>(smem + P2::kFactor) < 0.f)
+    if (kBlocks && !kSplit && *reinterpret_cast<volatile float *>(smem + P2::kFactor) < 0.f)
         put_nans<kWin>(a, win, 2, kThreads2);
 }
 
 std::mutex g_pair_mu;
 typedef void (*PairKernel)(const CUtensorMap, const CUtensorMap, const CUtensorMap, const PrefillArgs, const KeyWindow);
-unsigned long long g_pair_ctx[64][8] = {};   // per device and kernel: the context its limit was raised in
+unsigned long long g_pair_ctx[64][9] = {};   // per device and kernel: the context its limit was raised in
 
 }  // namespace
 
@@ -696,13 +722,15 @@ cudaError_t launch_prefill_pair(const PrefillArgs &a, const KeyWindow &win, cons
     // The folding kernel takes longer even where it folds nothing (4096 of 16384 tokens, 64
     // query heads: 1172 us instead of 1153), and where it does (2048 of 131072: 6.01 ms, in
     // one chain 5.74; 1024 of 524288: 12.4 and 11.8).
-    const bool folds = most_key_tiles(a, win) > kFold2;
-    const int which = (win.window > 0 ? 1 : 0) + (folds ? 2 : 0) + (a.v_refs ? 4 : 0);
-    static const PairKernel kernels[8] = {
-        paged_prefill_pair_kernel<false, false, false>, paged_prefill_pair_kernel<true, false, false>,
-        paged_prefill_pair_kernel<false, true, false>,  paged_prefill_pair_kernel<true, true, false>,
-        paged_prefill_pair_kernel<false, false, true>,  paged_prefill_pair_kernel<true, false, true>,
-        paged_prefill_pair_kernel<false, true, true>,   paged_prefill_pair_kernel<true, true, true>};
+    const bool split = a.v_refs && a.split > 1;          // (then no CTA has kFold2 key tiles)
+    const bool folds = !split && most_key_tiles(a, win) > kFold2;
+    const int which = split ? 8 : (win.window > 0 ? 1 : 0) + (folds ? 2 : 0) + (a.v_refs ? 4 : 0);
+    static const PairKernel kernels[9] = {
+        paged_prefill_pair_kernel<false, false, false, false>, paged_prefill_pair_kernel<true, false, false, false>,
+        paged_prefill_pair_kernel<false, true, false, false>,  paged_prefill_pair_kernel<true, true, false, false>,
+        paged_prefill_pair_kernel<false, false, true, false>,  paged_prefill_pair_kernel<true, false, true, false>,
+        paged_prefill_pair_kernel<false, true, true, false>,   paged_prefill_pair_kernel<true, true, true, false>,
+        paged_prefill_pair_kernel<true, false, true, true>};
     const PairKernel kernel = kernels[which];
     int dev = -1;
     cudaError_t e = cudaGetDevice(&dev);
@@ -723,7 +751,8 @@ cudaError_t launch_prefill_pair(const PrefillArgs &a, const KeyWindow &win, cons
         }
     }
     const int64_t grid = static_cast<int64_t>(a.batch) * a.hkv * ((a.max_tiles + 1) / 2);
-    kernel<<<static_cast<unsigned>(grid), kThreads2, P2::bytes(folds), stream>>>(tm_q, tm_k16, tm_v16, a, win);
+    kernel<<<dim3(static_cast<unsigned>(grid), split ? static_cast<unsigned>(a.split) : 1u), kThreads2, P2::bytes(folds),
+             stream>>>(tm_q, tm_k16, tm_v16, a, win);
     return cudaGetLastError();
 }
 

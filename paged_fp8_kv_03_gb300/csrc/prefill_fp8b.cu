@@ -8,7 +8,11 @@
 // largest V.  The output is multiplied by 2^(E - 6).  NaN codes of V become zeros
 // and are recorded, a bit a value.
 //
-// Two launches.  kv_refs_fp8b_kernel: a cluster of CTAs a sequence takes the maximum
+// Two launches, and a third behind the attention where few rows have a long past: its
+// CTAs then share a query tile's keys, and prefill_join_fp8b_kernel joins what they leave
+// (64 tokens of 32 query and 8 kv heads, past 32768: 93 us, else 427; 8 query heads of one
+// kv head, past 131072: 91 us, else 1525).
+// kv_refs_fp8b_kernel: a cluster of CTAs a sequence takes the maximum
 // of the bytes (a sixteenth of a byte a token and head), and CTA 0 lays out the
 // regions.  kv_widen_fp8b_kernel: a CTA half a tile of 128 rows (or a quarter of one,
 // where there are few); a thread takes 8 values of kRowsEach of its rows, of K and of V, 16
@@ -212,7 +216,135 @@ __global__ void __launch_bounds__(256) kv_widen_fp8b_kernel(const PrefillArgs a,
     }
 }
 
+// Joins the states of the CTAs that shared a query tile's keys: a warp a row, a lane four
+// dims; the weight of a part is 2^(m - the parts' largest m).  A part whose keys the row
+// does not see has m = -inf.  A CTA has kJoinRows rows or one token's.
+constexpr int kJoinThreads = 256, kJoinRows = 8;
+
+__global__ void __launch_bounds__(kJoinThreads) prefill_join_fp8b_kernel(const PrefillArgs a, const KeyWindow win)
+{
+    grid_wait();
+    const int tiles = a.out_f32 ? 1 : 2, per = (a.max_tiles + tiles - 1) / tiles;   // of an attention CTA
+    const int bh = static_cast<int>(blockIdx.x) / per, first = (per - 1 - (static_cast<int>(blockIdx.x) - bh * per)) * tiles;
+    const int b = bh / a.hkv, h = bh - b * a.hkv, G = a.group, tpt = a.tokens_per_tile;
+    const int q0 = __ldg(a.cu_q + b), q1 = __ldg(a.cu_q + b + 1), n = q1 - q0, L = __ldg(a.seq_lens + b);
+    if (!sequence_ok(a, b, q0, q1, L, false) || a.tile_off[b + 1] > a.rows_cap / kKeys)
+        return;
+    const int begin = first * tpt, end = min(n, begin + tiles * tpt), per_cta = max(1, kJoinRows / G);
+    const int t0 = begin + static_cast<int>(blockIdx.y) * per_cta, t1 = min(end, t0 + per_cta);
+    if (t0 >= t1)
+        return;
+    const int nt = (L - n + end - 1) / kKeys + 1 - key_tiles<true>(win, L - n + begin).skip;
+    const int parts = key_share(nt, 0, a.split).parts;
+    const float unit = a.v_refs[bh];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    for (int r = warp; r < (t1 - t0) * G; r += kJoinThreads / 32) {
+        const int t = t0 + r / G, g = r % G, x = (t - begin) / tpt;
+        const float *at = split_row(a, tiles, blockIdx.x, 0, x * kRows + (t - begin - x * tpt) * G + g);
+        const int64_t stride = static_cast<int64_t>(tiles) * kRows * kPartialStride;
+        float top = -INFINITY;
+        for (int p = lane; p < parts; p += 32)
+            top = fmaxf(top, __ldcg(at + p * stride + kHeadDim));
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1)
+            top = fmaxf(top, __shfl_xor_sync(kAll, top, o));
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        float sum = 0.f;
+        for (int p0 = 0; p0 < parts; p0 += 32) {
+            float weight = 0.f, l = 0.f;
+            if (p0 + lane < parts) {
+                const float2 s = __ldcg(reinterpret_cast<const float2 *>(at + (p0 + lane) * stride + kHeadDim));
+                weight = s.x == -INFINITY ? 0.f : ex2_approx(s.x - top);
+                l = s.y;
+            }
+            sum += weight * l;                           // (a lane's own parts; a NaN stays one)
+#pragma unroll 8
+            for (int p = 0; p < min(32, parts - p0); ++p) {
+                const float4 o = __ldcg(reinterpret_cast<const float4 *>(at + (p0 + p) * stride) + lane);
+                const float f = __shfl_sync(kAll, weight, p);
+                acc.x += f * o.x;
+                acc.y += f * o.y;
+                acc.z += f * o.z;
+                acc.w += f * o.w;
+            }
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1)
+            sum += __shfl_xor_sync(kAll, sum, o);
+        // (apart: their product may lie below fp32's range)
+        const float inv = 1.f / sum, scale = fabsf(unit);
+        acc = make_float4(acc.x * inv * scale, acc.y * inv * scale, acc.z * inv * scale, acc.w * inv * scale);
+        const int64_t row = (static_cast<int64_t>(q0) + t) * a.hq + static_cast<int64_t>(h) * G + g;
+        if (a.out_f32) {
+            reinterpret_cast<float4 *>(static_cast<float *>(a.out) + row * kHeadDim)[lane] = acc;
+        } else {
+            const __nv_bfloat162 lo = __floats2bfloat162_rn(acc.x, acc.y), hi = __floats2bfloat162_rn(acc.z, acc.w);
+            reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(a.out) + row * kHeadDim)[lane] =
+                make_uint2(*reinterpret_cast<const uint32_t *>(&lo), *reinterpret_cast<const uint32_t *>(&hi));
+        }
+    }
+    if (unit < 0.f) {
+        __syncthreads();
+        put_nans_of<true>(a, win, b, h, t0, t1, kJoinThreads);
+    }
+}
+
+// Where query tiles fill half of the SMs at most, as many CTAs share each one's keys as fill them
+// once.  A part has two key tiles at least, four where a row has more than 32 parts (64 tokens,
+// 8 query heads of 1 kv head, past 16384: in 64 parts of two 52 us, in 32 of four 44, in one 198),
+// and kMostPart at most, as the attention kernels then sum in one chain; so a long context has
+// more parts.  A CTA has to be spared kLeastSpared of them, as leaving and joining the states
+// takes as long as some (64 tokens, past 1024, 8 kv heads: 2 key tiles instead of 8 30.8 us, else
+// 31.9; 9 sequences of 1100: 5 instead of 9 42.1 us, else 40.1).
+constexpr int kSplitSms = 152, kMostPart = 128, kLeastSpared = 6;
+
+int split_of(int64_t ctas, int64_t most)
+{
+    if (ctas <= 0 || 2 * ctas > kSplitSms)
+        return 1;
+    const int64_t even = kSplitSms / ctas, pairs = most / 2 < 32 ? most / 2 : 32;
+    const int64_t worth = pairs > most / 4 ? pairs : most / 4, parts = even < worth ? even : worth;
+    if (parts < 2 || most - (most + parts - 1) / parts < kLeastSpared)
+        return 1;
+    const int64_t need = (most + kMostPart - 1) / kMostPart;
+    return static_cast<int>(parts > need ? parts : need);
+}
+
 }  // namespace
+
+int prefill_fp8b_split(const PrefillArgs &a, const KeyWindow &win, int longest)
+{
+    PrefillArgs bound = a;
+    bound.max_kv_len = longest;
+    const int64_t tiles = a.out_f32 ? a.max_tiles : (a.max_tiles + 1) / 2;
+    return longest > kNoWindow / 2 ? 1 : split_of(tiles * a.batch * a.hkv, most_key_tiles(bound, win));
+}
+
+size_t prefill_fp8b_split_bytes(int batch, int hkv, int max_q_len, int longest, const KeyWindow &win)
+{
+    // Between the CTAs of one query tile a kv head and of kSplitSms / 2 in all, whichever
+    // tiles the heads make: as many parts as SMs or, in long contexts, need a CTA.
+    const int64_t least = static_cast<int64_t>(batch) * hkv;
+    PrefillArgs a = {};
+    a.max_kv_len = longest;
+    a.tokens_per_tile = kRows;
+    const int64_t most = most_key_tiles(a, win);
+    if (max_q_len == 0 || split_of(least, most) == 1)
+        return 0;
+    const int64_t ctas = least * max_q_len < kSplitSms / 2 ? least * max_q_len : kSplitSms / 2;
+    const int64_t need = ctas * ((most + kMostPart - 1) / kMostPart);
+    return static_cast<size_t>(need > kSplitSms ? need : kSplitSms) * 2 * kRows * kPartialStride * sizeof(float) + 255;
+}
+
+cudaError_t launch_prefill_join(const PrefillArgs &a, const KeyWindow &win, cudaStream_t stream)
+{
+    const int tiles = a.out_f32 ? 1 : 2, per = (a.max_tiles + tiles - 1) / tiles;
+    const int per_cta = kJoinRows / a.group > 1 ? kJoinRows / a.group : 1;
+    const int tokens = a.max_q_len < tiles * a.tokens_per_tile ? a.max_q_len : tiles * a.tokens_per_tile;
+    return launch_with(prefill_join_fp8b_kernel,
+                       dim3(static_cast<unsigned>(a.batch * a.hkv * per), static_cast<unsigned>((tokens + per_cta - 1) / per_cta)),
+                       kJoinThreads, 0, 1, true, stream, a, win);
+}
 
 cudaError_t launch_widen_fp8b(const PrefillArgs &a, const KeyWindow &win, cudaStream_t stream)
 {

@@ -115,6 +115,18 @@ def test_more_refusals(lib):
         assert pkv.pkv_prefill_fp8b_workspace_size(*bad) == 0, bad
 
 
+def test_prefill_workspace_of_few_rows():
+    """Room for the states of the CTAs that share a query tile's keys, where there may be such."""
+    size = pkv.pkv_prefill_fp8b_workspace_size
+    copies = lambda b, h, tiles: 256 * h * ((tiles * 128 * (512 + 16) + tiles * 8) // 256) + 4096 * b  # noqa: E731 (about)
+    assert size(1, 8, 64, 1024) - size(1, 8, 64, 896) > 152 * 256 * 528      # 8 key tiles: shared
+    assert size(10, 8, 64, 1024) < copies(10, 8, 80) + 100000                # more CTAs than half the SMs
+    assert size(1, 8, 64, 32768, 0, 500, 0) < copies(1, 8, 8) + 100000       # a window that hides the past
+    assert size(1, 8, 64, 1 << 20, 890) < copies(1, 8, 9) + 100000           # no sequence that long
+    # a long context has as many parts as keep each at 128 key tiles
+    assert size(9, 8, 64, 1 << 20, 1 << 20) - copies(9, 8, 8192 + 9) > 76 * 64 * 256 * 528 - 100000
+
+
 def test_plan_calls_refuse(lib):
     for call in (_plan, _release):
         for bad, status in ((dict(B=-1), SHAPE), (dict(maxp=0), SHAPE), (dict(np_=0), SHAPE), (dict(P=8), UNSUPPORTED),

@@ -390,12 +390,20 @@ def _tight(q, k, v, p, window, sinks, sm):
     largest score when it is set and moves only upwards, so the largest P is at least
     2^12, and 2^-24 is 2^-36 of the largest weight, for each key: 2^-36 w_max sum |v|.
     (Decode refers weights to the largest contribution instead.)
+
+    Where CTAs share a row's keys, n of them, each part's sums are weighted and added, of
+    the outputs and of the weights: the exponential (2^-22), its argument's rounding (m - M
+    is off by 2^-24 of itself, and 2^(m - M) |m - M| ln 2 < 1), the product and n additions
+    (2^-24 each), twice: 2 (n + 6) 2^-24 sum w |v|.  A part has two key tiles or more.
     """
     Hq, g = q.shape[0], q.shape[0] // k.shape[1]
     t = fp4_ref.visible(p, window, sinks)
     s = np.einsum("hd,thd->ht", q, np.repeat(k[t], g, 1)) * sm
     w = np.exp(s - s.max(1, keepdims=True))
     lost = 2.0 ** -36 / w.sum(1)[:, None] * np.repeat(np.abs(v[t]).sum(0), g, 0)
+    parts = (p // 128 + 1) // 2
+    if parts > 1:
+        lost = lost + 2 * (parts + 6) * 2.0 ** -24 / w.sum(1)[:, None] * np.einsum("ht,thd->hd", w, np.abs(np.repeat(v[t], g, 1)))
     return fp4_tight.tolerance(q, k, v, p, window, sinks, sm) + lost
 
 
@@ -495,6 +503,93 @@ def test_prefill_nan_codes(pkv, cuda_device, out_dtype, window, sinks):
     seen = torch.tensor([200 in fp4_ref.visible(L - n + r, window, sinks) for r in range(n)], device=cuda_device)
     got = run()
     assert torch.isnan(got[seen]).all() and torch.equal(torch.isnan(got[~seen]), want[~seen])
+
+
+# Few rows over a long past: CTAs share a query tile's keys.  Lengths around the parts' ends (4 key
+# tiles of 128 in the longest sequence, 2 at least in others: of 897 tokens' 256 queries the first
+# ones see nothing of the last part), a sequence with one part, one of no tokens, more parts than lanes.
+FEW_ROWS = [([1024], [1], 1, 1), ([1025], [129], 2, 8), ([897, 4096, 130, 3, 0, 2049], [256, 1, 130, 3, 0, 200], 1, 1),
+            ([2000, 1100], [64, 0], 8, 4), ([1500, 3100], [40, 33], 3, 5), ([20000], [17], 1, 2)]
+
+
+@pytest.mark.parametrize("lens,ns,hkv,G", FEW_ROWS)
+@pytest.mark.parametrize("window,sinks", [(0, 0), (1200, 0), (1100, 300)])
+@pytest.mark.parametrize("out_dtype", [torch.float32, torch.bfloat16])
+def test_prefill_few_rows_over_a_long_past(pkv, cuda_device, lens, ns, hkv, G, window, sinks, out_dtype):
+    c = Cache(len(lens) + max(lens), lens, hkv, 16, cuda_device)
+    _prefill(pkv, c, ns, hkv * G, window, sinks, out_dtype, sample=8)
+
+
+@pytest.mark.parametrize("out_dtype", [torch.float32, torch.bfloat16])
+def test_prefill_parts_of_a_long_context(pkv, cuda_device, out_dtype):
+    """So many sequences that the longest one's parts would be above 128 key tiles: there are more of them."""
+    c = Cache(21, [1] * 30 + [40000] + [200] * 39, 1, 64, cuda_device)
+    _prefill(pkv, c, [1] * 30 + [5] + [7] * 39, 2, out_dtype=out_dtype, sample=2)
+
+
+@pytest.mark.parametrize("out_dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("window,sinks", [(0, 0), (1300, 130)])
+def test_prefill_few_rows_nan_codes(pkv, cuda_device, out_dtype, window, sinks):
+    """NaNs of V and of K in several parts of the keys."""
+    L, n, at = 2100, 150, {129: 5, 700: 64, 1990: 127, 2060: 0, 2099: 5}
+    c = Cache(22, [L], 1, 16, cuda_device)
+    cu = torch.tensor([0, n], dtype=torch.int32, device=cuda_device)
+    q, qd = c.queries(n, 3)
+
+    def run():
+        return pkv.paged_prefill_fp8b(qd, cu, *c.args, c.tabled, c.lensd, n, max_kv_len=L, out_dtype=out_dtype,
+                                      window=window, sinks=sinks)
+
+    def seen(t):
+        return torch.tensor([t in fp4_ref.visible(L - n + r, window, sinks) for r in range(n)], device=cuda_device)
+
+    base = run()
+    slot = fp4_ref.slots_of(c.table[0], L, 16)
+    for t, d in at.items():
+        c.args[1].view(-1, 128)[int(slot[t]), d] = 0xFF
+    got = run()
+    want = torch.zeros_like(got, dtype=torch.bool)
+    for t, d in at.items():
+        want[seen(t), :, d] = True
+    assert torch.equal(torch.isnan(got), want)
+    assert torch.equal(got[~want], base[~want])
+    for t in (805, 2080):
+        before = c.args[0].view(-1, 128)[int(slot[t]), 9].clone()
+        c.args[0].view(-1, 128)[int(slot[t]), 9] = 0x7F
+        bad = seen(t)
+        got = run()
+        assert torch.isnan(got[bad]).all() and torch.equal(torch.isnan(got[~bad]), want[~bad])
+        c.args[0].view(-1, 128)[int(slot[t]), 9] = before
+
+
+@pytest.mark.parametrize("out_dtype", [torch.float32, torch.bfloat16])
+def test_prefill_few_rows_captured(pkv, cuda_device, out_dtype):
+    """Nothing of the workspace is read that the call has not written; a replay after the lengths have changed."""
+    lens, ns = [897, 3000, 700, 90], [256, 20, 1, 90]
+    c = Cache(23, lens, 2, 16, cuda_device)
+    cu = _dev(np.concatenate(([0], np.cumsum(ns))).astype(np.int32), cuda_device)
+    _, qd = c.queries(int(cu[-1]), 8)
+    n = pkv.pkv_prefill_fp8b_workspace_size(4, 2, 256, 3000)
+    ws = torch.full((n,), 0xFF, dtype=torch.uint8, device=cuda_device)
+    got = torch.empty(qd.shape, dtype=out_dtype, device=cuda_device)
+
+    def call(out, **kw):
+        return pkv.paged_prefill_fp8b(qd, cu, *c.args, c.tabled, c.lensd, 256, out=out, max_kv_len=3000, **kw)
+
+    want = call(torch.empty_like(got))
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        call(got, workspace=ws)
+    g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(got, want) and not torch.isnan(want).any()
+    c.lensd[1] = 1000
+    c.lensd[2] = 1
+    g.replay()
+    ws.fill_(0xFF)
+    assert torch.equal(got, call(torch.empty_like(got)))
+    with pytest.raises(pkv.PkvError):
+        call(got, workspace=ws[:n - 512])
 
 
 def test_prefill_bad_input(pkv, cuda_device):
