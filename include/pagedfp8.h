@@ -702,7 +702,7 @@ pkv_status pkv_paged_gqa_decode_fp8b(const void *q,
  * type say), and their sums are joined in order.  num_kv_heads is at most 8192.
  *
  *   workspace      device, >= pkv_prefill_fp8b_workspace_size(...) bytes for the same
- *                  bounds, 256-byte aligned.  Where CTAs may share keys it has 41 MB for
+ *                  bounds, 256-byte aligned.  Where CTAs may share keys it has 21 MB for
  *                  them, or more for long contexts.
  */
 size_t pkv_prefill_fp8b_workspace_size(int batch, int num_kv_heads, int max_q_len, int max_kv_len,
