@@ -300,6 +300,8 @@ __global__ void __launch_bounds__(kPThreads, 1)
         return;
     // this sequence's widened region (laid out by the widening kernel); a
     // region past the workspace was flagged there and is not attended
+    if (kBlocks)
+        grid_wait();                                     // for the widening
     const int off0 = __ldg(a.tile_off + b), off1 = __ldg(a.tile_off + b + 1);
     const KeyTiles seq_kt = key_tiles<kWin>(win, L - n);
     if (off1 > a.rows_cap / 128 || off1 - off0 != a.hkv * ((L + kKeys - 1) / kKeys - seq_kt.skip))
@@ -360,7 +362,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
             mbar_init(bar(PS::LX + i), 64);
         *abort_flag = 0;
         if (kBlocks)
-            *reinterpret_cast<volatile float *>(smem + PS::kFactor) = __ldg(a.v_refs + bh);
+            *reinterpret_cast<volatile float *>(smem + PS::kFactor) = __ldcg(a.v_refs + bh);
         fence_barrier_init();
     }
     if (warp == 1) {
@@ -829,9 +831,10 @@ cudaError_t launch_attention(PrefillKernel kernel, size_t smem, const PrefillArg
                              const CUtensorMap &tm_q, const CUtensorMap &tm_k16, const CUtensorMap &tm_v16,
                              cudaStream_t stream)
 {
-    const int64_t grid = static_cast<int64_t>(a.batch) * a.hkv * a.max_tiles;
-    const unsigned parts = a.v_refs && a.split > 1 ? static_cast<unsigned>(a.split) : 1u;
-    kernel<<<dim3(static_cast<unsigned>(grid), parts), kPThreads, smem, stream>>>(tm_q, tm_k16, tm_v16, a, win);
+    const dim3 grid(static_cast<unsigned>(a.batch * a.hkv * a.max_tiles), a.v_refs && a.split > 1 ? static_cast<unsigned>(a.split) : 1u);
+    if (a.v_refs)
+        return launch_with(kernel, grid, kPThreads, smem, 1, true, stream, tm_q, tm_k16, tm_v16, a, win);
+    kernel<<<grid, kPThreads, smem, stream>>>(tm_q, tm_k16, tm_v16, a, win);
     return cudaGetLastError();
 }
 

@@ -310,6 +310,8 @@ __global__ void __launch_bounds__(kThreads2, 1)
     const int L = __ldg(a.seq_lens + b);
     if (!sequence_ok(a, b, q0, q1, L, qp == 0 && h == 0 && threadIdx.x == 0))
         return;
+    if (kBlocks)
+        grid_wait();                                     // for the widening
     const int off0 = __ldg(a.tile_off + b), off1 = __ldg(a.tile_off + b + 1);
     const KeyTiles seq_kt = key_tiles<kWin>(win, L - n);
     if (off1 > a.rows_cap / 128 || off1 - off0 != a.hkv * ((L + kKeys - 1) / kKeys - seq_kt.skip))
@@ -353,7 +355,7 @@ __global__ void __launch_bounds__(kThreads2, 1)
             mbar_init(bar(i), i >= P2::Q_READY && i < P2::K_FULL ? 4 : (i >= P2::P_FULL && i < P2::PV_DONE ? 4 : 1));
         *abort_flag = 0;
         if (kBlocks)
-            *reinterpret_cast<volatile float *>(smem + P2::kFactor) = __ldg(a.v_refs + bh);
+            *reinterpret_cast<volatile float *>(smem + P2::kFactor) = __ldcg(a.v_refs + bh);
         fence_barrier_init();
     }
     if (warp == 1) {
@@ -750,9 +752,10 @@ cudaError_t launch_prefill_pair(const PrefillArgs &a, const KeyWindow &win, cons
             g_pair_ctx[dev][which] = known ? ctx : 0;
         }
     }
-    const int64_t grid = static_cast<int64_t>(a.batch) * a.hkv * ((a.max_tiles + 1) / 2);
-    kernel<<<dim3(static_cast<unsigned>(grid), split ? static_cast<unsigned>(a.split) : 1u), kThreads2, P2::bytes(folds),
-             stream>>>(tm_q, tm_k16, tm_v16, a, win);
+    const dim3 grid(static_cast<unsigned>(a.batch * a.hkv * ((a.max_tiles + 1) / 2)), split ? static_cast<unsigned>(a.split) : 1u);
+    if (a.v_refs)
+        return launch_with(kernel, grid, kThreads2, P2::bytes(folds), 1, true, stream, tm_q, tm_k16, tm_v16, a, win);
+    kernel<<<grid, kThreads2, P2::bytes(folds), stream>>>(tm_q, tm_k16, tm_v16, a, win);
     return cudaGetLastError();
 }
 

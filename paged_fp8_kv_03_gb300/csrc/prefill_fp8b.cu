@@ -124,6 +124,7 @@ __global__ void __launch_bounds__(256) kv_widen_fp8b_kernel(const PrefillArgs a,
     static_assert(kPieces == 2 || kPieces == 4, "a tile's word has two bytes or one a piece");
     const int tid = threadIdx.x;
     const int part = tid & 15;                           // dims 8 part .. 8 part + 7
+    launch_dependents();
     grid_wait();
     const long long cap_tiles = a.rows_cap / kKeys;
     const int *off = a.tile_off;
