@@ -308,10 +308,10 @@ __global__ void __launch_bounds__(kThreads2, 1)
     const int q0 = __ldg(a.cu_q + b), q1 = __ldg(a.cu_q + b + 1);
     const int n = q1 - q0;
     const int L = __ldg(a.seq_lens + b);
+    if (kBlocks)
+        grid_wait();                                     // for the widening (every CTA, so that this ends after it)
     if (!sequence_ok(a, b, q0, q1, L, qp == 0 && h == 0 && threadIdx.x == 0))
         return;
-    if (kBlocks)
-        grid_wait();                                     // for the widening
     const int off0 = __ldg(a.tile_off + b), off1 = __ldg(a.tile_off + b + 1);
     const KeyTiles seq_kt = key_tiles<kWin>(win, L - n);
     if (off1 > a.rows_cap / 128 || off1 - off0 != a.hkv * ((L + kKeys - 1) / kKeys - seq_kt.skip))
