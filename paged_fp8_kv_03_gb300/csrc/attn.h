@@ -99,7 +99,13 @@ cudaError_t launch_prefill_join(const PrefillArgs &a, const KeyWindow &win, cuda
 
 // Launches clusters of `cluster` CTAs (1: none), and, if `early`, with
 // programmatic stream serialization: the kernel may be brought onto the GPU
-// before the one ahead of it has ended, and waits for that with grid_wait().
+// before the one ahead of it has ended, and waits for that with grid_wait(), ahead of
+// anything it reads or writes and in every CTA (a grid that ended without waiting could
+// let what follows begin beside what is ahead).  The block-scaled cache's and the plan's
+// calls are all launched this way: one behind another from Python, append and read back of
+// 64 tokens 5.4 us, else 10.2; plan and release 6.8 and 10.8; a decode of two short
+// sequences 4.4 and 6.1.  The rows' and the plan's kernels let the next in as they end, not
+// when they start (1021 requests planned 10.1 us a pass in a graph, 13.3 that way).
 template <typename... Params, typename... Args>
 cudaError_t launch_with(void (*kernel)(Params...), dim3 grid, unsigned threads, size_t smem, int cluster, bool early,
                         cudaStream_t stream, const Args &...args)

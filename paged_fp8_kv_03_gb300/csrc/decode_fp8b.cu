@@ -658,6 +658,7 @@ __global__ void __launch_bounds__(kListThreads, kListCtas)
     int *sums = reinterpret_cast<int *>(smem + ListSmem::kSums);
     if (tid < 2)
         prefetch_tensormap(tid ? &tm_v : &tm_k);
+    grid_wait();
     const bool no_empty = list_starts<kListWarps>(a, start, sums, ListInit{smem});
     zero_rows<kListThreads>(da, start);
     launch_dependents();
@@ -716,6 +717,8 @@ __global__ void __launch_bounds__(32 * kClusterWarps, 2)
     const int b = seg / a.hkv, h = seg % a.hkv;
     if (tid < 2)
         prefetch_tensormap(tid ? &tm_v : &tm_k);
+    launch_dependents();
+    grid_wait();
     const Sight sg = sight_of(a, b);
     // the query rows: on their way while the tiles are looked up
     uint4 raw[4];
@@ -948,10 +951,10 @@ cudaError_t launch_paged_decode_fp8b(const Fp8bDecodeArgs &da, const CUtensorMap
     if (da.cluster > 0) {
         const dim3 grid(static_cast<unsigned>(da.a.batch * da.a.hkv * da.cluster));
         return launch_with(two ? paged_gqa_decode_fp8b_cluster_kernel<2> : paged_gqa_decode_fp8b_cluster_kernel<1>, grid,
-                           32 * kClusterWarps, ClusterSmem::kBytes, da.cluster, false, stream, tm_k, tm_v, da);
+                           32 * kClusterWarps, ClusterSmem::kBytes, da.cluster, true, stream, tm_k, tm_v, da);
     }
     cudaError_t e = launch_with(two ? paged_gqa_decode_fp8b_kernel<2> : paged_gqa_decode_fp8b_kernel<1>,
-                                dim3(static_cast<unsigned>(ctas)), kListThreads, decode_fp8b_smem(da.a.batch), 1, false,
+                                dim3(static_cast<unsigned>(ctas)), kListThreads, decode_fp8b_smem(da.a.batch), 1, true,
                                 stream, tm_k, tm_v, da);
     if (e != cudaSuccess)
         return e;

@@ -17,6 +17,7 @@
 // and then draws a ticket; the one that draws the last writes them.  No CTA waits for
 // another, and the ticket is on its way while the rows are filled.
 #include "api.h"
+#include "grid.cuh"
 #include "internal.h"
 
 namespace pkv {
@@ -175,6 +176,7 @@ __device__ __forceinline__ int sequence_at(const int *sums, int batch, int x)
 
 __global__ void __launch_bounds__(kThreads) plan_pages_kernel(const PlanArgs a)
 {
+    grid_wait();
     extern __shared__ int dyn[];
     __shared__ PlanSmem s;
     __shared__ int free_count;
@@ -269,6 +271,7 @@ __global__ void __launch_bounds__(kThreads) plan_pages_kernel(const PlanArgs a)
 // (past: what is kept, null for nothing; fresh: the lengths.)
 __global__ void __launch_bounds__(kThreads) release_pages_kernel(const PlanArgs a)
 {
+    grid_wait();
     extern __shared__ int dyn[];
     __shared__ PlanSmem s;
     __shared__ int free_count;
@@ -335,8 +338,8 @@ cudaError_t launch_plan(void (*kernel)(const PlanArgs), const PlanArgs &a, long 
     if (most <= 0)
         return cudaErrorInvalidConfiguration;
     const long long want = (items + 4 * kThreads - 1) / (4 * kThreads);
-    kernel<<<static_cast<unsigned>(want < 1 ? 1 : (want < most ? want : most)), kThreads, smem, stream>>>(a);
-    return cudaGetLastError();
+    return launch_with(kernel, dim3(static_cast<unsigned>(want < 1 ? 1 : (want < most ? want : most))), kThreads, smem, 1, true,
+                       stream, a);
 }
 
 }  // namespace

@@ -72,6 +72,7 @@ __global__ void __launch_bounds__(kRefThreads) kv_refs_fp8b_kernel(const Prefill
     extern __shared__ int top[];                         // [hkv]: largest byte
     __shared__ int warp_sum[kRefThreads / 32];
     launch_dependents();
+    grid_wait();
     const int rank = static_cast<int>(blockIdx.x) % ctas, b = static_cast<int>(blockIdx.x) / ctas;
     if (b == a.batch) {
         if (rank == 0)
@@ -352,7 +353,7 @@ cudaError_t launch_widen_fp8b(const PrefillArgs &a, const KeyWindow &win, cudaSt
     // (clusters pay from a few thousand tokens on)
     const int ctas = a.max_kv_len <= 4096 ? 1 : kRefCtas;
     const cudaError_t e = launch_with(kv_refs_fp8b_kernel, dim3(static_cast<unsigned>((a.batch + 1) * ctas)), kRefThreads,
-                                      static_cast<size_t>(a.hkv) * sizeof(int), ctas, false, stream, a, win, ctas);
+                                      static_cast<size_t>(a.hkv) * sizeof(int), ctas, true, stream, a, win, ctas);
     if (e != cudaSuccess)
         return e;
     const int64_t tiles = a.rows_cap / kKeys, most = static_cast<int64_t>(device_sm_count()) * 8;

@@ -20,6 +20,7 @@
 //
 // What bounds them: the bytes, 256 or 512 a row of the call and 128 of the cache.
 #include "fp8b.h"
+#include "grid.cuh"
 
 namespace pkv {
 
@@ -217,6 +218,7 @@ __device__ __forceinline__ int nth_bit(uint64_t m, int k)
 template <bool kBf16>
 __global__ void __launch_bounds__(kRowThreads, kBf16 ? 4 : 2) kv_append_fp8b_kernel(const Fp8bRowArgs a, int tokens)
 {
+    grid_wait();
     const int lane = threadIdx.x & 31;
     const uint32_t id = blockIdx.x * (kRowThreads / 32) + (threadIdx.x >> 5), per = 2 * a.hkv;
     const uint32_t group = id / per, rest = id - group * per;
@@ -266,6 +268,7 @@ __global__ void __launch_bounds__(kRowThreads, kBf16 ? 4 : 2) kv_append_fp8b_ker
 template <bool kBf16, int kTokens>
 __global__ void __launch_bounds__(kRowThreads) kv_read_fp8b_kernel(const Fp8bRowArgs a)
 {
+    grid_wait();
     constexpr int kVals = kBf16 ? 8 : 4, kPerRow = kHeadDim / kVals;
     const uint32_t i = blockIdx.x * kRowThreads + threadIdx.x, row = i / kPerRow, part = i % kPerRow;
     const uint32_t group = row / static_cast<uint32_t>(a.hkv), h = row - group * a.hkv;
@@ -341,11 +344,8 @@ cudaError_t launch_kv_append_fp8b(const Fp8bRowArgs &a, bool bf16, cudaStream_t 
     const int64_t grid = (warps + kRowThreads / 32 - 1) / (kRowThreads / 32);
     if (warps > UINT32_MAX - kRowThreads)
         return cudaErrorInvalidValue;
-    if (bf16)
-        kv_append_fp8b_kernel<true><<<static_cast<unsigned>(grid), kRowThreads, 0, stream>>>(a, tokens);
-    else
-        kv_append_fp8b_kernel<false><<<static_cast<unsigned>(grid), kRowThreads, 0, stream>>>(a, tokens);
-    return cudaGetLastError();
+    return launch_with(bf16 ? kv_append_fp8b_kernel<true> : kv_append_fp8b_kernel<false>, dim3(static_cast<unsigned>(grid)),
+                       kRowThreads, 0, 1, true, stream, a, tokens);
 }
 
 typedef void (*ReadKernel)(const Fp8bRowArgs);
@@ -369,8 +369,8 @@ cudaError_t launch_kv_read_fp8b(const Fp8bRowArgs &args, bool bf16, cudaStream_t
         a.k_out = static_cast<uint8_t *>(args.k_out) + t * args.hkv * kHeadDim * (bf16 ? 2 : 4);
         a.v_out = static_cast<uint8_t *>(args.v_out) + t * args.hkv * kHeadDim * (bf16 ? 2 : 4);
         const int64_t threads = (a.num_tokens + (many ? kMany : 1) - 1) / (many ? kMany : 1) * per_token;
-        kernel<<<static_cast<unsigned>((threads + kRowThreads - 1) / kRowThreads), kRowThreads, 0, stream>>>(a);
-        const cudaError_t e = cudaGetLastError();
+        const cudaError_t e = launch_with(kernel, dim3(static_cast<unsigned>((threads + kRowThreads - 1) / kRowThreads)),
+                                          kRowThreads, 0, 1, true, stream, a);
         if (e != cudaSuccess)
             return e;
     }

@@ -688,3 +688,80 @@ def test_a_request_from_prompt_to_release(pkv, cuda_device):
     n = int(pool[0])
     assert n == int(free[0]) and sorted(pool[4:4 + n].tolist()) == sorted(free[4:4 + n].tolist())
     assert int(e.item()) == 0
+
+
+def test_calls_behind_copies_fills_and_other_streams(pkv, cuda_device):
+    """Each call, brought onto the GPU before what is ahead of it has ended, waits for that: kernels
+    of its own kind, copies, fills and another stream's work, captured; as with a synchronisation
+    between any two of them."""
+    dev, B, H, G, P, n, pages = cuda_device, 40, 4, 4, 16, 100, 300
+    gen = torch.Generator(device=dev).manual_seed(24)
+    pool0 = pkv.page_pool(pages, dev)
+    past0, new = torch.zeros(B, dtype=torch.int32, device=dev), torch.full((B,), n, dtype=torch.int32, device=dev)
+    new[3] = 0
+    T = B * n
+    src = [torch.empty((T, H, 128), dtype=torch.bfloat16, device=dev) for _ in range(2)]
+    qsrc = torch.empty((T, H * G, 128), dtype=torch.bfloat16, device=dev)
+    k, v, q, qd = *(torch.empty_like(x) for x in src), torch.empty_like(qsrc), torch.empty((B, H * G, 128), dtype=torch.bfloat16, device=dev)
+    (kc, ke), (vc, ve) = (pkv.fp8b_cache(pages, H, P, dev) for _ in range(2))
+    table, pool, past = torch.empty((B, 8), dtype=torch.int32, device=dev), pool0.clone(), past0.clone()
+    lens, cu = torch.empty_like(past0), torch.empty(B + 1, dtype=torch.int32, device=dev)
+    slots, pos = torch.empty(T, dtype=torch.int64, device=dev), torch.empty(T, dtype=torch.int32, device=dev)
+    e = torch.zeros(1, dtype=torch.int32, device=dev)
+    back = [torch.empty_like(k) for _ in range(2)]
+    od, op = torch.empty((B, H * G, 128), device=dev), torch.empty_like(q)
+    wd = torch.empty(pkv.pkv_decode_fp8b_workspace_size(B, H * G, H, max_seq_len=128), dtype=torch.uint8, device=dev)
+    wp = torch.empty(pkv.pkv_prefill_fp8b_workspace_size(B, H, n, 128), dtype=torch.uint8, device=dev)
+    side = torch.cuda.Stream(dev)
+
+    def on_the_side():
+        side.wait_stream(torch.cuda.current_stream(dev))
+        with torch.cuda.stream(side):
+            v.copy_(src[1])
+            od.fill_(7.0)
+        torch.cuda.current_stream(dev).wait_stream(side)
+
+    steps = [lambda: pool.copy_(pool0), lambda: past.copy_(past0), lambda: table.fill_(-1), lambda: e.zero_(),
+             lambda: pkv.plan_pages(past, new, table, pool, P, seq_lens=lens, cu_q=cu, slot_mapping=slots, positions=pos,
+                                    device_error=e),
+             lambda: k.copy_(src[0]), on_the_side,
+             lambda: pkv.kv_append_fp8b(k, v, slots, kc, vc, ke, ve, e),
+             lambda: pkv.kv_read_fp8b(slots, kc, vc, ke, ve, *back, device_error=e),
+             lambda: q.copy_(qsrc), lambda: op.zero_(),
+             lambda: pkv.paged_prefill_fp8b(q, cu, kc, vc, ke, ve, table, lens, n, out=op, workspace=wp, max_kv_len=128, device_error=e),
+             lambda: qd.copy_(qsrc[:B]),
+             lambda: pkv.paged_gqa_decode_fp8b(qd, kc, vc, ke, ve, table, lens, out=od, workspace=wd, max_seq_len=128, device_error=e),
+             lambda: pkv.release_pages(lens, table, pool, P, device_error=e),
+             lambda: pkv.plan_pages(past, new, table, pool, P, seq_lens=lens, cu_q=cu, slot_mapping=slots, positions=pos,
+                                    device_error=e)]
+    results = (table, pool, lens, cu, slots, pos, e, *back, op, od)
+
+    def fresh(seed):
+        gen.manual_seed(seed)
+        for x in (*src, qsrc):
+            x.normal_(generator=gen)
+
+    def apart():
+        for step in steps:
+            step()
+            torch.cuda.synchronize()
+        return [x.clone() for x in results]
+
+    fresh(0)
+    apart()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        for _ in range(2):
+            for step in steps:
+                step()
+    for seed in range(1, 5):
+        fresh(seed)
+        want = apart()
+        fresh(seed + 100)
+        apart()
+        fresh(seed)
+        g.replay()
+        torch.cuda.synchronize()
+        for i, (x, y) in enumerate(zip(results, want)):
+            assert torch.equal(x, y), i
+    assert int(e.item()) == 0
