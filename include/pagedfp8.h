@@ -699,7 +699,8 @@ pkv_status pkv_paged_gqa_decode_fp8b(const void *q,
  * of the largest one that the chunk sees are rounded to 2^-40 of that block's largest
  * value.  Three launches; a fourth where few rows have a long past: several CTAs then
  * share a query tile's keys (as many as batch, the bounds, the heads and the output's
- * type say), and their sums are joined in order.  num_kv_heads is at most 8192.
+ * type say), and their sums are joined in order; with a bf16 output and long contexts
+ * they read the cache itself, without 16-bit copies.  num_kv_heads is at most 8192.
  *
  *   workspace      device, >= pkv_prefill_fp8b_workspace_size(...) bytes for the same
  *                  bounds, 256-byte aligned.  Where CTAs may share keys it has 21 MB for

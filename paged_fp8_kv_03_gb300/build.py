@@ -22,7 +22,7 @@ BINDING = os.path.join(LIB_DIR, "_binding.so")      # the Python binding's fast 
 
 SOURCES = ["append.cu", "decode.cu", "api.cu", "noalloc.cu", "calibrate.cu", "prefill.cu",
            "rows_fp4.cu", "prefill_fp4.cu", "decode_fp4.cu", "api_fp4.cu",
-           "rows_fp8b.cu", "prefill_fp8b.cu", "decode_fp8b.cu", "api_fp8b.cu", "pages.cu"]
+           "rows_fp8b.cu", "prefill_fp8b.cu", "prefill_direct.cu", "decode_fp8b.cu", "api_fp8b.cu", "pages.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",
          "--expt-relaxed-constexpr"]

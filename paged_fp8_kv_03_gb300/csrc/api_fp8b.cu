@@ -250,13 +250,6 @@ pkv_status pkv_paged_prefill_fp8b(const void *q, const int32_t *cu_q, int total_
     float *refs = reinterpret_cast<float *>(base);
     __half *k16 = reinterpret_cast<__half *>(base + prefill_fp8b_refs_bytes(batch, num_kv_heads));
     __half *v16 = k16 + static_cast<size_t>(rows) * kHeadDim;
-    alignas(64) CUtensorMap tm_q;
-    alignas(64) CUtensorMap tm_k;
-    alignas(64) CUtensorMap tm_v;
-    if (!make_q_map(&tm_q, q, total_q, num_q_heads, group, tpt) ||
-        !make_kv16_map(&tm_k, k16, rows, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16) ||
-        !make_kv16_map(&tm_v, v16, rows, CU_TENSOR_MAP_DATA_TYPE_FLOAT16))
-        return cuda_failed(cudaErrorInvalidValue, "cuTensorMapEncodeTiled (block-scaled prefill)");
     PrefillArgs a = {};
     a.cu_q = cu_q;
     a.total_q = total_q;
@@ -290,7 +283,17 @@ pkv_status pkv_paged_prefill_fp8b(const void *q, const int32_t *cu_q, int total_
     a.out_f32 = out_dtype == PKV_F32;
     a.err = device_error;
     a.split = prefill_fp8b_split(a, win, longest);
+    a.direct = prefill_fp8b_direct(a);
     a.partials = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + ((copies + 255) & ~size_t(255)));
+    alignas(64) CUtensorMap tm_q;
+    alignas(64) CUtensorMap tm_k;
+    alignas(64) CUtensorMap tm_v;
+    if (!make_q_map(&tm_q, q, total_q, num_q_heads, group, tpt) ||
+        !(a.direct ? make_page_map(&tm_k, k_cache, num_pages, num_kv_heads, page_size)
+                 : make_kv16_map(&tm_k, k16, rows, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16)) ||
+        !(a.direct ? make_page_map(&tm_v, v_cache, num_pages, num_kv_heads, page_size)
+                 : make_kv16_map(&tm_v, v16, rows, CU_TENSOR_MAP_DATA_TYPE_FLOAT16)))
+        return cuda_failed(cudaErrorInvalidValue, "cuTensorMapEncodeTiled (block-scaled prefill)");
     const cudaError_t e = launch_prefill_windowed(a, win, tm_q, tm_k, tm_v,
                                                   launch_widen_fp8b, stream);
     return e == cudaSuccess ? PKV_OK : cuda_failed(e, "block-scaled prefill kernel launch");

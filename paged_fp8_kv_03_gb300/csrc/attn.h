@@ -94,6 +94,10 @@ cudaError_t launch_prefill_windowed(const PrefillArgs &a, const KeyWindow &win, 
                                     const CUtensorMap &tm_k16, const CUtensorMap &tm_v16, WidenLaunch widen,
                                     cudaStream_t stream);
 
+// The attention of a.direct: tm_k and tm_v are the pools' maps.
+cudaError_t launch_prefill_direct(const PrefillArgs &a, const KeyWindow &win, const CUtensorMap &tm_q, const CUtensorMap &tm_k,
+                                  const CUtensorMap &tm_v, cudaStream_t stream);
+
 // Joins what the CTAs of a split prefill have left, and writes the output.
 cudaError_t launch_prefill_join(const PrefillArgs &a, const KeyWindow &win, cudaStream_t stream);
 

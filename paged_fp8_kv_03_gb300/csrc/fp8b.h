@@ -65,6 +65,8 @@ inline size_t prefill_fp8b_bytes(int batch, int hkv, long long rows)
 // than `longest` tokens, 1 where one has them all; and the bytes that their rows' states
 // can take whatever the heads a kv head has and the output's type.
 int prefill_fp8b_split(const PrefillArgs &a, const KeyWindow &win, int longest);
+// Whether those of a.split take the keys from the cache itself.
+bool prefill_fp8b_direct(const PrefillArgs &a);
 size_t prefill_fp8b_split_bytes(int batch, int hkv, int max_q_len, int longest, const KeyWindow &win);
 
 cudaError_t launch_widen_fp8b(const PrefillArgs &a, const KeyWindow &win, cudaStream_t stream);

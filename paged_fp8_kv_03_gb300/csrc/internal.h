@@ -125,6 +125,7 @@ struct PrefillArgs {
                                     // workspace, written ahead of the widening, which makes it negative where V
                                     // holds a NaN); else nullptr
     int split;                      // block-scaled FP8 cache: CTAs that share a query tile's keys (1: one has them all)
+    int direct;                     // 1: they read the cache itself, not 16-bit copies (k16, v16: unused)
     float *partials;                // their rows: [query tiles or pairs][split][rows][kPartialStride]
     const int32_t *block_table;
     int max_pages;

@@ -886,8 +886,9 @@ cudaError_t launch_prefill_windowed(const PrefillArgs &a, const KeyWindow &win, 
         e = widen(a, win, stream);
     if (e != cudaSuccess)
         return e;
-    e = a.out_f32 ? launch_attention(kernel, PS::bytes(moves), a, seen, tm_q, tm_k16, tm_v16, stream)
-                  : launch_prefill_pair(a, seen, tm_q, tm_k16, tm_v16, stream);
+    e = a.out_f32  ? launch_attention(kernel, PS::bytes(moves), a, seen, tm_q, tm_k16, tm_v16, stream)
+        : a.direct ? launch_prefill_direct(a, seen, tm_q, tm_k16, tm_v16, stream)
+                   : launch_prefill_pair(a, seen, tm_q, tm_k16, tm_v16, stream);
     return e == cudaSuccess && split ? launch_prefill_join(a, seen, stream) : e;
 }
 

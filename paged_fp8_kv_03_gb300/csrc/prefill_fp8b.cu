@@ -18,9 +18,8 @@
 // where there are few); a thread takes 8 values of kRowsEach of its rows, of K and of V, 16
 // lanes write a row's 256 bytes.  Bytes bound it: 256 of the cache to 512 of the
 // copies a row.
-#include "fp8b.h"
-#include "prefill.cuh"
 #include "split.cuh"
+#include "widen_fp8b.cuh"
 
 namespace pkv {
 
@@ -113,11 +112,6 @@ __global__ void __launch_bounds__(kRefThreads) kv_refs_fp8b_kernel(const Prefill
     cluster_sync(ctas);                                  // no CTA leaves while its maxima are read
 }
 
-__device__ __forceinline__ float scale_of(uint32_t x)    // 2^(x - 127)
-{
-    return __uint_as_float(x == 0 ? 0x00400000u : x << 23);
-}
-
 template <int kRowsEach>
 __global__ void __launch_bounds__(256) kv_widen_fp8b_kernel(const PrefillArgs a, const KeyWindow win)
 {
@@ -165,7 +159,7 @@ __global__ void __launch_bounds__(256) kv_widen_fp8b_kernel(const PrefillArgs a,
                     kc[i] = __ldg(reinterpret_cast<const uint2 *>(a.k_cache + at * kHeadDim) + part);
                     vc[i] = __ldg(reinterpret_cast<const uint2 *>(a.v_cache + at * kHeadDim) + part);
                     ks[i] = scale_of(__ldg(a.k_exp + at / kBlock));
-                    vs[i] = __int_as_float(max(static_cast<int>(__ldg(a.v_exp + at / kBlock)) - ref + 127, 1) << 23);
+                    vs[i] = scale_of_v(__ldg(a.v_exp + at / kBlock), ref);
                 } else if (part == 0 && a.err) {
                     atomicOr(a.err, PKV_DEVERR_PAGE);
                 }
@@ -174,30 +168,9 @@ __global__ void __launch_bounds__(256) kv_widen_fp8b_kernel(const PrefillArgs a,
 #pragma unroll
         for (int i = 0; i < kRowsEach; ++i) {
             const int64_t at = (static_cast<int64_t>(tile) * kKeys + first + 16 * i) * kHeadDim + 8 * part;
-            const uint32_t n0 = __vcmpeq4(vc[i].x & 0x7F7F7F7Fu, 0x7F7F7F7Fu), n1 = __vcmpeq4(vc[i].y & 0x7F7F7F7Fu, 0x7F7F7F7Fu);
-            nans[i] = 0;
-            if ((n0 | n1) != 0) {
-                vc[i].x &= ~n0;
-                vc[i].y &= ~n1;
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    nans[i] |= ((n0 >> (8 * e)) & 1u) << e | ((n1 >> (8 * e)) & 1u) << (4 + e);
-                some = true;
-            }
-            uint32_t k[4], v[4];
-            e4m3x4_to_f16x4(kc[i].x, k[0], k[1]);
-            e4m3x4_to_f16x4(kc[i].y, k[2], k[3]);
-            e4m3x4_to_f16x4(vc[i].x, v[0], v[1]);
-            e4m3x4_to_f16x4(vc[i].y, v[2], v[3]);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const float2 kf = f16x2_to_f32x2(k[e]), vf = f16x2_to_f32x2(v[e]);
-                const __nv_bfloat162 kb = __floats2bfloat162_rn(kf.x * ks[i], kf.y * ks[i]);
-                k[e] = *reinterpret_cast<const uint32_t *>(&kb);
-                v[e] = f32x2_to_f16x2(vf.x * vs[i], vf.y * vs[i]);
-            }
-            *reinterpret_cast<uint4 *>(a.k16 + at) = make_uint4(k[0], k[1], k[2], k[3]);
-            *reinterpret_cast<uint4 *>(a.v16 + at) = make_uint4(v[0], v[1], v[2], v[3]);
+            *reinterpret_cast<uint4 *>(a.k16 + at) = widen_k(kc[i], ks[i]);
+            *reinterpret_cast<uint4 *>(a.v16 + at) = widen_v(vc[i], vs[i], nans[i]);
+            some = some || nans[i] != 0;
         }
         const bool any = __syncthreads_or(some) != 0;
         if (tid == 0) {
@@ -322,6 +295,16 @@ int prefill_fp8b_split(const PrefillArgs &a, const KeyWindow &win, int longest)
     return longest > kNoWindow / 2 ? 1 : split_of(tiles * a.batch * a.hkv, most_key_tiles(bound, win));
 }
 
+// A CTA that widens for itself takes 3.1 us a key tile, else 1.3, but the copies are neither
+// written nor read: 9 x 32 tokens of 32 query and 8 kv heads past 8192 116 us, else 160; 16
+// tokens of 64 and 8 past 131072 177 and 257.  With several pairs of query tiles a kv head each
+// widens them again (512 tokens past 32768: 411 and 255), and few keys' copies cost less than
+// the longer start (2048 key tiles, 64 tokens past 32768: 77 and 93; 1024: 95 and 91; 256: 40 and 40).
+bool prefill_fp8b_direct(const PrefillArgs &a)
+{
+    return a.split > 1 && !a.out_f32 && a.max_tiles <= 2 && a.rows_cap / kKeys >= 1536;
+}
+
 size_t prefill_fp8b_split_bytes(int batch, int hkv, int max_q_len, int longest, const KeyWindow &win)
 {
     // Between the CTAs of one query tile a kv head and of kSplitSms / 2 in all, whichever
@@ -354,7 +337,7 @@ cudaError_t launch_widen_fp8b(const PrefillArgs &a, const KeyWindow &win, cudaSt
     const int ctas = a.max_kv_len <= 4096 ? 1 : kRefCtas;
     const cudaError_t e = launch_with(kv_refs_fp8b_kernel, dim3(static_cast<unsigned>((a.batch + 1) * ctas)), kRefThreads,
                                       static_cast<size_t>(a.hkv) * sizeof(int), ctas, true, stream, a, win, ctas);
-    if (e != cudaSuccess)
+    if (e != cudaSuccess || a.direct)   // (that attention widens for itself)
         return e;
     const int64_t tiles = a.rows_cap / kKeys, most = static_cast<int64_t>(device_sm_count()) * 8;
     if (tiles * 4 <= most)

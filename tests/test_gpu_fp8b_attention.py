@@ -408,13 +408,13 @@ def _tight(q, k, v, p, window, sinks, sm):
 
 
 def _prefill(pkv, c, ns, hq, window=0, sinks=0, out_dtype=torch.float32, q_spread=1.0, sm=SM, sample=40, total=0, err=0,
-             pad_rows=3, skip=(), tight=False):
+             pad_rows=3, skip=(), tight=False, bound=0):
     cu = np.concatenate(([0], np.cumsum(ns))).astype(np.int32)
     q, qd = c.queries(int(cu[-1]) + pad_rows, hq, q_spread)
     out = torch.full(qd.shape, 9.0, dtype=out_dtype, device=c.dev)
     e = torch.zeros(1, dtype=torch.int32, device=c.dev)
     pkv.paged_prefill_fp8b(qd, _dev(cu, c.dev), *c.args, c.tabled, c.lensd, max(max(ns), 1), out=out,
-                           max_kv_len=max(max(c.lens), 1), sm_scale=sm, device_error=e, window=window, sinks=sinks,
+                           max_kv_len=max(max(c.lens), 1, bound), sm_scale=sm, device_error=e, window=window, sinks=sinks,
                            max_total_kv=total, seq_page_sizes=c.psd)
     torch.cuda.synchronize()
     assert int(e.item()) == err
@@ -518,6 +518,40 @@ FEW_ROWS = [([1024], [1], 1, 1), ([1025], [129], 2, 8), ([897, 4096, 130, 3, 0, 
 def test_prefill_few_rows_over_a_long_past(pkv, cuda_device, lens, ns, hkv, G, window, sinks, out_dtype):
     c = Cache(len(lens) + max(lens), lens, hkv, 16, cuda_device)
     _prefill(pkv, c, ns, hkv * G, window, sinks, out_dtype, sample=8)
+    if window == 0:                                              # a bound of so many keys that bf16 calls read the cache itself
+        _prefill(pkv, c, ns, hkv * G, window, sinks, out_dtype, sample=8, bound=200000)
+
+
+@pytest.mark.parametrize("G,P,page_sizes", [(8, 16, None), (4, 64, None), (5, 16, [16, 64, 16, 256, 32, 16, 128, 16])])
+@pytest.mark.parametrize("window,sinks", [(0, 0), (3000, 0), (2900, 140)])
+def test_prefill_from_the_cache_itself(pkv, cuda_device, G, P, page_sizes, window, sinks):
+    """Bounds that make bf16 calls widen in the attention; pages behind the window are never looked at."""
+    lens, ns = [4000, 1, 1, 3500, 1, 17, 0, 1100], [30, 1, 0, 9, 1, 17, 0, 32]
+    c = Cache(25 + G, lens, 8, P, cuda_device, page_sizes=page_sizes,
+              hidden=(window, sinks, [L - n for L, n in zip(lens, ns)]) if window else None)
+    _prefill(pkv, c, ns, 8 * G, window, sinks, torch.bfloat16, sample=4, bound=0 if window else 200000)
+
+
+@pytest.mark.parametrize("sizes", ["one large", "mixed", "huge", "tiny", "zeros"])
+def test_prefill_from_the_cache_itself_of_different_sizes(pkv, cuda_device, sizes):
+    """Scales outside f16's and bf16's, of K and of V."""
+    c = Cache(26, [1300, 700], 2, 16, cuda_device, sizes=SIZES[sizes])
+    _prefill(pkv, c, [33, 20], 8, q_spread=2.0, out_dtype=torch.bfloat16, bound=200000)
+    fixed = c.exps[0].copy()
+    for up in (13, 15, 100):                                      # K's exponents 2^up higher, the scale as much lower
+        c.args[2].copy_(torch.from_numpy(np.where(fixed == 255, 255, fixed.astype(np.int64) + up).clip(0, 255).astype(np.uint8)))
+        keep = [k.copy() for k in c.k]
+        c.k = [k * 2.0 ** up for k in keep]
+        _prefill(pkv, c, [33, 20], 8, q_spread=2.0, out_dtype=torch.bfloat16, bound=200000, sm=SM * 2.0 ** -up)
+        c.k = keep
+
+
+def test_prefill_from_the_cache_itself_bad_pages(pkv, cuda_device):
+    c = Cache(27, [1400, 64], 2, 16, cuda_device)
+    c.tabled[0, 2] = c.pages
+    for x in (c.k, c.v):
+        x[0][32:48] = 0
+    _prefill(pkv, c, [30, 10], 8, out_dtype=torch.bfloat16, err=pkv.DEVERR_PAGE, bound=200000)
 
 
 @pytest.mark.parametrize("out_dtype", [torch.float32, torch.bfloat16])
@@ -528,16 +562,16 @@ def test_prefill_parts_of_a_long_context(pkv, cuda_device, out_dtype):
 
 
 @pytest.mark.parametrize("out_dtype", [torch.float32, torch.bfloat16])
-@pytest.mark.parametrize("window,sinks", [(0, 0), (1300, 130)])
-def test_prefill_few_rows_nan_codes(pkv, cuda_device, out_dtype, window, sinks):
+@pytest.mark.parametrize("window,sinks,bound", [(0, 0, 2100), (1300, 130, 2100), (0, 0, 200000)])
+def test_prefill_few_rows_nan_codes(pkv, cuda_device, out_dtype, window, sinks, bound):
     """NaNs of V and of K in several parts of the keys."""
-    L, n, at = 2100, 150, {129: 5, 700: 64, 1990: 127, 2060: 0, 2099: 5}
+    L, n, at = 2100, 80, {129: 5, 700: 64, 1990: 127, 2060: 0, 2099: 5}
     c = Cache(22, [L], 1, 16, cuda_device)
     cu = torch.tensor([0, n], dtype=torch.int32, device=cuda_device)
     q, qd = c.queries(n, 3)
 
     def run():
-        return pkv.paged_prefill_fp8b(qd, cu, *c.args, c.tabled, c.lensd, n, max_kv_len=L, out_dtype=out_dtype,
+        return pkv.paged_prefill_fp8b(qd, cu, *c.args, c.tabled, c.lensd, n, max_kv_len=bound, out_dtype=out_dtype,
                                       window=window, sinks=sinks)
 
     def seen(t):
