@@ -28,15 +28,18 @@ def test_decode_times_out_and_recovers(pkv, cuda_device, max_ctas, out_dtype):
     _decode(pkv, c, q, qd, out_dtype=out_dtype, max_ctas=max_ctas)
 
 
-@pytest.mark.parametrize("window,out_dtype", [(0, torch.float32), (90, torch.bfloat16)])
-def test_prefill_times_out_and_recovers(pkv, cuda_device, window, out_dtype):
+@pytest.mark.parametrize("window,out_dtype,n,bound", [
+    (0, torch.float32, 40, 400), (90, torch.bfloat16, 40, 400),
+    (0, torch.float32, 40, 1100), (0, torch.bfloat16, 40, 1100),  # CTAs share the keys
+    (0, torch.bfloat16, 30, 200000)])                             # and read them from the cache
+def test_prefill_times_out_and_recovers(pkv, cuda_device, window, out_dtype, n, bound):
     c = Cache(42, [400], 1, 16, cuda_device)
-    q, qd = c.queries(40, 8)
-    cu = torch.tensor([0, 40], dtype=torch.int32, device=cuda_device)
+    q, qd = c.queries(n, 8)
+    cu = torch.tensor([0, n], dtype=torch.int32, device=cuda_device)
     e = torch.zeros(1, dtype=torch.int32, device=cuda_device)
 
     def call(e):
-        return pkv.paged_prefill_fp8b(qd, cu, *c.args, c.tabled, c.lensd, 40, out_dtype=out_dtype, max_kv_len=400,
+        return pkv.paged_prefill_fp8b(qd, cu, *c.args, c.tabled, c.lensd, n, out_dtype=out_dtype, max_kv_len=bound,
                                       device_error=e, window=window, sinks=2)
 
     def withheld():
@@ -48,6 +51,6 @@ def test_prefill_times_out_and_recovers(pkv, cuda_device, window, out_dtype):
     out = call(e)
     torch.cuda.synchronize()
     assert int(e.item()) == 0
-    for r in (0, 17, 39):
-        ref = fp4_ref.attend(q[r].astype(np.float64), c.k[0], c.v[0], 360 + r, window, 2, SM)
+    for r in (0, 17, n - 1):
+        ref = fp4_ref.attend(q[r].astype(np.float64), c.k[0], c.v[0], 400 - n + r, window, 2, SM)
         _check(out[r], ref, fp4_ref.attention_tolerance(q[r], c.k[0], c.v[0], ref, SM, out_dtype == torch.bfloat16), r)
