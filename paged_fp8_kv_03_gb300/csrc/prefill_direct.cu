@@ -489,8 +489,14 @@ cudaError_t launch_prefill_direct(const PrefillArgs &a, const KeyWindow &win, co
         const bool known = current_context_id(&ctx);
         std::lock_guard<std::mutex> lk(g_direct_mu);
         if (!known || g_direct_ctx[dev] != ctx) {
-            e = cudaFuncSetAttribute(paged_prefill_direct_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                     static_cast<int>(D::kBytes));
+            // (a warpgroup waits for registers that others give up: those of the launch must do)
+            cudaFuncAttributes f;
+            e = cudaFuncGetAttributes(&f, paged_prefill_direct_kernel);
+            if (e == cudaSuccess && f.numRegs * kThreadsS < 128 * (kRegsIssue + 2 * kRegsSoftmax + 2 * kRegsWiden))
+                e = cudaErrorInvalidConfiguration;
+            if (e == cudaSuccess)
+                e = cudaFuncSetAttribute(paged_prefill_direct_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         static_cast<int>(D::kBytes));
             if (e != cudaSuccess)
                 return e;
             g_direct_ctx[dev] = known ? ctx : 0;
