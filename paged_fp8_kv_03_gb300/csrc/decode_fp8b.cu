@@ -847,7 +847,8 @@ __global__ void __launch_bounds__(32 * kClusterWarps, 2)
             N = larger(Reference{__shfl_xor_sync(kEvery, N.n, o), __shfl_xor_sync(kEvery, N.e, o)}, N);
         }
         N = Reference{__shfl_sync(kEvery, N.n, 0), __shfl_sync(kEvery, N.e, 0)};
-        float sum = m == -INFINITY ? 0.f : ex2_approx(m - M) * l;
+        // (m = -inf: no units, l = 0, or only tokens whose scores are NaN, l = NaN)
+        float sum = m == -INFINITY ? l : ex2_approx(m - M) * l;
         // (not 0 where there is a state: a NaN of V in it is seen whatever its weight)
         const float e = m == -INFINITY ? 0.f : fmaxf(ex2_approx(ref.over(N)), 0x1p-126f);
 #pragma unroll
