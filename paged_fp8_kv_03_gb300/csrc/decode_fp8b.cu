@@ -379,7 +379,7 @@ __device__ __forceinline__ uint32_t tile_bytes(const Fp8bDecodeArgs &da, int t)
 {
     if (t < 0)
         return kExpBias | (kExpMin + kExpBias) << 8;
-    return __ldg(da.k_exp + t) | static_cast<uint32_t>(__ldg(da.v_exp + t)) << 8;
+    return da.k_exp[t] | static_cast<uint32_t>(da.v_exp[t]) << 8;
 }
 
 // 2^ek and ev.

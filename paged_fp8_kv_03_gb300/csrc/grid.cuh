@@ -4,7 +4,9 @@
 namespace pkv {
 
 // Waits until the kernels ahead in the stream have ended and their writes are
-// seen; lets the next kernel be brought onto the GPU (it waits in turn).
+// seen; lets the next kernel be brought onto the GPU (it waits in turn).  What is read
+// behind the wait may have been written while this kernel was on the GPU already, so the
+// loads are ordinary ones: __ldg() is for memory that nothing writes as long as a kernel lives.
 __device__ __forceinline__ void grid_wait()
 {
     asm volatile("griddepcontrol.wait;" ::: "memory");

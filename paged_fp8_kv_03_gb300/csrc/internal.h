@@ -196,7 +196,7 @@ __device__ __forceinline__ int seq_page_log2(const Args &a, int b)
 {
     if (a.page_sizes == nullptr)
         return a.pool_log2;
-    const int pb = __ldg(a.page_sizes + b);
+    const int pb = a.page_sizes[b];
     if (pb < a.page_size || pb > 256 || (pb & (pb - 1)) != 0)
         return -1;
     return 31 - __clz(pb);
@@ -208,7 +208,7 @@ __device__ __forceinline__ int seq_page_log2(const Args &a, int b)
 template <typename Args>
 __device__ __forceinline__ bool seq_token_page(const Args &a, int b, int lp, int t, int &phys, int &row)
 {
-    const int entry = __ldg(a.block_table + static_cast<int64_t>(b) * a.max_pages + (t >> lp));
+    const int entry = a.block_table[static_cast<int64_t>(b) * a.max_pages + (t >> lp)];
     const int o = t & ((1 << lp) - 1);
     if (entry < 0 || entry >= a.num_pages)
         return false;

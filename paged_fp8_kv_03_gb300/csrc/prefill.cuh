@@ -257,20 +257,20 @@ __device__ __forceinline__ uint32_t nan_blocks(const PrefillArgs &a, const KeyWi
     const uint32_t *tiles = nan_tiles(a);
     bool some = false;
     for (int i = lane; i < nt; i += 32)
-        some = some || __ldg(tiles + tile0 + copy_tile(i)) != 0;
+        some = some || tiles[tile0 + copy_tile(i)] != 0;
     uint32_t hit = 0;
     if (__any_sync(kAll, some)) {
 #pragma unroll 1
         for (int i = 0; i < nt; ++i) {
             const int64_t tile = tile0 + copy_tile(i);
-            const uint32_t word = __ldg(tiles + tile);
+            const uint32_t word = tiles[tile];
             if (word == 0)
                 continue;
 #pragma unroll 1
             for (int k = 0; k < kKeys; ++k) {
                 const int t = key_tile(i) * kKeys + k;
                 if ((word >> (8 * (k >> 5)) & 0xFFu) != 0 && t <= p && (!kWin || t > p - w.window || t < w.sinks))
-                    hit |= __ldg(nan_rows(a) + tile * kKeys + k);
+                    hit |= nan_rows(a)[tile * kKeys + k];
             }
         }
     }
@@ -294,8 +294,8 @@ __device__ __forceinline__ uint8_t *nan_value_rows(const PrefillArgs &a)
 template <bool kWin>
 __device__ __forceinline__ void put_nans_of(const PrefillArgs &a, const KeyWindow &w, int b, int h, int t0, int t1, int threads)
 {
-    const int q0 = __ldg(a.cu_q + b), n = __ldg(a.cu_q + b + 1) - q0, L = __ldg(a.seq_lens + b);
-    const int off0 = __ldg(a.tile_off + b), off1 = __ldg(a.tile_off + b + 1);
+    const int q0 = a.cu_q[b], n = a.cu_q[b + 1] - q0, L = a.seq_lens[b];
+    const int off0 = a.tile_off[b], off1 = a.tile_off[b + 1];
     const KeyTiles seq_kt = key_tiles<kWin>(w, L - n), kt = key_tiles<kWin>(w, L - n + t0);
     const int64_t tile0 = off0 + h * ((off1 - off0) / a.hkv);
     const int nt = (L - n + t1 - 1) / kKeys + 1 - kt.skip;
@@ -306,7 +306,7 @@ __device__ __forceinline__ void put_nans_of(const PrefillArgs &a, const KeyWindo
     };
     bool some = false;
     for (int i = threadIdx.x; i < nt; i += threads)
-        some = some || __ldg(nan_value_tiles(a) + tile0 + copy_tile(i)) != 0;
+        some = some || nan_value_tiles(a)[tile0 + copy_tile(i)] != 0;
     if (!__syncthreads_or(some))
         return;
     const uint32_t *rows = reinterpret_cast<const uint32_t *>(nan_value_rows(a));
@@ -317,14 +317,14 @@ __device__ __forceinline__ void put_nans_of(const PrefillArgs &a, const KeyWindo
 #pragma unroll 1
         for (int i = 0; i < nt; ++i) {
             const int64_t tile = tile0 + copy_tile(i);
-            const uint32_t word = __ldg(nan_value_tiles(a) + tile);
+            const uint32_t word = nan_value_tiles(a)[tile];
             if (word == 0)
                 continue;
 #pragma unroll 1
             for (int k = 0; k < kKeys; ++k) {
                 const int key = key_tile(i) * kKeys + k;
                 if ((word >> (8 * (k >> 5)) & 0xFFu) != 0 && key <= p && (!kWin || key > p - w.window || key < w.sinks))
-                    hit |= __ldg(rows + (tile * kKeys + k) * 4 + j);
+                    hit |= rows[(tile * kKeys + k) * 4 + j];
             }
         }
         const int64_t row = (static_cast<int64_t>(q0) + t) * a.hq + static_cast<int64_t>(h) * a.group;
@@ -347,7 +347,7 @@ __device__ __noinline__ void put_nans(const PrefillArgs &a, const KeyWindow &w, 
     const int per = (a.max_tiles + tiles - 1) / tiles;
     const int bh = blockIdx.x / per, first = (per - 1 - (static_cast<int>(blockIdx.x) - bh * per)) * tiles;
     const int b = bh / a.hkv, h = bh - b * a.hkv;
-    const int n = __ldg(a.cu_q + b + 1) - __ldg(a.cu_q + b);
+    const int n = a.cu_q[b + 1] - a.cu_q[b];
     put_nans_of<kWin>(a, w, b, h, first * a.tokens_per_tile, min(n, (first + tiles) * a.tokens_per_tile), threads);
 }
 
@@ -356,8 +356,8 @@ __device__ __noinline__ void put_nans(const PrefillArgs &a, const KeyWindow &w, 
 template <bool kWin>
 __device__ __forceinline__ long long region_tiles(const PrefillArgs &a, const KeyWindow &w, int b)
 {
-    const int q0 = __ldg(a.cu_q + b), q1 = __ldg(a.cu_q + b + 1);
-    const int L = __ldg(a.seq_lens + b);
+    const int q0 = a.cu_q[b], q1 = a.cu_q[b + 1];
+    const int L = a.seq_lens[b];
     if (q1 - q0 <= 0 || !sequence_ok(a, b, q0, q1, L, false))
         return 0;
     return static_cast<long long>(a.hkv) * ((L + kKeys - 1) / kKeys - key_tiles<kWin>(w, L - (q1 - q0)).skip);

@@ -174,7 +174,7 @@ __global__ void __launch_bounds__(kThreadsS, 1)
                                           : BlockPlace{-1, 0};
             };
             auto exponent = [&](const BlockPlace &p) {
-                return p.z >= 0 ? static_cast<int>(__ldg(exps + (static_cast<int64_t>(p.z) * a.page_size + p.y) / kBlock)) : -1;
+                return p.z >= 0 ? static_cast<int>(exps[(static_cast<int64_t>(p.z) * a.page_size + p.y) / kBlock]) : -1;
             };
             BlockPlace now = place(0), next = place(1);
             int x = exponent(now), t = 0;

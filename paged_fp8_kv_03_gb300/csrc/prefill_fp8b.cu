@@ -78,7 +78,7 @@ __global__ void __launch_bounds__(kRefThreads) kv_refs_fp8b_kernel(const Prefill
             lay_out(a, win, warp_sum);
         return;
     }
-    const int q0 = __ldg(a.cu_q + b), q1 = __ldg(a.cu_q + b + 1), L = __ldg(a.seq_lens + b);
+    const int q0 = a.cu_q[b], q1 = a.cu_q[b + 1], L = a.seq_lens[b];
     if (q1 - q0 <= 0 || !sequence_ok(a, b, q0, q1, L, false))
         return;                                          // (the whole cluster)
     for (int h = threadIdx.x; h < a.hkv; h += kRefThreads)
@@ -94,7 +94,7 @@ __global__ void __launch_bounds__(kRefThreads) kv_refs_fp8b_kernel(const Prefill
             continue;                                    // (the widening flags it)
         const uint8_t *x = a.v_exp + static_cast<int64_t>(pg) * a.hkv * per_page + row / kBlock;
         for (int h = 0; h < a.hkv; ++h) {
-            const int v = __ldg(x + static_cast<int64_t>(h) * per_page);
+            const int v = x[static_cast<int64_t>(h) * per_page];
             if (v > *const_cast<volatile int *>(top + h))
                 atomicMax(top + h, v);
         }
@@ -137,8 +137,8 @@ __global__ void __launch_bounds__(256) kv_widen_fp8b_kernel(const PrefillArgs a,
         const int b = lo, off0 = off[b], off1 = off[b + 1];
         if (off1 > cap_tiles)
             continue;                                    // region past the workspace: flagged above
-        const int L = __ldg(a.seq_lens + b), lp = seq_page_log2(a, b);
-        const KeyTiles kt = key_tiles<true>(win, L - (__ldg(a.cu_q + b + 1) - __ldg(a.cu_q + b)));
+        const int L = a.seq_lens[b], lp = seq_page_log2(a, b);
+        const KeyTiles kt = key_tiles<true>(win, L - (a.cu_q[b + 1] - a.cu_q[b]));
         const int per_head = (off1 - off0) / a.hkv;
         const int h = (tile - off0) / per_head, vt = (tile - off0) - h * per_head;
         const int key0 = (vt < kt.first ? vt : vt + kt.skip) * kKeys;
@@ -156,10 +156,10 @@ __global__ void __launch_bounds__(256) kv_widen_fp8b_kernel(const PrefillArgs a,
                 int pg, row;
                 if (seq_token_page(a, b, lp, t, pg, row)) {
                     const int64_t at = (static_cast<int64_t>(pg) * a.hkv + h) * a.page_size + row;
-                    kc[i] = __ldg(reinterpret_cast<const uint2 *>(a.k_cache + at * kHeadDim) + part);
-                    vc[i] = __ldg(reinterpret_cast<const uint2 *>(a.v_cache + at * kHeadDim) + part);
-                    ks[i] = scale_of(__ldg(a.k_exp + at / kBlock));
-                    vs[i] = scale_of_v(__ldg(a.v_exp + at / kBlock), ref);
+                    kc[i] = reinterpret_cast<const uint2 *>(a.k_cache + at * kHeadDim)[part];
+                    vc[i] = reinterpret_cast<const uint2 *>(a.v_cache + at * kHeadDim)[part];
+                    ks[i] = scale_of(a.k_exp[at / kBlock]);
+                    vs[i] = scale_of_v(a.v_exp[at / kBlock], ref);
                 } else if (part == 0 && a.err) {
                     atomicOr(a.err, PKV_DEVERR_PAGE);
                 }
@@ -202,7 +202,7 @@ __global__ void __launch_bounds__(kJoinThreads) prefill_join_fp8b_kernel(const P
     const int tiles = a.out_f32 ? 1 : 2, per = (a.max_tiles + tiles - 1) / tiles;   // of an attention CTA
     const int bh = static_cast<int>(blockIdx.x) / per, first = (per - 1 - (static_cast<int>(blockIdx.x) - bh * per)) * tiles;
     const int b = bh / a.hkv, h = bh - b * a.hkv, G = a.group, tpt = a.tokens_per_tile;
-    const int q0 = __ldg(a.cu_q + b), q1 = __ldg(a.cu_q + b + 1), n = q1 - q0, L = __ldg(a.seq_lens + b);
+    const int q0 = a.cu_q[b], q1 = a.cu_q[b + 1], n = q1 - q0, L = a.seq_lens[b];
     if (!sequence_ok(a, b, q0, q1, L, false) || a.tile_off[b + 1] > a.rows_cap / kKeys)
         return;
     const int begin = first * tpt, end = min(n, begin + tiles * tpt), per_cta = max(1, kJoinRows / G);

@@ -79,7 +79,7 @@ __device__ __forceinline__ void load_eight(const void *rows, int64_t at, Eight<k
                            : reinterpret_cast<const uint4 *>(static_cast<const float *>(rows) + at);
 #pragma unroll
     for (int i = 0; i < (kBf16 ? 1 : 2); ++i)
-        x.u[i] = __ldg(p + i);
+        x.u[i] = p[i];
 }
 
 template <bool kBf16>
@@ -228,7 +228,7 @@ __global__ void __launch_bounds__(kRowThreads, kBf16 ? 4 : 2) kv_append_fp8b_ker
         return;
     const void *in = rest & 1 ? a.v_in : a.k_in;
     uint8_t *cache = rest & 1 ? a.v_cache : a.k_cache, *exps = rest & 1 ? a.v_exp : a.k_exp;
-    auto slot_at = [&](int64_t t) { return t >= 0 && t < a.num_tokens ? __ldg(a.slots + t) : int64_t(-1); };
+    auto slot_at = [&](int64_t t) { return t >= 0 && t < a.num_tokens ? a.slots[t] : int64_t(-1); };
     const int64_t s = slot_at(first + lane), s0 = __shfl_sync(kWarp, s, 0);
     if (tokens == kBlock && s0 >= 0 && s0 < a.num_slots && (s0 & (kBlock - 1)) == 0 &&
         __all_sync(kWarp, lane >= kBlock || s == s0 + lane)) {
@@ -279,7 +279,7 @@ __global__ void __launch_bounds__(kRowThreads) kv_read_fp8b_kernel(const Fp8bRow
     uint32_t w[kTokens][2][kVals / 4], x[kTokens][2];
 #pragma unroll
     for (int n = 0; n < kTokens; ++n)
-        slot[n] = token + n < a.num_tokens ? __ldg(a.slots + token + n) : -1;
+        slot[n] = token + n < a.num_tokens ? a.slots[token + n] : -1;
 #pragma unroll
     for (int n = 0; n < kTokens; ++n) {
         const bool in = slot[n] >= 0 && slot[n] < a.num_slots;
@@ -288,13 +288,13 @@ __global__ void __launch_bounds__(kRowThreads) kv_read_fp8b_kernel(const Fp8bRow
         for (int kv = 0; kv < 2; ++kv) {
             const uint8_t *src = (kv ? a.v_cache : a.k_cache) + at * kHeadDim + part * kVals;
             if (kBf16) {
-                const uint2 u = in ? __ldg(reinterpret_cast<const uint2 *>(src)) : make_uint2(0u, 0u);
+                const uint2 u = in ? *reinterpret_cast<const uint2 *>(src) : make_uint2(0u, 0u);
                 w[n][kv][0] = u.x;
                 w[n][kv][kVals / 4 - 1] = u.y;
             } else {
-                w[n][kv][0] = in ? __ldg(reinterpret_cast<const uint32_t *>(src)) : 0u;
+                w[n][kv][0] = in ? *reinterpret_cast<const uint32_t *>(src) : 0u;
             }
-            x[n][kv] = in ? __ldg((kv ? a.v_exp : a.k_exp) + at / kBlock) : kExpBias;
+            x[n][kv] = in ? (kv ? a.v_exp : a.k_exp)[at / kBlock] : kExpBias;
         }
     }
 #pragma unroll

@@ -22,7 +22,7 @@ __device__ __forceinline__ Sight sight_of(const CacheAttnArgs &a, int b)
     const int lp = seq_page_log2(a, b);
     const long long cap = lp < 0 ? 0 : static_cast<long long>(a.max_pages) << lp;
     const int most = cap < a.max_len ? static_cast<int>(cap) : a.max_len;
-    const int L = __ldg(a.seq_lens + b);
+    const int L = a.seq_lens[b];
     s.len = L < 0 ? 0 : min(L, most);
     s.from = a.win.window == 0 ? 0 : max(0, s.len - a.win.window);
     s.sinks = min(a.win.sinks, s.from);
@@ -295,7 +295,7 @@ __device__ __forceinline__ void load_rows(const CacheAttnArgs &a, int b, int h, 
     const uint4 *src = reinterpret_cast<const uint4 *>(a.q + row * kHeadDim + 32 * c);
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-        raw[i] = __ldg(src + i);
+        raw[i] = src[i];
 }
 
 __device__ __forceinline__ void make_query(const CacheAttnArgs &a, const uint4 (&raw)[4], float k_scale, int r, int c,
@@ -354,7 +354,7 @@ __device__ __forceinline__ void flag_sequence(const CacheAttnArgs &a, int b, con
         return;
     if (seq_page_log2(a, b) < 0)
         atomicOr(a.err, PKV_DEVERR_PAGESIZE);
-    else if (__ldg(a.seq_lens + b) != s.len)
+    else if (a.seq_lens[b] != s.len)
         atomicOr(a.err, PKV_DEVERR_SEQLEN);
 }
 
