@@ -42,6 +42,11 @@ __device__ __forceinline__ float two_to(int e)             // -126 .. 127
     return __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
 }
 
+__device__ __forceinline__ float two_to_minus(int e)       // e: -117 .. 127 (2^-127 is a subnormal number)
+{
+    return e == 127 ? __uint_as_float(0x00400000u) : two_to(-e);
+}
+
 __device__ __forceinline__ uint32_t to_e4m3x4(float a, float b, float c, float d)
 {
     uint32_t w;
@@ -147,7 +152,8 @@ __device__ __forceinline__ void append_block(const Fp8bRowArgs &a, const void *i
         if (kFull || k < count)
             load_eight<kBf16>(in, ((t0 + t) * a.hkv + h) * kHeadDim + 8 * part, x[i]);
     }
-    const int old = begins ? kExpMin : min(static_cast<int>(*exp) - kExpBias, kExpMax);
+    // (a byte above an appended block's largest keeps its meaning; 255, which has none, counts as 254)
+    const int old = begins ? kExpMin : min(static_cast<int>(*exp), 254) - kExpBias;
     uint32_t top = 0;
 #pragma unroll
     for (int i = 0; i < kBlock / 2; ++i)
@@ -163,7 +169,7 @@ __device__ __forceinline__ void append_block(const Fp8bRowArgs &a, const void *i
         top = __reduce_max_sync(kWarp, top);
     }
     const int e = max(block_exponent(top), old);
-    const float down = two_to(-e);
+    const float down = two_to_minus(e);
 #pragma unroll
     for (int i = 0; i < kBlock / 2; ++i) {
         const int k = 2 * i + half, r = kFull ? k : __shfl_sync(kWarp, row, k);
