@@ -11,6 +11,8 @@ import subprocess
 import sys
 import sysconfig
 
+import torch
+
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
@@ -18,7 +20,11 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB_DIR = os.path.join(PKG, "lib")
 LIB = os.path.join(LIB_DIR, "libpagedfp8.so")
-BINDING = os.path.join(LIB_DIR, "_binding.so")      # the Python binding's fast path (needs torch's headers)
+
+# The Python binding's fast path.  It holds what it needs of torch's C++ interface, so it serves the
+# torch and the Python that it was built with, and says so in its name; without it the same calls are
+# checked in Python.
+BINDING = os.path.join(LIB_DIR, f"_binding.{sys.implementation.cache_tag}.torch-{torch.__version__}.so")
 
 SOURCES = ["append.cu", "decode.cu", "api.cu", "noalloc.cu", "calibrate.cu", "prefill.cu",
            "rows_fp4.cu", "prefill_fp4.cu", "decode_fp4.cu", "api_fp4.cu",
@@ -36,22 +42,26 @@ def _nvcc() -> str:
 
 
 def _deps() -> list:
-    files = [os.path.join(CSRC, f) for f in os.listdir(CSRC)]
+    files = [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f != "binding.cpp"]
     files.append(os.path.join(INCLUDE, "pagedfp8.h"))
     files.append(os.path.abspath(__file__))
     return files
 
 
+def _binding_deps() -> list:
+    return [os.path.join(CSRC, "binding.cpp"), os.path.join(INCLUDE, "pagedfp8.h"), os.path.abspath(__file__)]
+
+
+def _stale(target: str, files: list) -> bool:
+    return not os.path.exists(target) or any(os.path.getmtime(f) > os.path.getmtime(target) for f in files)
+
+
 def needs_build() -> bool:
-    if not os.path.exists(LIB) or not os.path.exists(BINDING):
-        return True
-    t = min(os.path.getmtime(LIB), os.path.getmtime(BINDING))
-    return any(os.path.getmtime(f) > t for f in _deps())
+    return _stale(LIB, _deps()) or _stale(BINDING, _binding_deps())
 
 
 def _binding_commands() -> tuple:
-    """The commands that compile and link the binding's fast path."""
-    import torch
+    """The commands that compile and link the binding's fast path, and the file they make."""
     base = os.path.dirname(torch.__file__)
     obj, tmp = os.path.join(BUILD, "binding.o"), BINDING + f".tmp{os.getpid()}"
     cuda = os.path.dirname(os.path.dirname(os.path.realpath(_nvcc())))
@@ -66,6 +76,17 @@ def _binding_commands() -> tuple:
     return compile_, link, tmp
 
 
+def _start(cmd: list):
+    return subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True)
+
+
+def _finish(proc, verbose: bool) -> bool:
+    out, _ = proc.communicate()
+    if verbose or proc.returncode != 0:
+        sys.stderr.write(out)
+    return proc.returncode == 0
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
     if not force and not needs_build():
         return LIB
@@ -74,29 +95,29 @@ def build(force: bool = False, verbose: bool = False) -> str:
     os.makedirs(LIB_DIR, exist_ok=True)
     procs = []
     objs = []
-    for src in SOURCES:
+    library, binding = force or _stale(LIB, _deps()), force or _stale(BINDING, _binding_deps())
+    for src in SOURCES if library else ():
         obj = os.path.join(BUILD, src.replace(".cu", ".o"))
         objs.append(obj)
         cmd = [nvcc, *ARCH, *FLAGS, "-I", INCLUDE, "-I", CSRC, "-c", os.path.join(CSRC, src), "-o", obj]
         if verbose:
             cmd.insert(1, "-Xptxas=-v")
-        procs.append((src, subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True)))
-    compile_, link, binding_tmp = _binding_commands()
-    procs.append(("binding.cpp", subprocess.Popen(compile_, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True)))
-    failed = []
-    for src, p in procs:
-        out, _ = p.communicate()
-        if verbose or p.returncode != 0:
-            sys.stderr.write(out)
-        if p.returncode != 0:
-            failed.append(src)
+        procs.append((src, _start(cmd)))
+    if binding:
+        compile_, link, binding_tmp = _binding_commands()
+        compiled = _start(compile_)
+    failed = [src for src, p in procs if not _finish(p, verbose)]
+    compiled = binding and _finish(compiled, verbose)
     if failed:
-        raise RuntimeError(f"compilation failed for {failed}")
-    tmp = LIB + f".tmp{os.getpid()}"
-    subprocess.run([nvcc, *ARCH, "-shared", "-o", tmp, *objs], check=True)
-    os.replace(tmp, LIB)
-    subprocess.run(link, check=True)
-    os.replace(binding_tmp, BINDING)
+        raise RuntimeError(f"nvcc failed for {failed}")
+    if library:
+        tmp = LIB + f".tmp{os.getpid()}"
+        subprocess.run([nvcc, *ARCH, "-shared", "-o", tmp, *objs], check=True)
+        os.replace(tmp, LIB)
+    if compiled and _finish(_start(link), verbose):
+        os.replace(binding_tmp, BINDING)
+    elif binding:
+        sys.stderr.write("the binding's fast path cannot be built here: its calls are checked in Python\n")
     return LIB
 
 
