@@ -695,9 +695,13 @@ pkv_status pkv_paged_gqa_decode_fp8b(const void *q,
 /*
  * paged_prefill_fp8b -- pkv_paged_prefill_fp4 over the block-scaled cache: the same
  * window and sinks, arguments, errors, untouched rows and determinism.  V is widened
- * in units of its own: of a sequence's kv head, blocks whose scale is less than 2^-21
- * of the largest one that the chunk sees are rounded to 2^-40 of that block's largest
- * value.  Three launches; a fourth where few rows have a long past: several CTAs then
+ * in units of its own: of a sequence's kv head, values in blocks whose scale is less
+ * than 2^-21 of the largest one 2^E that the chunk sees are off by up to 2^-31 of that
+ * 2^E (2^-39 of the largest value that it holds).  The weights are rounded by what they
+ * are themselves, not by what they contribute as decode's: small ones are off by up to
+ * 2^-27 (an fp32 output: 2^-37) of the row's largest weight w, which moves an output by up
+ * to that much of w times the sum of the |v| in sight.  So decode over the same cache is
+ * nearer where small weights meet values larger by more than that.  Three launches; a fourth where few rows have a long past: several CTAs then
  * share a query tile's keys (as many as batch, the bounds, the heads and the output's
  * type say), and their sums are joined in order; with a bf16 output and long contexts
  * they read the cache itself, without 16-bit copies.  num_kv_heads is at most 8192.

@@ -47,7 +47,9 @@ __device__ __forceinline__ void more_registers()
 
 // P = 2^(score - m), with m kLift below the row's maximum when it is set, moved when that
 // exceeds it by more than kMoveMax: P is within f16, and what its lower end loses is 2^-27 of the
-// largest weight a key, under the output's 2^-8.
+// largest weight a key: of the output, that much of this weight times the sum of |v|, which is under
+// its 2^-8 unless small weights meet values larger by as much.  (Decode refers its weights to what they
+// contribute; here the row's one reference comes from the scores.)
 constexpr float kMoveMax = 15.9f, kLift = 2.f;
 constexpr uint32_t kScoreCol = 128, kOutCol = 256;   // tile x: scores at 128 x, accumulator at 256 + 128 x
 

@@ -4,8 +4,8 @@
 //   v16 = code * 2^(ev - E) * 2^6,   E = the largest ev among the sequence's blocks
 //                                    of this kv head that some query of the chunk sees,
 // so that 448 comes out as 28672.  Exact for blocks down to 2^-21 of the largest
-// one's scale; below that f16's lower end rounds to 2^-25, 2^-40 of the head's
-// largest V.  The output is multiplied by 2^(E - 6).  NaN codes of V become zeros
+// one's scale; below that f16's lower end loses up to 2^-25 of a unit, 2^-31 of 2^E, 2^-39 of
+// the largest V that it holds.  The output is multiplied by 2^(E - 6).  NaN codes of V become zeros
 // and are recorded, a bit a value.
 //
 // Two launches, and a third behind the attention where few rows have a long past: its
