@@ -718,7 +718,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
             const int64_t orow = (static_cast<int64_t>(q0) + t0 + tl) * a.hq + h * G + g;
             uint32_t nans = 0;
             if (kFp4 && !kSplit)
-                nans = nan_blocks<kWin>(a, win, row0 / kKeys, nt, valid ? pos0 + tl : last, lane, key_tile, copy_tile);
+                nans = nan_blocks<kWin, kBlocks>(a, win, row0 / kKeys, nt, valid ? pos0 + tl : last, lane, key_tile, copy_tile);
             const bool have_o = nt > kFold;                // at least one segment was folded into O
 #pragma unroll 1
             for (int c = 0; c < 4; ++c) {

@@ -250,27 +250,30 @@ __device__ __forceinline__ uint8_t *nan_rows(const PrefillArgs &a)
 // Blocks of 16 dims (a bit each) in which a row at position p sees a NaN: nt
 // key tiles, the i-th one is key_tile(i) of the sequence and copy_tile(i) of the
 // copy, which starts at tile `tile0` (the whole warp).
-template <bool kWin, typename KeyTile, typename CopyTile>
+// (kBlocks: written while this kernel may be on the GPU already, see grid.cuh.  By ordinary loads
+// the attention's loop, which hangs on what stands behind it, takes longer: 4096 of 16384 tokens 1281 us, so 1260.)
+template <bool kWin, bool kBlocks, typename KeyTile, typename CopyTile>
 __device__ __forceinline__ uint32_t nan_blocks(const PrefillArgs &a, const KeyWindow &w, int tile0, int nt, int p, int lane,
                                                KeyTile key_tile, CopyTile copy_tile)
 {
     const uint32_t *tiles = nan_tiles(a);
+    auto load = [](auto *p) { return kBlocks ? __ldcg(p) : __ldg(p); };
     bool some = false;
     for (int i = lane; i < nt; i += 32)
-        some = some || tiles[tile0 + copy_tile(i)] != 0;
+        some = some || load(tiles + tile0 + copy_tile(i)) != 0;
     uint32_t hit = 0;
     if (__any_sync(kAll, some)) {
 #pragma unroll 1
         for (int i = 0; i < nt; ++i) {
             const int64_t tile = tile0 + copy_tile(i);
-            const uint32_t word = tiles[tile];
+            const uint32_t word = load(tiles + tile);
             if (word == 0)
                 continue;
 #pragma unroll 1
             for (int k = 0; k < kKeys; ++k) {
                 const int t = key_tile(i) * kKeys + k;
                 if ((word >> (8 * (k >> 5)) & 0xFFu) != 0 && t <= p && (!kWin || t > p - w.window || t < w.sinks))
-                    hit |= nan_rows(a)[tile * kKeys + k];
+                    hit |= load(nan_rows(a) + tile * kKeys + k);
             }
         }
     }

@@ -657,7 +657,7 @@ __global__ void __launch_bounds__(kThreads2, 1)
                     *reinterpret_cast<float2 *>(to + kHeadDim) = make_float2(m, l);
             } else {
                 const float inv = (kBlocks ? 1.f : __ldg(a.v_scale + h)) / l;
-                const uint32_t nans = nan_blocks<kWin>(a, win, row0 / kKeys, ntx, p_row, lane, key_tile, copy_tile);
+                const uint32_t nans = nan_blocks<kWin, kBlocks>(a, win, row0 / kKeys, ntx, p_row, lane, key_tile, copy_tile);
                 const int64_t orow = (static_cast<int64_t>(q0) + t0 + x * tpt + tl) * a.hq + h * G + g;
                 uint4 *dst = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.out) + orow * kHeadDim);
 #pragma unroll 1
