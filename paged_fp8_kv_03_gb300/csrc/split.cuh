@@ -222,13 +222,17 @@ __device__ __forceinline__ void store4(const CacheAttnArgs &a, int64_t row, int 
     store4(a.out, a.out_f32 != 0, row, d, v);
 }
 
-// a 2^d 2^e / l for a whole number e, whose power may lie at either end of fp32's
-// range where the result does not: it is multiplied in two halves, exactly.
+// a 2^d 2^e / l for a whole number e.  Either power may lie beyond fp32's range where the
+// result does not (a large weight that meets tiny values, beside a tiny one that meets large
+// ones): the whole part of both is multiplied in two halves, exactly.
 struct Quotient {
     float rest, low, high;
-    __device__ __forceinline__ Quotient(float d, float e, float l) : rest(ex2_approx(d) / l)
+    __device__ __forceinline__ Quotient(float d, float e, float l)
     {
-        const int whole = static_cast<int>(e), half = whole >> 1;
+        const float near = rintf(d);
+        rest = ex2_approx(d - near) / l;
+        // (a is below 2^60: with 2^-252 nothing is left of it, with 2^254 more than fp32 holds)
+        const int whole = static_cast<int>(fminf(fmaxf(near + e, -252.f), 254.f)), half = whole >> 1;
         low = __int_as_float((half + 127) << 23);
         high = __int_as_float((whole - half + 127) << 23);
     }
