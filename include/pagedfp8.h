@@ -634,8 +634,9 @@ pkv_status pkv_paged_prefill_fp4(const void *q, const int32_t *cu_q, int total_q
  *   slot_mapping   device int64 [num_tokens]; negative = do not write.  The tokens
  *                  of one block have to lie within 32 consecutive ones of the call,
  *                  in any order (those of a sequence, back to back, do); what a block
- *                  holds whose tokens lie further apart is undefined, and two tokens
- *                  with the same slot race.
+ *                  holds whose tokens lie further apart is undefined (the drafts of more
+ *                  than 31 sequences, token by token instead of sequence by sequence, do),
+ *                  and two tokens with the same slot race.
  *   k_new, v_new, in_dtype, page_size, device_error: as pkv_kv_append_fp8; the pools
  *                  as above.
  * num_tokens == 0 is a no-op.

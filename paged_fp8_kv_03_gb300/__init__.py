@@ -988,7 +988,8 @@ def _fp8b_rows(slot_mapping, k, v, H, dev):
 def pkv_kv_append_fp8b(k_new, v_new, slot_mapping, k_cache, v_cache, k_exp, v_exp, device_error=None,
                        stream=None) -> None:
     """k_new/v_new [T, Hkv, 128] fp32|bf16; slot_mapping int64 [T] (negative: not
-    written; a block's tokens within 32 consecutive ones); caches uint8
+    written; a block's tokens within 32 consecutive ones, as sequence by sequence
+    they are); caches uint8
     [num_pages, Hkv, P, 128] and k_exp/v_exp uint8 [num_pages, Hkv, P / 16]
     (written in place)."""
     st = (_fast or _load_and_fast()).append(k_new, v_new, slot_mapping, k_cache, v_cache, k_exp, v_exp, device_error, stream)

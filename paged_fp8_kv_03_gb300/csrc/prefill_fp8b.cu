@@ -10,8 +10,8 @@
 //
 // Two launches, and a third behind the attention where few rows have a long past: its
 // CTAs then share a query tile's keys, and prefill_join_fp8b_kernel joins what they leave
-// (64 tokens of 32 query and 8 kv heads, past 32768: 93 us, else 427; 8 query heads of one
-// kv head, past 131072: 91 us, else 1525).
+// (64 tokens of 32 query and 8 kv heads, past 32768, fp32 outputs: 99 us, else 374; 8 query heads
+// of one kv head, past 131072, bf16: 91 us, else 1525; calls that prefill_direct.cu takes, see there).
 // kv_refs_fp8b_kernel: a cluster of CTAs a sequence takes the maximum
 // of the bytes (a sixteenth of a byte a token and head), and CTA 0 lays out the
 // regions.  kv_widen_fp8b_kernel: a CTA half a tile of 128 rows (or a quarter of one,
@@ -265,7 +265,7 @@ __global__ void __launch_bounds__(kJoinThreads) prefill_join_fp8b_kernel(const P
 }
 
 // Where query tiles fill half of the SMs at most, as many CTAs share each one's keys as fill them
-// once.  A part has two key tiles at least, four where a row has more than 32 parts (64 tokens,
+// once (kSplitSms, a constant, so that the workspace's size goes by the bounds alone).  A part has two key tiles at least, four where a row has more than 32 parts (64 tokens,
 // 8 query heads of 1 kv head, past 16384: in 64 parts of two 52 us, in 32 of four 44, in one 198),
 // and kMostPart at most, as the attention kernels then sum in one chain; so a long context has
 // more parts.  A CTA has to be spared kLeastSpared of them, as leaving and joining the states
